@@ -37,8 +37,15 @@ ERR_DEVICE_TIMEOUT = -5
 WS_BUILD_BRIM = 0
 WS_PROFILE_COACT = 1
 WS_EXPERT_BWD = 2
+WS_BLOCK_NORM_BWD = 3
 STATIC_SCRATCH_BYTES = 1183744   # OCCULT_STATIC_SCRATCH_BYTES
 EPD_PAD = 128                    # OCCULT_EPD_PAD
+GATE_NONE = 0
+GATE_CHANNEL = 1
+GATE_TOKEN = 2
+STATE_BLOCK = 256                # OCCULT_STATE_BLOCK
+STATE_M = 0
+STATE_V = 1
 
 
 class occult_desc_t(ctypes.Structure):
@@ -61,6 +68,33 @@ class occult_desc_t(ctypes.Structure):
         return out
 
 
+class occult_norm_t(ctypes.Structure):
+    """Options of occult_block_norm (see occult.h)."""
+    _fields_ = [("eps", ctypes.c_float), ("res_scale", ctypes.c_float),
+                ("gate_kind", ctypes.c_int32), ("res_dtype", ctypes.c_int32)]
+
+
+class occult_balance_t(ctypes.Structure):
+    """Options of occult_balance_loss (see occult.h)."""
+    _fields_ = [("coef", ctypes.c_float), ("coef_dev", ctypes.c_float),
+                ("coef_z", ctypes.c_float), ("group_len", ctypes.c_int32)]
+
+
+class occult_adamw_t(ctypes.Structure):
+    """Options of occult_adamw (see occult.h); grad_scale is a device address or None."""
+    _fields_ = [(n, ctypes.c_double) for n in ("lr", "beta1", "beta2", "eps", "weight_decay")] + [
+        ("step", ctypes.c_int32), ("state_bits", ctypes.c_int32), ("seed", ctypes.c_uint32),
+        ("reserved", ctypes.c_uint32), ("grad_scale", ctypes.c_void_p)]
+
+
+class occult_param_t(ctypes.Structure):
+    """One tensor of an AdamW step (see occult.h)."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("param", "master", "grad", "m", "v", "m_exp",
+                                               "v_exp")] + [
+        ("n", ctypes.c_int64), ("first", ctypes.c_int64), ("dtype", ctypes.c_int32),
+        ("reserved", ctypes.c_int32)]
+
+
 class OccultError(RuntimeError):
     def __init__(self, fn: str, code: int):
         super().__init__(f"{fn} failed: {code} ({strerror(code)})")
@@ -70,6 +104,7 @@ class OccultError(RuntimeError):
 _VP = ctypes.c_void_p
 _I32 = ctypes.c_int32
 _D = ctypes.POINTER(occult_desc_t)
+_SZ = ctypes.c_size_t
 _SIGNATURES = {
     "occult_strerror": (ctypes.c_char_p, [ctypes.c_int]),
     "occult_check_desc": (ctypes.c_int, [_D]),
@@ -108,6 +143,13 @@ _SIGNATURES = {
     "occult_expert_wgrad_up": (ctypes.c_int, [_D] + [_VP] * 8),
     "occult_zero_f32": (ctypes.c_int, [_VP, ctypes.c_int64, _VP]),
     "occult_gate_grad": (ctypes.c_int, [_D] + [_VP] * 9),
+    "occult_block_norm": (ctypes.c_int, [_D] + [_VP] * 11),
+    "occult_block_norm_bwd": (ctypes.c_int, [_D] + [_VP] * 16 + [_SZ, _VP]),
+    "occult_balance_workspace_size": (ctypes.c_int, [_D, _VP, _VP]),
+    "occult_balance_loss": (ctypes.c_int, [_D] + [_VP] * 9 + [_SZ, _VP]),
+    "occult_balance_grad": (ctypes.c_int, [_D] + [_VP] * 6 + [_I32, _VP]),
+    "occult_adamw": (ctypes.c_int, [_VP, _VP, _I32, _VP]),
+    "occult_adamw_read": (ctypes.c_int, [_VP, _VP, ctypes.c_int64, _I32, _VP, _VP]),
     "occult_profile_coact": (ctypes.c_int, [_D, _VP, _I32, _VP, _VP, _VP, _VP, _VP,
                                             ctypes.c_size_t, _VP]),
 }
@@ -568,6 +610,143 @@ def occult_profile_coact(desc, ids, n_tok, C, ws, P=None, vmask=None, ct_hist=No
           _dev(ct_hist, torch.int64, max_ct + 1, "ct_hist", nullable=True),
           _dev(ws, torch.uint8, need, "ws", nullable=need == 0), ctypes.c_size_t(need),
           _stream(stream))
+
+
+def _res_torch_dtype(opt) -> torch.dtype:
+    return torch.bfloat16 if opt.res_dtype == OCCULT_BF16 else torch.float32
+
+
+def _gate_len(desc, opt) -> int:
+    return {GATE_CHANNEL: desc.d, GATE_TOKEN: desc.T}.get(opt.gate_kind, 0)
+
+
+def occult_block_norm(desc, opt, r, y=None, w_post=None, gate=None, w_pre=None, r_out=None,
+                      x=None, rstd_post=None, rstd_pre=None, stream=None):
+    """Norm of the block's output y, gate, residual sum and norm before the next block."""
+    T, d = desc.T, desc.d
+    dt, rt, f32 = desc.torch_dtype, _res_torch_dtype(opt), torch.float32
+    _call("occult_block_norm", ctypes.byref(desc), ctypes.byref(opt), _dev(r, rt, T * d, "r"),
+          _dev(y, f32, T * d, "y", nullable=True), _dev(w_post, dt, d, "w_post", nullable=True),
+          _dev(gate, f32, _gate_len(desc, opt), "gate", nullable=True),
+          _dev(w_pre, dt, d, "w_pre", nullable=True),
+          _dev(r_out, rt, T * d, "r_out", nullable=True), _dev(x, dt, T * d, "x", nullable=True),
+          _dev(rstd_post, f32, T, "rstd_post", nullable=True),
+          _dev(rstd_pre, f32, T, "rstd_pre", nullable=True), _stream(stream))
+
+
+def occult_block_norm_bwd(desc, opt, dr_out, r_out, dr, ws, dx=None, y=None, w_post=None,
+                          gate=None, w_pre=None, rstd_post=None, rstd_pre=None, dy=None,
+                          dw_post=None, dgate=None, dw_pre=None, stream=None):
+    """Gradients of occult_block_norm; dr_out (or, without w_pre, r_out) may be None."""
+    T, d = desc.T, desc.d
+    dt, rt, f32 = desc.torch_dtype, _res_torch_dtype(opt), torch.float32
+    need = workspace_size(desc, WS_BLOCK_NORM_BWD)
+    n_gate = _gate_len(desc, opt)
+    _call("occult_block_norm_bwd", ctypes.byref(desc), ctypes.byref(opt),
+          _dev(dr_out, rt, T * d, "dr_out", nullable=True),
+          _dev(dx, f32, T * d, "dx", nullable=True),
+          _dev(r_out, rt, T * d, "r_out", nullable=True),
+          _dev(y, f32, T * d, "y", nullable=True), _dev(w_post, dt, d, "w_post", nullable=True),
+          _dev(gate, f32, n_gate, "gate", nullable=True),
+          _dev(w_pre, dt, d, "w_pre", nullable=True),
+          _dev(rstd_post, f32, T, "rstd_post", nullable=True),
+          _dev(rstd_pre, f32, T, "rstd_pre", nullable=True), _dev(dr, rt, T * d, "dr"),
+          _dev(dy, dt, T * d, "dy", nullable=True),
+          _dev(dw_post, f32, d, "dw_post", nullable=True),
+          _dev(dgate, f32, n_gate, "dgate", nullable=True),
+          _dev(dw_pre, f32, d, "dw_pre", nullable=True),
+          _dev(ws, torch.uint8, need, "ws", nullable=need == 0), need, _stream(stream))
+
+
+def balance_groups(desc, opt) -> int:
+    """Number of groups of the balance loss."""
+    return max(1, -(-desc.T // opt.group_len)) if opt.group_len > 0 else 1
+
+
+def balance_workspace_size(desc, opt) -> int:
+    """Device workspace bytes of occult_balance_loss."""
+    n = ctypes.c_size_t(0)
+    _call("occult_balance_workspace_size", ctypes.byref(desc), ctypes.byref(opt), ctypes.byref(n))
+    return n.value
+
+
+def occult_balance_loss(desc, opt, logits, ids, expert_to_vdev, counts, grad_w, loss, ws,
+                        mask=None, stream=None):
+    """Per-expert counts and the auxiliary losses of the router."""
+    T, Ne, k, G = desc.T, desc.n_experts, desc.top_k, balance_groups(desc, opt)
+    i32, f32 = torch.int32, torch.float32
+    need = balance_workspace_size(desc, opt)
+    _call("occult_balance_loss", ctypes.byref(desc), ctypes.byref(opt),
+          _dev(logits, f32, T * Ne, "logits"), _dev(ids, i32, T * k, "ids"),
+          _dev(expert_to_vdev, i32, Ne, "expert_to_vdev"),
+          _dev(mask, torch.uint8, T, "mask", nullable=True), _dev(counts, i32, G * Ne, "counts"),
+          _dev(grad_w, f32, G * Ne + 1, "grad_w"), _dev(loss, f32, 4, "loss"),
+          _dev(ws, torch.uint8, need, "ws"), need, _stream(stream))
+
+
+def occult_balance_grad(desc, opt, logits, grad_w, dlogits, mask=None, dloss=None,
+                        accumulate=False, stream=None):
+    """Gradient of the total auxiliary loss, written to dlogits or added to it."""
+    T, Ne, f32 = desc.T, desc.n_experts, torch.float32
+    _call("occult_balance_grad", ctypes.byref(desc), ctypes.byref(opt),
+          _dev(logits, f32, T * Ne, "logits"),
+          _dev(grad_w, f32, balance_groups(desc, opt) * Ne + 1, "grad_w"),
+          _dev(mask, torch.uint8, T, "mask", nullable=True),
+          _dev(dloss, f32, 1, "dloss", nullable=True), _dev(dlogits, f32, T * Ne, "dlogits"),
+          int(bool(accumulate)), _stream(stream))
+
+
+class AdamTable:
+    """The host records of occult_adamw's tensors; keeps the tensors alive."""
+
+    def __init__(self, tensors):
+        self.tensors = tensors
+        self.records = (occult_param_t * max(1, len(tensors)))()
+        self.n = len(tensors)
+        bits = {t["m"].dtype for t in tensors}
+        if not bits <= {torch.float32, torch.uint8} or len(bits) > 1:
+            raise ValueError("the states of a table are all float32 or all uint8 codes")
+        self.state_bits = 8 if bits == {torch.uint8} else 32
+        st = torch.uint8 if self.state_bits == 8 else torch.float32
+        for rec, t in zip(self.records, tensors):
+            p = t["param"]
+            n = p.numel()
+            if p.dtype not in (torch.float32, torch.bfloat16):
+                raise ValueError(f"param must be float32 or bfloat16, got {p.dtype}")
+            if t.get("master") is not None and p.dtype != torch.bfloat16:
+                raise ValueError("only a bfloat16 parameter takes a master copy")
+            blocks = -(-n // STATE_BLOCK)
+            rec.param = _dev(p, None, n, "param")
+            rec.master = _dev(t.get("master"), torch.float32, n, "master", nullable=True)
+            rec.grad = _dev(t["grad"], torch.float32, n, "grad")
+            rec.m, rec.v = _dev(t["m"], st, n, "m"), _dev(t["v"], st, n, "v")
+            if st == torch.uint8:
+                rec.m_exp = _dev(t.get("m_exp"), torch.uint8, blocks, "m_exp")
+                rec.v_exp = _dev(t.get("v_exp"), torch.uint8, blocks, "v_exp")
+            rec.n, rec.first = n, int(t.get("first", 0))
+            rec.dtype = OCCULT_BF16 if p.dtype == torch.bfloat16 else OCCULT_F32
+
+
+def adamw_table(tensors) -> AdamTable:
+    """Records for occult_adamw from dicts of param, grad, m, v and, as needed,
+    master, m_exp, v_exp and first (position in the stream of draws)."""
+    return AdamTable(list(tensors))
+
+
+def occult_adamw(opt, table: AdamTable, stream=None):
+    """One AdamW step over the tensors of ``table``."""
+    if opt.state_bits != table.state_bits:
+        raise ValueError(f"opt asks for {opt.state_bits}-bit states, the table holds "
+                         f"{table.state_bits}-bit ones")
+    _call("occult_adamw", ctypes.byref(opt), table.records, table.n, _stream(stream))
+
+
+def occult_adamw_read(codes, exps, which, out, stream=None):
+    """The values of an 8-bit state (STATE_M: m, STATE_V: sqrt(v)) in bf16."""
+    n = codes.numel()
+    _call("occult_adamw_read", _dev(codes, torch.uint8, n, "codes"),
+          _dev(exps, torch.uint8, -(-n // STATE_BLOCK), "exps"), n, which,
+          _dev(out, torch.bfloat16, n, "out"), _stream(stream))
 
 
 from .pipeline import OccultMoE, desc_for  # noqa: E402  (needs the names above)

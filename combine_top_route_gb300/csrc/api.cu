@@ -2,6 +2,7 @@
 // include/occult.h for the meaning, layout and ownership of every argument.
 #include <stdio.h>
 
+#include <initializer_list>
 #include <mutex>
 
 #include "common.cuh"
@@ -124,6 +125,10 @@ int occult_workspace_size(const occult_desc_t* desc, int32_t op, int32_t n_tok, 
   }
   if (op == OCCULT_WS_EXPERT_BWD) {
     *bytes = expert_bwd_ws_bytes(*desc);
+    return OCCULT_OK;
+  }
+  if (op == OCCULT_WS_BLOCK_NORM_BWD) {
+    *bytes = block_norm_bwd_ws_bytes(*desc);
     return OCCULT_OK;
   }
   OCCULT_REQUIRE(op == OCCULT_WS_PROFILE_COACT && n_tok >= 0);
@@ -793,6 +798,178 @@ int occult_profile_coact(const occult_desc_t* desc, const int32_t* ids, int32_t 
   if (ws_bytes < need || (need > 0 && !ws)) return OCCULT_ERR_WORKSPACE;
   OCCULT_CTX(stream);
   return launch_profile(ctx, *desc, ids, n_tok, vmask, C, P, ct_hist, ws);
+}
+
+// Options and pointers common to both directions of the block norm.
+static int check_norm(const occult_desc_t* desc, const occult_norm_t* opt, const float* y,
+                      const void* w_post, const float* gate, const void* w_pre) {
+  OCCULT_REQUIRE(opt);
+  OCCULT_REQUIRE(opt->eps > 0.f && opt->eps < 1e30f && opt->res_scale == opt->res_scale);
+  OCCULT_REQUIRE(opt->gate_kind >= OCCULT_GATE_NONE && opt->gate_kind <= OCCULT_GATE_TOKEN);
+  OCCULT_REQUIRE(opt->res_dtype == OCCULT_F32 || opt->res_dtype == OCCULT_BF16);
+  if (desc->d > kNormMaxWidth) return OCCULT_ERR_UNSUPPORTED;
+  if (desc->T == 0) return OCCULT_OK;  // buffers of no rows may have no address
+  OCCULT_REQUIRE((gate != nullptr) == (opt->gate_kind != OCCULT_GATE_NONE));
+  OCCULT_REQUIRE(y ? true : (!w_post && !gate && w_pre));
+  return OCCULT_OK;
+}
+static bool aligned16(std::initializer_list<const void*> ps) {
+  for (const void* p : ps)
+    if (reinterpret_cast<uintptr_t>(p) % 16 != 0) return false;
+  return true;
+}
+
+int occult_block_norm(const occult_desc_t* desc, const occult_norm_t* opt, const void* r,
+                      const float* y, const void* w_post, const float* gate, const void* w_pre,
+                      void* r_out, void* x, float* rstd_post, float* rstd_pre,
+                      occult_stream_t stream) {
+  int rc = check(desc);
+  if (rc) return rc;
+  rc = check_norm(desc, opt, y, w_post, gate, w_pre);
+  if (rc) return rc;
+  OCCULT_REQUIRE(desc->T == 0 ||
+                 (r && (r_out != nullptr) == (y != nullptr) && (x != nullptr) == (w_pre != nullptr) &&
+                  (w_post || !rstd_post) && (w_pre || !rstd_pre)));
+  OCCULT_REQUIRE(aligned16({r, y, w_post, gate, w_pre, r_out, x}));
+  OCCULT_CTX(stream);
+  if (desc->T == 0) return OCCULT_OK;
+  NormArgs a{};
+  a.T = desc->T; a.d = desc->d; a.gate_kind = opt->gate_kind;
+  a.eps = opt->eps; a.res_scale = opt->res_scale;
+  a.r = r; a.y = y; a.w_post = w_post; a.gate = gate; a.w_pre = w_pre;
+  a.r_out = r_out; a.x = x; a.rstd_post_out = rstd_post; a.rstd_pre_out = rstd_pre;
+  return launch_block_norm(ctx, a, opt->res_dtype, desc->dtype);
+}
+
+int occult_block_norm_bwd(const occult_desc_t* desc, const occult_norm_t* opt,
+                          const void* dr_out, const float* dx, const void* r_out, const float* y,
+                          const void* w_post, const float* gate, const void* w_pre,
+                          const float* rstd_post, const float* rstd_pre, void* dr, void* dy,
+                          float* dw_post, float* dgate, float* dw_pre, void* ws,
+                          size_t ws_bytes, occult_stream_t stream) {
+  int rc = check(desc);
+  if (rc) return rc;
+  rc = check_norm(desc, opt, y, w_post, gate, w_pre);
+  if (rc) return rc;
+  // an output exactly where the forward had an input
+  OCCULT_REQUIRE((dw_post != nullptr) == (w_post != nullptr) &&
+                 (dw_pre != nullptr) == (w_pre != nullptr) &&
+                 (opt->gate_kind != OCCULT_GATE_CHANNEL || dgate));
+  OCCULT_REQUIRE(desc->T == 0 || ((dr_out || w_pre) && dr && (dy != nullptr) == (y != nullptr) &&
+                                  (dgate != nullptr) == (gate != nullptr) &&
+                                  (!w_pre || (dx && r_out && rstd_pre)) &&
+                                  (!w_post || rstd_post)));
+  OCCULT_REQUIRE(aligned16({dr_out, dx, r_out, y, w_post, gate, w_pre, dr, dy, ws}));
+  const size_t need = block_norm_bwd_ws_bytes(*desc);
+  if (ws_bytes < need || (need > 0 && !ws)) return OCCULT_ERR_WORKSPACE;
+  OCCULT_CTX(stream);
+  if (desc->T == 0) {
+    // no rows: the weight gradients are zero
+    const size_t d = static_cast<size_t>(desc->d);
+    if (dw_post && (rc = zero_weights(ctx, dw_post, d))) return rc;
+    if (dw_pre && (rc = zero_weights(ctx, dw_pre, d))) return rc;
+    return opt->gate_kind == OCCULT_GATE_CHANNEL ? zero_weights(ctx, dgate, d) : OCCULT_OK;
+  }
+  NormArgs a{};
+  a.T = desc->T; a.d = desc->d; a.gate_kind = opt->gate_kind;
+  a.eps = opt->eps; a.res_scale = opt->res_scale;
+  a.r = r_out; a.y = y; a.w_post = w_post; a.gate = gate; a.w_pre = w_pre;
+  a.dr_out = dr_out; a.dx = w_pre ? dx : nullptr; a.rstd_post = rstd_post; a.rstd_pre = rstd_pre;
+  a.dr = dr; a.dy = dy; a.dw_post = dw_post; a.dgate = dgate; a.dw_pre = dw_pre;
+  return launch_block_norm_bwd(ctx, a, opt->res_dtype, desc->dtype, ws);
+}
+
+static int check_balance(const occult_desc_t* desc, const occult_balance_t* opt) {
+  int rc = check(desc);
+  if (rc) return rc;
+  OCCULT_REQUIRE(opt && opt->group_len >= 0);
+  int L;
+  const int64_t G = balance_groups(desc->T, opt->group_len, &L);
+  return G * desc->n_experts < (1ll << 31) ? OCCULT_OK : OCCULT_ERR_UNSUPPORTED;
+}
+
+static BalanceArgs balance_args(const occult_desc_t* desc, const occult_balance_t* opt,
+                                const float* logits, const uint8_t* mask) {
+  BalanceArgs a{};
+  a.T = desc->T; a.Ne = desc->n_experts; a.k = desc->top_k; a.Nd = desc->n_vdev;
+  a.G = balance_groups(desc->T, opt->group_len, &a.L);
+  a.coef = opt->coef; a.coef_dev = opt->coef_dev; a.coef_z = opt->coef_z;
+  a.logits = logits; a.mask = mask;
+  return a;
+}
+
+int occult_balance_workspace_size(const occult_desc_t* desc, const occult_balance_t* opt,
+                                  size_t* bytes) {
+  int rc = check_balance(desc, opt);
+  if (rc) return rc;
+  OCCULT_REQUIRE(bytes);
+  *bytes = balance_ws_bytes(*desc, opt->group_len);
+  return OCCULT_OK;
+}
+
+int occult_balance_loss(const occult_desc_t* desc, const occult_balance_t* opt,
+                        const float* logits, const int32_t* ids, const int32_t* expert_to_vdev,
+                        const uint8_t* mask, int32_t* counts, float* grad_w, float* loss,
+                        void* ws, size_t ws_bytes, occult_stream_t stream) {
+  int rc = check_balance(desc, opt);
+  if (rc) return rc;
+  OCCULT_REQUIRE(expert_to_vdev && counts && grad_w && loss);
+  OCCULT_REQUIRE(desc->T == 0 || (logits && ids));
+  OCCULT_REQUIRE(aligned16({logits, ids, ws}));
+  if (ws_bytes < balance_ws_bytes(*desc, opt->group_len) || !ws) return OCCULT_ERR_WORKSPACE;
+  OCCULT_CTX(stream);
+  BalanceArgs a = balance_args(desc, opt, logits, mask);
+  a.ids = ids; a.e2v = expert_to_vdev;
+  a.counts = counts; a.grad_w = grad_w; a.loss = loss; a.ws = static_cast<float*>(ws);
+  return launch_balance_loss(ctx, a);
+}
+
+int occult_balance_grad(const occult_desc_t* desc, const occult_balance_t* opt,
+                        const float* logits, const float* grad_w, const uint8_t* mask,
+                        const float* dloss, float* dlogits, int32_t accumulate,
+                        occult_stream_t stream) {
+  int rc = check_balance(desc, opt);
+  if (rc) return rc;
+  OCCULT_REQUIRE(accumulate == 0 || accumulate == 1);
+  OCCULT_REQUIRE(desc->T == 0 || (logits && grad_w && dlogits));
+  OCCULT_REQUIRE(aligned16({logits, grad_w, dlogits}));
+  OCCULT_CTX(stream);
+  BalanceArgs a = balance_args(desc, opt, logits, mask);
+  a.grad_w = const_cast<float*>(grad_w);
+  a.dloss = dloss; a.dlogits = dlogits; a.accumulate = accumulate;
+  return launch_balance_grad(ctx, a);
+}
+
+int occult_adamw(const occult_adamw_t* opt, const occult_param_t* params, int32_t n_params,
+                 occult_stream_t stream) {
+  OCCULT_REQUIRE(opt && n_params >= 0 && (n_params == 0 || params));
+  OCCULT_REQUIRE(opt->state_bits == 32 || opt->state_bits == 8);
+  OCCULT_REQUIRE(opt->step >= 1 && opt->reserved == 0);
+  // (comparisons that a NaN fails)
+  OCCULT_REQUIRE(opt->beta1 >= 0 && opt->beta1 < 1 && opt->beta2 >= 0 && opt->beta2 < 1);
+  OCCULT_REQUIRE(opt->eps > 0 && opt->eps < 1e30 && opt->lr > -1e30 && opt->lr < 1e30 &&
+                 opt->weight_decay > -1e30 && opt->weight_decay < 1e30);
+  for (int i = 0; i < n_params; ++i) {
+    const occult_param_t& p = params[i];
+    OCCULT_REQUIRE(p.n >= 0 && p.first >= 0 && p.reserved == 0);
+    OCCULT_REQUIRE(p.dtype == OCCULT_F32 || p.dtype == OCCULT_BF16);
+    OCCULT_REQUIRE(!(p.master && p.dtype == OCCULT_F32));
+    OCCULT_REQUIRE(p.n == 0 || (p.param && p.grad && p.m && p.v));
+    OCCULT_REQUIRE(p.n == 0 || opt->state_bits == 32 || (p.m_exp && p.v_exp));
+    OCCULT_REQUIRE(aligned16({p.param, p.master, p.grad, p.m, p.v}));
+  }
+  OCCULT_CTX(stream);
+  return launch_adamw(ctx, *opt, params, n_params);
+}
+
+int occult_adamw_read(const uint8_t* codes, const uint8_t* exps, int64_t n, int32_t which,
+                      void* out, occult_stream_t stream) {
+  OCCULT_REQUIRE(n >= 0 && (n == 0 || (codes && exps && out)));
+  OCCULT_REQUIRE(which == OCCULT_STATE_M || which == OCCULT_STATE_V);
+  OCCULT_REQUIRE(aligned16({codes, out}));
+  OCCULT_CTX(stream);
+  if (n == 0) return OCCULT_OK;
+  return launch_adamw_read(ctx, codes, exps, n, which, out);
 }
 
 }  // extern "C"

@@ -133,6 +133,59 @@ int launch_gate_grad(const LaunchCtx& ctx, const occult_desc_t& ds, const int32_
 // one bounded wait that nothing completes (complete = 0) or that completes
 int launch_selftest_wait(const LaunchCtx& ctx, int complete, uint64_t limit_ns);
 
+// Block norm (occult_block_norm, occult_block_norm_bwd): the pointers of both
+// directions, NULL where a call has none.
+struct NormArgs {
+  int T, d, gate_kind;
+  float eps, res_scale;
+  const void* r;          // forward: r; backward: r' (r without y)
+  const float* y;
+  const void *w_post, *w_pre;
+  const float* gate;
+  // forward outputs
+  void *r_out, *x;
+  float *rstd_post_out, *rstd_pre_out;
+  // backward
+  const void* dr_out;
+  const float *dx, *rstd_post, *rstd_pre;
+  void *dr, *dy;
+  float *dw_post, *dgate, *dw_pre;
+};
+// rows of partial column sums of the backward
+constexpr int kNormMaxParts = 608;
+constexpr int kNormMaxWidth = 16384;
+int norm_bwd_parts(int T);
+size_t block_norm_bwd_ws_bytes(const occult_desc_t& ds);
+int launch_block_norm(const LaunchCtx& ctx, const NormArgs& a, int res_dtype, int dtype);
+int launch_block_norm_bwd(const LaunchCtx& ctx, const NormArgs& a, int res_dtype, int dtype,
+                          void* ws);
+
+// Balance loss over G groups of L tokens.
+struct BalanceArgs {
+  int T, Ne, k, Nd, L, G;
+  float coef, coef_dev, coef_z;
+  const float* logits;
+  const int32_t *ids, *e2v;
+  const uint8_t* mask;
+  int32_t* counts;
+  float *grad_w, *loss, *ws;
+  float* group_terms;     // in ws: {expert, device, sum lse^2} of every group
+  int* group_n;           // in ws: unmasked tokens of every group
+  const float* dloss;
+  float* dlogits;
+  int accumulate;
+};
+// number of groups; *L receives the tokens of a group
+int balance_groups(int T, int group_len, int* L);
+size_t balance_ws_bytes(const occult_desc_t& ds, int group_len);
+int launch_balance_loss(const LaunchCtx& ctx, BalanceArgs a);
+int launch_balance_grad(const LaunchCtx& ctx, const BalanceArgs& a);
+
+int launch_adamw(const LaunchCtx& ctx, const occult_adamw_t& opt, const occult_param_t* params,
+                 int n_params);
+int launch_adamw_read(const LaunchCtx& ctx, const uint8_t* codes, const uint8_t* exps, int64_t n,
+                      int which, void* out);
+
 // s[t] = sigmoid(w . x_t) for the shared-expert gate
 int launch_shared_gate(const LaunchCtx& ctx, const occult_desc_t& ds, const void* x,
                        const void* w_sg, float* s_gate);

@@ -110,6 +110,7 @@ int occult_check_desc(const occult_desc_t* desc);
 #define OCCULT_WS_BUILD_BRIM     0   /* occult_build_brim for desc->T tokens       */
 #define OCCULT_WS_PROFILE_COACT  1   /* occult_profile_coact for n_tok tokens      */
 #define OCCULT_WS_EXPERT_BWD     2   /* occult_expert_bwd for desc->T tokens       */
+#define OCCULT_WS_BLOCK_NORM_BWD 3   /* occult_block_norm_bwd for desc->T tokens   */
 
 /* Host: bytes of device workspace `ws` the entry point selected by `op` needs
  * (n_tok: profiled tokens, used by OCCULT_WS_PROFILE_COACT only).  The other
@@ -619,6 +620,205 @@ int occult_gate_grad(const occult_desc_t* desc, const int32_t* ids, const int32_
 int occult_profile_coact(const occult_desc_t* desc, const int32_t* ids, int32_t n_tok,
                          const uint32_t* vmask, int64_t* C, float* P, int64_t* ct_hist,
                          void* ws, size_t ws_bytes, occult_stream_t stream);
+
+/*
+ * The operators around the layer in a training step: the norms before and after
+ * a block with its gate and residual scale, the router's balance loss, and the
+ * AdamW update of the weights.  The paper trains the layer (Sec. 4) but leaves
+ * these to its host framework and gives no pseudo-code; each one's formula is
+ * stated here.
+ */
+
+/* Kinds of the gate on a block's output. */
+#define OCCULT_GATE_NONE     0
+#define OCCULT_GATE_CHANNEL  1   /* fp32 [d]: one factor for every channel          */
+#define OCCULT_GATE_TOKEN    2   /* fp32 [T]: one factor for every token            */
+
+/* Options of the block norm (host). */
+typedef struct occult_norm {
+  float eps;            /* added to the mean square; > 0                            */
+  float res_scale;      /* a: factor of the residual stream                         */
+  int32_t gate_kind;    /* OCCULT_GATE_*                                            */
+  int32_t res_dtype;    /* type of the residual stream: OCCULT_F32 | OCCULT_BF16    */
+} occult_norm_t;
+
+/*
+ * occult_block_norm -- the norm after a block, its gate, the residual sum and the
+ * norm before the next block, in one pass over the rows (RMS norms; per token t):
+ *   b  = y * rstd_post * w_post,   rstd_post = (mean(y^2) + eps)^(-1/2)
+ *        (b = y when w_post is NULL: no norm after the block)
+ *   r' = res_scale * r + gate * b
+ *   x  = r' * rstd_pre * w_pre,    rstd_pre = (mean(r'^2) + eps)^(-1/2)
+ * x and rstd_pre come from the fp32 r', before it is rounded to the stream's type.
+ *   opt    host.
+ *   r      [T, d] in opt->res_dtype, the residual stream.
+ *   y      fp32 [T, d] nullable: the block's output (e.g. of occult_combine).
+ *          NULL: only the norm before the first block, r' = r; then w_post, gate,
+ *          r_out and rstd_post must be NULL and gate_kind OCCULT_GATE_NONE.
+ *   w_post [d] layer dtype, nullable (needs y).
+ *   gate   fp32 [d] or [T] by opt->gate_kind; NULL for OCCULT_GATE_NONE.
+ *   w_pre  [d] layer dtype, nullable (needed without y): NULL after the last
+ *          block; then x and rstd_pre must be NULL.
+ *   r_out  out [T, d] in opt->res_dtype (with y); may be r itself.
+ *   x      out [T, d] layer dtype (with w_pre).
+ *   rstd_post, rstd_pre  out fp32 [T], nullable: kept for the backward.
+ * Apart from r_out = r no output may overlap an input.  d <= 16384.
+ */
+int occult_block_norm(const occult_desc_t* desc, const occult_norm_t* opt, const void* r,
+                      const float* y, const void* w_post, const float* gate, const void* w_pre,
+                      void* r_out, void* x, float* rstd_post, float* rstd_pre,
+                      occult_stream_t stream);
+
+/*
+ * occult_block_norm_bwd -- gradients of occult_block_norm.  With n = r' * rstd_pre,
+ * m = y * rstd_post (m = y, and the factor w_post left out, without w_post) and
+ * D the whole gradient at r':
+ *   D      = dr_out + rstd_pre * (w_pre dx - n * mean(w_pre dx n))
+ *   dr     = res_scale * D              (without y: dr = D)
+ *   dy     = rstd_post * (u - m * mean(u m)),  u = gate * w_post * D
+ *            (without w_post: dy = gate * D)
+ *   dw_pre = sum_t dx n,   dw_post = sum_t gate * D m,
+ *   dgate  = sum_t D w_post m  ([d])  or  sum_channels D w_post m  ([T]).
+ *   dr_out [T, d] in opt->res_dtype, nullable (zero: nothing reads r' but x).
+ *   dx     fp32 [T, d], gradient of x (with w_pre).
+ *   r_out  [T, d] in opt->res_dtype: r' as the forward wrote it (r without y);
+ *          read with w_pre only.
+ *   y      as in the forward; with neither w_post nor a gate it is not read, but
+ *          must still be given for dy to be written.
+ *   rstd_post, rstd_pre  from the forward.
+ *   dr     out [T, d] in opt->res_dtype; may be dr_out itself.
+ *   dy     out [T, d] layer dtype (with y), as the layer's backward takes it.
+ *   dw_post, dw_pre  out fp32 [d];  dgate  out fp32 [d] or [T].  Written, not
+ *          accumulated; sums over the tokens run in a fixed order.
+ *   ws     occult_workspace_size(OCCULT_WS_BLOCK_NORM_BWD) bytes.
+ * An output must be given exactly when its forward input was; apart from
+ * dr = dr_out none may overlap an input.
+ */
+int occult_block_norm_bwd(const occult_desc_t* desc, const occult_norm_t* opt,
+                          const void* dr_out, const float* dx, const void* r_out, const float* y,
+                          const void* w_post, const float* gate, const void* w_pre,
+                          const float* rstd_post, const float* rstd_pre, void* dr, void* dy,
+                          float* dw_post, float* dgate, float* dw_pre, void* ws,
+                          size_t ws_bytes, occult_stream_t stream);
+
+/* Options of the balance loss (host). */
+typedef struct occult_balance {
+  float coef;           /* weight of the expert term                                */
+  float coef_dev;       /* weight of the device term                                */
+  float coef_z;         /* weight of the z term                                     */
+  int32_t group_len;    /* tokens of a group (a sequence); 0: the batch is one      */
+} occult_balance_t;
+
+/* Host: number of groups, ceil(T / group_len), at least 1; and workspace bytes of
+ * occult_balance_loss. */
+int occult_balance_workspace_size(const occult_desc_t* desc, const occult_balance_t* opt,
+                                  size_t* bytes);
+
+/*
+ * occult_balance_loss -- per-expert counts and the router's auxiliary losses.
+ * The tokens are cut into groups of group_len (the last may be shorter); with
+ * p_t = softmax(logits_t), over the N_g unmasked tokens of group g
+ *   c_ge = slots of those tokens that chose expert e,  f_ge = Ne c_ge / (k N_g),
+ *   P_ge = mean of p_te;   A = groups with an unmasked token, N = sum_g N_g
+ *   expert = 1/A sum_g sum_e f_ge P_ge
+ *   device = 1/A sum_g sum_d (mean of f_ge over e on d) (sum of P_ge over e on d)
+ *   z      = 1/N sum_t (log sum_e exp logits_te)^2
+ * (all 0 when every token is masked).
+ *   logits  fp32 [T, Ne];  ids int32 [T, k] from the router (an id outside
+ *           [0, Ne), a dropped slot, counts nothing).
+ *   expert_to_vdev  int32 [Ne].
+ *   mask    uint8 [T] nullable: tokens with 0 take no part; their logits and ids
+ *           may hold anything.
+ *   counts  out int32 [G, Ne]: c_ge.
+ *   grad_w  out fp32 [G*Ne + 1]: what occult_balance_grad needs.
+ *   loss    out fp32 [4]: {coef expert + coef_dev device + coef_z z, expert,
+ *           device, z}.
+ * Every sum runs in a fixed order.
+ */
+int occult_balance_loss(const occult_desc_t* desc, const occult_balance_t* opt,
+                        const float* logits, const int32_t* ids, const int32_t* expert_to_vdev,
+                        const uint8_t* mask, int32_t* counts, float* grad_w, float* loss,
+                        void* ws, size_t ws_bytes, occult_stream_t stream);
+
+/*
+ * occult_balance_grad -- gradient of loss[0] with respect to the logits (the
+ * counts are constants: the choice of experts is piecewise constant):
+ *   dlogits_te = dloss * (p_te (w_ge - sum_j p_tj w_gj) + w_z lse_t p_te),
+ *   w_ge = (coef f_ge + coef_dev mean of f_g over e's device) / (A N_g),
+ *   w_z = 2 coef_z / N;  nothing for masked tokens.
+ *   grad_w  from occult_balance_loss with the same options and mask.
+ *   dloss   fp32 [1] nullable (1): the gradient of the total.
+ *   dlogits fp32 [T, Ne].  accumulate = 1: added to what it holds (e.g. from
+ *           occult_router_grad); 0: written (zeros for masked tokens).
+ */
+int occult_balance_grad(const occult_desc_t* desc, const occult_balance_t* opt,
+                        const float* logits, const float* grad_w, const uint8_t* mask,
+                        const float* dloss, float* dlogits, int32_t accumulate,
+                        occult_stream_t stream);
+
+/* Elements that share one exponent of an 8-bit optimizer state. */
+#define OCCULT_STATE_BLOCK  256
+#define OCCULT_STATE_M      0
+#define OCCULT_STATE_V      1
+
+/* Options of an AdamW step (host).  Doubles, so that 1 - beta2 keeps its digits. */
+typedef struct occult_adamw {
+  double lr, beta1, beta2, eps, weight_decay;
+  int32_t step;             /* this step's number, from 1                           */
+  int32_t state_bits;       /* 32 | 8                                               */
+  uint32_t seed;            /* of the roundings by draw                             */
+  uint32_t reserved;        /* 0                                                    */
+  const float* grad_scale;  /* device fp32 [1] nullable: factor of every gradient
+                               (loss scale, clipping)                               */
+} occult_adamw_t;
+
+/* One tensor of an AdamW step (a host record of device pointers). */
+typedef struct occult_param {
+  void* param;          /* [n] in `dtype`, in/out                                   */
+  float* master;        /* fp32 [n] in/out, nullable (bf16 parameters only)         */
+  const float* grad;    /* fp32 [n]                                                 */
+  void* m;              /* first moment in/out: fp32 [n], or its codes uint8 [n]    */
+  void* v;              /* second moment likewise (8 bits: codes of its root)       */
+  uint8_t* m_exp;       /* 8 bits: [ceil(n / OCCULT_STATE_BLOCK)] exponents         */
+  uint8_t* v_exp;
+  int64_t n;            /* elements (0: nothing to do)                              */
+  int64_t first;        /* position of the first element in the stream of draws     */
+  int32_t dtype;        /* OCCULT_F32 | OCCULT_BF16                                 */
+  int32_t reserved;     /* 0                                                        */
+} occult_param_t;
+
+/*
+ * occult_adamw -- one AdamW step over n_params tensors in one launch for every
+ * 256 of them:
+ *   g = grad_scale * grad
+ *   m = beta1 m + (1 - beta1) g,   v = beta2 v + (1 - beta2) g^2
+ *   w = (1 - lr weight_decay) w - lr / (1 - beta1^step) * m
+ *                                   / (sqrt(v / (1 - beta2^step)) + eps)
+ * in fp32 on the fp32 parameter, the master copy (the bf16 parameter is then its
+ * nearest value) or the widened bf16 parameter.  A bf16 parameter without a master
+ * is rounded up or down by a draw, so that updates below half a unit are not lost.
+ *   opt, params  host; copied at launch.  Pointers are 16-byte aligned (m_exp and
+ *                v_exp need no alignment); tensors do not overlap.
+ * state_bits 8 keeps m and sqrt(v) as 8-bit floats under one exponent E for every
+ * OCCULT_STATE_BLOCK elements of a tensor: of the binades below 2^(E+1) the largest
+ * sixteen, m with a sign and 8 steps a binade, sqrt(v) with 16; m below them is 0,
+ * a positive sqrt(v) the lowest code (so it never vanishes under m).  Values are
+ * rounded up or down by a draw, in expectation exact: rounding to nearest would
+ * hold v fast, as a step moves it by less than half a unit.  The draws are a hash
+ * of (first + i, step, seed): a tensor cut into several gives the same result.  A
+ * block that takes an infinity or NaN reads as NaN from then on.  All-zero codes
+ * and exponents are a fresh state.
+ */
+int occult_adamw(const occult_adamw_t* opt, const occult_param_t* params, int32_t n_params,
+                 occult_stream_t stream);
+
+/*
+ * occult_adamw_read -- the values an 8-bit state stands for, exactly, in bf16.
+ *   codes  uint8 [n], exps uint8 [ceil(n / OCCULT_STATE_BLOCK)] of one tensor;
+ *   which  OCCULT_STATE_M: m, OCCULT_STATE_V: sqrt(v);   out bf16 [n].
+ */
+int occult_adamw_read(const uint8_t* codes, const uint8_t* exps, int64_t n, int32_t which,
+                      void* out, occult_stream_t stream);
 
 #ifdef __cplusplus
 }

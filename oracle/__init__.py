@@ -20,6 +20,13 @@ across Experts for Accelerated Parallel MoE Training and Inference" (arXiv
 * ``placement`` -- Algorithm 1 expert placement.
 * ``backward``  -- analytic fp64 gradients of Eq. 1 for the training workload.
 
+The operators around the layer in a training step, whose formulas the paper leaves
+to its host framework, are written from their definitions:
+
+* ``block_norm`` -- RMS norms before and after a block, gate, residual scale.
+* ``balance``    -- expert, device and z losses of the router, with gradient.
+* ``adamw``      -- AdamW, and the 8-bit states as real arithmetic.
+
 Floating point is fp64 throughout, computed from the exact fp32/bf16 input
 values.  Where floating point decides an integer (top-k choice) the decision is
 taken on the fp32 inputs exactly as given, so both sides decide identically.
