@@ -202,6 +202,11 @@ def _dev(t: Optional[torch.Tensor], dtype: Optional[torch.dtype] = None, numel: 
     return ctypes.c_void_p(t.data_ptr())
 
 
+def _buf(t: torch.Tensor) -> int:
+    """Size in bytes of a workspace; the library compares it with what it needs."""
+    return t.numel() * t.element_size()
+
+
 def _stream(stream) -> ctypes.c_void_p:
     if stream is None:
         stream = torch.cuda.current_stream()
@@ -640,7 +645,6 @@ def occult_block_norm_bwd(desc, opt, dr_out, r_out, dr, ws, dx=None, y=None, w_p
     """Gradients of occult_block_norm; dr_out (or, without w_pre, r_out) may be None."""
     T, d = desc.T, desc.d
     dt, rt, f32 = desc.torch_dtype, _res_torch_dtype(opt), torch.float32
-    need = workspace_size(desc, WS_BLOCK_NORM_BWD)
     n_gate = _gate_len(desc, opt)
     _call("occult_block_norm_bwd", ctypes.byref(desc), ctypes.byref(opt),
           _dev(dr_out, rt, T * d, "dr_out", nullable=True),
@@ -655,7 +659,7 @@ def occult_block_norm_bwd(desc, opt, dr_out, r_out, dr, ws, dx=None, y=None, w_p
           _dev(dw_post, f32, d, "dw_post", nullable=True),
           _dev(dgate, f32, n_gate, "dgate", nullable=True),
           _dev(dw_pre, f32, d, "dw_pre", nullable=True),
-          _dev(ws, torch.uint8, need, "ws", nullable=need == 0), need, _stream(stream))
+          _dev(ws, torch.uint8, 0, "ws"), _buf(ws), _stream(stream))
 
 
 def balance_groups(desc, opt) -> int:
@@ -675,13 +679,12 @@ def occult_balance_loss(desc, opt, logits, ids, expert_to_vdev, counts, grad_w, 
     """Per-expert counts and the auxiliary losses of the router."""
     T, Ne, k, G = desc.T, desc.n_experts, desc.top_k, balance_groups(desc, opt)
     i32, f32 = torch.int32, torch.float32
-    need = balance_workspace_size(desc, opt)
     _call("occult_balance_loss", ctypes.byref(desc), ctypes.byref(opt),
           _dev(logits, f32, T * Ne, "logits"), _dev(ids, i32, T * k, "ids"),
           _dev(expert_to_vdev, i32, Ne, "expert_to_vdev"),
           _dev(mask, torch.uint8, T, "mask", nullable=True), _dev(counts, i32, G * Ne, "counts"),
           _dev(grad_w, f32, G * Ne + 1, "grad_w"), _dev(loss, f32, 4, "loss"),
-          _dev(ws, torch.uint8, need, "ws"), need, _stream(stream))
+          _dev(ws, torch.uint8, 0, "ws"), _buf(ws), _stream(stream))
 
 
 def occult_balance_grad(desc, opt, logits, grad_w, dlogits, mask=None, dloss=None,

@@ -95,14 +95,8 @@ __device__ __forceinline__ uint32_t bf16_by_draw(float w, uint32_t draw16) {
   return (bits + draw16) >> 16;
 }
 
-// The elements i0 .. i0+3 of a tensor (as many as `live`).
-template <typename T>
-__device__ __forceinline__ void load4(const T* p, int live, float (&f)[4]) {
-#pragma unroll
-  for (int j = 0; j < 4; ++j) f[j] = j < live ? to_f32(p[j]) : 0.f;
-}
-template <>
-__device__ __forceinline__ void load4<float>(const float* p, int live, float (&f)[4]) {
+// Four consecutive elements of a tensor, the first `live` of them in range.
+__device__ __forceinline__ void load4(const float* p, int live, float (&f)[4]) {
   if (live == 4) {
     const float4 v = *reinterpret_cast<const float4*>(p);
     f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w;
@@ -110,6 +104,24 @@ __device__ __forceinline__ void load4<float>(const float* p, int live, float (&f
 #pragma unroll
     for (int j = 0; j < 4; ++j) f[j] = j < live ? p[j] : 0.f;
   }
+}
+__device__ __forceinline__ void load4(const __nv_bfloat16* p, int live, float (&f)[4]) {
+  if (live == 4) {
+    const uint2 u = *reinterpret_cast<const uint2*>(p);
+    f[0] = __uint_as_float(u.x << 16); f[1] = __uint_as_float(u.x & 0xffff0000u);
+    f[2] = __uint_as_float(u.y << 16); f[3] = __uint_as_float(u.y & 0xffff0000u);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) f[j] = j < live ? to_f32(p[j]) : 0.f;
+  }
+}
+__device__ __forceinline__ uint32_t load4(const uint8_t* p, int live) {
+  if (live == 4) return *reinterpret_cast<const uint32_t*>(p);
+  uint32_t w = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (j < live) w |= static_cast<uint32_t>(p[j]) << (8 * j);
+  return w;
 }
 __device__ __forceinline__ void store4(float* p, int live, const float (&f)[4]) {
   if (live == 4) {
@@ -120,73 +132,91 @@ __device__ __forceinline__ void store4(float* p, int live, const float (&f)[4]) 
       if (j < live) p[j] = f[j];
   }
 }
+__device__ __forceinline__ void store4(uint16_t* p, int live, const uint32_t (&h)[4]) {
+  if (live == 4) {
+    *reinterpret_cast<uint2*>(p) =
+        make_uint2(__byte_perm(h[0], h[1], 0x5410), __byte_perm(h[2], h[3], 0x5410));
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (j < live) p[j] = static_cast<uint16_t>(h[j]);
+  }
+}
+__device__ __forceinline__ void store4(uint8_t* p, int live, const uint32_t (&c)[4]) {
+  if (live == 4) {
+    *reinterpret_cast<uint32_t*>(p) =
+        __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (j < live) p[j] = static_cast<uint8_t>(c[j]);
+  }
+}
 
 // One block of 256 elements by one warp: lane l has elements 4l .. 4l+3 of both
-// halves, so that every access of the warp is to consecutive words.
+// halves, so that every access of the warp is to consecutive words.  Products are
+// rounded before they are summed (no fused multiply-add in the moments and the
+// root, which a code is cut from): the same bits as the formula term by term.
 template <int BITS, int KIND>
 __device__ __forceinline__ void step_block(const AdamTable& a, const Tensor& T, int64_t blk,
                                            float gs) {
   const int lane = threadIdx.x & 31;
-  const int64_t b0 = blk * kBlock;
-  uint32_t em = 0, ev = 0;
+  const int64_t b0 = blk * kBlock + lane * 4;
+  int live[2];
+  float g[2][4], w[2][4], m[2][4], v[2][4], s[2][4];
+  uint32_t cm[2], cv[2], em = 0, ev = 0;
   if (BITS == 8) { em = T.m_exp[blk]; ev = T.v_exp[blk]; }
-  float m[2][4], s[2][4];
-  uint32_t top_m = 0, top_v = 0;
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    const int64_t i = b0 + h * 128 + lane * 4;
-    const int64_t left = T.n - i;
-    const int live = left >= 4 ? 4 : (left > 0 ? static_cast<int>(left) : 0);
-    float g[4], w[4], v[4];
-    load4(T.grad + i, live, g);
-    if (KIND == KIND_MASTER) load4(static_cast<const float*>(T.master) + i, live, w);
-    else if (KIND == KIND_F32) load4(static_cast<const float*>(T.param) + i, live, w);
-    else load4(static_cast<const __nv_bfloat16*>(T.param) + i, live, w);
+    const int64_t i = b0 + h * 128, left = T.n - i;
+    live[h] = left >= 4 ? 4 : (left > 0 ? static_cast<int>(left) : 0);
+    load4(T.grad + i, live[h], g[h]);
+    if (KIND == KIND_MASTER) load4(static_cast<const float*>(T.master) + i, live[h], w[h]);
+    else if (KIND == KIND_F32) load4(static_cast<const float*>(T.param) + i, live[h], w[h]);
+    else load4(static_cast<const __nv_bfloat16*>(T.param) + i, live[h], w[h]);
     if (BITS == 32) {
-      load4(static_cast<const float*>(T.m) + i, live, m[h]);
-      load4(static_cast<const float*>(T.v) + i, live, v);
+      load4(static_cast<const float*>(T.m) + i, live[h], m[h]);
+      load4(static_cast<const float*>(T.v) + i, live[h], v[h]);
     } else {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        m[h][j] = decode<3>(j < live ? static_cast<const uint8_t*>(T.m)[i + j] : 0u, em);
-        const float r = decode<4>(j < live ? static_cast<const uint8_t*>(T.v)[i + j] : 0u, ev);
-        v[j] = r * r;
-      }
-    }
-    float out[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float gj = gs * g[j];
-      m[h][j] = fmaf(a.b1, m[h][j], a.c1 * gj);
-      v[j] = fmaf(a.b2, v[j], a.c2 * gj * gj);
-      s[h][j] = sqrtf(v[j]);
-      out[j] = fmaf(-a.rate, m[h][j] / fmaf(s[h][j], a.inv_root, a.eps), w[j] * a.keep);
-      if (j < live) {
-        top_m = max(top_m, __float_as_uint(m[h][j]) & 0x7fffffffu);
-        top_v = max(top_v, __float_as_uint(s[h][j]) & 0x7fffffffu);
-      }
-    }
-    if (BITS == 32) {
-      store4(static_cast<float*>(T.m) + i, live, m[h]);
-      store4(static_cast<float*>(T.v) + i, live, v);
-    }
-    if (KIND == KIND_F32) store4(static_cast<float*>(T.param) + i, live, out);
-    if (KIND == KIND_MASTER) store4(T.master + i, live, out);
-    if (KIND != KIND_F32) {
-      uint16_t* p = static_cast<uint16_t*>(T.param) + i;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (j >= live) continue;
-        if (KIND == KIND_MASTER) {
-          p[j] = __bfloat16_as_ushort(__float2bfloat16_rn(out[j]));
-        } else {
-          const uint32_t h32 = mix(static_cast<uint32_t>(T.first + i + j) + a.key);
-          p[j] = static_cast<uint16_t>(bf16_by_draw(out[j], (h32 * kMul1) >> 16));
-        }
-      }
+      cm[h] = load4(static_cast<const uint8_t*>(T.m) + i, live[h]);
+      cv[h] = load4(static_cast<const uint8_t*>(T.v) + i, live[h]);
     }
   }
+  uint32_t top_m = 0, top_v = 0, draw[2][4];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int64_t i = b0 + h * 128;
+    float out[4];
+    uint32_t half[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (BITS == 8) {
+        m[h][j] = decode<3>((cm[h] >> (8 * j)) & 0xffu, em);
+        const float r = decode<4>((cv[h] >> (8 * j)) & 0xffu, ev);
+        v[h][j] = r * r;
+      }
+      if (BITS == 8 || KIND == KIND_BF16)
+        draw[h][j] = mix(static_cast<uint32_t>(T.first + i) + j + a.key);
+      const float gj = gs * g[h][j];
+      m[h][j] = __fadd_rn(__fmul_rn(a.b1, m[h][j]), __fmul_rn(a.c1, gj));
+      v[h][j] = __fadd_rn(__fmul_rn(a.b2, v[h][j]), __fmul_rn(__fmul_rn(a.c2, gj), gj));
+      s[h][j] = sqrtf(v[h][j]);
+      out[j] = fmaf(-a.rate, __fdividef(m[h][j], fmaf(s[h][j], a.inv_root, a.eps)), w[h][j] * a.keep);
+      top_m = max(top_m, __float_as_uint(m[h][j]) & 0x7fffffffu);
+      top_v = max(top_v, __float_as_uint(s[h][j]) & 0x7fffffffu);
+      if (KIND == KIND_MASTER) half[j] = __bfloat16_as_ushort(__float2bfloat16_rn(out[j]));
+      if (KIND == KIND_BF16) half[j] = bf16_by_draw(out[j], (draw[h][j] * kMul1) >> 16);
+    }
+    if (BITS == 32) {
+      store4(static_cast<float*>(T.m) + i, live[h], m[h]);
+      store4(static_cast<float*>(T.v) + i, live[h], v[h]);
+    }
+    if (KIND == KIND_F32) store4(static_cast<float*>(T.param) + i, live[h], out);
+    if (KIND == KIND_MASTER) store4(T.master + i, live[h], out);
+    if (KIND != KIND_F32) store4(static_cast<uint16_t*>(T.param) + i, live[h], half);
+  }
   if (BITS == 8) {
+    // (elements out of range are zeros here: they raise no exponent)
     const uint32_t new_m = block_exp<3>(warp_max_u32(top_m));
     const uint32_t new_v = block_exp<4>(warp_max_u32(top_v));
     if (lane == 0) {
@@ -195,16 +225,14 @@ __device__ __forceinline__ void step_block(const AdamTable& a, const Tensor& T, 
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int64_t i = b0 + h * 128 + lane * 4;
+      uint32_t km[4], kv[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        if (i + j >= T.n) continue;
-        const uint32_t h32 = mix(static_cast<uint32_t>(T.first + i + j) + a.key);
-        static_cast<uint8_t*>(T.m)[i + j] =
-            static_cast<uint8_t>(encode<3>(__float_as_uint(m[h][j]), h32 & 0xffffu, new_m));
-        static_cast<uint8_t*>(T.v)[i + j] =
-            static_cast<uint8_t>(encode<4>(__float_as_uint(s[h][j]), h32 >> 16, new_v));
+        km[j] = encode<3>(__float_as_uint(m[h][j]), draw[h][j] & 0xffffu, new_m);
+        kv[j] = encode<4>(__float_as_uint(s[h][j]), draw[h][j] >> 16, new_v);
       }
+      store4(static_cast<uint8_t*>(T.m) + b0 + h * 128, live[h], km);
+      store4(static_cast<uint8_t*>(T.v) + b0 + h * 128, live[h], kv);
     }
   }
 }
@@ -232,15 +260,28 @@ __global__ void __launch_bounds__(kAdamThreads) adamw_kernel(const __grid_consta
   }
 }
 
+// The values of 8-bit states: a thread turns 8 codes into 16 bytes.
 template <int MANT>
 __global__ void __launch_bounds__(256)
 adamw_read_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ exps, int64_t n,
                   __nv_bfloat16* __restrict__ out) {
   pdl_wait();
   pdl_trigger();
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < n;
-       i += static_cast<int64_t>(gridDim.x) * 256)
-    out[i] = __float2bfloat16_rn(decode<MANT>(codes[i], exps[i / kBlock]));
+  const int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 8;
+  if (i >= n) return;
+  const uint32_t e = exps[i / kBlock];
+  if (i + 8 <= n) {
+    const uint2 c = *reinterpret_cast<const uint2*>(codes + i);
+    float f[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      f[j] = decode<MANT>((c.x >> (8 * j)) & 0xffu, e);
+      f[4 + j] = decode<MANT>((c.y >> (8 * j)) & 0xffu, e);
+    }
+    st_v4(out + i, pack16(f, __nv_bfloat16()));
+  } else {
+    for (int64_t j = i; j < n; ++j) out[j] = __float2bfloat16_rn(decode<MANT>(codes[j], e));
+  }
 }
 
 }  // namespace
@@ -290,8 +331,9 @@ int launch_adamw(const LaunchCtx& ctx, const occult_adamw_t& o, const occult_par
 
 int launch_adamw_read(const LaunchCtx& ctx, const uint8_t* codes, const uint8_t* exps, int64_t n,
                       int which, void* out) {
-  const int64_t need = (n + 255) / 256, cap = static_cast<int64_t>(ctx.num_sms) * 16;
-  const int grid = static_cast<int>(need < cap ? need : cap);
+  const int64_t need = (n + 2047) / 2048;
+  if (need > 0x7fffffff) return OCCULT_ERR_UNSUPPORTED;
+  const unsigned grid = static_cast<unsigned>(need);
   __nv_bfloat16* o = static_cast<__nv_bfloat16*>(out);
   return cuda_status(
       which == OCCULT_STATE_M

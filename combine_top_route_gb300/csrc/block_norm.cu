@@ -59,52 +59,6 @@ __device__ __forceinline__ void block_sum(float (&v)[N], float (*s_red)[N]) {
   }
 }
 
-// One CTA a row; the fp32 r' of the row waits in shared memory for its mean square.
-template <typename R, typename L>
-__global__ void __launch_bounds__(kNormThreads) norm_fwd_kernel(NormArgs a) {
-  extern __shared__ float s_row[];
-  __shared__ float s_red[kNormThreads / 32][1];
-  pdl_wait();
-  pdl_trigger();
-  const L* w_post = static_cast<const L*>(a.w_post);
-  const L* w_pre = static_cast<const L*>(a.w_pre);
-  for (int t = blockIdx.x; t < a.T; t += gridDim.x) {
-    const size_t base = static_cast<size_t>(t) * a.d;
-    float rp = 1.f;
-    if (w_post) {
-      float s[1] = {0.f};
-      for (int c = threadIdx.x * 4; c < a.d; c += kNormThreads * 4) {
-        const float4 y = ld4(a.y + base + c);
-        s[0] += dot4(y, y);
-      }
-      block_sum<1>(s, s_red);
-      rp = rsqrtf(s[0] / a.d + a.eps);
-      if (threadIdx.x == 0 && a.rstd_post_out) a.rstd_post_out[t] = rp;
-    }
-    const float tok = a.gate_kind == OCCULT_GATE_TOKEN ? a.gate[t] : 1.f;
-    float q[1] = {0.f};
-    for (int c = threadIdx.x * 4; c < a.d; c += kNormThreads * 4) {
-      float4 r = ld4(static_cast<const R*>(a.r) + base + c);
-      if (a.y) {
-        float4 b = scale4(ld4(a.y + base + c), rp);
-        if (w_post) b = mul4(b, ld4(w_post + c));
-        if (a.gate_kind == OCCULT_GATE_CHANNEL) b = mul4(b, ld4(a.gate + c));
-        r = fma4(b, tok, scale4(r, a.res_scale));
-        st4(static_cast<R*>(a.r_out) + base + c, r);
-      }
-      q[0] += dot4(r, r);
-      *reinterpret_cast<float4*>(s_row + c) = r;
-    }
-    if (!w_pre) continue;
-    block_sum<1>(q, s_red);
-    const float rq = rsqrtf(q[0] / a.d + a.eps);
-    if (threadIdx.x == 0 && a.rstd_pre_out) a.rstd_pre_out[t] = rq;
-    for (int c = threadIdx.x * 4; c < a.d; c += kNormThreads * 4)
-      st4(static_cast<L*>(a.x) + base + c,
-          mul4(scale4(*reinterpret_cast<const float4*>(s_row + c), rq), ld4(w_pre + c)));
-  }
-}
-
 // Backward, one CTA a row.  D is linear in mean(w_pre dx n), so one round of sums
 // gives every mean: with g = w_pre dx, D0 = dr_out + rstd_pre g and
 // q = gate w_post m,
@@ -181,17 +135,315 @@ __global__ void __launch_bounds__(kNormThreads) norm_bwd_kernel(NormArgs a, floa
   for (int c = threadIdx.x * 4; c < 2 * a.d; c += kNormThreads * 4) st4(row + c, ld4(s_cols + c));
 }
 
-// Adds the CTAs' partial rows in order and turns the second sum into dw_post and a
-// channel gate's gradient.
-template <typename L>
-__global__ void __launch_bounds__(kNormThreads)
-norm_bwd_cols_kernel(NormArgs a, const float* __restrict__ part, int n_part) {
+// ---- rows held by groups of warps ------------------------------------------------
+// A group of G warps takes a row at a time; a thread owns the U units of four
+// columns 4 (u 32 G + j), j its place in the group, of every row it sees.  The
+// groups of a CTA (8 / G, at least one) work apart from each other.
+template <int G>
+struct Group {
+  static constexpr int kThreads = G > 8 ? 32 * G : 256;
+  static constexpr int kGroups = kThreads / (32 * G);
+  __device__ static int index() { return threadIdx.x / (32 * G); }
+  __device__ static int place() { return threadIdx.x % (32 * G); }
+  __device__ static void sync() {
+    if (G == 1) __syncwarp();
+    else if (kGroups == 1) __syncthreads();
+    else asm volatile("bar.sync %0, %1;" :: "r"(index() + 1), "n"(32 * G) : "memory");
+  }
+};
+
+// Sums of four values over a group in a fixed order; every thread gets them.  The
+// caller alternates between two s_red buffers, so that one sync a sum is enough.
+template <int G>
+__device__ __forceinline__ float4 group_sum(float4 v, float4* s_red) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
+    v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
+    v.z += __shfl_xor_sync(0xffffffffu, v.z, o);
+  }
+  if (G == 1) return v;
+  if ((threadIdx.x & 31) == 0) s_red[threadIdx.x >> 5] = v;
+  Group<G>::sync();
+  const float4* mine = s_red + Group<G>::index() * G;
+  v = mine[0];
+#pragma unroll
+  for (int w = 1; w < G; ++w) v = add4(v, mine[w]);
+  return v;
+}
+template <int G>
+__device__ __forceinline__ float group_sum1(float v, float* s_red) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if (G == 1) return v;
+  if ((threadIdx.x & 31) == 0) s_red[threadIdx.x >> 5] = v;
+  Group<G>::sync();
+  const float* mine = s_red + Group<G>::index() * G;
+  v = mine[0];
+#pragma unroll
+  for (int w = 1; w < G; ++w) v += mine[w];
+  return v;
+}
+
+// Forward: the row stays in registers from its loads to its stores.
+template <typename R, typename L, int G, int U>
+__global__ void __launch_bounds__(Group<G>::kThreads) norm_fwd_rows_kernel(NormArgs a) {
+  __shared__ float s_red[2][Group<G>::kThreads / 32];
   pdl_wait();
   pdl_trigger();
-  const int c = blockIdx.x * kNormThreads + threadIdx.x;
-  if (c >= 2 * a.d) return;
+  const L* w_post = static_cast<const L*>(a.w_post);
+  const L* w_pre = static_cast<const L*>(a.w_pre);
+  const int place = Group<G>::place();
+  int flip = 0;
+  const float inv_d = 1.f / a.d;
+  const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int t = blockIdx.x * Group<G>::kGroups + Group<G>::index(); t < a.T;
+       t += gridDim.x * Group<G>::kGroups) {
+    const size_t base = static_cast<size_t>(t) * a.d;
+    const R* r_in = static_cast<const R*>(a.r) + base;
+    float4 r[U], y[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int c = 4 * (u * 32 * G + place);
+      y[u] = a.y && c < a.d ? ld4(a.y + base + c) : zero;
+      r[u] = c < a.d ? ld4(r_in + c) : zero;
+    }
+    if (a.y) {
+      float scale = a.gate_kind == OCCULT_GATE_TOKEN ? a.gate[t] : 1.f;
+      if (w_post) {
+        float s = 0.f;
+#pragma unroll
+        for (int u = 0; u < U; ++u) s += dot4(y[u], y[u]);
+        const float rp = rsqrtf(group_sum1<G>(s, s_red[flip]) * inv_d + a.eps);
+        flip ^= 1;
+        if (place == 0 && a.rstd_post_out) a.rstd_post_out[t] = rp;
+        scale *= rp;
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int c = 4 * (u * 32 * G + place);
+        if (c >= a.d) continue;
+        float4 b = scale4(y[u], scale);
+        if (w_post) b = mul4(b, ld4(w_post + c));
+        if (a.gate_kind == OCCULT_GATE_CHANNEL) b = mul4(b, ld4(a.gate + c));
+        r[u] = fma4(r[u], a.res_scale, b);
+        st4(static_cast<R*>(a.r_out) + base + c, r[u]);
+      }
+    }
+    if (!w_pre) continue;
+    float s = 0.f;
+#pragma unroll
+    for (int u = 0; u < U; ++u) s += dot4(r[u], r[u]);
+    const float rq = rsqrtf(group_sum1<G>(s, s_red[flip]) * inv_d + a.eps);
+    flip ^= 1;
+    if (place == 0 && a.rstd_pre_out) a.rstd_pre_out[t] = rq;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int c = 4 * (u * 32 * G + place);
+      if (c < a.d)
+        st4(static_cast<L*>(a.x) + base + c, mul4(scale4(r[u], rq), ld4(w_pre + c)));
+    }
+  }
+}
+
+// Contiguous bytes (a multiple of 16) from global to shared memory, complete_tx on `bar`.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes,
+                                          uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+      :: "r"(smem_u32(dst)), "l"(src), "r"(bytes), "r"(smem_u32(bar)) : "memory");
+}
+
+// CTAs of an SM in the backward
+__host__ __device__ constexpr int bwd_ctas(int G) { return G > 8 ? 1 : 2; }
+
+// Bytes of one row in the backward's ring: dx, y, then dr_out and r'.
+template <typename R>
+__host__ __device__ __forceinline__ int bwd_row_bytes(int d) {
+  return (2 * d * static_cast<int>(sizeof(float)) + 2 * d * static_cast<int>(sizeof(R)) + 127) &
+         ~127;
+}
+
+// Backward.  The rows of a group come through a ring of `stages` rows in shared
+// memory, filled by bulk copies that run ahead of the arithmetic; the one sync of a
+// row's sums also says that all of the group have read the row, whose place is
+// then refilled.  The column sums stay in the registers of the threads that own
+// the columns, over all the rows of the group.
+template <typename R, typename L, int G, int U>
+__global__ void __launch_bounds__(Group<G>::kThreads, bwd_ctas(G))
+norm_bwd_rows_kernel(NormArgs a, float* part, int stages, int* dev_err) {
+  extern __shared__ __align__(128) unsigned char s_ring[];
+  constexpr int kMaxStages = 4;
+  __shared__ uint64_t s_full[Group<G>::kGroups][kMaxStages];
+  __shared__ float4 s_red[2][Group<G>::kThreads / 32];
+  __shared__ int s_abort;
+  const int group = Group<G>::index(), place = Group<G>::place();
+  const L* w_post = static_cast<const L*>(a.w_post);
+  const L* w_pre = static_cast<const L*>(a.w_pre);
+  const bool chan = a.gate_kind == OCCULT_GATE_CHANNEL, token = a.gate_kind == OCCULT_GATE_TOKEN;
+  const bool use_y = w_post || a.gate_kind != OCCULT_GATE_NONE;
+  const int d = a.d, row_bytes = bwd_row_bytes<R>(d);
+  unsigned char* ring = s_ring + static_cast<size_t>(group) * stages * row_bytes;
+  if (place < stages) mbar_init(&s_full[group][place], 1);
+  if (threadIdx.x == 0) s_abort = 0;
+  mbar_fence_init();
+  __syncthreads();
+  pdl_wait();
+  pdl_trigger();
+
+  const uint32_t tx = (w_pre ? d * (4 + sizeof(R)) : 0) + (use_y ? d * 4 : 0) +
+                      (a.dr_out ? d * sizeof(R) : 0);
+  auto fill = [&](int stage, int t) {  // by the group's first thread
+    unsigned char* p = ring + stage * row_bytes;
+    uint64_t* bar = &s_full[group][stage];
+    const size_t base = static_cast<size_t>(t) * d;
+    mbar_arrive_expect_tx(bar, tx);
+    if (w_pre) {
+      bulk_load(p, a.dx + base, d * 4, bar);
+      bulk_load(p + d * (8 + sizeof(R)), static_cast<const R*>(a.r) + base, d * sizeof(R), bar);
+    }
+    if (use_y) bulk_load(p + d * 4, a.y + base, d * 4, bar);
+    if (a.dr_out)
+      bulk_load(p + d * 8, static_cast<const R*>(a.dr_out) + base, d * sizeof(R), bar);
+  };
+  const int step = gridDim.x * Group<G>::kGroups;
+  const int first = blockIdx.x * Group<G>::kGroups + group;
+  if (place == 0)
+    for (int i = 0; i < stages; ++i)
+      if (static_cast<int64_t>(first) + static_cast<int64_t>(i) * step < a.T)
+        fill(i, first + i * step);
+
+  const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+  float4 wp[U], wq[U];                 // w_pre, and w_post times a channel gate
+  float4 sum_pre[U], sum_post[U];      // sum dx n; sum D m (of a token gate: gate D m)
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int c = 4 * (u * 32 * G + place);
+    wp[u] = w_pre && c < d ? ld4(w_pre + c) : zero;
+    wq[u] = make_float4(1.f, 1.f, 1.f, 1.f);
+    if (c < d) {
+      if (w_post) wq[u] = ld4(w_post + c);
+      if (chan) wq[u] = mul4(wq[u], ld4(a.gate + c));
+    }
+    sum_pre[u] = sum_post[u] = zero;
+  }
+  const float inv_d = 1.f / d;
+  const float out_scale = a.y ? a.res_scale : 1.f;
+  int stage = 0, flip = 0;
+  uint32_t parity = 0;
+  for (int64_t t = first; t < a.T; t += step) {
+    const float rp = w_post ? a.rstd_post[t] : 1.f;
+    const float rq = w_pre ? a.rstd_pre[t] : 0.f;
+    const float tok = token ? a.gate[t] : 1.f;
+    if (!mbar_wait(&s_full[group][stage], parity, &s_abort)) {
+      // gave up: the error is latched, the remaining rows run through without waits
+      latch_error(dev_err, OCCULT_ERR_DEVICE_TIMEOUT);
+      s_abort = 1;
+    }
+    const unsigned char* p = ring + stage * row_bytes;
+    const float* s_dx = reinterpret_cast<const float*>(p);
+    const float* s_y = s_dx + d;
+    const R* s_up = reinterpret_cast<const R*>(s_y + d);
+    const R* s_r = s_up + d;
+    float4 dx[U], r[U], y[U], D[U];
+    // with D0 = dr_out + rstd_pre w_pre dx:  sum w_pre dx r',  sum wq y D0,  sum wq y r'
+    float4 sum = zero;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int c = 4 * (u * 32 * G + place);
+      const bool in = c < d;
+      dx[u] = in && w_pre ? ld4(s_dx + c) : zero;
+      r[u] = in && w_pre ? ld4(s_r + c) : zero;
+      y[u] = in && use_y ? ld4(s_y + c) : zero;
+      D[u] = in && a.dr_out ? ld4(s_up + c) : zero;
+      const float4 g = mul4(dx[u], wp[u]);
+      const float4 q = mul4(y[u], wq[u]);
+      D[u] = fma4(g, rq, D[u]);
+      sum.x += dot4(g, r[u]);
+      sum.y += dot4(q, D[u]);
+      sum.z += dot4(q, r[u]);
+    }
+    sum = group_sum<G>(sum, s_red[flip]);
+    flip ^= 1;
+    if (G == 1) __syncwarp();
+    if (place == 0 && t + static_cast<int64_t>(stages) * step < a.T)
+      fill(stage, static_cast<int>(t + static_cast<int64_t>(stages) * step));
+    if (++stage == stages) { stage = 0; parity ^= 1; }
+    // mean(w_pre dx n) = rstd_pre sum.x / d;  sum wq m D and its mean
+    const float k1 = -rq * rq * rq * sum.x * inv_d;
+    const float qd = rp * fmaf(k1, sum.z, sum.y);
+    if (token && place == 0) a.dgate[t] = qd;
+    const float k2 = -rp * rp * tok * qd * inv_d;
+    const float ru = rp * tok;
+    const size_t base = static_cast<size_t>(t) * d;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int c = 4 * (u * 32 * G + place);
+      if (c >= d) continue;
+      D[u] = fma4(r[u], k1, D[u]);
+      sum_pre[u] = add4(sum_pre[u], mul4(dx[u], scale4(r[u], rq)));
+      st4(static_cast<R*>(a.dr) + base + c, scale4(D[u], out_scale));
+      if (!a.y) continue;
+      sum_post[u] = add4(sum_post[u], mul4(D[u], scale4(y[u], ru)));
+      float4 o = scale4(mul4(D[u], wq[u]), ru);
+      if (w_post) o = fma4(y[u], k2, o);
+      st4(static_cast<L*>(a.dy) + base + c, o);
+    }
+  }
+  if (s_abort && place == 0) {  // copies may still be in flight: give them the limit again
+    volatile int none = 0;
+    for (int i = 0; i < stages; ++i)
+      mbar_wait(&s_full[group][i], i < stage ? parity ^ 1 : parity, &none);
+  }
+  if (!part) return;
+  // the groups' sums, then one row of partial sums a CTA
+  float* row = part + static_cast<size_t>(blockIdx.x) * 2 * d;
+  float* s_sum = reinterpret_cast<float*>(s_ring);
+  if (Group<G>::kGroups > 1) {
+    __syncthreads();  // every group is done with the ring
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int c = 4 * (u * 32 * G + place);
+      if (c >= d) continue;
+      st4(s_sum + (2 * group) * d + c, sum_pre[u]);
+      st4(s_sum + (2 * group + 1) * d + c, sum_post[u]);
+    }
+    __syncthreads();
+    for (int c = threadIdx.x * 4; c < 2 * d; c += Group<G>::kThreads * 4) {
+      float4 v = ld4(s_sum + c);
+      for (int g = 1; g < Group<G>::kGroups; ++g) v = add4(v, ld4(s_sum + 2 * g * d + c));
+      st4(row + c, v);
+    }
+  } else {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int c = 4 * (u * 32 * G + place);
+      if (c >= d) continue;
+      st4(row + c, sum_pre[u]);
+      st4(row + d + c, sum_post[u]);
+    }
+  }
+}
+
+// Adds the CTAs' partial rows and turns the second sum into dw_post and a channel
+// gate's gradient: a CTA takes 32 columns, each of its warps every eighth row.
+template <typename L>
+__global__ void __launch_bounds__(256)
+norm_bwd_cols_kernel(NormArgs a, const float* __restrict__ part, int n_part) {
+  __shared__ float s_sum[8][32];
+  pdl_wait();
+  pdl_trigger();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int c = blockIdx.x * 32 + lane;
   float s = 0.f;
-  for (int p = 0; p < n_part; ++p) s += part[static_cast<size_t>(p) * 2 * a.d + c];
+  if (c < 2 * a.d) {
+#pragma unroll 8
+    for (int p = warp; p < n_part; p += 8) s += part[static_cast<size_t>(p) * 2 * a.d + c];
+  }
+  s_sum[warp][lane] = s;
+  __syncthreads();
+  if (warp != 0 || c >= 2 * a.d) return;
+  for (int w = 1; w < 8; ++w) s += s_sum[w][lane];
   if (c < a.d) {
     if (a.dw_pre) a.dw_pre[c] = s;
     return;
@@ -204,30 +456,90 @@ norm_bwd_cols_kernel(NormArgs a, const float* __restrict__ part, int n_part) {
 
 template <typename K>
 int allow_smem(K kernel, size_t bytes) {
-  if (bytes <= 48 * 1024) return OCCULT_OK;
+  if (bytes <= 40 * 1024) return OCCULT_OK;  // 48 KB less the static arrays
   return cuda_status(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                           static_cast<int>(bytes)));
 }
 
+template <typename R, typename L, int G, int U>
+int fwd_rows(const LaunchCtx& ctx, const NormArgs& a) {
+  const int need = (a.T + Group<G>::kGroups - 1) / Group<G>::kGroups;
+  const int cap = ctx.num_sms * 8;
+  return cuda_status(launch_pdl(norm_fwd_rows_kernel<R, L, G, U>, need < cap ? need : cap,
+                                Group<G>::kThreads, 0, ctx.stream, a));
+}
+
 template <typename R, typename L>
 int fwd(const LaunchCtx& ctx, const NormArgs& a) {
-  const size_t smem = static_cast<size_t>(a.d) * sizeof(float);
-  const int rc = allow_smem(norm_fwd_kernel<R, L>, smem);
+  const int d = a.d;
+  // Few rows: as many warps a row as give a thread one or two loads of each tensor
+  // (latency); many rows: as few as hold a row in registers (no or few syncs).
+  if (a.T < 4 * ctx.num_sms) {
+    if (d <= 256) return fwd_rows<R, L, 1, 2>(ctx, a);
+    if (d <= 512) return fwd_rows<R, L, 2, 2>(ctx, a);
+    if (d <= 1024) return fwd_rows<R, L, 4, 2>(ctx, a);
+    if (d <= 2048) return fwd_rows<R, L, 8, 2>(ctx, a);
+    if (d <= 4096) return fwd_rows<R, L, 16, 2>(ctx, a);
+    if (d <= 8192) return fwd_rows<R, L, 16, 4>(ctx, a);
+    return fwd_rows<R, L, 16, 8>(ctx, a);
+  }
+  if (d <= 256) return fwd_rows<R, L, 1, 2>(ctx, a);
+  if (d <= 512) return fwd_rows<R, L, 1, 4>(ctx, a);
+  if (d <= 1024) return fwd_rows<R, L, 1, 8>(ctx, a);
+  if (d <= 2048) return fwd_rows<R, L, 1, 16>(ctx, a);
+  if (d <= 4096) return fwd_rows<R, L, 2, 16>(ctx, a);
+  if (d <= 8192) return fwd_rows<R, L, 4, 16>(ctx, a);
+  return fwd_rows<R, L, 8, 16>(ctx, a);
+}
+
+constexpr int kRingBytes = 200 * 1024;  // of shared memory an SM, over its CTAs
+
+template <typename R, typename L, int G, int U>
+int bwd_rows(const LaunchCtx& ctx, const NormArgs& a, float* part, int* grid) {
+  constexpr int kCtas = bwd_ctas(G);
+  const int row = bwd_row_bytes<R>(a.d) * Group<G>::kGroups;
+  int stages = kRingBytes / kCtas / row;
+  stages = stages > 4 ? 4 : stages;
+  size_t smem = static_cast<size_t>(stages) * row;
+  const size_t sums = 2 * static_cast<size_t>(a.d) * Group<G>::kGroups * sizeof(float);
+  smem = smem > sums ? smem : sums;
+  int rc = allow_smem(norm_bwd_rows_kernel<R, L, G, U>, smem);
   if (rc) return rc;
-  const int grid = a.T < ctx.num_sms * 8 ? a.T : ctx.num_sms * 8;
-  return cuda_status(launch_pdl(norm_fwd_kernel<R, L>, grid, kNormThreads, smem, ctx.stream, a));
+  const int need = (a.T + Group<G>::kGroups - 1) / Group<G>::kGroups;
+  const int cap = ctx.num_sms * kCtas < kNormMaxParts ? ctx.num_sms * kCtas : kNormMaxParts;
+  *grid = need < cap ? need : cap;
+  return cuda_status(launch_pdl(norm_bwd_rows_kernel<R, L, G, U>, *grid, Group<G>::kThreads, smem,
+                                ctx.stream, a, part, stages, ctx.dev_err));
+}
+
+template <typename R, typename L>
+int bwd_any(const LaunchCtx& ctx, const NormArgs& a, float* part, int* grid) {
+  const size_t smem = 2 * static_cast<size_t>(a.d) * sizeof(float);
+  const int rc = allow_smem(norm_bwd_kernel<R, L>, smem);
+  if (rc) return rc;
+  *grid = norm_bwd_parts(a.T);
+  return cuda_status(launch_pdl(norm_bwd_kernel<R, L>, *grid, kNormThreads, smem, ctx.stream, a,
+                                part));
 }
 
 template <typename R, typename L>
 int bwd(const LaunchCtx& ctx, const NormArgs& a, float* part) {
-  const size_t smem = 2 * static_cast<size_t>(a.d) * sizeof(float);
-  int rc = allow_smem(norm_bwd_kernel<R, L>, smem);
-  if (rc) return rc;
-  const int grid = norm_bwd_parts(a.T);
-  rc = cuda_status(launch_pdl(norm_bwd_kernel<R, L>, grid, kNormThreads, smem, ctx.stream, a, part));
-  if (rc || !(a.dw_pre || a.dw_post || a.gate_kind == OCCULT_GATE_CHANNEL)) return rc;
-  return cuda_status(launch_pdl(norm_bwd_cols_kernel<L>, (2 * a.d + kNormThreads - 1) / kNormThreads,
-                                kNormThreads, 0, ctx.stream, a, part, grid));
+  const int d = a.d;
+  const bool sums = a.dw_pre || a.dw_post || a.gate_kind == OCCULT_GATE_CHANNEL;
+  int grid = 0, rc;
+  float* ws = part;
+  if (!sums) part = nullptr;
+  // bulk copies move whole 16 bytes; the ring holds a row of up to 8192 columns
+  if (d * sizeof(R) % 16 != 0 || d > 8192) rc = bwd_any<R, L>(ctx, a, ws, &grid);
+  else if (d <= 256) rc = bwd_rows<R, L, 1, 2>(ctx, a, part, &grid);
+  else if (d <= 512) rc = bwd_rows<R, L, 2, 2>(ctx, a, part, &grid);
+  else if (d <= 1024) rc = bwd_rows<R, L, 4, 2>(ctx, a, part, &grid);
+  else if (d <= 2048) rc = bwd_rows<R, L, 8, 2>(ctx, a, part, &grid);
+  else if (d <= 4096) rc = bwd_rows<R, L, 16, 2>(ctx, a, part, &grid);
+  else rc = bwd_rows<R, L, 16, 4>(ctx, a, part, &grid);
+  if (rc || !sums) return rc;
+  return cuda_status(launch_pdl(norm_bwd_cols_kernel<L>, (2 * d + 31) / 32, 256, 0, ctx.stream, a,
+                                part, grid));
 }
 
 }  // namespace

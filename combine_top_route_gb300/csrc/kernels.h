@@ -169,8 +169,6 @@ struct BalanceArgs {
   const uint8_t* mask;
   int32_t* counts;
   float *grad_w, *loss, *ws;
-  float* group_terms;     // in ws: {expert, device, sum lse^2} of every group
-  int* group_n;           // in ws: unmasked tokens of every group
   const float* dloss;
   float* dlogits;
   int accumulate;
@@ -178,7 +176,7 @@ struct BalanceArgs {
 // number of groups; *L receives the tokens of a group
 int balance_groups(int T, int group_len, int* L);
 size_t balance_ws_bytes(const occult_desc_t& ds, int group_len);
-int launch_balance_loss(const LaunchCtx& ctx, BalanceArgs a);
+int launch_balance_loss(const LaunchCtx& ctx, const BalanceArgs& a);
 int launch_balance_grad(const LaunchCtx& ctx, const BalanceArgs& a);
 
 int launch_adamw(const LaunchCtx& ctx, const occult_adamw_t& opt, const occult_param_t* params,
