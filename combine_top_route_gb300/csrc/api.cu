@@ -947,7 +947,7 @@ int occult_adamw(const occult_adamw_t* opt, const occult_param_t* params, int32_
   OCCULT_REQUIRE(opt->step >= 1 && opt->reserved == 0);
   // (comparisons that a NaN fails)
   OCCULT_REQUIRE(opt->beta1 >= 0 && opt->beta1 < 1 && opt->beta2 >= 0 && opt->beta2 < 1);
-  OCCULT_REQUIRE(opt->eps > 0 && opt->eps < 1e30 && opt->lr > -1e30 && opt->lr < 1e30 &&
+  OCCULT_REQUIRE(opt->eps >= 1e-30 && opt->eps < 1e30 && opt->lr > -1e30 && opt->lr < 1e30 &&
                  opt->weight_decay > -1e30 && opt->weight_decay < 1e30);
   for (int i = 0; i < n_params; ++i) {
     const occult_param_t& p = params[i];

@@ -57,142 +57,243 @@ __host__ __device__ inline Work work_of(float* ws, int64_t tiles, int Ne, int G)
   return w;
 }
 
-// The softmax of one token by LP lanes, lane s of them holding experts 8s .. 8s+7:
-// p gets exp(z - max) / sum; returns log sum exp.  `vec`: rows are whole float4s.
+// One token's row over LP lanes: lane s holds experts 4 (h LP + s) + i, h < 2, i < 4,
+// so that a row is read as consecutive 16-byte words (`vec`: rows are whole ones).
 template <int LP>
-__device__ __forceinline__ float softmax8(const float* row, int Ne, bool vec, int sub,
-                                          float (&p)[8]) {
-  const float NEG = -__int_as_float(0x7f800000);
-  const int e0 = sub * 8;
+__device__ __forceinline__ int expert_of(int sub, int j) { return 4 * ((j >> 2) * LP + sub) + (j & 3); }
+template <int LP>
+__device__ __forceinline__ void load_row(const float* row, int Ne, bool vec, int sub, float pad,
+                                         float (&v)[8]) {
   if (vec) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      float4 v = make_float4(NEG, NEG, NEG, NEG);
-      if (e0 + 4 * h < Ne) v = *reinterpret_cast<const float4*>(row + e0 + 4 * h);
-      p[4 * h] = v.x; p[4 * h + 1] = v.y; p[4 * h + 2] = v.z; p[4 * h + 3] = v.w;
+      float4 q = make_float4(pad, pad, pad, pad);
+      if (4 * (h * LP + sub) < Ne)
+        q = *reinterpret_cast<const float4*>(row + 4 * (h * LP + sub));
+      v[4 * h] = q.x; v[4 * h + 1] = q.y; v[4 * h + 2] = q.z; v[4 * h + 3] = q.w;
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) p[i] = e0 + i < Ne ? row[e0 + i] : NEG;
+    for (int j = 0; j < 8; ++j)
+      v[j] = expert_of<LP>(sub, j) < Ne ? row[expert_of<LP>(sub, j)] : pad;
   }
-  float mx = p[0];
+}
+__device__ __forceinline__ float minus_inf() { return -__int_as_float(0x7f800000); }
+
+// v = exp(z - max), *inv = 1 / their sum; returns log sum exp.  The exponentials are
+// powers of two of (z - max) log2 e: that product's rounding makes a probability 2^-m
+// of the largest m 2^-24 of itself less exact than expf would, which costs sums and
+// gradients nothing, at half of the instructions.
+template <int LP>
+__device__ __forceinline__ float softmax_row(float (&v)[8], float* inv) {
+  constexpr float kLog2e = 1.4426950408889634f;
+  float mx = v[0];
 #pragma unroll
-  for (int i = 1; i < 8; ++i) mx = fmaxf(mx, p[i]);
+  for (int i = 1; i < 8; ++i) mx = fmaxf(mx, v[i]);
 #pragma unroll
   for (int o = LP / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
   float z = 0.f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    p[i] = e0 + i < Ne ? expf(p[i] - mx) : 0.f;
-    z += p[i];
+    const float y = (v[i] - mx) * kLog2e;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(v[i]) : "f"(y));
+    z += v[i];
   }
 #pragma unroll
   for (int o = LP / 2; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
-  const float inv = 1.f / z;
+  *inv = __fdividef(1.f, z);  // z is about 1 .. 256
+  return mx + __logf(z);      // within 2^-21
+}
+
+// What a tile, a group or a batch of one CTA adds up to, in shared memory.
+struct Sums {
+  float p[OCCULT_MAX_EXPERTS];  // sum of probabilities
+  int c[OCCULT_MAX_EXPERTS];    // slots
+  float sq;                     // sum of lse^2
+  int n;                        // tokens
+};
+
+// The sums of tokens [t0, t1) by a CTA of kTileThreads, in a fixed order.
+template <int LP>
+struct TileScratch {
+  float p[kTileWarps][LP * 8];
+  float sq[kTileWarps];
+  int n[kTileWarps];
+};
+template <int LP>
+__device__ __forceinline__ void sum_tile(const BalanceArgs& a, int64_t t0, int64_t t1,
+                                         TileScratch<LP>& x, Sums& out) {
+  constexpr int kTok = 32 / LP;  // tokens of a warp's step
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane % LP;
+  const bool vec = a.Ne % 4 == 0;
+  for (int e = threadIdx.x; e < a.Ne; e += kTileThreads) out.c[e] = 0;
+  __syncthreads();
+  float acc[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) p[i] *= inv;
-  return mx + logf(z);
+  for (int i = 0; i < 8; ++i) acc[i] = 0.f;
+  float sq = 0.f;
+  int n = 0;
+  // the next step's row, mask and ids are on their way while this one's is summed
+  // (lanes past the end run along on the first row; what a masked row gives is dropped)
+  float next[8];
+  bool next_on = false;
+  int next_id[2];
+  auto fetch = [&](int64_t b) {
+    const int64_t t = b + lane / LP;
+    const bool in = t < t1;
+    load_row<LP>(a.logits + (in ? t : t0) * a.Ne, a.Ne, vec, sub, minus_inf(), next);
+    next_on = in && (!a.mask || a.mask[t]);
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+      next_id[r] = in && sub + r * LP < a.k ? a.ids[t * a.k + sub + r * LP] : -1;
+  };
+  int64_t b = t0 + warp * kTok;
+  if (b < t1) fetch(b);
+  for (; b < t1; b += kTileWarps * kTok) {
+    float v[8], inv;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = next[i];
+    const bool on = next_on;
+    const int id[2] = {next_id[0], next_id[1]};
+    if (b + kTileWarps * kTok < t1) fetch(b + kTileWarps * kTok);
+    const float lse = softmax_row<LP>(v, &inv);
+    if (on) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) acc[i] = fmaf(v[i], inv, acc[i]);
+      if (sub == 0) { sq = fmaf(lse, lse, sq); ++n; }
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+        if (static_cast<unsigned>(id[r]) < static_cast<unsigned>(a.Ne)) atomicAdd(&out.c[id[r]], 1);
+    }
+    __syncwarp();
+  }
+#pragma unroll
+  for (int o = 16; o >= LP; o >>= 1) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], o);
+    sq += __shfl_xor_sync(0xffffffffu, sq, o);
+    n += __shfl_xor_sync(0xffffffffu, n, o);
+  }
+  if (lane < LP)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x.p[warp][expert_of<LP>(lane, i)] = acc[i];
+  if (lane == 0) { x.sq[warp] = sq; x.n[warp] = n; }
+  __syncthreads();
+  for (int e = threadIdx.x; e < a.Ne; e += kTileThreads) {
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < kTileWarps; ++i) s += x.p[i][e];
+    out.p[e] = s;
+  }
+  if (threadIdx.x == kTileThreads - 1) {
+    float s = 0.f;
+    int m = 0;
+    for (int i = 0; i < kTileWarps; ++i) { s += x.sq[i]; m += x.n[i]; }
+    out.sq = s;
+    out.n = m;
+  }
+  __syncthreads();
+}
+
+// A group's counts, gradient weights and loss terms from its sums (`s.p` is
+// overwritten): 1 / A and the CTA's threads given; terms by its first thread.
+struct GroupScratch {
+  float f[OCCULT_MAX_EXPERTS];
+  float fd[OCCULT_MAX_VDEV], sd[OCCULT_MAX_VDEV];
+  int dev[OCCULT_MAX_EXPERTS];  // expert_to_vdev, filled by the caller
+};
+__device__ __forceinline__ void finish_group(const BalanceArgs& a, int64_t g, Sums& s,
+                                             GroupScratch& x, float inv_a, float (&terms)[3]) {
+  const int tid = threadIdx.x;
+  const float inv_g = 1.f / static_cast<float>(s.n > 0 ? s.n : 1);
+  const float scale = static_cast<float>(a.Ne) / static_cast<float>(a.k) * inv_g;
+  for (int e = tid; e < a.Ne; e += blockDim.x) {
+    a.counts[g * a.Ne + e] = s.c[e];
+    x.f[e] = static_cast<float>(s.c[e]) * scale;
+    s.p[e] *= inv_g;
+  }
+  __syncthreads();
+  // a warp a device
+  for (int d = tid >> 5; d < a.Nd; d += blockDim.x / 32) {
+    float f = 0.f, S = 0.f, m = 0.f;
+    for (int e = tid & 31; e < a.Ne; e += 32)
+      if (x.dev[e] == d) { f += x.f[e]; S += s.p[e]; m += 1.f; }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      f += __shfl_xor_sync(0xffffffffu, f, o);
+      S += __shfl_xor_sync(0xffffffffu, S, o);
+      m += __shfl_xor_sync(0xffffffffu, m, o);
+    }
+    if ((tid & 31) == 0) { x.fd[d] = m > 0.f ? f / m : 0.f; x.sd[d] = S; }
+  }
+  __syncthreads();
+  for (int e = tid; e < a.Ne; e += blockDim.x) {
+    const int d = x.dev[e];
+    const float fd = static_cast<unsigned>(d) < static_cast<unsigned>(a.Nd) ? x.fd[d] : 0.f;
+    a.grad_w[g * a.Ne + e] = (a.coef * x.f[e] + a.coef_dev * fd) * inv_g * inv_a;
+  }
+  if (tid < 32) {
+    float expert = 0.f, device = tid < a.Nd ? x.fd[tid] * x.sd[tid] : 0.f;
+    for (int e = tid; e < a.Ne; e += 32) expert += x.f[e] * s.p[e];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      expert += __shfl_xor_sync(0xffffffffu, expert, o);
+      device += __shfl_xor_sync(0xffffffffu, device, o);
+    }
+    terms[0] = expert;
+    terms[1] = device;
+    terms[2] = s.sq;
+  }
+}
+__device__ __forceinline__ void write_loss(const BalanceArgs& a, const float (&terms)[3], float inv_a,
+                                           float inv_n) {
+  const float expert = terms[0] * inv_a, device = terms[1] * inv_a, z = terms[2] * inv_n;
+  a.loss[0] = a.coef * expert + a.coef_dev * device + a.coef_z * z;
+  a.loss[1] = expert;
+  a.loss[2] = device;
+  a.loss[3] = z;
+  a.grad_w[static_cast<size_t>(a.G) * a.Ne] = 2.f * a.coef_z * inv_n;
+}
+
+// A batch of one group and few tokens: everything by one CTA.
+template <int LP>
+__global__ void __launch_bounds__(kTileThreads, 1) balance_one_kernel(BalanceArgs a) {
+  __shared__ TileScratch<LP> s_tile;
+  __shared__ Sums s_sums;
+  __shared__ GroupScratch s_group;
+  pdl_wait();
+  pdl_trigger();
+  for (int e = threadIdx.x; e < a.Ne; e += kTileThreads) s_group.dev[e] = a.e2v[e];
+  sum_tile<LP>(a, 0, a.T, s_tile, s_sums);
+  float terms[3];
+  finish_group(a, 0, s_sums, s_group, 1.f, terms);
+  if (threadIdx.x == 0)
+    write_loss(a, terms, 1.f, 1.f / static_cast<float>(s_sums.n > 0 ? s_sums.n : 1));
 }
 
 // Pass 1: CTA x of group y takes one tile of the group's tokens.
 template <int LP>
 __global__ void __launch_bounds__(kTileThreads, 2)
 balance_tiles_kernel(BalanceArgs a, Tiles tiles) {
-  constexpr int kTok = 32 / LP;  // tokens of a warp's step
-  __shared__ float s_p[kTileWarps][LP * 8];
-  __shared__ int s_c[LP * 8];
-  __shared__ float s_sq[kTileWarps];
-  __shared__ int s_n[kTileWarps];
+  __shared__ TileScratch<LP> s_tile;
+  __shared__ Sums s_sums;
   pdl_wait();
   pdl_trigger();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane % LP;
-  const bool vec = a.Ne % 4 == 0;
   const Work w = work_of(a.ws, tiles.n, a.Ne, a.G);
   if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *w.done = 0;
-  for (int e = threadIdx.x; e < LP * 8; e += kTileThreads) s_c[e] = 0;
-  __syncthreads();
   for (int g = blockIdx.y; g < a.G; g += gridDim.y) {
     const int64_t g0 = static_cast<int64_t>(g) * a.L;
     const int64_t g1 = min(static_cast<int64_t>(a.T), g0 + a.L);
     const int64_t t0 = g0 + static_cast<int64_t>(blockIdx.x) * tiles.len;
-    const int64_t t1 = min(g1, t0 + tiles.len);
-    float acc[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) acc[i] = 0.f;
-    float sq = 0.f;
-    int n = 0;
-#pragma unroll 2
-    for (int64_t b = t0 + warp * kTok; b < t1; b += kTileWarps * kTok) {
-      const int64_t t = b + lane / LP;
-      const bool on = t < t1 && (!a.mask || a.mask[t]);
-      float p[8];
-      // (lanes of a token that takes no part run along on the tile's first row)
-      const float lse = softmax8<LP>(a.logits + (on ? t : t0) * a.Ne, a.Ne, vec, sub, p);
-      if (!on) continue;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) acc[i] += p[i];
-      if (sub == 0) { sq += lse * lse; ++n; }
-      for (int j = sub; j < a.k; j += LP) {
-        const int e = a.ids[t * a.k + j];
-        if (static_cast<unsigned>(e) < static_cast<unsigned>(a.Ne)) atomicAdd(&s_c[e], 1);
-      }
-    }
-    __syncwarp();
-    // the tokens of a step, then the warps, in a fixed order
-#pragma unroll
-    for (int o = 16; o >= LP; o >>= 1) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], o);
-      sq += __shfl_xor_sync(0xffffffffu, sq, o);
-      n += __shfl_xor_sync(0xffffffffu, n, o);
-    }
-    if (lane < LP)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) s_p[warp][lane * 8 + i] = acc[i];
-    if (lane == 0) { s_sq[warp] = sq; s_n[warp] = n; }
-    __syncthreads();
+    sum_tile<LP>(a, t0, min(g1, t0 + tiles.len), s_tile, s_sums);
     const int64_t tile = static_cast<int64_t>(g) * tiles.per_group + blockIdx.x;
     for (int e = threadIdx.x; e < a.Ne; e += kTileThreads) {
-      float s = 0.f;
-#pragma unroll
-      for (int i = 0; i < kTileWarps; ++i) s += s_p[i][e];
-      w.p_sum[tile * a.Ne + e] = s;
-      w.count[tile * a.Ne + e] = s_c[e];
-      s_c[e] = 0;
+      w.p_sum[tile * a.Ne + e] = s_sums.p[e];
+      w.count[tile * a.Ne + e] = s_sums.c[e];
     }
-    if (threadIdx.x == 0) {
-      float s = 0.f;
-      int m = 0;
-      for (int i = 0; i < kTileWarps; ++i) { s += s_sq[i]; m += s_n[i]; }
-      w.sq[tile] = s;
-      w.n[tile] = m;
-    }
+    if (threadIdx.x == 0) { w.sq[tile] = s_sums.sq; w.n[tile] = s_sums.n; }
     __syncthreads();
   }
-}
-
-// Sums over the CTA (kSumThreads); every thread gets them.
-__device__ __forceinline__ float cta_sum(float v, float* s_red) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) s_red[threadIdx.x >> 5] = v;
-  __syncthreads();
-  v = s_red[threadIdx.x & 31];
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
-}
-__device__ __forceinline__ long long cta_sum(long long v, long long* s_red) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) s_red[threadIdx.x >> 5] = v;
-  __syncthreads();
-  v = s_red[threadIdx.x & 31];
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
 }
 
 // Pass 2, one CTA a group: the group's sums over its tiles, its counts, the
@@ -200,94 +301,95 @@ __device__ __forceinline__ long long cta_sum(long long v, long long* s_red) {
 __global__ void __launch_bounds__(kSumThreads) balance_groups_kernel(BalanceArgs a, Tiles tiles) {
   __shared__ float s_part[kSumThreads];
   __shared__ int s_cpart[kSumThreads];
-  __shared__ float s_f[OCCULT_MAX_EXPERTS], s_S[OCCULT_MAX_EXPERTS];
-  __shared__ float s_fd[OCCULT_MAX_VDEV], s_sd[OCCULT_MAX_VDEV];
-  __shared__ int s_dev[OCCULT_MAX_EXPERTS];
-  __shared__ float s_redf[32];
-  __shared__ long long s_redl[32];
+  __shared__ Sums s_sums;
+  __shared__ GroupScratch s_group;
+  __shared__ long long s_tok[kSumThreads / 32];
+  __shared__ float s_sq[kSumThreads / 32];
+  __shared__ float s_terms[kSumThreads / 32][3];
+  __shared__ int s_n[kSumThreads / 32];
   __shared__ bool s_last;
-  const int tid = threadIdx.x;
-  for (int e = tid; e < a.Ne; e += kSumThreads) s_dev[e] = a.e2v[e];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   pdl_wait();
   pdl_trigger();
+  for (int e = tid; e < a.Ne; e += kSumThreads) s_group.dev[e] = a.e2v[e];
   const Work w = work_of(a.ws, tiles.n, a.Ne, a.G);
-  // tokens, and groups that have any, over the whole batch
-  long long N = 0, A = 0;
-  for (int g = tid; g < a.G; g += kSumThreads) {
-    long long n = 0;
-    for (int i = 0; i < tiles.per_group; ++i)
+  // tokens, and groups that have any, over the whole batch (a group's tiles by one
+  // thread when they are few, by a warp when many); both are below 2^31
+  long long tok = 0;
+  const int wide = tiles.per_group > 16 ? 32 : 1, part = tid % wide;
+  for (int g = tid / wide; g < a.G; g += kSumThreads / wide) {
+    int n = 0;
+#pragma unroll 4
+    for (int i = part; i < tiles.per_group; i += wide)
       n += w.n[static_cast<int64_t>(g) * tiles.per_group + i];
-    N += n;
-    A += n > 0;
+    if (wide == 32) n = __reduce_add_sync(0xffffffffu, n);
+    if (part == 0) tok += n + (static_cast<long long>(n > 0) << 32);
   }
-  N = cta_sum(N, s_redl);
-  A = cta_sum(A, s_redl);
-  const float inv_a = 1.f / static_cast<float>(A > 0 ? A : 1);
-  const float inv_n = 1.f / static_cast<float>(N > 0 ? N : 1);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) tok += __shfl_xor_sync(0xffffffffu, tok, o);
+  if (lane == 0) s_tok[warp] = tok;
   int cols = 32;  // a power of two of at least Ne threads a slice of the tiles
   while (cols < a.Ne) cols *= 2;
   const int col = tid % cols, slice = tid / cols, slices = kSumThreads / cols;
+  float inv_a = 1.f, inv_n = 1.f;
   for (int g = blockIdx.x; g < a.G; g += gridDim.x) {
     const int64_t tile0 = static_cast<int64_t>(g) * tiles.per_group;
-    float s = 0.f;
-    int c = 0;
+    float s = 0.f, sq = 0.f;
+    int c = 0, n = 0;
     if (col < a.Ne) {
-#pragma unroll 4
+#pragma unroll 8
       for (int i = slice; i < tiles.per_group; i += slices) {
         s += w.p_sum[(tile0 + i) * a.Ne + col];
         c += w.count[(tile0 + i) * a.Ne + col];
       }
     }
-    float sq = 0.f;
-    long long n = 0;
     for (int i = tid; i < tiles.per_group; i += kSumThreads) {
       sq += w.sq[tile0 + i];
       n += w.n[tile0 + i];
     }
     s_part[tid] = s;
     s_cpart[tid] = c;
-    n = cta_sum(n, s_redl);
-    sq = cta_sum(sq, s_redf);
-    const float inv_g = 1.f / static_cast<float>(n > 0 ? n : 1);
+    n = __reduce_add_sync(0xffffffffu, n);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
+    if (lane == 0) { s_sq[warp] = sq; s_n[warp] = n; }
+    __syncthreads();
     if (tid < a.Ne) {
       for (int i = 1; i < slices; ++i) {
         s += s_part[i * cols + tid];
         c += s_cpart[i * cols + tid];
       }
-      a.counts[static_cast<size_t>(g) * a.Ne + tid] = c;
-      s_f[tid] = static_cast<float>(c) * (static_cast<float>(a.Ne) / static_cast<float>(a.k)) * inv_g;
-      s_S[tid] = s * inv_g;
+      s_sums.p[tid] = s;
+      s_sums.c[tid] = c;
     }
-    __syncthreads();
-    // a warp a device
-    for (int d = tid >> 5; d < a.Nd; d += kSumThreads / 32) {
-      float f = 0.f, S = 0.f, m = 0.f;
-      for (int e = tid & 31; e < a.Ne; e += 32)
-        if (s_dev[e] == d) { f += s_f[e]; S += s_S[e]; m += 1.f; }
+    // the last warp, which holds no expert, adds up the scalars
+    if (warp == kSumThreads / 32 - 1) {
+      sq = s_sq[lane];
+      n = __reduce_add_sync(0xffffffffu, s_n[lane]);
+      tok = s_tok[lane];
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) {
-        f += __shfl_xor_sync(0xffffffffu, f, o);
-        S += __shfl_xor_sync(0xffffffffu, S, o);
-        m += __shfl_xor_sync(0xffffffffu, m, o);
+        sq += __shfl_xor_sync(0xffffffffu, sq, o);
+        tok += __shfl_xor_sync(0xffffffffu, tok, o);
       }
-      if ((tid & 31) == 0) { s_fd[d] = m > 0.f ? f / m : 0.f; s_sd[d] = S; }
+      if (lane == 0) { s_sums.sq = sq; s_sums.n = n; s_tok[0] = tok; s_tok[1] = 0; }
+      if (lane > 0) s_tok[lane] = 0;
     }
     __syncthreads();
-    if (tid < a.Ne) {
-      const int d = s_dev[tid];
-      const float fd = static_cast<unsigned>(d) < static_cast<unsigned>(a.Nd) ? s_fd[d] : 0.f;
-      a.grad_w[static_cast<size_t>(g) * a.Ne + tid] =
-          (a.coef * s_f[tid] + a.coef_dev * fd) * inv_g * inv_a;
-    }
-    const float expert = cta_sum(tid < a.Ne ? s_f[tid] * s_S[tid] : 0.f, s_redf);
-    const float device = cta_sum(tid < a.Nd ? s_fd[tid] * s_sd[tid] : 0.f, s_redf);
+    tok = s_tok[0];
+    const int N = static_cast<int>(tok & 0xffffffffll), A = static_cast<int>(tok >> 32);
+    inv_a = 1.f / static_cast<float>(A > 0 ? A : 1);
+    inv_n = 1.f / static_cast<float>(N > 0 ? N : 1);
+    float terms[3];
+    finish_group(a, g, s_sums, s_group, inv_a, terms);
     if (tid == 0) {
-      w.terms[3 * static_cast<int64_t>(g)] = expert;
-      w.terms[3 * static_cast<int64_t>(g) + 1] = device;
-      w.terms[3 * static_cast<int64_t>(g) + 2] = sq;
+      if (a.G == 1) write_loss(a, terms, inv_a, inv_n);
+#pragma unroll
+      for (int i = 0; i < 3; ++i) w.terms[3 * static_cast<int64_t>(g) + i] = terms[i];
     }
     __syncthreads();
   }
+  if (a.G == 1) return;
   if (tid == 0) {
     __threadfence();
     s_last = atomicAdd(w.done, 1u) == gridDim.x - 1;
@@ -300,14 +402,18 @@ __global__ void __launch_bounds__(kSumThreads) balance_groups_kernel(BalanceArgs
 #pragma unroll
     for (int i = 0; i < 3; ++i) v[i] += __ldcg(&w.terms[3 * static_cast<int64_t>(g) + i]);
 #pragma unroll
-  for (int i = 0; i < 3; ++i) v[i] = cta_sum(v[i], s_redf);
+  for (int i = 0; i < 3; ++i) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+    if (lane == 0) s_terms[warp][i] = v[i];
+  }
+  __syncthreads();
   if (tid == 0) {
-    const float expert = v[0] * inv_a, device = v[1] * inv_a, sq = v[2] * inv_n;
-    a.loss[0] = a.coef * expert + a.coef_dev * device + a.coef_z * sq;
-    a.loss[1] = expert;
-    a.loss[2] = device;
-    a.loss[3] = sq;
-    a.grad_w[static_cast<size_t>(a.G) * a.Ne] = 2.f * a.coef_z * inv_n;
+    for (int i = 0; i < 3; ++i) {
+      v[i] = 0.f;
+      for (int k = 0; k < kSumThreads / 32; ++k) v[i] += s_terms[k][i];
+    }
+    write_loss(a, v, inv_a, inv_n);
   }
 }
 
@@ -317,48 +423,61 @@ __global__ void __launch_bounds__(kGradThreads) balance_grad_kernel(BalanceArgs 
   constexpr int kTok = 32 / LP;
   pdl_wait();
   pdl_trigger();
-  const int lane = threadIdx.x & 31, sub = lane % LP, e0 = sub * 8;
+  const int lane = threadIdx.x & 31, sub = lane % LP;
   const bool vec = a.Ne % 4 == 0;
   const float up = a.dloss ? *a.dloss : 1.f;
   const float wz = a.grad_w[static_cast<size_t>(a.G) * a.Ne];
   const int64_t step = static_cast<int64_t>(gridDim.x) * (kGradThreads / 32) * kTok;
-  for (int64_t b = (static_cast<int64_t>(blockIdx.x) * (kGradThreads / 32) + (threadIdx.x >> 5)) * kTok;
-       b < a.T; b += step) {
+  int64_t b = (static_cast<int64_t>(blockIdx.x) * (kGradThreads / 32) + (threadIdx.x >> 5)) * kTok;
+  // the next step's logits, and what the gradient is added to, are on their way while
+  // this one's are worked on
+  float next[8], next_old[8];
+  bool next_on = false;
+  auto fetch = [&](int64_t b) {
     const int64_t t = b + lane / LP;
-    const bool in = t < a.T, on = in && (!a.mask || a.mask[t]);
-    const int64_t row = (in ? t : b) * a.Ne;
-    float p[8], w[8];
-    const float lse = softmax8<LP>(a.logits + row, a.Ne, vec, sub, p);
-    const float* gw = a.grad_w + ((in ? t : b) / a.L) * a.Ne;
+    const bool in = t < a.T;
+    load_row<LP>(a.logits + (in ? t : b) * a.Ne, a.Ne, vec, sub, minus_inf(), next);
+    if (a.accumulate) load_row<LP>(a.dlogits + (in ? t : b) * a.Ne, a.Ne, vec, sub, 0.f, next_old);
+    next_on = in && (!a.mask || a.mask[t]);
+  };
+#pragma unroll
+  for (int i = 0; i < 8; ++i) next_old[i] = 0.f;
+  if (b < a.T) fetch(b);
+  for (; b < a.T; b += step) {
+    const int64_t t = b + lane / LP;
+    const bool in = t < a.T, on = next_on;
+    float v[8], old[8], w[8], inv;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) { v[i] = next[i]; old[i] = next_old[i]; }
+    if (b + step < a.T) fetch(b + step);
+    // (weights of a group's row: L1)
+    const unsigned g = a.G == 1 ? 0u
+                                : static_cast<unsigned>(in ? t : b) / static_cast<unsigned>(a.L);
+    load_row<LP>(a.grad_w + static_cast<size_t>(g) * a.Ne, a.Ne, vec, sub, 0.f, w);
+    const float lse = softmax_row<LP>(v, &inv);
     float dot = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      w[i] = e0 + i < a.Ne ? gw[e0 + i] : 0.f;
-      dot += p[i] * w[i];
+      v[i] *= inv;
+      dot = fmaf(v[i], w[i], dot);
     }
 #pragma unroll
     for (int o = LP / 2; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-    const float shift = wz * lse - dot;
-    float* out = a.dlogits + row;
     if (!in || (!on && a.accumulate)) continue;
+    const float shift = wz * lse - dot;
+    float* out = a.dlogits + t * a.Ne;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) p[i] = on ? up * (p[i] * (w[i] + shift)) : 0.f;
+    for (int i = 0; i < 8; ++i) v[i] = on ? fmaf(up * v[i], w[i] + shift, old[i]) : 0.f;
     if (vec) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        if (e0 + 4 * h >= a.Ne) continue;
-        float4 v = make_float4(p[4 * h], p[4 * h + 1], p[4 * h + 2], p[4 * h + 3]);
-        float4* q = reinterpret_cast<float4*>(out + e0 + 4 * h);
-        if (a.accumulate) {
-          const float4 o = *q;
-          v = make_float4(o.x + v.x, o.y + v.y, o.z + v.z, o.w + v.w);
-        }
-        *q = v;
-      }
+      for (int h = 0; h < 2; ++h)
+        if (4 * (h * LP + sub) < a.Ne)
+          *reinterpret_cast<float4*>(out + 4 * (h * LP + sub)) =
+              make_float4(v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]);
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        if (e0 + i < a.Ne) out[e0 + i] = a.accumulate ? out[e0 + i] + p[i] : p[i];
+        if (expert_of<LP>(sub, i) < a.Ne) out[expert_of<LP>(sub, i)] = v[i];
     }
   }
 }
@@ -380,11 +499,20 @@ size_t balance_ws_bytes(const occult_desc_t& ds, int group_len) {
 }
 
 int launch_balance_loss(const LaunchCtx& ctx, const BalanceArgs& a) {
+  // few tokens: one CTA does both passes (a step of all its warps is 64, 32 or 16
+  // tokens; beyond some steps the second launch costs less)
+  const int lp = a.Ne <= 64 ? 8 : a.Ne <= 128 ? 16 : 32;
+  if (a.G == 1 && a.T <= 8 * kTileThreads / lp) {
+    return cuda_status(
+        lp == 8    ? launch_pdl(balance_one_kernel<8>, 1, kTileThreads, 0, ctx.stream, a)
+        : lp == 16 ? launch_pdl(balance_one_kernel<16>, 1, kTileThreads, 0, ctx.stream, a)
+                   : launch_pdl(balance_one_kernel<32>, 1, kTileThreads, 0, ctx.stream, a));
+  }
   const Tiles tiles = tiles_of(a.T, a.L, a.G);
   const dim3 grid(tiles.per_group, a.G < 65535 ? a.G : 65535);
   const int rc = cuda_status(
-      a.Ne <= 64    ? launch_pdl(balance_tiles_kernel<8>, grid, kTileThreads, 0, ctx.stream, a, tiles)
-      : a.Ne <= 128 ? launch_pdl(balance_tiles_kernel<16>, grid, kTileThreads, 0, ctx.stream, a, tiles)
+      lp == 8    ? launch_pdl(balance_tiles_kernel<8>, grid, kTileThreads, 0, ctx.stream, a, tiles)
+      : lp == 16 ? launch_pdl(balance_tiles_kernel<16>, grid, kTileThreads, 0, ctx.stream, a, tiles)
                     : launch_pdl(balance_tiles_kernel<32>, grid, kTileThreads, 0, ctx.stream, a, tiles));
   if (rc) return rc;
   return cuda_status(launch_pdl(balance_groups_kernel, a.G < ctx.num_sms ? a.G : ctx.num_sms,

@@ -185,7 +185,7 @@ __device__ __forceinline__ float group_sum1(float v, float* s_red) {
   return v;
 }
 
-// Forward: the row stays in registers from its loads to its stores.
+// Forward of few rows: the row stays in registers from its loads to its stores.
 template <typename R, typename L, int G, int U>
 __global__ void __launch_bounds__(Group<G>::kThreads) norm_fwd_rows_kernel(NormArgs a) {
   __shared__ float s_red[2][Group<G>::kThreads / 32];
@@ -254,8 +254,124 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
       :: "r"(smem_u32(dst)), "l"(src), "r"(bytes), "r"(smem_u32(bar)) : "memory");
 }
 
-// CTAs of an SM in the backward
-__host__ __device__ constexpr int bwd_ctas(int G) { return G > 8 ? 1 : 2; }
+constexpr int kMaxStages = 4;  // rows of a ring
+// CTAs of an SM in the kernels with a ring (128 registers a thread)
+__host__ __device__ constexpr int ring_ctas(int G) { return G > 8 ? 1 : 2; }
+
+// Bytes of one row in the forward's ring: y, then r.
+template <typename R>
+__host__ __device__ __forceinline__ int fwd_row_bytes(int d) {
+  return (d * static_cast<int>(sizeof(float) + sizeof(R)) + 127) & ~127;
+}
+
+// Forward of many rows: a group's rows come through a ring of shared memory that bulk
+// copies fill ahead of the arithmetic.
+template <typename R, typename L, int G, int U>
+__global__ void __launch_bounds__(Group<G>::kThreads, ring_ctas(G))
+norm_fwd_ring_kernel(NormArgs a, int stages, int* dev_err) {
+  extern __shared__ __align__(128) unsigned char s_ring[];
+  __shared__ uint64_t s_full[Group<G>::kGroups][kMaxStages];
+  __shared__ float s_red[2][Group<G>::kThreads / 32];
+  __shared__ int s_abort;
+  const int group = Group<G>::index(), place = Group<G>::place();
+  const L* w_post = static_cast<const L*>(a.w_post);
+  const L* w_pre = static_cast<const L*>(a.w_pre);
+  const bool chan = a.gate_kind == OCCULT_GATE_CHANNEL;
+  const int d = a.d, row_bytes = fwd_row_bytes<R>(d);
+  unsigned char* ring = s_ring + static_cast<size_t>(group) * stages * row_bytes;
+  if (place < stages) mbar_init(&s_full[group][place], 1);
+  if (threadIdx.x == 0) s_abort = 0;
+  mbar_fence_init();
+  __syncthreads();
+  pdl_wait();
+  pdl_trigger();
+  const uint32_t tx = d * (a.y ? 4 + sizeof(R) : sizeof(R));
+  auto fill = [&](int stage, int t) {  // by the group's first thread
+    unsigned char* p = ring + stage * row_bytes;
+    uint64_t* bar = &s_full[group][stage];
+    const size_t base = static_cast<size_t>(t) * d;
+    mbar_arrive_expect_tx(bar, tx);
+    if (a.y) bulk_load(p, a.y + base, d * 4, bar);
+    bulk_load(p + d * 4, static_cast<const R*>(a.r) + base, d * sizeof(R), bar);
+  };
+  const int step = gridDim.x * Group<G>::kGroups;
+  const int first = blockIdx.x * Group<G>::kGroups + group;
+  if (place == 0)
+    for (int i = 0; i < stages; ++i)
+      if (static_cast<int64_t>(first) + static_cast<int64_t>(i) * step < a.T)
+        fill(i, first + i * step);
+  const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+  float4 wq[U], wp[U];  // w_post times a channel gate; w_pre
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int c = 4 * (u * 32 * G + place);
+    wp[u] = w_pre && c < d ? ld4(w_pre + c) : zero;
+    wq[u] = make_float4(1.f, 1.f, 1.f, 1.f);
+    if (c < d) {
+      if (w_post) wq[u] = ld4(w_post + c);
+      if (chan) wq[u] = mul4(wq[u], ld4(a.gate + c));
+    }
+  }
+  const float inv_d = 1.f / d;
+  int stage = 0, flip = 0;
+  uint32_t parity = 0;
+  for (int64_t t = first; t < a.T; t += step) {
+    float scale = a.gate_kind == OCCULT_GATE_TOKEN ? a.gate[t] : 1.f;
+    if (!mbar_wait(&s_full[group][stage], parity, &s_abort)) {
+      latch_error(dev_err, OCCULT_ERR_DEVICE_TIMEOUT);
+      s_abort = 1;
+    }
+    const float* s_y = reinterpret_cast<const float*>(ring + stage * row_bytes);
+    const R* s_r = reinterpret_cast<const R*>(s_y + d);
+    float4 r[U], y[U];
+    float s = 0.f;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int c = 4 * (u * 32 * G + place);
+      y[u] = a.y && c < d ? ld4(s_y + c) : zero;
+      r[u] = c < d ? ld4(s_r + c) : zero;
+      s += dot4(y[u], y[u]);
+    }
+    // this sync also says that the group has read the row: its place is refilled
+    s = group_sum1<G>(s, s_red[flip]);
+    flip ^= 1;
+    if (G == 1) __syncwarp();
+    if (place == 0 && t + static_cast<int64_t>(stages) * step < a.T)
+      fill(stage, static_cast<int>(t + static_cast<int64_t>(stages) * step));
+    if (++stage == stages) { stage = 0; parity ^= 1; }
+    const size_t base = static_cast<size_t>(t) * d;
+    if (a.y) {
+      if (w_post) {
+        const float rp = rsqrtf(s * inv_d + a.eps);
+        if (place == 0 && a.rstd_post_out) a.rstd_post_out[t] = rp;
+        scale *= rp;
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int c = 4 * (u * 32 * G + place);
+        r[u] = fma4(r[u], a.res_scale, mul4(scale4(y[u], scale), wq[u]));
+        if (c < d) st4(static_cast<R*>(a.r_out) + base + c, r[u]);
+      }
+    }
+    if (!w_pre) continue;
+    s = 0.f;
+#pragma unroll
+    for (int u = 0; u < U; ++u) s += dot4(r[u], r[u]);
+    const float rq = rsqrtf(group_sum1<G>(s, s_red[flip]) * inv_d + a.eps);
+    flip ^= 1;
+    if (place == 0 && a.rstd_pre_out) a.rstd_pre_out[t] = rq;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int c = 4 * (u * 32 * G + place);
+      if (c < d) st4(static_cast<L*>(a.x) + base + c, mul4(scale4(r[u], rq), wp[u]));
+    }
+  }
+  if (s_abort && place == 0) {  // copies may still be in flight: give them the limit again
+    volatile int none = 0;
+    for (int i = 0; i < stages; ++i)
+      mbar_wait(&s_full[group][i], i < stage ? parity ^ 1 : parity, &none);
+  }
+}
 
 // Bytes of one row in the backward's ring: dx, y, then dr_out and r'.
 template <typename R>
@@ -270,10 +386,9 @@ __host__ __device__ __forceinline__ int bwd_row_bytes(int d) {
 // then refilled.  The column sums stay in the registers of the threads that own
 // the columns, over all the rows of the group.
 template <typename R, typename L, int G, int U>
-__global__ void __launch_bounds__(Group<G>::kThreads, bwd_ctas(G))
+__global__ void __launch_bounds__(Group<G>::kThreads, ring_ctas(G))
 norm_bwd_rows_kernel(NormArgs a, float* part, int stages, int* dev_err) {
   extern __shared__ __align__(128) unsigned char s_ring[];
-  constexpr int kMaxStages = 4;
   __shared__ uint64_t s_full[Group<G>::kGroups][kMaxStages];
   __shared__ float4 s_red[2][Group<G>::kThreads / 32];
   __shared__ int s_abort;
@@ -469,37 +584,51 @@ int fwd_rows(const LaunchCtx& ctx, const NormArgs& a) {
                                 Group<G>::kThreads, 0, ctx.stream, a));
 }
 
-template <typename R, typename L>
-int fwd(const LaunchCtx& ctx, const NormArgs& a) {
-  const int d = a.d;
-  // Few rows: as many warps a row as give a thread one or two loads of each tensor
-  // (latency); many rows: as few as hold a row in registers (no or few syncs).
-  if (a.T < 4 * ctx.num_sms) {
-    if (d <= 256) return fwd_rows<R, L, 1, 2>(ctx, a);
-    if (d <= 512) return fwd_rows<R, L, 2, 2>(ctx, a);
-    if (d <= 1024) return fwd_rows<R, L, 4, 2>(ctx, a);
-    if (d <= 2048) return fwd_rows<R, L, 8, 2>(ctx, a);
-    if (d <= 4096) return fwd_rows<R, L, 16, 2>(ctx, a);
-    if (d <= 8192) return fwd_rows<R, L, 16, 4>(ctx, a);
-    return fwd_rows<R, L, 16, 8>(ctx, a);
-  }
-  if (d <= 256) return fwd_rows<R, L, 1, 2>(ctx, a);
-  if (d <= 512) return fwd_rows<R, L, 1, 4>(ctx, a);
-  if (d <= 1024) return fwd_rows<R, L, 1, 8>(ctx, a);
-  if (d <= 2048) return fwd_rows<R, L, 1, 16>(ctx, a);
-  if (d <= 4096) return fwd_rows<R, L, 2, 16>(ctx, a);
-  if (d <= 8192) return fwd_rows<R, L, 4, 16>(ctx, a);
-  return fwd_rows<R, L, 8, 16>(ctx, a);
-}
-
 constexpr int kRingBytes = 200 * 1024;  // of shared memory an SM, over its CTAs
 
 template <typename R, typename L, int G, int U>
+int fwd_ring(const LaunchCtx& ctx, const NormArgs& a) {
+  constexpr int kCtas = ring_ctas(G);
+  const int row = fwd_row_bytes<R>(a.d) * Group<G>::kGroups;
+  int stages = kRingBytes / kCtas / row;
+  stages = stages > kMaxStages ? kMaxStages : stages;
+  const size_t smem = static_cast<size_t>(stages) * row;
+  const int rc = allow_smem(norm_fwd_ring_kernel<R, L, G, U>, smem);
+  if (rc) return rc;
+  const int need = (a.T + Group<G>::kGroups - 1) / Group<G>::kGroups;
+  const int cap = ctx.num_sms * kCtas;
+  return cuda_status(launch_pdl(norm_fwd_ring_kernel<R, L, G, U>, need < cap ? need : cap,
+                                Group<G>::kThreads, smem, ctx.stream, a, stages, ctx.dev_err));
+}
+
+template <typename R, typename L>
+int fwd(const LaunchCtx& ctx, const NormArgs& a) {
+  const int d = a.d;
+  // Many rows come through the ring (its copies move whole 16 bytes and it holds rows
+  // of up to 8192 columns); few rows have as many warps each as give a thread two
+  // loads of each tensor, and no ring to set up.
+  if (a.T >= 4 * ctx.num_sms && d * sizeof(R) % 16 == 0 && d <= 8192) {
+    if (d <= 512) return fwd_ring<R, L, 1, 4>(ctx, a);
+    if (d <= 1024) return fwd_ring<R, L, 2, 4>(ctx, a);
+    if (d <= 2048) return fwd_ring<R, L, 4, 4>(ctx, a);
+    if (d <= 4096) return fwd_ring<R, L, 8, 4>(ctx, a);
+    return fwd_ring<R, L, 16, 4>(ctx, a);
+  }
+  if (d <= 256) return fwd_rows<R, L, 1, 2>(ctx, a);
+  if (d <= 512) return fwd_rows<R, L, 2, 2>(ctx, a);
+  if (d <= 1024) return fwd_rows<R, L, 4, 2>(ctx, a);
+  if (d <= 2048) return fwd_rows<R, L, 8, 2>(ctx, a);
+  if (d <= 4096) return fwd_rows<R, L, 16, 2>(ctx, a);
+  if (d <= 8192) return fwd_rows<R, L, 16, 4>(ctx, a);
+  return fwd_rows<R, L, 16, 8>(ctx, a);
+}
+
+template <typename R, typename L, int G, int U>
 int bwd_rows(const LaunchCtx& ctx, const NormArgs& a, float* part, int* grid) {
-  constexpr int kCtas = bwd_ctas(G);
+  constexpr int kCtas = ring_ctas(G);
   const int row = bwd_row_bytes<R>(a.d) * Group<G>::kGroups;
   int stages = kRingBytes / kCtas / row;
-  stages = stages > 4 ? 4 : stages;
+  stages = stages > kMaxStages ? kMaxStages : stages;
   size_t smem = static_cast<size_t>(stages) * row;
   const size_t sums = 2 * static_cast<size_t>(a.d) * Group<G>::kGroups * sizeof(float);
   smem = smem > sums ? smem : sums;

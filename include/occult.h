@@ -763,7 +763,7 @@ int occult_balance_grad(const occult_desc_t* desc, const occult_balance_t* opt,
 
 /* Options of an AdamW step (host).  Doubles, so that 1 - beta2 keeps its digits. */
 typedef struct occult_adamw {
-  double lr, beta1, beta2, eps, weight_decay;
+  double lr, beta1, beta2, eps, weight_decay;   /* eps >= 1e-30 (a normal fp32)   */
   int32_t step;             /* this step's number, from 1                           */
   int32_t state_bits;       /* 32 | 8                                               */
   uint32_t seed;            /* of the roundings by draw                             */
