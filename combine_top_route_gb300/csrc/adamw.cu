@@ -16,10 +16,10 @@ namespace occult {
 
 namespace {
 
-constexpr int kAdamThreads = 256;
+constexpr int kAdamThreads = 128;
 constexpr int kAdamWarps = kAdamThreads / 32;
 constexpr int kBlock = OCCULT_STATE_BLOCK;       // elements of a warp's step
-constexpr int kChunk = kAdamWarps * kBlock * 4;  // elements of a CTA
+constexpr int kMaxSteps = 2;                     // blocks of a warp
 constexpr int kMaxTensors = 256;                 // of one launch
 
 enum : int { KIND_F32 = 0, KIND_MASTER = 1, KIND_BF16 = 2 };
@@ -40,6 +40,7 @@ struct AdamTable {
   uint32_t key;
   const float* grad_scale;
   int n;
+  int cta_blocks;            // blocks of a CTA
   int chunk0[kMaxTensors + 1];  // first CTA of every tensor
   Tensor t[kMaxTensors];
 };
@@ -104,28 +105,32 @@ __device__ __forceinline__ float decode(uint32_t code, uint32_t exp) {
   if (MANT == 3) bits |= (code & 0x80u) << 24;
   return __uint_as_float(bits);
 }
-// Byte j of a word of codes; `base` = (exp - 15) << 23 (not of a NaN block).
+// Bytes j and j + 1 (j even) of a word of codes as two bf16 values in a register;
+// `base2` = lanes_base(exp), not of a NaN block.
+__device__ __forceinline__ uint32_t lanes_base(uint32_t exp) {
+  return (((exp - 15u) << 7) & 0xffffu) * 0x10001u;
+}
 template <int MANT>
-__device__ __forceinline__ float decode_byte(uint32_t w, int j, uint32_t base) {
-  constexpr uint32_t cut = 23 - MANT;
-  constexpr uint32_t mask = (16u << MANT) - 1;
-  uint32_t bits;
-  if (j < 3) {
-    const uint32_t mag = w & (mask << (8 * j));
-    bits = mag ? mag * (1u << (cut - 8 * j)) + base : 0u;
-  } else {
-    const uint32_t mag = (w >> 24) & mask;
-    bits = mag ? mag * (1u << cut) + base : 0u;
-  }
-  if (MANT == 3) bits |= (w << (24 - 8 * j)) & 0x80000000u;
-  return __uint_as_float(bits);
+__device__ __forceinline__ uint32_t decode_lanes(uint32_t w, int j, uint32_t base2) {
+  const uint32_t c = __byte_perm(w, 0u, j == 0 ? 0x4140 : 0x4342);
+  const uint32_t mag = MANT == 3 ? c & 0x007f007fu : c;
+  const uint32_t some = __vminu2(mag, 0x00010001u) * 0xffffu;   // a lane of ones where not 0
+  uint32_t x = (mag * (1u << (7 - MANT)) + base2) & some;
+  if (MANT == 3) x |= (c & 0x00800080u) * 256u;
+  return x;
+}
+template <int MANT>
+__device__ __forceinline__ float2 decode_pair(uint32_t w, int j, uint32_t base2) {
+  const uint32_t x = decode_lanes<MANT>(w, j, base2);
+  return make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u));
 }
 
-// bf16 by a draw: the low half of the word carries into the high one
-__device__ __forceinline__ uint32_t bf16_by_draw(float w, uint32_t draw16) {
-  uint32_t bits = __float_as_uint(w);
-  if (fabsf(w) < __int_as_float(0x7f800000)) bits += draw16;  // (not of a NaN: it would wrap)
-  return bits;  // the code is the upper half
+// Two values to bf16, each by the draw in its half of `draws`: the draw is added below
+// the cut of the fp32 word, which is then truncated.
+__device__ __forceinline__ uint32_t bf16x2_by_draw(float lo, float hi, uint32_t draws) {
+  uint32_t r;
+  asm("cvt.rs.bf16x2.f32 %0, %1, %2, %3;" : "=r"(r) : "f"(hi), "f"(lo), "r"(draws));
+  return r;
 }
 
 // Four consecutive elements of a tensor, the first `live` of them in range.
@@ -165,15 +170,13 @@ __device__ __forceinline__ void store4(float* p, int live, const float (&f)[4]) 
       if (j < live) p[j] = f[j];
   }
 }
-__device__ __forceinline__ void store4(uint16_t* p, int live, const uint32_t (&h)[4]) {
-  // the upper halves of four words
+__device__ __forceinline__ void store4(uint16_t* p, int live, const uint32_t (&w)[2]) {
   if (live == 4) {
-    *reinterpret_cast<uint2*>(p) =
-        make_uint2(__byte_perm(h[0], h[1], 0x7632), __byte_perm(h[2], h[3], 0x7632));
+    *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
   } else {
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      if (j < live) p[j] = static_cast<uint16_t>(h[j] >> 16);
+      if (j < live) p[j] = static_cast<uint16_t>(w[j >> 1] >> (16 * (j & 1)));
   }
 }
 __device__ __forceinline__ void store4(uint8_t* p, int live, uint32_t c) {
@@ -190,6 +193,7 @@ __device__ __forceinline__ float rcp_approx(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
+__device__ __forceinline__ float2 two(float x) { return make_float2(x, x); }
 // max of three that a NaN among them comes through
 __device__ __forceinline__ float max3_nan(float a, float b, float c) {
   float r;
@@ -247,7 +251,7 @@ __device__ __forceinline__ void step_block(const AdamTable& a, const Tensor& T, 
   float s[2][4];
   float top_m = 0.f, top_v = 0.f;
   uint32_t hash[2][4];
-  const uint32_t base_m = (x.em - 15u) << 23, base_v = (x.ev - 15u) << 23;
+  const uint32_t base_m = lanes_base(x.em), base_v = lanes_base(x.ev);
   // a NaN block comes back as NaN through the gradient's factor
   const float nan = __int_as_float(0x7fffffff);
   const float gs_m = BITS == 8 && x.em == 255u ? nan : gs;
@@ -258,26 +262,44 @@ __device__ __forceinline__ void step_block(const AdamTable& a, const Tensor& T, 
     const int live = live_of<FULL>(T, i);
     const uint32_t x0 = (static_cast<uint32_t>(T.first + i) + a.key) * kMul1;
     float out[4];
-    uint32_t word[4];
+    uint32_t word[2];
+    if (BITS == 8 || KIND == KIND_BF16) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < 4; ++j) hash[h][j] = mix_open(x0 + j * kMul1);
+    }
+    // two elements at a time: the packed fp32 operations take one issue slot for both
+#pragma unroll
+    for (int j = 0; j < 4; j += 2) {
+      float2 m, v;
       if (BITS == 8) {
-        x.m[h][j] = decode_byte<3>(x.cm[h], j, base_m);
-        const float r = decode_byte<4>(x.cv[h], j, base_v);
-        x.v[h][j] = r * r;
+        m = decode_pair<3>(x.cm[h], j, base_m);
+        v = decode_pair<4>(x.cv[h], j, base_v);
+        v = __fmul2_rn(v, v);
+      } else {
+        m = make_float2(x.m[h][j], x.m[h][j + 1]);
+        v = make_float2(x.v[h][j], x.v[h][j + 1]);
       }
-      if (BITS == 8 || KIND == KIND_BF16) hash[h][j] = mix_open(x0 + j * kMul1);
-      const float gm = gs_m * x.g[h][j], gv = gs_v * x.g[h][j];
-      x.m[h][j] = __fadd_rn(__fmul_rn(a.b1, x.m[h][j]), __fmul_rn(a.c1, gm));
-      x.v[h][j] = __fadd_rn(__fmul_rn(a.b2, x.v[h][j]), __fmul_rn(__fmul_rn(a.c2, gv), gv));
-      s[h][j] = sqrtf(x.v[h][j]);
-      out[j] = fmaf(-a.rate, x.m[h][j] * rcp_approx(fmaf(s[h][j], a.inv_root, a.eps)),
-                    x.w[h][j] * a.keep);
-      if (KIND == KIND_MASTER)
-        word[j] = static_cast<uint32_t>(__bfloat16_as_ushort(__float2bfloat16_rn(out[j]))) << 16;
+      const float2 g = make_float2(x.g[h][j], x.g[h][j + 1]);
+      const float2 gm = __fmul2_rn(two(gs_m), g), gv = __fmul2_rn(two(gs_v), g);
+      m = __fadd2_rn(__fmul2_rn(two(a.b1), m), __fmul2_rn(two(a.c1), gm));
+      v = __fadd2_rn(__fmul2_rn(two(a.b2), v), __fmul2_rn(__fmul2_rn(two(a.c2), gv), gv));
+      const float2 root = make_float2(sqrtf(v.x), sqrtf(v.y));
+      const float2 den = __ffma2_rn(root, two(a.inv_root), two(a.eps));
+      const float2 upd = __fmul2_rn(m, make_float2(rcp_approx(den.x), rcp_approx(den.y)));
+      const float2 w = __ffma2_rn(two(-a.rate), upd,
+                                  __fmul2_rn(make_float2(x.w[h][j], x.w[h][j + 1]), two(a.keep)));
+      x.m[h][j] = m.x; x.m[h][j + 1] = m.y;
+      x.v[h][j] = v.x; x.v[h][j + 1] = v.y;
+      s[h][j] = root.x; s[h][j + 1] = root.y;
+      out[j] = w.x; out[j + 1] = w.y;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; j += 2) {
+      if (KIND == KIND_MASTER) word[j / 2] = pack_bf16x2(out[j], out[j + 1]);
       if (KIND == KIND_BF16) {
-        const uint32_t full = hash[h][j] ^ (hash[h][j] >> 16);
-        word[j] = bf16_by_draw(out[j], (full * kMul1) >> 16);
+        const uint32_t a0 = (hash[h][j] ^ (hash[h][j] >> 16)) * kMul1;
+        const uint32_t a1 = (hash[h][j + 1] ^ (hash[h][j + 1] >> 16)) * kMul1;
+        word[j / 2] = bf16x2_by_draw(out[j], out[j + 1], __byte_perm(a0, a1, 0x7632));
       }
     }
     if (BITS == 8) {
@@ -346,7 +368,7 @@ __device__ __forceinline__ void step_blocks(const AdamTable& a, const Tensor& T,
 }
 
 template <int BITS>
-__global__ void __launch_bounds__(kAdamThreads) adamw_kernel(const __grid_constant__ AdamTable a) {
+__global__ void __launch_bounds__(kAdamThreads, 8) adamw_kernel(const __grid_constant__ AdamTable a) {
   pdl_wait();
   pdl_trigger();
   // the tensor of this CTA: the one whose CTAs include it (all looked at at once)
@@ -358,39 +380,48 @@ __global__ void __launch_bounds__(kAdamThreads) adamw_kernel(const __grid_consta
   __syncthreads();
   const Tensor T = a.t[s_which];
   const float gs = a.grad_scale ? *a.grad_scale : 1.f;
-  const int64_t blk0 = static_cast<int64_t>(blockIdx.x - a.chunk0[s_which]) * (kChunk / kBlock);
+  const int64_t blk0 = static_cast<int64_t>(blockIdx.x - a.chunk0[s_which]) * a.cta_blocks;
   const int64_t n_blk = (T.n + kBlock - 1) / kBlock;
-  const int64_t end = n_blk < blk0 + kChunk / kBlock ? n_blk : blk0 + kChunk / kBlock;
+  const int64_t end = n_blk < blk0 + a.cta_blocks ? n_blk : blk0 + a.cta_blocks;
   const int64_t mine = blk0 + (threadIdx.x >> 5);
   if (T.kind == KIND_F32) step_blocks<BITS, KIND_F32>(a, T, mine, end, gs);
   else if (T.kind == KIND_MASTER) step_blocks<BITS, KIND_MASTER>(a, T, mine, end, gs);
   else step_blocks<BITS, KIND_BF16>(a, T, mine, end, gs);
 }
 
-// The values of 8-bit states: a thread turns 8 codes into 16 bytes.
+// The values of 8-bit states: kReadSteps times a thread turns 8 codes into 16 bytes.
+constexpr int kReadSteps = 2;
+constexpr int kReadChunk = 256 * 8 * kReadSteps;
 template <int MANT>
 __global__ void __launch_bounds__(256)
 adamw_read_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ exps, int64_t n,
                   __nv_bfloat16* __restrict__ out) {
   pdl_wait();
   pdl_trigger();
-  const int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 8;
-  if (i >= n) return;
-  const uint32_t e = exps[i / kBlock], base = (e - 15u) << 23;
-  if (i + 8 <= n) {
-    const uint2 c = *reinterpret_cast<const uint2*>(codes + i);
-    uint32_t f[8];
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * kReadChunk + threadIdx.x * 8;
+  uint2 c[kReadSteps];
+  uint32_t e[kReadSteps];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      f[j] = __float_as_uint(decode_byte<MANT>(c.x, j, base));
-      f[4 + j] = __float_as_uint(decode_byte<MANT>(c.y, j, base));
+  for (int u = 0; u < kReadSteps; ++u) {
+    const int64_t i = first + u * 2048;
+    if (i + 8 <= n) {
+      c[u] = *reinterpret_cast<const uint2*>(codes + i);
+      e[u] = exps[i / kBlock];
     }
-    uint4 o = make_uint4(__byte_perm(f[0], f[1], 0x7632), __byte_perm(f[2], f[3], 0x7632),
-                         __byte_perm(f[4], f[5], 0x7632), __byte_perm(f[6], f[7], 0x7632));
-    if (e == 255u) o = make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);
-    st_v4(out + i, o);
-  } else {
-    for (int64_t j = i; j < n; ++j) out[j] = __float2bfloat16_rn(decode<MANT>(codes[j], e));
+  }
+#pragma unroll
+  for (int u = 0; u < kReadSteps; ++u) {
+    const int64_t i = first + u * 2048;
+    if (i + 8 <= n) {
+      const uint32_t base = lanes_base(e[u]);
+      uint4 o = make_uint4(decode_lanes<MANT>(c[u].x, 0, base), decode_lanes<MANT>(c[u].x, 2, base),
+                           decode_lanes<MANT>(c[u].y, 0, base), decode_lanes<MANT>(c[u].y, 2, base));
+      if (e[u] == 255u) o = make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);
+      st_v4(out + i, o);
+    } else {
+      for (int64_t j = i; j < n; ++j)
+        out[j] = __float2bfloat16_rn(decode<MANT>(codes[j], exps[j / kBlock]));
+    }
   }
 }
 
@@ -410,6 +441,14 @@ int launch_adamw(const LaunchCtx& ctx, const occult_adamw_t& o, const occult_par
   a.eps = static_cast<float>(o.eps);
   a.key = mix(o.seed + mix(static_cast<uint32_t>(o.step)));
   a.grad_scale = o.grad_scale;
+  // As many blocks a warp as leave four CTAs for each place on the GPU (a CTA spends a
+  // microsecond or two on finding its tensor and on its first loads), one for small sets.
+  int64_t blocks = 0;
+  for (int k = 0; k < n_params; ++k) blocks += (params[k].n + kBlock - 1) / kBlock;
+  int64_t steps = blocks / (static_cast<int64_t>(kAdamWarps) * 4 * 8 * ctx.num_sms);
+  steps = steps < 1 ? 1 : (steps > kMaxSteps ? kMaxSteps : steps);
+  a.cta_blocks = kAdamWarps * static_cast<int>(steps);
+  const int64_t chunk = static_cast<int64_t>(a.cta_blocks) * kBlock;
   int i = 0;
   while (i < n_params) {
     a.n = 0;
@@ -417,7 +456,7 @@ int launch_adamw(const LaunchCtx& ctx, const occult_adamw_t& o, const occult_par
     for (; i < n_params && a.n < kMaxTensors; ++i) {
       const occult_param_t& p = params[i];
       if (p.n == 0) continue;
-      const int64_t c = (p.n + kChunk - 1) / kChunk;
+      const int64_t c = (p.n + chunk - 1) / chunk;
       if (chunks + c > 0x7fffffff) {
         if (a.n > 0) break;
         return OCCULT_ERR_UNSUPPORTED;
@@ -441,7 +480,7 @@ int launch_adamw(const LaunchCtx& ctx, const occult_adamw_t& o, const occult_par
 
 int launch_adamw_read(const LaunchCtx& ctx, const uint8_t* codes, const uint8_t* exps, int64_t n,
                       int which, void* out) {
-  const int64_t need = (n + 2047) / 2048;
+  const int64_t need = (n + kReadChunk - 1) / kReadChunk;
   if (need > 0x7fffffff) return OCCULT_ERR_UNSUPPORTED;
   const unsigned grid = static_cast<unsigned>(need);
   __nv_bfloat16* o = static_cast<__nv_bfloat16*>(out);

@@ -313,31 +313,17 @@ __global__ void __launch_bounds__(kSumThreads) balance_groups_kernel(BalanceArgs
   pdl_trigger();
   for (int e = tid; e < a.Ne; e += kSumThreads) s_group.dev[e] = a.e2v[e];
   const Work w = work_of(a.ws, tiles.n, a.Ne, a.G);
-  // tokens, and groups that have any, over the whole batch (a group's tiles by one
-  // thread when they are few, by a warp when many); both are below 2^31
-  long long tok = 0;
-  const int wide = tiles.per_group > 16 ? 32 : 1, part = tid % wide;
-  for (int g = tid / wide; g < a.G; g += kSumThreads / wide) {
-    int n = 0;
-#pragma unroll 4
-    for (int i = part; i < tiles.per_group; i += wide)
-      n += w.n[static_cast<int64_t>(g) * tiles.per_group + i];
-    if (wide == 32) n = __reduce_add_sync(0xffffffffu, n);
-    if (part == 0) tok += n + (static_cast<long long>(n > 0) << 32);
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) tok += __shfl_xor_sync(0xffffffffu, tok, o);
-  if (lane == 0) s_tok[warp] = tok;
   int cols = 32;  // a power of two of at least Ne threads a slice of the tiles
   while (cols < a.Ne) cols *= 2;
   const int col = tid % cols, slice = tid / cols, slices = kSumThreads / cols;
   float inv_a = 1.f, inv_n = 1.f;
+  long long tok = 0;
   for (int g = blockIdx.x; g < a.G; g += gridDim.x) {
     const int64_t tile0 = static_cast<int64_t>(g) * tiles.per_group;
     float s = 0.f, sq = 0.f;
     int c = 0, n = 0;
     if (col < a.Ne) {
-#pragma unroll 8
+#pragma unroll 10
       for (int i = slice; i < tiles.per_group; i += slices) {
         s += w.p_sum[(tile0 + i) * a.Ne + col];
         c += w.count[(tile0 + i) * a.Ne + col];
@@ -346,6 +332,26 @@ __global__ void __launch_bounds__(kSumThreads) balance_groups_kernel(BalanceArgs
     for (int i = tid; i < tiles.per_group; i += kSumThreads) {
       sq += w.sq[tile0 + i];
       n += w.n[tile0 + i];
+    }
+    if (g == static_cast<int>(blockIdx.x)) {
+      // once: tokens, and groups that have any, over the whole batch (a group's tiles by
+      // one thread when they are few, by a warp when many); both are below 2^31
+      if (a.G == 1) {
+        tok = n;  // (summed below)
+      } else {
+        const int wide = tiles.per_group > 16 ? 32 : 1, part = tid % wide;
+        for (int k = tid / wide; k < a.G; k += kSumThreads / wide) {
+          int m = 0;
+#pragma unroll 4
+          for (int i = part; i < tiles.per_group; i += wide)
+            m += w.n[static_cast<int64_t>(k) * tiles.per_group + i];
+          if (wide == 32) m = __reduce_add_sync(0xffffffffu, m);
+          if (part == 0) tok += m + (static_cast<long long>(m > 0) << 32);
+        }
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) tok += __shfl_xor_sync(0xffffffffu, tok, o);
+      if (lane == 0) s_tok[warp] = tok;
     }
     s_part[tid] = s;
     s_cpart[tid] = c;
@@ -377,7 +383,8 @@ __global__ void __launch_bounds__(kSumThreads) balance_groups_kernel(BalanceArgs
     }
     __syncthreads();
     tok = s_tok[0];
-    const int N = static_cast<int>(tok & 0xffffffffll), A = static_cast<int>(tok >> 32);
+    const int N = static_cast<int>(tok & 0xffffffffll);
+    const int A = a.G == 1 ? 1 : static_cast<int>(tok >> 32);
     inv_a = 1.f / static_cast<float>(A > 0 ? A : 1);
     inv_n = 1.f / static_cast<float>(N > 0 ? N : 1);
     float terms[3];
