@@ -194,6 +194,11 @@ __device__ __forceinline__ float rcp_approx(float x) {
   return r;
 }
 __device__ __forceinline__ float2 two(float x) { return make_float2(x, x); }
+// The sums of the moments, one by one: a packed sum is contracted with the packed
+// products before it whatever rounding they ask for.
+__device__ __forceinline__ float2 add_rn(float2 a, float2 b) {
+  return make_float2(__fadd_rn(a.x, b.x), __fadd_rn(a.y, b.y));
+}
 // max of three that a NaN among them comes through
 __device__ __forceinline__ float max3_nan(float a, float b, float c) {
   float r;
@@ -281,8 +286,8 @@ __device__ __forceinline__ void step_block(const AdamTable& a, const Tensor& T, 
       }
       const float2 g = make_float2(x.g[h][j], x.g[h][j + 1]);
       const float2 gm = __fmul2_rn(two(gs_m), g), gv = __fmul2_rn(two(gs_v), g);
-      m = __fadd2_rn(__fmul2_rn(two(a.b1), m), __fmul2_rn(two(a.c1), gm));
-      v = __fadd2_rn(__fmul2_rn(two(a.b2), v), __fmul2_rn(__fmul2_rn(two(a.c2), gv), gv));
+      m = add_rn(__fmul2_rn(two(a.b1), m), __fmul2_rn(two(a.c1), gm));
+      v = add_rn(__fmul2_rn(two(a.b2), v), __fmul2_rn(__fmul2_rn(two(a.c2), gv), gv));
       const float2 root = make_float2(sqrtf(v.x), sqrtf(v.y));
       const float2 den = __ffma2_rn(root, two(a.inv_root), two(a.eps));
       const float2 upd = __fmul2_rn(m, make_float2(rcp_approx(den.x), rcp_approx(den.y)));

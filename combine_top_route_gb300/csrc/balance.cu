@@ -13,10 +13,15 @@ namespace occult {
 namespace {
 
 constexpr int kTileThreads = 512;
-constexpr int kTileWarps = kTileThreads / 32;
+constexpr int kOneThreads = 1024;
 constexpr int kSumThreads = 1024;
+constexpr int kMaxWarps = 32;
+static_assert(kSumThreads == 32 * kMaxWarps, "a warp reads one word of every warp");
 constexpr int kGradThreads = 256;
-constexpr int kMaxTiles = 304;   // of a batch that is not cut into more groups
+// Tiles of a batch: two CTAs an SM where the groups have their own second passes, one
+// where a single CTA adds all of them up (11.2 us at 304 tiles, 10.3 at 152 for the loss
+// of 32768 tokens and 64 experts in one group; 36 against 63 us with 32 groups of 4096).
+constexpr int kMaxTiles = 304, kMaxTilesOne = 152;
 constexpr int kMinTile = 64;     // tokens
 
 // Workspace, in words: probability sums and counts [tiles][Ne], then for every tile
@@ -29,7 +34,7 @@ struct Tiles {
 __host__ __device__ inline Tiles tiles_of(int T, int L, int G) {
   const int tokens = T < L ? (T > 0 ? T : 1) : L;
   // as many tiles as keep every SM busy, at least kMinTile tokens each
-  int per = kMaxTiles / G;
+  int per = G == 1 ? kMaxTilesOne : kMaxTiles / G;
   const int most = (tokens + kMinTile - 1) / kMinTile;
   per = per < 1 ? 1 : (per > most ? most : per);
   Tiles t;
@@ -113,57 +118,73 @@ struct Sums {
   int n;                        // tokens
 };
 
-// The sums of tokens [t0, t1) by a CTA of kTileThreads, in a fixed order.
-template <int LP>
+// The sums of tokens [t0, t1) by a CTA of THREADS, in a fixed order.
+template <int LP, int THREADS>
 struct TileScratch {
-  float p[kTileWarps][LP * 8];
-  float sq[kTileWarps];
-  int n[kTileWarps];
+  float p[THREADS / 32][LP * 8];
+  float sq[THREADS / 32];
+  int n[THREADS / 32];
 };
-template <int LP>
+template <int LP, int THREADS>
 __device__ __forceinline__ void sum_tile(const BalanceArgs& a, int64_t t0, int64_t t1,
-                                         TileScratch<LP>& x, Sums& out) {
-  constexpr int kTok = 32 / LP;  // tokens of a warp's step
+                                         TileScratch<LP, THREADS>& x, Sums& out) {
+  constexpr int kWarps = THREADS / 32;
+  constexpr int kTok = 32 / LP;            // tokens of a row of lanes
+  constexpr int kRows = 1;                 // of a step (2: registers spill, 35.6 -> 42.1 us)
+  constexpr int kStep = kWarps * kTok * kRows;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane % LP;
   const bool vec = a.Ne % 4 == 0;
-  for (int e = threadIdx.x; e < a.Ne; e += kTileThreads) out.c[e] = 0;
+  for (int e = threadIdx.x; e < a.Ne; e += THREADS) out.c[e] = 0;
   __syncthreads();
   float acc[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) acc[i] = 0.f;
   float sq = 0.f;
   int n = 0;
-  // the next step's row, mask and ids are on their way while this one's is summed
+  // the next step's rows, masks and ids are on their way while this one's are summed
   // (lanes past the end run along on the first row; what a masked row gives is dropped)
-  float next[8];
-  bool next_on = false;
-  int next_id[2];
+  float next[kRows][8];
+  bool next_on[kRows];
+  int next_id[kRows][2];
   auto fetch = [&](int64_t b) {
-    const int64_t t = b + lane / LP;
-    const bool in = t < t1;
-    load_row<LP>(a.logits + (in ? t : t0) * a.Ne, a.Ne, vec, sub, minus_inf(), next);
-    next_on = in && (!a.mask || a.mask[t]);
 #pragma unroll
-    for (int r = 0; r < 2; ++r)
-      next_id[r] = in && sub + r * LP < a.k ? a.ids[t * a.k + sub + r * LP] : -1;
+    for (int q = 0; q < kRows; ++q) {
+      const int64_t t = b + q * (kWarps * kTok) + lane / LP;
+      const bool in = t < t1;
+      load_row<LP>(a.logits + (in ? t : t0) * a.Ne, a.Ne, vec, sub, minus_inf(), next[q]);
+      next_on[q] = in && (!a.mask || a.mask[t]);
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+        next_id[q][r] = in && sub + r * LP < a.k ? a.ids[t * a.k + sub + r * LP] : -1;
+    }
   };
   int64_t b = t0 + warp * kTok;
   if (b < t1) fetch(b);
-  for (; b < t1; b += kTileWarps * kTok) {
-    float v[8], inv;
+  for (; b < t1; b += kStep) {
+    float v[kRows][8], inv[kRows], lse[kRows];
+    bool on[kRows];
+    int id[kRows][2];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = next[i];
-    const bool on = next_on;
-    const int id[2] = {next_id[0], next_id[1]};
-    if (b + kTileWarps * kTok < t1) fetch(b + kTileWarps * kTok);
-    const float lse = softmax_row<LP>(v, &inv);
-    if (on) {
+    for (int q = 0; q < kRows; ++q) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) acc[i] = fmaf(v[i], inv, acc[i]);
-      if (sub == 0) { sq = fmaf(lse, lse, sq); ++n; }
+      for (int i = 0; i < 8; ++i) v[q][i] = next[q][i];
+      on[q] = next_on[q];
+      id[q][0] = next_id[q][0];
+      id[q][1] = next_id[q][1];
+    }
+    if (b + kStep < t1) fetch(b + kStep);
+#pragma unroll
+    for (int q = 0; q < kRows; ++q) lse[q] = softmax_row<LP>(v[q], &inv[q]);
+#pragma unroll
+    for (int q = 0; q < kRows; ++q) {
+      if (!on[q]) continue;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) acc[i] = fmaf(v[q][i], inv[q], acc[i]);
+      if (sub == 0) { sq = fmaf(lse[q], lse[q], sq); ++n; }
 #pragma unroll
       for (int r = 0; r < 2; ++r)
-        if (static_cast<unsigned>(id[r]) < static_cast<unsigned>(a.Ne)) atomicAdd(&out.c[id[r]], 1);
+        if (static_cast<unsigned>(id[q][r]) < static_cast<unsigned>(a.Ne))
+          atomicAdd(&out.c[id[q][r]], 1);
     }
     __syncwarp();
   }
@@ -179,18 +200,18 @@ __device__ __forceinline__ void sum_tile(const BalanceArgs& a, int64_t t0, int64
     for (int i = 0; i < 8; ++i) x.p[warp][expert_of<LP>(lane, i)] = acc[i];
   if (lane == 0) { x.sq[warp] = sq; x.n[warp] = n; }
   __syncthreads();
-  for (int e = threadIdx.x; e < a.Ne; e += kTileThreads) {
+  for (int e = threadIdx.x; e < a.Ne; e += THREADS) {
     float s = 0.f;
 #pragma unroll
-    for (int i = 0; i < kTileWarps; ++i) s += x.p[i][e];
+    for (int i = 0; i < kWarps; ++i) s += x.p[i][e];
     out.p[e] = s;
   }
-  if (threadIdx.x == kTileThreads - 1) {
-    float s = 0.f;
-    int m = 0;
-    for (int i = 0; i < kTileWarps; ++i) { s += x.sq[i]; m += x.n[i]; }
-    out.sq = s;
-    out.n = m;
+  if (warp == kWarps - 1) {  // (no expert's warp: 256 of them are eight warps' threads)
+    float s = lane < kWarps ? x.sq[lane] : 0.f;
+    const int m = __reduce_add_sync(0xffffffffu, lane < kWarps ? x.n[lane] : 0);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (lane == 0) { out.sq = s; out.n = m; }
   }
   __syncthreads();
 }
@@ -257,14 +278,14 @@ __device__ __forceinline__ void write_loss(const BalanceArgs& a, const float (&t
 
 // A batch of one group and few tokens: everything by one CTA.
 template <int LP>
-__global__ void __launch_bounds__(kTileThreads, 1) balance_one_kernel(BalanceArgs a) {
-  __shared__ TileScratch<LP> s_tile;
+__global__ void __launch_bounds__(kOneThreads, 1) balance_one_kernel(BalanceArgs a) {
+  __shared__ TileScratch<LP, kOneThreads> s_tile;
   __shared__ Sums s_sums;
   __shared__ GroupScratch s_group;
   pdl_wait();
   pdl_trigger();
-  for (int e = threadIdx.x; e < a.Ne; e += kTileThreads) s_group.dev[e] = a.e2v[e];
-  sum_tile<LP>(a, 0, a.T, s_tile, s_sums);
+  for (int e = threadIdx.x; e < a.Ne; e += kOneThreads) s_group.dev[e] = a.e2v[e];
+  sum_tile<LP, kOneThreads>(a, 0, a.T, s_tile, s_sums);
   float terms[3];
   finish_group(a, 0, s_sums, s_group, 1.f, terms);
   if (threadIdx.x == 0)
@@ -275,7 +296,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) balance_one_kernel(BalanceArg
 template <int LP>
 __global__ void __launch_bounds__(kTileThreads, 2)
 balance_tiles_kernel(BalanceArgs a, Tiles tiles) {
-  __shared__ TileScratch<LP> s_tile;
+  __shared__ TileScratch<LP, kTileThreads> s_tile;
   __shared__ Sums s_sums;
   pdl_wait();
   pdl_trigger();
@@ -285,7 +306,7 @@ balance_tiles_kernel(BalanceArgs a, Tiles tiles) {
     const int64_t g0 = static_cast<int64_t>(g) * a.L;
     const int64_t g1 = min(static_cast<int64_t>(a.T), g0 + a.L);
     const int64_t t0 = g0 + static_cast<int64_t>(blockIdx.x) * tiles.len;
-    sum_tile<LP>(a, t0, min(g1, t0 + tiles.len), s_tile, s_sums);
+    sum_tile<LP, kTileThreads>(a, t0, min(g1, t0 + tiles.len), s_tile, s_sums);
     const int64_t tile = static_cast<int64_t>(g) * tiles.per_group + blockIdx.x;
     for (int e = threadIdx.x; e < a.Ne; e += kTileThreads) {
       w.p_sum[tile * a.Ne + e] = s_sums.p[e];
@@ -506,14 +527,14 @@ size_t balance_ws_bytes(const occult_desc_t& ds, int group_len) {
 }
 
 int launch_balance_loss(const LaunchCtx& ctx, const BalanceArgs& a) {
-  // few tokens: one CTA does both passes (a step of all its warps is 64, 32 or 16
-  // tokens; beyond some steps the second launch costs less)
+  // few tokens: one CTA does both passes (a step of all its warps is 256, 128 or 64
+  // tokens; beyond two steps the second launch costs less)
   const int lp = a.Ne <= 64 ? 8 : a.Ne <= 128 ? 16 : 32;
-  if (a.G == 1 && a.T <= 8 * kTileThreads / lp) {
+  if (a.G == 1 && a.T <= 4 * kOneThreads / lp) {
     return cuda_status(
-        lp == 8    ? launch_pdl(balance_one_kernel<8>, 1, kTileThreads, 0, ctx.stream, a)
-        : lp == 16 ? launch_pdl(balance_one_kernel<16>, 1, kTileThreads, 0, ctx.stream, a)
-                   : launch_pdl(balance_one_kernel<32>, 1, kTileThreads, 0, ctx.stream, a));
+        lp == 8    ? launch_pdl(balance_one_kernel<8>, 1, kOneThreads, 0, ctx.stream, a)
+        : lp == 16 ? launch_pdl(balance_one_kernel<16>, 1, kOneThreads, 0, ctx.stream, a)
+                   : launch_pdl(balance_one_kernel<32>, 1, kOneThreads, 0, ctx.stream, a));
   }
   const Tiles tiles = tiles_of(a.T, a.L, a.G);
   const dim3 grid(tiles.per_group, a.G < 65535 ? a.G : 65535);

@@ -254,9 +254,33 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
       :: "r"(smem_u32(dst)), "l"(src), "r"(bytes), "r"(smem_u32(bar)) : "memory");
 }
 
-constexpr int kMaxStages = 4;  // rows of a ring
-// CTAs of an SM in the kernels with a ring (128 registers a thread)
-__host__ __device__ constexpr int ring_ctas(int G) { return G > 8 ? 1 : 2; }
+constexpr int kMaxStages = 3;  // rows of a ring
+
+// One scalar for every row of a group: each warp holds those of 32 rows in its lanes and
+// has the next 32 on their way (a load at each row would cost its latency there).
+struct RowScalars {
+  const float* p;
+  int64_t first, step;
+  int T;
+  float now, next;
+  __device__ RowScalars(const float* p, float none, int first, int step, int T)
+      : p(p), first(first), step(step), T(T), now(none), next(none) {
+    if (p) { load(now, 0); load(next, 32); }
+  }
+  __device__ void load(float& v, int k) {
+    const int64_t t = first + (k + static_cast<int>(threadIdx.x & 31)) * step;
+    if (t < T) v = p[t];
+  }
+  // the scalar of the group's k-th row; k = 0, 1, 2, ... in order
+  __device__ float at(int k) {
+    if (!p) return now;
+    if ((k & 31) == 0 && k > 0) {
+      now = next;
+      load(next, k + 32);
+    }
+    return __shfl_sync(0xffffffffu, now, k & 31);
+  }
+};
 
 // Bytes of one row in the forward's ring: y, then r.
 template <typename R>
@@ -266,8 +290,8 @@ __host__ __device__ __forceinline__ int fwd_row_bytes(int d) {
 
 // Forward of many rows: a group's rows come through a ring of shared memory that bulk
 // copies fill ahead of the arithmetic.
-template <typename R, typename L, int G, int U>
-__global__ void __launch_bounds__(Group<G>::kThreads, ring_ctas(G))
+template <typename R, typename L, int G, int U, int CTAS>
+__global__ void __launch_bounds__(Group<G>::kThreads, CTAS)
 norm_fwd_ring_kernel(NormArgs a, int stages, int* dev_err) {
   extern __shared__ __align__(128) unsigned char s_ring[];
   __shared__ uint64_t s_full[Group<G>::kGroups][kMaxStages];
@@ -315,8 +339,10 @@ norm_fwd_ring_kernel(NormArgs a, int stages, int* dev_err) {
   const float inv_d = 1.f / d;
   int stage = 0, flip = 0;
   uint32_t parity = 0;
-  for (int64_t t = first; t < a.T; t += step) {
-    float scale = a.gate_kind == OCCULT_GATE_TOKEN ? a.gate[t] : 1.f;
+  RowScalars gate(a.gate_kind == OCCULT_GATE_TOKEN ? a.gate : nullptr, 1.f, first, step, a.T);
+  int k = 0;
+  for (int64_t t = first; t < a.T; t += step, ++k) {
+    float scale = gate.at(k);
     if (!mbar_wait(&s_full[group][stage], parity, &s_abort)) {
       latch_error(dev_err, OCCULT_ERR_DEVICE_TIMEOUT);
       s_abort = 1;
@@ -381,17 +407,20 @@ __host__ __device__ __forceinline__ int bwd_row_bytes(int d) {
 }
 
 // Backward.  The rows of a group come through a ring of `stages` rows in shared
-// memory, filled by bulk copies that run ahead of the arithmetic; the one sync of a
-// row's sums also says that all of the group have read the row, whose place is
-// then refilled.  The column sums stay in the registers of the threads that own
+// memory, filled by bulk copies that run ahead of the arithmetic.  Up to two units a
+// thread stay in registers from their sums to their stores, more are read from shared
+// memory a second time.  The one sync of a row's sums also says which rows all of the
+// group are done with, so that their places can be refilled.  The column sums stay in the registers of the threads that own
 // the columns, over all the rows of the group.
-template <typename R, typename L, int G, int U>
-__global__ void __launch_bounds__(Group<G>::kThreads, ring_ctas(G))
+template <typename R, typename L, int G, int U, int CTAS>
+__global__ void __launch_bounds__(Group<G>::kThreads, CTAS)
 norm_bwd_rows_kernel(NormArgs a, float* part, int stages, int* dev_err) {
   extern __shared__ __align__(128) unsigned char s_ring[];
   __shared__ uint64_t s_full[Group<G>::kGroups][kMaxStages];
   __shared__ float4 s_red[2][Group<G>::kThreads / 32];
   __shared__ int s_abort;
+  constexpr bool kKeep = U <= 2;
+  constexpr int KEEP = kKeep ? U : 1;
   const int group = Group<G>::index(), place = Group<G>::place();
   const L* w_post = static_cast<const L*>(a.w_post);
   const L* w_pre = static_cast<const L*>(a.w_pre);
@@ -446,10 +475,12 @@ norm_bwd_rows_kernel(NormArgs a, float* part, int stages, int* dev_err) {
   const float out_scale = a.y ? a.res_scale : 1.f;
   int stage = 0, flip = 0;
   uint32_t parity = 0;
-  for (int64_t t = first; t < a.T; t += step) {
-    const float rp = w_post ? a.rstd_post[t] : 1.f;
-    const float rq = w_pre ? a.rstd_pre[t] : 0.f;
-    const float tok = token ? a.gate[t] : 1.f;
+  RowScalars post(w_post ? a.rstd_post : nullptr, 1.f, first, step, a.T);
+  RowScalars pre(w_pre ? a.rstd_pre : nullptr, 0.f, first, step, a.T);
+  RowScalars gate(token ? a.gate : nullptr, 1.f, first, step, a.T);
+  int k = 0;
+  for (int64_t t = first; t < a.T; t += step, ++k) {
+    const float rp = post.at(k), rq = pre.at(k), tok = gate.at(k);
     if (!mbar_wait(&s_full[group][stage], parity, &s_abort)) {
       // gave up: the error is latched, the remaining rows run through without waits
       latch_error(dev_err, OCCULT_ERR_DEVICE_TIMEOUT);
@@ -460,30 +491,41 @@ norm_bwd_rows_kernel(NormArgs a, float* part, int stages, int* dev_err) {
     const float* s_y = s_dx + d;
     const R* s_up = reinterpret_cast<const R*>(s_y + d);
     const R* s_r = s_up + d;
-    float4 dx[U], r[U], y[U], D[U];
     // with D0 = dr_out + rstd_pre w_pre dx:  sum w_pre dx r',  sum wq y D0,  sum wq y r'
     float4 sum = zero;
+    float4 k_dx[KEEP], k_r[KEEP], k_y[KEEP], k_D[KEEP];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int c = 4 * (u * 32 * G + place);
-      const bool in = c < d;
-      dx[u] = in && w_pre ? ld4(s_dx + c) : zero;
-      r[u] = in && w_pre ? ld4(s_r + c) : zero;
-      y[u] = in && use_y ? ld4(s_y + c) : zero;
-      D[u] = in && a.dr_out ? ld4(s_up + c) : zero;
-      const float4 g = mul4(dx[u], wp[u]);
-      const float4 q = mul4(y[u], wq[u]);
-      D[u] = fma4(g, rq, D[u]);
-      sum.x += dot4(g, r[u]);
-      sum.y += dot4(q, D[u]);
-      sum.z += dot4(q, r[u]);
+      if (c >= d) continue;
+      float4 dx = zero, r = zero, y = zero, D = a.dr_out ? ld4(s_up + c) : zero;
+      if (w_pre) {
+        dx = ld4(s_dx + c);
+        r = ld4(s_r + c);
+        const float4 g = mul4(dx, wp[u]);
+        D = fma4(g, rq, D);
+        sum.x += dot4(g, r);
+      }
+      if (use_y) {
+        y = ld4(s_y + c);
+        const float4 q = mul4(y, wq[u]);
+        sum.y += dot4(q, D);
+        sum.z += dot4(q, r);
+      }
+      if (kKeep) { k_dx[u % KEEP] = dx; k_r[u % KEEP] = r; k_y[u % KEEP] = y; k_D[u % KEEP] = D; }
     }
     sum = group_sum<G>(sum, s_red[flip]);
     flip ^= 1;
     if (G == 1) __syncwarp();
-    if (place == 0 && t + static_cast<int64_t>(stages) * step < a.T)
-      fill(stage, static_cast<int>(t + static_cast<int64_t>(stages) * step));
-    if (++stage == stages) { stage = 0; parity ^= 1; }
+    // past that sync all of the group are done with this row, where it is kept in
+    // registers, and with the one before in any case: its place is refilled
+    if (kKeep) {
+      if (place == 0 && t + static_cast<int64_t>(stages) * step < a.T)
+        fill(stage, static_cast<int>(t + static_cast<int64_t>(stages) * step));
+    } else if (place == 0 && stages > 1 && t != first &&
+               t + static_cast<int64_t>(stages - 1) * step < a.T)
+      fill(stage == 0 ? stages - 1 : stage - 1,
+           static_cast<int>(t + static_cast<int64_t>(stages - 1) * step));
     // mean(w_pre dx n) = rstd_pre sum.x / d;  sum wq m D and its mean
     const float k1 = -rq * rq * rq * sum.x * inv_d;
     const float qd = rp * fmaf(k1, sum.z, sum.y);
@@ -495,15 +537,29 @@ norm_bwd_rows_kernel(NormArgs a, float* part, int stages, int* dev_err) {
     for (int u = 0; u < U; ++u) {
       const int c = 4 * (u * 32 * G + place);
       if (c >= d) continue;
-      D[u] = fma4(r[u], k1, D[u]);
-      sum_pre[u] = add4(sum_pre[u], mul4(dx[u], scale4(r[u], rq)));
-      st4(static_cast<R*>(a.dr) + base + c, scale4(D[u], out_scale));
+      float4 D = kKeep ? k_D[u % KEEP] : a.dr_out ? ld4(s_up + c) : zero;
+      if (w_pre) {
+        const float4 dx = kKeep ? k_dx[u % KEEP] : ld4(s_dx + c);
+        const float4 r = kKeep ? k_r[u % KEEP] : ld4(s_r + c);
+        if (!kKeep) D = fma4(mul4(dx, wp[u]), rq, D);
+        D = fma4(r, k1, D);
+        sum_pre[u] = add4(sum_pre[u], mul4(dx, scale4(r, rq)));
+      }
+      st4(static_cast<R*>(a.dr) + base + c, scale4(D, out_scale));
       if (!a.y) continue;
-      sum_post[u] = add4(sum_post[u], mul4(D[u], scale4(y[u], ru)));
-      float4 o = scale4(mul4(D[u], wq[u]), ru);
-      if (w_post) o = fma4(y[u], k2, o);
+      float4 o = scale4(mul4(D, wq[u]), ru);
+      if (use_y) {
+        const float4 y = kKeep ? k_y[u % KEEP] : ld4(s_y + c);
+        sum_post[u] = add4(sum_post[u], mul4(D, scale4(y, ru)));
+        if (w_post) o = fma4(y, k2, o);
+      }
       st4(static_cast<L*>(a.dy) + base + c, o);
     }
+    if (!kKeep && stages == 1) {  // one place: it is refilled when all are done with this row
+      Group<G>::sync();
+      if (place == 0 && t + static_cast<int64_t>(step) < a.T) fill(0, static_cast<int>(t + step));
+    }
+    if (++stage == stages) { stage = 0; parity ^= 1; }
   }
   if (s_abort && place == 0) {  // copies may still be in flight: give them the limit again
     volatile int none = 0;
@@ -584,20 +640,27 @@ int fwd_rows(const LaunchCtx& ctx, const NormArgs& a) {
                                 Group<G>::kThreads, 0, ctx.stream, a));
 }
 
+// Rows of a ring of `bytes` each (all groups of a CTA): three, two with an fp32 stream.
+// Reads that run further ahead of the stores slow both: T=30011, d=2048, norms on both
+// sides, us with two, three, four rows: forward 102, 93, 92 (bf16 stream) and 130, 147,
+// 149 (fp32); backward 155, 152, 153 and 199, 220, 222.
 constexpr int kRingBytes = 200 * 1024;  // of shared memory an SM, over its CTAs
+template <typename R>
+inline int ring_stages(int bytes, int ctas) {
+  const int fit = kRingBytes / ctas / bytes, n = sizeof(R) == 4 ? 2 : 3;
+  return n < fit ? n : fit;
+}
 
-template <typename R, typename L, int G, int U>
+template <typename R, typename L, int G, int U, int CTAS>
 int fwd_ring(const LaunchCtx& ctx, const NormArgs& a) {
-  constexpr int kCtas = ring_ctas(G);
   const int row = fwd_row_bytes<R>(a.d) * Group<G>::kGroups;
-  int stages = kRingBytes / kCtas / row;
-  stages = stages > kMaxStages ? kMaxStages : stages;
+  const int stages = ring_stages<R>(row, CTAS);
   const size_t smem = static_cast<size_t>(stages) * row;
-  const int rc = allow_smem(norm_fwd_ring_kernel<R, L, G, U>, smem);
+  const int rc = allow_smem(norm_fwd_ring_kernel<R, L, G, U, CTAS>, smem);
   if (rc) return rc;
   const int need = (a.T + Group<G>::kGroups - 1) / Group<G>::kGroups;
-  const int cap = ctx.num_sms * kCtas;
-  return cuda_status(launch_pdl(norm_fwd_ring_kernel<R, L, G, U>, need < cap ? need : cap,
+  const int cap = ctx.num_sms * CTAS;
+  return cuda_status(launch_pdl(norm_fwd_ring_kernel<R, L, G, U, CTAS>, need < cap ? need : cap,
                                 Group<G>::kThreads, smem, ctx.stream, a, stages, ctx.dev_err));
 }
 
@@ -608,11 +671,13 @@ int fwd(const LaunchCtx& ctx, const NormArgs& a) {
   // of up to 8192 columns); few rows have as many warps each as give a thread two
   // loads of each tensor, and no ring to set up.
   if (a.T >= 4 * ctx.num_sms && d * sizeof(R) % 16 == 0 && d <= 8192) {
-    if (d <= 512) return fwd_ring<R, L, 1, 4>(ctx, a);
-    if (d <= 1024) return fwd_ring<R, L, 2, 4>(ctx, a);
-    if (d <= 2048) return fwd_ring<R, L, 4, 4>(ctx, a);
-    if (d <= 4096) return fwd_ring<R, L, 8, 4>(ctx, a);
-    return fwd_ring<R, L, 16, 4>(ctx, a);
+    if (d <= 128) return fwd_ring<R, L, 1, 1, 5>(ctx, a);
+    if (d <= 256) return fwd_ring<R, L, 1, 2, 4>(ctx, a);
+    if (d <= 512) return fwd_ring<R, L, 2, 2, 3>(ctx, a);
+    if (d <= 1024) return fwd_ring<R, L, 4, 2, 2>(ctx, a);
+    if (d <= 2048) return fwd_ring<R, L, 8, 2, 2>(ctx, a);
+    if (d <= 4096) return fwd_ring<R, L, 16, 2, 2>(ctx, a);
+    return fwd_ring<R, L, 16, 4, 1>(ctx, a);
   }
   if (d <= 256) return fwd_rows<R, L, 1, 2>(ctx, a);
   if (d <= 512) return fwd_rows<R, L, 2, 2>(ctx, a);
@@ -623,22 +688,20 @@ int fwd(const LaunchCtx& ctx, const NormArgs& a) {
   return fwd_rows<R, L, 16, 8>(ctx, a);
 }
 
-template <typename R, typename L, int G, int U>
+template <typename R, typename L, int G, int U, int CTAS>
 int bwd_rows(const LaunchCtx& ctx, const NormArgs& a, float* part, int* grid) {
-  constexpr int kCtas = ring_ctas(G);
   const int row = bwd_row_bytes<R>(a.d) * Group<G>::kGroups;
-  int stages = kRingBytes / kCtas / row;
-  stages = stages > kMaxStages ? kMaxStages : stages;
+  const int stages = ring_stages<R>(row, CTAS);
   size_t smem = static_cast<size_t>(stages) * row;
   const size_t sums = 2 * static_cast<size_t>(a.d) * Group<G>::kGroups * sizeof(float);
   smem = smem > sums ? smem : sums;
-  int rc = allow_smem(norm_bwd_rows_kernel<R, L, G, U>, smem);
+  int rc = allow_smem(norm_bwd_rows_kernel<R, L, G, U, CTAS>, smem);
   if (rc) return rc;
   const int need = (a.T + Group<G>::kGroups - 1) / Group<G>::kGroups;
-  const int cap = ctx.num_sms * kCtas < kNormMaxParts ? ctx.num_sms * kCtas : kNormMaxParts;
+  const int cap = ctx.num_sms * CTAS < kNormMaxParts ? ctx.num_sms * CTAS : kNormMaxParts;
   *grid = need < cap ? need : cap;
-  return cuda_status(launch_pdl(norm_bwd_rows_kernel<R, L, G, U>, *grid, Group<G>::kThreads, smem,
-                                ctx.stream, a, part, stages, ctx.dev_err));
+  return cuda_status(launch_pdl(norm_bwd_rows_kernel<R, L, G, U, CTAS>, *grid, Group<G>::kThreads,
+                                smem, ctx.stream, a, part, stages, ctx.dev_err));
 }
 
 template <typename R, typename L>
@@ -660,12 +723,14 @@ int bwd(const LaunchCtx& ctx, const NormArgs& a, float* part) {
   if (!sums) part = nullptr;
   // bulk copies move whole 16 bytes; the ring holds a row of up to 8192 columns
   if (d * sizeof(R) % 16 != 0 || d > 8192) rc = bwd_any<R, L>(ctx, a, ws, &grid);
-  else if (d <= 256) rc = bwd_rows<R, L, 1, 2>(ctx, a, part, &grid);
-  else if (d <= 512) rc = bwd_rows<R, L, 2, 2>(ctx, a, part, &grid);
-  else if (d <= 1024) rc = bwd_rows<R, L, 4, 2>(ctx, a, part, &grid);
-  else if (d <= 2048) rc = bwd_rows<R, L, 8, 2>(ctx, a, part, &grid);
-  else if (d <= 4096) rc = bwd_rows<R, L, 16, 2>(ctx, a, part, &grid);
-  else rc = bwd_rows<R, L, 16, 4>(ctx, a, part, &grid);
+  else if (d <= 128) rc = bwd_rows<R, L, 1, 1, 3>(ctx, a, part, &grid);
+  else if (d <= 256) rc = bwd_rows<R, L, 1, 2, 2>(ctx, a, part, &grid);
+  else if (d <= 512) rc = bwd_rows<R, L, 2, 2, 2>(ctx, a, part, &grid);
+  else if (d <= 1024) rc = bwd_rows<R, L, 4, 2, 2>(ctx, a, part, &grid);
+  else if (d <= 2048) rc = bwd_rows<R, L, 8, 2, 2>(ctx, a, part, &grid);
+  else if (d <= 4096) rc = bwd_rows<R, L, 8, 4, 2>(ctx, a, part, &grid);
+  else if (d <= 6144) rc = bwd_rows<R, L, 16, 3, 1>(ctx, a, part, &grid);
+  else rc = bwd_rows<R, L, 16, 4, 1>(ctx, a, part, &grid);
   if (rc || !sums) return rc;
   return cuda_status(launch_pdl(norm_bwd_cols_kernel<L>, (2 * d + 31) / 32, 256, 0, ctx.stream, a,
                                 part, grid));
