@@ -773,3 +773,4 @@ def occult_adamw_read(codes, exps, which, out, stream=None):
 
 
 from .pipeline import OccultMoE, desc_for  # noqa: E402  (needs the names above)
+from .train import OccultAdamW, OccultBlock  # noqa: E402

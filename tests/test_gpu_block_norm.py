@@ -355,3 +355,81 @@ def test_binding_refuses_strided_and_wrong_types(occ):
         occ.occult_block_norm(c.desc(occ), c.opt(occ), x, w_pre=w, x=x[:3].contiguous())
     with pytest.raises(occ.OccultError):      # y without its residual output
         occ.occult_block_norm(c.desc(occ), c.opt(occ), x, y=torch.zeros(4, 128, device="cuda"))
+
+
+def test_offsets_past_32_bits(occ):
+    """2^31 elements and more (T = 1048600, d = 2048): the last rows, both directions."""
+    T, d, k = 1048600, 2048, 40
+    ds = occ.desc_for(synth.CONFIGS["olmoe_fwd"].with_(T=T, d=d, inter=64))
+    opt = occ.occult_norm_t(EPS, 0.75, occ.GATE_TOKEN, occ.OCCULT_BF16)
+    c = Case(k, d, "bf16", "bf16", gate="token", seed=12)
+    z = lambda dt: torch.zeros(T, d, dtype=dt, device="cuda")  # noqa: E731
+    r, y, r_out, x = z(torch.bfloat16), z(torch.float32), z(torch.bfloat16), z(torch.bfloat16)
+    gate = torch.ones(T, device="cuda")
+    rp, rq = torch.empty(T, device="cuda"), torch.empty(T, device="cuda")
+    r[-k:], y[-k:], gate[-k:] = dev(c.r, "bf16"), dev(c.y, "f32"), dev(c.g, "f32").view(-1)
+    w_post, w_pre = dev(c.w_post, "bf16"), dev(c.w_pre, "bf16")
+    occ.occult_block_norm(ds, opt, r, y=y, w_post=w_post, gate=gate, w_pre=w_pre, r_out=r_out, x=x,
+                          rstd_post=rp, rstd_pre=rq)
+    want = onorm.forward(c.r, c.y, c.w_post, c.g, c.w_pre, EPS, 0.75)
+    for got, key in ((r_out, "r_out"), (x, "x")):
+        a, b = got[-k:].double().cpu().numpy(), want[key]
+        assert np.abs(a - b).max() <= 2.0 ** -7 * np.abs(b).max()
+        assert not got[:-k:4099].any()
+    del x
+    dx = z(torch.float32)
+    dx[-k:] = dev(c.dx, "f32")
+    dr_out = r.zero_()
+    dr_out[-k:] = dev(c.dr_out, "bf16")
+    dy = z(torch.bfloat16)
+    sums = [torch.empty(d, device="cuda") for _ in range(2)]
+    ws = torch.empty(occ.workspace_size(ds, occ.WS_BLOCK_NORM_BWD), dtype=torch.uint8, device="cuda")
+    saved = r_out[-k:].double().cpu().numpy()
+    dgate = torch.empty(T, device="cuda")
+    occ.occult_block_norm_bwd(ds, opt, dr_out, r_out, dr_out, ws, dx=dx, y=y, w_post=w_post,
+                              gate=gate, w_pre=w_pre, rstd_post=rp, rstd_pre=rq, dy=dy,
+                              dw_post=sums[0], dgate=dgate, dw_pre=sums[1])
+    want = onorm.backward(c.dr_out, c.dx, saved, c.y, c.w_post, c.g, c.w_pre,
+                          rp[-k:].double().cpu().numpy(), rq[-k:].double().cpu().numpy(), 0.75)
+    for got, key in ((dr_out[-k:], "dr"), (dy[-k:], "dy"), (sums[0], "dw_post"), (sums[1], "dw_pre")):
+        a, b = got.double().cpu().numpy(), want[key]
+        assert np.abs(a - b).max() <= 2.0 ** -7 * np.abs(b).max(), key
+    assert not dy[:-k:4099].any()
+
+
+def test_replays_from_a_cuda_graph(occ):
+    c = Case(900, 1024, "bf16", "bf16", gate="channel", seed=14)
+    ds, opt = c.desc(occ), c.opt(occ)
+    t = {k: dev(getattr(c, k), kind) for k, kind in (("r", "bf16"), ("y", "f32"), ("w_post", "bf16"),
+                                                     ("w_pre", "bf16"), ("g", "f32"),
+                                                     ("dr_out", "bf16"), ("dx", "f32"))}
+    o = {k: torch.zeros(900, 1024, dtype=torch.bfloat16, device="cuda") for k in ("r_out", "x", "dr", "dy")}
+    f = {k: torch.zeros(n, device="cuda") for k, n in (("rp", 900), ("rq", 900), ("dw_post", 1024),
+                                                       ("dgate", 1024), ("dw_pre", 1024))}
+    ws = torch.empty(occ.workspace_size(ds, occ.WS_BLOCK_NORM_BWD), dtype=torch.uint8, device="cuda")
+
+    def run():
+        occ.occult_block_norm(ds, opt, t["r"], y=t["y"], w_post=t["w_post"], gate=t["g"],
+                              w_pre=t["w_pre"], r_out=o["r_out"], x=o["x"], rstd_post=f["rp"],
+                              rstd_pre=f["rq"])
+        occ.occult_block_norm_bwd(ds, opt, t["dr_out"], o["r_out"], o["dr"], ws, dx=t["dx"], y=t["y"],
+                                  w_post=t["w_post"], gate=t["g"], w_pre=t["w_pre"],
+                                  rstd_post=f["rp"], rstd_pre=f["rq"], dy=o["dy"],
+                                  dw_post=f["dw_post"], dgate=f["dgate"], dw_pre=f["dw_pre"])
+
+    run()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run()
+    t["y"].mul_(0.5)
+    t["dx"].add_(1.0)
+    run()
+    torch.cuda.synchronize()
+    want = {k: v.clone() for k, v in {**o, **f}.items()}
+    for v in {**o, **f}.values():
+        v.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    for k, v in {**o, **f}.items():
+        assert torch.equal(v, want[k]), k
