@@ -353,7 +353,14 @@ __device__ __forceinline__ void step_blocks(const AdamTable& a, const Tensor& T,
   const int64_t whole = T.n / kBlock;
   const int64_t full_end = end < whole ? end : whole;
   Raw<BITS> x;
-  if (BITS == 8) {
+  if (BITS == 8 && KIND == KIND_BF16 && blk + kAdamWarps < full_end) {
+    Raw<BITS> y;
+    load_block<BITS, KIND, true>(T, blk, x);
+    load_block<BITS, KIND, true>(T, blk + kAdamWarps, y);
+    step_block<BITS, KIND, true>(a, T, blk, gs, x);
+    step_block<BITS, KIND, true>(a, T, blk + kAdamWarps, gs, y);
+    blk += 2 * kAdamWarps;
+  } else if (BITS == 8) {
     if (blk < full_end) load_block<BITS, KIND, true>(T, blk, x);
     for (; blk < full_end; blk += kAdamWarps) {
       Raw<BITS> y = x;
