@@ -11,7 +11,7 @@ namespace occult {
 
 namespace {
 
-constexpr int kNormThreads = 256;
+constexpr int kWideThreads = 1024;  // of the backward of rows too wide for a ring
 
 __device__ __forceinline__ float4 ld4(const float* p) { return *reinterpret_cast<const float4*>(p); }
 __device__ __forceinline__ float4 ld4(const __nv_bfloat16* p) {
@@ -80,7 +80,7 @@ __device__ __forceinline__ void block_sum(float (&v)[N], float (*s_red)[N]) {
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     v[i] = 0.f;
-    for (int w = 0; w < kNormThreads / 32; ++w) v[i] += s_red[w][i];
+    for (int w = 0; w < kWideThreads / 32; ++w) v[i] += s_red[w][i];
   }
 }
 
@@ -92,9 +92,9 @@ __device__ __forceinline__ void block_sum(float (&v)[N], float (*s_red)[N]) {
 // The column sums stay with the threads that own the columns, in shared memory,
 // and go to one row of partial sums a CTA.
 template <typename R, typename L>
-__global__ void __launch_bounds__(kNormThreads) norm_bwd_kernel(NormArgs a, float* part) {
+__global__ void __launch_bounds__(kWideThreads) norm_bwd_kernel(NormArgs a, float* part) {
   extern __shared__ float s_cols[];  // [2][d]: sum dx n, sum (gate) D m
-  __shared__ float s_red[kNormThreads / 32][3];
+  __shared__ float s_red[kWideThreads / 32][3];
   pdl_wait();
   pdl_trigger();
   const L* w_post = static_cast<const L*>(a.w_post);
@@ -103,7 +103,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_bwd_kernel(NormArgs a, floa
   const bool chan = a.gate_kind == OCCULT_GATE_CHANNEL, token = a.gate_kind == OCCULT_GATE_TOKEN;
   const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
   const float4 one = make_float4(1.f, 1.f, 1.f, 1.f);
-  for (int c = threadIdx.x * 4; c < a.d; c += kNormThreads * 4) {
+  for (int c = threadIdx.x * 4; c < a.d; c += kWideThreads * 4) {
     st4(s_cols + c, zero);
     st4(s_cols + a.d + c, zero);
   }
@@ -113,7 +113,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_bwd_kernel(NormArgs a, floa
     const float rq = w_pre ? a.rstd_pre[t] : 0.f;
     const float tok = token ? a.gate[t] : 1.f;
     float s[3] = {0.f, 0.f, 0.f};
-    for (int c = threadIdx.x * 4; c < a.d; c += kNormThreads * 4) {
+    for (int c = threadIdx.x * 4; c < a.d; c += kWideThreads * 4) {
       const float4 up = a.dr_out ? ld4(static_cast<const R*>(a.dr_out) + base + c) : zero;
       float4 g = zero, n = zero, q = zero;
       if (w_pre) {
@@ -134,7 +134,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_bwd_kernel(NormArgs a, floa
     const float qd = s[1] - c1 * rq * s[2];  // sum q D without the token's gate
     if (token && threadIdx.x == 0) a.dgate[t] = qd;
     const float c2 = tok * qd / a.d;         // mean(u m)
-    for (int c = threadIdx.x * 4; c < a.d; c += kNormThreads * 4) {
+    for (int c = threadIdx.x * 4; c < a.d; c += kWideThreads * 4) {
       float4 D = a.dr_out ? ld4(static_cast<const R*>(a.dr_out) + base + c) : zero;
       if (w_pre) {
         const float4 dx = ld4(a.dx + base + c);
@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_bwd_kernel(NormArgs a, floa
   }
   __syncthreads();  // the copy below goes over both sums in one stride
   float* row = part + static_cast<size_t>(blockIdx.x) * 2 * a.d;
-  for (int c = threadIdx.x * 4; c < 2 * a.d; c += kNormThreads * 4) st4(row + c, ld4(s_cols + c));
+  for (int c = threadIdx.x * 4; c < 2 * a.d; c += kWideThreads * 4) st4(row + c, ld4(s_cols + c));
 }
 
 // ---- rows held by groups of warps ------------------------------------------------
@@ -629,29 +629,35 @@ norm_bwd_rows_kernel(NormArgs a, float* part, int stages, int* dev_err) {
 }
 
 // Adds the CTAs' partial rows and turns the second sum into dw_post and a channel
-// gate's gradient: a CTA takes 32 columns, each of its warps every eighth row.
+// gate's gradient: a CTA takes 32 columns, each of its warps every 32nd row, so that
+// the loads of some 300 rows are all on their way at once.
+constexpr int kColWarps = 32;
 template <typename L>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(kColWarps * 32)
 norm_bwd_cols_kernel(NormArgs a, const float* __restrict__ part, int n_part) {
-  __shared__ float s_sum[8][32];
+  __shared__ float s_sum[kColWarps][33];
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
   float s = 0.f;
   if (c < 2 * a.d) {
-#pragma unroll 8
-    for (int p = warp; p < n_part; p += 8) s += part[static_cast<size_t>(p) * 2 * a.d + c];
+#pragma unroll 10
+    for (int p = warp; p < n_part; p += kColWarps) s += part[static_cast<size_t>(p) * 2 * a.d + c];
   }
   s_sum[warp][lane] = s;
   __syncthreads();
-  if (warp != 0 || c >= 2 * a.d) return;
-  for (int w = 1; w < 8; ++w) s += s_sum[w][lane];
-  if (c < a.d) {
-    if (a.dw_pre) a.dw_pre[c] = s;
+  // warp w adds column w of the 32
+  s = s_sum[lane][warp];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  const int col = blockIdx.x * 32 + warp;
+  if (lane != 0 || col >= 2 * a.d) return;
+  if (col < a.d) {
+    if (a.dw_pre) a.dw_pre[col] = s;
     return;
   }
-  const int j = c - a.d;
+  const int j = col - a.d;
   const bool chan = a.gate_kind == OCCULT_GATE_CHANNEL;
   if (a.dw_post) a.dw_post[j] = chan ? s * a.gate[j] : s;
   if (chan) a.dgate[j] = a.w_post ? s * to_f32(static_cast<const L*>(a.w_post)[j]) : s;
@@ -741,8 +747,8 @@ int bwd_any(const LaunchCtx& ctx, const NormArgs& a, float* part, int* grid) {
   const size_t smem = 2 * static_cast<size_t>(a.d) * sizeof(float);
   const int rc = allow_smem(norm_bwd_kernel<R, L>, smem);
   if (rc) return rc;
-  *grid = norm_bwd_parts(a.T);
-  return cuda_status(launch_pdl(norm_bwd_kernel<R, L>, *grid, kNormThreads, smem, ctx.stream, a,
+  *grid = a.T < ctx.num_sms ? a.T : ctx.num_sms;  // (a CTA's column sums fill most of an SM)
+  return cuda_status(launch_pdl(norm_bwd_kernel<R, L>, *grid, kWideThreads, smem, ctx.stream, a,
                                 part));
 }
 
@@ -764,7 +770,7 @@ int bwd(const LaunchCtx& ctx, const NormArgs& a, float* part) {
   else if (d <= 6144) rc = bwd_rows<R, L, 16, 3, 1>(ctx, a, part, &grid);
   else rc = bwd_rows<R, L, 16, 4, 1>(ctx, a, part, &grid);
   if (rc || !sums) return rc;
-  return cuda_status(launch_pdl(norm_bwd_cols_kernel<L>, (2 * d + 31) / 32, 256, 0, ctx.stream, a,
+  return cuda_status(launch_pdl(norm_bwd_cols_kernel<L>, (2 * d + 31) / 32, kColWarps * 32, 0, ctx.stream, a,
                                 part, grid));
 }
 
