@@ -7,6 +7,14 @@
 // the block's largest (rounded up) value, are the code, 0 .. 16 * 2^MANT - 1.
 // All of it is integer arithmetic on the fp32 words, and every code stands for a
 // value that bf16 holds exactly.
+//
+// Bound by the bytes: an element moves 30 with fp32 states, a bf16 parameter and its
+// master (28 for an fp32 parameter), 18 with 8-bit states and a master, 16 for an fp32
+// and 12 for a bf16 parameter alone.  Measured on one GB300, 402.8 M weights: 1733 us =
+// 7.0 TB/s, 1040 us = 7.0 TB/s, 945 us = 6.8 TB/s, and 907 us = 5.3 TB/s for the last,
+// which takes 67 instructions an element, a dozen of them the correctly rounded root,
+// and 75 % of the issue slots.  Moments, roots and parameters are fp32 until they are
+// stored.
 #include <math.h>
 
 #include "common.cuh"
@@ -19,7 +27,7 @@ namespace {
 constexpr int kAdamThreads = 128;
 constexpr int kAdamWarps = kAdamThreads / 32;
 constexpr int kBlock = OCCULT_STATE_BLOCK;       // elements of a warp's step
-constexpr int kMaxSteps = 2;                     // blocks of a warp
+constexpr int kMaxSteps = 2;                     // blocks of a warp at most
 constexpr int kMaxTensors = 256;                 // of one launch
 
 enum : int { KIND_F32 = 0, KIND_MASTER = 1, KIND_BF16 = 2 };
@@ -345,8 +353,10 @@ __device__ __forceinline__ void step_block(const AdamTable& a, const Tensor& T, 
   }
 }
 
-// The blocks first, first + stride, ... below end of a tensor by one warp; with 8-bit
-// states the next block's words are on their way while this one's are worked on.
+// The blocks blk, blk + kAdamWarps, ... below end of a tensor by one warp; with 8-bit
+// states the next block's words are on their way while this one's are worked on (without
+// that 1139 us where it takes 940), for a bf16 parameter without a master, whose words are
+// few, both blocks' from the start (907 us; with a master 1273 against 1040 us).
 template <int BITS, int KIND>
 __device__ __forceinline__ void step_blocks(const AdamTable& a, const Tensor& T, int64_t blk,
                                             int64_t end, float gs) {
@@ -402,6 +412,7 @@ __global__ void __launch_bounds__(kAdamThreads, 8) adamw_kernel(const __grid_con
 }
 
 // The values of 8-bit states: kReadSteps times a thread turns 8 codes into 16 bytes.
+// 402.8 M values in 171 us = 7.1 TB/s (205 us with one step a thread).
 constexpr int kReadSteps = 2;
 constexpr int kReadChunk = 256 * 8 * kReadSteps;
 template <int MANT>
@@ -453,8 +464,10 @@ int launch_adamw(const LaunchCtx& ctx, const occult_adamw_t& o, const occult_par
   a.eps = static_cast<float>(o.eps);
   a.key = mix(o.seed + mix(static_cast<uint32_t>(o.step)));
   a.grad_scale = o.grad_scale;
-  // As many blocks a warp as leave four CTAs for each place on the GPU (a CTA spends a
-  // microsecond or two on finding its tensor and on its first loads), one for small sets.
+  // Two blocks a warp, which share a CTA's search for its tensor and its first loads' wait,
+  // where that leaves four CTAs for each place on the GPU; one for smaller sets.  With four
+  // the CTAs' streams lie too far apart: one, two, four blocks took 1075, 977, 962 us with
+  // 8-bit states alone and 1119, 1046, 1178 us with a master.
   int64_t blocks = 0;
   for (int k = 0; k < n_params; ++k) blocks += (params[k].n + kBlock - 1) / kBlock;
   int64_t steps = blocks / (static_cast<int64_t>(kAdamWarps) * 4 * 8 * ctx.num_sms);
