@@ -612,8 +612,8 @@ def occult_profile_coact(desc, ids, n_tok, C, ws, P=None, vmask=None, ct_hist=No
           _stream(stream))
 
 
-# The calls below are short next to their marshalling (a decoded token's norm is 2.5 us
-# on the GPU), so they check and pass plain addresses: 13 us a call before, 8 us so.
+# The calls below are short next to their marshalling (a decoded token's norm is 2.4 us
+# on the GPU), so they check and pass plain addresses: 13 us a call before, 7 us so.
 def _at(t, dtype, numel, name):
     """Address of an optional contiguous CUDA tensor (checked), or None."""
     if t is None:
@@ -653,10 +653,13 @@ def occult_block_norm(desc, opt, r, y=None, w_post=None, gate=None, w_pre=None, 
     rt = _BF if opt.res_dtype == OCCULT_BF16 else _F32
     if r is None:
         _need(r=r)
-    _call("occult_block_norm", desc, ctypes.byref(opt), _at(r, rt, n, "r"), _at(y, _F32, n, "y"),
-          _at(w_post, dt, d, "w_post"), _at(gate, _F32, _gate_len(desc, opt), "gate"),
-          _at(w_pre, dt, d, "w_pre"), _at(r_out, rt, n, "r_out"), _at(x, dt, n, "x"),
-          _at(rstd_post, _F32, T, "rstd_post"), _at(rstd_pre, _F32, T, "rstd_pre"), _on(stream))
+    rc = lib().occult_block_norm(
+        desc, ctypes.byref(opt), _at(r, rt, n, "r"), _at(y, _F32, n, "y"),
+        _at(w_post, dt, d, "w_post"), _at(gate, _F32, _gate_len(desc, opt), "gate"),
+        _at(w_pre, dt, d, "w_pre"), _at(r_out, rt, n, "r_out"), _at(x, dt, n, "x"),
+        _at(rstd_post, _F32, T, "rstd_post"), _at(rstd_pre, _F32, T, "rstd_pre"), _on(stream))
+    if rc:
+        raise OccultError("occult_block_norm", rc)
 
 
 def occult_block_norm_bwd(desc, opt, dr_out, r_out, dr, ws, dx=None, y=None, w_post=None,
@@ -669,13 +672,16 @@ def occult_block_norm_bwd(desc, opt, dr_out, r_out, dr, ws, dx=None, y=None, w_p
     rt = _BF if opt.res_dtype == OCCULT_BF16 else _F32
     if dr is None or ws is None:
         _need(dr=dr, ws=ws)
-    _call("occult_block_norm_bwd", desc, ctypes.byref(opt), _at(dr_out, rt, n, "dr_out"),
-          _at(dx, _F32, n, "dx"), _at(r_out, rt, n, "r_out"), _at(y, _F32, n, "y"),
-          _at(w_post, dt, d, "w_post"), _at(gate, _F32, n_gate, "gate"),
-          _at(w_pre, dt, d, "w_pre"), _at(rstd_post, _F32, T, "rstd_post"),
-          _at(rstd_pre, _F32, T, "rstd_pre"), _at(dr, rt, n, "dr"), _at(dy, dt, n, "dy"),
-          _at(dw_post, _F32, d, "dw_post"), _at(dgate, _F32, n_gate, "dgate"),
-          _at(dw_pre, _F32, d, "dw_pre"), _at(ws, _U8, 0, "ws"), ws.numel(), _on(stream))
+    rc = lib().occult_block_norm_bwd(
+        desc, ctypes.byref(opt), _at(dr_out, rt, n, "dr_out"),
+        _at(dx, _F32, n, "dx"), _at(r_out, rt, n, "r_out"), _at(y, _F32, n, "y"),
+        _at(w_post, dt, d, "w_post"), _at(gate, _F32, n_gate, "gate"),
+        _at(w_pre, dt, d, "w_pre"), _at(rstd_post, _F32, T, "rstd_post"),
+        _at(rstd_pre, _F32, T, "rstd_pre"), _at(dr, rt, n, "dr"), _at(dy, dt, n, "dy"),
+        _at(dw_post, _F32, d, "dw_post"), _at(dgate, _F32, n_gate, "dgate"),
+        _at(dw_pre, _F32, d, "dw_pre"), _at(ws, _U8, 0, "ws"), ws.numel(), _on(stream))
+    if rc:
+        raise OccultError("occult_block_norm_bwd", rc)
 
 
 def balance_groups(desc, opt) -> int:
@@ -699,11 +705,14 @@ def occult_balance_loss(desc, opt, logits, ids, expert_to_vdev, counts, grad_w, 
             or grad_w is None or loss is None or ws is None):
         _need(logits=logits, ids=ids, expert_to_vdev=expert_to_vdev, counts=counts,
               grad_w=grad_w, loss=loss, ws=ws)
-    _call("occult_balance_loss", desc, ctypes.byref(opt), _at(logits, _F32, T * Ne, "logits"),
-          _at(ids, _I32T, T * desc.top_k, "ids"), _at(expert_to_vdev, _I32T, Ne, "expert_to_vdev"),
-          _at(mask, _U8, T, "mask"), _at(counts, _I32T, n, "counts"),
-          _at(grad_w, _F32, n + 1, "grad_w"), _at(loss, _F32, 4, "loss"), _at(ws, _U8, 0, "ws"),
-          ws.numel(), _on(stream))
+    rc = lib().occult_balance_loss(
+        desc, ctypes.byref(opt), _at(logits, _F32, T * Ne, "logits"),
+        _at(ids, _I32T, T * desc.top_k, "ids"), _at(expert_to_vdev, _I32T, Ne, "expert_to_vdev"),
+        _at(mask, _U8, T, "mask"), _at(counts, _I32T, n, "counts"),
+        _at(grad_w, _F32, n + 1, "grad_w"), _at(loss, _F32, 4, "loss"), _at(ws, _U8, 0, "ws"),
+        ws.numel(), _on(stream))
+    if rc:
+        raise OccultError("occult_balance_loss", rc)
 
 
 def occult_balance_grad(desc, opt, logits, grad_w, dlogits, mask=None, dloss=None,
@@ -712,10 +721,13 @@ def occult_balance_grad(desc, opt, logits, grad_w, dlogits, mask=None, dloss=Non
     T, Ne = desc.T, desc.n_experts
     if logits is None or grad_w is None or dlogits is None:
         _need(logits=logits, grad_w=grad_w, dlogits=dlogits)
-    _call("occult_balance_grad", desc, ctypes.byref(opt), _at(logits, _F32, T * Ne, "logits"),
-          _at(grad_w, _F32, balance_groups(desc, opt) * Ne + 1, "grad_w"),
-          _at(mask, _U8, T, "mask"), _at(dloss, _F32, 1, "dloss"),
-          _at(dlogits, _F32, T * Ne, "dlogits"), 1 if accumulate else 0, _on(stream))
+    rc = lib().occult_balance_grad(
+        desc, ctypes.byref(opt), _at(logits, _F32, T * Ne, "logits"),
+        _at(grad_w, _F32, balance_groups(desc, opt) * Ne + 1, "grad_w"),
+        _at(mask, _U8, T, "mask"), _at(dloss, _F32, 1, "dloss"),
+        _at(dlogits, _F32, T * Ne, "dlogits"), 1 if accumulate else 0, _on(stream))
+    if rc:
+        raise OccultError("occult_balance_grad", rc)
 
 
 class AdamTable:

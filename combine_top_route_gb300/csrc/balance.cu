@@ -3,7 +3,8 @@
 //
 // Everything is a softmax of each token's row, so both directions are bound by the
 // logits they read (and the gradients they write); at the sizes of a router both
-// often sit in L2 and what counts is latency.  The loss is two launches: tiles of
+// often sit in L2 and what counts is latency.  The loss of a small batch is one launch
+// of a cluster that adds its CTAs' sums up over shared memory, else it is two: tiles of
 // tokens leave partial sums and counts, then one CTA a group adds them up.  Logits,
 // sums and gradients are fp32 throughout, counts are integers.
 //
@@ -21,6 +22,8 @@ namespace {
 
 constexpr int kTileThreads = 512;
 constexpr int kOneThreads = 1024;
+constexpr int kCluster = 16;                       // CTAs of the one-launch kernel
+constexpr int kOneSteps = 2, kClusterSteps = 4;    // steps of a CTA
 constexpr int kSumThreads = 1024;
 constexpr int kMaxWarps = 32;
 static_assert(kSumThreads == 32 * kMaxWarps, "a warp reads one word of every warp");
@@ -283,20 +286,80 @@ __device__ __forceinline__ void write_loss(const BalanceArgs& a, const float (&t
   a.grad_w[static_cast<size_t>(a.G) * a.Ne] = 2.f * a.coef_z * inv_n;
 }
 
-// A batch of one group and few tokens: everything by one CTA.
+// A word of another CTA's shared memory, at the offset of `p` in this CTA's.
+__device__ __forceinline__ uint32_t ld_cluster(const void* p, uint32_t rank) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(smem_addr_in_rank(p, rank)));
+  return v;
+}
+
+// A batch of one group and not too many tokens in one launch: the grid is one cluster
+// (or one CTA), whose CTAs each sum a tile and whose first then reads the others' sums.
 template <int LP>
-__global__ void __launch_bounds__(kOneThreads, 1) balance_one_kernel(BalanceArgs a) {
+__global__ void __launch_bounds__(kOneThreads, 1) balance_cluster_kernel(BalanceArgs a) {
   __shared__ TileScratch<LP, kOneThreads> s_tile;
   __shared__ Sums s_sums;
   __shared__ GroupScratch s_group;
   pdl_wait();
   pdl_trigger();
+  const int lane = threadIdx.x & 31, rank = blockIdx.x, ctas = gridDim.x;
   for (int e = threadIdx.x; e < a.Ne; e += kOneThreads) s_group.dev[e] = a.e2v[e];
-  sum_tile<LP, kOneThreads>(a, 0, a.T, s_tile, s_sums);
+  const int64_t len = (static_cast<int64_t>(a.T) + ctas - 1) / ctas, t0 = rank * len;
+  sum_tile<LP, kOneThreads>(a, t0, min(static_cast<int64_t>(a.T), t0 + len), s_tile, s_sums);
+  if (ctas > 1) {
+    cluster_sync();
+    float p = 0.f, sq = 0.f;
+    int c = 0, n = 0;
+    if (rank == 0) {
+      if (static_cast<int>(threadIdx.x) < a.Ne) {
+#pragma unroll 16
+        for (int r = 0; r < ctas; ++r) {
+          p += __uint_as_float(ld_cluster(&s_sums.p[threadIdx.x], r));
+          c += static_cast<int>(ld_cluster(&s_sums.c[threadIdx.x], r));
+        }
+      }
+      if (lane < ctas) {
+        sq = __uint_as_float(ld_cluster(&s_sums.sq, lane));
+        n = static_cast<int>(ld_cluster(&s_sums.n, lane));
+      }
+    }
+    cluster_sync();  // all of it is read: the CTAs may end, the first may overwrite
+    if (rank != 0) return;
+    n = __reduce_add_sync(0xffffffffu, n);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
+    if (static_cast<int>(threadIdx.x) < a.Ne) {
+      s_sums.p[threadIdx.x] = p;
+      s_sums.c[threadIdx.x] = c;
+    }
+    if (threadIdx.x == 0) { s_sums.sq = sq; s_sums.n = n; }
+    __syncthreads();
+  }
   float terms[3];
   finish_group(a, 0, s_sums, s_group, 1.f, terms);
   if (threadIdx.x == 0)
     write_loss(a, terms, 1.f, 1.f / static_cast<float>(s_sums.n > 0 ? s_sums.n : 1));
+}
+
+template <int LP>
+int launch_cluster(const LaunchCtx& ctx, const BalanceArgs& a, int ctas) {
+  void (*kernel)(BalanceArgs) = balance_cluster_kernel<LP>;
+  if (ctas == 1) return cuda_status(launch_pdl(kernel, 1, kOneThreads, 0, ctx.stream, a));
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+    return OCCULT_ERR_CUDA;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = ctas;
+  cfg.blockDim = kOneThreads;
+  cfg.stream = ctx.stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = ctas;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cuda_status(cudaLaunchKernelEx(&cfg, kernel, a));
 }
 
 // Pass 1: CTA x of group y takes one tile of the group's tokens.  131072 x 256: 28 us,
@@ -538,14 +601,17 @@ size_t balance_ws_bytes(const occult_desc_t& ds, int group_len) {
 }
 
 int launch_balance_loss(const LaunchCtx& ctx, const BalanceArgs& a) {
-  // few tokens: one CTA does both passes (a step of all its warps is 256, 128 or 64
-  // tokens; beyond two steps the second launch costs less)
   const int lp = a.Ne <= 64 ? 8 : a.Ne <= 128 ? 16 : 32;
-  if (a.G == 1 && a.T <= 4 * kOneThreads / lp) {
-    return cuda_status(
-        lp == 8    ? launch_pdl(balance_one_kernel<8>, 1, kOneThreads, 0, ctx.stream, a)
-        : lp == 16 ? launch_pdl(balance_one_kernel<16>, 1, kOneThreads, 0, ctx.stream, a)
-                   : launch_pdl(balance_one_kernel<32>, 1, kOneThreads, 0, ctx.stream, a));
+  // One launch for a batch of one group: by one CTA for two steps of all its warps (128,
+  // 64 or 32 tokens each), by a cluster of 16 for four of each, two launches beyond that.
+  // 64 experts, us by one CTA, the cluster, two launches: 4.8, 5.4, 6.1 for 256 tokens,
+  // -, 6.7, 7.1 for 4096, -, 8.4, 8.4 for 8192, -, 11.3, 9.1 for 16384.
+  const int64_t steps = (static_cast<int64_t>(a.T) * lp + kOneThreads - 1) / kOneThreads;
+  if (a.G == 1 && steps <= kClusterSteps * kCluster) {
+    const int ctas = steps <= kOneSteps ? 1 : kCluster;
+    return lp == 8    ? launch_cluster<8>(ctx, a, ctas)
+           : lp == 16 ? launch_cluster<16>(ctx, a, ctas)
+                      : launch_cluster<32>(ctx, a, ctas);
   }
   const Tiles tiles = tiles_of(a.T, a.L, a.G);
   const dim3 grid(tiles.per_group, a.G < 65535 ? a.G : 65535);

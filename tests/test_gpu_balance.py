@@ -112,7 +112,9 @@ def check(occ, z, ids, Nd, group_len=0, mask=None, base=None, dloss=None, seed=1
 @pytest.mark.parametrize("T,Ne,k,Nd", [(1, 8, 2, 4), (7, 8, 2, 4), (256, 8, 2, 4), (300, 60, 4, 4),
                                        (1000, 64, 8, 8), (513, 33, 3, 1), (129, 96, 12, 32),
                                        (700, 128, 16, 16), (333, 256, 8, 32), (64, 1, 1, 1),
-                                       (50, 2, 2, 2), (4100, 64, 6, 8), (90, 255, 5, 5)])
+                                       (50, 2, 2, 2), (4100, 64, 6, 8), (90, 255, 5, 5),
+                                       (257, 64, 4, 8), (8192, 64, 2, 8), (8193, 64, 2, 8),
+                                       (65, 256, 8, 8), (2048, 256, 2, 8), (2049, 256, 2, 8)])
 def test_sizes(occ, T, Ne, k, Nd):
     z, ids = case(T, Ne, k, seed=T)
     check(occ, z, ids, Nd)
@@ -215,3 +217,27 @@ def test_large_batch_against_doubles(occ):
     dz = p * (w - (p * w).sum(1, keepdim=True))
     err = (p * w.amax(1, keepdim=True)) * (2 * (2 * P + 32 * U)) + 3 * U * dz.abs() + 1e-37
     assert ((dl.double() - dz).abs() <= err).all()
+
+
+def test_more_groups_than_a_grid_has_rows(occ):
+    """70000 sequences of one token, every third masked, against fp64 on the GPU."""
+    T, Ne, k = 70000, 8, 2
+    g = torch.Generator(device="cuda").manual_seed(4)
+    z = torch.randn(T, Ne, generator=g, device="cuda")
+    ids = z.topk(k, dim=1).indices.to(torch.int32).contiguous()
+    mask = (torch.arange(T, device="cuda") % 3 != 0).to(torch.uint8)
+    ds = occ.desc_for(synth.CONFIGS["olmoe_fwd"].with_(T=T, n_experts=Ne, top_k=k, n_vdev=4))
+    opt = occ.occult_balance_t(1.0, 0.0, 0.5, 1)
+    assert occ.balance_groups(ds, opt) == T
+    counts = torch.empty(T, Ne, dtype=torch.int32, device="cuda")
+    grad_w, loss = torch.empty(T * Ne + 1, device="cuda"), torch.empty(4, device="cuda")
+    ws = torch.empty(occ.balance_workspace_size(ds, opt), dtype=torch.uint8, device="cuda")
+    e2v = (torch.arange(Ne, device="cuda") % 4).to(torch.int32)
+    occ.occult_balance_loss(ds, opt, z, ids, e2v, counts, grad_w, loss, ws, mask=mask)
+    on = mask.double()[:, None]
+    one = torch.nn.functional.one_hot(ids.long(), Ne).sum(1) * mask[:, None]
+    assert torch.equal(counts.long(), one)
+    p, lse = z.double().softmax(1), z.double().logsumexp(1)
+    bal = float((one * (Ne / k) * p * on).sum() / on.sum())
+    sq = float((lse.square() * on[:, 0]).sum() / on.sum())
+    assert abs(float(loss[1]) - bal) <= SUM * bal and abs(float(loss[3]) - sq) <= SUM * sq
