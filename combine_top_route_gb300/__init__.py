@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional
 
 import torch
@@ -730,6 +731,9 @@ def occult_balance_grad(desc, opt, logits, grad_w, dlogits, mask=None, dloss=Non
         raise OccultError("occult_balance_grad", rc)
 
 
+_RECORD = struct.Struct("7Q2q2i")   # occult_param_t
+
+
 class AdamTable:
     """The host records of occult_adamw's tensors; keeps the tensors alive."""
 
@@ -742,23 +746,25 @@ class AdamTable:
             raise ValueError("the states of a table are all float32 or all uint8 codes")
         self.state_bits = 8 if bits == {torch.uint8} else 32
         st = torch.uint8 if self.state_bits == 8 else torch.float32
-        for rec, t in zip(self.records, tensors):
-            p = t["param"]
-            n = p.numel()
-            if p.dtype not in (torch.float32, torch.bfloat16):
+        # (packed as bytes: hundreds of small tensors are what a table is for)
+        for i, t in enumerate(tensors):
+            p, get = t["param"], t.get
+            n, bf, master = p.numel(), p.dtype is _BF, get("master")
+            if not bf and p.dtype is not _F32:
                 raise ValueError(f"param must be float32 or bfloat16, got {p.dtype}")
-            if t.get("master") is not None and p.dtype != torch.bfloat16:
+            if master is not None and not bf:
                 raise ValueError("only a bfloat16 parameter takes a master copy")
-            blocks = -(-n // STATE_BLOCK)
-            rec.param = _dev(p, None, n, "param")
-            rec.master = _dev(t.get("master"), torch.float32, n, "master", nullable=True)
-            rec.grad = _dev(t["grad"], torch.float32, n, "grad")
-            rec.m, rec.v = _dev(t["m"], st, n, "m"), _dev(t["v"], st, n, "v")
-            if st == torch.uint8:
-                rec.m_exp = _dev(t.get("m_exp"), torch.uint8, blocks, "m_exp")
-                rec.v_exp = _dev(t.get("v_exp"), torch.uint8, blocks, "v_exp")
-            rec.n, rec.first = n, int(t.get("first", 0))
-            rec.dtype = OCCULT_BF16 if p.dtype == torch.bfloat16 else OCCULT_F32
+            if t["grad"] is None or t["m"] is None or t["v"] is None:
+                _need(grad=t["grad"], m=t["m"], v=t["v"])
+            em = ev = 0
+            if self.state_bits == 8:
+                blocks = -(-n // STATE_BLOCK)
+                _need(m_exp=get("m_exp"), v_exp=get("v_exp"))
+                em, ev = _at(t["m_exp"], _U8, blocks, "m_exp"), _at(t["v_exp"], _U8, blocks, "v_exp")
+            _RECORD.pack_into(self.records, i * _RECORD.size, _at(p, p.dtype, n, "param"),
+                              _at(master, _F32, n, "master") or 0, _at(t["grad"], _F32, n, "grad"),
+                              _at(t["m"], st, n, "m"), _at(t["v"], st, n, "v"), em, ev, n,
+                              int(get("first", 0)), OCCULT_BF16 if bf else OCCULT_F32, 0)
 
 
 def adamw_table(tensors) -> AdamTable:

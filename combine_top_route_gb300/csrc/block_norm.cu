@@ -447,6 +447,26 @@ norm_fwd_ring_kernel(NormArgs a, int stages, int* dev_err) {
   }
 }
 
+// Column `col` of the two sums over all tokens, [dx n | D m], to what they are: dw_pre,
+// dw_post and a channel gate's gradient.
+template <typename L>
+__device__ __forceinline__ void write_column(const NormArgs& a, int col, float s) {
+  if (col < a.d) {
+    if (a.dw_pre) a.dw_pre[col] = s;
+    return;
+  }
+  const int j = col - a.d;
+  const bool chan = a.gate_kind == OCCULT_GATE_CHANNEL;
+  if (a.dw_post) a.dw_post[j] = chan ? s * a.gate[j] : s;
+  if (chan) a.dgate[j] = a.w_post ? s * to_f32(static_cast<const L*>(a.w_post)[j]) : s;
+}
+// A float of another CTA's shared memory, at the offset of `p` in this CTA's.
+__device__ __forceinline__ float ld_cluster(const float* p, uint32_t rank) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(smem_addr_in_rank(p, rank)));
+  return v;
+}
+
 // Bytes of one row in the backward's ring: dx, y, then dr_out and r'.
 template <typename R>
 __host__ __device__ __forceinline__ int bwd_row_bytes(int d) {
@@ -466,7 +486,7 @@ __host__ __device__ __forceinline__ int bwd_row_bytes(int d) {
 // 267 against 171 us at d=5632.
 template <typename R, typename L, int G, int U, int CTAS>
 __global__ void __launch_bounds__(Group<G>::kThreads, CTAS)
-norm_bwd_rows_kernel(NormArgs a, float* part, int stages, int* dev_err) {
+norm_bwd_rows_kernel(NormArgs a, bool sums, float* part, int stages, int* dev_err) {
   extern __shared__ __align__(128) unsigned char s_ring[];
   __shared__ uint64_t s_full[Group<G>::kGroups][kMaxStages];
   __shared__ float4 s_red[2][Group<G>::kThreads / 32];
@@ -621,11 +641,12 @@ norm_bwd_rows_kernel(NormArgs a, float* part, int stages, int* dev_err) {
     for (int i = 0; i < stages; ++i)
       mbar_wait(&s_full[group][i], i < stage ? parity ^ 1 : parity, &none);
   }
-  if (!part) return;
-  // the groups' sums, then one row of partial sums a CTA
-  float* row = part + static_cast<size_t>(blockIdx.x) * 2 * d;
+  if (!sums) return;
+  // the groups' sums, then this CTA's: a row of partial sums, or, where the grid is one
+  // cluster (part NULL), shared memory that every CTA reads its share of the columns from
   float* s_sum = reinterpret_cast<float*>(s_ring);
-  if (Group<G>::kGroups > 1) {
+  float* row = part ? part + static_cast<size_t>(blockIdx.x) * 2 * d : s_sum;
+  if (Group<G>::kGroups > 1 || !part) {
     __syncthreads();  // every group is done with the ring
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -635,10 +656,12 @@ norm_bwd_rows_kernel(NormArgs a, float* part, int stages, int* dev_err) {
       st4(s_sum + (2 * group + 1) * d + c, sum_post[u]);
     }
     __syncthreads();
-    for (int c = threadIdx.x * 4; c < 2 * d; c += Group<G>::kThreads * 4) {
-      float4 v = ld4(s_sum + c);
-      for (int g = 1; g < Group<G>::kGroups; ++g) v = add4(v, ld4(s_sum + 2 * g * d + c));
-      st4(row + c, v);
+    if (Group<G>::kGroups > 1) {
+      for (int c = threadIdx.x * 4; c < 2 * d; c += Group<G>::kThreads * 4) {
+        float4 v = ld4(s_sum + c);
+        for (int g = 1; g < Group<G>::kGroups; ++g) v = add4(v, ld4(s_sum + 2 * g * d + c));
+        st4(row + c, v);
+      }
     }
   } else {
 #pragma unroll
@@ -649,6 +672,16 @@ norm_bwd_rows_kernel(NormArgs a, float* part, int stages, int* dev_err) {
       st4(row + d + c, sum_post[u]);
     }
   }
+  if (part) return;
+  cluster_sync();
+  for (int c = blockIdx.x * Group<G>::kThreads + threadIdx.x; c < 2 * d;
+       c += gridDim.x * Group<G>::kThreads) {
+    float v = 0.f;
+#pragma unroll 8
+    for (int r = 0; r < static_cast<int>(gridDim.x); ++r) v += ld_cluster(s_sum + c, r);
+    write_column<L>(a, c, v);
+  }
+  cluster_sync();  // no CTA ends while its sums are read
 }
 
 // Adds the CTAs' partial rows and turns the second sum into dw_post and a channel
@@ -676,14 +709,7 @@ norm_bwd_cols_kernel(NormArgs a, const float* __restrict__ part, int n_part) {
   for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
   const int col = blockIdx.x * 32 + warp;
   if (lane != 0 || col >= 2 * a.d) return;
-  if (col < a.d) {
-    if (a.dw_pre) a.dw_pre[col] = s;
-    return;
-  }
-  const int j = col - a.d;
-  const bool chan = a.gate_kind == OCCULT_GATE_CHANNEL;
-  if (a.dw_post) a.dw_post[j] = chan ? s * a.gate[j] : s;
-  if (chan) a.dgate[j] = a.w_post ? s * to_f32(static_cast<const L*>(a.w_post)[j]) : s;
+  write_column<L>(a, col, s);
 }
 
 template <typename K>
@@ -751,20 +777,49 @@ int fwd(const LaunchCtx& ctx, const NormArgs& a) {
   return fwd_rows<R, L, 16, 8>(ctx, a);
 }
 
+// Few rows in one launch: a cluster whose CTAs add their column sums up over shared
+// memory, for one row a group, three of narrow ones.  On the GPU that is no faster than
+// two launches (us: 128 x 64 4.0 and 4.5, 257 x 64 5.4 and 4.7, 16 x 2048 5.1 and 4.9; two
+// rows a group of 2048 6.1 and 5.0), but the host has one launch (2 us) less, which is
+// what bounds calls of this size.
+constexpr int kCluster = 16;
+constexpr int cluster_rows(int G) { return G == 1 ? 3 : 1; }
+
 template <typename R, typename L, int G, int U, int CTAS>
-int bwd_rows(const LaunchCtx& ctx, const NormArgs& a, float* part, int* grid) {
+int bwd_rows(const LaunchCtx& ctx, const NormArgs& a, bool sums, float* part, int* n_part) {
+  void (*kernel)(NormArgs, bool, float*, int, int*) = norm_bwd_rows_kernel<R, L, G, U, CTAS>;
   const int row = bwd_row_bytes<R>(a.d) * Group<G>::kGroups;
   const int stages = ring_stages<R>(row, CTAS);
   size_t smem = static_cast<size_t>(stages) * row;
-  const size_t sums = 2 * static_cast<size_t>(a.d) * Group<G>::kGroups * sizeof(float);
-  smem = smem > sums ? smem : sums;
-  int rc = allow_smem(norm_bwd_rows_kernel<R, L, G, U, CTAS>, smem);
+  const size_t all = 2 * static_cast<size_t>(a.d) * Group<G>::kGroups * sizeof(float);
+  smem = smem > all ? smem : all;
+  int rc = allow_smem(kernel, smem);
   if (rc) return rc;
   const int need = (a.T + Group<G>::kGroups - 1) / Group<G>::kGroups;
+  *n_part = 0;
+  if (sums && need <= kCluster * cluster_rows(G)) {
+    rc = cuda_status(cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1));
+    if (rc) return rc;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = kCluster;
+    cfg.blockDim = Group<G>::kThreads;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = ctx.stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cfg.gridDim.x;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cuda_status(cudaLaunchKernelEx(&cfg, kernel, a, sums, static_cast<float*>(nullptr),
+                                          stages, ctx.dev_err));
+  }
   const int cap = ctx.num_sms * CTAS < kNormMaxParts ? ctx.num_sms * CTAS : kNormMaxParts;
-  *grid = need < cap ? need : cap;
-  return cuda_status(launch_pdl(norm_bwd_rows_kernel<R, L, G, U, CTAS>, *grid, Group<G>::kThreads,
-                                smem, ctx.stream, a, part, stages, ctx.dev_err));
+  *n_part = need < cap ? need : cap;
+  return cuda_status(launch_pdl(kernel, *n_part, Group<G>::kThreads, smem, ctx.stream, a, sums, part,
+                                stages, ctx.dev_err));
 }
 
 template <typename R, typename L>
@@ -781,24 +836,22 @@ template <typename R, typename L>
 int bwd(const LaunchCtx& ctx, const NormArgs& a, float* part) {
   const int d = a.d;
   const bool sums = a.dw_pre || a.dw_post || a.gate_kind == OCCULT_GATE_CHANNEL;
-  int grid = 0, rc;
-  float* ws = part;
-  if (!sums) part = nullptr;
+  int n_part = 0, rc;  // rows of partial sums that are left to add up
   // bulk copies move whole 16 bytes; the ring holds a row of up to 8192 columns.  Above
   // 2048 columns three or four units a thread (16 warps of two units, one CTA an SM: 210
   // against 175 us at 16384 x 4096).
-  if (d * sizeof(R) % 16 != 0 || d > 8192) rc = bwd_any<R, L>(ctx, a, ws, &grid);
-  else if (d <= 128) rc = bwd_rows<R, L, 1, 1, 3>(ctx, a, part, &grid);
-  else if (d <= 256) rc = bwd_rows<R, L, 1, 2, 2>(ctx, a, part, &grid);
-  else if (d <= 512) rc = bwd_rows<R, L, 2, 2, 2>(ctx, a, part, &grid);
-  else if (d <= 1024) rc = bwd_rows<R, L, 4, 2, 2>(ctx, a, part, &grid);
-  else if (d <= 2048) rc = bwd_rows<R, L, 8, 2, 2>(ctx, a, part, &grid);
-  else if (d <= 4096) rc = bwd_rows<R, L, 8, 4, 2>(ctx, a, part, &grid);
-  else if (d <= 6144) rc = bwd_rows<R, L, 16, 3, 1>(ctx, a, part, &grid);
-  else rc = bwd_rows<R, L, 16, 4, 1>(ctx, a, part, &grid);
-  if (rc || !sums) return rc;
-  return cuda_status(launch_pdl(norm_bwd_cols_kernel<L>, (2 * d + 31) / 32, kColWarps * 32, 0, ctx.stream, a,
-                                part, grid));
+  if (d * sizeof(R) % 16 != 0 || d > 8192) rc = bwd_any<R, L>(ctx, a, part, &n_part);
+  else if (d <= 128) rc = bwd_rows<R, L, 1, 1, 3>(ctx, a, sums, part, &n_part);
+  else if (d <= 256) rc = bwd_rows<R, L, 1, 2, 2>(ctx, a, sums, part, &n_part);
+  else if (d <= 512) rc = bwd_rows<R, L, 2, 2, 2>(ctx, a, sums, part, &n_part);
+  else if (d <= 1024) rc = bwd_rows<R, L, 4, 2, 2>(ctx, a, sums, part, &n_part);
+  else if (d <= 2048) rc = bwd_rows<R, L, 8, 2, 2>(ctx, a, sums, part, &n_part);
+  else if (d <= 4096) rc = bwd_rows<R, L, 8, 4, 2>(ctx, a, sums, part, &n_part);
+  else if (d <= 6144) rc = bwd_rows<R, L, 16, 3, 1>(ctx, a, sums, part, &n_part);
+  else rc = bwd_rows<R, L, 16, 4, 1>(ctx, a, sums, part, &n_part);
+  if (rc || !sums || n_part == 0) return rc;
+  return cuda_status(launch_pdl(norm_bwd_cols_kernel<L>, (2 * d + 31) / 32, kColWarps * 32, 0,
+                                ctx.stream, a, part, n_part));
 }
 
 }  // namespace

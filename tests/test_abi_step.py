@@ -170,3 +170,13 @@ def test_binding_refuses_what_the_records_cannot_say(occ):
     table = occ.adamw_table([])
     with pytest.raises(ValueError):
         occ.occult_adamw(occ.occult_adamw_t(state_bits=8, step=1), table)
+
+
+def test_packed_record_is_the_struct(occ):
+    """The binding packs occult_param_t as bytes: the same size and field offsets."""
+    rec = occ.occult_param_t()
+    vals = [0x1000 * (i + 1) for i in range(7)] + [12345678901, 98765432109, 1, 0]
+    assert occ._RECORD.size == ctypes.sizeof(rec)
+    occ._RECORD.pack_into(rec, 0, *vals)
+    got = [getattr(rec, n) for n, _ in rec._fields_]
+    assert got == vals
