@@ -25,8 +25,9 @@ constexpr int kOneThreads = 1024;
 constexpr int kCluster = 16;                       // CTAs of the one-launch kernel
 constexpr int kOneSteps = 2, kClusterSteps = 4;    // steps of a CTA
 constexpr int kSumThreads = 1024;
-constexpr int kMaxWarps = 32;
-static_assert(kSumThreads == 32 * kMaxWarps, "a warp reads one word of every warp");
+constexpr int kSumWarps = kSumThreads / 32;
+static_assert(kSumWarps <= 32 && kSumThreads >= OCCULT_MAX_EXPERTS,
+              "a lane a warp's word, a thread an expert");
 constexpr int kGradThreads = 256;
 // Tiles of a batch: two CTAs an SM where the groups have their own second passes, one
 // where a single CTA adds all of them up (11.2 us at 304 tiles, 10.3 at 152 for the loss
@@ -396,10 +397,10 @@ __global__ void __launch_bounds__(kSumThreads) balance_groups_kernel(BalanceArgs
   __shared__ int s_cpart[kSumThreads];
   __shared__ Sums s_sums;
   __shared__ GroupScratch s_group;
-  __shared__ long long s_tok[kSumThreads / 32];
-  __shared__ float s_sq[kSumThreads / 32];
-  __shared__ float s_terms[kSumThreads / 32][3];
-  __shared__ int s_n[kSumThreads / 32];
+  __shared__ long long s_tok[kSumWarps];
+  __shared__ float s_sq[kSumWarps];
+  __shared__ float s_terms[kSumWarps][3];
+  __shared__ int s_n[kSumWarps];
   __shared__ bool s_last;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   pdl_wait();
@@ -461,18 +462,19 @@ __global__ void __launch_bounds__(kSumThreads) balance_groups_kernel(BalanceArgs
       s_sums.p[tid] = s;
       s_sums.c[tid] = c;
     }
-    // the last warp, which holds no expert, adds up the scalars
-    if (warp == kSumThreads / 32 - 1) {
-      sq = s_sq[lane];
-      n = __reduce_add_sync(0xffffffffu, s_n[lane]);
-      tok = s_tok[lane];
+    // the last warp adds up the scalars
+    if (warp == kSumWarps - 1) {
+      const bool have = lane < kSumWarps;
+      sq = have ? s_sq[lane] : 0.f;
+      n = __reduce_add_sync(0xffffffffu, have ? s_n[lane] : 0);
+      tok = have ? s_tok[lane] : 0;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) {
         sq += __shfl_xor_sync(0xffffffffu, sq, o);
         tok += __shfl_xor_sync(0xffffffffu, tok, o);
       }
-      if (lane == 0) { s_sums.sq = sq; s_sums.n = n; s_tok[0] = tok; s_tok[1] = 0; }
-      if (lane > 0) s_tok[lane] = 0;
+      if (lane == 0) { s_sums.sq = sq; s_sums.n = n; }
+      if (have) s_tok[lane] = lane == 0 ? tok : 0;  // (added up again for the next group)
     }
     __syncthreads();
     tok = s_tok[0];
@@ -511,7 +513,7 @@ __global__ void __launch_bounds__(kSumThreads) balance_groups_kernel(BalanceArgs
   if (tid == 0) {
     for (int i = 0; i < 3; ++i) {
       v[i] = 0.f;
-      for (int k = 0; k < kSumThreads / 32; ++k) v[i] += s_terms[k][i];
+      for (int k = 0; k < kSumWarps; ++k) v[i] += s_terms[k][i];
     }
     write_loss(a, v, inv_a, inv_n);
   }
