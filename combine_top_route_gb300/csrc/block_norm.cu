@@ -46,7 +46,7 @@ __device__ __forceinline__ float4 fma4(const float4& a, float b, const float4& c
 }
 
 // The same as packed operations of two columns, which take half the issue slots (the
-// backward 165 -> 161 us at T=32768, d=2048, 178 -> 171 us at 11000 x 5632; the forward,
+// backward 165 -> 161 us at T=32768, d=2048, 178 -> 160 us at 11000 x 5632; the forward,
 // which waits for memory alone, gained nothing and keeps the plain ones).
 __device__ __forceinline__ float2 lo2(const float4& a) { return make_float2(a.x, a.y); }
 __device__ __forceinline__ float2 hi2(const float4& a) { return make_float2(a.z, a.w); }
@@ -90,9 +90,10 @@ __device__ __forceinline__ void block_sum(float (&v)[N], float (*s_red)[N]) {
   }
 }
 
-// Backward of rows too wide for a ring (or not whole 16 bytes), one CTA a row, read
-// twice (the second time from L2): 4096 x 16384 in 398 us = 2.7 TB/s, bound by the
-// latency of its two passes with one CTA an SM.  D is linear in mean(w_pre dx n), so
+// Backward of rows too wide for a ring (fp32 streams above 12800 columns) or not whole
+// 16 bytes, one CTA a row, read twice (the second time from L2): 4096 x 16384 with a bf16
+// stream took 398 us = 2.7 TB/s this way (321 us through the ring), bound by the latency
+// of its two passes with one CTA an SM.  D is linear in mean(w_pre dx n), so
 // one round of sums gives every mean: with g = w_pre dx, D0 = dr_out + rstd_pre g and
 // q = gate w_post m,
 //   s0 = sum g n,  s1 = sum q D0,  s2 = sum q n
@@ -483,7 +484,7 @@ __host__ __device__ __forceinline__ int bwd_row_bytes(int d) {
 // T=32768, d=2048: 161 us = 6.7 TB/s, a row at a time 312 us; 131 us without a norm after
 // the block (12 bytes an element, 90 % of a copy: the sync and the sums of a row).  Two
 // units a thread read twice instead of kept: 192 us; four units kept: registers spill,
-// 267 against 171 us at d=5632.
+// 267 against 160 us at d=5632.
 template <typename R, typename L, int G, int U, int CTAS>
 __global__ void __launch_bounds__(Group<G>::kThreads, CTAS)
 norm_bwd_rows_kernel(NormArgs a, bool sums, float* part, int stages, int* dev_err) {
@@ -530,17 +531,24 @@ norm_bwd_rows_kernel(NormArgs a, bool sums, float* part, int stages, int* dev_er
         fill(i, first + i * step);
 
   const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
-  float4 wp[U], wq[U];                 // w_pre, and w_post times a channel gate
+  // w_pre, and w_post times a channel gate: held, or (32 warps have no registers for
+  // them) read where they are used
+  constexpr bool kHold = G <= 16;
+  auto load_wp = [&](int c) { return w_pre && c < d ? ld4(w_pre + c) : zero; };
+  auto load_wq = [&](int c) {
+    float4 w = make_float4(1.f, 1.f, 1.f, 1.f);
+    if (c < d) {
+      if (w_post) w = ld4(w_post + c);
+      if (chan) w = mul4(w, ld4(a.gate + c));
+    }
+    return w;
+  };
+  float4 held_p[kHold ? U : 1], held_q[kHold ? U : 1];
   float4 sum_pre[U], sum_post[U];      // sum dx n; sum D m (of a token gate: gate D m)
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const int c = 4 * (u * 32 * G + place);
-    wp[u] = w_pre && c < d ? ld4(w_pre + c) : zero;
-    wq[u] = make_float4(1.f, 1.f, 1.f, 1.f);
-    if (c < d) {
-      if (w_post) wq[u] = ld4(w_post + c);
-      if (chan) wq[u] = mul4(wq[u], ld4(a.gate + c));
-    }
+    if (kHold) { held_p[u] = load_wp(c); held_q[u] = load_wq(c); }
     sum_pre[u] = sum_post[u] = zero;
   }
   const float inv_d = 1.f / d;
@@ -574,13 +582,13 @@ norm_bwd_rows_kernel(NormArgs a, bool sums, float* part, int stages, int* dev_er
       if (w_pre) {
         dx = ld4(s_dx + c);
         r = ld4(s_r + c);
-        const float4 g = pmul4(dx, wp[u]);
+        const float4 g = pmul4(dx, kHold ? held_p[kHold ? u : 0] : load_wp(c));
         D = pfma4(g, rq, D);
         sx = pdot(g, r, sx);
       }
       if (use_y) {
         y = ld4(s_y + c);
-        const float4 q = pmul4(y, wq[u]);
+        const float4 q = pmul4(y, kHold ? held_q[kHold ? u : 0] : load_wq(c));
         sy = pdot(q, D, sy);
         sz = pdot(q, r, sz);
       }
@@ -616,13 +624,13 @@ norm_bwd_rows_kernel(NormArgs a, bool sums, float* part, int stages, int* dev_er
       if (w_pre) {
         const float4 dx = kKeep ? k_dx[u % KEEP] : ld4(s_dx + c);
         const float4 r = kKeep ? k_r[u % KEEP] : ld4(s_r + c);
-        if (!kKeep) D = pfma4(pmul4(dx, wp[u]), rq, D);
+        if (!kKeep) D = pfma4(pmul4(dx, kHold ? held_p[kHold ? u : 0] : load_wp(c)), rq, D);
         D = pfma4(r, k1, D);
         sum_pre[u] = pfma4(dx, pscale4(r, rq), sum_pre[u]);
       }
       st4(static_cast<R*>(a.dr) + base + c, pscale4(D, out_scale));
       if (!a.y) continue;
-      float4 o = pscale4(pmul4(D, wq[u]), ru);
+      float4 o = pscale4(pmul4(D, kHold ? held_q[kHold ? u : 0] : load_wq(c)), ru);
       if (use_y) {
         const float4 y = kKeep ? k_y[u % KEEP] : ld4(s_y + c);
         sum_post[u] = pfma4(D, pscale4(y, ru), sum_post[u]);
@@ -837,10 +845,11 @@ int bwd(const LaunchCtx& ctx, const NormArgs& a, float* part) {
   const int d = a.d;
   const bool sums = a.dw_pre || a.dw_post || a.gate_kind == OCCULT_GATE_CHANNEL;
   int n_part = 0, rc;  // rows of partial sums that are left to add up
-  // bulk copies move whole 16 bytes; the ring holds a row of up to 8192 columns.  Above
-  // 2048 columns three or four units a thread (16 warps of two units, one CTA an SM: 210
-  // against 175 us at 16384 x 4096).
-  if (d * sizeof(R) % 16 != 0 || d > 8192) rc = bwd_any<R, L>(ctx, a, part, &n_part);
+  // bulk copies move whole 16 bytes; the ring holds a row of up to 16384 columns (12800
+  // with an fp32 stream).  Above 2048 columns three or four units a thread (16 warps of
+  // two units, one CTA an SM: 210 against 175 us at 16384 x 4096).
+  if (d * sizeof(R) % 16 != 0 || bwd_row_bytes<R>(d) > kRingBytes)
+    rc = bwd_any<R, L>(ctx, a, part, &n_part);
   else if (d <= 128) rc = bwd_rows<R, L, 1, 1, 3>(ctx, a, sums, part, &n_part);
   else if (d <= 256) rc = bwd_rows<R, L, 1, 2, 2>(ctx, a, sums, part, &n_part);
   else if (d <= 512) rc = bwd_rows<R, L, 2, 2, 2>(ctx, a, sums, part, &n_part);
@@ -848,7 +857,8 @@ int bwd(const LaunchCtx& ctx, const NormArgs& a, float* part) {
   else if (d <= 2048) rc = bwd_rows<R, L, 8, 2, 2>(ctx, a, sums, part, &n_part);
   else if (d <= 4096) rc = bwd_rows<R, L, 8, 4, 2>(ctx, a, sums, part, &n_part);
   else if (d <= 6144) rc = bwd_rows<R, L, 16, 3, 1>(ctx, a, sums, part, &n_part);
-  else rc = bwd_rows<R, L, 16, 4, 1>(ctx, a, sums, part, &n_part);
+  else if (d <= 8192) rc = bwd_rows<R, L, 16, 4, 1>(ctx, a, sums, part, &n_part);
+  else rc = bwd_rows<R, L, 32, 4, 1>(ctx, a, sums, part, &n_part);
   if (rc || !sums || n_part == 0) return rc;
   return cuda_status(launch_pdl(norm_bwd_cols_kernel<L>, (2 * d + 31) / 32, kColWarps * 32, 0,
                                 ctx.stream, a, part, n_part));

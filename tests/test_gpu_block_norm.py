@@ -433,3 +433,21 @@ def test_replays_from_a_cuda_graph(occ):
     torch.cuda.synchronize()
     for k, v in {**o, **f}.items():
         assert torch.equal(v, want[k]), k
+
+
+@pytest.mark.parametrize("res", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [8256, 12800, 12864, 16384])
+def test_wide_rows(occ, d, res):
+    """Rows around what a ring of one row holds (12800 columns with an fp32 stream)."""
+    for gate, post in (("channel", True), ("token", True), ("none", False)):
+        c = Case(170, d, "bf16", res, post=post, gate=gate, seed=d)
+        check_forward(occ, c)
+        check_backward(occ, c)
+
+
+@pytest.mark.parametrize("T,d", [(1500, 4), (1500, 36), (700, 128)])
+def test_in_place_narrow_rows(occ, T, d):
+    """Neighbouring rows share cache lines while copies run ahead of the stores."""
+    c = Case(T, d, "f32", "f32", gate="token", seed=d)
+    check_forward(occ, c, inplace=True)
+    check_backward(occ, c, inplace=True)
