@@ -9,10 +9,10 @@
 // sums and gradients are fp32 throughout, counts are integers.
 //
 // Measured on one GB300, loss + gradient (added to what is there): 32768 tokens, 64
-// experts, top-8 10.2 + 4.5 us (the first launch 3.8 us, bound by two steps of loads;
+// experts, top-8 10.0 + 3.7 us (the first launch 3.6 us, bound by two steps of loads;
 // the second by its chain of sums in one CTA); 131072 tokens, 256 experts, masked, 32
 // sequences 35 + 56 us = 3.9 and 7.2 TB/s (the logits twice, the gradient in and out);
-// 256 tokens, 8 experts 4.7 + 1.8 us.
+// 256 tokens, 8 experts 4.7 + 1.7 us.
 #include "common.cuh"
 #include "kernels.h"
 
@@ -94,6 +94,9 @@ __device__ __forceinline__ void load_row(const float* row, int Ne, bool vec, int
       v[j] = expert_of<LP>(sub, j) < Ne ? row[expert_of<LP>(sub, j)] : pad;
   }
 }
+__device__ __forceinline__ float2 two(float v) { return make_float2(v, v); }
+__device__ __forceinline__ float2 pair(const float (&v)[8], int i) { return make_float2(v[i], v[i + 1]); }
+__device__ __forceinline__ void put(float (&v)[8], int i, float2 x) { v[i] = x.x; v[i + 1] = x.y; }
 __device__ __forceinline__ float minus_inf() { return -__int_as_float(0x7f800000); }
 
 // v = exp(z - max), *inv = 1 / their sum; returns log sum exp.  The exponentials are
@@ -108,13 +111,15 @@ __device__ __forceinline__ float softmax_row(float (&v)[8], float* inv) {
   for (int i = 1; i < 8; ++i) mx = fmaxf(mx, v[i]);
 #pragma unroll
   for (int o = LP / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-  float z = 0.f;
+  float2 z2 = two(0.f);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float y = (v[i] - mx) * kLog2e;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(v[i]) : "f"(y));
-    z += v[i];
+  for (int i = 0; i < 8; i += 2) {
+    const float2 y = __fmul2_rn(__fadd2_rn(pair(v, i), two(-mx)), two(kLog2e));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(v[i]) : "f"(y.x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(v[i + 1]) : "f"(y.y));
+    z2 = __fadd2_rn(z2, pair(v, i));
   }
+  float z = z2.x + z2.y;
 #pragma unroll
   for (int o = LP / 2; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
   *inv = __fdividef(1.f, z);  // z is about 1 .. 256
@@ -190,7 +195,8 @@ __device__ __forceinline__ void sum_tile(const BalanceArgs& a, int64_t t0, int64
     for (int q = 0; q < kRows; ++q) {
       if (!on[q]) continue;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) acc[i] = fmaf(v[q][i], inv[q], acc[i]);
+      for (int i = 0; i < 8; i += 2)
+        put(acc, i, __ffma2_rn(pair(v[q], i), two(inv[q]), pair(acc, i)));
       if (sub == 0) { sq = fmaf(lse[q], lse[q], sq); ++n; }
 #pragma unroll
       for (int r = 0; r < 2; ++r)
@@ -363,9 +369,9 @@ int launch_cluster(const LaunchCtx& ctx, const BalanceArgs& a, int ctas) {
   return cuda_status(cudaLaunchKernelEx(&cfg, kernel, a));
 }
 
-// Pass 1: CTA x of group y takes one tile of the group's tokens.  131072 x 256: 28 us,
-// 70 % of the issue slots (168 instructions a token and warp, of which 40 for eight
-// exponentials a lane); a token a warp with scalar loads and expf took 55 us.
+// Pass 1: CTA x of group y takes one tile of the group's tokens.  131072 x 256: 27 us,
+// near both bounds (5.0 TB/s and two thirds of the issue slots, at some 150 instructions a
+// token and warp); a token a warp with scalar loads and expf took 55 us.
 template <int LP>
 __global__ void __launch_bounds__(kTileThreads, 2)
 balance_tiles_kernel(BalanceArgs a, Tiles tiles) {
@@ -521,9 +527,10 @@ __global__ void __launch_bounds__(kSumThreads) balance_groups_kernel(BalanceArgs
 
 // dz = dloss (p (w - w . p) + w_z lse p), LP lanes a token as in the first pass.  131072
 // x 256 added to a gradient: 56 us = 7.2 TB/s, bound by memory (85 us with the gradient
-// read after the softmax and a 64-bit division a token).
+// read after the softmax and a 64-bit division a token).  Four CTAs an SM: three (the
+// registers it would take) 65 us, five (spills) 63 us.
 template <int LP>
-__global__ void __launch_bounds__(kGradThreads) balance_grad_kernel(BalanceArgs a) {
+__global__ void __launch_bounds__(kGradThreads, 4) balance_grad_kernel(BalanceArgs a) {
   constexpr int kTok = 32 / LP;
   pdl_wait();
   pdl_trigger();
@@ -559,19 +566,24 @@ __global__ void __launch_bounds__(kGradThreads) balance_grad_kernel(BalanceArgs 
                                 : static_cast<unsigned>(in ? t : b) / static_cast<unsigned>(a.L);
     load_row<LP>(a.grad_w + static_cast<size_t>(g) * a.Ne, a.Ne, vec, sub, 0.f, w);
     const float lse = softmax_row<LP>(v, &inv);
-    float dot = 0.f;
+    float2 dot2 = two(0.f);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      v[i] *= inv;
-      dot = fmaf(v[i], w[i], dot);
+    for (int i = 0; i < 8; i += 2) {
+      put(v, i, __fmul2_rn(pair(v, i), two(inv)));
+      dot2 = __ffma2_rn(pair(v, i), pair(w, i), dot2);
     }
+    float dot = dot2.x + dot2.y;
 #pragma unroll
     for (int o = LP / 2; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
     if (!in || (!on && a.accumulate)) continue;
     const float shift = wz * lse - dot;
     float* out = a.dlogits + t * a.Ne;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = on ? fmaf(up * v[i], w[i] + shift, old[i]) : 0.f;
+    for (int i = 0; i < 8; i += 2) {
+      const float2 dz = __ffma2_rn(__fmul2_rn(pair(v, i), two(up)),
+                                   __fadd2_rn(pair(w, i), two(shift)), pair(old, i));
+      put(v, i, on ? dz : two(0.f));
+    }
     if (vec) {
 #pragma unroll
       for (int h = 0; h < 2; ++h)
