@@ -1,4 +1,4 @@
-// AdamW over many tensors in one launch, with fp32 states or 8-bit ones.
+// AdamW over many tensors in a launch for each kind, with fp32 states or 8-bit ones.
 //
 // The 8-bit states are floats of their own: magnitudes x > 0 of a block of 256
 // elements are cut to MANT mantissa bits (m: 3 and a sign, sqrt(v): 4) by adding
@@ -10,10 +10,10 @@
 //
 // Bound by the bytes: an element moves 30 with fp32 states, a bf16 parameter and its
 // master (28 for an fp32 parameter), 18 with 8-bit states and a master, 16 for an fp32
-// and 12 for a bf16 parameter alone.  Measured on one GB300, 402.8 M weights: 1733 us =
-// 7.0 TB/s, 1040 us = 7.0 TB/s, 945 us = 6.8 TB/s, and 907 us = 5.3 TB/s for the last,
+// and 12 for a bf16 parameter alone.  Measured on one GB300, 402.8 M weights: 1723 us =
+// 7.0 TB/s, 1031 us = 7.0 TB/s, 943 us = 6.8 TB/s, and 852 us = 5.7 TB/s for the last,
 // which takes 67 instructions an element, a dozen of them the correctly rounded root,
-// and 75 % of the issue slots.  Moments, roots and parameters are fp32 until they are
+// and most of the issue slots.  Moments, roots and parameters are fp32 until they are
 // stored.
 #include <math.h>
 
@@ -39,7 +39,6 @@ struct Tensor {
   void *m, *v;
   uint8_t *m_exp, *v_exp;
   int64_t n, first;
-  int kind;
 };
 struct AdamTable {
   float b1, c1, b2, c2;      // beta, 1 - beta
@@ -356,7 +355,7 @@ __device__ __forceinline__ void step_block(const AdamTable& a, const Tensor& T, 
 // The blocks blk, blk + kAdamWarps, ... below end of a tensor by one warp; with 8-bit
 // states the next block's words are on their way while this one's are worked on (without
 // that 1139 us where it takes 940), for a bf16 parameter without a master, whose words are
-// few, both blocks' from the start (907 us; with a master 1273 against 1040 us).
+// few, both blocks' from the start (852 against 962 us; with a master 1273 against 1040).
 template <int BITS, int KIND>
 __device__ __forceinline__ void step_blocks(const AdamTable& a, const Tensor& T, int64_t blk,
                                             int64_t end, float gs) {
@@ -389,8 +388,15 @@ __device__ __forceinline__ void step_blocks(const AdamTable& a, const Tensor& T,
   }
 }
 
-template <int BITS>
-__global__ void __launch_bounds__(kAdamThreads, 8) adamw_kernel(const __grid_constant__ AdamTable a) {
+// CTAs of an SM: eight, nine for the kind that the issue rate bounds (64 bytes of stack a
+// thread for the spills, and 852 us where eight CTAs take 880, ten 887); nine cost the
+// other two with 8-bit states more than they give (1087 against 1031 us with masters).
+__host__ __device__ constexpr int adam_ctas(int bits, int kind) {
+  return bits == 8 && kind == KIND_BF16 ? 9 : 8;
+}
+template <int BITS, int KIND>
+__global__ void __launch_bounds__(kAdamThreads, adam_ctas(BITS, KIND))
+adamw_kernel(const __grid_constant__ AdamTable a) {
   pdl_wait();
   pdl_trigger();
   // the tensor of this CTA: the one whose CTAs include it (all looked at at once)
@@ -406,9 +412,7 @@ __global__ void __launch_bounds__(kAdamThreads, 8) adamw_kernel(const __grid_con
   const int64_t n_blk = (T.n + kBlock - 1) / kBlock;
   const int64_t end = n_blk < blk0 + a.cta_blocks ? n_blk : blk0 + a.cta_blocks;
   const int64_t mine = blk0 + (threadIdx.x >> 5);
-  if (T.kind == KIND_F32) step_blocks<BITS, KIND_F32>(a, T, mine, end, gs);
-  else if (T.kind == KIND_MASTER) step_blocks<BITS, KIND_MASTER>(a, T, mine, end, gs);
-  else step_blocks<BITS, KIND_BF16>(a, T, mine, end, gs);
+  step_blocks<BITS, KIND>(a, T, mine, end, gs);
 }
 
 // The values of 8-bit states: kReadSteps times a thread turns 8 codes into 16 bytes.
@@ -448,6 +452,14 @@ adamw_read_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__
   }
 }
 
+int kind_of(const occult_param_t& p) {
+  return p.dtype == OCCULT_F32 ? KIND_F32 : p.master ? KIND_MASTER : KIND_BF16;
+}
+template <int BITS, int KIND>
+cudaError_t launch(const LaunchCtx& ctx, const AdamTable& a, unsigned grid) {
+  return launch_pdl(adamw_kernel<BITS, KIND>, grid, kAdamThreads, 0, ctx.stream, a);
+}
+
 }  // namespace
 
 int launch_adamw(const LaunchCtx& ctx, const occult_adamw_t& o, const occult_param_t* params,
@@ -474,31 +486,39 @@ int launch_adamw(const LaunchCtx& ctx, const occult_adamw_t& o, const occult_par
   steps = steps < 1 ? 1 : (steps > kMaxSteps ? kMaxSteps : steps);
   a.cta_blocks = kAdamWarps * static_cast<int>(steps);
   const int64_t chunk = static_cast<int64_t>(a.cta_blocks) * kBlock;
-  int i = 0;
-  while (i < n_params) {
-    a.n = 0;
-    int64_t chunks = 0;
-    for (; i < n_params && a.n < kMaxTensors; ++i) {
-      const occult_param_t& p = params[i];
-      if (p.n == 0) continue;
-      const int64_t c = (p.n + chunk - 1) / chunk;
-      if (chunks + c > 0x7fffffff) {
-        if (a.n > 0) break;
-        return OCCULT_ERR_UNSUPPORTED;
+  // A kernel for each kind of tensor, for up to kMaxTensors at a time (one kernel for all
+  // kinds has their worst registers: 907 instead of 852 us for bf16 alone with 8-bit
+  // states, 1748 instead of 1723 us with masters and fp32 states).
+  for (int kind = KIND_F32; kind <= KIND_BF16; ++kind) {
+    int i = 0;
+    while (i < n_params) {
+      a.n = 0;
+      int64_t chunks = 0;
+      for (; i < n_params && a.n < kMaxTensors; ++i) {
+        const occult_param_t& p = params[i];
+        if (p.n == 0 || kind_of(p) != kind) continue;
+        const int64_t c = (p.n + chunk - 1) / chunk;
+        if (chunks + c > 0x7fffffff) {
+          if (a.n > 0) break;
+          return OCCULT_ERR_UNSUPPORTED;
+        }
+        a.t[a.n] = {p.param, p.master, p.grad, p.m, p.v, p.m_exp, p.v_exp, p.n, p.first};
+        a.chunk0[a.n++] = static_cast<int>(chunks);
+        chunks += c;
       }
-      Tensor& t = a.t[a.n];
-      t.param = p.param; t.master = p.master; t.grad = p.grad; t.m = p.m; t.v = p.v;
-      t.m_exp = p.m_exp; t.v_exp = p.v_exp; t.n = p.n; t.first = p.first;
-      t.kind = p.dtype == OCCULT_F32 ? KIND_F32 : p.master ? KIND_MASTER : KIND_BF16;
-      a.chunk0[a.n++] = static_cast<int>(chunks);
-      chunks += c;
+      if (a.n == 0) break;
+      const unsigned grid = static_cast<unsigned>(chunks);
+      cudaError_t e;
+      if (o.state_bits == 32)
+        e = kind == KIND_F32 ? launch<32, KIND_F32>(ctx, a, grid)
+            : kind == KIND_MASTER ? launch<32, KIND_MASTER>(ctx, a, grid)
+                                  : launch<32, KIND_BF16>(ctx, a, grid);
+      else
+        e = kind == KIND_F32 ? launch<8, KIND_F32>(ctx, a, grid)
+            : kind == KIND_MASTER ? launch<8, KIND_MASTER>(ctx, a, grid)
+                                  : launch<8, KIND_BF16>(ctx, a, grid);
+      if (e != cudaSuccess) return OCCULT_ERR_CUDA;
     }
-    if (a.n == 0) break;
-    const cudaError_t e =
-        o.state_bits == 32
-            ? launch_pdl(adamw_kernel<32>, static_cast<unsigned>(chunks), kAdamThreads, 0, ctx.stream, a)
-            : launch_pdl(adamw_kernel<8>, static_cast<unsigned>(chunks), kAdamThreads, 0, ctx.stream, a);
-    if (e != cudaSuccess) return OCCULT_ERR_CUDA;
   }
   return OCCULT_OK;
 }

@@ -788,8 +788,8 @@ typedef struct occult_param {
 } occult_param_t;
 
 /*
- * occult_adamw -- one AdamW step over n_params tensors in one launch for every
- * 256 of them:
+ * occult_adamw -- one AdamW step over n_params tensors, in one launch for each kind
+ * of tensor among them (fp32, bf16 with a master copy, bf16 alone) and every 256:
  *   g = grad_scale * grad
  *   m = beta1 m + (1 - beta1) g,   v = beta2 v + (1 - beta2) g^2
  *   w = (1 - lr weight_decay) w - lr / (1 - beta1^step) * m
