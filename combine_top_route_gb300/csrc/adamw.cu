@@ -1,4 +1,4 @@
-// AdamW over many tensors in a launch for each kind, with fp32 states or 8-bit ones.
+// AdamW over many tensors at once, with fp32 states or 8-bit ones.
 //
 // The 8-bit states are floats of their own: magnitudes x > 0 of a block of 256
 // elements are cut to MANT mantissa bits (m: 3 and a sign, sqrt(v): 4) by adding
@@ -29,8 +29,9 @@ constexpr int kAdamWarps = kAdamThreads / 32;
 constexpr int kBlock = OCCULT_STATE_BLOCK;       // elements of a warp's step
 constexpr int kMaxSteps = 2;                     // blocks of a warp at most
 constexpr int kMaxTensors = 256;                 // of one launch
+constexpr int64_t kOwnWeights = 1 << 25;         // of a kind, for a launch of its own
 
-enum : int { KIND_F32 = 0, KIND_MASTER = 1, KIND_BF16 = 2 };
+enum : int { KIND_F32 = 0, KIND_MASTER = 1, KIND_BF16 = 2, KIND_ANY = 3 };
 
 struct Tensor {
   void* param;
@@ -39,6 +40,7 @@ struct Tensor {
   void *m, *v;
   uint8_t *m_exp, *v_exp;
   int64_t n, first;
+  int kind;
 };
 struct AdamTable {
   float b1, c1, b2, c2;      // beta, 1 - beta
@@ -412,7 +414,10 @@ adamw_kernel(const __grid_constant__ AdamTable a) {
   const int64_t n_blk = (T.n + kBlock - 1) / kBlock;
   const int64_t end = n_blk < blk0 + a.cta_blocks ? n_blk : blk0 + a.cta_blocks;
   const int64_t mine = blk0 + (threadIdx.x >> 5);
-  step_blocks<BITS, KIND>(a, T, mine, end, gs);
+  const int kind = KIND == KIND_ANY ? T.kind : KIND;
+  if (kind == KIND_F32) step_blocks<BITS, KIND_F32>(a, T, mine, end, gs);
+  else if (kind == KIND_MASTER) step_blocks<BITS, KIND_MASTER>(a, T, mine, end, gs);
+  else step_blocks<BITS, KIND_BF16>(a, T, mine, end, gs);
 }
 
 // The values of 8-bit states: kReadSteps times a thread turns 8 codes into 16 bytes.
@@ -455,9 +460,13 @@ adamw_read_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__
 int kind_of(const occult_param_t& p) {
   return p.dtype == OCCULT_F32 ? KIND_F32 : p.master ? KIND_MASTER : KIND_BF16;
 }
-template <int BITS, int KIND>
-cudaError_t launch(const LaunchCtx& ctx, const AdamTable& a, unsigned grid) {
-  return launch_pdl(adamw_kernel<BITS, KIND>, grid, kAdamThreads, 0, ctx.stream, a);
+template <int BITS>
+cudaError_t launch(const LaunchCtx& ctx, int kind, const AdamTable& a, unsigned grid) {
+  const auto k = kind == KIND_F32      ? adamw_kernel<BITS, KIND_F32>
+                 : kind == KIND_MASTER ? adamw_kernel<BITS, KIND_MASTER>
+                 : kind == KIND_BF16   ? adamw_kernel<BITS, KIND_BF16>
+                                       : adamw_kernel<BITS, KIND_ANY>;
+  return launch_pdl(k, grid, kAdamThreads, 0, ctx.stream, a);
 }
 
 }  // namespace
@@ -480,43 +489,48 @@ int launch_adamw(const LaunchCtx& ctx, const occult_adamw_t& o, const occult_par
   // where that leaves four CTAs for each place on the GPU; one for smaller sets.  With four
   // the CTAs' streams lie too far apart: one, two, four blocks took 1075, 977, 962 us with
   // 8-bit states alone and 1119, 1046, 1178 us with a master.
-  int64_t blocks = 0;
-  for (int k = 0; k < n_params; ++k) blocks += (params[k].n + kBlock - 1) / kBlock;
+  int64_t blocks = 0, of_kind[3] = {0, 0, 0};
+  for (int k = 0; k < n_params; ++k) {
+    const int64_t b = (params[k].n + kBlock - 1) / kBlock;
+    blocks += b;
+    of_kind[kind_of(params[k])] += b;
+  }
   int64_t steps = blocks / (static_cast<int64_t>(kAdamWarps) * 4 * 8 * ctx.num_sms);
   steps = steps < 1 ? 1 : (steps > kMaxSteps ? kMaxSteps : steps);
   a.cta_blocks = kAdamWarps * static_cast<int>(steps);
   const int64_t chunk = static_cast<int64_t>(a.cta_blocks) * kBlock;
-  // A kernel for each kind of tensor, for up to kMaxTensors at a time (one kernel for all
-  // kinds has their worst registers: 907 instead of 852 us for bf16 alone with 8-bit
-  // states, 1748 instead of 1723 us with masters and fp32 states).
-  for (int kind = KIND_F32; kind <= KIND_BF16; ++kind) {
+  // A kernel of its own for a kind of 2^25 weights and more, or where there is no other;
+  // the rest go together.  Own registers save 402.8 M weights 55 us (bf16 alone with 8-bit
+  // states) or 25 us (masters and fp32 states); a launch more costs 3 to 5 us, and 60
+  // tensors of three kinds and 2560 weights each take 5 us in one, 11 us in three launches,
+  // of 2^20 each with 8-bit states 161 and 169 us.
+  bool own[4];
+  own[KIND_ANY] = true;
+  for (int k = 0; k < KIND_ANY; ++k)
+    own[k] = of_kind[k] == blocks || of_kind[k] >= kOwnWeights / kBlock;
+  for (int kind = KIND_F32; kind <= KIND_ANY; ++kind) {
+    if (!own[kind]) continue;
     int i = 0;
     while (i < n_params) {
       a.n = 0;
       int64_t chunks = 0;
       for (; i < n_params && a.n < kMaxTensors; ++i) {
         const occult_param_t& p = params[i];
-        if (p.n == 0 || kind_of(p) != kind) continue;
+        const int its = kind_of(p);
+        if (p.n == 0 || (own[its] ? its : KIND_ANY) != kind) continue;
         const int64_t c = (p.n + chunk - 1) / chunk;
         if (chunks + c > 0x7fffffff) {
           if (a.n > 0) break;
           return OCCULT_ERR_UNSUPPORTED;
         }
-        a.t[a.n] = {p.param, p.master, p.grad, p.m, p.v, p.m_exp, p.v_exp, p.n, p.first};
+        a.t[a.n] = {p.param, p.master, p.grad, p.m, p.v, p.m_exp, p.v_exp, p.n, p.first, its};
         a.chunk0[a.n++] = static_cast<int>(chunks);
         chunks += c;
       }
       if (a.n == 0) break;
       const unsigned grid = static_cast<unsigned>(chunks);
-      cudaError_t e;
-      if (o.state_bits == 32)
-        e = kind == KIND_F32 ? launch<32, KIND_F32>(ctx, a, grid)
-            : kind == KIND_MASTER ? launch<32, KIND_MASTER>(ctx, a, grid)
-                                  : launch<32, KIND_BF16>(ctx, a, grid);
-      else
-        e = kind == KIND_F32 ? launch<8, KIND_F32>(ctx, a, grid)
-            : kind == KIND_MASTER ? launch<8, KIND_MASTER>(ctx, a, grid)
-                                  : launch<8, KIND_BF16>(ctx, a, grid);
+      const cudaError_t e = o.state_bits == 32 ? launch<32>(ctx, kind, a, grid)
+                                               : launch<8>(ctx, kind, a, grid);
       if (e != cudaSuccess) return OCCULT_ERR_CUDA;
     }
   }

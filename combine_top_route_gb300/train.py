@@ -10,7 +10,7 @@ kernels:
     backward  from the gradient of r' through the second norm, the layer, the
               router (the auxiliary losses' gradient added to the gates') and the
               first norm to the gradient of r and of every weight
-    step      AdamW over all of the block's weights, a launch for each kind of tensor
+    step      AdamW over all of the block's weights, up to 256 tensors a launch
 
 ``OccultAdamW`` is that update on its own, for any tensors with fp32 gradients.
 """

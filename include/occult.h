@@ -788,8 +788,9 @@ typedef struct occult_param {
 } occult_param_t;
 
 /*
- * occult_adamw -- one AdamW step over n_params tensors, in one launch for each kind
- * of tensor among them (fp32, bf16 with a master copy, bf16 alone) and every 256:
+ * occult_adamw -- one AdamW step over n_params tensors, up to 256 of them a launch
+ * (fp32, bf16 with a master copy and bf16 alone go together, except that each has its
+ * own launches from 2^25 weights on):
  *   g = grad_scale * grad
  *   m = beta1 m + (1 - beta1) g,   v = beta2 v + (1 - beta2) g^2
  *   w = (1 - lr weight_decay) w - lr / (1 - beta1^step) * m

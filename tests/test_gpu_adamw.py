@@ -322,3 +322,37 @@ def test_offsets_past_32_bits(occ):
                 v_exp=ve[lo // 256:])
     check(occ, s, {}, view, 1)
     assert not p[:lo:4096].any() and not m[:lo:4096].any()
+
+
+@pytest.mark.parametrize("large", KINDS)
+@pytest.mark.parametrize("bits", [32, 8])
+def test_a_tensor_steps_the_same_beside_others(occ, bits, large):
+    """One kind large enough for launches of its own, the others small: the bits that
+    each tensor gets when it is stepped alone."""
+    big = (1 << 25) + 300
+    st = torch.float32 if bits == 32 else torch.uint8
+    gen = torch.Generator(device="cuda").manual_seed(12)
+
+    def tensor(kind, n, first):
+        w = torch.randn(n, generator=gen, device="cuda") * 0.05
+        t = dict(param=w if kind == "f32" else w.to(torch.bfloat16), first=first,
+                 grad=torch.randn(n, generator=gen, device="cuda") * 1e-2,
+                 m=torch.zeros(n, dtype=st, device="cuda"), v=torch.zeros(n, dtype=st, device="cuda"))
+        if kind == "master":
+            t["master"] = w
+        if bits == 8:
+            t.update({k: torch.zeros(-(-n // 256), dtype=torch.uint8, device="cuda")
+                      for k in ("m_exp", "v_exp")})
+        return t
+
+    together = [tensor(kind, big if kind == large and i == 1 else 1000 + 7 * i, 1000 * i)
+                for i in range(3) for kind in KINDS]
+    alone = [{k: x.clone() if isinstance(x, torch.Tensor) else x for k, x in t.items()}
+             for t in together]
+    for t in (1, 2):
+        step(occ, together, t, bits)
+        for x in alone:
+            step(occ, [x], t, bits)
+    for a, b in zip(together, alone):
+        for k in a:
+            assert torch.equal(a[k], b[k]) if isinstance(a[k], torch.Tensor) else a[k] == b[k], k
