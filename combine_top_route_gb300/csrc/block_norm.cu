@@ -175,8 +175,8 @@ __global__ void __launch_bounds__(kWideThreads) norm_bwd_kernel(NormArgs a, floa
 // groups of a CTA (8 / G, at least one) work apart from each other.
 template <int G>
 struct Group {
-  static constexpr int kThreads = G > 8 ? 32 * G : 256;
-  static constexpr int kGroups = kThreads / (32 * G);
+  static constexpr int kGroups = G > 8 ? 1 : 8 / G;
+  static constexpr int kThreads = 32 * G * kGroups;
   __device__ static int index() { return threadIdx.x / (32 * G); }
   __device__ static int place() { return threadIdx.x % (32 * G); }
   __device__ static void sync() {
@@ -739,7 +739,11 @@ int fwd_rows(const LaunchCtx& ctx, const NormArgs& a) {
 // Reads that run further ahead of the stores slow both: T=30011, d=2048, norms on both
 // sides, us with two, three, four rows: forward 102, 93, 92 (bf16 stream) and 130, 147,
 // 149 (fp32); backward 155, 152, 153 and 199, 220, 222.
-constexpr int kRingBytes = 200 * 1024;  // of shared memory an SM, over its CTAs
+// So do three rows of the forward that are more than 100 KB an SM together (two and three:
+// 104 and 114 us at 29127 x 2304, 105 and 116 at 8192 x 8192; at 11915 x 5632, 99 KB, 107
+// and 101).
+constexpr int kRingBytes = 200 * 1024;   // of shared memory an SM, over its CTAs
+constexpr int kAheadBytes = 100 * 1024;  // of them for three rows of the forward
 template <typename R>
 inline int ring_stages(int bytes, int ctas) {
   const int fit = kRingBytes / ctas / bytes, n = sizeof(R) == 4 ? 2 : 3;
@@ -749,7 +753,8 @@ inline int ring_stages(int bytes, int ctas) {
 template <typename R, typename L, int G, int U, int CTAS>
 int fwd_ring(const LaunchCtx& ctx, const NormArgs& a) {
   const int row = fwd_row_bytes<R>(a.d) * Group<G>::kGroups;
-  const int stages = ring_stages<R>(row, CTAS);
+  int stages = ring_stages<R>(row, CTAS);
+  if (stages > 2 && stages * row * CTAS > kAheadBytes) stages = 2;
   const size_t smem = static_cast<size_t>(stages) * row;
   const int rc = allow_smem(norm_fwd_ring_kernel<R, L, G, U, CTAS>, smem);
   if (rc) return rc;
@@ -765,15 +770,27 @@ int fwd(const LaunchCtx& ctx, const NormArgs& a) {
   // Many rows come through the ring (its copies move whole 16 bytes and it holds rows
   // of up to 8192 columns); few rows have as many warps each as give a thread two
   // loads of each tensor, and no ring to set up.  (608 rows of 2048 take 3.5 us either
-  // way.)  Warps a row and CTAs an SM by width: two units a thread, and groups enough
-  // to hide one row's latency behind the others' copies.
+  // way.)  Warps a row and CTAs an SM by width: two units a thread with most of the
+  // threads at work, and groups enough to hide one row's latency behind the others'
+  // copies, but no more than that (their streams take the memory's rows from each other).
+  // With only powers of two warps a row, us before and now: 32768 x 320 27 and 20, x 768 50
+  // and 42, x 1408 95 and 73, 31775 x 2112 174 and 105, 23831 x 2816 135 and 105; with an
+  // fp32 stream x 768 and x 320 gain nothing, x 1408 109 and 101, x 2112 175 and 141, and
+  // 16384 x 4096 takes 146 us with one CTA an SM, 163 with two.
   if (a.T >= 4 * ctx.num_sms && d * sizeof(R) % 16 == 0 && d <= 8192) {
-    if (d <= 128) return fwd_ring<R, L, 1, 1, 5>(ctx, a);
+    constexpr bool kF32 = sizeof(R) == 4;
+    if (d <= 128) return fwd_ring<R, L, 1, 1, 4>(ctx, a);
     if (d <= 256) return fwd_ring<R, L, 1, 2, 4>(ctx, a);
+    if (d <= 384 && !kF32) return fwd_ring<R, L, 1, 3, 3>(ctx, a);
     if (d <= 512) return fwd_ring<R, L, 2, 2, 3>(ctx, a);
+    if (d <= 768) return fwd_ring<R, L, 3, 2, 3>(ctx, a);
     if (d <= 1024) return fwd_ring<R, L, 4, 2, 2>(ctx, a);
+    if (d <= 1536) return fwd_ring<R, L, 6, 2, 3>(ctx, a);
     if (d <= 2048) return fwd_ring<R, L, 8, 2, 2>(ctx, a);
-    if (d <= 4096) return fwd_ring<R, L, 16, 2, 2>(ctx, a);
+    if (d <= 2304) return fwd_ring<R, L, 9, 2, kF32 ? 2 : 3>(ctx, a);
+    if (d <= 2816) return fwd_ring<R, L, kF32 ? 16 : 11, 2, 2>(ctx, a);
+    if (d <= 4096) return fwd_ring<R, L, 16, 2, kF32 ? 1 : 2>(ctx, a);
+    if (d <= 6144) return fwd_ring<R, L, 16, 3, 1>(ctx, a);
     return fwd_ring<R, L, 16, 4, 1>(ctx, a);
   }
   if (d <= 256) return fwd_rows<R, L, 1, 2>(ctx, a);
@@ -844,17 +861,25 @@ template <typename R, typename L>
 int bwd(const LaunchCtx& ctx, const NormArgs& a, float* part) {
   const int d = a.d;
   const bool sums = a.dw_pre || a.dw_post || a.gate_kind == OCCULT_GATE_CHANNEL;
+  constexpr bool kF32 = sizeof(R) == 4;
   int n_part = 0, rc;  // rows of partial sums that are left to add up
   // bulk copies move whole 16 bytes; the ring holds a row of up to 16384 columns (12800
   // with an fp32 stream).  Above 2048 columns three or four units a thread (16 warps of
-  // two units, one CTA an SM: 210 against 175 us at 16384 x 4096).
+  // two units, one CTA an SM: 210 against 175 us at 16384 x 4096); one, three or six warps
+  // a row where powers of two leave a third of the threads or more without work (us: 32768
+  // x 320 45 -> 40, x 768 84 -> 71, x 1408 149 -> 130, 31775 x 2112 204 -> 179; with an fp32
+  // stream 259 -> 225 at 2112, the others the same, but x 320, which keeps two warps).
   if (d * sizeof(R) % 16 != 0 || bwd_row_bytes<R>(d) > kRingBytes)
     rc = bwd_any<R, L>(ctx, a, part, &n_part);
   else if (d <= 128) rc = bwd_rows<R, L, 1, 1, 3>(ctx, a, sums, part, &n_part);
   else if (d <= 256) rc = bwd_rows<R, L, 1, 2, 2>(ctx, a, sums, part, &n_part);
+  else if (d <= 384 && !kF32) rc = bwd_rows<R, L, 1, 3, 2>(ctx, a, sums, part, &n_part);
   else if (d <= 512) rc = bwd_rows<R, L, 2, 2, 2>(ctx, a, sums, part, &n_part);
+  else if (d <= 768) rc = bwd_rows<R, L, 3, 2, 2>(ctx, a, sums, part, &n_part);
   else if (d <= 1024) rc = bwd_rows<R, L, 4, 2, 2>(ctx, a, sums, part, &n_part);
+  else if (d <= 1536) rc = bwd_rows<R, L, 6, 2, 2>(ctx, a, sums, part, &n_part);
   else if (d <= 2048) rc = bwd_rows<R, L, 8, 2, 2>(ctx, a, sums, part, &n_part);
+  else if (d <= 2304) rc = bwd_rows<R, L, 6, 3, kF32 ? 3 : 2>(ctx, a, sums, part, &n_part);
   else if (d <= 4096) rc = bwd_rows<R, L, 8, 4, 2>(ctx, a, sums, part, &n_part);
   else if (d <= 6144) rc = bwd_rows<R, L, 16, 3, 1>(ctx, a, sums, part, &n_part);
   else if (d <= 8192) rc = bwd_rows<R, L, 16, 4, 1>(ctx, a, sums, part, &n_part);

@@ -451,3 +451,18 @@ def test_in_place_narrow_rows(occ, T, d):
     c = Case(T, d, "f32", "f32", gate="token", seed=d)
     check_forward(occ, c, inplace=True)
     check_backward(occ, c, inplace=True)
+
+
+@pytest.mark.parametrize("d,dtype,res", [
+    (d, dtype, res) for d in (32, 248, 320, 384, 504, 768, 776, 832, 1408, 1536, 1544, 1600, 2112,
+                              2304, 2312, 2368, 2816, 2824, 2880, 4096, 6144, 6152, 6208)
+    for dtype, res in TYPES if dtype == "f32" or d % 64 == 0])
+def test_every_width_of_many_rows(occ, d, dtype, res):
+    """Rows enough for a ring of several each, at the ends of the widths that take the
+    same number of warps (bf16 layers take multiples of 64)."""
+    c = Case(1237, d, dtype, res, gate="token", seed=d)
+    check_forward(occ, c, inplace=True)
+    check_backward(occ, c, inplace=True)
+    c = Case(700, d, dtype, res, pre=False, gate="channel", seed=d + 1)
+    check_forward(occ, c)
+    check_backward(occ, c)
