@@ -9,10 +9,12 @@
 // sums and gradients are fp32 throughout, counts are integers.
 //
 // Measured on one GB300, loss + gradient (added to what is there): 32768 tokens, 64
-// experts, top-8 10.0 + 3.7 us (the first launch 3.6 us, bound by two steps of loads;
+// experts, top-8 9.9 + 3.7 us (the first launch 3.6 us, bound by two steps of loads;
 // the second by its chain of sums in one CTA); 131072 tokens, 256 experts, masked, 32
 // sequences 35 + 56 us = 3.9 and 7.2 TB/s (the logits twice, the gradient in and out);
-// 256 tokens, 8 experts 4.7 + 1.7 us.
+// 256 tokens, 8 experts 3.8 + 1.5 us.
+#include <type_traits>
+
 #include "common.cuh"
 #include "kernels.h"
 
@@ -31,8 +33,11 @@ static_assert(kSumWarps <= 32 && kSumThreads >= OCCULT_MAX_EXPERTS,
 constexpr int kGradThreads = 256;
 // Tiles of a batch: two CTAs an SM where the groups have their own second passes, one
 // where a single CTA adds all of them up (11.2 us at 304 tiles, 10.3 at 152 for the loss
-// of 32768 tokens and 64 experts in one group; 36 against 63 us with 32 groups of 4096).
+// of 32768 tokens and 64 experts in one group; 36 against 63 us with 32 groups of 4096)
+// and the first pass is not long: 2^20 lanes of tokens (131072 tokens of 33 experts 16 us
+// at 304, 19 at 152, of 256 experts 38 and 49; half of that, 65536 of 64, 12.4 either way).
 constexpr int kMaxTiles = 304, kMaxTilesOne = 152;
+constexpr int64_t kManyLanes = 1 << 20;
 constexpr int kMinTile = 64;     // tokens
 
 // Workspace, in words: probability sums and counts [tiles][Ne], then for every tile
@@ -42,10 +47,10 @@ struct Tiles {
   int per_group, len;
   int64_t n;
 };
-__host__ __device__ inline Tiles tiles_of(int T, int L, int G) {
+__host__ __device__ inline Tiles tiles_of(int T, int L, int G, int lp) {
   const int tokens = T < L ? (T > 0 ? T : 1) : L;
   // as many tiles as keep every SM busy, at least kMinTile tokens each
-  int per = G == 1 ? kMaxTilesOne : kMaxTiles / G;
+  int per = G == 1 && static_cast<int64_t>(T) * lp < kManyLanes ? kMaxTilesOne : kMaxTiles / G;
   const int most = (tokens + kMinTile - 1) / kMinTile;
   per = per < 1 ? 1 : (per > most ? most : per);
   Tiles t;
@@ -74,9 +79,13 @@ __host__ __device__ inline Work work_of(float* ws, int64_t tiles, int Ne, int G)
 }
 
 // One token's row over LP lanes: lane s holds experts 4 (h LP + s) + i, h < 2, i < 4,
-// so that a row is read as consecutive 16-byte words (`vec`: rows are whole ones).
+// so that a row is read as consecutive 16-byte words (`vec`: rows are whole ones), or
+// experts j LP + s, j < 8, consecutive words (131072 x 255, loss + gradient: 39 + 64 us;
+// with the other order 54 + 73).
 template <int LP>
-__device__ __forceinline__ int expert_of(int sub, int j) { return 4 * ((j >> 2) * LP + sub) + (j & 3); }
+__device__ __forceinline__ int expert_of(int sub, int j, bool vec) {
+  return vec ? 4 * ((j >> 2) * LP + sub) + (j & 3) : j * LP + sub;
+}
 template <int LP>
 __device__ __forceinline__ void load_row(const float* row, int Ne, bool vec, int sub, float pad,
                                          float (&v)[8]) {
@@ -91,7 +100,7 @@ __device__ __forceinline__ void load_row(const float* row, int Ne, bool vec, int
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-      v[j] = expert_of<LP>(sub, j) < Ne ? row[expert_of<LP>(sub, j)] : pad;
+      v[j] = j * LP + sub < Ne ? row[j * LP + sub] : pad;
   }
 }
 __device__ __forceinline__ float2 two(float v) { return make_float2(v, v); }
@@ -214,7 +223,7 @@ __device__ __forceinline__ void sum_tile(const BalanceArgs& a, int64_t t0, int64
   }
   if (lane < LP)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x.p[warp][expert_of<LP>(lane, i)] = acc[i];
+    for (int i = 0; i < 8; ++i) x.p[warp][expert_of<LP>(lane, i, vec)] = acc[i];
   if (lane == 0) { x.sq[warp] = sq; x.n[warp] = n; }
   __syncthreads();
   for (int e = threadIdx.x; e < a.Ne; e += THREADS) {
@@ -529,13 +538,12 @@ __global__ void __launch_bounds__(kSumThreads) balance_groups_kernel(BalanceArgs
 // x 256 added to a gradient: 56 us = 7.2 TB/s, bound by memory (85 us with the gradient
 // read after the softmax and a 64-bit division a token).  Four CTAs an SM: three (the
 // registers it would take) 65 us, five (spills) 63 us.
-template <int LP>
+template <int LP, bool VEC>
 __global__ void __launch_bounds__(kGradThreads, 4) balance_grad_kernel(BalanceArgs a) {
   constexpr int kTok = 32 / LP;
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31, sub = lane % LP;
-  const bool vec = a.Ne % 4 == 0;
   const float up = a.dloss ? *a.dloss : 1.f;
   const float wz = a.grad_w[static_cast<size_t>(a.G) * a.Ne];
   const int64_t step = static_cast<int64_t>(gridDim.x) * (kGradThreads / 32) * kTok;
@@ -547,8 +555,8 @@ __global__ void __launch_bounds__(kGradThreads, 4) balance_grad_kernel(BalanceAr
   auto fetch = [&](int64_t b) {
     const int64_t t = b + lane / LP;
     const bool in = t < a.T;
-    load_row<LP>(a.logits + (in ? t : b) * a.Ne, a.Ne, vec, sub, minus_inf(), next);
-    if (a.accumulate) load_row<LP>(a.dlogits + (in ? t : b) * a.Ne, a.Ne, vec, sub, 0.f, next_old);
+    load_row<LP>(a.logits + (in ? t : b) * a.Ne, a.Ne, VEC, sub, minus_inf(), next);
+    if (a.accumulate) load_row<LP>(a.dlogits + (in ? t : b) * a.Ne, a.Ne, VEC, sub, 0.f, next_old);
     next_on = in && (!a.mask || a.mask[t]);
   };
 #pragma unroll
@@ -564,7 +572,7 @@ __global__ void __launch_bounds__(kGradThreads, 4) balance_grad_kernel(BalanceAr
     // (weights of a group's row: L1)
     const unsigned g = a.G == 1 ? 0u
                                 : static_cast<unsigned>(in ? t : b) / static_cast<unsigned>(a.L);
-    load_row<LP>(a.grad_w + static_cast<size_t>(g) * a.Ne, a.Ne, vec, sub, 0.f, w);
+    load_row<LP>(a.grad_w + static_cast<size_t>(g) * a.Ne, a.Ne, VEC, sub, 0.f, w);
     const float lse = softmax_row<LP>(v, &inv);
     float2 dot2 = two(0.f);
 #pragma unroll
@@ -584,7 +592,7 @@ __global__ void __launch_bounds__(kGradThreads, 4) balance_grad_kernel(BalanceAr
                                    __fadd2_rn(pair(w, i), two(shift)), pair(old, i));
       put(v, i, on ? dz : two(0.f));
     }
-    if (vec) {
+    if (VEC) {
 #pragma unroll
       for (int h = 0; h < 2; ++h)
         if (4 * (h * LP + sub) < a.Ne)
@@ -593,9 +601,27 @@ __global__ void __launch_bounds__(kGradThreads, 4) balance_grad_kernel(BalanceAr
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        if (expert_of<LP>(sub, i) < a.Ne) out[expert_of<LP>(sub, i)] = v[i];
+        if (i * LP + sub < a.Ne) out[i * LP + sub] = v[i];
     }
   }
+}
+
+// Lanes a token: eight of its experts and two of its slots each.  Loss + gradient, us with
+// eight lanes at least and so: 131072 tokens of 8 experts 16.4 + 9.7 and 8.8 + 2.6, of 24
+// experts 16.5 + 9.8 and 12.1 + 6.5, 256 of 8 experts 4.8 + 1.8 and 4.0 + 1.6.
+int lanes_of(int Ne, int k) {
+  int lp = 1;
+  while (lp < 32 && (8 * lp < Ne || 2 * lp < k)) lp *= 2;
+  return lp;
+}
+template <typename F>
+int with_lanes(int lp, F f) {
+  return lp == 1    ? f(std::integral_constant<int, 1>{})
+         : lp == 2  ? f(std::integral_constant<int, 2>{})
+         : lp == 4  ? f(std::integral_constant<int, 4>{})
+         : lp == 8  ? f(std::integral_constant<int, 8>{})
+         : lp == 16 ? f(std::integral_constant<int, 16>{})
+                    : f(std::integral_constant<int, 32>{});
 }
 
 }  // namespace
@@ -609,30 +635,28 @@ int balance_groups(int T, int group_len, int* L) {
 size_t balance_ws_bytes(const occult_desc_t& ds, int group_len) {
   int L;
   const int G = balance_groups(ds.T, group_len, &L);
-  const Tiles t = tiles_of(ds.T, L, G);
+  const Tiles t = tiles_of(ds.T, L, G, lanes_of(ds.n_experts, ds.top_k));
   return (static_cast<size_t>(t.n) * (2 * ds.n_experts + 2) + 3 * static_cast<size_t>(G) + 1) *
          sizeof(float);
 }
 
 int launch_balance_loss(const LaunchCtx& ctx, const BalanceArgs& a) {
-  const int lp = a.Ne <= 64 ? 8 : a.Ne <= 128 ? 16 : 32;
-  // One launch for a batch of one group: by one CTA for two steps of all its warps (128,
-  // 64 or 32 tokens each), by a cluster of 16 for four of each, two launches beyond that.
+  const int lp = lanes_of(a.Ne, a.k);
+  // One launch for a batch of one group: by one CTA for two steps of all its warps (1024 /
+  // lp tokens each), by a cluster of 16 for four of each, two launches beyond that.
   // 64 experts, us by one CTA, the cluster, two launches: 4.8, 5.4, 6.1 for 256 tokens,
   // -, 6.7, 7.1 for 4096, -, 8.4, 8.4 for 8192, -, 11.3, 9.1 for 16384.
   const int64_t steps = (static_cast<int64_t>(a.T) * lp + kOneThreads - 1) / kOneThreads;
   if (a.G == 1 && steps <= kClusterSteps * kCluster) {
     const int ctas = steps <= kOneSteps ? 1 : kCluster;
-    return lp == 8    ? launch_cluster<8>(ctx, a, ctas)
-           : lp == 16 ? launch_cluster<16>(ctx, a, ctas)
-                      : launch_cluster<32>(ctx, a, ctas);
+    return with_lanes(lp, [&](auto n) { return launch_cluster<decltype(n)::value>(ctx, a, ctas); });
   }
-  const Tiles tiles = tiles_of(a.T, a.L, a.G);
+  const Tiles tiles = tiles_of(a.T, a.L, a.G, lp);
   const dim3 grid(tiles.per_group, a.G < 65535 ? a.G : 65535);
-  const int rc = cuda_status(
-      lp == 8    ? launch_pdl(balance_tiles_kernel<8>, grid, kTileThreads, 0, ctx.stream, a, tiles)
-      : lp == 16 ? launch_pdl(balance_tiles_kernel<16>, grid, kTileThreads, 0, ctx.stream, a, tiles)
-                    : launch_pdl(balance_tiles_kernel<32>, grid, kTileThreads, 0, ctx.stream, a, tiles));
+  const int rc = with_lanes(lp, [&](auto n) {
+    return cuda_status(launch_pdl(balance_tiles_kernel<decltype(n)::value>, grid, kTileThreads, 0,
+                                  ctx.stream, a, tiles));
+  });
   if (rc) return rc;
   return cuda_status(launch_pdl(balance_groups_kernel, a.G < ctx.num_sms ? a.G : ctx.num_sms,
                                 kSumThreads, 0, ctx.stream, a, tiles));
@@ -640,13 +664,15 @@ int launch_balance_loss(const LaunchCtx& ctx, const BalanceArgs& a) {
 
 int launch_balance_grad(const LaunchCtx& ctx, const BalanceArgs& a) {
   if (a.T == 0) return OCCULT_OK;
-  const int tok = (a.Ne <= 64 ? 4 : a.Ne <= 128 ? 2 : 1) * (kGradThreads / 32);
+  const int lp = lanes_of(a.Ne, 1), tok = 32 / lp * (kGradThreads / 32);
   const int64_t need = (static_cast<int64_t>(a.T) + tok - 1) / tok;
   const int grid = static_cast<int>(need < ctx.num_sms * 16 ? need : ctx.num_sms * 16);
-  return cuda_status(
-      a.Ne <= 64    ? launch_pdl(balance_grad_kernel<8>, grid, kGradThreads, 0, ctx.stream, a)
-      : a.Ne <= 128 ? launch_pdl(balance_grad_kernel<16>, grid, kGradThreads, 0, ctx.stream, a)
-                    : launch_pdl(balance_grad_kernel<32>, grid, kGradThreads, 0, ctx.stream, a));
+  return with_lanes(lp, [&](auto n) {
+    constexpr int LP = decltype(n)::value;
+    return cuda_status(launch_pdl(a.Ne % 4 == 0 ? balance_grad_kernel<LP, true>
+                                                : balance_grad_kernel<LP, false>,
+                                  grid, kGradThreads, 0, ctx.stream, a));
+  });
 }
 
 }  // namespace occult

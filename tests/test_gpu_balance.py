@@ -241,3 +241,15 @@ def test_more_groups_than_a_grid_has_rows(occ):
     bal = float((one * (Ne / k) * p * on).sum() / on.sum())
     sq = float((lse.square() * on[:, 0]).sum() / on.sum())
     assert abs(float(loss[1]) - bal) <= SUM * bal and abs(float(loss[3]) - sq) <= SUM * sq
+
+
+@pytest.mark.parametrize("T,group_len", [(70000, 0), (5000, 1300)])
+@pytest.mark.parametrize("Ne,k", [(1, 1), (5, 2), (8, 2), (7, 7), (8, 5), (13, 2), (16, 4), (16, 16),
+                                  (20, 3), (31, 8), (32, 8), (33, 8), (37, 16), (100, 6), (130, 1),
+                                  (255, 16)])
+def test_every_number_of_lanes(occ, Ne, k, T, group_len):
+    """Experts and slots around what one to 32 lanes a token hold, whole rows of 16-byte
+    words and others, in two launches."""
+    z, ids = case(T, Ne, k, seed=Ne + k)
+    mask = np.random.default_rng(3).random(T) < 0.8
+    check(occ, z, ids, 1, group_len, mask)
