@@ -10,8 +10,8 @@
 //
 // Bound by the bytes: an element moves 30 with fp32 states, a bf16 parameter and its
 // master (28 for an fp32 parameter), 18 with 8-bit states and a master, 16 for an fp32
-// and 12 for a bf16 parameter alone.  Measured on one GB300, 402.8 M weights: 1723 us =
-// 7.0 TB/s, 1031 us = 7.0 TB/s, 943 us = 6.8 TB/s, and 852 us = 5.7 TB/s for the last,
+// and 12 for a bf16 parameter alone.  Measured on one GB300, 402.8 M weights: 1699 us =
+// 7.1 TB/s, 1025 us = 7.1 TB/s, 927 us = 7.0 TB/s, and 808 us = 6.0 TB/s for the last,
 // which takes 67 instructions an element, a dozen of them the correctly rounded root,
 // and most of the issue slots.  Moments, roots and parameters are fp32 until they are
 // stored.
@@ -29,6 +29,7 @@ constexpr int kAdamWarps = kAdamThreads / 32;
 constexpr int kBlock = OCCULT_STATE_BLOCK;       // elements of a warp's step
 constexpr int kMaxSteps = 2;                     // blocks of a warp at most
 constexpr int kMaxTensors = 256;                 // of one launch
+constexpr int kSpans = 127;                      // of CTAs, in the search for a CTA's tensor
 constexpr int64_t kOwnWeights = 1 << 25;         // of a kind, for a launch of its own
 
 enum : int { KIND_F32 = 0, KIND_MASTER = 1, KIND_BF16 = 2, KIND_ANY = 3 };
@@ -50,7 +51,9 @@ struct AdamTable {
   const float* grad_scale;
   int n;
   int cta_blocks;            // blocks of a CTA
-  int chunk0[kMaxTensors + 1];  // first CTA of every tensor
+  int span_log2;             // CTAs of a span
+  uint8_t span_first[kSpans + 1];  // tensor of a span's first CTA
+  int chunk0[kMaxTensors];   // first CTA of every tensor
   Tensor t[kMaxTensors];
 };
 
@@ -357,7 +360,7 @@ __device__ __forceinline__ void step_block(const AdamTable& a, const Tensor& T, 
 // The blocks blk, blk + kAdamWarps, ... below end of a tensor by one warp; with 8-bit
 // states the next block's words are on their way while this one's are worked on (without
 // that 1139 us where it takes 940), for a bf16 parameter without a master, whose words are
-// few, both blocks' from the start (852 against 962 us; with a master 1273 against 1040).
+// few, both blocks' from the start (a tenth faster; with a master 1273 against 1040).
 template <int BITS, int KIND>
 __device__ __forceinline__ void step_blocks(const AdamTable& a, const Tensor& T, int64_t blk,
                                             int64_t end, float gs) {
@@ -391,8 +394,8 @@ __device__ __forceinline__ void step_blocks(const AdamTable& a, const Tensor& T,
 }
 
 // CTAs of an SM: eight, nine for the kind that the issue rate bounds (64 bytes of stack a
-// thread for the spills, and 852 us where eight CTAs take 880, ten 887); nine cost the
-// other two with 8-bit states more than they give (1087 against 1031 us with masters).
+// thread for the spills, and 811 us where eight CTAs take 830, ten 832); nine cost the
+// other two with 8-bit states more than they give (with masters 5 %).
 __host__ __device__ constexpr int adam_ctas(int bits, int kind) {
   return bits == 8 && kind == KIND_BF16 ? 9 : 8;
 }
@@ -401,16 +404,20 @@ __global__ void __launch_bounds__(kAdamThreads, adam_ctas(BITS, KIND))
 adamw_kernel(const __grid_constant__ AdamTable a) {
   pdl_wait();
   pdl_trigger();
-  // the tensor of this CTA: the one whose CTAs include it (all looked at at once)
-  __shared__ int s_which;
-  for (int i = threadIdx.x; i < a.n; i += kAdamThreads)
-    if (a.chunk0[i] <= static_cast<int>(blockIdx.x) &&
-        (i + 1 == a.n || a.chunk0[i + 1] > static_cast<int>(blockIdx.x)))
-      s_which = i;
-  __syncthreads();
-  const Tensor T = a.t[s_which];
+  // the tensor of this CTA: the last that begins at or before it, between those of the
+  // ends of its span of CTAs.  (Each thread looking at its share of the table, whose
+  // lines then come one by one, and a sync: 200 tensors of 0.5 M fp32 weights 6.9 us, now
+  // 3.3, of 315 M bf16 ones with 8-bit states 764, now 643 us.)
+  const int cta = static_cast<int>(blockIdx.x), span = cta >> a.span_log2;
+  int which = a.span_first[span], last = a.span_first[span + 1];
+  while (which < last) {
+    const int mid = (which + last + 1) >> 1;
+    if (a.chunk0[mid] <= cta) which = mid;
+    else last = mid - 1;
+  }
+  const Tensor T = a.t[which];
   const float gs = a.grad_scale ? *a.grad_scale : 1.f;
-  const int64_t blk0 = static_cast<int64_t>(blockIdx.x - a.chunk0[s_which]) * a.cta_blocks;
+  const int64_t blk0 = static_cast<int64_t>(cta - a.chunk0[which]) * a.cta_blocks;
   const int64_t n_blk = (T.n + kBlock - 1) / kBlock;
   const int64_t end = n_blk < blk0 + a.cta_blocks ? n_blk : blk0 + a.cta_blocks;
   const int64_t mine = blk0 + (threadIdx.x >> 5);
@@ -485,10 +492,11 @@ int launch_adamw(const LaunchCtx& ctx, const occult_adamw_t& o, const occult_par
   a.eps = static_cast<float>(o.eps);
   a.key = mix(o.seed + mix(static_cast<uint32_t>(o.step)));
   a.grad_scale = o.grad_scale;
-  // Two blocks a warp, which share a CTA's search for its tensor and its first loads' wait,
-  // where that leaves four CTAs for each place on the GPU; one for smaller sets.  With four
-  // the CTAs' streams lie too far apart: one, two, four blocks took 1075, 977, 962 us with
-  // 8-bit states alone and 1119, 1046, 1178 us with a master.
+  // With 8-bit states two blocks a warp, whose loads and arithmetic overlap, where that
+  // leaves four CTAs for each place on the GPU; one for smaller sets and for 32-bit states,
+  // which wait for memory alone.  One, two, three blocks took, us for 402.8 M weights: bf16
+  // alone with 8-bit states 1030, 808, 937, with masters 1057, 1025, 1206 (the CTAs' streams
+  // lie too far apart then); with fp32 states and masters 1699, 1711 (two).
   int64_t blocks = 0, of_kind[3] = {0, 0, 0};
   for (int k = 0; k < n_params; ++k) {
     const int64_t b = (params[k].n + kBlock - 1) / kBlock;
@@ -496,14 +504,14 @@ int launch_adamw(const LaunchCtx& ctx, const occult_adamw_t& o, const occult_par
     of_kind[kind_of(params[k])] += b;
   }
   int64_t steps = blocks / (static_cast<int64_t>(kAdamWarps) * 4 * 8 * ctx.num_sms);
-  steps = steps < 1 ? 1 : (steps > kMaxSteps ? kMaxSteps : steps);
+  steps = steps < 1 || o.state_bits == 32 ? 1 : (steps > kMaxSteps ? kMaxSteps : steps);
   a.cta_blocks = kAdamWarps * static_cast<int>(steps);
   const int64_t chunk = static_cast<int64_t>(a.cta_blocks) * kBlock;
   // A kernel of its own for a kind of 2^25 weights and more, or where there is no other;
-  // the rest go together.  Own registers save 402.8 M weights 55 us (bf16 alone with 8-bit
-  // states) or 25 us (masters and fp32 states); a launch more costs 3 to 5 us, and 60
-  // tensors of three kinds and 2560 weights each take 5 us in one, 11 us in three launches,
-  // of 2^20 each with 8-bit states 161 and 169 us.
+  // the rest go together.  Own registers save 402.8 M weights 23 us (bf16 alone with 8-bit
+  // states, or masters and fp32 states); a launch more costs 2 to 3 us, and 60 tensors of
+  // three kinds and 2560 weights each take 5 us in one, 12 us in three launches, of 2^20
+  // each with 8-bit states 152 and 161 us.
   bool own[4];
   own[KIND_ANY] = true;
   for (int k = 0; k < KIND_ANY; ++k)
@@ -529,6 +537,12 @@ int launch_adamw(const LaunchCtx& ctx, const occult_adamw_t& o, const occult_par
       }
       if (a.n == 0) break;
       const unsigned grid = static_cast<unsigned>(chunks);
+      a.span_log2 = 0;
+      while (((grid - 1) >> a.span_log2) >= kSpans) ++a.span_log2;
+      for (int s = 0, k = 0; s <= kSpans; ++s) {  // tensors of the spans' first CTAs
+        while (k + 1 < a.n && a.chunk0[k + 1] <= static_cast<int64_t>(s) << a.span_log2) ++k;
+        a.span_first[s] = static_cast<uint8_t>(k);
+      }
       const cudaError_t e = o.state_bits == 32 ? launch<32>(ctx, kind, a, grid)
                                                : launch<8>(ctx, kind, a, grid);
       if (e != cudaSuccess) return OCCULT_ERR_CUDA;

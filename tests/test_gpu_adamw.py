@@ -356,3 +356,32 @@ def test_a_tensor_steps_the_same_beside_others(occ, bits, large):
     for a, b in zip(together, alone):
         for k in a:
             assert torch.equal(a[k], b[k]) if isinstance(a[k], torch.Tensor) else a[k] == b[k], k
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("many", [1, 150, 256])
+def test_every_cta_finds_its_tensor(occ, bits, many):
+    """Tensors of a block next to ones of thousands, in every order: a launch of more
+    CTAs than its search has spans, against each tensor alone."""
+    sizes = [1 + 300 * (i % 5) for i in range(many)] + [5000000]
+    for order in (sizes, sizes[::-1], sizes[::2] + sizes[1::2][::-1]):
+        order = order[-256:]
+        gen = torch.Generator(device="cuda").manual_seed(many)
+        st = torch.float32 if bits == 32 else torch.uint8
+        together = []
+        for i, n in enumerate(order):
+            t = dict(param=torch.randn(n, generator=gen, device="cuda").to(torch.bfloat16),
+                     grad=torch.randn(n, generator=gen, device="cuda"), first=i * 7,
+                     m=torch.zeros(n, dtype=st, device="cuda"),
+                     v=torch.zeros(n, dtype=st, device="cuda"))
+            if bits == 8:
+                t.update({k: torch.zeros(-(-n // 256), dtype=torch.uint8, device="cuda")
+                          for k in ("m_exp", "v_exp")})
+            together.append(t)
+        alone = [{k: x.clone() if isinstance(x, torch.Tensor) else x for k, x in t.items()}
+                 for t in together]
+        step(occ, together, 1, bits)
+        for x in alone:
+            step(occ, [x], 1, bits)
+        for a, b in zip(together, alone):
+            assert all(torch.equal(a[k], b[k]) for k in a if k != "first")
