@@ -27,7 +27,8 @@ namespace {
 constexpr int kAdamThreads = 128;
 constexpr int kAdamWarps = kAdamThreads / 32;
 constexpr int kBlock = OCCULT_STATE_BLOCK;       // elements of a warp's step
-constexpr int kMaxSteps = 2;                     // blocks of a warp at most
+constexpr int kCtaLog2 = 10;                     // log2 of the weights of kAdamWarps blocks
+static_assert(kAdamWarps * kBlock == 1 << kCtaLog2, "a CTA's weights");
 constexpr int kMaxTensors = 256;                 // of one launch
 constexpr int kSpans = 127;                      // of CTAs, in the search for a CTA's tensor
 constexpr int64_t kOwnWeights = 1 << 25;         // of a kind, for a launch of its own
@@ -503,21 +504,19 @@ int launch_adamw(const LaunchCtx& ctx, const occult_adamw_t& o, const occult_par
     blocks += b;
     of_kind[kind_of(params[k])] += b;
   }
-  int64_t steps = blocks / (static_cast<int64_t>(kAdamWarps) * 4 * 8 * ctx.num_sms);
-  steps = steps < 1 || o.state_bits == 32 ? 1 : (steps > kMaxSteps ? kMaxSteps : steps);
-  a.cta_blocks = kAdamWarps * static_cast<int>(steps);
-  const int64_t chunk = static_cast<int64_t>(a.cta_blocks) * kBlock;
+  const bool two = o.state_bits == 8 && blocks >= static_cast<int64_t>(kAdamWarps) * 2 * 4 * 8 * ctx.num_sms;
+  a.cta_blocks = kAdamWarps << two;
+  const int chunk_log2 = kCtaLog2 + two;  // weights of a CTA (no division: the host's time counts)
   // A kernel of its own for a kind of 2^25 weights and more, or where there is no other;
   // the rest go together.  Own registers save 402.8 M weights 23 us (bf16 alone with 8-bit
   // states, or masters and fp32 states); a launch more costs 2 to 3 us, and 60 tensors of
   // three kinds and 2560 weights each take 5 us in one, 12 us in three launches, of 2^20
   // each with 8-bit states 152 and 161 us.
-  bool own[4];
-  own[KIND_ANY] = true;
+  bool own[3];
   for (int k = 0; k < KIND_ANY; ++k)
-    own[k] = of_kind[k] == blocks || of_kind[k] >= kOwnWeights / kBlock;
+    own[k] = of_kind[k] == blocks || of_kind[k] >= kOwnWeights / kBlock || of_kind[k] == 0;
   for (int kind = KIND_F32; kind <= KIND_ANY; ++kind) {
-    if (!own[kind]) continue;
+    if (kind == KIND_ANY ? own[0] && own[1] && own[2] : !own[kind] || of_kind[kind] == 0) continue;
     int i = 0;
     while (i < n_params) {
       a.n = 0;
@@ -526,7 +525,7 @@ int launch_adamw(const LaunchCtx& ctx, const occult_adamw_t& o, const occult_par
         const occult_param_t& p = params[i];
         const int its = kind_of(p);
         if (p.n == 0 || (own[its] ? its : KIND_ANY) != kind) continue;
-        const int64_t c = (p.n + chunk - 1) / chunk;
+        const int64_t c = ((p.n - 1) >> chunk_log2) + 1;
         if (chunks + c > 0x7fffffff) {
           if (a.n > 0) break;
           return OCCULT_ERR_UNSUPPORTED;

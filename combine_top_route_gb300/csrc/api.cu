@@ -814,9 +814,9 @@ static int check_norm(const occult_desc_t* desc, const occult_norm_t* opt, const
   return OCCULT_OK;
 }
 static bool aligned16(std::initializer_list<const void*> ps) {
-  for (const void* p : ps)
-    if (reinterpret_cast<uintptr_t>(p) % 16 != 0) return false;
-  return true;
+  uintptr_t bits = 0;
+  for (const void* p : ps) bits |= reinterpret_cast<uintptr_t>(p);
+  return bits % 16 == 0;
 }
 
 int occult_block_norm(const occult_desc_t* desc, const occult_norm_t* opt, const void* r,
