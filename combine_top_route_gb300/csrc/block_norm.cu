@@ -571,9 +571,12 @@ norm_bwd_rows_kernel(NormArgs a, bool sums, float* part, int stages, int* dev_er
     const float* s_y = s_dx + d;
     const R* s_up = reinterpret_cast<const R*>(s_y + d);
     const R* s_r = s_up + d;
-    // with D0 = dr_out + rstd_pre w_pre dx:  sum w_pre dx r',  sum wq y D0,  sum wq y r'
+    // with D0 = dr_out + rstd_pre w_pre dx:  sum w_pre dx n,  sum wq m D0,  sum wq m n
+    // (rows read twice: of r' and y, the factors follow).  A factor of a row meets the
+    // row's values or their sums before it meets itself: products of factors alone leave
+    // fp32's range (rows of 1e13, zero rows at a small eps) where n, m and means do not.
     float2 sx = two(0.f), sy = two(0.f), sz = two(0.f);
-    float4 k_dx[KEEP], k_r[KEEP], k_y[KEEP], k_D[KEEP];
+    float4 k_dx[KEEP], k_n[KEEP], k_m[KEEP], k_D[KEEP];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int c = 4 * (u * 32 * G + place);
@@ -582,17 +585,19 @@ norm_bwd_rows_kernel(NormArgs a, bool sums, float* part, int stages, int* dev_er
       if (w_pre) {
         dx = ld4(s_dx + c);
         r = ld4(s_r + c);
+        if (kKeep) r = pscale4(r, rq);  // n
         const float4 g = pmul4(dx, kHold ? held_p[kHold ? u : 0] : load_wp(c));
         D = pfma4(g, rq, D);
         sx = pdot(g, r, sx);
       }
       if (use_y) {
         y = ld4(s_y + c);
+        if (kKeep) y = pscale4(y, rp);  // m
         const float4 q = pmul4(y, kHold ? held_q[kHold ? u : 0] : load_wq(c));
         sy = pdot(q, D, sy);
         sz = pdot(q, r, sz);
       }
-      if (kKeep) { k_dx[u % KEEP] = dx; k_r[u % KEEP] = r; k_y[u % KEEP] = y; k_D[u % KEEP] = D; }
+      if (kKeep) { k_dx[u % KEEP] = dx; k_n[u % KEEP] = r; k_m[u % KEEP] = y; k_D[u % KEEP] = D; }
     }
     float4 sum = make_float4(sx.x + sx.y, sy.x + sy.y, sz.x + sz.y, 0.f);
     sum = group_sum<G>(sum, use_y, s_red[flip]);
@@ -609,11 +614,12 @@ norm_bwd_rows_kernel(NormArgs a, bool sums, float* part, int stages, int* dev_er
       fill(stage == 0 ? stages - 1 : stage - 1,
            static_cast<int>(t + static_cast<int64_t>(stages - 1) * step));
     }
-    // mean(w_pre dx n) = rstd_pre sum.x / d;  sum wq m D and its mean
-    const float k1 = -rq * rq * rq * sum.x * inv_d;
-    const float qd = rp * fmaf(k1, sum.z, sum.y);
+    // mean(w_pre dx n); sum wq m D and its mean
+    const float fr = kKeep ? 1.f : rq, fy = kKeep ? 1.f : rp;
+    const float k1 = -rq * (fr * sum.x * inv_d);
+    const float qd = fy * fmaf(k1, fr * sum.z, sum.y);
     if (token && place == 0) a.dgate[t] = qd;
-    const float k2 = -rp * rp * tok * qd * inv_d;
+    const float k2 = -rp * (qd * inv_d);
     const float ru = rp * tok;
     const size_t base = static_cast<size_t>(t) * d;
 #pragma unroll
@@ -623,18 +629,19 @@ norm_bwd_rows_kernel(NormArgs a, bool sums, float* part, int stages, int* dev_er
       float4 D = kKeep ? k_D[u % KEEP] : a.dr_out ? ld4(s_up + c) : zero;
       if (w_pre) {
         const float4 dx = kKeep ? k_dx[u % KEEP] : ld4(s_dx + c);
-        const float4 r = kKeep ? k_r[u % KEEP] : ld4(s_r + c);
         if (!kKeep) D = pfma4(pmul4(dx, kHold ? held_p[kHold ? u : 0] : load_wp(c)), rq, D);
-        D = pfma4(r, k1, D);
-        sum_pre[u] = pfma4(dx, pscale4(r, rq), sum_pre[u]);
+        const float4 n = kKeep ? k_n[u % KEEP] : pscale4(ld4(s_r + c), rq);
+        D = pfma4(n, k1, D);
+        sum_pre[u] = pfma4(dx, n, sum_pre[u]);
       }
       st4(static_cast<R*>(a.dr) + base + c, pscale4(D, out_scale));
       if (!a.y) continue;
       float4 o = pscale4(pmul4(D, kHold ? held_q[kHold ? u : 0] : load_wq(c)), ru);
       if (use_y) {
-        const float4 y = kKeep ? k_y[u % KEEP] : ld4(s_y + c);
-        sum_post[u] = pfma4(D, pscale4(y, ru), sum_post[u]);
-        if (w_post) o = pfma4(y, k2, o);
+        float4 m = kKeep ? k_m[u % KEEP] : pscale4(ld4(s_y + c), ru);  // times the gate
+        if (kKeep && token) m = pscale4(m, tok);
+        sum_post[u] = pfma4(D, m, sum_post[u]);
+        if (w_post) o = pfma4(m, k2, o);
       }
       st4(static_cast<L*>(a.dy) + base + c, o);
     }

@@ -466,3 +466,56 @@ def test_every_width_of_many_rows(occ, d, dtype, res):
     c = Case(700, d, dtype, res, pre=False, gate="channel", seed=d + 1)
     check_forward(occ, c)
     check_backward(occ, c)
+
+
+@pytest.mark.parametrize("d,dtype", [(64, "f32"), (64, "bf16"), (1408, "bf16"), (2048, "bf16"),
+                                     (2304, "bf16"), (4096, "f32"), (8256, "f32"), (16384, "f32"),
+                                     (36, "f32")])
+@pytest.mark.parametrize("kr,ky,kg", [(50, 50, 0), (-50, -50, 0), (57, 0, -40), (0, 50, -40)])
+def test_backward_scales_exactly_with_its_rows(occ, d, dtype, kr, ky, kg):
+    """r' times 2^kr, y times 2^ky and dx times 2^kg, the row factors with them: every
+    product and sum of the definition is then the same but for a power of two, so that
+    nothing but the exponents of the gradients may change, to the last bit.  Magnitudes of
+    2^50 = 1e15 and more: the cube of a row's factor is no fp32 number there, though the
+    gradients (at least 2^-101 times ones of about one, 2^25 above the least normal
+    number) are."""
+    T = 37
+    c = Case(T, d, dtype, "f32" if dtype == "f32" else "bf16", gate="token", seed=d)
+    ds, opt = c.desc(occ), c.opt(occ)
+    ws = torch.empty(occ.workspace_size(ds, occ.WS_BLOCK_NORM_BWD), dtype=torch.uint8, device="cuda")
+    factor = lambda v: dev(rounded(onorm.rstd(v, 0.0), "f32"), "f32")  # noqa: E731
+    rq, rp = factor(c.r), factor(c.y)
+
+    def run(kr, ky, kg):
+        o = {k: torch.empty(T, d, dtype=DT[c.res if k == "dr" else c.dtype], device="cuda")
+             for k in ("dr", "dy")}
+        o.update({k: torch.empty(n, device="cuda") for k, n in (("dw_post", d), ("dgate", T),
+                                                                ("dw_pre", d))})
+        occ.occult_block_norm_bwd(
+            ds, opt, None, dev(c.r * 2.0 ** kr, c.res), o["dr"], ws, dx=dev(c.dx * 2.0 ** kg, "f32"),
+            y=dev(c.y * 2.0 ** ky, "f32"), w_post=dev(c.w_post, c.dtype), gate=dev(c.g, "f32"),
+            w_pre=dev(c.w_pre, c.dtype), rstd_post=rp * 2.0 ** -ky, rstd_pre=rq * 2.0 ** -kr,
+            dy=o["dy"], dw_post=o["dw_post"], dgate=o["dgate"], dw_pre=o["dw_pre"])
+        torch.cuda.synchronize()
+        return {k: t.double() for k, t in o.items()}
+
+    base, got = run(0, 0, 0), run(kr, ky, kg)
+    D = kg - kr                    # of D; dy has y's factor besides, dw_pre only that of dx
+    for k, e in (("dr", D), ("dy", D - ky), ("dw_post", D), ("dgate", D), ("dw_pre", kg)):
+        want = base[k] * 2.0 ** e
+        assert want.isfinite().all() and torch.equal(got[k], want), \
+            (k, float((got[k] - want).abs().max() / want.abs().max()))
+
+
+@pytest.mark.parametrize("d", [64, 2048, 2304, 4096, 16384])
+@pytest.mark.parametrize("eps,both", [(1e-26, True), (1e-30, True), (1e-40, False)])
+def test_backward_of_zero_rows_at_a_small_eps(occ, d, eps, both, monkeypatch):
+    """A zero row has the factor eps^(-1/2), and finite gradients: the means over it are 0.
+    (Where both norms see zeros dy has both factors: 1e40 at the least eps.)"""
+    monkeypatch.setitem(globals(), "EPS", eps)
+    for gate in ("token", "channel"):
+        c = Case(20, d, "f32", "f32", gate=gate, seed=15)
+        c.y[7] = 0
+        if both:
+            c.y[3], c.r[3] = 0, 0
+        check_backward(occ, c)
