@@ -152,14 +152,16 @@ class OccultBlock:
     def forward(self, r: torch.Tensor, mask: Optional[torch.Tensor] = None) -> torch.Tensor:
         """r' [T, d] for the residual stream r; the auxiliary losses in ``self.losses``
         ({weighted total, expert, device, z}), the experts' loads in ``self.counts``.
-        ``mask`` (uint8 [T]): tokens with 0 take no part in the losses."""
+        ``mask`` (uint8 [T]): tokens with 0 take no part in the losses.  Under pruning
+        that puts other experts in the place of some the router chose, losses and loads
+        are of the experts that run."""
         ds, moe = self.desc, self.moe
         self.r, self.mask = r, mask
         occult_block_norm(ds, self.pre_opt, r, w_pre=self.w_pre, x=self.x, rstd_pre=self.rstd_pre)
         self.x32 = self.x.float()
         torch.mm(self.x32, self.w_router.t(), out=self.logits)
         y = moe.forward(self.logits, self.x)
-        occult_balance_loss(ds, self.bal_opt, self.logits, moe.routed, moe.expert_to_vdev,
+        occult_balance_loss(ds, self.bal_opt, self.logits, moe.ids, moe.expert_to_vdev,
                             self.counts, self.grad_w, self.losses, self.bal_ws, mask=mask)
         occult_block_norm(ds, self.post_opt, r, y=y, w_post=self.w_post, gate=self.gate,
                           r_out=self.r_out, rstd_post=self.rstd_post)

@@ -145,3 +145,32 @@ def test_optimizer_updates_every_parameter(occ):
         occ.OccultAdamW([before[0]], [], lr=1e-3)
     with pytest.raises(ValueError):
         occ.OccultAdamW([before[0]], [before[0].float()], lr=1e-3, state_bits=16)
+
+
+@pytest.mark.parametrize("masked", [False, True])
+def test_loads_under_pruning_are_those_the_layer_carries(occ, masked):
+    """Similarity-based pruning puts other experts in the place of some that the router
+    chose: counts, losses and the losses' gradient are of the experts that run.  (Counts
+    exact; sums of positive terms within 1100 units of fp32, 7e-5, of themselves, and a
+    gradient within 1e-4 of its largest element, as no term of it is larger.)"""
+    from oracle import balance as obal
+    cfg = config().with_(route_mode="similarity_pruned", limit_devices=1, n_clusters=2)
+    g = torch.Generator(device="cuda").manual_seed(5)
+    placement = torch.arange(cfg.n_experts, dtype=torch.int32).view(cfg.n_vdev, -1)
+    block = occ.OccultBlock(occ.desc_for(cfg), synth.expert_weights(cfg, device="cuda"), placement,
+                            0.3 * torch.randn(cfg.n_experts, cfg.d, generator=g, device="cuda"),
+                            balance=(0.3, 0.2, 0.1), group_len=100,
+                            sim_table=synth.random_similarity_table(cfg))
+    r = torch.randn(cfg.T, cfg.d, generator=g, device="cuda").bfloat16()
+    mask = (torch.rand(cfg.T, generator=g, device="cuda") < 0.8).to(torch.uint8) if masked else None
+    block.forward(r, mask)
+    block.backward(torch.zeros_like(r))      # what is left in dlogits is the losses' gradient
+    torch.cuda.synchronize()
+    assert not torch.equal(block.moe.ids, block.moe.routed)
+    host = lambda t: None if t is None else t.cpu().numpy()  # noqa: E731
+    loss, counts, grad = obal.loss_and_grad(
+        host(block.logits), host(block.moe.ids), host(block.moe.expert_to_vdev), cfg.n_vdev, 100,
+        host(mask), coef=0.3, coef_dev=0.2, coef_z=0.1)
+    assert (host(block.counts) == counts).all()
+    np.testing.assert_allclose(host(block.losses), loss, rtol=1e-4)
+    assert np.abs(host(block.moe.dlogits) - grad).max() <= 1e-4 * np.abs(grad).max()
