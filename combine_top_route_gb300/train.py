@@ -28,6 +28,13 @@ from . import (GATE_CHANNEL, GATE_NONE, OCCULT_BF16, OCCULT_F32, STATE_BLOCK, ST
 from .pipeline import OccultMoE
 
 
+def _torch_stream(stream):
+    """torch's object for a stream given as one, as a handle, or not at all (None)."""
+    if stream is None or isinstance(stream, torch.cuda.Stream):
+        return stream
+    return torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)))
+
+
 class OccultAdamW:
     """AdamW over tensors of one device, its states in fp32 or in 8 bits.
 
@@ -78,15 +85,17 @@ class OccultAdamW:
         occult_adamw(self.opt, self.table, stream)
 
     def moments(self, i: int, stream=None):
-        """(m, v) of parameter ``i`` in fp32, as its state holds them."""
+        """(m, v) of parameter ``i`` in fp32, as its state holds them; all of it on
+        ``stream``, behind the steps there."""
         s = self.states[i]
-        if self.opt.state_bits == 32:
-            return s["m"].clone(), s["v"].clone()
-        out = [torch.empty(s["m"].numel(), dtype=torch.bfloat16, device=s["m"].device)
-               for _ in range(2)]
-        occult_adamw_read(s["m"], s["m_exp"], STATE_M, out[0], stream)
-        occult_adamw_read(s["v"], s["v_exp"], STATE_V, out[1], stream)
-        return out[0].float(), out[1].float().square()
+        with torch.cuda.stream(_torch_stream(stream)):
+            if self.opt.state_bits == 32:
+                return s["m"].clone(), s["v"].clone()
+            out = [torch.empty(s["m"].numel(), dtype=torch.bfloat16, device=s["m"].device)
+                   for _ in range(2)]
+            occult_adamw_read(s["m"], s["m_exp"], STATE_M, out[0])
+            occult_adamw_read(s["v"], s["v_exp"], STATE_V, out[1])
+            return out[0].float(), out[1].float().square()
 
 
 class OccultBlock:

@@ -174,3 +174,26 @@ def test_loads_under_pruning_are_those_the_layer_carries(occ, masked):
     assert (host(block.counts) == counts).all()
     np.testing.assert_allclose(host(block.losses), loss, rtol=1e-4)
     assert np.abs(host(block.moe.dlogits) - grad).max() <= 1e-4 * np.abs(grad).max()
+
+
+@pytest.mark.parametrize("state_bits", [32, 8])
+@pytest.mark.parametrize("raw", [False, True])
+def test_moments_are_read_behind_the_steps_of_their_stream(occ, state_bits, raw):
+    """Steps and read-out on a side stream that still has other work before them."""
+    g = torch.Generator(device="cuda").manual_seed(2)
+    p = torch.randn(70000, generator=g, device="cuda").bfloat16()
+    grad = torch.randn(70000, generator=g, device="cuda")
+    opt = occ.OccultAdamW([p], [grad], lr=1e-3, state_bits=state_bits)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(50_000_000)        # some 30 ms
+    on = s.cuda_stream if raw else s
+    opt.step(stream=on)
+    m, v = opt.moments(0, stream=on)
+    s.synchronize()
+    want_m, want_v = opt.moments(0)
+    torch.cuda.synchronize()
+    assert torch.equal(m, want_m) and torch.equal(v, want_v)
+    # (and they are a first step's: (1 - beta1) g within a code's unit)
+    assert ((m - 0.1 * grad).abs() <= 0.13 * (0.1 * grad).abs() + 1e-4).all()
