@@ -77,12 +77,17 @@ class OccultAdamW:
         if grad_scale is not None and (grad_scale.dtype != torch.float32
                                        or not grad_scale.is_cuda or grad_scale.numel() < 1):
             raise ValueError("grad_scale must be a float32 CUDA tensor")
-        self._scale = grad_scale  # alive until the next step
-        self.opt.grad_scale = None if grad_scale is None else grad_scale.data_ptr()
+        opt, before = self.opt, (self.opt.grad_scale, self.opt.lr, self.opt.step)
+        opt.grad_scale = None if grad_scale is None else grad_scale.data_ptr()
         if lr is not None:
-            self.opt.lr = lr
-        self.opt.step += 1
-        occult_adamw(self.opt, self.table, stream)
+            opt.lr = lr
+        opt.step += 1
+        try:
+            occult_adamw(opt, self.table, stream)
+        except Exception:
+            opt.grad_scale, opt.lr, opt.step = before  # a refused step is none
+            raise
+        self._scale = grad_scale  # alive until the next step
 
     def moments(self, i: int, stream=None):
         """(m, v) of parameter ``i`` in fp32, as its state holds them; all of it on

@@ -180,3 +180,13 @@ def test_packed_record_is_the_struct(occ):
     occ._RECORD.pack_into(rec, 0, *vals)
     got = [getattr(rec, n) for n, _ in rec._fields_]
     assert got == vals
+
+
+@pytest.mark.parametrize("kw", [dict(lr=float("inf")), dict(lr=float("nan"))])
+def test_a_refused_step_is_not_counted(occ, kw):
+    """The step's number (of the bias corrections and the draws) and the rate stay."""
+    opt = occ.OccultAdamW([], [], lr=1e-3)
+    opt.opt.step = 7
+    with pytest.raises(occ.OccultError):
+        opt.step(stream=0, **kw)
+    assert opt.opt.step == 7 and opt.opt.lr == 1e-3 and opt.opt.grad_scale is None
