@@ -87,7 +87,9 @@ class OccultAdamW:
         except Exception:
             opt.grad_scale, opt.lr, opt.step = before  # a refused step is none
             raise
-        self._scale = grad_scale  # alive until the next step
+        self._scale = grad_scale  # alive until the next step, on the device until this one ran
+        if grad_scale is not None:
+            grad_scale.record_stream(_torch_stream(stream) or torch.cuda.current_stream())
 
     def moments(self, i: int, stream=None):
         """(m, v) of parameter ``i`` in fp32, as its state holds them; all of it on

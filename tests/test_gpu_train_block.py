@@ -197,3 +197,30 @@ def test_moments_are_read_behind_the_steps_of_their_stream(occ, state_bits, raw)
     assert torch.equal(m, want_m) and torch.equal(v, want_v)
     # (and they are a first step's: (1 - beta1) g within a code's unit)
     assert ((m - 0.1 * grad).abs() <= 0.13 * (0.1 * grad).abs() + 1e-4).all()
+
+
+@pytest.mark.parametrize("raw", [False, True])
+def test_a_factor_of_the_gradients_outlives_its_step(occ, raw):
+    """Factors dropped by the host while a busy side stream has yet to read them: their
+    memory goes to nothing that the current stream writes meanwhile."""
+    p = torch.zeros(4096, device="cuda")
+    grad = torch.ones(4096, device="cuda")
+    opt = occ.OccultAdamW([p], [grad], lr=1e-3)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(50_000_000)        # some 30 ms
+    m = 0.0
+    for i in range(8):
+        factor = torch.empty(1, device="cuda")
+        with torch.cuda.stream(s):
+            factor.fill_(2.0 ** i)           # written and read behind the other work
+        opt.step(grad_scale=factor, stream=s.cuda_stream if raw else s)
+        m = 0.9 * m + 0.1 * 2.0 ** i
+        del factor
+    torch.zeros(64, 1, device="cuda")
+    keep = [torch.zeros(1, device="cuda") for _ in range(64)]
+    s.synchronize()
+    assert len(keep) == 64
+    got = opt.states[0]["m"]
+    assert ((got - m).abs() <= 1e-6 * m).all()
