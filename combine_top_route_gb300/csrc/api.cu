@@ -813,11 +813,12 @@ static int check_norm(const occult_desc_t* desc, const occult_norm_t* opt, const
   OCCULT_REQUIRE(y ? true : (!w_post && !gate && w_pre));
   return OCCULT_OK;
 }
-static bool aligned16(std::initializer_list<const void*> ps) {
+static bool aligned(int bytes, std::initializer_list<const void*> ps) {
   uintptr_t bits = 0;
   for (const void* p : ps) bits |= reinterpret_cast<uintptr_t>(p);
-  return bits % 16 == 0;
+  return bits % bytes == 0;
 }
+static bool aligned16(std::initializer_list<const void*> ps) { return aligned(16, ps); }
 
 int occult_block_norm(const occult_desc_t* desc, const occult_norm_t* opt, const void* r,
                       const float* y, const void* w_post, const float* gate, const void* w_pre,
@@ -932,7 +933,7 @@ int occult_balance_grad(const occult_desc_t* desc, const occult_balance_t* opt,
   if (rc) return rc;
   OCCULT_REQUIRE(accumulate == 0 || accumulate == 1);
   OCCULT_REQUIRE(desc->T == 0 || (logits && grad_w && dlogits));
-  OCCULT_REQUIRE(aligned16({logits, grad_w, dlogits}));
+  OCCULT_REQUIRE(aligned16({logits, dlogits}) && aligned(4, {grad_w}));
   OCCULT_CTX(stream);
   BalanceArgs a = balance_args(desc, opt, logits, mask);
   a.grad_w = const_cast<float*>(grad_w);

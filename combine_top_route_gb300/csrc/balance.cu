@@ -667,10 +667,12 @@ int launch_balance_grad(const LaunchCtx& ctx, const BalanceArgs& a) {
   const int lp = lanes_of(a.Ne, 1), tok = 32 / lp * (kGradThreads / 32);
   const int64_t need = (static_cast<int64_t>(a.T) + tok - 1) / tok;
   const int grid = static_cast<int>(need < ctx.num_sms * 16 ? need : ctx.num_sms * 16);
+  // 16-byte words where rows are whole ones and the weights begin at one (those of one
+  // layer of several, G Ne + 1 words apart, need not)
+  const bool vec = a.Ne % 4 == 0 && reinterpret_cast<uintptr_t>(a.grad_w) % 16 == 0;
   return with_lanes(lp, [&](auto n) {
     constexpr int LP = decltype(n)::value;
-    return cuda_status(launch_pdl(a.Ne % 4 == 0 ? balance_grad_kernel<LP, true>
-                                                : balance_grad_kernel<LP, false>,
+    return cuda_status(launch_pdl(vec ? balance_grad_kernel<LP, true> : balance_grad_kernel<LP, false>,
                                   grid, kGradThreads, 0, ctx.stream, a));
   });
 }

@@ -190,3 +190,11 @@ def test_a_refused_step_is_not_counted(occ, kw):
     with pytest.raises(occ.OccultError):
         opt.step(stream=0, **kw)
     assert opt.opt.step == 7 and opt.opt.lr == 1e-3 and opt.opt.grad_scale is None
+
+
+def test_balance_grad_refuses_weights_off_a_word(occ):
+    """They need no whole 16 bytes, but a float must be where a float can be."""
+    ds, opt = desc(occ), occ.occult_balance_t(0.01, 0.0, 0.0, 0)
+    g = occ.lib().occult_balance_grad
+    args = lambda w: (ctypes.byref(ds), ctypes.byref(opt), V, w, NULL, NULL, V, 0, NULL)  # noqa: E731
+    assert g(*args(ODD)) == INVALID

@@ -253,3 +253,38 @@ def test_every_number_of_lanes(occ, Ne, k, T, group_len):
     z, ids = case(T, Ne, k, seed=Ne + k)
     mask = np.random.default_rng(3).random(T) < 0.8
     check(occ, z, ids, 1, group_len, mask)
+
+
+@pytest.mark.parametrize("Ne", [8, 64, 160])
+@pytest.mark.parametrize("off", [1, 2, 3])
+@pytest.mark.parametrize("group_len", [0, 300])
+def test_weights_of_one_layer_of_several(occ, Ne, off, group_len):
+    """grad_w rows of a buffer of several layers' (G Ne + 1 words each) begin at no whole 16
+    bytes; loss and gradient take them alike, with the gradient of an aligned buffer but
+    for the order of one sum."""
+    T, k = 1000, 2
+    z, ids = case(T, Ne, k, seed=Ne)
+    ds = occ.desc_for(synth.CONFIGS["olmoe_fwd"].with_(T=T, n_experts=Ne, top_k=k, n_vdev=4))
+    opt = occ.occult_balance_t(COEF["coef"], COEF["coef_dev"], COEF["coef_z"], group_len)
+    n = occ.balance_groups(ds, opt) * Ne + 1
+    z, ids = torch.as_tensor(z).cuda(), torch.as_tensor(ids).cuda()
+    e2v = (torch.arange(Ne, device="cuda") % 4).to(torch.int32)
+    counts, loss = torch.empty((n - 1,), dtype=torch.int32, device="cuda"), torch.empty(4, device="cuda")
+    ws = torch.empty(occ.balance_workspace_size(ds, opt), dtype=torch.uint8, device="cuda")
+    grads = []
+    for o in (0, off):
+        grad_w = torch.full((n + 8,), -7.0, device="cuda")
+        view = grad_w[o:o + n]
+        dl = torch.empty(T, Ne, device="cuda")
+        occ.occult_balance_loss(ds, opt, z, ids, e2v, counts, view, loss, ws)
+        occ.occult_balance_grad(ds, opt, z, view, dl)
+        assert (grad_w[:o] == -7).all() and (grad_w[o + n:] == -7).all()
+        grads.append((view.clone(), dl.double()))
+    (wa, a), (wb, b) = grads
+    assert torch.equal(wa, wb)
+    # p (w - w.p + wz lse): two orders of a sum of Ne positive terms, within 32 units of w
+    # for a factor of p, and the units of the products
+    p = z.double().softmax(1)
+    w = wa[:-1].double().view(-1, Ne).repeat_interleave(group_len or T, 0)[:T]
+    err = p * (32 * U * w.amax(1, keepdim=True)) + 4 * U * a.abs()
+    assert ((a - b).abs() <= err + 1e-37).all()
