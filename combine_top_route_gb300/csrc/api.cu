@@ -832,6 +832,7 @@ int occult_block_norm(const occult_desc_t* desc, const occult_norm_t* opt, const
                  (r && (r_out != nullptr) == (y != nullptr) && (x != nullptr) == (w_pre != nullptr) &&
                   (w_post || !rstd_post) && (w_pre || !rstd_pre)));
   OCCULT_REQUIRE(aligned16({r, y, w_post, gate, w_pre, r_out, x}));
+  OCCULT_REQUIRE(aligned(4, {rstd_post, rstd_pre}));
   OCCULT_CTX(stream);
   if (desc->T == 0) return OCCULT_OK;
   NormArgs a{};
@@ -861,6 +862,7 @@ int occult_block_norm_bwd(const occult_desc_t* desc, const occult_norm_t* opt,
                                   (!w_pre || (dx && r_out && rstd_pre)) &&
                                   (!w_post || rstd_post)));
   OCCULT_REQUIRE(aligned16({dr_out, dx, r_out, y, w_post, gate, w_pre, dr, dy, ws}));
+  OCCULT_REQUIRE(aligned(4, {rstd_post, rstd_pre, dw_post, dgate, dw_pre}));
   const size_t need = block_norm_bwd_ws_bytes(*desc);
   if (ws_bytes < need || (need > 0 && !ws)) return OCCULT_ERR_WORKSPACE;
   OCCULT_CTX(stream);
@@ -916,7 +918,7 @@ int occult_balance_loss(const occult_desc_t* desc, const occult_balance_t* opt,
   if (rc) return rc;
   OCCULT_REQUIRE(expert_to_vdev && counts && grad_w && loss);
   OCCULT_REQUIRE(desc->T == 0 || (logits && ids));
-  OCCULT_REQUIRE(aligned16({logits, ids, ws}));
+  OCCULT_REQUIRE(aligned16({logits, ids, ws}) && aligned(4, {expert_to_vdev, counts, grad_w, loss}));
   if (ws_bytes < balance_ws_bytes(*desc, opt->group_len) || !ws) return OCCULT_ERR_WORKSPACE;
   OCCULT_CTX(stream);
   BalanceArgs a = balance_args(desc, opt, logits, mask);
@@ -933,7 +935,7 @@ int occult_balance_grad(const occult_desc_t* desc, const occult_balance_t* opt,
   if (rc) return rc;
   OCCULT_REQUIRE(accumulate == 0 || accumulate == 1);
   OCCULT_REQUIRE(desc->T == 0 || (logits && grad_w && dlogits));
-  OCCULT_REQUIRE(aligned16({logits, dlogits}) && aligned(4, {grad_w}));
+  OCCULT_REQUIRE(aligned16({logits, dlogits}) && aligned(4, {grad_w, dloss}));
   OCCULT_CTX(stream);
   BalanceArgs a = balance_args(desc, opt, logits, mask);
   a.grad_w = const_cast<float*>(grad_w);
@@ -945,7 +947,7 @@ int occult_adamw(const occult_adamw_t* opt, const occult_param_t* params, int32_
                  occult_stream_t stream) {
   OCCULT_REQUIRE(opt && n_params >= 0 && (n_params == 0 || params));
   OCCULT_REQUIRE(opt->state_bits == 32 || opt->state_bits == 8);
-  OCCULT_REQUIRE(opt->step >= 1 && opt->reserved == 0);
+  OCCULT_REQUIRE(opt->step >= 1 && opt->reserved == 0 && aligned(4, {opt->grad_scale}));
   // (comparisons that a NaN fails)
   OCCULT_REQUIRE(opt->beta1 >= 0 && opt->beta1 < 1 && opt->beta2 >= 0 && opt->beta2 < 1);
   OCCULT_REQUIRE(opt->eps >= 1e-30 && opt->eps < 1e30 && opt->lr > -1e30 && opt->lr < 1e30 &&

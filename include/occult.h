@@ -662,7 +662,8 @@ typedef struct occult_norm {
  *   r_out  out [T, d] in opt->res_dtype (with y); may be r itself.
  *   x      out [T, d] layer dtype (with w_pre).
  *   rstd_post, rstd_pre  out fp32 [T], nullable: kept for the backward.
- * Apart from r_out = r no output may overlap an input.  d <= 16384.
+ * Apart from r_out = r no output may overlap an input.  d <= 16384.  Pointers are
+ * 16-byte aligned, rstd_post and rstd_pre 4-byte.
  */
 int occult_block_norm(const occult_desc_t* desc, const occult_norm_t* opt, const void* r,
                       const float* y, const void* w_post, const float* gate, const void* w_pre,
@@ -692,7 +693,8 @@ int occult_block_norm(const occult_desc_t* desc, const occult_norm_t* opt, const
  *          accumulated; sums over the tokens run in a fixed order.
  *   ws     occult_workspace_size(OCCULT_WS_BLOCK_NORM_BWD) bytes.
  * An output must be given exactly when its forward input was; apart from
- * dr = dr_out none may overlap an input.
+ * dr = dr_out none may overlap an input.  Pointers are 16-byte aligned, the row
+ * factors, dw_post, dgate and dw_pre 4-byte.
  */
 int occult_block_norm_bwd(const occult_desc_t* desc, const occult_norm_t* opt,
                           const void* dr_out, const float* dx, const void* r_out, const float* y,
@@ -733,7 +735,8 @@ int occult_balance_workspace_size(const occult_desc_t* desc, const occult_balanc
  *   grad_w  out fp32 [G*Ne + 1]: what occult_balance_grad needs.
  *   loss    out fp32 [4]: {coef expert + coef_dev device + coef_z z, expert,
  *           device, z}.
- * Every sum runs in a fixed order.
+ * Every sum runs in a fixed order.  logits, ids and ws are 16-byte aligned, the other
+ * pointers but mask 4-byte.
  */
 int occult_balance_loss(const occult_desc_t* desc, const occult_balance_t* opt,
                         const float* logits, const int32_t* ids, const int32_t* expert_to_vdev,
@@ -750,6 +753,8 @@ int occult_balance_loss(const occult_desc_t* desc, const occult_balance_t* opt,
  *   dloss   fp32 [1] nullable (1): the gradient of the total.
  *   dlogits fp32 [T, Ne].  accumulate = 1: added to what it holds (e.g. from
  *           occult_router_grad); 0: written (zeros for masked tokens).
+ * logits and dlogits are 16-byte aligned, the other pointers but mask 4-byte (grad_w at
+ * 16 bytes, as an allocation begins, is read faster).
  */
 int occult_balance_grad(const occult_desc_t* desc, const occult_balance_t* opt,
                         const float* logits, const float* grad_w, const uint8_t* mask,
@@ -799,7 +804,7 @@ typedef struct occult_param {
  * nearest value) or the widened bf16 parameter.  A bf16 parameter without a master
  * is rounded up or down by a draw, so that updates below half a unit are not lost.
  *   opt, params  host; copied at launch.  Pointers are 16-byte aligned (m_exp and
- *                v_exp need no alignment); tensors do not overlap.
+ *                v_exp need no alignment, grad_scale a float's); tensors do not overlap.
  * state_bits 8 keeps m and sqrt(v) as 8-bit floats under one exponent E for every
  * OCCULT_STATE_BLOCK elements of a tensor: of the binades below 2^(E+1) the largest
  * sixteen, m with a sign and 8 steps a binade, sqrt(v) with 16; m below them is 0,
@@ -817,6 +822,7 @@ int occult_adamw(const occult_adamw_t* opt, const occult_param_t* params, int32_
  * occult_adamw_read -- the values an 8-bit state stands for, exactly, in bf16.
  *   codes  uint8 [n], exps uint8 [ceil(n / OCCULT_STATE_BLOCK)] of one tensor;
  *   which  OCCULT_STATE_M: m, OCCULT_STATE_V: sqrt(v);   out bf16 [n].
+ * codes and out are 16-byte aligned.
  */
 int occult_adamw_read(const uint8_t* codes, const uint8_t* exps, int64_t n, int32_t which,
                       void* out, occult_stream_t stream);

@@ -198,3 +198,19 @@ def test_balance_grad_refuses_weights_off_a_word(occ):
     g = occ.lib().occult_balance_grad
     args = lambda w: (ctypes.byref(ds), ctypes.byref(opt), V, w, NULL, NULL, V, 0, NULL)  # noqa: E731
     assert g(*args(ODD)) == INVALID
+
+
+def test_words_off_a_word_are_refused(occ):
+    """Buffers that are read and written by single words: at an odd address a kernel would
+    fault, so the call says so."""
+    for k in ("rstd_post", "rstd_pre"):
+        assert norm(occ, **{k: ODD}) == INVALID
+        assert norm_bwd(occ, **{k: ODD}) == INVALID
+    for k in ("dw_post", "dgate", "dw_pre"):
+        assert norm_bwd(occ, **{k: ODD}) == INVALID
+    for k in ("e2v", "counts", "grad_w", "loss"):
+        assert balance(occ, **{k: ODD}) == INVALID
+    ds, opt = desc(occ), occ.occult_balance_t(0.01, 0.0, 0.0, 0)
+    assert occ.lib().occult_balance_grad(ctypes.byref(ds), ctypes.byref(opt), V, V, NULL, ODD, V, 0,
+                                         NULL) == INVALID
+    assert adamw(occ, dict(grad_scale=258)) == INVALID
