@@ -20,10 +20,37 @@ constexpr int kMaxDevices = 64;
 struct DeviceInfo {
   std::once_flag once;
   int num_sms = 0;
+  bool clusters = false;
   int* err = nullptr;
   cudaError_t status = cudaSuccess;
 };
 DeviceInfo g_devices[kMaxDevices];
+
+// Stands for the kernels of such clusters in the question whether they can be placed.
+__global__ void cluster_kernel() {}
+
+bool can_place_clusters() {
+  constexpr int kSmem = 200 * 1024;  // an SM a CTA, as the widest of them
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = kClusterCtas;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = kClusterCtas;
+  cfg.blockDim = 1024;
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaFuncSetAttribute(cluster_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) ==
+          cudaSuccess &&
+      cudaFuncSetAttribute(cluster_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) ==
+          cudaSuccess &&
+      cudaOccupancyMaxActiveClusters(&n, cluster_kernel, &cfg) == cudaSuccess)
+    return n > 0;
+  cudaGetLastError();
+  return false;
+}
 
 }  // namespace
 
@@ -35,11 +62,13 @@ int launch_ctx(occult_stream_t stream, LaunchCtx* ctx) {
     di.status = cudaDeviceGetAttribute(&di.num_sms, cudaDevAttrMultiProcessorCount, dev);
     if (di.status == cudaSuccess)
       di.status = cudaGetSymbolAddress(reinterpret_cast<void**>(&di.err), g_dev_err);
+    if (di.status == cudaSuccess) di.clusters = can_place_clusters();
   });
   if (di.status != cudaSuccess) return OCCULT_ERR_CUDA;
   ctx->stream = static_cast<cudaStream_t>(stream);
   ctx->dev_err = di.err;
   ctx->num_sms = di.num_sms;
+  ctx->clusters = di.clusters;
   return OCCULT_OK;
 }
 

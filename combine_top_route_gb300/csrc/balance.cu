@@ -24,7 +24,6 @@ namespace {
 
 constexpr int kTileThreads = 512;
 constexpr int kOneThreads = 1024;
-constexpr int kCluster = 16;                       // CTAs of the one-launch kernel
 constexpr int kOneSteps = 2, kClusterSteps = 4;    // steps of a CTA
 constexpr int kSumThreads = 1024;
 constexpr int kSumWarps = kSumThreads / 32;
@@ -643,12 +642,14 @@ size_t balance_ws_bytes(const occult_desc_t& ds, int group_len) {
 int launch_balance_loss(const LaunchCtx& ctx, const BalanceArgs& a) {
   const int lp = lanes_of(a.Ne, a.k);
   // One launch for a batch of one group: by one CTA for two steps of all its warps (1024 /
-  // lp tokens each), by a cluster of 16 for four of each, two launches beyond that.
+  // lp tokens each), by a cluster of 16 for four of each (where the device has a place for
+  // one: a partition of few SMs has not), two launches beyond that.
   // 64 experts, us by one CTA, the cluster, two launches: 4.8, 5.4, 6.1 for 256 tokens,
   // -, 6.7, 7.1 for 4096, -, 8.4, 8.4 for 8192, -, 11.3, 9.1 for 16384.
   const int64_t steps = (static_cast<int64_t>(a.T) * lp + kOneThreads - 1) / kOneThreads;
-  if (a.G == 1 && steps <= kClusterSteps * kCluster) {
-    const int ctas = steps <= kOneSteps ? 1 : kCluster;
+  const int one_launch = ctx.clusters ? kClusterSteps * kClusterCtas : kOneSteps;
+  if (a.G == 1 && steps <= one_launch) {
+    const int ctas = steps <= kOneSteps ? 1 : kClusterCtas;
     return with_lanes(lp, [&](auto n) { return launch_cluster<decltype(n)::value>(ctx, a, ctas); });
   }
   const Tiles tiles = tiles_of(a.T, a.L, a.G, lp);

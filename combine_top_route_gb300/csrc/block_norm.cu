@@ -814,7 +814,6 @@ int fwd(const LaunchCtx& ctx, const NormArgs& a) {
 // two launches (us: 128 x 64 4.0 and 4.5, 257 x 64 5.4 and 4.7, 16 x 2048 5.1 and 4.9; two
 // rows a group of 2048 6.1 and 5.0), but the host has one launch (2 us) less, which is
 // what bounds calls of this size.
-constexpr int kCluster = 16;
 constexpr int cluster_rows(int G) { return G == 1 ? 3 : 1; }
 
 template <typename R, typename L, int G, int U, int CTAS>
@@ -829,11 +828,11 @@ int bwd_rows(const LaunchCtx& ctx, const NormArgs& a, bool sums, float* part, in
   if (rc) return rc;
   const int need = (a.T + Group<G>::kGroups - 1) / Group<G>::kGroups;
   *n_part = 0;
-  if (sums && need <= kCluster * cluster_rows(G)) {
+  if (sums && ctx.clusters && need <= kClusterCtas * cluster_rows(G)) {
     rc = cuda_status(cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1));
     if (rc) return rc;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = kCluster;
+    cfg.gridDim = kClusterCtas;
     cfg.blockDim = Group<G>::kThreads;
     cfg.dynamicSmemBytes = smem;
     cfg.stream = ctx.stream;

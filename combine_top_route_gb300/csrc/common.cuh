@@ -18,7 +18,12 @@ struct LaunchCtx {
   cudaStream_t stream;
   int* dev_err;     // device error word (see occult_device_error)
   int num_sms;
+  bool clusters;    // whether clusters of kClusterCtas CTAs, an SM each, can be placed
 };
+
+// CTAs of the clusters that take a small problem in one launch: more than the portable 8,
+// so that a part of a device may have no place for them.
+constexpr int kClusterCtas = 16;
 
 int launch_ctx(occult_stream_t stream, LaunchCtx* ctx);
 
