@@ -224,3 +224,48 @@ def test_a_factor_of_the_gradients_outlives_its_step(occ, raw):
     assert len(keep) == 64
     got = opt.states[0]["m"]
     assert ((got - m).abs() <= 1e-6 * m).all()
+
+
+@pytest.mark.parametrize("state_bits", [32, 8])
+@pytest.mark.parametrize("masters", [True, False])
+def test_first_step_of_every_parameter(occ, state_bits, masters):
+    """The first step from zero states: w (1 - lr wd) - lr g / (|g| + eps), m = (1 - b1) g and
+    v = (1 - b2) g^2, for each parameter.  Tolerances: fp32 arithmetic (2^-18 of the terms);
+    a bf16 parameter is its master's nearest value, or by a draw within a whole unit (2^-7);
+    8-bit codes a unit of their binade (1/8 of m, 1/16 of the root of v) and, below a
+    block's sixteen binades, what its largest value leaves (2^-15 of it, twice that where
+    a rounding up moves the binades)."""
+    from train_block import make_block
+    cfg = config()
+    block = make_block(cfg)
+    lr, wd, eps = 1e-2, 0.1, 1e-8
+    opt = block.optimizer(lr=lr, weight_decay=wd, eps=eps, state_bits=state_bits, masters=masters)
+    g = torch.Generator(device="cuda").manual_seed(7)
+    block.forward(torch.randn(cfg.T, cfg.d, generator=g, device="cuda").bfloat16())
+    block.backward(torch.randn(cfg.T, cfg.d, generator=g, device="cuda").bfloat16())
+    before = [p.detach().double().view(-1) for _, p, _ in block.parameters()]
+    opt.step()
+
+    def block_top(x):
+        pad = torch.nn.functional.pad(x.abs(), (0, -len(x) % 256))
+        return pad.view(-1, 256).amax(1).repeat_interleave(256)[:len(x)]
+
+    for i, (name, p, grad) in enumerate(block.parameters()):
+        dw = grad.double().view(-1)
+        assert float((dw.abs() > 1e-7).float().mean()) > 0.9, name
+        want = before[i] * (1 - lr * wd) - lr * dw / (dw.abs() + eps)
+        tol = 2.0 ** -18 * (before[i].abs() + lr)
+        got = p.view(-1)
+        if p.dtype == torch.bfloat16 and masters:
+            master = opt.states[i]["master"].view(-1)
+            assert torch.equal(got, master.to(torch.bfloat16)), name
+            got = master
+        elif p.dtype == torch.bfloat16:
+            tol = tol + 2.0 ** -7 * want.abs()
+        assert ((got.double() - want).abs() <= tol).all(), name
+        m, v = (t.double() for t in opt.moments(i))
+        for x, w, part in ((m, 0.1 * dw, 8), (v.sqrt(), 0.05 ** 0.5 * dw.abs(), 16)):
+            err = 2.0 ** -18 * w.abs()
+            if state_bits == 8:
+                err = w.abs() / part * 1.001 + 2.0 ** -14 * block_top(w)
+            assert ((x - w).abs() <= err + 1e-30).all(), (name, part)
