@@ -359,9 +359,10 @@ __device__ __forceinline__ void step_block(const AdamTable& a, const Tensor& T, 
 }
 
 // The blocks blk, blk + kAdamWarps, ... below end of a tensor by one warp; with 8-bit
-// states the next block's words are on their way while this one's are worked on (without
-// that 1139 us where it takes 940), for a bf16 parameter without a master, whose words are
-// few, both blocks' from the start (a tenth faster; with a master 1273 against 1040).
+// states the next block's words are on their way while this one's are worked on, for a
+// bf16 parameter without a master, whose words are few, both blocks' from the start.  402.8
+// M weights, us with neither, the next block's and both from the start: bf16 alone 848,
+// 940, 812; with a master 1401, 1027, 1100; fp32 1325, 930, 979.
 template <int BITS, int KIND>
 __device__ __forceinline__ void step_blocks(const AdamTable& a, const Tensor& T, int64_t blk,
                                             int64_t end, float gs) {
@@ -395,8 +396,9 @@ __device__ __forceinline__ void step_blocks(const AdamTable& a, const Tensor& T,
 }
 
 // CTAs of an SM: eight, nine for the kind that the issue rate bounds (64 bytes of stack a
-// thread for the spills, and 811 us where eight CTAs take 830, ten 832); nine cost the
-// other two with 8-bit states more than they give (with masters 5 %).
+// thread for the spills, and 812 us where eight CTAs take 831, ten 832); nine cost the
+// other two with 8-bit states more than they give (1083 for 1027 us with masters, 981 for
+// 930 in fp32).
 __host__ __device__ constexpr int adam_ctas(int bits, int kind) {
   return bits == 8 && kind == KIND_BF16 ? 9 : 8;
 }
@@ -496,7 +498,7 @@ int launch_adamw(const LaunchCtx& ctx, const occult_adamw_t& o, const occult_par
   // With 8-bit states two blocks a warp, whose loads and arithmetic overlap, where that
   // leaves four CTAs for each place on the GPU; one for smaller sets and for 32-bit states,
   // which wait for memory alone.  One, two, three blocks took, us for 402.8 M weights: bf16
-  // alone with 8-bit states 1030, 808, 937, with masters 1057, 1025, 1206 (the CTAs' streams
+  // alone with 8-bit states 1030, 808, 932, with masters 1058, 1025, 1221 (the CTAs' streams
   // lie too far apart then); with fp32 states and masters 1699, 1711 (two).
   int64_t blocks = 0, of_kind[3] = {0, 0, 0};
   for (int k = 0; k < n_params; ++k) {
@@ -511,7 +513,7 @@ int launch_adamw(const LaunchCtx& ctx, const occult_adamw_t& o, const occult_par
   // the rest go together.  Own registers save 402.8 M weights 23 us (bf16 alone with 8-bit
   // states, or masters and fp32 states); a launch more costs 2 to 3 us, and 60 tensors of
   // three kinds and 2560 weights each take 5 us in one, 12 us in three launches, of 2^20
-  // each with 8-bit states 152 and 161 us.
+  // each with 8-bit states 152 and 162 us.
   bool own[3];
   for (int k = 0; k < KIND_ANY; ++k)
     own[k] = of_kind[k] == blocks || of_kind[k] >= kOwnWeights / kBlock || of_kind[k] == 0;

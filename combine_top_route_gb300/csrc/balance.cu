@@ -12,7 +12,7 @@
 // experts, top-8 9.9 + 3.7 us (the first launch 3.6 us, bound by two steps of loads;
 // the second by its chain of sums in one CTA); 131072 tokens, 256 experts, masked, 32
 // sequences 35 + 56 us = 3.9 and 7.2 TB/s (the logits twice, the gradient in and out);
-// 256 tokens, 8 experts 3.8 + 1.5 us.
+// 256 tokens, 8 experts 4.0 + 1.7 us.
 #include <type_traits>
 
 #include "common.cuh"
@@ -131,7 +131,7 @@ __device__ __forceinline__ float softmax_row(float (&v)[8], float* inv) {
 #pragma unroll
   for (int o = LP / 2; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
   *inv = __fdividef(1.f, z);  // z is about 1 .. 256
-  return mx + __logf(z);      // within 2^-21
+  return mx + __logf(z);      // z is 1 .. 256: within 3 * 2^-21, and the sum's rounding
 }
 
 // What a tile, a group or a batch of one CTA adds up to, in shared memory.
@@ -378,8 +378,8 @@ int launch_cluster(const LaunchCtx& ctx, const BalanceArgs& a, int ctas) {
 }
 
 // Pass 1: CTA x of group y takes one tile of the group's tokens.  131072 x 256: 27 us,
-// near both bounds (5.0 TB/s and two thirds of the issue slots, at some 150 instructions a
-// token and warp); a token a warp with scalar loads and expf took 55 us.
+// near both bounds (5.0 TB/s and two thirds of the issue slots, at 155 instructions a token
+// and warp); a token a warp with scalar loads and expf took 55 us.
 template <int LP>
 __global__ void __launch_bounds__(kTileThreads, 2)
 balance_tiles_kernel(BalanceArgs a, Tiles tiles) {

@@ -92,7 +92,7 @@ __device__ __forceinline__ void block_sum(float (&v)[N], float (*s_red)[N]) {
 
 // Backward of rows too wide for a ring (fp32 streams above 12800 columns) or not whole
 // 16 bytes, one CTA a row, read twice (the second time from L2): 4096 x 16384 with a bf16
-// stream took 398 us = 2.7 TB/s this way (321 us through the ring), bound by the latency
+// stream took 398 us = 2.7 TB/s this way (325 us through the ring), bound by the latency
 // of its two passes with one CTA an SM.  D is linear in mean(w_pre dx n), so
 // one round of sums gives every mean: with g = w_pre dx, D0 = dr_out + rstd_pre g and
 // q = gate w_post m,
@@ -780,6 +780,9 @@ int fwd(const LaunchCtx& ctx, const NormArgs& a) {
   // way.)  Warps a row and CTAs an SM by width: two units a thread with most of the
   // threads at work, and groups enough to hide one row's latency behind the others'
   // copies, but no more than that (their streams take the memory's rows from each other).
+  // The steps end at the widths that were measured; one between them runs on the next
+  // step's warps, some of them idle (2880 on 16 warps, 30 % idle, 0.74 of its floor where
+  // 2816 on 11 and 4096 on 16 reach 0.93 and 0.96; 3584, 12 % idle, 0.88).
   // With only powers of two warps a row, us before and now: 32768 x 320 27 and 20, x 768 50
   // and 42, x 1408 95 and 73, 31775 x 2112 174 and 105, 23831 x 2816 135 and 105; with an
   // fp32 stream x 768 and x 320 gain nothing, x 1408 109 and 101, x 2112 175 and 141, and
@@ -872,9 +875,11 @@ int bwd(const LaunchCtx& ctx, const NormArgs& a, float* part) {
   // bulk copies move whole 16 bytes; the ring holds a row of up to 16384 columns (12800
   // with an fp32 stream).  Above 2048 columns three or four units a thread (16 warps of
   // two units, one CTA an SM: 210 against 175 us at 16384 x 4096); one, three or six warps
-  // a row where powers of two leave a third of the threads or more without work (us: 32768
+  // a row up to 384, 768, 1536 and 2304 columns, where the next power of two would leave a
+  // quarter to a half of the threads without work (wider ones keep theirs, and 2880 and
+  // 6144 columns of bf16 reach 0.82 and 0.69 of their floors).  Powers of two and so, us: 32768
   // x 320 45 -> 40, x 768 84 -> 71, x 1408 149 -> 130, 31775 x 2112 204 -> 179; with an fp32
-  // stream 259 -> 225 at 2112, the others the same, but x 320, which keeps two warps).
+  // stream 259 -> 225 at 2112, the others the same, but x 320, which keeps two warps.
   if (d * sizeof(R) % 16 != 0 || bwd_row_bytes<R>(d) > kRingBytes)
     rc = bwd_any<R, L>(ctx, a, part, &n_part);
   else if (d <= 128) rc = bwd_rows<R, L, 1, 1, 3>(ctx, a, sums, part, &n_part);
