@@ -41,7 +41,8 @@ class OccultAdamW:
     ``params``: contiguous bf16 or fp32 tensors, updated in place; ``grads``: the
     fp32 buffers their gradients are written to before every ``step``.  ``masters``:
     keep an fp32 copy of every bf16 parameter (otherwise its update is rounded up
-    or down by a draw).
+    or down by a draw).  The step's number and rate are the host's: ``step`` is called
+    every time, not replayed from a CUDA graph, which would repeat the one captured.
     """
 
     def __init__(self, params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], lr: float,
@@ -113,7 +114,9 @@ class OccultBlock:
                  eps: float = 1e-6, res_scale: float = 1.0, res_dtype=torch.bfloat16,
                  post_norm: bool = True, gate: Optional[torch.Tensor] = None,
                  balance=(0.01, 0.0, 0.001), group_len: int = 0, sim_table=None):
-        """``weights``: w1 and w2 as OccultMoE takes them; ``w_router`` fp32 [Ne, d];
+        """``weights``: w1 and w2 as OccultMoE takes them (bf16 ones on the device are
+        used where they are, so that an optimizer's steps change the caller's tensors;
+        the other weights are copied); ``w_router`` fp32 [Ne, d];
         ``gate`` fp32 [d] or None; ``balance``: the weights of the expert, device and z
         terms; ``group_len``: tokens of a sequence for them (0: the batch)."""
         if desc.dtype != OCCULT_BF16 or desc.n_shared:

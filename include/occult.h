@@ -636,7 +636,7 @@ int occult_profile_coact(const occult_desc_t* desc, const int32_t* ids, int32_t 
 
 /* Options of the block norm (host). */
 typedef struct occult_norm {
-  float eps;            /* added to the mean square; > 0                            */
+  float eps;            /* added to the mean square; > 0, < 1e30                    */
   float res_scale;      /* a: factor of the residual stream                         */
   int32_t gate_kind;    /* OCCULT_GATE_*                                            */
   int32_t res_dtype;    /* type of the residual stream: OCCULT_F32 | OCCULT_BF16    */
@@ -803,7 +803,9 @@ typedef struct occult_param {
  * in fp32 on the fp32 parameter, the master copy (the bf16 parameter is then its
  * nearest value) or the widened bf16 parameter.  A bf16 parameter without a master
  * is rounded up or down by a draw, so that updates below half a unit are not lost.
- *   opt, params  host; copied at launch.  Pointers are 16-byte aligned (m_exp and
+ *   opt, params  host; copied at launch, so that a CUDA graph repeats the step that it
+ *                captured, with its number, rate and draws: a graph of a training step
+ *                leaves this call out, or is captured anew.  Pointers are 16-byte aligned (m_exp and
  *                v_exp need no alignment, grad_scale a float's); tensors do not overlap.
  * state_bits 8 keeps m and sqrt(v) as 8-bit floats under one exponent E for every
  * OCCULT_STATE_BLOCK elements of a tensor: of the binades below 2^(E+1) the largest
