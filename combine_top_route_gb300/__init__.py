@@ -47,6 +47,10 @@ GATE_TOKEN = 2
 STATE_BLOCK = 256                # OCCULT_STATE_BLOCK
 STATE_M = 0
 STATE_V = 1
+SCORE_SOFTMAX = 0
+SCORE_SIGMOID = 1
+GROUP_BLOCKS = 0
+GROUP_VDEV = 1
 
 
 class occult_desc_t(ctypes.Structure):
@@ -94,6 +98,18 @@ class occult_param_t(ctypes.Structure):
                                                "v_exp")] + [
         ("n", ctypes.c_int64), ("first", ctypes.c_int64), ("dtype", ctypes.c_int32),
         ("reserved", ctypes.c_int32)]
+
+
+class occult_score_t(ctypes.Structure):
+    """Options of the scored router (see occult.h); the defaults are a plain top-k."""
+    _fields_ = [("score", ctypes.c_int32), ("n_groups", ctypes.c_int32),
+                ("keep_groups", ctypes.c_int32), ("group_best", ctypes.c_int32),
+                ("group_kind", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("bias_rate", ctypes.c_float)]
+
+    def __init__(self, score=SCORE_SIGMOID, n_groups=1, keep_groups=1, group_best=1,
+                 group_kind=GROUP_BLOCKS, scale=1.0, bias_rate=0.0):
+        super().__init__(score, n_groups, keep_groups, group_best, group_kind, scale, bias_rate)
 
 
 class OccultError(RuntimeError):
@@ -151,6 +167,9 @@ _SIGNATURES = {
     "occult_balance_grad": (ctypes.c_int, [_D] + [_VP] * 6 + [_I32, _VP]),
     "occult_adamw": (ctypes.c_int, [_VP, _VP, _I32, _VP]),
     "occult_adamw_read": (ctypes.c_int, [_VP, _VP, ctypes.c_int64, _I32, _VP, _VP]),
+    "occult_route_scored": (ctypes.c_int, [_D] + [_VP] * 8),
+    "occult_route_scored_grad": (ctypes.c_int, [_D] + [_VP] * 6),
+    "occult_route_bias_step": (ctypes.c_int, [_D, _VP, _VP, _I32, _VP, _VP]),
     "occult_profile_coact": (ctypes.c_int, [_D, _VP, _I32, _VP, _VP, _VP, _VP, _VP,
                                             ctypes.c_size_t, _VP]),
 }
@@ -729,6 +748,41 @@ def occult_balance_grad(desc, opt, logits, grad_w, dlogits, mask=None, dloss=Non
         _at(dlogits, _F32, T * Ne, "dlogits"), 1 if accumulate else 0, _on(stream))
     if rc:
         raise OccultError("occult_balance_grad", rc)
+
+
+def occult_route_scored(desc, opt, logits, expert_to_vdev, ids, gates, vmask, bias=None,
+                        stream=None):
+    """The scored router: ids, gates and device masks, as occult_route gives them."""
+    T, Ne, k = desc.T, desc.n_experts, desc.top_k
+    if logits is None or expert_to_vdev is None or ids is None or gates is None or vmask is None:
+        _need(logits=logits, expert_to_vdev=expert_to_vdev, ids=ids, gates=gates, vmask=vmask)
+    rc = lib().occult_route_scored(
+        desc, ctypes.byref(opt), _at(logits, _F32, T * Ne, "logits"), _at(bias, _F32, Ne, "bias"),
+        _at(expert_to_vdev, _I32T, Ne, "expert_to_vdev"), _at(ids, _I32T, T * k, "ids"),
+        _at(gates, _F32, T * k, "gates"), _at(vmask, _I32T, T, "vmask"), _on(stream))
+    if rc:
+        raise OccultError("occult_route_scored", rc)
+
+
+def occult_route_scored_grad(desc, opt, logits, ids, dgates, dlogits, stream=None):
+    """Gradient of the scored router's gates with respect to the logits."""
+    T, Ne, k = desc.T, desc.n_experts, desc.top_k
+    if logits is None or ids is None or dgates is None or dlogits is None:
+        _need(logits=logits, ids=ids, dgates=dgates, dlogits=dlogits)
+    rc = lib().occult_route_scored_grad(
+        desc, ctypes.byref(opt), _at(logits, _F32, T * Ne, "logits"), _at(ids, _I32T, T * k, "ids"),
+        _at(dgates, _F32, T * k, "dgates"), _at(dlogits, _F32, T * Ne, "dlogits"), _on(stream))
+    if rc:
+        raise OccultError("occult_route_scored_grad", rc)
+
+
+def occult_route_bias_step(desc, opt, counts, bias, stream=None):
+    """One step of the bias by opt.bias_rate; counts int32 [G, Ne] of occult_balance_loss."""
+    _need(counts=counts, bias=bias)
+    Ne = desc.n_experts
+    G = counts.numel() // max(1, Ne)
+    _call("occult_route_bias_step", desc, ctypes.byref(opt), _at(counts, _I32T, G * Ne, "counts"),
+          G, _at(bias, _F32, Ne, "bias"), _on(stream))
 
 
 _RECORD = struct.Struct("7Q2q2i")   # occult_param_t

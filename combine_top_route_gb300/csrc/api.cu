@@ -1004,4 +1004,53 @@ int occult_adamw_read(const uint8_t* codes, const uint8_t* exps, int64_t n, int3
   return launch_adamw_read(ctx, codes, exps, n, which, out);
 }
 
+static int check_score(const occult_desc_t* desc, const occult_score_t* opt) {
+  int rc = check(desc);
+  if (rc) return rc;
+  OCCULT_REQUIRE(opt && desc->route_mode == OCCULT_ROUTE_EXACT);
+  OCCULT_REQUIRE(opt->score == OCCULT_SCORE_SOFTMAX || opt->score == OCCULT_SCORE_SIGMOID);
+  OCCULT_REQUIRE(opt->n_groups >= 1 && opt->n_groups <= 32 && desc->n_experts % opt->n_groups == 0);
+  OCCULT_REQUIRE(opt->keep_groups >= 1 && opt->keep_groups <= opt->n_groups);
+  OCCULT_REQUIRE(opt->keep_groups * (desc->n_experts / opt->n_groups) >= desc->top_k);
+  OCCULT_REQUIRE(opt->group_best == 1 || opt->group_best == 2);
+  OCCULT_REQUIRE(opt->group_kind == OCCULT_GROUP_BLOCKS ||
+                 (opt->group_kind == OCCULT_GROUP_VDEV && opt->n_groups == desc->n_vdev));
+  // (comparisons that a NaN fails)
+  OCCULT_REQUIRE(opt->scale > -1e30f && opt->scale < 1e30f && opt->bias_rate > -1e30f &&
+                 opt->bias_rate < 1e30f);
+  return OCCULT_OK;
+}
+
+int occult_route_scored(const occult_desc_t* desc, const occult_score_t* opt,
+                        const float* logits, const float* bias, const int32_t* expert_to_vdev,
+                        int32_t* ids, float* gates, uint32_t* vmask, occult_stream_t stream) {
+  int rc = check_score(desc, opt);
+  if (rc) return rc;
+  OCCULT_REQUIRE(expert_to_vdev && (desc->T == 0 || (logits && ids && gates && vmask)));
+  OCCULT_REQUIRE(aligned(4, {logits, bias, expert_to_vdev, ids, gates, vmask}));
+  OCCULT_CTX(stream);
+  return launch_route_scored(ctx, *desc, *opt, logits, bias, expert_to_vdev, ids, gates, vmask);
+}
+
+int occult_route_scored_grad(const occult_desc_t* desc, const occult_score_t* opt,
+                             const float* logits, const int32_t* ids, const float* dgates,
+                             float* dlogits, occult_stream_t stream) {
+  int rc = check_score(desc, opt);
+  if (rc) return rc;
+  OCCULT_REQUIRE(desc->T == 0 || (logits && ids && dgates && dlogits));
+  OCCULT_REQUIRE(aligned(4, {logits, ids, dgates, dlogits}));
+  OCCULT_CTX(stream);
+  return launch_route_scored_grad(ctx, *desc, *opt, logits, ids, dgates, dlogits);
+}
+
+int occult_route_bias_step(const occult_desc_t* desc, const occult_score_t* opt,
+                           const int32_t* counts, int32_t G, float* bias,
+                           occult_stream_t stream) {
+  int rc = check_score(desc, opt);
+  if (rc) return rc;
+  OCCULT_REQUIRE(G >= 1 && counts && bias && aligned(4, {counts, bias}));
+  OCCULT_CTX(stream);
+  return launch_route_bias_step(ctx, desc->n_experts, counts, G, opt->bias_rate, bias);
+}
+
 }  // extern "C"

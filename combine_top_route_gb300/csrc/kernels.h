@@ -15,6 +15,16 @@ int launch_route(const LaunchCtx& ctx, const occult_desc_t& ds, const float* log
 int launch_router_grad(const LaunchCtx& ctx, const occult_desc_t& ds, const float* logits,
                        const int32_t* gate_ids, const float* dgates, float* dlogits);
 
+// The scored router, its gradient and the step of its bias (route_scored.cu)
+int launch_route_scored(const LaunchCtx& ctx, const occult_desc_t& ds, const occult_score_t& opt,
+                        const float* logits, const float* bias, const int32_t* e2v, int32_t* ids,
+                        float* gates, uint32_t* vmask);
+int launch_route_scored_grad(const LaunchCtx& ctx, const occult_desc_t& ds,
+                             const occult_score_t& opt, const float* logits, const int32_t* ids,
+                             const float* dgates, float* dlogits);
+int launch_route_bias_step(const LaunchCtx& ctx, int Ne, const int32_t* counts, int G, float rate,
+                           float* bias);
+
 int launch_build_brim(const LaunchCtx& ctx, const occult_desc_t& ds, const int32_t* ids,
                       const float* gates, const uint32_t* vmask, const int32_t* placement,
                       int32_t* brim0, int32_t* seg_off, int32_t* brim1, int32_t* exp_off,

@@ -829,6 +829,84 @@ int occult_adamw(const occult_adamw_t* opt, const occult_param_t* params, int32_
 int occult_adamw_read(const uint8_t* codes, const uint8_t* exps, int64_t n, int32_t which,
                       void* out, occult_stream_t stream);
 
+/*
+ * The scored router: the choice of experts by softmax or sigmoid scores, with a bias
+ * that evens out the loads and groups of experts.  The paper's router is Eq. 2
+ * (occult_route); this one is what larger expert counts are trained with.
+ */
+
+/* Scores of the scored router. */
+#define OCCULT_SCORE_SOFTMAX 0
+#define OCCULT_SCORE_SIGMOID 1
+/* Groups of experts a token's choice may be limited to. */
+#define OCCULT_GROUP_BLOCKS  0   /* n_experts / n_groups consecutive experts           */
+#define OCCULT_GROUP_VDEV    1   /* the experts of a virtual device (n_groups = n_vdev) */
+
+/* Options of the scored router (host). */
+typedef struct occult_score {
+  int32_t score;        /* OCCULT_SCORE_*                                           */
+  int32_t n_groups;     /* divides n_experts; 1: no groups; <= 32                   */
+  int32_t keep_groups;  /* groups a token may use; they hold at least top_k experts  */
+  int32_t group_best;   /* 1 | 2: a group's worth is the sum of its best 1 or 2      */
+  int32_t group_kind;   /* OCCULT_GROUP_*                                           */
+  float scale;          /* factor of the gates, finite                              */
+  float bias_rate;      /* step of occult_route_bias_step, finite                   */
+} occult_score_t;
+
+/*
+ * occult_route_scored -- the scored router (desc->route_mode must be
+ * OCCULT_ROUTE_EXACT).  Per token, with z its logits and b the bias:
+ *   s_e    = sigmoid(z_e)  or  softmax(z)_e
+ *   rank_e = s_e + b_e with a bias, z_e without one
+ *   worth of a group = sum of the largest group_best (s_e + b_e) of its experts
+ *   ids    = the top_k experts of largest rank among those of the keep_groups groups
+ *            of largest worth, in descending rank; equal ranks (worths) go to the
+ *            lower expert (group)
+ *   gate_j = scale * s_j            (desc->renorm: scale * s_j / sum_i s_i, the sum
+ *            over the chosen; 0 where that sum is 0)
+ * The bias moves the choice, never the gates.
+ *   logits  fp32 [T, Ne].  A logit of -inf, or of fp32's lowest value, switches its
+ *           expert off: s_e = 0, no part of a group's worth (a group without any
+ *           other expert ranks last), and chosen, lowest expert first, only where
+ *           the kept groups have no other left.  A NaN logit ranks as one switched
+ *           off; what the formulas make of it is in the gates.
+ *   bias    fp32 [Ne] nullable; a NaN puts its expert behind every other that is on.
+ *   expert_to_vdev  int32 [Ne] device of each expert, each with Ne/Nd of them.
+ *   ids, gates, vmask  out, as occult_route: for occult_build_brim.
+ * The choice is that of the formula to 64 bits: ranks and worths too near for fp32
+ * are compared in fp64, worths as multiples of 2^-48 (on which sigmoid(x) + sigmoid(-x)
+ * is 1 for every x).
+ * Pointers are 4-byte aligned.
+ */
+int occult_route_scored(const occult_desc_t* desc, const occult_score_t* opt,
+                        const float* logits, const float* bias, const int32_t* expert_to_vdev,
+                        int32_t* ids, float* gates, uint32_t* vmask, occult_stream_t stream);
+
+/*
+ * occult_route_scored_grad -- gradient of sum_tj dgates_tj * gates_tj with respect to
+ * the logits (the choice of experts is piecewise constant).  With u_j = scale dg_j,
+ * S = sum_j s_j over the chosen, and ds_j = u_j, or with desc->renorm
+ * ds_j = (u_j - sum_i u_i s_i / S) / S (0 where S = 0):
+ *   sigmoid  dz_e = sum_{j: id_j = e} ds_j s_e (1 - s_e)
+ *   softmax  dz_e = s_e (sum_{j: id_j = e} ds_j - sum_j ds_j s_j)
+ *   ids      int32 [T, k] from occult_route_scored; one outside [0, Ne) takes no part.
+ *   dgates   fp32 [T, k] (occult_gate_grad);  dlogits  out fp32 [T, Ne], written.
+ * Pointers are 4-byte aligned.
+ */
+int occult_route_scored_grad(const occult_desc_t* desc, const occult_score_t* opt,
+                             const float* logits, const int32_t* ids, const float* dgates,
+                             float* dlogits, occult_stream_t stream);
+
+/*
+ * occult_route_bias_step -- moves the bias towards even loads: with c_e = sum over g of
+ * counts[g, e],  bias_e += opt->bias_rate * sign(sum_i c_i - Ne c_e).
+ *   counts  int32 [G, Ne], the counts of G groups of tokens (of occult_balance_loss);
+ *   bias    fp32 [Ne] in/out.
+ */
+int occult_route_bias_step(const occult_desc_t* desc, const occult_score_t* opt,
+                           const int32_t* counts, int32_t G, float* bias,
+                           occult_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
