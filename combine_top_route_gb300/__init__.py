@@ -51,6 +51,7 @@ SCORE_SOFTMAX = 0
 SCORE_SIGMOID = 1
 GROUP_BLOCKS = 0
 GROUP_VDEV = 1
+MAX_TEACHER = 128                # OCCULT_MAX_TEACHER
 
 
 class occult_desc_t(ctypes.Structure):
@@ -112,6 +113,18 @@ class occult_score_t(ctypes.Structure):
         super().__init__(score, n_groups, keep_groups, group_best, group_kind, scale, bias_rate)
 
 
+class occult_head_t(ctypes.Structure):
+    """Options of the output head (see occult.h)."""
+    _fields_ = [("vocab", ctypes.c_int32), ("topk", ctypes.c_int32),
+                ("grad_dtype", ctypes.c_int32), ("piece", ctypes.c_int32),
+                ("coef", ctypes.c_float), ("coef_kd", ctypes.c_float),
+                ("coef_z", ctypes.c_float), ("temperature", ctypes.c_float)]
+
+    def __init__(self, vocab=1, topk=0, grad_dtype=OCCULT_F32, piece=0, coef=1.0, coef_kd=0.0,
+                 coef_z=0.0, temperature=1.0):
+        super().__init__(vocab, topk, grad_dtype, piece, coef, coef_kd, coef_z, temperature)
+
+
 class OccultError(RuntimeError):
     def __init__(self, fn: str, code: int):
         super().__init__(f"{fn} failed: {code} ({strerror(code)})")
@@ -170,6 +183,9 @@ _SIGNATURES = {
     "occult_route_scored": (ctypes.c_int, [_D] + [_VP] * 8),
     "occult_route_scored_grad": (ctypes.c_int, [_D] + [_VP] * 6),
     "occult_route_bias_step": (ctypes.c_int, [_D, _VP, _VP, _I32, _VP, _VP]),
+    "occult_head_workspace_size": (ctypes.c_int, [_D, _VP, _I32, _VP]),
+    "occult_head_loss": (ctypes.c_int, [_D] + [_VP] * 10 + [_SZ, _VP]),
+    "occult_head_step": (ctypes.c_int, [_D] + [_VP] * 13 + [_SZ, _VP]),
     "occult_profile_coact": (ctypes.c_int, [_D, _VP, _I32, _VP, _VP, _VP, _VP, _VP,
                                             ctypes.c_size_t, _VP]),
 }
@@ -783,6 +799,49 @@ def occult_route_bias_step(desc, opt, counts, bias, stream=None):
     G = counts.numel() // max(1, Ne)
     _call("occult_route_bias_step", desc, ctypes.byref(opt), _at(counts, _I32T, G * Ne, "counts"),
           G, _at(bias, _F32, Ne, "bias"), _on(stream))
+
+
+def head_workspace_size(desc, opt, step=True) -> int:
+    """Device workspace bytes of occult_head_step, or of occult_head_loss."""
+    n = ctypes.c_size_t(0)
+    _call("occult_head_workspace_size", desc, ctypes.byref(opt), 1 if step else 0, ctypes.byref(n))
+    return n.value
+
+
+def occult_head_loss(desc, opt, x, w, loss, ws, labels=None, teacher_ids=None,
+                     teacher_logits=None, lse=None, token_loss=None, stream=None):
+    """Losses of the output head over a vocabulary, without its logits."""
+    T, d, n = desc.T, desc.d, desc.T * opt.topk
+    dt = _BF if desc.dtype == OCCULT_BF16 else _F32
+    if x is None or w is None or loss is None or ws is None:
+        _need(x=x, w=w, loss=loss, ws=ws)
+    rc = lib().occult_head_loss(
+        desc, ctypes.byref(opt), _at(x, dt, T * d, "x"), _at(w, dt, opt.vocab * d, "w"),
+        _at(labels, _I32T, T, "labels"), _at(teacher_ids, _I32T, n, "teacher_ids"),
+        _at(teacher_logits, _F32, n, "teacher_logits"), _at(lse, _F32, T, "lse"),
+        _at(token_loss, _F32, T, "token_loss"), _at(loss, _F32, 4, "loss"), _at(ws, _U8, 0, "ws"),
+        ws.numel(), _on(stream))
+    if rc:
+        raise OccultError("occult_head_loss", rc)
+
+
+def occult_head_step(desc, opt, x, w, loss, ws, dx=None, dw=None, labels=None, teacher_ids=None,
+                     teacher_logits=None, dloss=None, lse=None, token_loss=None, stream=None):
+    """Losses of the output head and the gradients of x and w."""
+    T, d, n = desc.T, desc.d, desc.T * opt.topk
+    dt = _BF if desc.dtype == OCCULT_BF16 else _F32
+    gt = _BF if opt.grad_dtype == OCCULT_BF16 else _F32
+    if x is None or w is None or loss is None or ws is None:
+        _need(x=x, w=w, loss=loss, ws=ws)
+    rc = lib().occult_head_step(
+        desc, ctypes.byref(opt), _at(x, dt, T * d, "x"), _at(w, dt, opt.vocab * d, "w"),
+        _at(labels, _I32T, T, "labels"), _at(teacher_ids, _I32T, n, "teacher_ids"),
+        _at(teacher_logits, _F32, n, "teacher_logits"), _at(dloss, _F32, 1, "dloss"),
+        _at(lse, _F32, T, "lse"), _at(token_loss, _F32, T, "token_loss"),
+        _at(loss, _F32, 4, "loss"), _at(dx, gt, T * d, "dx"), _at(dw, gt, opt.vocab * d, "dw"),
+        _at(ws, _U8, 0, "ws"), ws.numel(), _on(stream))
+    if rc:
+        raise OccultError("occult_head_step", rc)
 
 
 _RECORD = struct.Struct("7Q2q2i")   # occult_param_t

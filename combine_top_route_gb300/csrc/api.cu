@@ -6,6 +6,7 @@
 #include <mutex>
 
 #include "common.cuh"
+#include "head.h"
 #include "kernels.h"
 
 namespace occult {
@@ -1051,6 +1052,77 @@ int occult_route_bias_step(const occult_desc_t* desc, const occult_score_t* opt,
   OCCULT_REQUIRE(G >= 1 && counts && bias && aligned(4, {counts, bias}));
   OCCULT_CTX(stream);
   return launch_route_bias_step(ctx, desc->n_experts, counts, G, opt->bias_rate, bias);
+}
+
+static int check_head(const occult_desc_t* desc, const occult_head_t* opt) {
+  int rc = check(desc);
+  if (rc) return rc;
+  OCCULT_REQUIRE(opt && opt->vocab >= 1 && opt->topk >= 0 && opt->piece >= 0);
+  OCCULT_REQUIRE(opt->grad_dtype == OCCULT_F32 || opt->grad_dtype == OCCULT_BF16);
+  // (comparisons that a NaN fails)
+  OCCULT_REQUIRE(opt->coef >= 0.f && opt->coef < 1e30f && opt->coef_kd >= 0.f &&
+                 opt->coef_kd < 1e30f && opt->coef_z >= 0.f && opt->coef_z < 1e30f);
+  OCCULT_REQUIRE(opt->topk == 0 || (opt->temperature >= 0.25f && opt->temperature <= 10.f));
+  if (opt->topk > OCCULT_MAX_TEACHER || desc->d > 16384 || opt->vocab > (1 << 28))
+    return OCCULT_ERR_UNSUPPORTED;
+  return static_cast<int64_t>(desc->T) * (opt->topk + 1) < (1ll << 31) ? OCCULT_OK
+                                                                       : OCCULT_ERR_UNSUPPORTED;
+}
+
+int occult_head_workspace_size(const occult_desc_t* desc, const occult_head_t* opt, int32_t step,
+                               size_t* bytes) {
+  int rc = check_head(desc, opt);
+  if (rc) return rc;
+  OCCULT_REQUIRE(bytes && (step == 0 || step == 1));
+  *bytes = head_plan(*desc, *opt, step != 0).total;
+  return OCCULT_OK;
+}
+
+// What both calls of the head check and run.
+static int head_call(const occult_desc_t* desc, const occult_head_t* opt, const HeadArgs& a,
+                     bool step, size_t ws_bytes, occult_stream_t stream) {
+  int rc = check_head(desc, opt);
+  if (rc) return rc;
+  OCCULT_REQUIRE(a.loss && a.w && (!step || a.dx || a.dw));
+  OCCULT_REQUIRE(desc->T == 0 || (a.x && (a.labels || opt->topk > 0)));
+  OCCULT_REQUIRE(desc->T == 0 || (opt->topk > 0 ? a.t_ids && a.t_logits : !a.t_ids && !a.t_logits));
+  OCCULT_REQUIRE(desc->T == 0 || !a.token_loss || a.labels);
+  OCCULT_REQUIRE(aligned16({a.x, a.w, a.dx, a.dw, a.ws}));
+  OCCULT_REQUIRE(aligned(4, {a.labels, a.t_ids, a.t_logits, a.dloss, a.lse, a.token_loss, a.loss}));
+  const HeadPlan p = head_plan(*desc, *opt, step);
+  if (ws_bytes < p.total || !a.ws) return OCCULT_ERR_WORKSPACE;
+  OCCULT_CTX(stream);
+  if (desc->T == 0) {
+    // no tokens: no loss, and no gradient of the weights
+    rc = launch_zero_f32(ctx, a.loss, 4);
+    const size_t n = static_cast<size_t>(opt->vocab) * desc->d;
+    if (!rc && a.dw)
+      rc = launch_zero_f32(ctx, static_cast<float*>(a.dw), opt->grad_dtype == OCCULT_BF16 ? n / 2 : n);
+    return rc;
+  }
+  return launch_head(ctx, p, a);
+}
+
+int occult_head_loss(const occult_desc_t* desc, const occult_head_t* opt, const void* x,
+                     const void* w, const int32_t* labels, const int32_t* teacher_ids,
+                     const float* teacher_logits, float* lse, float* token_loss, float* loss,
+                     void* ws, size_t ws_bytes, occult_stream_t stream) {
+  HeadArgs a{};
+  a.x = x; a.w = w; a.labels = labels; a.t_ids = teacher_ids; a.t_logits = teacher_logits;
+  a.lse = lse; a.token_loss = token_loss; a.loss = loss; a.ws = static_cast<char*>(ws);
+  return head_call(desc, opt, a, false, ws_bytes, stream);
+}
+
+int occult_head_step(const occult_desc_t* desc, const occult_head_t* opt, const void* x,
+                     const void* w, const int32_t* labels, const int32_t* teacher_ids,
+                     const float* teacher_logits, const float* dloss, float* lse,
+                     float* token_loss, float* loss, void* dx, void* dw, void* ws,
+                     size_t ws_bytes, occult_stream_t stream) {
+  HeadArgs a{};
+  a.x = x; a.w = w; a.labels = labels; a.t_ids = teacher_ids; a.t_logits = teacher_logits;
+  a.dloss = dloss; a.lse = lse; a.token_loss = token_loss; a.loss = loss; a.dx = dx; a.dw = dw;
+  a.ws = static_cast<char*>(ws);
+  return head_call(desc, opt, a, true, ws_bytes, stream);
 }
 
 }  // extern "C"

@@ -58,6 +58,7 @@
 #include <mutex>
 
 #include "common.cuh"
+#include "head.h"
 #include "kernels.h"
 
 namespace occult {
@@ -1522,6 +1523,11 @@ int launch_grouped_gemm_bf16(const LaunchCtx& ctx, const GroupedGemm& g) {
                   : launch_tc<OP_TMA_MN, OP_TMA_MN, EPI_F32, true, false>(ctx, ma, mb, mc, md, p);
   }
   return OCCULT_ERR_UNSUPPORTED;
+}
+
+int tensor_map_bf16(CUtensorMap* m, const void* base, int64_t rows, int64_t cols,
+                    uint32_t box_cols, uint32_t box_rows) {
+  return make_map(m, base, rows, cols, box_cols, box_rows);
 }
 
 }  // namespace occult

@@ -1,0 +1,672 @@
+// The output head: everything around its products.
+//
+// A call goes: rows (which tokens a term counts, compacted) -> entries (each row's label
+// and teacher tokens, sorted by id, with the teacher's probabilities) -> the product with
+// its maxima, sums and entries' logits -> the rows' losses and their means -> (step) the
+// gradient of the logits, put together from the kept logits -> dx and dw.
+//
+// Softmax over the vocabulary is done in powers of two: y = z log2(e), and with m the
+// maximum of a row's part, sum 2^(y - m); the parts of a row (128 columns each) are
+// joined at the end.  The gradient of a logit is then
+//   dz_v = k1 2^(y_v - L) + k2 2^(y_v / tau - L') - (at the entries) their factors,
+// L and L' the rows' log2 of the sums at temperature 1 and tau.  Its common factor
+// (coef / N) is left to the fp32 sums of dx and dw.
+#include <algorithm>
+
+#include "head.h"
+#include "kernels.h"
+
+namespace occult {
+
+namespace {
+
+constexpr uint32_t kFull = 0xffffffffu;
+
+__device__ __forceinline__ float ex2(float v) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+  return v;
+}
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, o));
+  return v;
+}
+
+enum : uint8_t { kRowCe = 1, kRowKd = 2 };
+
+// ---- rows -----------------------------------------------------------------------
+// One block: thread i takes a run of consecutive tokens, counts those that a term
+// counts, and writes their rows behind those of the threads before it.
+__global__ void __launch_bounds__(1024)
+head_rows_kernel(const int32_t* __restrict__ labels, const int32_t* __restrict__ t_ids, int T,
+                 int V, int K, HeadCounts* cnt, int32_t* __restrict__ idx,
+                 int32_t* __restrict__ pos, uint8_t* __restrict__ flag, int32_t* __restrict__ ent,
+                 float* __restrict__ ent_q, float* __restrict__ lse, float* __restrict__ token_loss) {
+  __shared__ int s_n[32], s_ce[32], s_kd[32];
+  pdl_wait();
+  pdl_trigger();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = (T + 1023) / 1024;
+  const int t0 = min(T, tid * per), t1 = min(T, t0 + per);
+  auto flag_of = [&](int t) -> int {
+    int f = 0;
+    if (labels && static_cast<unsigned>(labels[t]) < static_cast<unsigned>(V)) f |= kRowCe;
+    if (K && static_cast<unsigned>(t_ids[static_cast<size_t>(t) * K]) < static_cast<unsigned>(V)) f |= kRowKd;
+    return f;
+  };
+  int n = 0, ce = 0, kd = 0;
+  for (int t = t0; t < t1; ++t) {
+    const int f = flag_of(t);
+    n += f != 0;
+    ce += (f & kRowCe) != 0;
+    kd += (f & kRowKd) != 0;
+  }
+  int incl = n;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(kFull, incl, o);
+    if (lane >= o) incl += v;
+  }
+  ce = __reduce_add_sync(kFull, ce);
+  kd = __reduce_add_sync(kFull, kd);
+  if (lane == 31) { s_n[warp] = incl; s_ce[warp] = ce; s_kd[warp] = kd; }
+  __syncthreads();
+  int before = 0, all = 0, all_ce = 0, all_kd = 0;
+  for (int w = 0; w < 32; ++w) {
+    if (w < warp) before += s_n[w];
+    all += s_n[w];
+    all_ce += s_ce[w];
+    all_kd += s_kd[w];
+  }
+  int r = before + incl - n;
+  for (int t = t0; t < t1; ++t) {
+    const int f = flag_of(t);
+    if (f) {
+      idx[r] = t;
+      flag[r] = static_cast<uint8_t>(f);
+      if (K == 0) {   // the label is a row's only entry
+        ent[r] = labels[t];
+        ent_q[r] = -1.f;
+      }
+      pos[t] = r++;
+    } else {
+      pos[t] = -1;
+      if (lse) lse[t] = 0.f;
+      if (token_loss) token_loss[t] = 0.f;
+    }
+  }
+  if (tid == 0) {
+    cnt->n = all;
+    cnt->n_ce = all_ce;
+    cnt->n_kd = all_kd;
+    cnt->ticket = 0;
+  }
+}
+
+// ---- compact copy of x (bf16) -----------------------------------------------------
+// Only where some token is left out: the products read x itself otherwise.  Rows up to
+// the next multiple of 64 are zeros, so that dw's reduction may run over them.
+__global__ void __launch_bounds__(256)
+head_gather_kernel(const uint4* __restrict__ x, uint4* __restrict__ xc, const HeadCounts* cnt,
+                   const int32_t* __restrict__ idx, int T, int vecs) {
+  pdl_wait();
+  pdl_trigger();
+  const int n = cnt->n;
+  if (n == T) return;
+  const int rows = min((n + 63) & ~63, (T + kHeadRowAlign - 1) / kHeadRowAlign * kHeadRowAlign);
+  for (int r = blockIdx.x; r < rows; r += gridDim.x) {
+    const uint4* src = r < n ? x + static_cast<size_t>(idx[r]) * vecs : nullptr;
+    uint4* dst = xc + static_cast<size_t>(r) * vecs;
+    for (int i = threadIdx.x; i < vecs; i += blockDim.x) dst[i] = src ? src[i] : make_uint4(0, 0, 0, 0);
+  }
+}
+
+// ---- entries ----------------------------------------------------------------------
+// One warp a row: the teacher's probabilities at temperature tau, and the row's entries
+// (label: q = -1) in ascending token order, absent ones behind.
+constexpr int kEntWarps = 4;
+__global__ void __launch_bounds__(kEntWarps * 32)
+head_entries_kernel(const int32_t* __restrict__ labels, const int32_t* __restrict__ t_ids,
+                    const float* __restrict__ t_logits, const HeadCounts* cnt,
+                    const int32_t* __restrict__ idx, uint8_t* __restrict__ flag, int V, int K,
+                    float inv_tau, int32_t* __restrict__ ent, float* __restrict__ ent_q) {
+  constexpr int kPer = (OCCULT_MAX_TEACHER + 1 + 31) / 32;
+  __shared__ int s_id[kEntWarps][32 * kPer];
+  pdl_wait();
+  pdl_trigger();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int n = cnt->n, E = K + 1;
+  int* ids = s_id[warp];
+  for (int r = blockIdx.x * kEntWarps + warp; r < n; r += gridDim.x * kEntWarps) {
+    const size_t t = idx[r];
+    const int f = flag[r];
+    int id[kPer];
+    float q[kPer];
+    float top = -__int_as_float(0x7f800000);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int j = lane + 32 * i;
+      id[i] = kHeadNoEntry;
+      q[i] = -__int_as_float(0x7f800000);
+      if (j < K && (f & kRowKd)) {
+        const int v = t_ids[t * K + j];
+        if (static_cast<unsigned>(v) < static_cast<unsigned>(V)) {
+          id[i] = v;
+          q[i] = t_logits[t * K + j] * inv_tau;
+          top = fmaxf(top, q[i]);
+        }
+      }
+    }
+    top = warp_max(top);
+    if (top == -__int_as_float(0x7f800000)) top = 0.f;
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      q[i] = id[i] == kHeadNoEntry ? 0.f : expf(q[i] - top);
+      sum += q[i];
+    }
+    sum = warp_sum(sum);
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    // nothing to learn from: its term is 0, and so is its gradient
+    if (sum == 0.f && lane == 0) flag[r] = static_cast<uint8_t>(f & ~kRowKd);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int j = lane + 32 * i;
+      q[i] *= inv;
+      if (j == K) {
+        id[i] = (f & kRowCe) ? labels[t] : kHeadNoEntry;
+        q[i] = -1.f;
+      }
+      ids[j] = j < E ? id[i] : kHeadNoEntry;
+    }
+    __syncwarp();
+    int rank[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) rank[i] = 0;
+    for (int k = 0; k < E; ++k) {
+      const int other = ids[k];
+#pragma unroll
+      for (int i = 0; i < kPer; ++i)
+        rank[i] += (other < id[i] || (other == id[i] && k < lane + 32 * i)) ? 1 : 0;
+    }
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (lane + 32 * i < E) {
+        ent[static_cast<size_t>(r) * E + rank[i]] = id[i];
+        ent_q[static_cast<size_t>(r) * E + rank[i]] = q[i];
+      }
+    __syncwarp();
+  }
+}
+
+// ---- a row's sums, losses and the means ---------------------------------------------
+// A block takes 32 rows: warp w joins the parts w, w + 32, ... of all of them (a lane a
+// row, so that reads run along the rows), then finishes row w.  The last block to arrive
+// adds the blocks' sums in their order.
+constexpr int kSumWarps = 32;
+template <bool TWO>
+__global__ void __launch_bounds__(kSumWarps * 32)
+head_sum_kernel(HeadCounts* cnt, const float* __restrict__ pm, const float* __restrict__ ps,
+                const float* __restrict__ ps2, int ldp, int halves, int row0, int rows_max, int E,
+                const int32_t* __restrict__ idx, const uint8_t* __restrict__ flag,
+                const int32_t* __restrict__ ent, const float* __restrict__ ent_q,
+                const float* __restrict__ zt, float tau, float coef, float coef_kd,
+                float coef_z, float* __restrict__ l1, float* __restrict__ l2,
+                float* __restrict__ lse_out, float* __restrict__ token_out, float* __restrict__ sums,
+                int block0, int n_blocks, float* __restrict__ loss) {
+  __shared__ float s_m[kSumWarps][33], s_s[kSumWarps][33], s_s2[kSumWarps][33];
+  __shared__ float s_ce[32], s_kd[32], s_z[32];
+  __shared__ bool s_last;
+  pdl_wait();
+  pdl_trigger();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int n = min(cnt->n - row0, rows_max);
+  const int r_first = blockIdx.x * 32;
+  const float NEG = -__int_as_float(0x7f800000);
+  const float inv_tau = 1.f / tau;
+  if (r_first < n) {
+    // parts of row r_first + lane
+    const int r = min(r_first + lane, n - 1);
+    float m = NEG, s = 0.f, s2 = 0.f;
+    for (int h0 = warp; h0 < halves; h0 += 4 * kSumWarps) {
+      float vm[4], vs[4], vt[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int h = h0 + u * kSumWarps;
+        const size_t at = static_cast<size_t>(h) * ldp + r;
+        vm[u] = h < halves ? pm[at] : NEG;
+        vs[u] = h < halves ? ps[at] : 0.f;
+        vt[u] = TWO && h < halves ? ps2[at] : 0.f;
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const float hi = fmaxf(m, vm[u]);
+        if (hi == NEG) { s += vs[u]; continue; }   // (a NaN sum stays one)
+        const float fa = ex2(m - hi), fb = ex2(vm[u] - hi);
+        s = s * fa + vs[u] * fb;
+        if (TWO) s2 = s2 * ex2((m - hi) * inv_tau) + vt[u] * ex2((vm[u] - hi) * inv_tau);
+        m = hi;
+      }
+    }
+    s_m[warp][lane] = m;
+    s_s[warp][lane] = s;
+    if (TWO) s_s2[warp][lane] = s2;
+  }
+  __syncthreads();
+  // warp w: row r_first + w
+  const int r = r_first + warp;
+  float ce = 0.f, kd = 0.f, zz = 0.f;
+  if (r < n) {
+    const float m = s_m[lane][warp];
+    const float top = warp_max(m);
+    const float safe = top == NEG ? 0.f : top;
+    const float L = safe + log2f(warp_sum(s_s[lane][warp] * ex2(m - safe)));
+    float L2 = L;
+    if (TWO) L2 = safe * inv_tau + log2f(warp_sum(s_s2[lane][warp] * ex2((m - safe) * inv_tau)));
+    const size_t rg = static_cast<size_t>(row0) + r;
+    const int f = flag[rg];
+    const float lse = L * kLn2;
+    float tok = 0.f;
+    for (int e = lane; e < E; e += 32) {
+      const int id = ent[rg * E + e];
+      if (id == kHeadNoEntry) continue;
+      const float q = ent_q[rg * E + e], z = zt[rg * E + e];
+      if (q < 0.f) tok = lse - z;
+      else if (q != 0.f) kd += q * (logf(q) - (z * inv_tau - L2 * kLn2));
+    }
+    tok = warp_sum(tok);
+    kd = warp_sum(kd);
+    ce = (f & kRowCe) ? tok : 0.f;
+    zz = lse * lse;
+    if (lane == 0) {
+      l1[rg] = L;
+      l2[rg] = L2;
+      const int t = idx[rg];
+      if (lse_out) lse_out[t] = lse;
+      if (token_out) token_out[t] = ce;
+    }
+  }
+  if (lane == 0) { s_ce[warp] = ce; s_kd[warp] = kd; s_z[warp] = zz; }
+  __syncthreads();
+  if (warp == 0) {
+    const float a = warp_sum(s_ce[lane]), b = warp_sum(s_kd[lane]), c = warp_sum(s_z[lane]);
+    if (lane == 0) {
+      float* out = sums + 3 * static_cast<size_t>(block0 + blockIdx.x);
+      out[0] = a;
+      out[1] = b;
+      out[2] = c;
+      __threadfence();
+      s_last = atomicAdd(&cnt->ticket, 1u) == static_cast<unsigned>(n_blocks - 1);
+    }
+  }
+  __syncthreads();
+  if (!s_last) return;
+  __threadfence();
+  // every block of the call is done: each thread adds a run of them, then a tree
+  float a = 0.f, b = 0.f, c = 0.f;
+  for (int i = threadIdx.x; i < n_blocks; i += blockDim.x) {
+    a += __ldcg(sums + 3 * static_cast<size_t>(i));
+    b += __ldcg(sums + 3 * static_cast<size_t>(i) + 1);
+    c += __ldcg(sums + 3 * static_cast<size_t>(i) + 2);
+  }
+  a = warp_sum(a); b = warp_sum(b); c = warp_sum(c);
+  if (lane == 0) { s_ce[warp] = a; s_kd[warp] = b; s_z[warp] = c; }
+  __syncthreads();
+  if (warp == 0) {
+    a = warp_sum(s_ce[lane]); b = warp_sum(s_kd[lane]); c = warp_sum(s_z[lane]);
+    if (lane == 0) {
+      a = cnt->n_ce > 0 ? a / static_cast<float>(cnt->n_ce) : 0.f;
+      b = cnt->n_kd > 0 ? tau * tau * b / static_cast<float>(cnt->n_kd) : 0.f;
+      c = cnt->n > 0 ? c / static_cast<float>(cnt->n) : 0.f;
+      loss[0] = coef * a + coef_kd * b + coef_z * c;
+      loss[1] = a;
+      loss[2] = b;
+      loss[3] = c;
+    }
+  }
+}
+
+// ---- gradient of the logits -----------------------------------------------------------
+struct DzArgs {
+  const HeadCounts* cnt;
+  const float *pm, *l1, *l2;
+  const uint8_t* flag;
+  int ldp, row0, piece, V, ld;
+  float inv_tau, q_step, coef, coef_kd, coef_z, tau;
+  bool two;
+};
+// A row's factors of the two softmaxes.
+__device__ __forceinline__ void row_factors(const DzArgs& a, const HeadScale& sc, int f, float L,
+                                            float& k1, float& k2) {
+  k1 = ((f & kRowCe) ? sc.k_ce : 0.f) + sc.k_z * (L * kLn2);
+  k2 = (f & kRowKd) ? sc.k_kd : 0.f;
+  if (!a.two) {   // one softmax for both
+    k1 += k2;
+    k2 = 0.f;
+  }
+}
+
+// bf16 layers: the kept 16-bit logits (units of q_step octaves below the maximum of
+// their 128 columns) become bf16 gradients where they lie.  A warp takes 32 rows of 128
+// columns: the maxima come in along the rows, 16 lanes read a row's 256 bytes.
+__global__ void __launch_bounds__(256)
+head_dz_bf16_kernel(const DzArgs a, uint16_t* __restrict__ kept) {
+  pdl_wait();
+  pdl_trigger();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int n = min(a.cnt->n - a.row0, a.piece);
+  if (n <= 0) return;
+  const HeadScale sc = head_scale(a.cnt->n, a.cnt->n_ce, a.cnt->n_kd, a.coef, a.coef_kd, a.coef_z, a.tau);
+  const int r0 = blockIdx.y * 32;
+  if (r0 >= ((n + kHeadRowAlign - 1) & ~(kHeadRowAlign - 1))) return;
+  const int h = blockIdx.x * 8 + warp;
+  if (h * 128 >= a.ld) return;
+  const int r = r0 + lane;
+  float m = 0.f, L1 = 0.f, L2 = 0.f, k1 = 0.f, k2 = 0.f;
+  if (r < n) {
+    m = a.pm[static_cast<size_t>(h) * a.ldp + r];
+    if (m == -__int_as_float(0x7f800000)) m = 0.f;
+    L1 = a.l1[a.row0 + r];
+    L2 = a.l2[a.row0 + r];
+    row_factors(a, sc, a.flag[a.row0 + r], L1, k1, k2);
+  }
+  const int c0 = h * 128 + (lane & 15) * 8;
+  char* base = reinterpret_cast<char*>(kept + static_cast<size_t>(r0) * a.ld + c0);
+#pragma unroll 4
+  for (int i = 0; i < 16; ++i) {
+    const int rr = 2 * i + (lane >> 4);
+    const float mm = __shfl_sync(kFull, m, rr), La = __shfl_sync(kFull, L1, rr);
+    const float Lb = __shfl_sync(kFull, L2, rr);
+    const float ka = __shfl_sync(kFull, k1, rr), kb = __shfl_sync(kFull, k2, rr);
+    uint4* at = reinterpret_cast<uint4*>(base + static_cast<size_t>(rr) * a.ld * 2);
+    if (r0 + rr >= n) {
+      *at = make_uint4(0, 0, 0, 0);
+      continue;
+    }
+    const uint4 u = *at;
+    const uint32_t wds[4] = {u.x, u.y, u.z, u.w};
+    float g[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float q = static_cast<float>(j & 1 ? wds[j >> 1] >> 16 : wds[j >> 1] & 0xffffu);
+      const float y = fmaf(q, -a.q_step, mm);
+      g[j] = ka * ex2(y - La);
+      if (a.two) g[j] = fmaf(kb, ex2(fmaf(y, a.inv_tau, -Lb)), g[j]);
+      if (c0 + j >= a.V) g[j] = 0.f;
+    }
+    // (one rounding to bf16: what the tensor cores take)
+    *at = pack16(g, __nv_bfloat16());
+  }
+}
+
+// fp32 layers: the kept logits themselves.
+__global__ void __launch_bounds__(256)
+head_dz_f32_kernel(const DzArgs a, float* __restrict__ kept) {
+  pdl_wait();
+  pdl_trigger();
+  const int n = min(a.cnt->n - a.row0, a.piece);
+  const HeadScale sc = head_scale(a.cnt->n, a.cnt->n_ce, a.cnt->n_kd, a.coef, a.coef_kd, a.coef_z, a.tau);
+  for (int r = blockIdx.y; r < n; r += gridDim.y) {
+    const float L1 = a.l1[a.row0 + r], L2 = a.l2[a.row0 + r];
+    float k1, k2;
+    row_factors(a, sc, a.flag[a.row0 + r], L1, k1, k2);
+    for (int c = blockIdx.x * blockDim.x + threadIdx.x; c < a.V; c += gridDim.x * blockDim.x) {
+      float* at = kept + static_cast<size_t>(r) * a.ld + c;
+      const float z = *at;
+      float g = k1 * exp2f(z * kLog2e - L1);
+      if (a.two) g += k2 * exp2f(z * (kLog2e * a.inv_tau) - L2);
+      *at = g;
+    }
+  }
+}
+
+// The entries' columns: the softmaxes at the entry's own fp32 logit, minus the factors of
+// every entry of that token.
+template <typename G>
+__global__ void __launch_bounds__(256)
+head_dz_entries_kernel(const DzArgs a, const int32_t* __restrict__ ent,
+                       const float* __restrict__ ent_q, const float* __restrict__ zt, int E,
+                       G* __restrict__ dz) {
+  pdl_wait();
+  pdl_trigger();
+  const int n = min(a.cnt->n - a.row0, a.piece);
+  const HeadScale sc = head_scale(a.cnt->n, a.cnt->n_ce, a.cnt->n_kd, a.coef, a.coef_kd, a.coef_z, a.tau);
+  const int64_t total = static_cast<int64_t>(n) * E;
+  for (int64_t i = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; i < total;
+       i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
+    const int r = static_cast<int>(i / E), e = static_cast<int>(i - static_cast<int64_t>(r) * E);
+    const size_t rg = static_cast<size_t>(a.row0) + r, at = rg * E + e;
+    const int id = ent[at];
+    if (id == kHeadNoEntry || (e > 0 && ent[at - 1] == id)) continue;   // the first one writes
+    const float L1 = a.l1[rg], z = zt[at];
+    float k1, k2;
+    row_factors(a, sc, a.flag[rg], L1, k1, k2);
+    float g = k1 * exp2f(z * kLog2e - L1);
+    if (a.two) g += k2 * exp2f(z * (kLog2e * a.inv_tau) - a.l2[rg]);
+    for (int f = e; f < E && ent[at + f - e] == id; ++f) {
+      const float q = ent_q[at + f - e];
+      g -= q < 0.f ? sc.k_ce : sc.k_kd * q;
+    }
+    dz[static_cast<size_t>(r) * a.ld + id] = from_f32<G>(g);
+  }
+}
+
+// ---- dx from its parts (bf16 layers) -----------------------------------------------------
+template <typename O>
+__global__ void __launch_bounds__(256)
+head_dx_kernel(const HeadCounts* cnt, const int32_t* __restrict__ pos, const float* __restrict__ part,
+               int splits, size_t split_stride, int row0, int piece, int T, int d, bool zeros,
+               float coef, float coef_kd, float coef_z, float tau, const float* __restrict__ dloss,
+               O* __restrict__ dx) {
+  pdl_wait();
+  pdl_trigger();
+  const HeadScale sc = head_scale(cnt->n, cnt->n_ce, cnt->n_kd, coef, coef_kd, coef_z, tau);
+  const float g = sc.unit * (dloss ? *dloss : 1.f);
+  constexpr int VN = 16 / sizeof(O);   // elements of a 16-byte store
+  const int vecs = d / VN;
+  for (int t = blockIdx.x; t < T; t += gridDim.x) {
+    const int r = pos[t];
+    const bool mine = r >= row0 && r < row0 + piece;
+    if (!mine && !(r < 0 && zeros)) continue;
+    for (int i = threadIdx.x; i < vecs; i += blockDim.x) {
+      float v[VN] = {};
+      if (mine)
+        for (int s = 0; s < splits; ++s) {
+          const float4* src = reinterpret_cast<const float4*>(
+              part + s * split_stride + static_cast<size_t>(r - row0) * d + i * VN);
+#pragma unroll
+          for (int j = 0; j < VN / 4; ++j) {
+            const float4 u = src[j];
+            v[4 * j] += u.x; v[4 * j + 1] += u.y; v[4 * j + 2] += u.z; v[4 * j + 3] += u.w;
+          }
+        }
+#pragma unroll
+      for (int j = 0; j < VN; ++j) v[j] *= g;
+      *reinterpret_cast<uint4*>(dx + static_cast<size_t>(t) * d + i * VN) = pack16(v, O());
+    }
+  }
+}
+
+size_t up(size_t v, size_t a) { return (v + a - 1) / a * a; }
+
+}  // namespace
+
+// Parts of dx's reduction over the vocabulary: as many as leave the fewest rounds of
+// tiles idle, where a part more costs its share of the fp32 sums written and read
+// (about 1/64 of a product of that depth).
+static int dx_splits(int rows, int d, int V) {
+  const bool pair = rows > 128;
+  const int64_t units = static_cast<int64_t>((rows + (pair ? 255 : 127)) / (pair ? 256 : 128)) *
+                        ((d + 255) / 256);
+  const int64_t slots = pair ? 76 : 152;   // CTA pairs or CTAs of a GB300
+  const int most = std::max(1, std::min(64, (V + 1023) / 1024));
+  int best = 1;
+  double best_t = 1e300;
+  for (int s = 1; s <= most; ++s) {
+    const double t = static_cast<double>((units * s + slots - 1) / slots) / s + s / 64.0;
+    if (t < best_t - 1e-12) { best_t = t; best = s; }
+  }
+  return best;
+}
+
+// Width of the logits' tiles: 256 columns, or what leaves the last round of a small batch
+// fuller (each tile costs some 24 columns' time besides its own).
+static int tile_width(int rows, int V) {
+  const bool pair = rows > 128;
+  const int64_t m = (rows + (pair ? 255 : 127)) / (pair ? 256 : 128);
+  const int64_t slots = pair ? 76 : 152;
+  int best = 256;
+  int64_t best_t = (((V + 255) / 256) * m + slots - 1) / slots * (256 + 24);
+  for (int bn = 224; bn >= 64; bn -= 32) {
+    const int64_t t = (((V + bn - 1) / bn) * m + slots - 1) / slots * (bn + 24);
+    if (t < best_t) { best_t = t; best = bn; }
+  }
+  return best;
+}
+
+HeadPlan head_plan(const occult_desc_t& ds, const occult_head_t& opt, bool step) {
+  HeadPlan p{};
+  p.T = ds.T; p.d = ds.d; p.V = opt.vocab; p.K = opt.topk; p.E = opt.topk + 1;
+  p.dtype = ds.dtype; p.grad_dtype = opt.grad_dtype; p.step = step;
+  p.tau = p.K ? opt.temperature : 1.f;
+  p.coef = opt.coef; p.coef_kd = p.K ? opt.coef_kd : 0.f; p.coef_z = opt.coef_z;
+  p.two = p.K > 0 && opt.temperature != 1.f;
+  const bool bf = ds.dtype == OCCULT_BF16;
+  const int Tr = static_cast<int>(up(std::max(1, ds.T), kHeadRowAlign));
+  p.ld = static_cast<int>(up(p.V, 256));
+  const int64_t row_bytes = static_cast<int64_t>(p.ld) * (bf ? 2 : 4);
+  int64_t piece = opt.piece > 0 ? opt.piece : (int64_t(1) << 30) / row_bytes;
+  piece = std::min<int64_t>(1 << 19, piece);   // (a grid's second dimension)
+  piece = std::max<int64_t>(kHeadRowAlign, piece / kHeadRowAlign * kHeadRowAlign);
+  p.piece = step ? static_cast<int>(std::min<int64_t>(piece, Tr)) : Tr;
+  p.n_pieces = (Tr + p.piece - 1) / p.piece;
+  // (the gradient of the logits is put together in parts of 128 columns)
+  p.bn = !bf ? 128 : step ? 256 : tile_width(std::min(p.piece, std::max(1, ds.T)), p.V);
+  p.n_tiles = (p.V + p.bn - 1) / p.bn;
+  p.halves = 2 * p.n_tiles;
+  p.splits = bf && step ? dx_splits(std::min(p.piece, std::max(1, ds.T)), p.d, p.V) : 1;
+  p.q_step = std::max(24.f, 20.f * p.tau) / 65535.f;
+  size_t o = 0;
+  auto take = [&](size_t bytes) { const size_t at = o; o += up(bytes, 256); return at; };
+  const size_t T = Tr, P = p.piece;
+  p.o_cnt = take(sizeof(HeadCounts));
+  p.o_idx = take(4 * T); p.o_pos = take(4 * T); p.o_flag = take(T);
+  p.o_ent = take(4 * T * p.E); p.o_q = take(4 * T * p.E); p.o_zt = take(4 * T * p.E);
+  p.o_xc = take(bf ? T * p.d * 2 : 0);
+  p.o_m = take(4 * P * p.halves); p.o_s = take(4 * P * p.halves);
+  p.o_s2 = take(p.two ? 4 * P * p.halves : 0);
+  p.o_l1 = take(4 * T); p.o_l2 = take(4 * T);
+  p.o_sum = take(12 * (T / 32 + p.n_pieces));
+  p.o_kept = take(step ? P * row_bytes : 0);
+  p.o_part = take(bf && step ? 4 * static_cast<size_t>(p.splits) * P * p.d : 0);
+  p.o_acc = take(step && p.n_pieces > 1 && p.grad_dtype == OCCULT_BF16
+                     ? 4 * static_cast<size_t>(p.V) * p.d : 0);
+  p.total = o;
+  return p;
+}
+
+int launch_head(const LaunchCtx& ctx, const HeadPlan& p, const HeadArgs& a) {
+  char* ws = a.ws;
+  auto* cnt = reinterpret_cast<HeadCounts*>(ws + p.o_cnt);
+  auto* idx = reinterpret_cast<int32_t*>(ws + p.o_idx);
+  auto* pos = reinterpret_cast<int32_t*>(ws + p.o_pos);
+  auto* flag = reinterpret_cast<uint8_t*>(ws + p.o_flag);
+  auto* ent = reinterpret_cast<int32_t*>(ws + p.o_ent);
+  auto* ent_q = reinterpret_cast<float*>(ws + p.o_q);
+  auto* zt = reinterpret_cast<float*>(ws + p.o_zt);
+  auto* pm = reinterpret_cast<float*>(ws + p.o_m);
+  auto* ps = reinterpret_cast<float*>(ws + p.o_s);
+  auto* ps2 = reinterpret_cast<float*>(ws + p.o_s2);
+  auto* l1 = reinterpret_cast<float*>(ws + p.o_l1);
+  auto* l2 = reinterpret_cast<float*>(ws + p.o_l2);
+  auto* sums = reinterpret_cast<float*>(ws + p.o_sum);
+  auto* part = reinterpret_cast<float*>(ws + p.o_part);
+  const bool bf = p.dtype == OCCULT_BF16;
+  cudaError_t e = launch_pdl(head_rows_kernel, 1, 1024, 0, ctx.stream, a.labels, a.t_ids, p.T, p.V, p.K,
+                             cnt, idx, pos, flag, ent, ent_q, a.lse, a.token_loss);
+  if (e != cudaSuccess) return OCCULT_ERR_CUDA;
+  if (bf) {
+    e = launch_pdl(head_gather_kernel, std::min(p.T + 63, ctx.num_sms * 8), 256, 0, ctx.stream,
+                   static_cast<const uint4*>(a.x), reinterpret_cast<uint4*>(ws + p.o_xc), cnt, idx,
+                   p.T, p.d / 8);
+    if (e != cudaSuccess) return OCCULT_ERR_CUDA;
+  }
+  if (p.K) {
+    e = launch_pdl(head_entries_kernel, std::min((p.T + kEntWarps - 1) / kEntWarps, ctx.num_sms * 16),
+                   kEntWarps * 32, 0, ctx.stream, a.labels, a.t_ids, a.t_logits, cnt, idx, flag, p.V,
+                   p.K, 1.f / p.tau, ent, ent_q);
+    if (e != cudaSuccess) return OCCULT_ERR_CUDA;
+  }
+  int n_blocks = 0;
+  for (int i = 0; i < p.n_pieces; ++i)
+    n_blocks += (std::min(p.piece, p.T - i * p.piece) + 31) / 32;
+  int block0 = 0;
+  for (int i = 0; i < p.n_pieces; ++i) {
+    const int row0 = i * p.piece, rows = std::min(p.piece, p.T - row0);
+    int rc = bf ? launch_head_logits_bf16(ctx, p, a, row0) : launch_head_logits_f32(ctx, p, a, row0);
+    if (rc) return rc;
+    const int blocks = (rows + 31) / 32;
+    e = launch_pdl(p.two ? head_sum_kernel<true> : head_sum_kernel<false>, blocks, kSumWarps * 32, 0,
+                   ctx.stream, cnt, pm, ps, ps2, p.piece, p.halves, row0, rows, p.E, idx, flag, ent,
+                   ent_q, zt, p.tau, p.coef, p.coef_kd, p.coef_z, l1, l2, a.lse, a.token_loss,
+                   sums, block0, n_blocks, a.loss);
+    if (e != cudaSuccess) return OCCULT_ERR_CUDA;
+    block0 += blocks;
+    if (!p.step) continue;
+    DzArgs z{};
+    z.cnt = cnt; z.pm = pm; z.l1 = l1; z.l2 = l2; z.flag = flag;
+    z.ldp = p.piece; z.row0 = row0; z.piece = p.piece; z.V = p.V; z.ld = p.ld;
+    z.inv_tau = 1.f / p.tau; z.q_step = p.q_step; z.tau = p.tau;
+    z.coef = p.coef; z.coef_kd = p.coef_kd; z.coef_z = p.coef_z;
+    z.two = p.two;
+    const int eb = static_cast<int>(std::min<int64_t>((static_cast<int64_t>(rows) * p.E + 255) / 256,
+                                                      ctx.num_sms * 16));
+    if (bf) {
+      auto* kept = reinterpret_cast<uint16_t*>(ws + p.o_kept);
+      const dim3 grid((p.ld / 128 + 7) / 8, (rows + kHeadRowAlign - 1) / kHeadRowAlign * (kHeadRowAlign / 32));
+      e = launch_pdl(head_dz_bf16_kernel, grid, 256, 0, ctx.stream, z, kept);
+      if (e != cudaSuccess) return OCCULT_ERR_CUDA;
+      e = launch_pdl(head_dz_entries_kernel<__nv_bfloat16>, eb, 256, 0, ctx.stream, z, ent, ent_q, zt,
+                     p.E, reinterpret_cast<__nv_bfloat16*>(kept));
+    } else {
+      auto* kept = reinterpret_cast<float*>(ws + p.o_kept);
+      const dim3 grid(std::min((p.V + 255) / 256, 64), std::min(rows, 4096));
+      e = launch_pdl(head_dz_f32_kernel, grid, 256, 0, ctx.stream, z, kept);
+      if (e != cudaSuccess) return OCCULT_ERR_CUDA;
+      e = launch_pdl(head_dz_entries_kernel<float>, eb, 256, 0, ctx.stream, z, ent, ent_q, zt, p.E, kept);
+    }
+    if (e != cudaSuccess) return OCCULT_ERR_CUDA;
+    if (a.dx) {
+      rc = bf ? launch_head_dx_bf16(ctx, p, a, row0) : launch_head_dx_f32(ctx, p, a, row0);
+      if (rc) return rc;
+      if (bf) {
+        const int nb = std::min(p.T, ctx.num_sms * 8);
+        const size_t stride = static_cast<size_t>(p.piece) * p.d;
+        if (p.grad_dtype == OCCULT_BF16)
+          e = launch_pdl(head_dx_kernel<__nv_bfloat16>, nb, 256, 0, ctx.stream, cnt, pos, part, p.splits,
+                         stride, row0, p.piece, p.T, p.d, i == 0, p.coef, p.coef_kd, p.coef_z, p.tau,
+                         a.dloss, static_cast<__nv_bfloat16*>(a.dx));
+        else
+          e = launch_pdl(head_dx_kernel<float>, nb, 256, 0, ctx.stream, cnt, pos, part, p.splits,
+                         stride, row0, p.piece, p.T, p.d, i == 0, p.coef, p.coef_kd, p.coef_z, p.tau,
+                         a.dloss, static_cast<float*>(a.dx));
+        if (e != cudaSuccess) return OCCULT_ERR_CUDA;
+      }
+    }
+    if (a.dw) {
+      const bool first = i == 0, last = i == p.n_pieces - 1;
+      rc = bf ? launch_head_dw_bf16(ctx, p, a, row0, first, last)
+              : launch_head_dw_f32(ctx, p, a, row0, first, last);
+      if (rc) return rc;
+    }
+  }
+  return OCCULT_OK;
+}
+
+}  // namespace occult

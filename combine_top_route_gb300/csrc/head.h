@@ -1,0 +1,93 @@
+// What the output head's parts share: the host's plan of a call and the scalars that
+// its kernels take (head.cu: rows, entries, sums, gradients of the logits; head_gemm.cu:
+// the products of bf16 layers; head_simt.cu: those of fp32 layers).
+#pragma once
+
+#include "common.cuh"
+
+namespace occult {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kHeadRowAlign = 256;   // rows of a piece and of its buffers
+constexpr int kHeadNoEntry = 0x7fffffff;
+
+// Device counters at the head of the workspace.
+struct HeadCounts {
+  int n;        // tokens that a term counts: compact rows
+  int n_ce;     // of them with a label
+  int n_kd;     // of them with a teacher row
+  unsigned ticket;
+};
+
+// Sizes and workspace offsets of a call; every launcher works from one of these.
+struct HeadPlan {
+  int T, d, V, K, E;        // E = K + 1 entries a row: the teacher's and the label
+  int dtype, grad_dtype;
+  bool step, two;           // two: sums at temperature 1 and tau
+  int piece, n_pieces;      // tokens of a piece (a multiple of kHeadRowAlign)
+  int ld;                   // columns of the kept logits
+  int bn;                   // vocabulary columns of a tile
+  int n_tiles, halves;      // tiles, and partial sums a row
+  int splits;               // parts of the reduction of dx
+  float tau, coef, coef_kd, coef_z;
+  float q_step;             // octaves of a unit of the kept 16-bit logits
+  // workspace
+  size_t o_cnt, o_idx, o_pos, o_flag, o_ent, o_q, o_zt, o_xc, o_m, o_s, o_s2, o_l1, o_l2, o_sum,
+      o_kept, o_part, o_acc, total;
+};
+
+struct HeadArgs {
+  const void* x;
+  const void* w;
+  const int32_t* labels;
+  const int32_t* t_ids;
+  const float* t_logits;
+  const float* dloss;
+  float *lse, *token_loss, *loss;
+  void *dx, *dw;
+  char* ws;
+};
+
+// Factors of a term's gradient over the mean of its tokens, and the common factor that
+// is kept out of the rounded gradients of the logits: the cross entropy's where it
+// counts, so that its -1 at the label is exact.
+struct HeadScale {
+  float unit;      // common factor
+  float k_ce, k_kd, k_z;   // coef / N_ce, coef_kd tau / N_kd, 2 coef_z / N over it
+};
+__host__ __device__ inline HeadScale head_scale(int n, int n_ce, int n_kd, float coef,
+                                                float coef_kd, float coef_z, float tau) {
+  HeadScale s;
+  const float a = n_ce > 0 ? coef / static_cast<float>(n_ce) : 0.f;
+  const float b = n_kd > 0 ? coef_kd * tau / static_cast<float>(n_kd) : 0.f;
+  const float c = n > 0 ? 2.f * coef_z / static_cast<float>(n) : 0.f;
+  s.unit = a > 0.f ? a : b > 0.f ? b : c > 0.f ? c : 1.f;
+  s.k_ce = a / s.unit;
+  s.k_kd = b / s.unit;
+  s.k_z = c / s.unit;
+  return s;
+}
+
+HeadPlan head_plan(const occult_desc_t& ds, const occult_head_t& opt, bool step);
+int launch_head(const LaunchCtx& ctx, const HeadPlan& p, const HeadArgs& a);
+
+// Products of bf16 layers over the rows [row0, row0 + piece) of the compact rows.
+//  logits: partial maxima and sums, the logits of the entries, and (step) the logits in
+//          16 bits;  dx: parts [splits][piece][d] fp32;  dw: written (first piece) or
+//          added to, scaled.
+int launch_head_logits_bf16(const LaunchCtx& ctx, const HeadPlan& p, const HeadArgs& a, int row0);
+int launch_head_dx_bf16(const LaunchCtx& ctx, const HeadPlan& p, const HeadArgs& a, int row0);
+int launch_head_dw_bf16(const LaunchCtx& ctx, const HeadPlan& p, const HeadArgs& a, int row0,
+                        bool first, bool last);
+// The same of fp32 layers; dx is written to its tokens' rows.
+int launch_head_logits_f32(const LaunchCtx& ctx, const HeadPlan& p, const HeadArgs& a, int row0);
+int launch_head_dx_f32(const LaunchCtx& ctx, const HeadPlan& p, const HeadArgs& a, int row0);
+int launch_head_dw_f32(const LaunchCtx& ctx, const HeadPlan& p, const HeadArgs& a, int row0,
+                       bool first, bool last);
+
+// 2-D bf16 tensor map of a row-major [rows, cols] matrix, 128-byte swizzle.
+int tensor_map_bf16(CUtensorMap* m, const void* base, int64_t rows, int64_t cols,
+                    uint32_t box_cols, uint32_t box_rows);
+
+}  // namespace occult

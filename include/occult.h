@@ -907,6 +907,82 @@ int occult_route_bias_step(const occult_desc_t* desc, const occult_score_t* opt,
                            const int32_t* counts, int32_t G, float* bias,
                            occult_stream_t stream);
 
+/*
+ * The output head: the logits z = x w^T of a vocabulary, never stored as a whole, and
+ * the losses on them -- cross entropy against labels, distillation from a teacher's top
+ * logits, and a z term -- with the gradients of x and w.  The paper fine-tunes pruned
+ * models (Sec. 4) and leaves the loss to its host framework.
+ */
+
+/* Largest number of teacher entries a token. */
+#define OCCULT_MAX_TEACHER  128
+
+/* Options of the head (host). */
+typedef struct occult_head {
+  int32_t vocab;        /* V >= 1, rows of w                                        */
+  int32_t topk;         /* K teacher entries a token; 0: no teacher                 */
+  int32_t grad_dtype;   /* type of dx and dw: OCCULT_F32 | OCCULT_BF16              */
+  int32_t piece;        /* tokens of a piece of occult_head_step; 0: as many as keep
+                           the piece's 16-bit logits within 1 GiB                   */
+  float coef;           /* weight of the cross entropy, >= 0                        */
+  float coef_kd;        /* weight of the distillation, >= 0                         */
+  float coef_z;         /* weight of the z term, >= 0                               */
+  float temperature;    /* tau of the distillation, 1/4 .. 10                       */
+} occult_head_t;
+
+/* Host: workspace bytes of occult_head_loss (step = 0) or occult_head_step (1). */
+int occult_head_workspace_size(const occult_desc_t* desc, const occult_head_t* opt, int32_t step,
+                               size_t* bytes);
+
+/*
+ * occult_head_loss -- losses of the head for desc->T tokens of width desc->d.
+ *   x       [T, d] layer dtype;  w  [V, d] layer dtype;  z_tv = sum_i x_ti w_vi.
+ *   labels  int32 [T] nullable: a token whose label lies outside [0, V) is ignored
+ *           by the cross entropy.
+ *   teacher_ids, teacher_logits  int32 and fp32 [T, K], given where topk > 0: the
+ *           teacher's top tokens and their logits, in any order.  A token whose first
+ *           id lies outside [0, V) is ignored by the distillation; other ids outside
+ *           are left out.  A token named twice counts twice.
+ *   ce = mean over its tokens of lse_t - z_{t,label},   lse_t = log sum_v exp z_tv
+ *   q_t = softmax over the entries of teacher_logits / tau,  p = softmax_v(z / tau)
+ *   kd = tau^2 * mean over its tokens of sum_k q_tk (log q_tk - log p_{t,id_k})
+ *   z  = mean over the tokens that ce or kd counts of lse_t^2
+ *   loss    out fp32 [4]: {coef ce + coef_kd kd + coef_z z, ce, kd, z}; a term without
+ *           tokens is 0.  A teacher row whose logits are all -inf adds 0
+ *           (as a counted token), and no gradient.
+ *   lse     out fp32 [T] nullable: lse_t, 0 for tokens that neither term counts.
+ *   token_loss  out fp32 [T] nullable, with labels only: lse_t - z_{t,label}, 0 where
+ *           ignored.
+ *   ws      occult_head_workspace_size bytes.
+ * Rows of x that neither term counts are not used and may hold anything.  Sums run in a
+ * fixed order.  bf16 heads run on the tensor cores (fp32 accumulation).  Pointers are
+ * 16-byte aligned; labels, teacher_*, loss, lse, token_loss and dloss 4-byte.  d <= 16384,
+ * T * (K + 1) < 2^31.
+ */
+int occult_head_loss(const occult_desc_t* desc, const occult_head_t* opt, const void* x,
+                     const void* w, const int32_t* labels, const int32_t* teacher_ids,
+                     const float* teacher_logits, float* lse, float* token_loss, float* loss,
+                     void* ws, size_t ws_bytes, occult_stream_t stream);
+
+/*
+ * occult_head_step -- occult_head_loss and, in the same call, the gradients of loss[0]:
+ *   dz = coef/N_ce (softmax(z) - onehot(label)) + 2 coef_z/N lse softmax(z)
+ *        + coef_kd tau/N_kd (p - scatter(q))
+ *   dx = dloss * dz w,   dw = dloss * dz^T x
+ *   dloss   fp32 [1] device, nullable (1).
+ *   dx      out [T, d] in opt->grad_dtype, nullable: 0 for tokens no term counts.
+ *   dw      out [V, d] in opt->grad_dtype, nullable (dx or dw is needed).  Written.
+ * The batch goes in pieces of opt->piece tokens; one piece's logits stay in the
+ * workspace in 16 bits (fp32 layers: 32), so that the gradients need no second product.
+ * bf16 layers round dz to bf16 once (its factor coef/N is applied to the fp32 sums);
+ * outputs in OCCULT_F32 then carry that rounding.
+ */
+int occult_head_step(const occult_desc_t* desc, const occult_head_t* opt, const void* x,
+                     const void* w, const int32_t* labels, const int32_t* teacher_ids,
+                     const float* teacher_logits, const float* dloss, float* lse,
+                     float* token_loss, float* loss, void* dx, void* dw, void* ws,
+                     size_t ws_bytes, occult_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

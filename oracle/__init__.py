@@ -27,6 +27,7 @@ to its host framework, are written from their definitions:
 * ``balance``    -- expert, device and z losses of the router, with gradient.
 * ``adamw``      -- AdamW, and the 8-bit states as real arithmetic.
 * ``scored``     -- the router by scores, bias and groups, with gradient.
+* ``head``       -- cross entropy, distillation and z term of the output head.
 
 Floating point is fp64 throughout, computed from the exact fp32/bf16 input
 values.  Where floating point decides an integer (top-k choice) the decision is

@@ -1,5 +1,5 @@
-"""Host-side refusals of the scored router's entry points: bad options, missing and
-misaligned buffers, all before anything launches (a call that got past its checks here,
+"""Host-side refusals of the scored router's and the output head's entry points: bad
+options, missing and misaligned buffers, small workspaces, all before anything launches (a call that got past its checks here,
 without a GPU, would report a CUDA error)."""
 import ctypes
 
@@ -96,3 +96,94 @@ def test_binding_refuses_wrong_tensors(occ):
         occ.occult_route_scored(ds, opt, None, t.int(), t.int(), t, t.int())
     with pytest.raises(ValueError, match="required"):
         occ.occult_route_scored_grad(ds, opt, t, None, t, t)
+
+
+# ---- the output head ------------------------------------------------------------------
+ODD16 = ctypes.c_void_p(256 + 8)   # on a word, off a 16-byte boundary
+BIG = 1 << 40
+
+
+def head(occ, step, ds=None, opt=None, ws_bytes=BIG, **kw):
+    a = dict(x=V, w=V, labels=V, t_ids=NULL, t_logits=NULL)
+    if step:
+        a.update(dloss=NULL)
+    a.update(lse=NULL, token_loss=NULL, loss=V)
+    if step:
+        a.update(dx=V, dw=V)
+    a.update(ws=V)
+    a.update({k: v for k, v in kw.items() if k in a})
+    ds, opt = ds or desc(occ), opt or occ.occult_head_t(vocab=1000)
+    f = occ.lib().occult_head_step if step else occ.lib().occult_head_loss
+    return f(ctypes.byref(ds), ctypes.byref(opt), *a.values(), ws_bytes, NULL)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(vocab=0), dict(vocab=-5), dict(topk=-1), dict(piece=-1), dict(grad_dtype=2), dict(coef=-1.0),
+    dict(coef=NAN), dict(coef_kd=INF), dict(coef_z=NAN), dict(coef_kd=-0.5),
+    dict(topk=4, temperature=0.0), dict(topk=4, temperature=NAN), dict(topk=4, temperature=0.2),
+    dict(topk=4, temperature=11.0)])
+def test_head_refuses_bad_options(occ, kw):
+    opt = occ.occult_head_t(**{"vocab": 1000, **kw})
+    more = dict(t_ids=V, t_logits=V) if kw.get("topk", 0) > 0 else {}
+    assert head(occ, True, opt=opt, **more) == INVALID
+    assert head(occ, False, opt=opt, **more) == INVALID
+    n = ctypes.c_size_t(0)
+    assert occ.lib().occult_head_workspace_size(ctypes.byref(desc(occ)), ctypes.byref(opt), 1,
+                                                ctypes.byref(n)) == INVALID
+
+
+@pytest.mark.parametrize("step", [True, False])
+@pytest.mark.parametrize("kw", [
+    dict(x=NULL), dict(w=NULL), dict(loss=NULL), dict(labels=NULL),          # neither labels nor a teacher
+    dict(t_ids=V, t_logits=V), dict(t_ids=V),                                # a teacher with topk 0
+    dict(labels=NULL, token_loss=V), dict(x=ODD16), dict(w=ODD16), dict(ws=ODD16), dict(labels=ODD),
+    dict(loss=ODD), dict(lse=ODD), dict(token_loss=ODD)])
+def test_head_refuses_bad_buffers(occ, step, kw):
+    assert head(occ, step, **kw) == INVALID
+
+
+def test_head_refuses_bad_teachers_and_gradients(occ):
+    opt = occ.occult_head_t(vocab=1000, topk=8)
+    assert head(occ, True, opt=opt) == INVALID                      # no teacher given
+    assert head(occ, True, opt=opt, t_ids=V) == INVALID
+    assert head(occ, True, opt=opt, t_ids=ODD, t_logits=V) == INVALID
+    assert head(occ, False, opt=opt, labels=NULL, token_loss=V, t_ids=V, t_logits=V) == INVALID
+    assert head(occ, True, dx=NULL, dw=NULL) == INVALID
+    assert head(occ, True, dx=ODD16) == INVALID and head(occ, True, dw=ODD16) == INVALID
+    assert head(occ, True, dloss=ODD) == INVALID
+
+
+def test_head_refuses_what_it_does_not_run(occ):
+    assert head(occ, True, opt=occ.occult_head_t(vocab=1000, topk=129), t_ids=V, t_logits=V) == UNSUPPORTED
+    assert head(occ, True, opt=occ.occult_head_t(vocab=1 << 29)) == UNSUPPORTED
+    assert head(occ, True, ds=desc(occ, d=16448)) == UNSUPPORTED
+    assert head(occ, False, ds=desc(occ, d=2050)) == UNSUPPORTED
+    assert head(occ, True, ds=desc(occ, T=1 << 25, n_experts=8, top_k=2),
+                opt=occ.occult_head_t(vocab=1000, topk=100), t_ids=V, t_logits=V) == UNSUPPORTED
+
+
+@pytest.mark.parametrize("step", [True, False])
+@pytest.mark.parametrize("T,V_,K,dtype", [(1, 1, 0, 1), (4096, 50304, 64, 1), (32768, 151936, 0, 1),
+                                          (257, 1009, 5, 0)])
+def test_head_workspace(occ, step, T, V_, K, dtype):
+    """The size asked for is the size refused below; a step's logits stay within 1 GiB."""
+    ds, opt = desc(occ, T=T, dtype=dtype), occ.occult_head_t(vocab=V_, topk=K)
+    need = occ.head_workspace_size(ds, opt, step=step)
+    more = dict(t_ids=V, t_logits=V) if K else {}
+    assert head(occ, step, ds=ds, opt=opt, ws_bytes=need - 1, **more) == WORKSPACE
+    assert head(occ, step, ds=ds, opt=opt, ws=NULL, **more) == WORKSPACE
+    if T == 32768:
+        rest = 2 * T * 2048 + 4 * T * 40 + 12 * 4096 * 1200   # x's copy, rows, sums
+        assert need < (1 << 30) + rest + 4 * 64 * 4096 * 2048
+    n = ctypes.c_size_t(0)
+    bad = lambda *a: occ.lib().occult_head_workspace_size(ctypes.byref(ds), ctypes.byref(opt), *a)  # noqa: E731
+    assert bad(2, ctypes.byref(n)) == INVALID and bad(1, NULL) == INVALID
+
+
+def test_head_binding_refuses_wrong_tensors(occ):
+    ds, opt = desc(occ, T=4), occ.occult_head_t(vocab=10)
+    t = torch.zeros(4 * 2048, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="CUDA"):
+        occ.occult_head_loss(ds, opt, t, t, torch.zeros(4), torch.zeros(8, dtype=torch.uint8))
+    with pytest.raises(ValueError, match="required"):
+        occ.occult_head_step(ds, opt, t, None, torch.zeros(4), torch.zeros(8, dtype=torch.uint8))

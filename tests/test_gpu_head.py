@@ -1,0 +1,367 @@
+"""GPU parity of the output head (occult_head_loss, occult_head_step) with the fp64 oracle.
+
+Tolerances, with u = 2^-24.  A logit: its products are exact in fp32, each 16-deep step
+of the tensor cores (each product of the fp32 units) adds one rounding of at most 2 u of
+a = sum |x_i w_i|: ez = (d / 16 + 8) 2 u a (fp32: (d + 8) 2 u a).  A row's log-sum: ez, the exponentials
+(2^-22) and their arguments' rounding, 128 additions one after the other and their
+joining, 300 u in all, and 4 u of itself.  A probability: that twice, and in training
+steps of bf16 layers the kept logits' half step, s ln 2 / 2 with s = max(24, 20 tau) /
+65535 octaves (over tau for the tempered one), and what lies under their range, 2^-20 of
+the row's largest.  The gradient of a logit is rounded once to bf16 (2^-8), the sums of
+dx and dw add (V / 16 + 8) or (T / 16 + 8) steps of 2 u of the sum of magnitudes, the
+outputs their own rounding (2^-8 or u).
+"""
+import numpy as np
+import pytest
+import torch
+
+import synth
+from oracle import head as ohead
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+SENTINEL = -77.0
+
+
+@pytest.fixture(scope="module")
+def occ():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from combine_top_route_gb300 import build
+    build.build()
+    import combine_top_route_gb300 as occ
+    occ.lib()
+    yield occ
+    assert occ.device_error() == 0
+
+
+def case(T, d, V, dtype="bf16", K=0, ignored=0.0, seed=0, spread=1.8):
+    """Inputs on the host: normed rows leaning to their label, a teacher's top tokens."""
+    rng = np.random.default_rng(seed + T + d + V)
+    w = rng.normal(size=(V, d)).astype(np.float32) * np.float32(spread / d ** 0.5)
+    labels = rng.integers(0, V, T).astype(np.int32)
+    lean = w[labels] / np.linalg.norm(w[labels], axis=1, keepdims=True)
+    x = (rng.normal(size=(T, d)) + 2 * lean).astype(np.float32)
+    if dtype == "bf16":
+        x, w = (torch.as_tensor(a).bfloat16().float().numpy() for a in (x, w))
+    out = rng.random(T) < ignored
+    ids = tl = None
+    if K:
+        ids = rng.integers(0, V, size=(T, K)).astype(np.int32)   # some twice
+        ids[:, 0] = labels
+        ids[rng.random(T) < 0.2, K // 2 + 1:] = -1
+        ids[rng.random(T) < 0.1, 0] = V      # no teacher for these
+        tl = (rng.normal(size=(T, K)) * 2 + 5).astype(np.float32)
+        tl[rng.random((T, K)) < 0.05] = -np.inf
+        ids[out, 0] = -1
+    labels[out] = -100
+    return x, w, labels, ids, tl
+
+
+def gpu(a, dt=None):
+    if a is None:
+        return None
+    t = torch.as_tensor(np.ascontiguousarray(a))
+    return (t if dt is None else t.to(dt)).cuda()
+
+
+def run(occ, x, w, labels, ids, tl, dtype="bf16", grad="f32", step=True, want=("dx", "dw"), piece=0,
+        tau=1.0, coef=1.0, coef_kd=0.0, coef_z=0.0, dloss=None, stream=None, ws=None):
+    T, d = x.shape
+    V = len(w)
+    K = 0 if ids is None else ids.shape[1]
+    cfg = synth.CONFIGS["olmoe_fwd"].with_(T=T, d=d, dtype=dtype)
+    ds = occ.desc_for(cfg)
+    dt = ds.torch_dtype
+    gt = torch.bfloat16 if grad == "bf16" else torch.float32
+    opt = occ.occult_head_t(vocab=V, topk=K, grad_dtype=occ.OCCULT_BF16 if grad == "bf16" else occ.OCCULT_F32,
+                            piece=piece, coef=coef, coef_kd=coef_kd, coef_z=coef_z, temperature=tau)
+    need = occ.head_workspace_size(ds, opt, step=step)
+    ws = torch.full((need + 256,), 255, dtype=torch.uint8, device="cuda") if ws is None else ws
+    new = lambda n, t=torch.float32: torch.full((n + 64,), SENTINEL, dtype=t, device="cuda")  # noqa: E731
+    lse, token, loss = new(T), None if labels is None else new(T), new(4)
+    kw = dict(labels=gpu(labels), teacher_ids=gpu(ids), teacher_logits=gpu(tl), lse=lse, token_loss=token,
+              stream=stream)
+    gx, gw = gpu(x, dt), gpu(w, dt)
+    dx = dw = None
+    torch.cuda.synchronize()
+    if step:
+        dx, dw = (new(n, gt) if name in want else None for name, n in (("dx", T * d), ("dw", V * d)))
+        up = None if dloss is None else torch.full((1,), dloss, device="cuda")
+        torch.cuda.synchronize()
+        occ.occult_head_step(ds, opt, gx, gw, loss, ws[:need], dx=dx, dw=dw, dloss=up, **kw)
+    else:
+        occ.occult_head_loss(ds, opt, gx, gw, loss, ws[:need], **kw)
+    torch.cuda.synchronize()
+    assert (ws[need:] == 255).all()
+    out = {}
+    for name, t, n in (("loss", loss, 4), ("lse", lse, T), ("token_loss", token, T), ("dx", dx, T * d),
+                       ("dw", dw, V * d)):
+        if t is not None:
+            assert (t[n:] == SENTINEL).all(), name
+            out[name] = t[:n].double().cpu().numpy()
+            if name in ("dx", "dw"):
+                out[name] = out[name].reshape(-1, d)
+    return out
+
+
+def check(occ, c, dtype="bf16", grad="f32", step=True, tau=1.0, coef=1.0, coef_kd=0.0, coef_z=0.0,
+          dloss=None, **kw):
+    x, w, labels, ids, tl = c
+    (T, d), V = x.shape, len(w)
+    got = run(occ, *c, dtype=dtype, grad=grad, step=step, tau=tau, coef=coef, coef_kd=coef_kd,
+              coef_z=coef_z, dloss=dloss, **kw)
+    up = 1.0 if dloss is None else dloss
+    clean = np.nan_to_num(x, nan=0.0, posinf=0.0, neginf=0.0)
+    want = ohead.losses(clean, w, labels, ids, tl, tau=tau, coef=coef, coef_kd=coef_kd, coef_z=coef_z,
+                        dloss=up, grads=step)
+    x64, w64 = clean.astype(np.float64), w.astype(np.float64)
+    bf = dtype == "bf16"
+    inside = lambda a: (a >= 0) & (a < V)  # noqa: E731
+    ce_on = np.zeros(T, bool) if labels is None else inside(labels)
+    kd_on = np.zeros(T, bool) if ids is None else inside(ids[:, 0])
+    on = ce_on | kd_on
+    mag = np.abs(x64) @ np.abs(w64).T
+    ez = ((d / 16 if bf else d) + 8) * 2 * U * mag.max(axis=1)
+    e_lse = on * (ez + 300 * U + 4 * U * np.abs(want["lse"]))
+    assert (np.abs(got["lse"] - want["lse"]) <= e_lse).all(), np.max(np.abs(got["lse"] - want["lse"]) - e_lse)
+    e_tok = e_lse + on * (ez + 4 * U * (np.abs(want["lse"]) + mag.max(axis=1)))
+    if labels is not None:
+        assert (np.abs(got["token_loss"] - want["token_loss"]) <= e_tok * ce_on).all()
+    n_ce, n_kd, n = max(1, ce_on.sum()), max(1, kd_on.sum()), max(1, on.sum())
+    red = 40 * U   # the means' trees and the divisions
+    e_ce = (e_tok * ce_on).sum() / n_ce + red * want["loss"][1]
+    # the terms of kd are of both signs: q (log q - log p), each factor of the size of |log|
+    big = 2 * np.abs(tl[np.isfinite(tl)]).max() / tau + 2 * mag.max() / tau + np.log(V) + 40 if ids is not None else 0
+    e_kd = tau * tau * ((2 * e_tok / min(1.0, tau) + 160 * U * big) * kd_on).sum() / n_kd
+    e_z = (2 * np.abs(want["lse"]) * e_lse).sum() / n + red * want["loss"][3]
+    tol = np.array([0, e_ce, e_kd, e_z])
+    tol[0] = coef * e_ce + coef_kd * e_kd + coef_z * e_z + 8 * U * (
+        coef * want["loss"][1] + coef_kd * np.abs(want["loss"][2]) + coef_z * want["loss"][3])
+    assert (np.abs(got["loss"] - want["loss"]) <= tol).all(), (got["loss"], want["loss"], tol)
+    if not step:
+        return got
+    # probabilities of both softmaxes and their errors
+    z = x64 @ w64.T
+    soft = lambda v: np.exp(v - v.max(axis=1, keepdims=True)) / np.exp(v - v.max(axis=1, keepdims=True)).sum(axis=1, keepdims=True)  # noqa: E731
+    p1, p2 = soft(z), soft(z / tau)
+    half = max(24.0, 20 * tau) / 65535 * np.log(2) / 2 if bf else 0.0
+    floor = 2.0 ** -20 if bf else 0.0
+    e1 = ((2 * ez + 700 * U + 8 * U * np.abs(want["lse"]))[:, None] + half) * p1 + floor * p1.max(axis=1, keepdims=True)
+    e2 = (((2 * ez + 8 * U * np.abs(want["lse"])) / tau + 700 * U)[:, None] + half / tau) * p2 + floor * p2.max(axis=1, keepdims=True)
+    k1 = (ce_on * coef / n_ce + on * 2 * coef_z / n * want["lse"])[:, None]
+    has_q = kd_on if ids is None else kd_on & np.array([np.isfinite(tl[t][inside(ids[t])]).any() for t in range(T)])
+    k2 = (has_q * coef_kd * tau / n_kd)[:, None]
+    dz = k1 * p1 + k2 * p2
+    k1e = 2 * coef_z / n * e_lse[:, None]
+    pos = np.zeros_like(dz)      # magnitude of what is taken off at the entries
+    if labels is not None:
+        pos[ce_on, labels[ce_on]] += coef / n_ce
+    if ids is not None:
+        for t in np.flatnonzero(has_q):
+            at = inside(ids[t])
+            e = np.exp((tl[t][at].astype(np.float64) - tl[t][at].max()) / tau)
+            np.add.at(pos[t], ids[t][at], coef_kd * tau / n_kd * e / e.sum())
+    err = k1 * e1 + k2 * e2 + k1e * p1 + 40 * U * (dz + pos)
+    if ids is not None:   # the teacher's probabilities: expf and its argument
+        err += (2 * np.abs(np.where(np.isfinite(tl), tl, 0)).max() / tau + 20) * U * pos
+    size = np.abs(dz - pos)
+    if bf:
+        err += 2.0 ** -8 * (size + err)
+    steps = lambda n_: ((n_ / 16 if bf else n_) + 8) * 2 * U  # noqa: E731
+    out_err = 2.0 ** -8 if grad == "bf16" else 2 * U
+    for name, a, b, e, k in (("dx", size, w64, err, V), ("dw", size.T, x64, err.T, T)):
+        if name not in got:
+            continue
+        bound = abs(up) * (e @ np.abs(b) + steps(k) * (a @ np.abs(b))) * (1 + 2.0 ** -7) \
+            + out_err * np.abs(want[name]) + 1e-36
+        off = np.abs(got[name] - want[name])
+        assert (off <= bound).all(), (name, np.max(off / bound))
+    return got
+
+
+SIZES = [(1, 64, 16), (1, 2048, 5003), (5, 128, 100), (128, 64, 257), (129, 64, 1000), (257, 192, 777),
+         (300, 256, 5000), (513, 320, 2049), (64, 1408, 300), (1, 64, 1), (255, 128, 256), (600, 64, 31)]
+
+
+@pytest.mark.parametrize("T,d,V", SIZES)
+@pytest.mark.parametrize("grad", ["f32", "bf16"])
+def test_sizes(occ, T, d, V, grad):
+    c = case(T, d, V)
+    check(occ, c, grad=grad, coef_z=1e-3)
+    check(occ, c, step=False, coef_z=1e-3)
+
+
+@pytest.mark.parametrize("T,d,V", [(1, 4, 3), (7, 64, 1009), (257, 64, 1009), (65, 36, 129), (130, 100, 64)])
+@pytest.mark.parametrize("grad", ["f32", "bf16"])
+@pytest.mark.parametrize("K,tau", [(0, 1.0), (6, 1.5)])
+def test_fp32_layers(occ, T, d, V, grad, K, tau):
+    c = case(T, d, V, "f32", K=min(K, V), ignored=0.2)
+    kw = dict(dtype="f32", coef=0.6, coef_kd=0.5, coef_z=1e-3, tau=tau)
+    check(occ, c, grad=grad, dloss=0.5, **kw)
+    check(occ, c, step=False, **kw)
+    if T > 256:
+        check(occ, c, grad=grad, piece=256, **kw)
+
+
+@pytest.mark.parametrize("K", [1, 5, 33, 64, 128])
+@pytest.mark.parametrize("tau", [1.0, 2.0, 0.25, 10.0])
+@pytest.mark.parametrize("coef", [0.0, 0.7])
+def test_teachers(occ, K, tau, coef):
+    """Teacher rows with tokens named twice, out of the vocabulary, at -inf, or none at all."""
+    for T, d, V, ignored in ((140, 128, 700, 0.3), (33, 64, 400, 0.0)):
+        c = case(T, d, V, K=K, ignored=ignored)
+        kw = dict(tau=tau, coef=coef, coef_kd=0.4, coef_z=1e-3 if coef else 0.0)
+        check(occ, c, **kw)
+        check(occ, c, step=False, **kw)
+    x, w, _, ids, tl = c
+    tl[:5] = -np.inf
+    tl[5:9, 1:] = -np.inf
+    check(occ, (x, w, None, ids, tl), tau=tau, coef=0.0, coef_kd=1.0, grad="bf16")
+
+
+@pytest.mark.parametrize("ignored", [0.0, 0.3, 0.97, 1.0])
+@pytest.mark.parametrize("piece", [0, 256])
+def test_ignored_rows_and_pieces(occ, ignored, piece):
+    """Rows that no term counts may hold anything; a batch in pieces; pieces left empty."""
+    for grad in ("f32", "bf16"):
+        x, w, labels, ids, tl = case(700, 128, 900, ignored=ignored, seed=3)
+        x[labels < 0] = np.nan
+        x[np.flatnonzero(labels < 0)[::2]] = np.inf
+        check(occ, (x, w, labels, ids, tl), grad=grad, piece=piece, coef_z=1e-3, dloss=-3.0)
+        check(occ, (x, w, labels, ids, tl), step=False)
+
+
+def test_one_gradient_alone(occ):
+    c = case(300, 192, 1200, K=8)
+    kw = dict(tau=2.0, coef=0.5, coef_kd=0.5)
+    both = check(occ, c, **kw)
+    for name in ("dx", "dw"):
+        got = check(occ, c, want=(name,), **kw)
+        assert set(got) == {"loss", "lse", "token_loss", name}
+        assert (got[name] == both[name]).all()
+
+
+def test_large_logits(occ):
+    """Logits of thousands: one-hot softmaxes, nothing overflows."""
+    for spread in (60.0, 900.0):
+        c = case(150, 128, 600, K=7, spread=spread)
+        got = check(occ, c, tau=2.0, coef=0.5, coef_kd=0.5)
+        assert all(np.isfinite(v).all() for v in got.values())
+
+
+def test_equal_logits_and_repeats(occ):
+    """A zero head; and the same bits from the same call, at any alignment of its tail."""
+    x, w, labels, _, _ = case(200, 128, 1000)
+    got = check(occ, (x, 0 * w, labels, None, None), coef_z=0.1)
+    np.testing.assert_allclose(got["token_loss"], np.log(1000), rtol=1e-6)
+    c = case(700, 256, 3001, K=16, ignored=0.2)
+    kw = dict(tau=2.0, coef=0.5, coef_kd=0.5, grad="bf16")
+    a, b = run(occ, *c, **kw), run(occ, *c, **kw)
+    assert all((a[k] == b[k]).all() for k in a)
+
+
+def test_gradient_is_the_difference_quotient(occ):
+    """The kernel's loss of fp32 layers, moved along a random direction of x and of w."""
+    c = case(40, 32, 90, "f32", K=5)
+    kw = dict(dtype="f32", tau=1.5, coef=0.6, coef_kd=0.5, coef_z=1e-2)
+    base = run(occ, *c, **kw)
+    rng = np.random.default_rng(1)
+    for at, name in ((0, "dx"), (1, "dw")):
+        way = rng.normal(size=c[at].shape).astype(np.float32)
+        h = 2.0 ** -7
+        ends = []
+        for sgn in (1, -1):
+            cc = list(c)
+            cc[at] = c[at] + np.float32(sgn * h) * way
+            ends.append(run(occ, *cc, step=False, **kw)["loss"][0])
+        num, ana = (ends[0] - ends[1]) / (2 * h), (base[name] * way).sum()
+        # the loss is a mean of functions of logits that move by |dz| <= h * s along the way,
+        # s their largest speed: third derivatives stay under 4 of it; and fp32's losses
+        move = way @ c[1].T if at == 0 else c[0] @ way.T
+        s = np.abs(move).max()
+        assert abs(num - ana) <= 4 * s ** 3 * h * h / 6 + 64 * U * (abs(ends[0]) + 1) / h
+
+
+def test_streams_graphs_and_shared_workspaces(occ):
+    """A side stream; two graphs over one workspace, replayed in turn on new inputs."""
+    T, d, V, K = 300, 128, 1500, 6
+    cs = [case(T, d, V, K=K, ignored=0.3, seed=s) for s in (1, 2)]
+    kw = dict(tau=2.0, coef=0.5, coef_kd=0.5)
+    want = [run(occ, *c, **kw) for c in cs]
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        got = run(occ, *cs[0], stream=s, **kw)
+    assert all((got[k] == want[0][k]).all() for k in got)
+    ds = occ.desc_for(synth.CONFIGS["olmoe_fwd"].with_(T=T, d=d))
+    opt = occ.occult_head_t(vocab=V, topk=K, coef=0.5, coef_kd=0.5, temperature=2.0)
+    need = max(occ.head_workspace_size(ds, opt, step=b) for b in (True, False))
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    x, w = (torch.empty(n, d, dtype=torch.bfloat16, device="cuda") for n in (T, V))
+    lab, ids = torch.empty(T, dtype=torch.int32, device="cuda"), torch.empty(T, K, dtype=torch.int32, device="cuda")
+    tl, lse = torch.empty(T, K, device="cuda"), torch.empty(T, device="cuda")
+    loss, dx, dw = torch.empty(2, 4, device="cuda"), torch.empty(T, d, device="cuda"), torch.empty(V, d, device="cuda")
+
+    def fill(c):
+        for t, a in zip((x, w, lab, ids, tl), c):
+            t.copy_(torch.as_tensor(a))
+
+    fill(cs[0])
+    args = dict(labels=lab, teacher_ids=ids, teacher_logits=tl)
+    step = lambda: occ.occult_head_step(ds, opt, x, w, loss[0], ws, dx=dx, dw=dw, lse=lse, **args)  # noqa: E731
+    only = lambda: occ.occult_head_loss(ds, opt, x, w, loss[1], ws, **args)  # noqa: E731
+    step(), only()
+    torch.cuda.synchronize()
+    graphs = []
+    for f in (step, only):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            f()
+        graphs.append(g)
+    for i in (1, 0, 1):
+        fill(cs[i])
+        graphs[0].replay()
+        graphs[1].replay()
+        torch.cuda.synchronize()
+        assert (dx.double().cpu().numpy() == want[i]["dx"]).all()
+        assert (dw.double().cpu().numpy() == want[i]["dw"]).all()
+        np.testing.assert_allclose(loss.double().cpu().numpy(), np.tile(want[i]["loss"], (2, 1)), rtol=1e-5)
+
+
+def test_no_tokens(occ):
+    for dtype in ("bf16", "f32"):
+        x, w, labels, _, _ = case(3, 64, 50, dtype)
+        for grad in ("f32", "bf16"):
+            got = run(occ, x[:0], w, labels[:0], None, None, dtype=dtype, grad=grad)
+            assert (got["loss"] == 0).all() and (got["dw"] == 0).all()
+
+
+def test_offsets_past_32_bits(occ):
+    """A head of 1.1 million rows of 2048: w and dw hold over 2^31 elements."""
+    T, d, V = 3, 2048, 1_100_000
+    g = torch.Generator(device="cuda").manual_seed(1)
+    w = torch.empty(V, d, dtype=torch.bfloat16, device="cuda")
+    for a in range(0, V, 100_000):
+        w[a:a + 100_000] = 0.02 * torch.randn(min(100_000, V - a), d, generator=g, device="cuda")
+    x = torch.randn(T, d, generator=g, device="cuda").bfloat16()
+    labels = torch.tensor([V - 1, 5, V - 700], dtype=torch.int32, device="cuda")
+    ds = occ.desc_for(synth.CONFIGS["olmoe_fwd"].with_(T=T, d=d))
+    opt = occ.occult_head_t(vocab=V, grad_dtype=occ.OCCULT_BF16)
+    ws = torch.empty(occ.head_workspace_size(ds, opt), dtype=torch.uint8, device="cuda")
+    loss, dx, dw = torch.empty(4, device="cuda"), torch.empty_like(x), torch.empty_like(w)
+    occ.occult_head_step(ds, opt, x, w, loss, ws, dx=dx, dw=dw, labels=labels)
+    z = torch.cat([x.double() @ w[a:a + 100_000].double().t() for a in range(0, V, 100_000)], dim=1)
+    lse = torch.logsumexp(z, dim=1)
+    ref = (lse - z[torch.arange(T), labels.long()]).mean()
+    # (sums of magnitudes: logits of 2048 products, see above)
+    assert abs(float(loss[1]) - float(ref)) < 1e-3
+    dz = torch.exp(z - lse[:, None]) / T
+    dz[torch.arange(T), labels.long()] -= 1.0 / T
+    for rows in (slice(V - 1024, V), slice(0, 64), slice(V // 2, V // 2 + 64)):
+        want = dz[:, rows].t() @ x.double()
+        size = dz[:, rows].abs().t() @ x.double().abs()
+        assert ((dw[rows].double() - want).abs() <= 2.0 ** -6 * size + 1e-9).all()
+    want = sum(dz[:, a:a + 100_000] @ w[a:a + 100_000].double() for a in range(0, V, 100_000))
+    size = sum(dz[:, a:a + 100_000].abs() @ w[a:a + 100_000].double().abs() for a in range(0, V, 100_000))
+    assert ((dx.double() - want).abs() <= 2.0 ** -6 * size).all()
