@@ -3,7 +3,8 @@
 ``OccultMoE`` owns the layer's weights, its expert placement and every buffer
 of the pipeline, sized for the worst case so that no step waits on the host:
 
-    route -> build BRIMs -> dispatch (ORI -> SFD, first all-to-all's send buffer)
+    route (Eq. 2, or by scores with a bias and groups) -> build BRIMs
+    -> dispatch (ORI -> SFD, first all-to-all's send buffer)
     -> expert_up (SFD -> EPD, SwiGLU, modulation) -> [shared experts]
     -> expert_down_merge (the second linear layer; its rows added into the
        token rows with fp32 atomics, the paper's merging SMM)
@@ -35,8 +36,9 @@ from . import (MAX_SOURCES, OCCULT_BF16, OCCULT_F32, ROUTE_DEVICE_LIMITED, ROUTE
                occult_expert_down,
                occult_expert_down_merge, occult_expert_bwd_merge,
                occult_expert_up, occult_gate_grad, occult_merge_sfd, occult_route,
-               occult_route_similarity, occult_router_grad, occult_shard_plan,
-               occult_shared_ffn, epd_copy_rows, workspace_size)
+               occult_route_scored, occult_route_scored_grad, occult_route_similarity,
+               occult_router_grad, occult_score_t, occult_shard_plan, occult_shared_ffn,
+               epd_copy_rows, workspace_size)
 
 
 def desc_for(cfg, T: Optional[int] = None) -> occult_desc_t:
@@ -66,8 +68,11 @@ class OccultMoE:
     def __init__(self, desc: occult_desc_t, weights: Dict[str, torch.Tensor],
                  placement: torch.Tensor, device="cuda", materialize_sfd: bool = False,
                  train: bool = False, sim_table: Optional[torch.Tensor] = None,
-                 src_off: Optional[Sequence[int]] = None, merge: Optional[str] = None):
-        """``merge``: "atomic" (default; fp32 atomic adds into the token rows) or
+                 src_off: Optional[Sequence[int]] = None, merge: Optional[str] = None,
+                 score: Optional[occult_score_t] = None, bias: Optional[torch.Tensor] = None):
+        """``score``: options of the scored router, which then takes Eq. 2's place (route_mode
+        "exact" only), with ``bias`` (fp32 [Ne], used where it is if on the device) on the
+        choice.  ``merge``: "atomic" (default; fp32 atomic adds into the token rows) or
         "ordered" (fixed order, bit-reproducible; the only one with a
         materialised SFD stage or source shards, and their default)."""
         self.desc = desc
@@ -80,9 +85,15 @@ class OccultMoE:
         self.merge = merge
         if desc.route_mode == ROUTE_SIMILARITY_PRUNED and sim_table is None:
             raise ValueError("similarity-based pruning needs sim_table [Ne, Ne] (fp32)")
+        if score is None and bias is not None:
+            raise ValueError("a bias needs the scored router (score)")
+        if score is not None and desc.route_mode != ROUTE_EXACT:
+            raise ValueError("the scored router takes route_mode exact")
         dev = torch.device(device)
         dt = desc.torch_dtype
         self.device = dev
+        self.score = score
+        self.bias = None if bias is None else bias.to(dev, torch.float32).contiguous()
         self.w = {k: v.to(dev, dt).contiguous() for k, v in weights.items()}
         placement = torch.as_tensor(placement, dtype=torch.int32)
         # the kernels index by the placement without checking it (it lives in
@@ -179,7 +190,10 @@ class OccultMoE:
     def route_and_index(self, logits: torch.Tensor, stream=None) -> None:
         ds = self.desc
         self.logits = logits
-        if ds.route_mode == ROUTE_SIMILARITY_PRUNED:
+        if self.score is not None:
+            occult_route_scored(ds, self.score, logits, self.expert_to_vdev, self.ids, self.gates,
+                                self.vmask, self.bias, stream)
+        elif ds.route_mode == ROUTE_SIMILARITY_PRUNED:
             occult_route_similarity(ds, logits, self.expert_to_vdev, self.sim_table, self.ids,
                                     self.gates, self.vmask, self.routed, stream)
         else:
@@ -271,7 +285,8 @@ class OccultMoE:
         it to the SFD rows and the first exchange moves them.  The expert backward
         runs on the EPD rows, and the two-stage merge brings dx back to the
         tokens; dgates return through BRIM0 -> BRIM1 as well, and on through the
-        softmax of Eq. 2 to the logits the forward was given.
+        router's scores (the softmax of Eq. 2 or the scored router's) to the logits the
+        forward was given.
         """
         if not self.train:
             raise RuntimeError("OccultMoE was built without train=True")
@@ -293,7 +308,11 @@ class OccultMoE:
             self._expert_bwd_ordered(stream)
         occult_gate_grad(ds, self.ids, self.placement, self.brim0, self.seg_off, self.brim1,
                          self.exp_off, self.dg_epd, self.dgates, stream)
-        occult_router_grad(ds, self.logits, self.routed, self.dgates, self.dlogits, stream)
+        if self.score is not None:
+            occult_route_scored_grad(ds, self.score, self.logits, self.ids, self.dgates,
+                                     self.dlogits, stream)
+        else:
+            occult_router_grad(ds, self.logits, self.routed, self.dgates, self.dlogits, stream)
         return self.dx, self.dw1, self.dw2, self.dgates
 
     def _expert_bwd_ordered(self, stream) -> None:

@@ -1,4 +1,5 @@
-"""One MoE block in training: the layer between its norms, its losses and its update.
+"""One MoE block in training: the layer between its norms, its losses and its update;
+and the head that ends a model.
 
 ``OccultBlock`` runs a block r -> r' of a residual stream as a training step needs
 it, every step but the router's three small matrix products in the library's
@@ -12,7 +13,9 @@ kernels:
               first norm to the gradient of r and of every weight
     step      AdamW over all of the block's weights, up to 256 tensors a launch
 
-``OccultAdamW`` is that update on its own, for any tensors with fp32 gradients.
+``OccultHead`` is the last norm and the loss over a vocabulary: labels, a teacher's top
+logits, or both, forward and backward in one call.
+``OccultAdamW`` is the update on its own, for any tensors with fp32 gradients.
 """
 from __future__ import annotations
 
@@ -24,7 +27,9 @@ from . import (GATE_CHANNEL, GATE_NONE, OCCULT_BF16, OCCULT_F32, STATE_BLOCK, ST
                WS_BLOCK_NORM_BWD, adamw_table, balance_groups, balance_workspace_size,
                occult_adamw, occult_adamw_read, occult_adamw_t, occult_balance_grad,
                occult_balance_loss, occult_balance_t, occult_block_norm, occult_block_norm_bwd,
-               occult_desc_t, occult_norm_t, workspace_size)
+               head_workspace_size, occult_desc_t, occult_head_loss, occult_head_step,
+               occult_head_t, occult_norm_t, occult_route_bias_step, occult_score_t,
+               workspace_size)
 from .pipeline import OccultMoE
 
 
@@ -113,17 +118,19 @@ class OccultBlock:
                  placement: torch.Tensor, w_router: torch.Tensor, device="cuda",
                  eps: float = 1e-6, res_scale: float = 1.0, res_dtype=torch.bfloat16,
                  post_norm: bool = True, gate: Optional[torch.Tensor] = None,
-                 balance=(0.01, 0.0, 0.001), group_len: int = 0, sim_table=None):
+                 balance=(0.01, 0.0, 0.001), group_len: int = 0, sim_table=None,
+                 score: Optional[occult_score_t] = None, bias: Optional[torch.Tensor] = None):
         """``weights``: w1 and w2 as OccultMoE takes them (bf16 ones on the device are
         used where they are, so that an optimizer's steps change the caller's tensors;
         the other weights are copied); ``w_router`` fp32 [Ne, d];
         ``gate`` fp32 [d] or None; ``balance``: the weights of the expert, device and z
-        terms; ``group_len``: tokens of a sequence for them (0: the batch)."""
+        terms; ``group_len``: tokens of a sequence for them (0: the batch); ``score`` and
+        ``bias``: the scored router's, as OccultMoE takes them."""
         if desc.dtype != OCCULT_BF16 or desc.n_shared:
             raise ValueError("OccultBlock trains bf16 layers without shared experts")
         self.desc = desc
         self.moe = OccultMoE(desc, weights, placement, device=device, train=True,
-                             sim_table=sim_table)
+                             sim_table=sim_table, score=score, bias=bias)
         dev = self.moe.device
         T, d, Ne = desc.T, desc.d, desc.n_experts
         f32, bf = torch.float32, torch.bfloat16
@@ -168,6 +175,12 @@ class OccultBlock:
         ps = self.parameters()
         return OccultAdamW([p for _, p, _ in ps], [g for _, _, g in ps], **kw)
 
+    def bias_step(self, stream=None) -> None:
+        """Moves the scored router's bias towards even loads, by the last forward's counts."""
+        if self.moe.bias is None:
+            raise RuntimeError("the block's router has no bias")
+        occult_route_bias_step(self.desc, self.moe.score, self.counts, self.moe.bias, stream)
+
     def forward(self, r: torch.Tensor, mask: Optional[torch.Tensor] = None) -> torch.Tensor:
         """r' [T, d] for the residual stream r; the auxiliary losses in ``self.losses``
         ({weighted total, expert, device, z}), the experts' loads in ``self.counts``.
@@ -202,3 +215,64 @@ class OccultBlock:
         occult_block_norm_bwd(ds, self.pre_opt, self.dr_mid, self.r, self.dr, self.norm_ws, dx=dx,
                               w_pre=self.w_pre, rstd_pre=self.rstd_pre, dw_pre=self.dw_pre)
         return self.dr
+
+
+class OccultHead:
+    """The end of a model: the last norm, the product with the vocabulary and its losses."""
+
+    def __init__(self, desc: occult_desc_t, w_head: torch.Tensor, device="cuda", eps: float = 1e-6,
+                 res_dtype=torch.bfloat16, topk: int = 0, coef: float = 1.0, coef_kd: float = 0.0,
+                 coef_z: float = 0.0, temperature: float = 1.0, piece: int = 0):
+        """``desc``: T, d and dtype are the head's; ``w_head`` [V, d] (in the layer type and on
+        the device it is used where it is); ``topk``: teacher entries a token; the other
+        options as in occult_head_t."""
+        dev, dt = torch.device(device), desc.torch_dtype
+        T, d, V = desc.T, desc.d, w_head.shape[0]
+        if tuple(w_head.shape) != (V, d):
+            raise ValueError(f"w_head must be [V, {d}]")
+        self.desc = desc
+        self.opt = occult_head_t(vocab=V, topk=topk, coef=coef, coef_kd=coef_kd, coef_z=coef_z,
+                                 temperature=temperature, piece=piece)
+        self.norm_opt = occult_norm_t(eps, 1.0, GATE_NONE,
+                                      OCCULT_BF16 if res_dtype == torch.bfloat16 else OCCULT_F32)
+        e = lambda *s, dtype=torch.float32: torch.empty(*s, dtype=dtype, device=dev)  # noqa: E731
+        self.w = w_head.to(dev, dt).contiguous()
+        self.w_norm = torch.ones(d, dtype=dt, device=dev)
+        self.x, self.rstd = e(T, d, dtype=dt), e(T)
+        self.losses, self.lse, self.token_loss = e(4), e(T), e(T)
+        self.dx, self.dr, self.dw, self.dw_norm = e(T, d), e(T, d, dtype=res_dtype), e(V, d), e(d)
+        need = max(head_workspace_size(desc, self.opt, step=b) for b in (True, False))
+        self.ws = e(max(1, need), dtype=torch.uint8)
+        self.norm_ws = e(max(1, workspace_size(desc, WS_BLOCK_NORM_BWD)), dtype=torch.uint8)
+
+    def parameters(self):
+        """[(name, parameter, its fp32 gradient)], as OccultBlock.parameters."""
+        return [("w_head", self.w, self.dw), ("w_norm", self.w_norm, self.dw_norm)]
+
+    def _norm(self, r):
+        occult_block_norm(self.desc, self.norm_opt, r, w_pre=self.w_norm, x=self.x, rstd_pre=self.rstd)
+
+    def _inputs(self, labels, teacher):
+        ids, logits = (None, None) if teacher is None else teacher
+        return dict(labels=labels, teacher_ids=ids, teacher_logits=logits, lse=self.lse,
+                    token_loss=None if labels is None else self.token_loss)
+
+    def loss(self, r: torch.Tensor, labels: Optional[torch.Tensor] = None, teacher=None):
+        """[4] {total, cross entropy, distillation, z} of the residual stream r, without a
+        gradient; ``labels`` int32 [T], ``teacher`` (int32 [T, K] tokens, fp32 [T, K] logits).
+        The tokens' own losses are left in ``token_loss``, their log-sums in ``lse``."""
+        self._norm(r)
+        occult_head_loss(self.desc, self.opt, self.x, self.w, self.losses, self.ws,
+                         **self._inputs(labels, teacher))
+        return self.losses
+
+    def step(self, r: torch.Tensor, labels: Optional[torch.Tensor] = None, teacher=None,
+             dloss: Optional[torch.Tensor] = None):
+        """(losses [4], gradient of r): as ``loss``, with the total's gradients (times the
+        fp32 CUDA tensor ``dloss``); the weights' are left in their buffers."""
+        self._norm(r)
+        occult_head_step(self.desc, self.opt, self.x, self.w, self.losses, self.ws, dx=self.dx,
+                         dw=self.dw, dloss=dloss, **self._inputs(labels, teacher))
+        occult_block_norm_bwd(self.desc, self.norm_opt, None, r, self.dr, self.norm_ws, dx=self.dx,
+                              w_pre=self.w_norm, rstd_pre=self.rstd, dw_pre=self.dw_norm)
+        return self.losses, self.dr
