@@ -15,9 +15,9 @@
 // 128-row tile that is mostly padding: there the weights' stream is the bound, and the
 // padding costs tensor time that is idle anyway.
 //
-// CTA = 10 warps: warp 0 TMA producer, warp 1 owner of TMEM (two accumulators, so that a
+// CTA = 12 warps: warp 0 TMA producer, warp 1 owner of TMEM (two accumulators, so that a
 // tile's epilogue runs under the next one's products) and issuer of the products (in a
-// pair the even CTA's), warps 2..9 epilogue, two to a TMEM lane quarter, half of the
+// pair the even CTA's), warps 4..11 epilogue, two to a TMEM lane quarter, half of the
 // columns each.  Every wait is bounded.
 #include <algorithm>
 #include <mutex>
@@ -32,8 +32,10 @@ namespace {
 constexpr int BM = 128, BN = 256, BK = 64;
 constexpr int kABytes = BM * BK * 2;          // 16 KB
 constexpr int kMnAtom = BK * 128;             // 64 columns of an MN-major operand
-constexpr int kEpiWarps = 8, kEpiWarp0 = 2;
+constexpr int kEpiWarps = 8, kEpiWarp0 = 4;   // whole warpgroups, for their registers
 constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarps);
+constexpr int kLaunchRegs = 168, kCtrlRegs = 40, kEpiRegs = 232;   // a thread
+static_assert(32 * (kEpiWarp0 * kCtrlRegs + kEpiWarps * kEpiRegs) <= kThreads * kLaunchRegs, "registers");
 constexpr uint32_t kTmemCols = 512;
 constexpr int kMaxStages = 6;
 
@@ -220,106 +222,112 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
   // bytes of a stage: the boxes are whole wherever they lie
   const uint32_t cta_bytes = kABytes + static_cast<uint32_t>(b_rows) * (BK * 2);
 
-  if (warp == 0) {
-    int stage = 0;
-    uint32_t phase = 0;
-    bool ok = true;
-    const CUtensorMap* ma = kLogits && !whole ? &tmA2 : &tmA;
-    const CUtensorMap* mb = MODE == HEAD_DW && !whole ? &tmB2 : &tmB;
-    if (lane == 0) { prefetch_tmap(ma); prefetch_tmap(mb); }
-    for (int u = unit0; u < total && ok; u += stride) {
-      const Unit t = unit_of<MODE, PAIR>(u, p, m_units, rank, kb_rows);
-      const int bc = t.n0 + (PAIR ? rank * b_rows : 0);   // this CTA's first column
-      for (int kb = t.k0; kb < t.k1; ++kb) {
-        if (!mbar_wait(&tail->empty[stage], phase ^ 1u, abort_flag)) { ok = false; break; }
-        if (lane == 0) {
-          uint8_t* sa = smem + stage * kStageBytes;
-          uint8_t* sb = sa + kABytes;
-          uint64_t* bar = &tail->full[stage];
-          const uint32_t lbar = full_lead + stage * 8;
-          if (leader) mbar_arrive_expect_tx(bar, PAIR ? 2 * cta_bytes : cta_bytes);
-          if (kAMn) {
-            for (int a = 0; a < BM / 64; ++a) {
-              if (PAIR) tma_load_2d_pair(sa + a * kMnAtom, ma, t.m0 + 64 * a, kb * BK, lbar);
-              else tma_load_2d(sa + a * kMnAtom, ma, t.m0 + 64 * a, kb * BK, bar);
-            }
-          } else {
-            const int row = kLogits ? p.row0 + t.m0 : t.m0;
-            if (PAIR) tma_load_2d_pair(sa, ma, kb * BK, row, lbar);
-            else tma_load_2d(sa, ma, kb * BK, row, bar);
-          }
-          if (kBMn) {
-            const int krow = MODE == HEAD_DW ? p.row0 + kb * BK : kb * BK;
-            for (int a = 0; a < b_rows / 64; ++a) {
-              if (PAIR) tma_load_2d_pair(sb + a * kMnAtom, mb, bc + 64 * a, krow, lbar);
-              else tma_load_2d(sb + a * kMnAtom, mb, bc + 64 * a, krow, bar);
-            }
-          } else {
-            if (PAIR) tma_load_2d_pair(sb, mb, kb * BK, bc, lbar);
-            else tma_load_2d(sb, mb, kb * BK, bc, bar);
-          }
-        }
-        __syncwarp();
-        if (++stage == kStages) { stage = 0; phase ^= 1u; }
-      }
-    }
-    if (PAIR && ok) {
-      // no release of a stage lands after the CTA has exited
-      for (int i = 0; i < kStages && ok; ++i) {
-        if (!mbar_wait(&tail->empty[stage], phase ^ 1u, abort_flag)) ok = false;
-        if (++stage == kStages) { stage = 0; phase ^= 1u; }
-      }
-    }
-    if (!ok) {
-      if (lane == 0) latch_error(p.dev_err, OCCULT_ERR_DEVICE_TIMEOUT);
-      *abort_flag = 1;
-    }
-  } else if (warp == 1) {
-    if (lane == 0 && leader) {
-      int stage = 0, it = 0;
+  // The logits' epilogue holds a row's 128 sums beside its work: the launch's 384 x 168
+  // registers are dealt out anew, 128 x 40 + 256 x 232.
+  if (warp < kEpiWarp0) {
+    if (kLogits) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kCtrlRegs));
+    if (warp == 0) {
+      int stage = 0;
       uint32_t phase = 0;
       bool ok = true;
-      const uint32_t idesc = idesc_bf16_f32(RM, p.bn) | (kAMn ? 1u << 15 : 0u) | (kBMn ? 1u << 16 : 0u);
+      const CUtensorMap* ma = kLogits && !whole ? &tmA2 : &tmA;
+      const CUtensorMap* mb = MODE == HEAD_DW && !whole ? &tmB2 : &tmB;
+      if (lane == 0) { prefetch_tmap(ma); prefetch_tmap(mb); }
       for (int u = unit0; u < total && ok; u += stride) {
         const Unit t = unit_of<MODE, PAIR>(u, p, m_units, rank, kb_rows);
-        int kb = t.k0;
-        do {   // (a unit without k blocks still hands over its accumulator)
-          const int end = kLogits ? min(t.k1, kb + p.seg) : t.k1;
-          const int a = it & 1;
-          const uint32_t aph = (it >> 1) & 1;
-          ++it;
-          if (!(PAIR ? mbar_wait_cluster(&tail->tempty[a], aph ^ 1u, abort_flag)
-                     : mbar_wait(&tail->tempty[a], aph ^ 1u, abort_flag))) { ok = false; break; }
-          tc_fence_after();
-          const uint32_t acc = tbase + a * BN;
-          for (const int first = kb; kb < end; ++kb) {
-            if (!(PAIR ? mbar_wait_cluster(&tail->full[stage], phase, abort_flag)
-                       : mbar_wait(&tail->full[stage], phase, abort_flag))) { ok = false; break; }
-            tc_fence_after();
-            const uint32_t sa = smem_u32(smem + stage * kStageBytes), sb = sa + kABytes;
-#pragma unroll
-            for (int kk = 0; kk < BK / 16; ++kk) {
-              const bool add = kb != first || kk != 0;
-              if (PAIR) tc_mma_f16_pair(acc, operand_desc<kAMn>(sa, kk), operand_desc<kBMn>(sb, kk), idesc, add);
-              else tc_mma_f16(acc, operand_desc<kAMn>(sa, kk), operand_desc<kBMn>(sb, kk), idesc, add);
+        const int bc = t.n0 + (PAIR ? rank * b_rows : 0);   // this CTA's first column
+        for (int kb = t.k0; kb < t.k1; ++kb) {
+          if (!mbar_wait(&tail->empty[stage], phase ^ 1u, abort_flag)) { ok = false; break; }
+          if (lane == 0) {
+            uint8_t* sa = smem + stage * kStageBytes;
+            uint8_t* sb = sa + kABytes;
+            uint64_t* bar = &tail->full[stage];
+            const uint32_t lbar = full_lead + stage * 8;
+            if (leader) mbar_arrive_expect_tx(bar, PAIR ? 2 * cta_bytes : cta_bytes);
+            if (kAMn) {
+              for (int a = 0; a < BM / 64; ++a) {
+                if (PAIR) tma_load_2d_pair(sa + a * kMnAtom, ma, t.m0 + 64 * a, kb * BK, lbar);
+                else tma_load_2d(sa + a * kMnAtom, ma, t.m0 + 64 * a, kb * BK, bar);
+              }
+            } else {
+              const int row = kLogits ? p.row0 + t.m0 : t.m0;
+              if (PAIR) tma_load_2d_pair(sa, ma, kb * BK, row, lbar);
+              else tma_load_2d(sa, ma, kb * BK, row, bar);
             }
-            if (PAIR) tc_commit_pair(&tail->empty[stage], 0x3);
-            else tc_commit(&tail->empty[stage]);
-            if (++stage == kStages) { stage = 0; phase ^= 1u; }
+            if (kBMn) {
+              const int krow = MODE == HEAD_DW ? p.row0 + kb * BK : kb * BK;
+              for (int a = 0; a < b_rows / 64; ++a) {
+                if (PAIR) tma_load_2d_pair(sb + a * kMnAtom, mb, bc + 64 * a, krow, lbar);
+                else tma_load_2d(sb + a * kMnAtom, mb, bc + 64 * a, krow, bar);
+              }
+            } else {
+              if (PAIR) tma_load_2d_pair(sb, mb, kb * BK, bc, lbar);
+              else tma_load_2d(sb, mb, kb * BK, bc, bar);
+            }
           }
-          if (ok) {
-            if (PAIR) tc_commit_pair(&tail->tfull[a], 0x3);
-            else tc_commit(&tail->tfull[a]);
-          }
-        } while (ok && kb < t.k1);
+          __syncwarp();
+          if (++stage == kStages) { stage = 0; phase ^= 1u; }
+        }
+      }
+      if (PAIR && ok) {
+        // no release of a stage lands after the CTA has exited
+        for (int i = 0; i < kStages && ok; ++i) {
+          if (!mbar_wait(&tail->empty[stage], phase ^ 1u, abort_flag)) ok = false;
+          if (++stage == kStages) { stage = 0; phase ^= 1u; }
+        }
       }
       if (!ok) {
-        latch_error(p.dev_err, OCCULT_ERR_DEVICE_TIMEOUT);
+        if (lane == 0) latch_error(p.dev_err, OCCULT_ERR_DEVICE_TIMEOUT);
         *abort_flag = 1;
       }
+    } else if (warp == 1) {
+      if (lane == 0 && leader) {
+        int stage = 0, it = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        const uint32_t idesc = idesc_bf16_f32(RM, p.bn) | (kAMn ? 1u << 15 : 0u) | (kBMn ? 1u << 16 : 0u);
+        for (int u = unit0; u < total && ok; u += stride) {
+          const Unit t = unit_of<MODE, PAIR>(u, p, m_units, rank, kb_rows);
+          int kb = t.k0;
+          do {   // (a unit without k blocks still hands over its accumulator)
+            const int end = kLogits ? min(t.k1, kb + p.seg) : t.k1;
+            const int a = it & 1;
+            const uint32_t aph = (it >> 1) & 1;
+            ++it;
+            if (!(PAIR ? mbar_wait_cluster(&tail->tempty[a], aph ^ 1u, abort_flag)
+                       : mbar_wait(&tail->tempty[a], aph ^ 1u, abort_flag))) { ok = false; break; }
+            tc_fence_after();
+            const uint32_t acc = tbase + a * BN;
+            for (const int first = kb; kb < end; ++kb) {
+              if (!(PAIR ? mbar_wait_cluster(&tail->full[stage], phase, abort_flag)
+                         : mbar_wait(&tail->full[stage], phase, abort_flag))) { ok = false; break; }
+              tc_fence_after();
+              const uint32_t sa = smem_u32(smem + stage * kStageBytes), sb = sa + kABytes;
+  #pragma unroll
+              for (int kk = 0; kk < BK / 16; ++kk) {
+                const bool add = kb != first || kk != 0;
+                if (PAIR) tc_mma_f16_pair(acc, operand_desc<kAMn>(sa, kk), operand_desc<kBMn>(sb, kk), idesc, add);
+                else tc_mma_f16(acc, operand_desc<kAMn>(sa, kk), operand_desc<kBMn>(sb, kk), idesc, add);
+              }
+              if (PAIR) tc_commit_pair(&tail->empty[stage], 0x3);
+              else tc_commit(&tail->empty[stage]);
+              if (++stage == kStages) { stage = 0; phase ^= 1u; }
+            }
+            if (ok) {
+              if (PAIR) tc_commit_pair(&tail->tfull[a], 0x3);
+              else tc_commit(&tail->tfull[a]);
+            }
+          } while (ok && kb < t.k1);
+        }
+        if (!ok) {
+          latch_error(p.dev_err, OCCULT_ERR_DEVICE_TIMEOUT);
+          *abort_flag = 1;
+        }
+      }
+      __syncwarp();
     }
-    __syncwarp();
   } else {
+    if (kLogits) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(kEpiRegs));
     // ---- epilogue ----------------------------------------------------------
     const int quarter = warp & 3, half = (warp - kEpiWarp0) / 4;
     uint32_t* buf = reinterpret_cast<uint32_t*>(reinterpret_cast<uint8_t*>(tail) + kTailBytes) +
@@ -578,6 +586,13 @@ int launch_one(const LaunchCtx& ctx, const CUtensorMap& ma, const CUtensorMap& m
   static int n_pairs = 0;
   std::call_once(once, [&] {
     err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes(PAIR));
+    if (err == cudaSuccess && (MODE == HEAD_STATS || MODE == HEAD_KEEP)) {
+      // the split of the registers adds up to a launch with this many: another count
+      // (of another compiler) would leave warps waiting for theirs
+      cudaFuncAttributes fa;
+      err = cudaFuncGetAttributes(&fa, kern);
+      if (err == cudaSuccess && fa.numRegs != kLaunchRegs) err = cudaErrorLaunchOutOfResources;
+    }
     if (PAIR && err == cudaSuccess) {
       cfg.gridDim = dim3(2 * (ctx.num_sms / 2));
       err = cudaOccupancyMaxActiveClusters(&n_pairs, kern, &cfg);
