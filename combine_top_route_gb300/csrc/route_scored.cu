@@ -27,9 +27,10 @@ constexpr uint32_t kFull = 0xffffffffu;
 constexpr float kLowest = -3.402823466e+38f;   // a logit as low as this is switched off
 #define OCCULT_NEG_INF (-__int_as_float(0x7f800000))
 
-// Words of the choice: on (bit 31), switched off (bit 30), in no kept group (bit 29);
+// Words of the choice: on (bit 31) or switched off (bit 30);
 // bits 8..30 the rank, the lowest eight 255 - expert (equal ranks: the lower expert).
-constexpr uint32_t kOn = 1u << 31, kOff = 1u << 30, kOut = 1u << 29;
+// 0: none, or in no kept group (the kept ones hold at least k).
+constexpr uint32_t kOn = 1u << 31, kOff = 1u << 30;
 
 __device__ __forceinline__ bool is_off(float z) { return !(z > kLowest); }  // NaN too
 
@@ -37,6 +38,19 @@ __device__ __forceinline__ bool is_off(float z) { return !(z > kLowest); }  // N
 __device__ __forceinline__ uint32_t order_bits(float v) {
   const uint32_t u = __float_as_uint(v + 0.f);
   return (u & 0x80000000u) ? ~u : u | 0x80000000u;
+}
+__device__ __forceinline__ uint64_t order_bits64(double v) {
+  const uint64_t u = static_cast<uint64_t>(__double_as_longlong(v + 0.));
+  return (u >> 63) ? ~u : u | (1ull << 63);
+}
+__device__ __forceinline__ double from_bits64(uint64_t u) {
+  return __longlong_as_double(static_cast<long long>((u >> 63) ? u & ~(1ull << 63) : ~u));
+}
+__device__ __forceinline__ uint64_t shfl_xor64(uint64_t v, int o) {
+  return static_cast<uint64_t>(__shfl_xor_sync(kFull, static_cast<unsigned long long>(v), o));
+}
+__device__ __forceinline__ uint64_t shfl64(uint64_t v, int lane) {
+  return static_cast<uint64_t>(__shfl_sync(kFull, static_cast<unsigned long long>(v), lane));
 }
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
@@ -81,94 +95,130 @@ __device__ __forceinline__ float score_of(float z, float top, float total) {
 }
 
 // ---- the choice in fp64 --------------------------------------------------------------
-// One token, same rules, ranks and worths as doubles.  Returns slot `lane`'s expert.
-// `exp_of` gives the expert at this lane's place i, or -1.
+// An fp64 instruction takes a warp 64 cycles of its scheduler here, a logistic function
+// some fifty of them; comparisons are made on integers of the same order.
+
+// The worth of a group of lanes from the best two (as ordered integers, 0: none).
+__device__ __forceinline__ uint64_t group_worth(uint64_t b1, uint64_t b2, int group_lanes, int best) {
+  for (int o = 1; o < group_lanes; o <<= 1) {
+    const uint64_t c1 = shfl_xor64(b1, o), c2 = shfl_xor64(b2, o);
+    const uint64_t lo = min(b1, c1);
+    b2 = max(max(b2, c2), lo);
+    b1 = max(b1, c1);
+  }
+  if (b1 == 0) return 0;
+  double w = from_bits64(b1);
+  if (best == 2 && b2 != 0) w += from_bits64(b2);
+  // as multiples of 2^-48: sums that the formula makes equal, as sigmoid(x) +
+  // sigmoid(-x) = 1 for every x, then do not hang on the last bits of exp
+  if (fabs(w) < 256.) w = rint(w * 0x1p48) * 0x1p-48;
+  return order_bits64(w);
+}
+
+// The whole choice of one token, ranks and worths as doubles.  Returns slot `lane`'s
+// expert.
 template <bool SIG, int PL>
 __device__ __noinline__ int choose_exactly(const RouteArgs& a, const float* row, const int* s_exp) {
   const int lane = threadIdx.x & 31;
-  const double kNone = -1e300;   // below every rank of finite biases
-  double s[PL];
   float z[PL];
-  uint32_t live = 0, off = 0;
+  uint64_t r[PL];   // rank by score and bias; 0: none or switched off
 #pragma unroll
   for (int i = 0; i < PL; ++i) {
     const int e = s_exp[lane * PL + i];
     z[i] = e >= 0 ? row[e] : kLowest;
-    if (e >= 0) live |= 1u << i;
-    if (is_off(z[i])) off |= 1u << i;
   }
-  if (SIG) {
-#pragma unroll
-    for (int i = 0; i < PL; ++i) s[i] = 1. / (1. + exp(-static_cast<double>(z[i])));
-  } else {
-    float top = kLowest;
+  double inv = 1.;
+  float top = kLowest;
+  if (!SIG) {
 #pragma unroll
     for (int i = 0; i < PL; ++i) top = fmaxf(top, z[i]);
     top = warp_max(top);
     double total = 0.;
-#pragma unroll
-    for (int i = 0; i < PL; ++i) {
-      s[i] = ((off >> i) & 1u) ? 0. : exp(static_cast<double>(z[i]) - static_cast<double>(top));
-      total += s[i];
-    }
+    for (int i = 0; i < PL; ++i)
+      if (!is_off(z[i])) total += exp(static_cast<double>(z[i]) - static_cast<double>(top));
     for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(kFull, total, o);
-#pragma unroll
-    for (int i = 0; i < PL; ++i) s[i] /= total;
+    inv = 1. / total;
   }
-  double b1 = kNone, b2 = kNone;
-#pragma unroll
+  uint64_t b1 = 0, b2 = 0;
+#pragma unroll 1
   for (int i = 0; i < PL; ++i) {
-    if (a.bias && ((live >> i) & 1u)) s[i] += static_cast<double>(a.bias[s_exp[lane * PL + i]]);
-    if (s[i] != s[i]) s[i] = OCCULT_NEG_INF;   // a NaN ranks below every number
-    if (!((off >> i) & 1u)) {
-      if (s[i] > b1) { b2 = b1; b1 = s[i]; } else if (s[i] > b2) b2 = s[i];
-    }
+    const int e = s_exp[lane * PL + i];
+    r[i] = 0;
+    if (is_off(z[i])) continue;
+    double v = SIG ? 1. / (1. + exp(-static_cast<double>(z[i])))
+                   : exp(static_cast<double>(z[i]) - static_cast<double>(top)) * inv;
+    if (a.bias) v += static_cast<double>(a.bias[e]);
+    // a NaN ranks below every number
+    r[i] = order_bits64(v == v ? v : static_cast<double>(OCCULT_NEG_INF));
+    if (r[i] > b1) { b2 = b1; b1 = r[i]; } else if (r[i] > b2) b2 = r[i];
   }
-  uint32_t kept = kFull;
+  bool in = true;
   if (a.G > 1) {
-    for (int o = 1; o < a.group_lanes; o <<= 1) {
-      const double c1 = __shfl_xor_sync(kFull, b1, o), c2 = __shfl_xor_sync(kFull, b2, o);
-      b2 = fmax(fmax(b2, c2), fmin(b1, c1));
-      b1 = fmax(b1, c1);
-    }
-    double worth = a.best == 2 && b2 > kNone ? b1 + b2 : b1;
-    // as multiples of 2^-48: sums that the formula makes equal, as sigmoid(x) +
-    // sigmoid(-x) = 1 for every x, then do not hang on the last bits of exp
-    if (fabs(worth) < 256.) worth = rint(worth * 0x1p48) * 0x1p-48;
+    const uint64_t worth = group_worth(b1, b2, a.group_lanes, a.best);
     const int mine = lane / a.group_lanes;
     int place = 0;
     for (int g = 0; g < a.G; ++g) {
-      const double w = __shfl_sync(kFull, worth, g * a.group_lanes);
+      const uint64_t w = shfl64(worth, g * a.group_lanes);
       place += (w > worth || (w == worth && g < mine)) ? 1 : 0;
     }
-    kept = __ballot_sync(kFull, place < a.keep);
+    in = mine < a.G && place < a.keep;
   }
-  const bool in = (kept >> lane) & 1u;
+  // an expert's word: on (far above 1 for every number), off, or none
+#pragma unroll 1
+  for (int i = 0; i < PL; ++i) {
+    const int e = s_exp[lane * PL + i];
+    r[i] = e < 0 || !in ? 0
+         : is_off(z[i]) ? 1
+         : a.bias ? r[i] : static_cast<uint64_t>(order_bits(z[i]));
+  }
   int mine = 0;
+  uint32_t gone = 0;
   for (int j = 0; j < a.k; ++j) {
-    // best of this lane by level, rank, expert
-    int level = -1, id = 0x7fffffff;
-    double v = kNone;
-#pragma unroll
+    uint64_t v = 0;
+    int id = 0x7fffffff;
+#pragma unroll 1
     for (int i = 0; i < PL; ++i) {
-      if (!((live >> i) & 1u)) continue;
       const int e = s_exp[lane * PL + i];
-      const int lv = !in ? 0 : ((off >> i) & 1u) ? 1 : 2;
-      const double r = lv == 2 ? (a.bias ? s[i] : static_cast<double>(z[i])) : kNone;
-      if (lv > level || (lv == level && (r > v || (r == v && e < id)))) { level = lv; v = r; id = e; }
+      if (((gone >> i) & 1u) || r[i] == 0) continue;
+      if (r[i] > v || (r[i] == v && e < id)) { v = r[i]; id = e; }
     }
     for (int o = 16; o > 0; o >>= 1) {
-      const int lv = __shfl_xor_sync(kFull, level, o);
-      const double r = __shfl_xor_sync(kFull, v, o);
+      const uint64_t w = shfl_xor64(v, o);
       const int e = __shfl_xor_sync(kFull, id, o);
-      if (lv > level || (lv == level && (r > v || (r == v && e < id)))) { level = lv; v = r; id = e; }
+      if (w > v || (w == v && e < id)) { v = w; id = e; }
     }
-#pragma unroll
+#pragma unroll 1
     for (int i = 0; i < PL; ++i)
-      if (s_exp[lane * PL + i] == id) live &= ~(1u << i);
+      if (s_exp[lane * PL + i] == id) gone |= 1u << i;
     if (lane == j) mine = id;
   }
   return mine;
+}
+
+// The border of the kept groups, `last` the last kept and `next` the first left out, whose
+// worths fp32 cannot tell apart: made again in fp64 from the experts of these two that can
+// be among their best (`e1`, `e2`: a lane's two, where `c1`, `c2`).
+// True: the group left out is the better one.
+template <bool SIG, bool BIAS>
+__device__ __noinline__ bool next_is_better(const RouteArgs& a, const float* row, const float* s_bias,
+                                            float top, int e1, int e2, bool c1, bool c2, int last,
+                                            int next) {
+  auto rank = [&](int e, bool c) -> uint64_t {
+    if (!__any_sync(kFull, c)) return 0;
+    uint64_t r = 0;
+    if (c) {
+      const double z = static_cast<double>(row[e]);
+      // (without a bias a softmax's total is a common factor: left out)
+      double v = SIG ? 1. / (1. + exp(-z)) : exp(z - static_cast<double>(top));
+      if (BIAS) v += static_cast<double>(s_bias[e]);
+      r = order_bits64(v);
+    }
+    return r;
+  };
+  const uint64_t r1 = rank(e1, c1), r2 = rank(e2, c2);
+  const uint64_t worth = group_worth(max(r1, r2), min(r1, r2), a.group_lanes, a.best);
+  const uint64_t w0 = shfl64(worth, last * a.group_lanes), w1 = shfl64(worth, next * a.group_lanes);
+  return w1 > w0 || (w1 == w0 && next < last);
 }
 
 template <int PL>
@@ -177,32 +227,98 @@ __device__ __forceinline__ void cas(uint32_t (&v)[PL], int i, int j) {
   v[i] = hi;
   v[j] = lo;
 }
-// A lane's words in descending order (odd-even merge networks).
+// A lane's words in descending order (odd-even merges).
 template <int PL>
 __device__ __forceinline__ void sort_down(uint32_t (&v)[PL]) {
+  if constexpr (PL > 1) {
 #pragma unroll
-  for (int p = 1; p < PL; p *= 2)
+    for (int p = 1; p < PL; p *= 2)
 #pragma unroll
-    for (int q = p; q >= 1; q /= 2)
+      for (int q = p; q >= 1; q /= 2)
 #pragma unroll
-      for (int j = q % p; j + q < PL; j += 2 * q)
+        for (int j = q % p; j + q < PL; j += 2 * q)
 #pragma unroll
-        for (int i = 0; i < q; ++i)
-          if (i + j + q < PL && (i + j) / (2 * p) == (i + j + q) / (2 * p)) cas<PL>(v, i + j, i + j + q);
+          for (int i = 0; i < q; ++i)
+            if (i + j + q < PL && (i + j) / (2 * p) == (i + j + q) / (2 * p)) cas<PL>(v, i + j, i + j + q);
+  }
 }
 
-template <bool SIG, int PL>
-__global__ void __launch_bounds__(kWarps * 32)
+// Blocks an SM: registers for 24 warps, 32 where a lane holds few experts.
+constexpr int blocks_per_sm(int pl) { return pl <= 4 ? 4 : pl <= 8 ? 3 : 1; }
+
+// The first places of a warp's sorted words, a maximum at a time; lane j keeps place j.
+template <int PL>
+__device__ __forceinline__ void draw(uint32_t (&key)[PL], int j, uint32_t& mine) {
+  const uint32_t w = __reduce_max_sync(kFull, key[0]);
+  if (key[0] == w) {
+#pragma unroll
+    for (int i = 0; i + 1 < PL; ++i) key[i] = key[i + 1];
+    key[PL - 1] = 0;
+  }
+  if ((threadIdx.x & 31) == j) mine = w;
+}
+
+// Places too near to each other for their words: more of them until one is clearly lower,
+// then in order by logits, or by fp64 ranks where there is a bias.  False: the whole
+// choice has to be made in fp64.
+template <bool SIG, bool BIAS, int PL>
+__device__ __noinline__ bool order_near(uint32_t (&key)[PL], uint32_t mine, int have, int k, int Ne,
+                                        uint32_t gap_max, const float* row, const float* s_bias,
+                                        int& my_id) {
+  const int lane = threadIdx.x & 31;
+  float z = mine >= kOn ? row[my_id] : 0.f;
+  {
+    // the same logit under the same bias is a tie, and stands in order
+    const float b = BIAS && mine >= kOn ? s_bias[my_id] : 0.f;
+    const uint32_t nxt = __shfl_down_sync(kFull, mine, 1);
+    const float nz = __shfl_down_sync(kFull, z, 1), nb = __shfl_down_sync(kFull, b, 1);
+    if (!__any_sync(kFull, lane < k && lane < 31 && mine >= kOn && nxt >= kOn &&
+                               (mine >> 8) - (nxt >> 8) <= gap_max && !(z == nz && b == nb)))
+      return true;
+  }
+  if (BIAS && !SIG) return false;   // a softmax's total in fp64 takes every expert
+  for (;;) {
+    const uint32_t last = __shfl_sync(kFull, mine, have - 1), prev = __shfl_sync(kFull, mine, have - 2);
+    if (last < kOn || (prev >> 8) - (last >> 8) > gap_max || have == Ne) break;
+    if (have == 32) return false;
+    draw<PL>(key, have++, mine);
+  }
+  my_id = 255 - static_cast<int>(mine & 255u);
+  const bool on = lane < have && mine >= kOn;
+  uint64_t r = 0;   // above 0 for places that are on: they stand before the others
+  if (on) {
+    z = row[my_id];
+    r = BIAS ? order_bits64(1. / (1. + exp(-static_cast<double>(z))) + static_cast<double>(s_bias[my_id]))
+             : static_cast<uint64_t>(order_bits(z)) + 1;
+  }
+  int place = on ? 0 : lane;
+  for (int j = 0; j < have; ++j) {
+    const uint64_t o = shfl64(r, j);
+    const int e = __shfl_sync(kFull, my_id, j);
+    if (on && (o > r || (o == r && e < my_id))) ++place;
+  }
+  int sorted = my_id;
+  for (int j = 0; j < have; ++j) {
+    const int at = __shfl_sync(kFull, place, j), e = __shfl_sync(kFull, my_id, j);
+    if (at == lane) sorted = e;
+  }
+  my_id = sorted;
+  return true;
+}
+
+template <bool SIG, bool BIAS, int PL>
+__global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(PL))
 route_scored_kernel(const RouteArgs a) {
   __shared__ int s_dev[OCCULT_MAX_EXPERTS], s_exp[PL * 32];
   __shared__ float s_bias[OCCULT_MAX_EXPERTS], s_span[2];
+  __shared__ bool s_odd;
   pdl_wait();
   pdl_trigger();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   // the experts of every lane's places, and the bias's span
   for (int e = tid; e < a.Ne; e += blockDim.x) {
     s_dev[e] = a.e2v[e] & 31;
-    s_bias[e] = a.bias ? a.bias[e] : 0.f;
+    s_bias[e] = BIAS ? a.bias[e] : 0.f;
   }
   for (int i = tid; i < PL * 32; i += blockDim.x) {
     const int g = i / PL / a.group_lanes, j = i - g * a.group_lanes * PL;
@@ -216,38 +332,49 @@ route_scored_kernel(const RouteArgs a) {
       for (int f = 0; f < e; ++f) j += s_dev[f] == g ? 1 : 0;
       if (g < a.G && j < a.per) s_exp[g * a.group_lanes * PL + j] = e;
     }
-  if (a.bias && warp == 0) {
+  if (BIAS && warp == 0) {
     float lo = 3e38f, hi = -3e38f;
+    bool odd = false;
     for (int e = lane; e < a.Ne; e += 32) {
-      const float b = s_bias[e];
-      if (fabsf(b) < 1e30f) { lo = fminf(lo, b); hi = fmaxf(hi, b); }
+      lo = fminf(lo, s_bias[e]);
+      hi = fmaxf(hi, s_bias[e]);
+      odd |= !(fabsf(s_bias[e]) < 1e18f);
     }
     lo = -warp_max(-lo);
     hi = warp_max(hi);
-    if (lane == 0) { s_span[0] = fminf(lo, hi); s_span[1] = fmaxf(hi, lo); }
+    odd = __any_sync(kFull, odd);
+    if (lane == 0) { s_span[0] = lo; s_span[1] = hi; s_odd = odd; }
   }
   __syncthreads();
+  // Ranks with a bias lie in [base, base + span]: s * q_mul + c, in whole numbers behind
+  // 2^23, is a rank's place in 2^23 steps of the span.
+  const bool odd = BIAS && s_odd;   // biases without a span: every token in fp64
+  const float base = BIAS && !odd ? s_span[0] : 0.f;
+  const float span = BIAS && !odd ? 1.f + (s_span[1] - s_span[0]) : 1.f;
+  const float q_mul = 8388600.f / span;
+  // A score made with ex2 and rcp is within 2^-21 of itself (|z| <= 16; beyond that its
+  // distance from 0 or 1 is; a softmax's total errs by some 2^-20 as well, for all of its
+  // scores alike), bias and rank within 2^-24 of their size, the steps add a half each:
+  // two ranks further apart than this many steps are in order.
+  const float slack = (SIG ? 0x1p-20f : 0x1p-19f) + 0x1p-22f * (fabsf(base) + span);
+  const uint32_t gap_max = BIAS ? static_cast<uint32_t>(fminf(slack * q_mul, 8388606.f)) + 3u : 0u;
+  // (the words' steps come on top where worths are made from them)
+  const float slack_worth = 2.f * slack + (BIAS ? 4.f / q_mul : 0.f);
   int ex[PL];
-  float b[PL];
+  uint32_t low[PL];
+  float c[PL];
 #pragma unroll
   for (int i = 0; i < PL; ++i) {
     ex[i] = s_exp[lane * PL + i];
-    b[i] = ex[i] >= 0 ? s_bias[ex[i]] : 0.f;
+    low[i] = 255u - static_cast<uint32_t>(ex[i]);
+    c[i] = BIAS && ex[i] >= 0 ? fmaf(s_bias[ex[i]] - base, q_mul, 8388608.f) : 0.f;
   }
-  // ranks with a bias lie in [base, base + span]; a word holds them in 2^23 steps
-  const float base = a.bias ? s_span[0] : 0.f, span = a.bias ? 1.f + (s_span[1] - s_span[0]) : 1.f;
-  const float q_mul = 8388607.f / span;
-  // A score made with ex2 and rcp is within 2^-21 of itself (|z| <= 16; beyond that its
-  // distance from 0 or 1 is), the sum with the bias within 2^-24 of the rank's size, the
-  // step adds its half: two ranks further apart than this many steps are in order.  (A
-  // softmax's total errs by some 2^-20 as well, for all of its scores alike.)
-  const float slack = (SIG ? 0x1p-20f : 0x1p-19f) + 0x1p-23f * fmaxf(fabsf(base), fabsf(base + span));
-  const uint32_t near = static_cast<uint32_t>(fminf(slack * q_mul, 8388606.f)) + 2u;
   const int my_group = lane / a.group_lanes;
+  const int rounds = min(min(a.k + 1, a.Ne), 32);
 
   for (int t = blockIdx.x * kWarps + warp; t < a.T; t += gridDim.x * kWarps) {
     const float* row = a.logits + static_cast<size_t>(t) * a.Ne;
-    float z[PL], s[PL];
+    float z[PL];
     if (PL % 4 == 0 && a.vec) {
 #pragma unroll
       for (int i = 0; i < PL; i += 4) {
@@ -259,8 +386,7 @@ route_scored_kernel(const RouteArgs a) {
 #pragma unroll
       for (int i = 0; i < PL; ++i) z[i] = ex[i] >= 0 ? row[ex[i]] : kLowest;
     }
-    float top = 0.f, total = 1.f;
-    const bool scored = a.bias || a.G > 1;   // else the logits alone choose
+    float top = 0.f, total = 1.f, s[PL];
     if (!SIG) {
       top = kLowest;
 #pragma unroll
@@ -277,23 +403,40 @@ route_scored_kernel(const RouteArgs a) {
       const float inv = total > 0.f ? 1.f / total : 0.f;
 #pragma unroll
       for (int i = 0; i < PL; ++i) s[i] *= inv;
-    } else if (scored) {
+    } else if (BIAS || a.G > 1) {
 #pragma unroll
       for (int i = 0; i < PL; ++i) s[i] = rcp(1.f + ex2(z[i] * -kLog2e));
-    } else {
+    } else {   // the logits alone choose
 #pragma unroll
       for (int i = 0; i < PL; ++i) s[i] = 0.f;
     }
 
-    bool in = true, exact = false;
-    if (a.G > 1) {
-      float b1 = kLowest, b2 = kLowest;
+    uint32_t key[PL];
 #pragma unroll
-      for (int i = 0; i < PL; ++i) {
-        float r = s[i] + b[i];
-        r = is_off(z[i]) ? kLowest : r == r ? r : OCCULT_NEG_INF;
-        b2 = fmaxf(b2, fminf(b1, r));
-        b1 = fmaxf(b1, r);
+    for (int i = 0; i < PL; ++i) {
+      const uint32_t q = BIAS ? __float_as_uint(fmaf(s[i], q_mul, c[i])) << 8
+                              : (order_bits(z[i]) >> 1) & 0x7fffff00u;
+      key[i] = is_off(z[i]) ? kOff | low[i] : q + (kOn | low[i]);
+      if (ex[i] < 0) key[i] = 0;
+    }
+    sort_down<PL>(key);
+
+    bool exact = odd;
+    if (a.G > 1) {
+      // the group's best two: with a bias from the words, else from the scores
+      float b1 = kLowest, b2 = kLowest;
+      if (BIAS) {
+        const float back = span / 8388600.f;
+        if (key[0] >= kOn) b1 = fmaf(static_cast<float>((key[0] >> 8) & 0x7fffffu), back, base);
+        if (PL > 1 && key[PL > 1 ? 1 : 0] >= kOn)
+          b2 = fmaf(static_cast<float>((key[PL > 1 ? 1 : 0] >> 8) & 0x7fffffu), back, base);
+      } else {
+#pragma unroll
+        for (int i = 0; i < PL; ++i) {
+          const float r = is_off(z[i]) ? kLowest : s[i];
+          b2 = fmaxf(b2, fminf(b1, r));
+          b1 = fmaxf(b1, r);
+        }
       }
       for (int o = 1; o < a.group_lanes; o <<= 1) {
         const float c1 = __shfl_xor_sync(kFull, b1, o), c2 = __shfl_xor_sync(kFull, b2, o);
@@ -301,102 +444,63 @@ route_scored_kernel(const RouteArgs a) {
         b1 = fmaxf(b1, c1);
       }
       const float worth = a.best == 2 && b2 > kLowest ? b1 + b2 : b1;
-      int place = 0;
-      float gap = 3e38f;   // to the nearest other worth
-      for (int g = 0; g < a.G; ++g) {
-        const float w = __shfl_sync(kFull, worth, g * a.group_lanes);
-        place += (w > worth || (w == worth && g < my_group)) ? 1 : 0;
-        if (g != my_group) gap = fminf(gap, fabsf(w - worth));
+      // the keep groups of largest worth, one maximum each: equal ones from the left; then
+      // the first left out, which the last kept must be clearly above
+      uint32_t wkey = my_group < a.G ? order_bits(worth) : 0u;
+      uint32_t in = 0, last = 0, before = 0;
+      int g_last = 0;
+      for (int g = 0; g < a.keep; ++g) {
+        before = last;
+        last = __reduce_max_sync(kFull, wkey);
+        g_last = (__ffs(__ballot_sync(kFull, wkey == last)) - 1) / a.group_lanes;
+        if (my_group == g_last) { wkey = 0; in = 1; }
       }
-      in = place < a.keep;
-      // the last group kept: within the scores' error of a neighbour (two groups without
-      // an expert are equal exactly)
-      exact = __any_sync(kFull, my_group < a.G && a.keep < a.G && place == a.keep - 1 &&
-                                    worth > kLowest && gap <= 2.f * slack + 0x1p-22f * fabsf(worth));
+      if (a.keep < a.G) {
+        auto unbits = [](uint32_t u) { return __uint_as_float((u & 0x80000000u) ? u & 0x7fffffffu : ~u); };
+        const uint32_t next = __reduce_max_sync(kFull, wkey);
+        const float w0 = unbits(last), w1 = unbits(next);
+        const float tell = slack_worth + 0x1p-22f * (fabsf(w0) + fabsf(w1));
+        // (two groups without an expert are equal exactly)
+        if (w1 > kLowest && w0 - w1 <= tell) {
+          const int g_next = (__ffs(__ballot_sync(kFull, wkey == next)) - 1) / a.group_lanes;
+          const uint32_t after = __reduce_max_sync(kFull, my_group == g_next ? 0u : wkey);
+          // what can be among the best of these two groups: a lane's best two, no third
+          const float edge = (a.best == 2 && b2 > kLowest ? b2 : b1) - tell;
+          const bool here = my_group == g_last || my_group == g_next;
+          int e1 = -1, e2 = -1;
+          bool many = false;
+          float r1 = kLowest;
+#pragma unroll
+          for (int i = 0; i < PL; ++i) {
+            const float r = BIAS ? s[i] + s_bias[max(ex[i], 0)] : s[i];
+            if (!here || is_off(z[i]) || !(r >= edge)) continue;
+            many |= e2 >= 0;
+            if (r > r1) { e2 = e1; e1 = ex[i]; r1 = r; } else e2 = ex[i];
+          }
+          if ((BIAS && !SIG) || __any_sync(kFull, many) || (a.keep > 1 && unbits(before) - w1 <= tell) ||
+              (after != 0 && w0 - unbits(after) <= tell)) {
+            exact = true;
+          } else if (next_is_better<SIG, BIAS>(a, row, s_bias, top, e1, e2, e1 >= 0, e2 >= 0, g_last, g_next)) {
+            if (my_group == g_last) in = 0;
+            if (my_group == g_next) in = 1;
+          }
+        }
+      }
+      if (!in) {
+#pragma unroll
+        for (int i = 0; i < PL; ++i) key[i] = 0;
+      }
     }
 
     int my_id = 0;
     if (!exact) {
-      uint32_t key[PL];
-#pragma unroll
-      for (int i = 0; i < PL; ++i) {
-        const uint32_t low = 255u - static_cast<uint32_t>(ex[i]);
-        uint32_t q;
-        if (a.bias) {
-          const float r = s[i] + b[i];
-          q = __float_as_uint(fminf(fmaxf(fmaf(r - base, q_mul, 8388608.f), 8388608.f), 16777215.f)) & 0x7fffffu;
-        } else {
-          q = order_bits(z[i]) >> 9;
-        }
-        key[i] = ex[i] < 0 ? 0u : !in ? kOut | low : is_off(z[i]) ? kOff | low : kOn | (q << 8) | low;
-      }
-      sort_down<PL>(key);
-      // the first k + 1 (at most 32, at most all): lane j keeps place j
-      const int rounds = min(min(a.k + 1, a.Ne), 32);
       uint32_t mine = 0;
-      auto draw = [&](int j) {
-        const uint32_t w = __reduce_max_sync(kFull, key[0]);
-        if (key[0] == w) {
-#pragma unroll
-          for (int i = 0; i + 1 < PL; ++i) key[i] = key[i + 1];
-          key[PL - 1] = 0;
-        }
-        if (lane == j) mine = w;
-      };
-      for (int j = 0; j < rounds; ++j) draw(j);
+      for (int j = 0; j < rounds; ++j) draw<PL>(key, j, mine);
       my_id = 255 - static_cast<int>(mine & 255u);
-      // A place not clearly above the next: the same logit under the same bias is a tie
-      // (the lower expert stands first already), others are looked at closely.
-      const uint32_t gap_max = a.bias ? near : 0u;
-      const int n_exp = a.Ne;
-      bool on = lane < rounds && mine >= kOn;
-      float cz = on ? row[my_id] : 0.f, cb = on ? s_bias[my_id] : 0.f;
-      auto close = [&]() -> bool {   // of this lane's place and the next
-        const uint32_t nxt = __shfl_down_sync(kFull, mine, 1);
-        const float nz = __shfl_down_sync(kFull, cz, 1), nb = __shfl_down_sync(kFull, cb, 1);
-        return lane < 31 && mine >= kOn && nxt >= kOn && (mine >> 8) - (nxt >> 8) <= gap_max &&
-               !(cz == nz && cb == nb);
-      };
-      if (__any_sync(kFull, close() && lane < a.k)) {
-        // more places until one is clearly below (a tie counts as not clear here)
-        int have = rounds;
-        while (have < min(n_exp, 32)) {
-          const uint32_t last = __shfl_sync(kFull, mine, have - 1), prev = __shfl_sync(kFull, mine, have - 2);
-          if (last < kOn || (prev >> 8) - (last >> 8) > gap_max) break;
-          draw(have++);
-        }
-        const uint32_t last = __shfl_sync(kFull, mine, have - 1), prev = __shfl_sync(kFull, mine, max(0, have - 2));
-        if ((a.bias && !SIG) || (have == 32 && n_exp > 32 && last >= kOn && (prev >> 8) - (last >> 8) <= gap_max)) {
-          exact = true;   // (a softmax's total in fp64 takes every expert)
-        } else {
-          my_id = 255 - static_cast<int>(mine & 255u);
-          on = lane < have && mine >= kOn;
-          cz = on ? row[my_id] : 0.f;
-          // the rank in fp64; lanes that hold no place, or one switched off, stay behind
-          double r = -1e305;
-          if (on) {
-            r = static_cast<double>(cz);
-            if (a.bias) {
-              r = 1. / (1. + exp(-r)) + static_cast<double>(s_bias[my_id]);
-              if (r != r || r < -1e300) r = -1e301;
-            }
-          }
-          int place = 0;
-          for (int j = 0; j < have; ++j) {
-            const double o = __shfl_sync(kFull, r, j);
-            const int e = __shfl_sync(kFull, my_id, j);
-            const bool other_on = __shfl_sync(kFull, static_cast<int>(on), j);
-            place += on ? (other_on && (o > r || (o == r && e < my_id)) ? 1 : 0) : (j < lane ? 1 : 0);
-          }
-          // (places behind the ones that are on keep their order)
-          int sorted = 0;
-          for (int j = 0; j < have; ++j) {
-            const int at = __shfl_sync(kFull, place, j), e = __shfl_sync(kFull, my_id, j);
-            if (at == lane) sorted = e;
-          }
-          my_id = sorted;
-        }
-      }
+      const uint32_t nxt = __shfl_down_sync(kFull, mine, 1);
+      if (__any_sync(kFull, lane < a.k && lane < 31 && mine >= kOn && nxt >= kOn &&
+                                (mine >> 8) - (nxt >> 8) <= gap_max))
+        exact = !order_near<SIG, BIAS, PL>(key, mine, rounds, a.k, a.Ne, gap_max, row, s_bias, my_id);
     }
     if (exact) my_id = choose_exactly<SIG, PL>(a, row, s_exp);
     if (my_id < 0 || my_id >= a.Ne) my_id = 0;   // (devices that do not share the experts evenly)
@@ -404,7 +508,7 @@ route_scored_kernel(const RouteArgs a) {
     float g = lane < a.k ? score_of<SIG>(row[my_id], top, total) : 0.f;
     if (a.renorm) {
       const float sum = warp_sum(g);
-      g = sum == 0.f ? 0.f : g / sum;
+      g = sum == 0.f ? 0.f : __fdividef(g, sum);
     }
     const uint32_t vm = __reduce_or_sync(kFull, lane < a.k ? 1u << s_dev[my_id] : 0u);
     if (lane < a.k) {
@@ -504,9 +608,9 @@ bias_step_kernel(const int32_t* __restrict__ counts, int G, int Ne, float rate,
   }
 }
 
-int blocks_for(const LaunchCtx& ctx, int T) {
+int blocks_for(const LaunchCtx& ctx, int T, int per_sm) {
   const int blocks = (T + kWarps - 1) / kWarps;
-  return blocks < ctx.num_sms * 8 ? blocks : ctx.num_sms * 8;
+  return blocks < ctx.num_sms * per_sm ? blocks : ctx.num_sms * per_sm;
 }
 
 }  // namespace
@@ -530,10 +634,12 @@ int launch_route_scored(const LaunchCtx& ctx, const occult_desc_t& ds, const occ
   // whole fours of a row: consecutive experts, none cut off, rows on 16 bytes
   a.vec = !a.vdev_groups && a.per % 4 == 0 && a.Ne % 4 == 0 && reinterpret_cast<uintptr_t>(logits) % 16 == 0;
   const bool sig = opt.score == OCCULT_SCORE_SIGMOID;
-  const int nb = blocks_for(ctx, ds.T);
-#define OCCULT_SCORED(PL) \
-  cuda_status(launch_pdl(sig ? route_scored_kernel<true, PL> : route_scored_kernel<false, PL>, nb, \
-                         kWarps * 32, 0, ctx.stream, a))
+#define OCCULT_SCORED(PL)                                                                  \
+  cuda_status(launch_pdl(sig ? (bias ? route_scored_kernel<true, true, PL>                 \
+                                     : route_scored_kernel<true, false, PL>)               \
+                             : (bias ? route_scored_kernel<false, true, PL>                \
+                                     : route_scored_kernel<false, false, PL>),             \
+                         blocks_for(ctx, ds.T, blocks_per_sm(PL)), kWarps * 32, 0, ctx.stream, a))
   if (need <= 1) return OCCULT_SCORED(1);
   if (need <= 2) return OCCULT_SCORED(2);
   if (need <= 4) return OCCULT_SCORED(4);
@@ -547,7 +653,7 @@ int launch_route_scored_grad(const LaunchCtx& ctx, const occult_desc_t& ds,
                              const float* dgates, float* dlogits) {
   if (ds.T == 0) return OCCULT_OK;
   const bool sig = opt.score == OCCULT_SCORE_SIGMOID;
-  const int nb = blocks_for(ctx, ds.T);
+  const int nb = blocks_for(ctx, ds.T, 8);
 #define OCCULT_SCORED_GRAD(PL)                                                                         \
   cuda_status(launch_pdl(sig ? route_scored_grad_kernel<true, PL> : route_scored_grad_kernel<false, PL>, \
                          nb, kWarps * 32, 0, ctx.stream, logits, ids, dgates, dlogits, ds.T,           \
