@@ -82,7 +82,8 @@ struct RouteArgs {
   float* gates;
   uint32_t* vmask;
   int T, Ne, k, G, keep, best, vdev_groups, renorm;
-  int per, group_lanes;    // experts and lanes of a group
+  int per, group_lanes;    // experts and lanes of a group (2^group_shift)
+  int group_shift, holes;  // holes: some of the lanes' places hold no expert
   int vec;                 // a lane's experts are aligned fours of consecutive logits
   float scale;
 };
@@ -244,7 +245,7 @@ __device__ __forceinline__ void sort_down(uint32_t (&v)[PL]) {
 }
 
 // Blocks an SM: registers for 24 warps, 32 where a lane holds few experts.
-constexpr int blocks_per_sm(int pl) { return pl <= 4 ? 4 : pl <= 8 ? 3 : 1; }
+constexpr int blocks_per_sm(int pl) { return pl <= 2 ? 5 : pl <= 8 ? 4 : 1; }
 
 // The first places of a warp's sorted words, a maximum at a time; lane j keeps place j.
 template <int PL>
@@ -369,7 +370,7 @@ route_scored_kernel(const RouteArgs a) {
     low[i] = 255u - static_cast<uint32_t>(ex[i]);
     c[i] = BIAS && ex[i] >= 0 ? fmaf(s_bias[ex[i]] - base, q_mul, 8388608.f) : 0.f;
   }
-  const int my_group = lane / a.group_lanes;
+  const int my_group = lane >> a.group_shift;
   const int rounds = min(min(a.k + 1, a.Ne), 32);
 
   for (int t = blockIdx.x * kWarps + warp; t < a.T; t += gridDim.x * kWarps) {
@@ -417,7 +418,11 @@ route_scored_kernel(const RouteArgs a) {
       const uint32_t q = BIAS ? __float_as_uint(fmaf(s[i], q_mul, c[i])) << 8
                               : (order_bits(z[i]) >> 1) & 0x7fffff00u;
       key[i] = is_off(z[i]) ? kOff | low[i] : q + (kOn | low[i]);
-      if (ex[i] < 0) key[i] = 0;
+    }
+    if (a.holes) {
+#pragma unroll
+      for (int i = 0; i < PL; ++i)
+        if (ex[i] < 0) key[i] = 0;
     }
     sort_down<PL>(key);
 
@@ -452,7 +457,7 @@ route_scored_kernel(const RouteArgs a) {
       for (int g = 0; g < a.keep; ++g) {
         before = last;
         last = __reduce_max_sync(kFull, wkey);
-        g_last = (__ffs(__ballot_sync(kFull, wkey == last)) - 1) / a.group_lanes;
+        g_last = (__ffs(__ballot_sync(kFull, wkey == last)) - 1) >> a.group_shift;
         if (my_group == g_last) { wkey = 0; in = 1; }
       }
       if (a.keep < a.G) {
@@ -462,7 +467,7 @@ route_scored_kernel(const RouteArgs a) {
         const float tell = slack_worth + 0x1p-22f * (fabsf(w0) + fabsf(w1));
         // (two groups without an expert are equal exactly)
         if (w1 > kLowest && w0 - w1 <= tell) {
-          const int g_next = (__ffs(__ballot_sync(kFull, wkey == next)) - 1) / a.group_lanes;
+          const int g_next = (__ffs(__ballot_sync(kFull, wkey == next)) - 1) >> a.group_shift;
           const uint32_t after = __reduce_max_sync(kFull, my_group == g_next ? 0u : wkey);
           // what can be among the best of these two groups: a lane's best two, no third
           const float edge = (a.best == 2 && b2 > kLowest ? b2 : b1) - tell;
@@ -495,6 +500,7 @@ route_scored_kernel(const RouteArgs a) {
     int my_id = 0;
     if (!exact) {
       uint32_t mine = 0;
+#pragma unroll 3
       for (int j = 0; j < rounds; ++j) draw<PL>(key, j, mine);
       my_id = 255 - static_cast<int>(mine & 255u);
       const uint32_t nxt = __shfl_down_sync(kFull, mine, 1);
@@ -630,16 +636,18 @@ int launch_route_scored(const LaunchCtx& ctx, const occult_desc_t& ds, const occ
   int groups = 1;   // the power of two from G up
   while (groups < a.G) groups *= 2;
   a.group_lanes = 32 / groups;
+  while ((1 << a.group_shift) < a.group_lanes) ++a.group_shift;
   const int need = (a.per + a.group_lanes - 1) / a.group_lanes;   // experts a lane: at most 15
   // whole fours of a row: consecutive experts, none cut off, rows on 16 bytes
   a.vec = !a.vdev_groups && a.per % 4 == 0 && a.Ne % 4 == 0 && reinterpret_cast<uintptr_t>(logits) % 16 == 0;
   const bool sig = opt.score == OCCULT_SCORE_SIGMOID;
 #define OCCULT_SCORED(PL)                                                                  \
-  cuda_status(launch_pdl(sig ? (bias ? route_scored_kernel<true, true, PL>                 \
+  (a.holes = a.vdev_groups || a.group_lanes * a.G != 32 || a.per != a.group_lanes * PL,    \
+   cuda_status(launch_pdl(sig ? (bias ? route_scored_kernel<true, true, PL>                 \
                                      : route_scored_kernel<true, false, PL>)               \
                              : (bias ? route_scored_kernel<false, true, PL>                \
                                      : route_scored_kernel<false, false, PL>),             \
-                         blocks_for(ctx, ds.T, blocks_per_sm(PL)), kWarps * 32, 0, ctx.stream, a))
+                         blocks_for(ctx, ds.T, blocks_per_sm(PL)), kWarps * 32, 0, ctx.stream, a)))
   if (need <= 1) return OCCULT_SCORED(1);
   if (need <= 2) return OCCULT_SCORED(2);
   if (need <= 4) return OCCULT_SCORED(4);
