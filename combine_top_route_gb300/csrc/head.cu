@@ -41,90 +41,102 @@ __device__ __forceinline__ float warp_max(float v) {
 enum : uint8_t { kRowCe = 1, kRowKd = 2 };
 
 // ---- rows -----------------------------------------------------------------------
-// One block: thread i takes a run of consecutive tokens, counts those that a term
-// counts, and writes their rows behind those of the threads before it.
-__global__ void __launch_bounds__(1024)
+// Which tokens a term counts, and their compact rows in token order.  A block has `per`
+// tokens of its own and counts all of them (a few KB from L2, which is cheaper than
+// another launch): those before its own give its first row, all of them the totals.
+// Where some token is left out, bf16 layers' rows of x are copied to their compact place
+// on the way (else the products read x itself), with zeros up to the next multiple of 64,
+// so that dw's reduction may run over them.
+constexpr int kRowThreads = 256;
+__global__ void __launch_bounds__(kRowThreads)
 head_rows_kernel(const int32_t* __restrict__ labels, const int32_t* __restrict__ t_ids, int T,
-                 int V, int K, HeadCounts* cnt, int32_t* __restrict__ idx,
+                 int V, int K, int per, HeadCounts* cnt, int32_t* __restrict__ idx,
                  int32_t* __restrict__ pos, uint8_t* __restrict__ flag, int32_t* __restrict__ ent,
-                 float* __restrict__ ent_q, float* __restrict__ lse, float* __restrict__ token_loss) {
-  __shared__ int s_n[32], s_ce[32], s_kd[32];
+                 float* __restrict__ ent_q, float* __restrict__ lse, float* __restrict__ token_loss,
+                 const uint4* __restrict__ x, uint4* __restrict__ xc, int vecs) {
+  __shared__ int s_sum[4][kRowThreads / 32], s_warp[kRowThreads / 32], s_pos[kRowThreads];
   pdl_wait();
   pdl_trigger();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int per = (T + 1023) / 1024;
-  const int t0 = min(T, tid * per), t1 = min(T, t0 + per);
+  const int t0 = min(T, static_cast<int>(blockIdx.x) * per), t1 = min(T, t0 + per);
   auto flag_of = [&](int t) -> int {
     int f = 0;
     if (labels && static_cast<unsigned>(labels[t]) < static_cast<unsigned>(V)) f |= kRowCe;
     if (K && static_cast<unsigned>(t_ids[static_cast<size_t>(t) * K]) < static_cast<unsigned>(V)) f |= kRowKd;
     return f;
   };
-  int n = 0, ce = 0, kd = 0;
-  for (int t = t0; t < t1; ++t) {
+  int sum[4] = {0, 0, 0, 0};   // rows before this block's, rows, with a label, with a teacher
+#pragma unroll 8
+  for (int t = tid; t < T; t += kRowThreads) {
     const int f = flag_of(t);
-    n += f != 0;
-    ce += (f & kRowCe) != 0;
-    kd += (f & kRowKd) != 0;
+    sum[0] += (f != 0 && t < t0) ? 1 : 0;
+    sum[1] += f != 0 ? 1 : 0;
+    sum[2] += (f & kRowCe) ? 1 : 0;
+    sum[3] += (f & kRowKd) ? 1 : 0;
   }
-  int incl = n;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int v = __shfl_up_sync(kFull, incl, o);
-    if (lane >= o) incl += v;
+  for (int i = 0; i < 4; ++i) {
+    const int v = __reduce_add_sync(kFull, sum[i]);
+    if (lane == 0) s_sum[i][warp] = v;
   }
-  ce = __reduce_add_sync(kFull, ce);
-  kd = __reduce_add_sync(kFull, kd);
-  if (lane == 31) { s_n[warp] = incl; s_ce[warp] = ce; s_kd[warp] = kd; }
   __syncthreads();
-  int before = 0, all = 0, all_ce = 0, all_kd = 0;
-  for (int w = 0; w < 32; ++w) {
-    if (w < warp) before += s_n[w];
-    all += s_n[w];
-    all_ce += s_ce[w];
-    all_kd += s_kd[w];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    sum[i] = 0;
+    for (int w = 0; w < kRowThreads / 32; ++w) sum[i] += s_sum[i][w];
   }
-  int r = before + incl - n;
-  for (int t = t0; t < t1; ++t) {
-    const int f = flag_of(t);
-    if (f) {
-      idx[r] = t;
-      flag[r] = static_cast<uint8_t>(f);
-      if (K == 0) {   // the label is a row's only entry
-        ent[r] = labels[t];
-        ent_q[r] = -1.f;
-      }
-      pos[t] = r++;
-    } else {
-      pos[t] = -1;
-      if (lse) lse[t] = 0.f;
-      if (token_loss) token_loss[t] = 0.f;
-    }
-  }
-  if (tid == 0) {
-    cnt->n = all;
-    cnt->n_ce = all_ce;
-    cnt->n_kd = all_kd;
+  const int n = sum[1];
+  if (blockIdx.x == 0 && tid == 0) {
+    cnt->n = n;
+    cnt->n_ce = sum[2];
+    cnt->n_kd = sum[3];
     cnt->ticket = 0;
   }
-}
-
-// ---- compact copy of x (bf16) -----------------------------------------------------
-// Only where some token is left out: the products read x itself otherwise.  Rows up to
-// the next multiple of 64 are zeros, so that dw's reduction may run over them.
-__global__ void __launch_bounds__(256)
-head_gather_kernel(const uint4* __restrict__ x, uint4* __restrict__ xc, const HeadCounts* cnt,
-                   const int32_t* __restrict__ idx, int T, int vecs) {
-  pdl_wait();
-  pdl_trigger();
-  const int n = cnt->n;
-  if (n == T) return;
-  const int rows = min((n + 63) & ~63, (T + kHeadRowAlign - 1) / kHeadRowAlign * kHeadRowAlign);
-  for (int r = blockIdx.x; r < rows; r += gridDim.x) {
-    const uint4* src = r < n ? x + static_cast<size_t>(idx[r]) * vecs : nullptr;
-    uint4* dst = xc + static_cast<size_t>(r) * vecs;
-    for (int i = threadIdx.x; i < vecs; i += blockDim.x) dst[i] = src ? src[i] : make_uint4(0, 0, 0, 0);
+  const bool copy = xc && n < T;
+  int row = sum[0];   // first row of the block's next tokens
+  for (int base = t0; base < t1; base += kRowThreads) {
+    const int t = base + tid;
+    const int f = t < t1 ? flag_of(t) : 0;
+    const unsigned on = __ballot_sync(kFull, f != 0);
+    if (lane == 0) s_warp[warp] = __popc(on);
+    __syncthreads();
+    int r = row + __popc(on & lanemask_lt()), all = 0;
+    for (int w = 0; w < kRowThreads / 32; ++w) {
+      if (w < warp) r += s_warp[w];
+      all += s_warp[w];
+    }
+    s_pos[tid] = f ? r : -1;
+    if (t < t1) {
+      pos[t] = f ? r : -1;
+      if (f) {
+        idx[r] = t;
+        flag[r] = static_cast<uint8_t>(f);
+        if (K == 0) {   // the label is a row's only entry
+          ent[r] = labels[t];
+          ent_q[r] = -1.f;
+        }
+      } else {
+        if (lse) lse[t] = 0.f;
+        if (token_loss) token_loss[t] = 0.f;
+      }
+    }
+    __syncthreads();
+    if (copy)
+      for (int i = warp; i < min(kRowThreads, t1 - base); i += kRowThreads / 32) {
+        const int to = s_pos[i];
+        if (to < 0) continue;
+        const uint4* src = x + static_cast<size_t>(base + i) * vecs;
+        uint4* dst = xc + static_cast<size_t>(to) * vecs;
+#pragma unroll 4
+        for (int v = lane; v < vecs; v += 32) dst[v] = src[v];
+      }
+    row += all;
+    __syncthreads();
   }
+  if (copy && blockIdx.x == gridDim.x - 1)
+    for (size_t i = static_cast<size_t>(n) * vecs + tid; i < static_cast<size_t>((n + 63) & ~63) * vecs;
+         i += kRowThreads)
+      xc[i] = make_uint4(0, 0, 0, 0);
 }
 
 // ---- entries ----------------------------------------------------------------------
@@ -234,25 +246,29 @@ head_sum_kernel(HeadCounts* cnt, const float* __restrict__ pm, const float* __re
     // parts of row r_first + lane
     const int r = min(r_first + lane, n - 1);
     float m = NEG, s = 0.f, s2 = 0.f;
-    for (int h0 = warp; h0 < halves; h0 += 4 * kSumWarps) {
-      float vm[4], vs[4], vt[4];
+    constexpr int kAhead = TWO ? 6 : 8;   // parts in flight
+    for (int h0 = warp; h0 < halves; h0 += kAhead * kSumWarps) {
+      float vm[kAhead], vs[kAhead], vt[kAhead];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
+      for (int u = 0; u < kAhead; ++u) {
         const int h = h0 + u * kSumWarps;
         const size_t at = static_cast<size_t>(h) * ldp + r;
         vm[u] = h < halves ? pm[at] : NEG;
         vs[u] = h < halves ? ps[at] : 0.f;
         vt[u] = TWO && h < halves ? ps2[at] : 0.f;
       }
+      float hi = m;
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const float hi = fmaxf(m, vm[u]);
-        if (hi == NEG) { s += vs[u]; continue; }   // (a NaN sum stays one)
-        const float fa = ex2(m - hi), fb = ex2(vm[u] - hi);
-        s = s * fa + vs[u] * fb;
-        if (TWO) s2 = s2 * ex2((m - hi) * inv_tau) + vt[u] * ex2((vm[u] - hi) * inv_tau);
-        m = hi;
+      for (int u = 0; u < kAhead; ++u) hi = fmaxf(hi, vm[u]);
+      const float to = hi == NEG ? 0.f : hi;
+      s *= ex2(m - to);
+      if (TWO) s2 *= ex2((m - to) * inv_tau);
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        s = fmaf(vs[u], ex2(vm[u] - to), s);
+        if (TWO) s2 = fmaf(vt[u], ex2((vm[u] - to) * inv_tau), s2);
       }
+      m = hi;
     }
     s_m[warp][lane] = m;
     s_s[warp][lane] = s;
@@ -353,8 +369,9 @@ __device__ __forceinline__ void row_factors(const DzArgs& a, const HeadScale& sc
 }
 
 // bf16 layers: the kept 16-bit logits (units of q_step octaves below the maximum of
-// their 128 columns) become bf16 gradients where they lie.  A warp takes 32 rows of 128
-// columns: the maxima come in along the rows, 16 lanes read a row's 256 bytes.
+// their 128 columns) become bf16 gradients where they lie.  A warp takes 8 rows of 128
+// columns, 16 lanes a row's 256 bytes, all of its loads in flight at once.
+constexpr int kDzRows = 8;
 __global__ void __launch_bounds__(256)
 head_dz_bf16_kernel(const DzArgs a, uint16_t* __restrict__ kept) {
   pdl_wait();
@@ -363,11 +380,11 @@ head_dz_bf16_kernel(const DzArgs a, uint16_t* __restrict__ kept) {
   const int n = min(a.cnt->n - a.row0, a.piece);
   if (n <= 0) return;
   const HeadScale sc = head_scale(a.cnt->n, a.cnt->n_ce, a.cnt->n_kd, a.coef, a.coef_kd, a.coef_z, a.tau);
-  const int r0 = blockIdx.y * 32;
+  const int r0 = blockIdx.y * kDzRows;
   if (r0 >= ((n + kHeadRowAlign - 1) & ~(kHeadRowAlign - 1))) return;
   const int h = blockIdx.x * 8 + warp;
   if (h * 128 >= a.ld) return;
-  const int r = r0 + lane;
+  const int r = r0 + (lane & (kDzRows - 1));
   float m = 0.f, L1 = 0.f, L2 = 0.f, k1 = 0.f, k2 = 0.f;
   if (r < n) {
     m = a.pm[static_cast<size_t>(h) * a.ldp + r];
@@ -378,8 +395,14 @@ head_dz_bf16_kernel(const DzArgs a, uint16_t* __restrict__ kept) {
   }
   const int c0 = h * 128 + (lane & 15) * 8;
   char* base = reinterpret_cast<char*>(kept + static_cast<size_t>(r0) * a.ld + c0);
-#pragma unroll 4
-  for (int i = 0; i < 16; ++i) {
+  uint4 u[kDzRows / 2];
+#pragma unroll
+  for (int i = 0; i < kDzRows / 2; ++i) {
+    const int rr = 2 * i + (lane >> 4);
+    if (r0 + rr < n) u[i] = *reinterpret_cast<const uint4*>(base + static_cast<size_t>(rr) * a.ld * 2);
+  }
+#pragma unroll
+  for (int i = 0; i < kDzRows / 2; ++i) {
     const int rr = 2 * i + (lane >> 4);
     const float mm = __shfl_sync(kFull, m, rr), La = __shfl_sync(kFull, L1, rr);
     const float Lb = __shfl_sync(kFull, L2, rr);
@@ -389,8 +412,7 @@ head_dz_bf16_kernel(const DzArgs a, uint16_t* __restrict__ kept) {
       *at = make_uint4(0, 0, 0, 0);
       continue;
     }
-    const uint4 u = *at;
-    const uint32_t wds[4] = {u.x, u.y, u.z, u.w};
+    const uint32_t wds[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
     float g[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
@@ -457,7 +479,13 @@ head_dz_entries_kernel(const DzArgs a, const int32_t* __restrict__ ent,
   }
 }
 
-// ---- dx from its parts (bf16 layers) -----------------------------------------------------
+// ---- dx from its parts ---------------------------------------------------------------------
+// A block takes four tokens at a time, their parts' loads in flight together.
+constexpr int kDxTokens = 4;
+__device__ __forceinline__ void store4(float* p, const float4& v) { *reinterpret_cast<float4*>(p) = v; }
+__device__ __forceinline__ void store4(__nv_bfloat16* p, const float4& v) {
+  *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+}
 template <typename O>
 __global__ void __launch_bounds__(256)
 head_dx_kernel(const HeadCounts* cnt, const int32_t* __restrict__ pos, const float* __restrict__ part,
@@ -468,27 +496,35 @@ head_dx_kernel(const HeadCounts* cnt, const int32_t* __restrict__ pos, const flo
   pdl_trigger();
   const HeadScale sc = head_scale(cnt->n, cnt->n_ce, cnt->n_kd, coef, coef_kd, coef_z, tau);
   const float g = sc.unit * (dloss ? *dloss : 1.f);
-  constexpr int VN = 16 / sizeof(O);   // elements of a 16-byte store
-  const int vecs = d / VN;
-  for (int t = blockIdx.x; t < T; t += gridDim.x) {
-    const int r = pos[t];
-    const bool mine = r >= row0 && r < row0 + piece;
-    if (!mine && !(r < 0 && zeros)) continue;
-    for (int i = threadIdx.x; i < vecs; i += blockDim.x) {
-      float v[VN] = {};
-      if (mine)
-        for (int s = 0; s < splits; ++s) {
-          const float4* src = reinterpret_cast<const float4*>(
-              part + s * split_stride + static_cast<size_t>(r - row0) * d + i * VN);
+  for (int t0 = blockIdx.x * kDxTokens; t0 < T; t0 += gridDim.x * kDxTokens) {
+    int r[kDxTokens];
+    bool any = false;
 #pragma unroll
-          for (int j = 0; j < VN / 4; ++j) {
-            const float4 u = src[j];
-            v[4 * j] += u.x; v[4 * j + 1] += u.y; v[4 * j + 2] += u.z; v[4 * j + 3] += u.w;
+    for (int j = 0; j < kDxTokens; ++j) {
+      // this piece's rows (from 0), -1: a row of zeros, -2: not now
+      const int at = t0 + j < T ? pos[t0 + j] : INT32_MAX;
+      r[j] = at < 0 ? (zeros ? -1 : -2) : at >= row0 && at < row0 + piece ? at - row0 : -2;
+      any |= r[j] > -2;
+    }
+    if (!any) continue;
+    for (int i = threadIdx.x * 4; i < d; i += blockDim.x * 4) {
+      float4 v[kDxTokens];
+#pragma unroll
+      for (int j = 0; j < kDxTokens; ++j) v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+      for (int s = 0; s < splits; ++s)
+#pragma unroll
+        for (int j = 0; j < kDxTokens; ++j)
+          if (r[j] >= 0) {
+            const float4 f = __ldcs(reinterpret_cast<const float4*>(
+                part + s * split_stride + static_cast<size_t>(r[j]) * d + i));
+            v[j].x += f.x; v[j].y += f.y; v[j].z += f.z; v[j].w += f.w;
           }
-        }
 #pragma unroll
-      for (int j = 0; j < VN; ++j) v[j] *= g;
-      *reinterpret_cast<uint4*>(dx + static_cast<size_t>(t) * d + i * VN) = pack16(v, O());
+      for (int j = 0; j < kDxTokens; ++j)
+        if (r[j] > -2)
+          store4(dx + static_cast<size_t>(t0 + j) * d + i,
+                 make_float4(g * v[j].x, g * v[j].y, g * v[j].z, g * v[j].w));
     }
   }
 }
@@ -513,6 +549,13 @@ static int dx_splits(int rows, int d, int V) {
     if (t < best_t - 1e-12) { best_t = t; best = s; }
   }
   return best;
+}
+
+// The same for fp32 layers: two tiles for every SM, of no less than 128 products' depth.
+static int dx_splits_f32(int rows, int d, int V) {
+  const int ts = head_f32_tile(rows, d);
+  const int64_t tiles = static_cast<int64_t>((rows + ts - 1) / ts) * ((d + ts - 1) / ts);
+  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({2 * 152 / tiles, V / 128, 64})));
 }
 
 // Width of the logits' tiles: 256 columns, or what leaves the last round of a small batch
@@ -542,15 +585,16 @@ HeadPlan head_plan(const occult_desc_t& ds, const occult_head_t& opt, bool step)
   p.ld = static_cast<int>(up(p.V, 256));
   const int64_t row_bytes = static_cast<int64_t>(p.ld) * (bf ? 2 : 4);
   int64_t piece = opt.piece > 0 ? opt.piece : (int64_t(1) << 30) / row_bytes;
-  piece = std::min<int64_t>(1 << 19, piece);   // (a grid's second dimension)
+  piece = std::min<int64_t>(kDzRows * 32768, piece);   // (a grid's second dimension)
   piece = std::max<int64_t>(kHeadRowAlign, piece / kHeadRowAlign * kHeadRowAlign);
   p.piece = step ? static_cast<int>(std::min<int64_t>(piece, Tr)) : Tr;
   p.n_pieces = (Tr + p.piece - 1) / p.piece;
   // (the gradient of the logits is put together in parts of 128 columns)
-  p.bn = !bf ? 128 : step ? 256 : tile_width(std::min(p.piece, std::max(1, ds.T)), p.V);
+  const int rows = std::min(p.piece, std::max(1, ds.T));
+  p.bn = !bf ? head_f32_tile(rows, p.V) : step ? 256 : tile_width(rows, p.V);
   p.n_tiles = (p.V + p.bn - 1) / p.bn;
-  p.halves = 2 * p.n_tiles;
-  p.splits = bf && step ? dx_splits(std::min(p.piece, std::max(1, ds.T)), p.d, p.V) : 1;
+  p.halves = bf ? 2 * p.n_tiles : p.n_tiles;
+  p.splits = !step ? 1 : bf ? dx_splits(rows, p.d, p.V) : dx_splits_f32(rows, p.d, p.V);
   p.q_step = std::max(24.f, 20.f * p.tau) / 65535.f;
   size_t o = 0;
   auto take = [&](size_t bytes) { const size_t at = o; o += up(bytes, 256); return at; };
@@ -564,7 +608,7 @@ HeadPlan head_plan(const occult_desc_t& ds, const occult_head_t& opt, bool step)
   p.o_l1 = take(4 * T); p.o_l2 = take(4 * T);
   p.o_sum = take(12 * (T / 32 + p.n_pieces));
   p.o_kept = take(step ? P * row_bytes : 0);
-  p.o_part = take(bf && step ? 4 * static_cast<size_t>(p.splits) * P * p.d : 0);
+  p.o_part = take(step ? 4 * static_cast<size_t>(p.splits) * P * p.d : 0);
   p.o_acc = take(step && p.n_pieces > 1 && p.grad_dtype == OCCULT_BF16
                      ? 4 * static_cast<size_t>(p.V) * p.d : 0);
   p.total = o;
@@ -588,15 +632,13 @@ int launch_head(const LaunchCtx& ctx, const HeadPlan& p, const HeadArgs& a) {
   auto* sums = reinterpret_cast<float*>(ws + p.o_sum);
   auto* part = reinterpret_cast<float*>(ws + p.o_part);
   const bool bf = p.dtype == OCCULT_BF16;
-  cudaError_t e = launch_pdl(head_rows_kernel, 1, 1024, 0, ctx.stream, a.labels, a.t_ids, p.T, p.V, p.K,
-                             cnt, idx, pos, flag, ent, ent_q, a.lse, a.token_loss);
+  // at most about 1024 blocks, each of which counts every token
+  const int per = static_cast<int>(up((p.T + 1023) / 1024, 32));
+  cudaError_t e = launch_pdl(head_rows_kernel, (p.T + per - 1) / per, kRowThreads, 0, ctx.stream, a.labels,
+                             a.t_ids, p.T, p.V, p.K, per, cnt, idx, pos, flag, ent, ent_q, a.lse,
+                             a.token_loss, static_cast<const uint4*>(a.x),
+                             bf ? reinterpret_cast<uint4*>(ws + p.o_xc) : nullptr, p.d / 8);
   if (e != cudaSuccess) return OCCULT_ERR_CUDA;
-  if (bf) {
-    e = launch_pdl(head_gather_kernel, std::min(p.T + 63, ctx.num_sms * 8), 256, 0, ctx.stream,
-                   static_cast<const uint4*>(a.x), reinterpret_cast<uint4*>(ws + p.o_xc), cnt, idx,
-                   p.T, p.d / 8);
-    if (e != cudaSuccess) return OCCULT_ERR_CUDA;
-  }
   if (p.K) {
     e = launch_pdl(head_entries_kernel, std::min((p.T + kEntWarps - 1) / kEntWarps, ctx.num_sms * 16),
                    kEntWarps * 32, 0, ctx.stream, a.labels, a.t_ids, a.t_logits, cnt, idx, flag, p.V,
@@ -629,7 +671,7 @@ int launch_head(const LaunchCtx& ctx, const HeadPlan& p, const HeadArgs& a) {
                                                       ctx.num_sms * 16));
     if (bf) {
       auto* kept = reinterpret_cast<uint16_t*>(ws + p.o_kept);
-      const dim3 grid((p.ld / 128 + 7) / 8, (rows + kHeadRowAlign - 1) / kHeadRowAlign * (kHeadRowAlign / 32));
+      const dim3 grid((p.ld / 128 + 7) / 8, (rows + kHeadRowAlign - 1) / kHeadRowAlign * (kHeadRowAlign / kDzRows));
       e = launch_pdl(head_dz_bf16_kernel, grid, 256, 0, ctx.stream, z, kept);
       if (e != cudaSuccess) return OCCULT_ERR_CUDA;
       e = launch_pdl(head_dz_entries_kernel<__nv_bfloat16>, eb, 256, 0, ctx.stream, z, ent, ent_q, zt,
@@ -645,19 +687,17 @@ int launch_head(const LaunchCtx& ctx, const HeadPlan& p, const HeadArgs& a) {
     if (a.dx) {
       rc = bf ? launch_head_dx_bf16(ctx, p, a, row0) : launch_head_dx_f32(ctx, p, a, row0);
       if (rc) return rc;
-      if (bf) {
-        const int nb = std::min(p.T, ctx.num_sms * 8);
-        const size_t stride = static_cast<size_t>(p.piece) * p.d;
-        if (p.grad_dtype == OCCULT_BF16)
-          e = launch_pdl(head_dx_kernel<__nv_bfloat16>, nb, 256, 0, ctx.stream, cnt, pos, part, p.splits,
-                         stride, row0, p.piece, p.T, p.d, i == 0, p.coef, p.coef_kd, p.coef_z, p.tau,
-                         a.dloss, static_cast<__nv_bfloat16*>(a.dx));
-        else
-          e = launch_pdl(head_dx_kernel<float>, nb, 256, 0, ctx.stream, cnt, pos, part, p.splits,
-                         stride, row0, p.piece, p.T, p.d, i == 0, p.coef, p.coef_kd, p.coef_z, p.tau,
-                         a.dloss, static_cast<float*>(a.dx));
-        if (e != cudaSuccess) return OCCULT_ERR_CUDA;
-      }
+      const int nb = std::min((p.T + kDxTokens - 1) / kDxTokens, ctx.num_sms * 8);
+      const size_t stride = static_cast<size_t>(p.piece) * p.d;
+      if (p.grad_dtype == OCCULT_BF16)
+        e = launch_pdl(head_dx_kernel<__nv_bfloat16>, nb, 256, 0, ctx.stream, cnt, pos, part, p.splits,
+                       stride, row0, p.piece, p.T, p.d, i == 0, p.coef, p.coef_kd, p.coef_z, p.tau,
+                       a.dloss, static_cast<__nv_bfloat16*>(a.dx));
+      else
+        e = launch_pdl(head_dx_kernel<float>, nb, 256, 0, ctx.stream, cnt, pos, part, p.splits, stride,
+                       row0, p.piece, p.T, p.d, i == 0, p.coef, p.coef_kd, p.coef_z, p.tau, a.dloss,
+                       static_cast<float*>(a.dx));
+      if (e != cudaSuccess) return OCCULT_ERR_CUDA;
     }
     if (a.dw) {
       const bool first = i == 0, last = i == p.n_pieces - 1;

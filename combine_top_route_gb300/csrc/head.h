@@ -28,7 +28,7 @@ struct HeadPlan {
   int piece, n_pieces;      // tokens of a piece (a multiple of kHeadRowAlign)
   int ld;                   // columns of the kept logits
   int bn;                   // vocabulary columns of a tile
-  int n_tiles, halves;      // tiles, and partial sums a row
+  int n_tiles, halves;      // tiles, and parts of a row's sums (bf16: two a tile)
   int splits;               // parts of the reduction of dx
   float tau, coef, coef_kd, coef_z;
   float q_step;             // octaves of a unit of the kept 16-bit logits
@@ -69,6 +69,12 @@ __host__ __device__ inline HeadScale head_scale(int n, int n_ce, int n_kd, float
   return s;
 }
 
+// Edge of the fp32 products' tiles over rows x columns: 64 where that makes two for every
+// SM, else 32.
+inline int head_f32_tile(int64_t rows, int64_t cols) {
+  return ((rows + 63) / 64) * ((cols + 63) / 64) >= 2 * 152 ? 64 : 32;
+}
+
 HeadPlan head_plan(const occult_desc_t& ds, const occult_head_t& opt, bool step);
 int launch_head(const LaunchCtx& ctx, const HeadPlan& p, const HeadArgs& a);
 
@@ -80,7 +86,7 @@ int launch_head_logits_bf16(const LaunchCtx& ctx, const HeadPlan& p, const HeadA
 int launch_head_dx_bf16(const LaunchCtx& ctx, const HeadPlan& p, const HeadArgs& a, int row0);
 int launch_head_dw_bf16(const LaunchCtx& ctx, const HeadPlan& p, const HeadArgs& a, int row0,
                         bool first, bool last);
-// The same of fp32 layers; dx is written to its tokens' rows.
+// The same of fp32 layers.
 int launch_head_logits_f32(const LaunchCtx& ctx, const HeadPlan& p, const HeadArgs& a, int row0);
 int launch_head_dx_f32(const LaunchCtx& ctx, const HeadPlan& p, const HeadArgs& a, int row0);
 int launch_head_dw_f32(const LaunchCtx& ctx, const HeadPlan& p, const HeadArgs& a, int row0,
