@@ -217,6 +217,139 @@ head_entries_kernel(const int32_t* __restrict__ labels, const int32_t* __restric
   }
 }
 
+// ---- few tokens -----------------------------------------------------------------------
+// Up to four tokens (scoring while decoding): the weights' stream is all that counts, and
+// the fp32 units keep up with it.  A warp takes a run of vocabulary rows, four at a time,
+// a lane 16 bytes of each per step; every row's products are added in fp32 in 32 sums and
+// joined over the lanes, so all lanes know a row's logits and keep the warp's maxima and
+// sums.  A block is a part of the rows' sums.  The entries' logits are products of their
+// own, a warp each, so that no row has to be looked up.
+constexpr int kFewThreads = 256, kFewRows = 4;
+template <int NT>
+__device__ __forceinline__ void few_products(float (&acc)[kFewRows][NT], const __nv_bfloat16* const (&w)[kFewRows],
+                                             const __nv_bfloat16* xs, int d) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int i = 0; i < kFewRows; ++i)
+#pragma unroll
+    for (int t = 0; t < NT; ++t) acc[i][t] = 0.f;
+#pragma unroll 2
+  for (int c = lane * 8; c < d; c += 256) {
+    uint4 u[kFewRows];
+#pragma unroll
+    for (int i = 0; i < kFewRows; ++i) u[i] = ld_nc_v4(w[i] + c);
+    float f[kFewRows][8];
+#pragma unroll
+    for (int i = 0; i < kFewRows; ++i) unpack16(u[i], f[i], __nv_bfloat16());
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      float g[8];
+      unpack16(*reinterpret_cast<const uint4*>(xs + t * d + c), g, __nv_bfloat16());
+#pragma unroll
+      for (int i = 0; i < kFewRows; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[i][t] = fmaf(f[i][j], g[j], acc[i][t]);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kFewRows; ++i)
+#pragma unroll
+    for (int t = 0; t < NT; ++t) acc[i][t] = warp_sum(acc[i][t]);
+}
+
+template <int NT, bool TWO>
+__global__ void __launch_bounds__(kFewThreads)
+head_few_kernel(const HeadCounts* cnt, const __nv_bfloat16* __restrict__ x, const __nv_bfloat16* __restrict__ w,
+                const int32_t* __restrict__ idx, const int32_t* __restrict__ ent, float* __restrict__ zt,
+                int E, int V, int d, float inv_tau, float* __restrict__ pm, float* __restrict__ ps,
+                float* __restrict__ ps2, int ldp) {
+  extern __shared__ __align__(16) uint8_t few_smem[];
+  __nv_bfloat16* xs = reinterpret_cast<__nv_bfloat16*>(few_smem);
+  __shared__ float s_m[kFewThreads / 32][NT], s_s[kFewThreads / 32][NT], s_s2[kFewThreads / 32][NT];
+  pdl_wait();
+  pdl_trigger();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int n = cnt->n;
+  for (int i = tid * 8; i < NT * d; i += kFewThreads * 8) {
+    const int t = i / d;
+    *reinterpret_cast<uint4*>(xs + i) =
+        t < n ? *reinterpret_cast<const uint4*>(x + static_cast<size_t>(idx[t]) * d + (i - t * d)) : make_uint4(0, 0, 0, 0);
+  }
+  __syncthreads();
+  const float NEG = -__int_as_float(0x7f800000);
+  const int gw = blockIdx.x * (kFewThreads / 32) + warp, n_warps = gridDim.x * (kFewThreads / 32);
+  const __nv_bfloat16* rows[kFewRows];
+  float acc[kFewRows][NT];
+  for (int i = gw; i < n * E; i += n_warps) {
+    const int id = ent[i], t = i / E;
+    if (id == kHeadNoEntry) continue;
+#pragma unroll
+    for (int j = 0; j < kFewRows; ++j) rows[j] = w + static_cast<size_t>(id) * d;
+    few_products<NT>(acc, rows, xs, d);
+    float z = acc[0][0];
+#pragma unroll
+    for (int u = 1; u < NT; ++u) z = t == u ? acc[0][u] : z;
+    if (lane == 0) zt[i] = z;
+  }
+  float m[NT], s[NT], s2[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) { m[t] = NEG; s[t] = 0.f; s2[t] = 0.f; }
+  const int v1 = static_cast<int>(static_cast<int64_t>(V) * (gw + 1) / n_warps);
+  for (int v = static_cast<int>(static_cast<int64_t>(V) * gw / n_warps); v < v1; v += kFewRows) {
+    // (a row past the run is read again in the last one's place and left out)
+#pragma unroll
+    for (int j = 0; j < kFewRows; ++j) rows[j] = w + static_cast<size_t>(min(v + j, v1 - 1)) * d;
+    few_products<NT>(acc, rows, xs, d);
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      float y[kFewRows], hi = m[t];
+#pragma unroll
+      for (int j = 0; j < kFewRows; ++j) {
+        y[j] = v + j < v1 ? acc[j][t] * kLog2e : NEG;
+        hi = fmaxf(hi, y[j]);
+      }
+      const float to = hi == NEG ? 0.f : hi;
+      s[t] *= ex2(m[t] - to);
+      if (TWO) s2[t] *= ex2((m[t] - to) * inv_tau);
+#pragma unroll
+      for (int j = 0; j < kFewRows; ++j) {
+        s[t] += ex2(y[j] - to);
+        if (TWO) s2[t] += ex2((y[j] - to) * inv_tau);
+      }
+      m[t] = hi;
+    }
+  }
+  if (lane == 0)
+#pragma unroll
+    for (int t = 0; t < NT; ++t) { s_m[warp][t] = m[t]; s_s[warp][t] = s[t]; s_s2[warp][t] = s2[t]; }
+  __syncthreads();
+  if (tid < NT && tid < n) {
+    float hi = NEG, a = 0.f, b = 0.f;
+    for (int i = 0; i < kFewThreads / 32; ++i) hi = fmaxf(hi, s_m[i][tid]);
+    const float to = hi == NEG ? 0.f : hi;
+    for (int i = 0; i < kFewThreads / 32; ++i) {
+      a += s_s[i][tid] * ex2(s_m[i][tid] - to);
+      if (TWO) b += s_s2[i][tid] * ex2((s_m[i][tid] - to) * inv_tau);
+    }
+    const size_t at = static_cast<size_t>(blockIdx.x) * ldp + tid;
+    pm[at] = hi;
+    ps[at] = a;
+    if (TWO) ps2[at] = b;
+  }
+}
+
+template <int NT>
+cudaError_t launch_few(const LaunchCtx& ctx, const HeadPlan& p, const HeadArgs& a) {
+  char* ws = a.ws;
+  return launch_pdl(p.two ? head_few_kernel<NT, true> : head_few_kernel<NT, false>, p.halves, kFewThreads,
+                    static_cast<size_t>(NT) * p.d * 2, ctx.stream,
+                    reinterpret_cast<const HeadCounts*>(ws + p.o_cnt), static_cast<const __nv_bfloat16*>(a.x),
+                    static_cast<const __nv_bfloat16*>(a.w), reinterpret_cast<const int32_t*>(ws + p.o_idx),
+                    reinterpret_cast<const int32_t*>(ws + p.o_ent), reinterpret_cast<float*>(ws + p.o_zt), p.E,
+                    p.V, p.d, 1.f / p.tau, reinterpret_cast<float*>(ws + p.o_m),
+                    reinterpret_cast<float*>(ws + p.o_s), reinterpret_cast<float*>(ws + p.o_s2), p.piece);
+}
+
 // ---- a row's sums, losses and the means ---------------------------------------------
 // A block takes 32 rows: warp w joins the parts w, w + 32, ... of all of them (a lane a
 // row, so that reads run along the rows), then finishes row w.  The last block to arrive
@@ -594,6 +727,10 @@ HeadPlan head_plan(const occult_desc_t& ds, const occult_head_t& opt, bool step)
   p.bn = !bf ? head_f32_tile(rows, p.V) : step ? 256 : tile_width(rows, p.V);
   p.n_tiles = (p.V + p.bn - 1) / p.bn;
   p.halves = bf ? 2 * p.n_tiles : p.n_tiles;
+  // Up to four tokens' losses: the weights' stream through the fp32 units (four blocks an
+  // SM, fewer of 128 rows each), whose x fits the 48 KB that a block has unasked.
+  p.few = bf && !step && ds.T <= 4 && static_cast<int64_t>(ds.T) * p.d * 2 <= 48 * 1024 - 1024;
+  if (p.few) p.halves = std::max(1, std::min(152 * 4, (p.V + 127) / 128));
   p.splits = !step ? 1 : bf ? dx_splits(rows, p.d, p.V) : dx_splits_f32(rows, p.d, p.V);
   p.q_step = std::max(24.f, 20.f * p.tau) / 65535.f;
   size_t o = 0;
@@ -651,8 +788,15 @@ int launch_head(const LaunchCtx& ctx, const HeadPlan& p, const HeadArgs& a) {
   int block0 = 0;
   for (int i = 0; i < p.n_pieces; ++i) {
     const int row0 = i * p.piece, rows = std::min(p.piece, p.T - row0);
-    int rc = bf ? launch_head_logits_bf16(ctx, p, a, row0) : launch_head_logits_f32(ctx, p, a, row0);
-    if (rc) return rc;
+    int rc = OCCULT_OK;
+    if (p.few) {
+      e = p.T == 1 ? launch_few<1>(ctx, p, a) : p.T == 2 ? launch_few<2>(ctx, p, a)
+        : p.T == 3 ? launch_few<3>(ctx, p, a) : launch_few<4>(ctx, p, a);
+      if (e != cudaSuccess) return OCCULT_ERR_CUDA;
+    } else {
+      rc = bf ? launch_head_logits_bf16(ctx, p, a, row0) : launch_head_logits_f32(ctx, p, a, row0);
+      if (rc) return rc;
+    }
     const int blocks = (rows + 31) / 32;
     e = launch_pdl(p.two ? head_sum_kernel<true> : head_sum_kernel<false>, blocks, kSumWarps * 32, 0,
                    ctx.stream, cnt, pm, ps, ps2, p.piece, p.halves, row0, rows, p.E, idx, flag, ent,

@@ -25,6 +25,7 @@ struct HeadPlan {
   int T, d, V, K, E;        // E = K + 1 entries a row: the teacher's and the label
   int dtype, grad_dtype;
   bool step, two;           // two: sums at temperature 1 and tau
+  bool few;                 // the loss of up to four tokens on the fp32 units
   int piece, n_pieces;      // tokens of a piece (a multiple of kHeadRowAlign)
   int ld;                   // columns of the kept logits
   int bn;                   // vocabulary columns of a tile

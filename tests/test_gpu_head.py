@@ -365,3 +365,22 @@ def test_offsets_past_32_bits(occ):
     want = sum(dz[:, a:a + 100_000] @ w[a:a + 100_000].double() for a in range(0, V, 100_000))
     size = sum(dz[:, a:a + 100_000].abs() @ w[a:a + 100_000].double().abs() for a in range(0, V, 100_000))
     assert ((dx.double() - want).abs() <= 2.0 ** -6 * size).all()
+
+
+@pytest.mark.parametrize("T", [1, 2, 3, 4, 5])
+@pytest.mark.parametrize("d,V", [(64, 1), (64, 3), (2048, 5003), (320, 700), (16384, 130)])
+@pytest.mark.parametrize("K,tau", [(0, 1.0), (9, 2.0), (128, 1.0)])
+def test_scoring_few_tokens(occ, T, d, V, K, tau):
+    c = case(T, d, V, K=K, seed=T)
+    check(occ, c, step=False, tau=tau, coef=0.6, coef_kd=0.4, coef_z=1e-3)
+    x, w, labels, ids, tl = c
+    if T > 1:       # one of them ignored, its row anything
+        labels[1] = -1
+        x[1] = np.nan
+        if K:
+            ids[1, 0] = V
+        check(occ, c, step=False, tau=tau, coef=0.6, coef_kd=0.4)
+    labels[:] = -1
+    if K:
+        ids[:, 0] = -1
+    check(occ, c, step=False, tau=tau, coef=0.6, coef_kd=0.4)
