@@ -20,26 +20,6 @@ namespace occult {
 
 namespace {
 
-constexpr uint32_t kFull = 0xffffffffu;
-
-__device__ __forceinline__ float ex2(float v) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
-  return r;
-}
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
-  return v;
-}
-__device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, o));
-  return v;
-}
-
-enum : uint8_t { kRowCe = 1, kRowKd = 2 };
-
 // ---- rows -----------------------------------------------------------------------
 // Which tokens a term counts, and their compact rows in token order.  A block has `per`
 // tokens of its own and counts all of them (a few KB from L2, which is cheaper than
@@ -217,154 +197,18 @@ head_entries_kernel(const int32_t* __restrict__ labels, const int32_t* __restric
   }
 }
 
-// ---- few tokens -----------------------------------------------------------------------
-// Up to four tokens (scoring while decoding): the weights' stream is all that counts, and
-// the fp32 units keep up with it.  A warp takes a run of vocabulary rows, four at a time,
-// a lane 16 bytes of each per step; every row's products are added in fp32 in 32 sums and
-// joined over the lanes, so all lanes know a row's logits and keep the warp's maxima and
-// sums.  A block is a part of the rows' sums.  The entries' logits are products of their
-// own, a warp each, so that no row has to be looked up.
-constexpr int kFewThreads = 256, kFewRows = 4;
-template <int NT>
-__device__ __forceinline__ void few_products(float (&acc)[kFewRows][NT], const __nv_bfloat16* const (&w)[kFewRows],
-                                             const __nv_bfloat16* xs, int d) {
-  const int lane = threadIdx.x & 31;
-#pragma unroll
-  for (int i = 0; i < kFewRows; ++i)
-#pragma unroll
-    for (int t = 0; t < NT; ++t) acc[i][t] = 0.f;
-#pragma unroll 2
-  for (int c = lane * 8; c < d; c += 256) {
-    uint4 u[kFewRows];
-#pragma unroll
-    for (int i = 0; i < kFewRows; ++i) u[i] = ld_nc_v4(w[i] + c);
-    float f[kFewRows][8];
-#pragma unroll
-    for (int i = 0; i < kFewRows; ++i) unpack16(u[i], f[i], __nv_bfloat16());
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      float g[8];
-      unpack16(*reinterpret_cast<const uint4*>(xs + t * d + c), g, __nv_bfloat16());
-#pragma unroll
-      for (int i = 0; i < kFewRows; ++i)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) acc[i][t] = fmaf(f[i][j], g[j], acc[i][t]);
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < kFewRows; ++i)
-#pragma unroll
-    for (int t = 0; t < NT; ++t) acc[i][t] = warp_sum(acc[i][t]);
-}
-
-template <int NT, bool TWO>
-__global__ void __launch_bounds__(kFewThreads)
-head_few_kernel(const HeadCounts* cnt, const __nv_bfloat16* __restrict__ x, const __nv_bfloat16* __restrict__ w,
-                const int32_t* __restrict__ idx, const int32_t* __restrict__ ent, float* __restrict__ zt,
-                int E, int V, int d, float inv_tau, float* __restrict__ pm, float* __restrict__ ps,
-                float* __restrict__ ps2, int ldp) {
-  extern __shared__ __align__(16) uint8_t few_smem[];
-  __nv_bfloat16* xs = reinterpret_cast<__nv_bfloat16*>(few_smem);
-  __shared__ float s_m[kFewThreads / 32][NT], s_s[kFewThreads / 32][NT], s_s2[kFewThreads / 32][NT];
-  pdl_wait();
-  pdl_trigger();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int n = cnt->n;
-  for (int i = tid * 8; i < NT * d; i += kFewThreads * 8) {
-    const int t = i / d;
-    *reinterpret_cast<uint4*>(xs + i) =
-        t < n ? *reinterpret_cast<const uint4*>(x + static_cast<size_t>(idx[t]) * d + (i - t * d)) : make_uint4(0, 0, 0, 0);
-  }
-  __syncthreads();
-  const float NEG = -__int_as_float(0x7f800000);
-  const int gw = blockIdx.x * (kFewThreads / 32) + warp, n_warps = gridDim.x * (kFewThreads / 32);
-  const __nv_bfloat16* rows[kFewRows];
-  float acc[kFewRows][NT];
-  for (int i = gw; i < n * E; i += n_warps) {
-    const int id = ent[i], t = i / E;
-    if (id == kHeadNoEntry) continue;
-#pragma unroll
-    for (int j = 0; j < kFewRows; ++j) rows[j] = w + static_cast<size_t>(id) * d;
-    few_products<NT>(acc, rows, xs, d);
-    float z = acc[0][0];
-#pragma unroll
-    for (int u = 1; u < NT; ++u) z = t == u ? acc[0][u] : z;
-    if (lane == 0) zt[i] = z;
-  }
-  float m[NT], s[NT], s2[NT];
-#pragma unroll
-  for (int t = 0; t < NT; ++t) { m[t] = NEG; s[t] = 0.f; s2[t] = 0.f; }
-  const int v1 = static_cast<int>(static_cast<int64_t>(V) * (gw + 1) / n_warps);
-  for (int v = static_cast<int>(static_cast<int64_t>(V) * gw / n_warps); v < v1; v += kFewRows) {
-    // (a row past the run is read again in the last one's place and left out)
-#pragma unroll
-    for (int j = 0; j < kFewRows; ++j) rows[j] = w + static_cast<size_t>(min(v + j, v1 - 1)) * d;
-    few_products<NT>(acc, rows, xs, d);
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      float y[kFewRows], hi = m[t];
-#pragma unroll
-      for (int j = 0; j < kFewRows; ++j) {
-        y[j] = v + j < v1 ? acc[j][t] * kLog2e : NEG;
-        hi = fmaxf(hi, y[j]);
-      }
-      const float to = hi == NEG ? 0.f : hi;
-      s[t] *= ex2(m[t] - to);
-      if (TWO) s2[t] *= ex2((m[t] - to) * inv_tau);
-#pragma unroll
-      for (int j = 0; j < kFewRows; ++j) {
-        s[t] += ex2(y[j] - to);
-        if (TWO) s2[t] += ex2((y[j] - to) * inv_tau);
-      }
-      m[t] = hi;
-    }
-  }
-  if (lane == 0)
-#pragma unroll
-    for (int t = 0; t < NT; ++t) { s_m[warp][t] = m[t]; s_s[warp][t] = s[t]; s_s2[warp][t] = s2[t]; }
-  __syncthreads();
-  if (tid < NT && tid < n) {
-    float hi = NEG, a = 0.f, b = 0.f;
-    for (int i = 0; i < kFewThreads / 32; ++i) hi = fmaxf(hi, s_m[i][tid]);
-    const float to = hi == NEG ? 0.f : hi;
-    for (int i = 0; i < kFewThreads / 32; ++i) {
-      a += s_s[i][tid] * ex2(s_m[i][tid] - to);
-      if (TWO) b += s_s2[i][tid] * ex2((s_m[i][tid] - to) * inv_tau);
-    }
-    const size_t at = static_cast<size_t>(blockIdx.x) * ldp + tid;
-    pm[at] = hi;
-    ps[at] = a;
-    if (TWO) ps2[at] = b;
-  }
-}
-
-template <int NT>
-cudaError_t launch_few(const LaunchCtx& ctx, const HeadPlan& p, const HeadArgs& a) {
-  char* ws = a.ws;
-  return launch_pdl(p.two ? head_few_kernel<NT, true> : head_few_kernel<NT, false>, p.halves, kFewThreads,
-                    static_cast<size_t>(NT) * p.d * 2, ctx.stream,
-                    reinterpret_cast<const HeadCounts*>(ws + p.o_cnt), static_cast<const __nv_bfloat16*>(a.x),
-                    static_cast<const __nv_bfloat16*>(a.w), reinterpret_cast<const int32_t*>(ws + p.o_idx),
-                    reinterpret_cast<const int32_t*>(ws + p.o_ent), reinterpret_cast<float*>(ws + p.o_zt), p.E,
-                    p.V, p.d, 1.f / p.tau, reinterpret_cast<float*>(ws + p.o_m),
-                    reinterpret_cast<float*>(ws + p.o_s), reinterpret_cast<float*>(ws + p.o_s2), p.piece);
-}
-
 // ---- a row's sums, losses and the means ---------------------------------------------
-// A block takes 32 rows: warp w joins the parts w, w + 32, ... of all of them (a lane a
-// row, so that reads run along the rows), then finishes row w.  The last block to arrive
-// adds the blocks' sums in their order.
-constexpr int kSumWarps = 32;
-template <bool TWO>
+// A block takes 32 rows: its warps join every so many parts of all of them (a lane a row,
+// so that reads run along the rows), then finish the rows one by one.  The last block to
+// arrive adds the blocks' sums in their order.  32 warps a block where there are few of
+// them, 16 where two to an SM save a second round of blocks.
+template <bool TWO, int kSumWarps>
 __global__ void __launch_bounds__(kSumWarps * 32)
-head_sum_kernel(HeadCounts* cnt, const float* __restrict__ pm, const float* __restrict__ ps,
-                const float* __restrict__ ps2, int ldp, int halves, int row0, int rows_max, int E,
-                const int32_t* __restrict__ idx, const uint8_t* __restrict__ flag,
-                const int32_t* __restrict__ ent, const float* __restrict__ ent_q,
-                const float* __restrict__ zt, float tau, float coef, float coef_kd,
-                float coef_z, float* __restrict__ l1, float* __restrict__ l2,
-                float* __restrict__ lse_out, float* __restrict__ token_out, float* __restrict__ sums,
-                int block0, int n_blocks, float* __restrict__ loss) {
+head_sum_kernel(HeadCounts* cnt, const HeadLossOut o, const float* __restrict__ pm,
+                const float* __restrict__ ps, const float* __restrict__ ps2, int ldp, int halves, int row0,
+                int rows_max, const int32_t* __restrict__ idx, const uint8_t* __restrict__ flag,
+                float* __restrict__ l1, float* __restrict__ l2, float* __restrict__ sums, int block0,
+                int n_blocks) {
   __shared__ float s_m[kSumWarps][33], s_s[kSumWarps][33], s_s2[kSumWarps][33];
   __shared__ float s_ce[32], s_kd[32], s_z[32];
   __shared__ bool s_last;
@@ -374,7 +218,7 @@ head_sum_kernel(HeadCounts* cnt, const float* __restrict__ pm, const float* __re
   const int n = min(cnt->n - row0, rows_max);
   const int r_first = blockIdx.x * 32;
   const float NEG = -__int_as_float(0x7f800000);
-  const float inv_tau = 1.f / tau;
+  const float inv_tau = 1.f / o.tau;
   if (r_first < n) {
     // parts of row r_first + lane
     const int r = min(r_first + lane, n - 1);
@@ -408,43 +252,26 @@ head_sum_kernel(HeadCounts* cnt, const float* __restrict__ pm, const float* __re
     if (TWO) s_s2[warp][lane] = s2;
   }
   __syncthreads();
-  // warp w: row r_first + w
-  const int r = r_first + warp;
-  float ce = 0.f, kd = 0.f, zz = 0.f;
-  if (r < n) {
-    const float m = s_m[lane][warp];
+  RowSums mine{0.f, 0.f, 0.f};
+  for (int own = warp; own < 32 && r_first + own < n; own += kSumWarps) {
+    const size_t r = static_cast<size_t>(row0) + r_first + own;
+    const float m = lane < kSumWarps ? s_m[lane][own] : NEG;
     const float top = warp_max(m);
     const float safe = top == NEG ? 0.f : top;
-    const float L = safe + log2f(warp_sum(s_s[lane][warp] * ex2(m - safe)));
+    const float L = safe + log2f(warp_sum(lane < kSumWarps ? s_s[lane][own] * ex2(m - safe) : 0.f));
     float L2 = L;
-    if (TWO) L2 = safe * inv_tau + log2f(warp_sum(s_s2[lane][warp] * ex2((m - safe) * inv_tau)));
-    const size_t rg = static_cast<size_t>(row0) + r;
-    const int f = flag[rg];
-    const float lse = L * kLn2;
-    float tok = 0.f;
-    for (int e = lane; e < E; e += 32) {
-      const int id = ent[rg * E + e];
-      if (id == kHeadNoEntry) continue;
-      const float q = ent_q[rg * E + e], z = zt[rg * E + e];
-      if (q < 0.f) tok = lse - z;
-      else if (q != 0.f) kd += q * (logf(q) - (z * inv_tau - L2 * kLn2));
-    }
-    tok = warp_sum(tok);
-    kd = warp_sum(kd);
-    ce = (f & kRowCe) ? tok : 0.f;
-    zz = lse * lse;
-    if (lane == 0) {
-      l1[rg] = L;
-      l2[rg] = L2;
-      const int t = idx[rg];
-      if (lse_out) lse_out[t] = lse;
-      if (token_out) token_out[t] = ce;
-    }
+    if (TWO)
+      L2 = safe * inv_tau +
+           log2f(warp_sum(lane < kSumWarps ? s_s2[lane][own] * ex2((m - safe) * inv_tau) : 0.f));
+    if (lane == 0) { l1[r] = L; l2[r] = L2; }
+    row_losses(o, r, flag[r], idx[r], L, L2, inv_tau, mine);
   }
-  if (lane == 0) { s_ce[warp] = ce; s_kd[warp] = kd; s_z[warp] = zz; }
+  if (lane == 0) { s_ce[warp] = mine.ce; s_kd[warp] = mine.kd; s_z[warp] = mine.z; }
   __syncthreads();
+  const bool have = lane < kSumWarps;
   if (warp == 0) {
-    const float a = warp_sum(s_ce[lane]), b = warp_sum(s_kd[lane]), c = warp_sum(s_z[lane]);
+    const float a = warp_sum(have ? s_ce[lane] : 0.f), b = warp_sum(have ? s_kd[lane] : 0.f),
+                c = warp_sum(have ? s_z[lane] : 0.f);
     if (lane == 0) {
       float* out = sums + 3 * static_cast<size_t>(block0 + blockIdx.x);
       out[0] = a;
@@ -468,16 +295,10 @@ head_sum_kernel(HeadCounts* cnt, const float* __restrict__ pm, const float* __re
   if (lane == 0) { s_ce[warp] = a; s_kd[warp] = b; s_z[warp] = c; }
   __syncthreads();
   if (warp == 0) {
-    a = warp_sum(s_ce[lane]); b = warp_sum(s_kd[lane]); c = warp_sum(s_z[lane]);
-    if (lane == 0) {
-      a = cnt->n_ce > 0 ? a / static_cast<float>(cnt->n_ce) : 0.f;
-      b = cnt->n_kd > 0 ? tau * tau * b / static_cast<float>(cnt->n_kd) : 0.f;
-      c = cnt->n > 0 ? c / static_cast<float>(cnt->n) : 0.f;
-      loss[0] = coef * a + coef_kd * b + coef_z * c;
-      loss[1] = a;
-      loss[2] = b;
-      loss[3] = c;
-    }
+    a = warp_sum(have ? s_ce[lane] : 0.f);
+    b = warp_sum(have ? s_kd[lane] : 0.f);
+    c = warp_sum(have ? s_z[lane] : 0.f);
+    if (lane == 0) mean_losses(o, *cnt, a, b, c);
   }
 }
 
@@ -521,7 +342,7 @@ head_dz_bf16_kernel(const DzArgs a, uint16_t* __restrict__ kept) {
   float m = 0.f, L1 = 0.f, L2 = 0.f, k1 = 0.f, k2 = 0.f;
   if (r < n) {
     m = a.pm[static_cast<size_t>(h) * a.ldp + r];
-    if (m == -__int_as_float(0x7f800000)) m = 0.f;
+    m = (m == -__int_as_float(0x7f800000) ? 0.f : m) + 65536.f * a.q_step;
     L1 = a.l1[a.row0 + r];
     L2 = a.l2[a.row0 + r];
     row_factors(a, sc, a.flag[a.row0 + r], L1, k1, k2);
@@ -549,7 +370,9 @@ head_dz_bf16_kernel(const DzArgs a, uint16_t* __restrict__ kept) {
     float g[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const float q = static_cast<float>(j & 1 ? wds[j >> 1] >> 16 : wds[j >> 1] & 0xffffu);
+      // 65536 + q by its bits: the conversion unit is the exponentials' as well
+      const float q = __uint_as_float(0x47800000u | (j & 1 ? (wds[j >> 1] >> 9) & 0x7fff80u
+                                                           : (wds[j >> 1] & 0xffffu) << 7));
       const float y = fmaf(q, -a.q_step, mm);
       g[j] = ka * ex2(y - La);
       if (a.two) g[j] = fmaf(kb, ex2(fmaf(y, a.inv_tau, -Lb)), g[j]);
@@ -667,18 +490,21 @@ size_t up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 }  // namespace
 
 // Parts of dx's reduction over the vocabulary: as many as leave the fewest rounds of
-// tiles idle, where a part more costs its share of the fp32 sums written and read
-// (about 1/64 of a product of that depth).
+// tiles idle.  In rounds of tiles of the whole depth (278 us at 50304 columns), a part
+// costs its share of the rounds and its fp32 sums' way out and back: 8 bytes a value
+// against V products of 256 x 256 by a pair, 2.1e-4 rows d / V.  (8192 x 2048 x 50304: two
+// parts, 911 + 29 us; five, the fewest rounds, 873 + 62 us.)
 static int dx_splits(int rows, int d, int V) {
   const bool pair = rows > 128;
   const int64_t units = static_cast<int64_t>((rows + (pair ? 255 : 127)) / (pair ? 256 : 128)) *
                         ((d + 255) / 256);
   const int64_t slots = pair ? 76 : 152;   // CTA pairs or CTAs of a GB300
+  const double sums = 2.1e-4 * rows * d / V;
   const int most = std::max(1, std::min(64, (V + 1023) / 1024));
   int best = 1;
   double best_t = 1e300;
   for (int s = 1; s <= most; ++s) {
-    const double t = static_cast<double>((units * s + slots - 1) / slots) / s + s / 64.0;
+    const double t = static_cast<double>((units * s + slots - 1) / slots) / s + s * sums;
     if (t < best_t - 1e-12) { best_t = t; best = s; }
   }
   return best;
@@ -727,10 +553,9 @@ HeadPlan head_plan(const occult_desc_t& ds, const occult_head_t& opt, bool step)
   p.bn = !bf ? head_f32_tile(rows, p.V) : step ? 256 : tile_width(rows, p.V);
   p.n_tiles = (p.V + p.bn - 1) / p.bn;
   p.halves = bf ? 2 * p.n_tiles : p.n_tiles;
-  // Up to four tokens' losses: the weights' stream through the fp32 units (four blocks an
-  // SM, fewer of 128 rows each), whose x fits the 48 KB that a block has unasked.
-  p.few = bf && !step && ds.T <= 4 && static_cast<int64_t>(ds.T) * p.d * 2 <= 48 * 1024 - 1024;
-  if (p.few) p.halves = std::max(1, std::min(152 * 4, (p.V + 127) / 128));
+  // Up to four tokens' losses: the weights' stream through the fp32 units.
+  p.few = bf && !step && ds.T <= kHeadFewTokens;
+  if (p.few) p.halves = head_few_blocks(p.V, p.d);
   p.splits = !step ? 1 : bf ? dx_splits(rows, p.d, p.V) : dx_splits_f32(rows, p.d, p.V);
   p.q_step = std::max(24.f, 20.f * p.tau) / 65535.f;
   size_t o = 0;
@@ -788,20 +613,15 @@ int launch_head(const LaunchCtx& ctx, const HeadPlan& p, const HeadArgs& a) {
   int block0 = 0;
   for (int i = 0; i < p.n_pieces; ++i) {
     const int row0 = i * p.piece, rows = std::min(p.piece, p.T - row0);
-    int rc = OCCULT_OK;
-    if (p.few) {
-      e = p.T == 1 ? launch_few<1>(ctx, p, a) : p.T == 2 ? launch_few<2>(ctx, p, a)
-        : p.T == 3 ? launch_few<3>(ctx, p, a) : launch_few<4>(ctx, p, a);
-      if (e != cudaSuccess) return OCCULT_ERR_CUDA;
-    } else {
-      rc = bf ? launch_head_logits_bf16(ctx, p, a, row0) : launch_head_logits_f32(ctx, p, a, row0);
-      if (rc) return rc;
-    }
+    if (p.few) return launch_head_few(ctx, p, a);
+    int rc = bf ? launch_head_logits_bf16(ctx, p, a, row0) : launch_head_logits_f32(ctx, p, a, row0);
+    if (rc) return rc;
     const int blocks = (rows + 31) / 32;
-    e = launch_pdl(p.two ? head_sum_kernel<true> : head_sum_kernel<false>, blocks, kSumWarps * 32, 0,
-                   ctx.stream, cnt, pm, ps, ps2, p.piece, p.halves, row0, rows, p.E, idx, flag, ent,
-                   ent_q, zt, p.tau, p.coef, p.coef_kd, p.coef_z, l1, l2, a.lse, a.token_loss,
-                   sums, block0, n_blocks, a.loss);
+    const int warps = blocks > ctx.num_sms ? 16 : 32;
+    auto* sum = warps == 32 ? (p.two ? head_sum_kernel<true, 32> : head_sum_kernel<false, 32>)
+                            : (p.two ? head_sum_kernel<true, 16> : head_sum_kernel<false, 16>);
+    e = launch_pdl(sum, blocks, warps * 32, 0, ctx.stream, cnt, head_loss_out(p, a), pm, ps, ps2, p.piece,
+                   p.halves, row0, rows, idx, flag, l1, l2, sums, block0, n_blocks);
     if (e != cudaSuccess) return OCCULT_ERR_CUDA;
     block0 += blocks;
     if (!p.step) continue;

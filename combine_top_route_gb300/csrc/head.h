@@ -20,6 +20,9 @@ struct HeadCounts {
   unsigned ticket;
 };
 
+// What a row is to the loss.
+enum : uint8_t { kRowCe = 1, kRowKd = 2 };   // it has a label, a teacher
+
 // Sizes and workspace offsets of a call; every launcher works from one of these.
 struct HeadPlan {
   int T, d, V, K, E;        // E = K + 1 entries a row: the teacher's and the label
@@ -49,6 +52,77 @@ struct HeadArgs {
   void *dx, *dw;
   char* ws;
 };
+
+// The losses' outputs, and what they are made from.
+struct HeadLossOut {
+  const int32_t* ent;    // entries of the compact rows: token, probability (-1: the label),
+  const float* ent_q;    // the student's logit
+  const float* zt;
+  float *lse, *token_loss, *loss;
+  int E;
+  float tau, coef, coef_kd, coef_z;
+};
+inline HeadLossOut head_loss_out(const HeadPlan& p, const HeadArgs& a) {
+  return {reinterpret_cast<const int32_t*>(a.ws + p.o_ent), reinterpret_cast<const float*>(a.ws + p.o_q),
+          reinterpret_cast<const float*>(a.ws + p.o_zt), a.lse, a.token_loss, a.loss, p.E, p.tau, p.coef,
+          p.coef_kd, p.coef_z};
+}
+
+#ifdef __CUDACC__
+constexpr uint32_t kFull = 0xffffffffu;
+__device__ __forceinline__ float ex2(float v) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+  return v;
+}
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, o));
+  return v;
+}
+
+// A warp finishes compact row r from the log2 of its sums (L at temperature 1, L2 at tau):
+// writes the token's outputs and adds its terms to `sum`.
+struct RowSums { float ce, kd, z; };
+__device__ __forceinline__ void row_losses(const HeadLossOut& o, size_t r, int flag, int token, float L,
+                                           float L2, float inv_tau, RowSums& sum) {
+  const int lane = threadIdx.x & 31;
+  const float lse = L * kLn2;
+  float tok = 0.f, kd = 0.f;
+  for (int e = lane; e < o.E; e += 32) {
+    const int id = __ldcg(o.ent + r * o.E + e);
+    const float q = __ldcg(o.ent_q + r * o.E + e), z = __ldcg(o.zt + r * o.E + e);
+    if (id == kHeadNoEntry) continue;
+    if (q < 0.f) tok = lse - z;
+    else if (q != 0.f) kd += q * (logf(q) - (z * inv_tau - L2 * kLn2));
+  }
+  tok = warp_sum(tok);
+  const float ce = (flag & kRowCe) ? tok : 0.f;
+  sum.ce += ce;
+  sum.kd += warp_sum(kd);
+  sum.z += lse * lse;
+  if (lane == 0) {
+    if (o.lse) o.lse[token] = lse;
+    if (o.token_loss) o.token_loss[token] = ce;
+  }
+}
+// The means, from the sums over all rows.
+__device__ __forceinline__ void mean_losses(const HeadLossOut& o, const HeadCounts& cnt, float ce, float kd,
+                                            float z) {
+  ce = cnt.n_ce > 0 ? ce / static_cast<float>(cnt.n_ce) : 0.f;
+  kd = cnt.n_kd > 0 ? o.tau * o.tau * kd / static_cast<float>(cnt.n_kd) : 0.f;
+  z = cnt.n > 0 ? z / static_cast<float>(cnt.n) : 0.f;
+  o.loss[0] = o.coef * ce + o.coef_kd * kd + o.coef_z * z;
+  o.loss[1] = ce;
+  o.loss[2] = kd;
+  o.loss[3] = z;
+}
+#endif
 
 // Factors of a term's gradient over the mean of its tokens, and the common factor that
 // is kept out of the rounded gradients of the logits: the cross entropy's where it
@@ -92,6 +166,12 @@ int launch_head_logits_f32(const LaunchCtx& ctx, const HeadPlan& p, const HeadAr
 int launch_head_dx_f32(const LaunchCtx& ctx, const HeadPlan& p, const HeadArgs& a, int row0);
 int launch_head_dw_f32(const LaunchCtx& ctx, const HeadPlan& p, const HeadArgs& a, int row0,
                        bool first, bool last);
+
+// The loss of up to kHeadFewTokens tokens of a bf16 layer, from its rows and entries to its
+// outputs (head_few.cu); blocks that share the vocabulary.
+constexpr int kHeadFewTokens = 4;
+int head_few_blocks(int V, int d);
+int launch_head_few(const LaunchCtx& ctx, const HeadPlan& p, const HeadArgs& a);
 
 // 2-D bf16 tensor map of a row-major [rows, cols] matrix, 128-byte swizzle.
 int tensor_map_bf16(CUtensorMap* m, const void* base, int64_t rows, int64_t cols,

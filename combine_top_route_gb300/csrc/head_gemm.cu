@@ -81,12 +81,6 @@ struct GemmArgs {
   int* dev_err;
 };
 
-__device__ __forceinline__ float ex2(float v) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
-  return r;
-}
-
 // One tile of the schedule.
 struct Unit {
   int m0;      // first row of this CTA's 128 (rows of the piece; dw: of the vocabulary)
