@@ -24,9 +24,9 @@ namespace {
 // Which tokens a term counts, and their compact rows in token order.  A block has `per`
 // tokens of its own and counts all of them (a few KB from L2, which is cheaper than
 // another launch): those before its own give its first row, all of them the totals.
-// Where some token is left out, bf16 layers' rows of x are copied to their compact place
-// on the way (else the products read x itself), with zeros up to the next multiple of 64,
-// so that dw's reduction may run over them.
+// Where some token is left out, the rows of x are copied to their compact place on the way
+// (else the products read x itself), with zeros up to the next multiple of 64, so that
+// dw's reduction may run over them.
 constexpr int kRowThreads = 256;
 __global__ void __launch_bounds__(kRowThreads)
 head_rows_kernel(const int32_t* __restrict__ labels, const int32_t* __restrict__ t_ids, int T,
@@ -72,7 +72,7 @@ head_rows_kernel(const int32_t* __restrict__ labels, const int32_t* __restrict__
     cnt->n_kd = sum[3];
     cnt->ticket = 0;
   }
-  const bool copy = xc && n < T;
+  const bool copy = n < T;
   int row = sum[0];   // first row of the block's next tokens
   for (int base = t0; base < t1; base += kRowThreads) {
     const int t = base + tid;
@@ -323,63 +323,68 @@ __device__ __forceinline__ void row_factors(const DzArgs& a, const HeadScale& sc
 }
 
 // bf16 layers: the kept 16-bit logits (units of q_step octaves below the maximum of
-// their 128 columns) become bf16 gradients where they lie.  A warp takes 8 rows of 128
+// their 128 columns) become bf16 gradients where they lie.  A warp takes 16 rows of 128
 // columns, 16 lanes a row's 256 bytes, all of its loads in flight at once.
-constexpr int kDzRows = 8;
+constexpr int kDzRows = 16;
 __global__ void __launch_bounds__(256)
 head_dz_bf16_kernel(const DzArgs a, uint16_t* __restrict__ kept) {
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int n = min(a.cnt->n - a.row0, a.piece);
-  if (n <= 0) return;
-  const HeadScale sc = head_scale(a.cnt->n, a.cnt->n_ce, a.cnt->n_kd, a.coef, a.coef_kd, a.coef_z, a.tau);
-  const int r0 = blockIdx.y * kDzRows;
-  if (r0 >= ((n + kHeadRowAlign - 1) & ~(kHeadRowAlign - 1))) return;
   const int h = blockIdx.x * 8 + warp;
-  if (h * 128 >= a.ld) return;
-  const int r = r0 + (lane & (kDzRows - 1));
-  float m = 0.f, L1 = 0.f, L2 = 0.f, k1 = 0.f, k2 = 0.f;
-  if (r < n) {
-    m = a.pm[static_cast<size_t>(h) * a.ldp + r];
-    m = (m == -__int_as_float(0x7f800000) ? 0.f : m) + 65536.f * a.q_step;
-    L1 = a.l1[a.row0 + r];
-    L2 = a.l2[a.row0 + r];
-    row_factors(a, sc, a.flag[a.row0 + r], L1, k1, k2);
-  }
+  if (n <= 0 || h * 128 >= a.ld) return;
+  const HeadScale sc = head_scale(a.cnt->n, a.cnt->n_ce, a.cnt->n_kd, a.coef, a.coef_kd, a.coef_z, a.tau);
+  const int rows = (n + kHeadRowAlign - 1) & ~(kHeadRowAlign - 1);
   const int c0 = h * 128 + (lane & 15) * 8;
-  char* base = reinterpret_cast<char*>(kept + static_cast<size_t>(r0) * a.ld + c0);
-  uint4 u[kDzRows / 2];
+  const bool edge = h * 128 + 128 > a.V;
+  for (int r0 = blockIdx.y * kDzRows; r0 < rows; r0 += gridDim.y * kDzRows) {
+    char* base = reinterpret_cast<char*>(kept + static_cast<size_t>(r0) * a.ld + c0);
+    uint4 u[kDzRows / 2];
 #pragma unroll
-  for (int i = 0; i < kDzRows / 2; ++i) {
-    const int rr = 2 * i + (lane >> 4);
-    if (r0 + rr < n) u[i] = *reinterpret_cast<const uint4*>(base + static_cast<size_t>(rr) * a.ld * 2);
-  }
-#pragma unroll
-  for (int i = 0; i < kDzRows / 2; ++i) {
-    const int rr = 2 * i + (lane >> 4);
-    const float mm = __shfl_sync(kFull, m, rr), La = __shfl_sync(kFull, L1, rr);
-    const float Lb = __shfl_sync(kFull, L2, rr);
-    const float ka = __shfl_sync(kFull, k1, rr), kb = __shfl_sync(kFull, k2, rr);
-    uint4* at = reinterpret_cast<uint4*>(base + static_cast<size_t>(rr) * a.ld * 2);
-    if (r0 + rr >= n) {
-      *at = make_uint4(0, 0, 0, 0);
-      continue;
+    for (int i = 0; i < kDzRows / 2; ++i) {
+      const int rr = 2 * i + (lane >> 4);
+      if (r0 + rr < n) u[i] = *reinterpret_cast<const uint4*>(base + static_cast<size_t>(rr) * a.ld * 2);
     }
-    const uint32_t wds[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
-    float g[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      // 65536 + q by its bits: the conversion unit is the exponentials' as well
-      const float q = __uint_as_float(0x47800000u | (j & 1 ? (wds[j >> 1] >> 9) & 0x7fff80u
-                                                           : (wds[j >> 1] & 0xffffu) << 7));
-      const float y = fmaf(q, -a.q_step, mm);
-      g[j] = ka * ex2(y - La);
-      if (a.two) g[j] = fmaf(kb, ex2(fmaf(y, a.inv_tau, -Lb)), g[j]);
-      if (c0 + j >= a.V) g[j] = 0.f;
+    const int r = r0 + (lane & (kDzRows - 1));
+    float m = 0.f, L1 = 0.f, L2 = 0.f, k1 = 0.f, k2 = 0.f;
+    if (r < n) {
+      m = a.pm[static_cast<size_t>(h) * a.ldp + r];
+      m = (m == -__int_as_float(0x7f800000) ? 0.f : m) + 65536.f * a.q_step;
+      L1 = a.l1[a.row0 + r];
+      L2 = a.l2[a.row0 + r];
+      row_factors(a, sc, a.flag[a.row0 + r], L1, k1, k2);
     }
-    // (one rounding to bf16: what the tensor cores take)
-    *at = pack16(g, __nv_bfloat16());
+#pragma unroll
+    for (int i = 0; i < kDzRows / 2; ++i) {
+      const int rr = 2 * i + (lane >> 4);
+      const float mm = __shfl_sync(kFull, m, rr), La = __shfl_sync(kFull, L1, rr);
+      const float Lb = __shfl_sync(kFull, L2, rr);
+      const float ka = __shfl_sync(kFull, k1, rr), kb = __shfl_sync(kFull, k2, rr);
+      uint4* at = reinterpret_cast<uint4*>(base + static_cast<size_t>(rr) * a.ld * 2);
+      if (r0 + rr >= n) {
+        *at = make_uint4(0, 0, 0, 0);
+        continue;
+      }
+      const uint32_t wds[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+      float g[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        // 65536 + q by its bits: the conversion unit is the exponentials' as well
+        const float q = __uint_as_float(0x47800000u | (j & 1 ? (wds[j >> 1] >> 9) & 0x7fff80u
+                                                             : (wds[j >> 1] & 0xffffu) << 7));
+        const float y = fmaf(q, -a.q_step, mm);
+        g[j] = ka * ex2(y - La);
+        if (a.two) g[j] = fmaf(kb, ex2(fmaf(y, a.inv_tau, -Lb)), g[j]);
+      }
+      if (edge) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (c0 + j >= a.V) g[j] = 0.f;
+      }
+      // (one rounding to bf16: what the tensor cores take)
+      *at = pack16(g, __nv_bfloat16());
+    }
   }
 }
 
@@ -436,13 +441,14 @@ head_dz_entries_kernel(const DzArgs a, const int32_t* __restrict__ ent,
 }
 
 // ---- dx from its parts ---------------------------------------------------------------------
-// A block takes four tokens at a time, their parts' loads in flight together.
-constexpr int kDxTokens = 4;
+// A block takes four tokens at a time, their parts' loads in flight together; where the
+// tokens are few and the parts many, one, and eight parts at a time (129 tokens, 31 parts
+// of 512: 23 us by four).
 __device__ __forceinline__ void store4(float* p, const float4& v) { *reinterpret_cast<float4*>(p) = v; }
 __device__ __forceinline__ void store4(__nv_bfloat16* p, const float4& v) {
   *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
 }
-template <typename O>
+template <typename O, int kDxTokens>
 __global__ void __launch_bounds__(256)
 head_dx_kernel(const HeadCounts* cnt, const int32_t* __restrict__ pos, const float* __restrict__ part,
                int splits, size_t split_stride, int row0, int piece, int T, int d, bool zeros,
@@ -467,7 +473,7 @@ head_dx_kernel(const HeadCounts* cnt, const int32_t* __restrict__ pos, const flo
       float4 v[kDxTokens];
 #pragma unroll
       for (int j = 0; j < kDxTokens; ++j) v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 2
+#pragma unroll (8 / kDxTokens)
       for (int s = 0; s < splits; ++s)
 #pragma unroll
         for (int j = 0; j < kDxTokens; ++j)
@@ -544,7 +550,7 @@ HeadPlan head_plan(const occult_desc_t& ds, const occult_head_t& opt, bool step)
   p.ld = static_cast<int>(up(p.V, 256));
   const int64_t row_bytes = static_cast<int64_t>(p.ld) * (bf ? 2 : 4);
   int64_t piece = opt.piece > 0 ? opt.piece : (int64_t(1) << 30) / row_bytes;
-  piece = std::min<int64_t>(kDzRows * 32768, piece);   // (a grid's second dimension)
+  piece = std::min<int64_t>(1 << 20, piece);
   piece = std::max<int64_t>(kHeadRowAlign, piece / kHeadRowAlign * kHeadRowAlign);
   p.piece = step ? static_cast<int>(std::min<int64_t>(piece, Tr)) : Tr;
   p.n_pieces = (Tr + p.piece - 1) / p.piece;
@@ -564,7 +570,7 @@ HeadPlan head_plan(const occult_desc_t& ds, const occult_head_t& opt, bool step)
   p.o_cnt = take(sizeof(HeadCounts));
   p.o_idx = take(4 * T); p.o_pos = take(4 * T); p.o_flag = take(T);
   p.o_ent = take(4 * T * p.E); p.o_q = take(4 * T * p.E); p.o_zt = take(4 * T * p.E);
-  p.o_xc = take(bf ? T * p.d * 2 : 0);
+  p.o_xc = take(T * p.d * (bf ? 2 : 4));
   p.o_m = take(4 * P * p.halves); p.o_s = take(4 * P * p.halves);
   p.o_s2 = take(p.two ? 4 * P * p.halves : 0);
   p.o_l1 = take(4 * T); p.o_l2 = take(4 * T);
@@ -599,7 +605,7 @@ int launch_head(const LaunchCtx& ctx, const HeadPlan& p, const HeadArgs& a) {
   cudaError_t e = launch_pdl(head_rows_kernel, (p.T + per - 1) / per, kRowThreads, 0, ctx.stream, a.labels,
                              a.t_ids, p.T, p.V, p.K, per, cnt, idx, pos, flag, ent, ent_q, a.lse,
                              a.token_loss, static_cast<const uint4*>(a.x),
-                             bf ? reinterpret_cast<uint4*>(ws + p.o_xc) : nullptr, p.d / 8);
+                             reinterpret_cast<uint4*>(ws + p.o_xc), p.d / (bf ? 8 : 4));
   if (e != cudaSuccess) return OCCULT_ERR_CUDA;
   if (p.K) {
     e = launch_pdl(head_entries_kernel, std::min((p.T + kEntWarps - 1) / kEntWarps, ctx.num_sms * 16),
@@ -635,7 +641,9 @@ int launch_head(const LaunchCtx& ctx, const HeadPlan& p, const HeadArgs& a) {
                                                       ctx.num_sms * 16));
     if (bf) {
       auto* kept = reinterpret_cast<uint16_t*>(ws + p.o_kept);
-      const dim3 grid((p.ld / 128 + 7) / 8, (rows + kHeadRowAlign - 1) / kHeadRowAlign * (kHeadRowAlign / kDzRows));
+      // some eight blocks an SM, however many of the rows count
+      const int gx = (p.ld / 128 + 7) / 8, row_blocks = (rows + kHeadRowAlign - 1) / kHeadRowAlign * (kHeadRowAlign / kDzRows);
+      const dim3 grid(gx, std::min(row_blocks, std::max(1, (ctx.num_sms * 8 + gx - 1) / gx)));
       e = launch_pdl(head_dz_bf16_kernel, grid, 256, 0, ctx.stream, z, kept);
       if (e != cudaSuccess) return OCCULT_ERR_CUDA;
       e = launch_pdl(head_dz_entries_kernel<__nv_bfloat16>, eb, 256, 0, ctx.stream, z, ent, ent_q, zt,
@@ -651,16 +659,16 @@ int launch_head(const LaunchCtx& ctx, const HeadPlan& p, const HeadArgs& a) {
     if (a.dx) {
       rc = bf ? launch_head_dx_bf16(ctx, p, a, row0) : launch_head_dx_f32(ctx, p, a, row0);
       if (rc) return rc;
-      const int nb = std::min((p.T + kDxTokens - 1) / kDxTokens, ctx.num_sms * 8);
+      const int tokens = p.T >= 4 * ctx.num_sms ? 4 : 1;
+      const int nb = std::min((p.T + tokens - 1) / tokens, ctx.num_sms * 8);
+      const int threads = std::min(256, (p.d / 4 + 31) / 32 * 32);
       const size_t stride = static_cast<size_t>(p.piece) * p.d;
-      if (p.grad_dtype == OCCULT_BF16)
-        e = launch_pdl(head_dx_kernel<__nv_bfloat16>, nb, 256, 0, ctx.stream, cnt, pos, part, p.splits,
-                       stride, row0, p.piece, p.T, p.d, i == 0, p.coef, p.coef_kd, p.coef_z, p.tau,
-                       a.dloss, static_cast<__nv_bfloat16*>(a.dx));
-      else
-        e = launch_pdl(head_dx_kernel<float>, nb, 256, 0, ctx.stream, cnt, pos, part, p.splits, stride,
-                       row0, p.piece, p.T, p.d, i == 0, p.coef, p.coef_kd, p.coef_z, p.tau, a.dloss,
-                       static_cast<float*>(a.dx));
+#define OCCULT_HEAD_DX(O)                                                                          \
+  launch_pdl(tokens == 4 ? head_dx_kernel<O, 4> : head_dx_kernel<O, 1>, nb, threads, 0, ctx.stream, \
+             cnt, pos, part, p.splits, stride, row0, p.piece, p.T, p.d, i == 0, p.coef, p.coef_kd, \
+             p.coef_z, p.tau, a.dloss, static_cast<O*>(a.dx))
+      e = p.grad_dtype == OCCULT_BF16 ? OCCULT_HEAD_DX(__nv_bfloat16) : OCCULT_HEAD_DX(float);
+#undef OCCULT_HEAD_DX
       if (e != cudaSuccess) return OCCULT_ERR_CUDA;
     }
     if (a.dw) {

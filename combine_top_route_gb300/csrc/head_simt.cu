@@ -62,14 +62,19 @@ __device__ __forceinline__ void tile_product(float (&acc)[TS / 16][TS / 16], int
 
 struct SimtArgs {
   const HeadCounts* cnt;
-  const float *x, *w, *dloss;
-  const int32_t *idx, *ent;
+  const float *x, *xc, *w, *dloss;   // x, and its compact copy where tokens are left out
+  const int32_t* ent;
   float *zt, *pm, *ps, *ps2, *kept;   // kept: the logits, then their gradient
   float *part, *acc;
   void* out;
-  int row0, piece, V, d, E, ld, halves, splits, two, bf16, first, last;
+  int T, row0, piece, V, d, E, ld, halves, splits, two, bf16, first, last;
   float inv_tau, coef, coef_kd, coef_z, tau;
 };
+
+// The piece's first compact row of x.
+__device__ __forceinline__ const float* x_rows(const SimtArgs& a) {
+  return (a.cnt->n == a.T ? a.x : a.xc) + static_cast<size_t>(a.row0) * a.d;
+}
 
 // Logits: a tile's columns are a part of its rows' maxima and sums.
 template <int TS>
@@ -82,11 +87,12 @@ __global__ void __launch_bounds__(256) head_logits_f32_kernel(const SimtArgs a) 
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   const int c0 = blockIdx.x * TS;
   const float NEG = -__int_as_float(0x7f800000);
+  const float* x = x_rows(a);
   for (int m0 = blockIdx.y * TS; m0 < n; m0 += gridDim.y * TS) {
     float acc[V][V] = {};
     tile_product<TS, true, true>(
         acc, 0, c0 < a.V ? a.d : 0,
-        [&](int m, int k) { return m0 + m < n ? a.x[static_cast<size_t>(a.idx[a.row0 + m0 + m]) * a.d + k] : 0.f; },
+        [&](int m, int k) { return m0 + m < n ? x[static_cast<size_t>(m0 + m) * a.d + k] : 0.f; },
         [&](int v, int k) { return c0 + v < a.V ? a.w[static_cast<size_t>(c0 + v) * a.d + k] : 0.f; });
 #pragma unroll
     for (int i = 0; i < V; ++i)
@@ -165,13 +171,14 @@ __global__ void __launch_bounds__(256) head_dw_f32_kernel(const SimtArgs a) {
   const int c0 = blockIdx.x * TS;
   const HeadScale sc = head_scale(a.cnt->n, a.cnt->n_ce, a.cnt->n_kd, a.coef, a.coef_kd, a.coef_z, a.tau);
   const float g = sc.unit * (a.dloss ? *a.dloss : 1.f);
+  const float* x = x_rows(a);
   for (int m0 = blockIdx.y * TS; m0 < a.V; m0 += gridDim.y * TS) {
     float acc[V][V] = {};
     tile_product<TS, false, false>(
         acc, 0, n,
         [&](int m, int k) { return m0 + m < a.V ? a.kept[static_cast<size_t>(k) * a.ld + m0 + m] : 0.f; },
         [&](int c, int k) {
-          return c0 + c < a.d ? a.x[static_cast<size_t>(a.idx[a.row0 + k]) * a.d + c0 + c] : 0.f;
+          return c0 + c < a.d ? x[static_cast<size_t>(k) * a.d + c0 + c] : 0.f;
         });
     float* sum = a.bf16 ? a.acc : static_cast<float*>(a.out);
 #pragma unroll
@@ -195,7 +202,8 @@ SimtArgs simt_args(const HeadPlan& p, const HeadArgs& a, int row0) {
   g.x = static_cast<const float*>(a.x);
   g.w = static_cast<const float*>(a.w);
   g.dloss = a.dloss;
-  g.idx = reinterpret_cast<const int32_t*>(ws + p.o_idx);
+  g.xc = reinterpret_cast<const float*>(ws + p.o_xc);
+  g.T = p.T;
   g.ent = reinterpret_cast<const int32_t*>(ws + p.o_ent);
   g.zt = reinterpret_cast<float*>(ws + p.o_zt);
   g.pm = reinterpret_cast<float*>(ws + p.o_m);
