@@ -313,26 +313,37 @@ route_scored_kernel(const RouteArgs a) {
   __shared__ int s_dev[OCCULT_MAX_EXPERTS], s_exp[PL * 32];
   __shared__ float s_bias[OCCULT_MAX_EXPERTS], s_span[2];
   __shared__ bool s_odd;
+  __shared__ int s_count[kWarps][32];
   pdl_wait();
   pdl_trigger();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   // the experts of every lane's places, and the bias's span
-  for (int e = tid; e < a.Ne; e += blockDim.x) {
-    s_dev[e] = a.e2v[e] & 31;
-    s_bias[e] = BIAS ? a.bias[e] : 0.f;
+  static_assert(kWarps * 32 >= OCCULT_MAX_EXPERTS, "a thread an expert");
+  const int dev = tid < a.Ne ? a.e2v[tid] & 31 : 32;
+  if (tid < a.Ne) {
+    s_dev[tid] = dev;
+    s_bias[tid] = BIAS ? a.bias[tid] : 0.f;
   }
-  for (int i = tid; i < PL * 32; i += blockDim.x) {
-    const int g = i / PL / a.group_lanes, j = i - g * a.group_lanes * PL;
+  for (int i = tid; i < PL * 32; i += kWarps * 32) {
+    const int g = (i / PL) >> a.group_shift, j = i - (g << a.group_shift) * PL;
     s_exp[i] = !a.vdev_groups && g < a.G && j < a.per ? g * a.per + j : -1;
   }
-  __syncthreads();
-  if (a.vdev_groups)
-    for (int e = tid; e < a.Ne; e += blockDim.x) {
-      const int g = s_dev[e];
-      int j = 0;
-      for (int f = 0; f < e; ++f) j += s_dev[f] == g ? 1 : 0;
-      if (g < a.G && j < a.per) s_exp[g * a.group_lanes * PL + j] = e;
+  if (a.vdev_groups) {
+    // an expert's number among its device's: those before it in its warp, and the warps'
+    // counts
+    for (int i = tid; i < kWarps * 32; i += kWarps * 32) s_count[i / 32][i % 32] = 0;
+    __syncthreads();
+    const uint32_t same = __match_any_sync(kFull, dev);
+    int j = __popc(same & lanemask_lt());
+    if (j == 0 && dev < 32) s_count[warp][dev] = __popc(same);
+    __syncthreads();
+    if (dev < a.G) {
+      for (int w = 0; w < warp; ++w) j += s_count[w][dev];
+      if (j < a.per) s_exp[(dev << a.group_shift) * PL + j] = tid;
     }
+  } else {
+    __syncthreads();
+  }
   if (BIAS && warp == 0) {
     float lo = 3e38f, hi = -3e38f;
     bool odd = false;
