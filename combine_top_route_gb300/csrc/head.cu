@@ -20,20 +20,92 @@ namespace occult {
 
 namespace {
 
+// ---- entries ----------------------------------------------------------------------
+// A warp makes a row's entries: the teacher's probabilities at temperature tau, and the
+// label (q = -1), in ascending token order, absent ones behind.  Returns whether the
+// teacher says anything.  `ids`: 160 words of the warp's own.
+constexpr int kEntPer = (OCCULT_MAX_TEACHER + 1 + 31) / 32;
+__device__ __forceinline__ bool make_entries(const int32_t* __restrict__ t_ids, const float* __restrict__ t_logits,
+                                             int t, int f, int label, int V, int K, float inv_tau, int* ids,
+                                             int32_t* __restrict__ ent, float* __restrict__ ent_q) {
+  const int lane = threadIdx.x & 31, E = K + 1;
+  const float NEG = -__int_as_float(0x7f800000);
+  int id[kEntPer];
+  float q[kEntPer];
+  float top = NEG;
+#pragma unroll
+  for (int i = 0; i < kEntPer; ++i) {
+    const int j = lane + 32 * i;
+    id[i] = kHeadNoEntry;
+    q[i] = NEG;
+    if (j < K && (f & kRowKd)) {
+      const size_t at = static_cast<size_t>(t) * K + j;
+      const int v = t_ids[at];
+      const float l = t_logits[at] * inv_tau;
+      if (static_cast<unsigned>(v) < static_cast<unsigned>(V)) {
+        id[i] = v;
+        q[i] = l;
+        top = fmaxf(top, l);
+      }
+    }
+  }
+  top = warp_max(top);
+  if (top == NEG) top = 0.f;
+  float sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < kEntPer; ++i) {
+    q[i] = id[i] == kHeadNoEntry ? 0.f : expf(q[i] - top);
+    sum += q[i];
+  }
+  sum = warp_sum(sum);
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+  for (int i = 0; i < kEntPer; ++i) {
+    const int j = lane + 32 * i;
+    q[i] *= inv;
+    if (j == K) {
+      id[i] = (f & kRowCe) ? label : kHeadNoEntry;
+      q[i] = -1.f;
+    }
+    ids[j] = j < E ? id[i] : kHeadNoEntry;
+  }
+  __syncwarp();
+  int rank[kEntPer];
+#pragma unroll
+  for (int i = 0; i < kEntPer; ++i) rank[i] = 0;
+  for (int k = 0; k < E; ++k) {
+    const int other = ids[k];
+#pragma unroll
+    for (int i = 0; i < kEntPer; ++i)
+      if (32 * i < E) rank[i] += (other < id[i] || (other == id[i] && k < lane + 32 * i)) ? 1 : 0;
+  }
+#pragma unroll
+  for (int i = 0; i < kEntPer; ++i)
+    if (lane + 32 * i < E) {
+      ent[rank[i]] = id[i];
+      ent_q[rank[i]] = q[i];
+    }
+  __syncwarp();
+  return sum != 0.f;
+}
+
 // ---- rows -----------------------------------------------------------------------
 // Which tokens a term counts, and their compact rows in token order.  A block has `per`
 // tokens of its own and counts all of them (a few KB from L2, which is cheaper than
 // another launch): those before its own give its first row, all of them the totals.
 // Where some token is left out, the rows of x are copied to their compact place on the way
 // (else the products read x itself), with zeros up to the next multiple of 64, so that
-// dw's reduction may run over them.
+// dw's reduction may run over them; and that token's outputs are zeros.  With a teacher a
+// warp then makes the entries of its tokens' rows.
 constexpr int kRowThreads = 256;
 __global__ void __launch_bounds__(kRowThreads)
-head_rows_kernel(const int32_t* __restrict__ labels, const int32_t* __restrict__ t_ids, int T,
-                 int V, int K, int per, HeadCounts* cnt, int32_t* __restrict__ idx,
-                 int32_t* __restrict__ pos, uint8_t* __restrict__ flag, int32_t* __restrict__ ent,
-                 float* __restrict__ ent_q, float* __restrict__ lse, float* __restrict__ token_loss,
-                 const uint4* __restrict__ x, uint4* __restrict__ xc, int vecs) {
+head_rows_kernel(const int32_t* __restrict__ labels, const int32_t* __restrict__ t_ids,
+                 const float* __restrict__ t_logits, int T, int V, int K, float inv_tau, int per,
+                 HeadCounts* cnt, int32_t* __restrict__ idx, uint8_t* __restrict__ flag,
+                 int32_t* __restrict__ ent, float* __restrict__ ent_q, float* __restrict__ lse,
+                 float* __restrict__ token_loss, const uint4* __restrict__ x, uint4* __restrict__ xc, int vecs,
+                 char* __restrict__ dx, int dx_bytes) {
+  __shared__ int s_ids[kRowThreads / 32][32 * kEntPer];
   __shared__ int s_sum[4][kRowThreads / 32], s_warp[kRowThreads / 32], s_pos[kRowThreads];
   pdl_wait();
   pdl_trigger();
@@ -87,7 +159,6 @@ head_rows_kernel(const int32_t* __restrict__ labels, const int32_t* __restrict__
     }
     s_pos[tid] = f ? r : -1;
     if (t < t1) {
-      pos[t] = f ? r : -1;
       if (f) {
         idx[r] = t;
         flag[r] = static_cast<uint8_t>(f);
@@ -101,15 +172,30 @@ head_rows_kernel(const int32_t* __restrict__ labels, const int32_t* __restrict__
       }
     }
     __syncthreads();
-    if (copy)
-      for (int i = warp; i < min(kRowThreads, t1 - base); i += kRowThreads / 32) {
-        const int to = s_pos[i];
-        if (to < 0) continue;
-        const uint4* src = x + static_cast<size_t>(base + i) * vecs;
+    for (int i = warp; i < min(kRowThreads, t1 - base); i += kRowThreads / 32) {
+      const int to = s_pos[i], ti = base + i;
+      if (to < 0) {
+        // (rows of 8 bytes at least)
+        if (dx)
+          for (int v = lane * 8; v < dx_bytes; v += 256)
+            *reinterpret_cast<uint2*>(dx + static_cast<size_t>(ti) * dx_bytes + v) = make_uint2(0, 0);
+        continue;
+      }
+      if (copy) {
+        const uint4* src = x + static_cast<size_t>(ti) * vecs;
         uint4* dst = xc + static_cast<size_t>(to) * vecs;
 #pragma unroll 4
         for (int v = lane; v < vecs; v += 32) dst[v] = src[v];
       }
+      if (K) {
+        const int fi = flag_of(ti);
+        const size_t at = static_cast<size_t>(to) * (K + 1);
+        const bool says = make_entries(t_ids, t_logits, ti, fi, labels ? labels[ti] : 0, V, K, inv_tau,
+                                       s_ids[warp], ent + at, ent_q + at);
+        // nothing to learn from: its term is 0, and so is its gradient
+        if (!says && lane == 0) flag[to] = static_cast<uint8_t>(fi & ~kRowKd);
+      }
+    }
     row += all;
     __syncthreads();
   }
@@ -117,84 +203,6 @@ head_rows_kernel(const int32_t* __restrict__ labels, const int32_t* __restrict__
     for (size_t i = static_cast<size_t>(n) * vecs + tid; i < static_cast<size_t>((n + 63) & ~63) * vecs;
          i += kRowThreads)
       xc[i] = make_uint4(0, 0, 0, 0);
-}
-
-// ---- entries ----------------------------------------------------------------------
-// One warp a row: the teacher's probabilities at temperature tau, and the row's entries
-// (label: q = -1) in ascending token order, absent ones behind.
-constexpr int kEntWarps = 4;
-__global__ void __launch_bounds__(kEntWarps * 32)
-head_entries_kernel(const int32_t* __restrict__ labels, const int32_t* __restrict__ t_ids,
-                    const float* __restrict__ t_logits, const HeadCounts* cnt,
-                    const int32_t* __restrict__ idx, uint8_t* __restrict__ flag, int V, int K,
-                    float inv_tau, int32_t* __restrict__ ent, float* __restrict__ ent_q) {
-  constexpr int kPer = (OCCULT_MAX_TEACHER + 1 + 31) / 32;
-  __shared__ int s_id[kEntWarps][32 * kPer];
-  pdl_wait();
-  pdl_trigger();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int n = cnt->n, E = K + 1;
-  int* ids = s_id[warp];
-  for (int r = blockIdx.x * kEntWarps + warp; r < n; r += gridDim.x * kEntWarps) {
-    const size_t t = idx[r];
-    const int f = flag[r];
-    int id[kPer];
-    float q[kPer];
-    float top = -__int_as_float(0x7f800000);
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int j = lane + 32 * i;
-      id[i] = kHeadNoEntry;
-      q[i] = -__int_as_float(0x7f800000);
-      if (j < K && (f & kRowKd)) {
-        const int v = t_ids[t * K + j];
-        if (static_cast<unsigned>(v) < static_cast<unsigned>(V)) {
-          id[i] = v;
-          q[i] = t_logits[t * K + j] * inv_tau;
-          top = fmaxf(top, q[i]);
-        }
-      }
-    }
-    top = warp_max(top);
-    if (top == -__int_as_float(0x7f800000)) top = 0.f;
-    float sum = 0.f;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      q[i] = id[i] == kHeadNoEntry ? 0.f : expf(q[i] - top);
-      sum += q[i];
-    }
-    sum = warp_sum(sum);
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    // nothing to learn from: its term is 0, and so is its gradient
-    if (sum == 0.f && lane == 0) flag[r] = static_cast<uint8_t>(f & ~kRowKd);
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int j = lane + 32 * i;
-      q[i] *= inv;
-      if (j == K) {
-        id[i] = (f & kRowCe) ? labels[t] : kHeadNoEntry;
-        q[i] = -1.f;
-      }
-      ids[j] = j < E ? id[i] : kHeadNoEntry;
-    }
-    __syncwarp();
-    int rank[kPer];
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) rank[i] = 0;
-    for (int k = 0; k < E; ++k) {
-      const int other = ids[k];
-#pragma unroll
-      for (int i = 0; i < kPer; ++i)
-        rank[i] += (other < id[i] || (other == id[i] && k < lane + 32 * i)) ? 1 : 0;
-    }
-#pragma unroll
-    for (int i = 0; i < kPer; ++i)
-      if (lane + 32 * i < E) {
-        ent[static_cast<size_t>(r) * E + rank[i]] = id[i];
-        ent_q[static_cast<size_t>(r) * E + rank[i]] = q[i];
-      }
-    __syncwarp();
-  }
 }
 
 // ---- a row's sums, losses and the means ---------------------------------------------
@@ -272,7 +280,10 @@ head_sum_kernel(HeadCounts* cnt, const HeadLossOut o, const float* __restrict__ 
   if (warp == 0) {
     const float a = warp_sum(have ? s_ce[lane] : 0.f), b = warp_sum(have ? s_kd[lane] : 0.f),
                 c = warp_sum(have ? s_z[lane] : 0.f);
-    if (lane == 0) {
+    if (lane == 0 && n_blocks == 1) {
+      mean_losses(o, *cnt, a, b, c);   // a block alone
+      s_last = false;
+    } else if (lane == 0) {
       float* out = sums + 3 * static_cast<size_t>(block0 + blockIdx.x);
       out[0] = a;
       out[1] = b;
@@ -388,55 +399,77 @@ head_dz_bf16_kernel(const DzArgs a, uint16_t* __restrict__ kept) {
   }
 }
 
-// fp32 layers: the kept logits themselves.
+// Gradient at entry e of row r, the first of its token: the softmaxes at the entry's own fp32
+// logit, minus the factors of every entry of that token.
+__device__ __forceinline__ float entry_dz(const DzArgs& a, const HeadScale& sc, const HeadLossOut& o, size_t at,
+                                          int e, int id, float L1, float L2, float k1, float k2) {
+  const float z = o.zt[at];
+  float g = k1 * exp2f(z * kLog2e - L1);
+  if (a.two) g += k2 * exp2f(z * (kLog2e * a.inv_tau) - L2);
+  for (int f = e; f < o.E && o.ent[at + f - e] == id; ++f) {
+    const float q = o.ent_q[at + f - e];
+    g -= q < 0.f ? sc.k_ce : sc.k_kd * q;
+  }
+  return g;
+}
+
+// bf16 layers: the entries' columns, written over.
 __global__ void __launch_bounds__(256)
-head_dz_f32_kernel(const DzArgs a, float* __restrict__ kept) {
+head_dz_entries_kernel(const DzArgs a, const HeadLossOut o, __nv_bfloat16* __restrict__ dz) {
   pdl_wait();
   pdl_trigger();
   const int n = min(a.cnt->n - a.row0, a.piece);
   const HeadScale sc = head_scale(a.cnt->n, a.cnt->n_ce, a.cnt->n_kd, a.coef, a.coef_kd, a.coef_z, a.tau);
-  for (int r = blockIdx.y; r < n; r += gridDim.y) {
-    const float L1 = a.l1[a.row0 + r], L2 = a.l2[a.row0 + r];
+  const int64_t total = static_cast<int64_t>(n) * o.E;
+  for (int64_t i = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; i < total;
+       i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
+    const int r = static_cast<int>(i / o.E), e = static_cast<int>(i - static_cast<int64_t>(r) * o.E);
+    const size_t rg = static_cast<size_t>(a.row0) + r, at = rg * o.E + e;
+    const int id = o.ent[at];
+    if (id == kHeadNoEntry || (e > 0 && o.ent[at - 1] == id)) continue;   // the first one writes
     float k1, k2;
-    row_factors(a, sc, a.flag[a.row0 + r], L1, k1, k2);
-    for (int c = blockIdx.x * blockDim.x + threadIdx.x; c < a.V; c += gridDim.x * blockDim.x) {
-      float* at = kept + static_cast<size_t>(r) * a.ld + c;
-      const float z = *at;
-      float g = k1 * exp2f(z * kLog2e - L1);
-      if (a.two) g += k2 * exp2f(z * (kLog2e * a.inv_tau) - L2);
-      *at = g;
-    }
+    row_factors(a, sc, a.flag[rg], a.l1[rg], k1, k2);
+    dz[static_cast<size_t>(r) * a.ld + id] =
+        __float2bfloat16_rn(entry_dz(a, sc, o, at, e, id, a.l1[rg], a.l2[rg], k1, k2));
   }
 }
 
-// The entries' columns: the softmaxes at the entry's own fp32 logit, minus the factors of
-// every entry of that token.
-template <typename G>
+// fp32 layers: the kept logits themselves, a block a row, its entries behind them.  (The
+// products' blocks are let in only when this one is done: in among its blocks they would
+// gather on few SMs, 40 us for the small layer's step instead of 32.)
 __global__ void __launch_bounds__(256)
-head_dz_entries_kernel(const DzArgs a, const int32_t* __restrict__ ent,
-                       const float* __restrict__ ent_q, const float* __restrict__ zt, int E,
-                       G* __restrict__ dz) {
+head_dz_f32_kernel(const DzArgs a, const HeadLossOut o, float* __restrict__ kept) {
   pdl_wait();
-  pdl_trigger();
   const int n = min(a.cnt->n - a.row0, a.piece);
   const HeadScale sc = head_scale(a.cnt->n, a.cnt->n_ce, a.cnt->n_kd, a.coef, a.coef_kd, a.coef_z, a.tau);
-  const int64_t total = static_cast<int64_t>(n) * E;
-  for (int64_t i = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; i < total;
-       i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-    const int r = static_cast<int>(i / E), e = static_cast<int>(i - static_cast<int64_t>(r) * E);
-    const size_t rg = static_cast<size_t>(a.row0) + r, at = rg * E + e;
-    const int id = ent[at];
-    if (id == kHeadNoEntry || (e > 0 && ent[at - 1] == id)) continue;   // the first one writes
-    const float L1 = a.l1[rg], z = zt[at];
+  for (int r = blockIdx.x; r < n; r += gridDim.x) {
+    const size_t rg = static_cast<size_t>(a.row0) + r;
+    const float L1 = a.l1[rg], L2 = a.l2[rg];
     float k1, k2;
     row_factors(a, sc, a.flag[rg], L1, k1, k2);
-    float g = k1 * exp2f(z * kLog2e - L1);
-    if (a.two) g += k2 * exp2f(z * (kLog2e * a.inv_tau) - a.l2[rg]);
-    for (int f = e; f < E && ent[at + f - e] == id; ++f) {
-      const float q = ent_q[at + f - e];
-      g -= q < 0.f ? sc.k_ce : sc.k_kd * q;
+    float* row = kept + static_cast<size_t>(r) * a.ld;
+    for (int c0 = threadIdx.x; c0 < a.V; c0 += 4 * blockDim.x) {
+      float z[4];   // (loaded ahead of the first store)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int c = c0 + j * blockDim.x;
+        z[j] = c < a.V ? row[c] : 0.f;
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int c = c0 + j * blockDim.x;
+        float g = k1 * exp2f(z[j] * kLog2e - L1);
+        if (a.two) g += k2 * exp2f(z[j] * (kLog2e * a.inv_tau) - L2);
+        if (c < a.V) row[c] = g;
+      }
     }
-    dz[static_cast<size_t>(r) * a.ld + id] = from_f32<G>(g);
+    __syncthreads();
+    for (int e = threadIdx.x; e < o.E; e += blockDim.x) {
+      const size_t at = rg * o.E + e;
+      const int id = o.ent[at];
+      if (id == kHeadNoEntry || (e > 0 && o.ent[at - 1] == id)) continue;
+      row[id] = entry_dz(a, sc, o, at, e, id, L1, L2, k1, k2);
+    }
   }
 }
 
@@ -450,25 +483,18 @@ __device__ __forceinline__ void store4(__nv_bfloat16* p, const float4& v) {
 }
 template <typename O, int kDxTokens>
 __global__ void __launch_bounds__(256)
-head_dx_kernel(const HeadCounts* cnt, const int32_t* __restrict__ pos, const float* __restrict__ part,
-               int splits, size_t split_stride, int row0, int piece, int T, int d, bool zeros,
-               float coef, float coef_kd, float coef_z, float tau, const float* __restrict__ dloss,
-               O* __restrict__ dx) {
+head_dx_kernel(const HeadCounts* cnt, const int32_t* __restrict__ idx, const float* __restrict__ part,
+               int splits, size_t split_stride, int row0, int piece, int d, float coef, float coef_kd,
+               float coef_z, float tau, const float* __restrict__ dloss, O* __restrict__ dx) {
   pdl_wait();
   pdl_trigger();
+  const int n = min(cnt->n - row0, piece);
   const HeadScale sc = head_scale(cnt->n, cnt->n_ce, cnt->n_kd, coef, coef_kd, coef_z, tau);
   const float g = sc.unit * (dloss ? *dloss : 1.f);
-  for (int t0 = blockIdx.x * kDxTokens; t0 < T; t0 += gridDim.x * kDxTokens) {
-    int r[kDxTokens];
-    bool any = false;
+  for (int r0 = blockIdx.x * kDxTokens; r0 < n; r0 += gridDim.x * kDxTokens) {
+    int t[kDxTokens];
 #pragma unroll
-    for (int j = 0; j < kDxTokens; ++j) {
-      // this piece's rows (from 0), -1: a row of zeros, -2: not now
-      const int at = t0 + j < T ? pos[t0 + j] : INT32_MAX;
-      r[j] = at < 0 ? (zeros ? -1 : -2) : at >= row0 && at < row0 + piece ? at - row0 : -2;
-      any |= r[j] > -2;
-    }
-    if (!any) continue;
+    for (int j = 0; j < kDxTokens; ++j) t[j] = r0 + j < n ? idx[row0 + r0 + j] : -1;
     for (int i = threadIdx.x * 4; i < d; i += blockDim.x * 4) {
       float4 v[kDxTokens];
 #pragma unroll
@@ -477,15 +503,15 @@ head_dx_kernel(const HeadCounts* cnt, const int32_t* __restrict__ pos, const flo
       for (int s = 0; s < splits; ++s)
 #pragma unroll
         for (int j = 0; j < kDxTokens; ++j)
-          if (r[j] >= 0) {
+          if (r0 + j < n) {
             const float4 f = __ldcs(reinterpret_cast<const float4*>(
-                part + s * split_stride + static_cast<size_t>(r[j]) * d + i));
+                part + s * split_stride + static_cast<size_t>(r0 + j) * d + i));
             v[j].x += f.x; v[j].y += f.y; v[j].z += f.z; v[j].w += f.w;
           }
 #pragma unroll
       for (int j = 0; j < kDxTokens; ++j)
-        if (r[j] > -2)
-          store4(dx + static_cast<size_t>(t0 + j) * d + i,
+        if (t[j] >= 0)
+          store4(dx + static_cast<size_t>(t[j]) * d + i,
                  make_float4(g * v[j].x, g * v[j].y, g * v[j].z, g * v[j].w));
     }
   }
@@ -495,22 +521,23 @@ size_t up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
 }  // namespace
 
-// Parts of dx's reduction over the vocabulary: as many as leave the fewest rounds of
-// tiles idle.  In rounds of tiles of the whole depth (278 us at 50304 columns), a part
-// costs its share of the rounds and its fp32 sums' way out and back: 8 bytes a value
-// against V products of 256 x 256 by a pair, 2.1e-4 rows d / V.  (8192 x 2048 x 50304: two
-// parts, 911 + 29 us; five, the fewest rounds, 873 + 62 us.)
-static int dx_splits(int rows, int d, int V) {
-  const bool pair = rows > 128;
-  const int64_t units = static_cast<int64_t>((rows + (pair ? 255 : 127)) / (pair ? 256 : 128)) *
-                        ((d + 255) / 256);
-  const int64_t slots = pair ? 76 : 152;   // CTA pairs or CTAs of a GB300
-  const double sums = 2.1e-4 * rows * d / V;
-  const int most = std::max(1, std::min(64, (V + 1023) / 1024));
+// Parts of dx's reduction over the vocabulary, of bf16 layers.  In k blocks' time (0.33 us
+// where the tensor cores are the bound): a tile lasts its blocks and some five more, a
+// part costs its fp32 sums' way out and back, 8 bytes a value.  Beside dw's tiles the
+// longest of dx or a CTA pair's share of all counts (8192 x 2048 x 50304: one part,
+// written straight to its rows); alone the rounds of dx's tiles.
+static int dx_splits(int rows, int d, int V, bool alone) {
+  constexpr int64_t pairs = 76;
+  const int64_t cols = (d + 255) / 256, units = (rows + 255) / 256 * cols;
+  const int64_t kb = (V + 63) / 64, dw = (V + 255) / 256 * cols * ((rows + 63) / 64 + 5);
+  const int most = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(64, kb / 8)));
   int best = 1;
   double best_t = 1e300;
   for (int s = 1; s <= most; ++s) {
-    const double t = static_cast<double>((units * s + slots - 1) / slots) / s + s * sums;
+    const double tile = static_cast<double>(kb) / s + 5;
+    double t = alone ? (units * s + pairs - 1) / pairs * tile
+                     : std::max(tile, (units * s * tile + dw) / pairs);
+    if (s > 1) t += s * 3.6e-6 * rows * d;
     if (t < best_t - 1e-12) { best_t = t; best = s; }
   }
   return best;
@@ -562,13 +589,14 @@ HeadPlan head_plan(const occult_desc_t& ds, const occult_head_t& opt, bool step)
   // Up to four tokens' losses: the weights' stream through the fp32 units.
   p.few = bf && !step && ds.T <= kHeadFewTokens;
   if (p.few) p.halves = head_few_blocks(p.V, p.d);
-  p.splits = !step ? 1 : bf ? dx_splits(rows, p.d, p.V) : dx_splits_f32(rows, p.d, p.V);
+  p.splits = !step ? 1 : bf ? dx_splits(rows, p.d, p.V, false) : dx_splits_f32(rows, p.d, p.V);
+  p.splits_alone = !step ? 1 : bf ? dx_splits(rows, p.d, p.V, true) : p.splits;
   p.q_step = std::max(24.f, 20.f * p.tau) / 65535.f;
   size_t o = 0;
   auto take = [&](size_t bytes) { const size_t at = o; o += up(bytes, 256); return at; };
   const size_t T = Tr, P = p.piece;
   p.o_cnt = take(sizeof(HeadCounts));
-  p.o_idx = take(4 * T); p.o_pos = take(4 * T); p.o_flag = take(T);
+  p.o_idx = take(4 * T); p.o_flag = take(T);
   p.o_ent = take(4 * T * p.E); p.o_q = take(4 * T * p.E); p.o_zt = take(4 * T * p.E);
   p.o_xc = take(T * p.d * (bf ? 2 : 4));
   p.o_m = take(4 * P * p.halves); p.o_s = take(4 * P * p.halves);
@@ -576,7 +604,8 @@ HeadPlan head_plan(const occult_desc_t& ds, const occult_head_t& opt, bool step)
   p.o_l1 = take(4 * T); p.o_l2 = take(4 * T);
   p.o_sum = take(12 * (T / 32 + p.n_pieces));
   p.o_kept = take(step ? P * row_bytes : 0);
-  p.o_part = take(step ? 4 * static_cast<size_t>(p.splits) * P * p.d : 0);
+  const size_t parts = std::max(p.splits, p.splits_alone);
+  p.o_part = take(step && (!bf || parts > 1) ? 4 * parts * P * p.d : 0);
   p.o_acc = take(step && p.n_pieces > 1 && p.grad_dtype == OCCULT_BF16
                      ? 4 * static_cast<size_t>(p.V) * p.d : 0);
   p.total = o;
@@ -587,11 +616,9 @@ int launch_head(const LaunchCtx& ctx, const HeadPlan& p, const HeadArgs& a) {
   char* ws = a.ws;
   auto* cnt = reinterpret_cast<HeadCounts*>(ws + p.o_cnt);
   auto* idx = reinterpret_cast<int32_t*>(ws + p.o_idx);
-  auto* pos = reinterpret_cast<int32_t*>(ws + p.o_pos);
   auto* flag = reinterpret_cast<uint8_t*>(ws + p.o_flag);
   auto* ent = reinterpret_cast<int32_t*>(ws + p.o_ent);
   auto* ent_q = reinterpret_cast<float*>(ws + p.o_q);
-  auto* zt = reinterpret_cast<float*>(ws + p.o_zt);
   auto* pm = reinterpret_cast<float*>(ws + p.o_m);
   auto* ps = reinterpret_cast<float*>(ws + p.o_s);
   auto* ps2 = reinterpret_cast<float*>(ws + p.o_s2);
@@ -600,19 +627,16 @@ int launch_head(const LaunchCtx& ctx, const HeadPlan& p, const HeadArgs& a) {
   auto* sums = reinterpret_cast<float*>(ws + p.o_sum);
   auto* part = reinterpret_cast<float*>(ws + p.o_part);
   const bool bf = p.dtype == OCCULT_BF16;
-  // at most about 1024 blocks, each of which counts every token
-  const int per = static_cast<int>(up((p.T + 1023) / 1024, 32));
+  // at most about 1024 blocks, each of which counts every token; a warp or two for every
+  // row of entries
+  const int per = static_cast<int>(up((p.T + 1023) / 1024, p.K ? 8 : 32));
+  const int grad_size = p.grad_dtype == OCCULT_BF16 ? 2 : 4;
   cudaError_t e = launch_pdl(head_rows_kernel, (p.T + per - 1) / per, kRowThreads, 0, ctx.stream, a.labels,
-                             a.t_ids, p.T, p.V, p.K, per, cnt, idx, pos, flag, ent, ent_q, a.lse,
-                             a.token_loss, static_cast<const uint4*>(a.x),
-                             reinterpret_cast<uint4*>(ws + p.o_xc), p.d / (bf ? 8 : 4));
+                             a.t_ids, a.t_logits, p.T, p.V, p.K, 1.f / p.tau, per, cnt, idx, flag, ent, ent_q,
+                             a.lse, a.token_loss, static_cast<const uint4*>(a.x),
+                             reinterpret_cast<uint4*>(ws + p.o_xc), p.d / (bf ? 8 : 4),
+                             static_cast<char*>(a.dx), p.d * grad_size);
   if (e != cudaSuccess) return OCCULT_ERR_CUDA;
-  if (p.K) {
-    e = launch_pdl(head_entries_kernel, std::min((p.T + kEntWarps - 1) / kEntWarps, ctx.num_sms * 16),
-                   kEntWarps * 32, 0, ctx.stream, a.labels, a.t_ids, a.t_logits, cnt, idx, flag, p.V,
-                   p.K, 1.f / p.tau, ent, ent_q);
-    if (e != cudaSuccess) return OCCULT_ERR_CUDA;
-  }
   int n_blocks = 0;
   for (int i = 0; i < p.n_pieces; ++i)
     n_blocks += (std::min(p.piece, p.T - i * p.piece) + 31) / 32;
@@ -637,8 +661,6 @@ int launch_head(const LaunchCtx& ctx, const HeadPlan& p, const HeadArgs& a) {
     z.inv_tau = 1.f / p.tau; z.q_step = p.q_step; z.tau = p.tau;
     z.coef = p.coef; z.coef_kd = p.coef_kd; z.coef_z = p.coef_z;
     z.two = p.two;
-    const int eb = static_cast<int>(std::min<int64_t>((static_cast<int64_t>(rows) * p.E + 255) / 256,
-                                                      ctx.num_sms * 16));
     if (bf) {
       auto* kept = reinterpret_cast<uint16_t*>(ws + p.o_kept);
       // some eight blocks an SM, however many of the rows count
@@ -646,36 +668,32 @@ int launch_head(const LaunchCtx& ctx, const HeadPlan& p, const HeadArgs& a) {
       const dim3 grid(gx, std::min(row_blocks, std::max(1, (ctx.num_sms * 8 + gx - 1) / gx)));
       e = launch_pdl(head_dz_bf16_kernel, grid, 256, 0, ctx.stream, z, kept);
       if (e != cudaSuccess) return OCCULT_ERR_CUDA;
-      e = launch_pdl(head_dz_entries_kernel<__nv_bfloat16>, eb, 256, 0, ctx.stream, z, ent, ent_q, zt,
-                     p.E, reinterpret_cast<__nv_bfloat16*>(kept));
+      const int eb = static_cast<int>(std::min<int64_t>((static_cast<int64_t>(rows) * p.E + 255) / 256,
+                                                        ctx.num_sms * 16));
+      e = launch_pdl(head_dz_entries_kernel, eb, 256, 0, ctx.stream, z, head_loss_out(p, a),
+                     reinterpret_cast<__nv_bfloat16*>(kept));
     } else {
-      auto* kept = reinterpret_cast<float*>(ws + p.o_kept);
-      const dim3 grid(std::min((p.V + 255) / 256, 64), std::min(rows, 4096));
-      e = launch_pdl(head_dz_f32_kernel, grid, 256, 0, ctx.stream, z, kept);
-      if (e != cudaSuccess) return OCCULT_ERR_CUDA;
-      e = launch_pdl(head_dz_entries_kernel<float>, eb, 256, 0, ctx.stream, z, ent, ent_q, zt, p.E, kept);
+      e = launch_pdl(head_dz_f32_kernel, std::min(rows, ctx.num_sms * 8), 256, 0, ctx.stream, z,
+                     head_loss_out(p, a), reinterpret_cast<float*>(ws + p.o_kept));
     }
     if (e != cudaSuccess) return OCCULT_ERR_CUDA;
-    if (a.dx) {
-      rc = bf ? launch_head_dx_bf16(ctx, p, a, row0) : launch_head_dx_f32(ctx, p, a, row0);
-      if (rc) return rc;
-      const int tokens = p.T >= 4 * ctx.num_sms ? 4 : 1;
-      const int nb = std::min((p.T + tokens - 1) / tokens, ctx.num_sms * 8);
+    const bool first = i == 0, last = i == p.n_pieces - 1;
+    rc = bf ? launch_head_grads_bf16(ctx, p, a, row0, first, last)
+            : launch_head_grads_f32(ctx, p, a, row0, first, last);
+    if (rc) return rc;
+    const int splits = head_splits(p, a);
+    if (a.dx && (!bf || splits > 1)) {
+      const int tokens = rows >= 4 * ctx.num_sms ? 4 : 1;
+      const int nb = std::min((rows + tokens - 1) / tokens, ctx.num_sms * 8);
       const int threads = std::min(256, (p.d / 4 + 31) / 32 * 32);
       const size_t stride = static_cast<size_t>(p.piece) * p.d;
 #define OCCULT_HEAD_DX(O)                                                                          \
   launch_pdl(tokens == 4 ? head_dx_kernel<O, 4> : head_dx_kernel<O, 1>, nb, threads, 0, ctx.stream, \
-             cnt, pos, part, p.splits, stride, row0, p.piece, p.T, p.d, i == 0, p.coef, p.coef_kd, \
-             p.coef_z, p.tau, a.dloss, static_cast<O*>(a.dx))
+             cnt, idx, part, splits, stride, row0, p.piece, p.d, p.coef, p.coef_kd, p.coef_z,      \
+             p.tau, a.dloss, static_cast<O*>(a.dx))
       e = p.grad_dtype == OCCULT_BF16 ? OCCULT_HEAD_DX(__nv_bfloat16) : OCCULT_HEAD_DX(float);
 #undef OCCULT_HEAD_DX
       if (e != cudaSuccess) return OCCULT_ERR_CUDA;
-    }
-    if (a.dw) {
-      const bool first = i == 0, last = i == p.n_pieces - 1;
-      rc = bf ? launch_head_dw_bf16(ctx, p, a, row0, first, last)
-              : launch_head_dw_f32(ctx, p, a, row0, first, last);
-      if (rc) return rc;
     }
   }
   return OCCULT_OK;

@@ -33,11 +33,11 @@ struct HeadPlan {
   int ld;                   // columns of the kept logits
   int bn;                   // vocabulary columns of a tile
   int n_tiles, halves;      // tiles, and parts of a row's sums (bf16: two a tile)
-  int splits;               // parts of the reduction of dx
+  int splits, splits_alone; // parts of dx's reduction: beside dw, and without it
   float tau, coef, coef_kd, coef_z;
   float q_step;             // octaves of a unit of the kept 16-bit logits
   // workspace
-  size_t o_cnt, o_idx, o_pos, o_flag, o_ent, o_q, o_zt, o_xc, o_m, o_s, o_s2, o_l1, o_l2, o_sum,
+  size_t o_cnt, o_idx, o_flag, o_ent, o_q, o_zt, o_xc, o_m, o_s, o_s2, o_l1, o_l2, o_sum,
       o_kept, o_part, o_acc, total;
 };
 
@@ -155,17 +155,16 @@ int launch_head(const LaunchCtx& ctx, const HeadPlan& p, const HeadArgs& a);
 
 // Products of bf16 layers over the rows [row0, row0 + piece) of the compact rows.
 //  logits: partial maxima and sums, the logits of the entries, and (step) the logits in
-//          16 bits;  dx: parts [splits][piece][d] fp32;  dw: written (first piece) or
-//          added to, scaled.
+//          16 bits;  grads: dx (to its tokens' rows, or parts [splits][piece][d] fp32) and dw
+//          (written for the first piece, or added to), scaled.
 int launch_head_logits_bf16(const LaunchCtx& ctx, const HeadPlan& p, const HeadArgs& a, int row0);
-int launch_head_dx_bf16(const LaunchCtx& ctx, const HeadPlan& p, const HeadArgs& a, int row0);
-int launch_head_dw_bf16(const LaunchCtx& ctx, const HeadPlan& p, const HeadArgs& a, int row0,
-                        bool first, bool last);
+int launch_head_grads_bf16(const LaunchCtx& ctx, const HeadPlan& p, const HeadArgs& a, int row0,
+                           bool first, bool last);
+inline int head_splits(const HeadPlan& p, const HeadArgs& a) { return a.dw ? p.splits : p.splits_alone; }
 // The same of fp32 layers.
 int launch_head_logits_f32(const LaunchCtx& ctx, const HeadPlan& p, const HeadArgs& a, int row0);
-int launch_head_dx_f32(const LaunchCtx& ctx, const HeadPlan& p, const HeadArgs& a, int row0);
-int launch_head_dw_f32(const LaunchCtx& ctx, const HeadPlan& p, const HeadArgs& a, int row0,
-                       bool first, bool last);
+int launch_head_grads_f32(const LaunchCtx& ctx, const HeadPlan& p, const HeadArgs& a, int row0,
+                          bool first, bool last);
 
 // The loss of up to kHeadFewTokens tokens of a bf16 layer, from its rows and entries to its
 // outputs (head_few.cu); blocks that share the vocabulary.

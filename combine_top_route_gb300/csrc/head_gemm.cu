@@ -7,8 +7,10 @@
 //           keeps the logits in 16 bits: octaves below the part's maximum, in steps fine
 //           enough (3.7e-4 octaves at temperature 1) that a probability is within 1.3e-4
 //           of itself, a thirtieth of bf16's rounding of the gradient made from it.
-//   dx      dz w over the vocabulary, cut into parts where rows are few.
-//   dw      dz^T x over the rows.
+//   gradients  dx = dz w over the vocabulary (cut into parts where its tiles would not
+//           go round) and dw = dz^T x over the rows, the tiles of both in one launch: dx's
+//           first, dealt in turn, then dw's, of which pairs that got one dx tile less
+//           take as many more as that one's time.
 //
 // Persistent CTA pairs (tcgen05.mma.cta_group::2: a 256 x 256 tile, rows 0..127 in the
 // even CTA, half of the columns' operand in each) or, up to 128 rows, single CTAs with a
@@ -37,13 +39,13 @@ constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarps);
 constexpr int kLaunchRegs = 168, kCtrlRegs = 40, kEpiRegs = 232;   // a thread
 static_assert(32 * (kEpiWarp0 * kCtrlRegs + kEpiWarps * kEpiRegs) <= kThreads * kLaunchRegs, "registers");
 constexpr uint32_t kTmemCols = 512;
-constexpr int kMaxStages = 6;
+constexpr int kMaxStages = 8;
 
-enum : int { HEAD_STATS = 0, HEAD_KEEP = 1, HEAD_DX = 2, HEAD_DW = 3 };
+enum : int { HEAD_STATS = 0, HEAD_KEEP = 1, HEAD_GRADS = 2 };
 
-__host__ __device__ constexpr int n_stages(bool pair) { return pair ? 6 : 4; }
-__host__ __device__ constexpr int b_bytes(bool pair) { return pair ? 16384 : 32768; }
-__host__ __device__ constexpr int stage_bytes(bool pair) { return kABytes + b_bytes(pair); }
+// The ring: 192 KB in stages of A's 16 KB and as much of B as the tile has columns.
+constexpr int kRingBytes = 192 * 1024;
+constexpr int kPairStage = kABytes + BN / 2 * BK * 2;
 
 struct Tail {
   uint64_t full[kMaxStages], empty[kMaxStages], tfull[2], tempty[2];
@@ -52,15 +54,14 @@ struct Tail {
 };
 constexpr int kTailBytes = (static_cast<int>(sizeof(Tail)) + 127) & ~127;
 constexpr int kEpiBytes = kEpiWarps * 32 * 32 * 4;   // 4 KB a warp
-__host__ __device__ constexpr int smem_bytes(bool pair) {
-  return 1024 + n_stages(pair) * stage_bytes(pair) + kTailBytes + kEpiBytes;
-}
-static_assert(smem_bytes(true) <= 232448 && smem_bytes(false) <= 232448, "shared memory");
+constexpr int kSmemBytes = 1024 + kRingBytes + kTailBytes + kEpiBytes;
+static_assert(kSmemBytes <= 232448, "shared memory");
 
 struct GemmArgs {
   const HeadCounts* cnt;
   int T, row0, piece;     // tokens; the piece's first compact row and its rows
   int V, d, bn, n_tiles;  // vocabulary, width, columns of a tile, tiles
+  int stages, stage_bytes;   // of single CTAs
   // logits
   const int32_t* ent;
   float* zt;
@@ -69,12 +70,13 @@ struct GemmArgs {
   int ldp, ld;
   uint16_t* kept;
   float inv_tau, q_inv;
-  // dx, dw
-  int splits;
-  int seg;                // logits: k blocks added up in TMEM before they go to registers
+  int seg;                // k blocks added up in TMEM before they go to registers
+  // gradients
+  int splits;             // dx: parts; with one it is written to its tokens' rows
   float* part;
-  void* out;              // dw
-  float* acc;             // dw of earlier pieces in fp32 (nullptr: in `out`)
+  const int32_t* idx;
+  void *dx, *dw;          // either may be missing
+  float* acc;             // dw of earlier pieces in fp32 (nullptr: in dw)
   const float* dloss;
   float coef, coef_kd, coef_z, tau;
   int out_bf16, first, last;
@@ -87,44 +89,77 @@ struct Unit {
   int n0;      // first column of the tile
   int nt;      // its number
   int k0, k1;  // k blocks
-  int split;
+  int split;   // dx: part
+  bool dw;
 };
 
 // Logits: bands of 32 row tiles; inside one all row tiles of a column tile follow each
 // other, so that a weight tile is read once a band and the band's rows stay in L2.
 constexpr int kBand = 32;
 
+// What a tile costs besides its k blocks, in their time.
+constexpr int kTileCost = 5;
+
+// A launch's tiles, and the ones of a CTA (pair) `me` of `all`.
 template <int MODE, bool PAIR>
-__device__ __forceinline__ Unit unit_of(int u, const GemmArgs& p, int m_units, int rank, int kb_rows) {
-  constexpr int RM = PAIR ? 2 * BM : BM;
-  Unit t;
-  t.split = 0;
-  if (MODE == HEAD_STATS || MODE == HEAD_KEEP) {
-    const int band = u / (kBand * p.n_tiles);
-    const int in = u - band * (kBand * p.n_tiles);
-    const int rows = min(kBand, m_units - band * kBand);
-    t.nt = in / rows;
-    t.m0 = (band * kBand + in - t.nt * rows) * RM + rank * BM;
-    t.k0 = 0;
-    t.k1 = p.d / BK;
-  } else {
-    const int per = m_units * p.n_tiles;
-    t.split = MODE == HEAD_DX ? u / per : 0;
-    const int in = u - t.split * per;
-    t.nt = in % p.n_tiles;
-    t.m0 = in / p.n_tiles * RM + rank * BM;
-    if (MODE == HEAD_DX) {
-      const int kb = (p.V + BK - 1) / BK;
-      t.k0 = static_cast<int>(static_cast<int64_t>(kb) * t.split / p.splits);
-      t.k1 = static_cast<int>(static_cast<int64_t>(kb) * (t.split + 1) / p.splits);
-    } else {
-      t.k0 = 0;
-      t.k1 = kb_rows;
-    }
+struct Schedule {
+  static constexpr bool kLogits = MODE != HEAD_GRADS;
+  static constexpr int RM = PAIR ? 2 * BM : BM;
+  const GemmArgs& p;
+  int me, all, rank, m_units, kb_rows, n_first, n_second;   // logits or dx tiles; dw tiles
+  int firsts, rest, extra;
+
+  __device__ __forceinline__ Schedule(const GemmArgs& p_, int n, int me_, int all_, int rank_)
+      : p(p_), me(me_), all(all_), rank(rank_) {
+    m_units = (n + RM - 1) / RM;
+    kb_rows = (n + BK - 1) / BK;
+    n_first = kLogits || p.dx ? m_units * p.n_tiles * (kLogits ? 1 : p.splits) : 0;
+    n_second = !kLogits && p.dw ? (p.V + RM - 1) / RM * p.n_tiles : 0;
+    firsts = (n_first - me + all - 1) / all;
+    rest = n_first % all;
+    // dw tiles to the time of a dx tile
+    extra = rest ? ((p.V + BK - 1) / BK / p.splits + kTileCost) / (kb_rows + kTileCost) : 0;
   }
-  t.n0 = t.nt * p.bn;
-  return t;
-}
+  // The i-th tile's number, -1 behind the last.
+  __device__ __forceinline__ int at(int i) const {
+    if (i < firsts) return me + i * all;
+    if (kLogits) return -1;
+    const int j = i - firsts, more = rest ? all - rest : 0;
+    int64_t u;
+    if (me >= rest && j < extra && more) u = static_cast<int64_t>(j) * more + (me - rest);
+    else u = static_cast<int64_t>(more) * extra + static_cast<int64_t>(j - (more && me >= rest ? extra : 0)) * all + me;
+    return u < n_second ? n_first + static_cast<int>(u) : -1;
+  }
+  __device__ __forceinline__ Unit unit(int u) const {
+    Unit t;
+    t.split = 0;
+    t.k0 = 0;
+    t.dw = u >= n_first;
+    if (kLogits) {
+      const int band = u / (kBand * p.n_tiles);
+      const int in = u - band * (kBand * p.n_tiles);
+      const int rows = min(kBand, m_units - band * kBand);
+      t.nt = in / rows;
+      t.m0 = (band * kBand + in - t.nt * rows) * RM + rank * BM;
+      t.k1 = p.d / BK;
+    } else {
+      int in = u - (t.dw ? n_first : 0);
+      if (!t.dw) {
+        const int per = m_units * p.n_tiles, kb = (p.V + BK - 1) / BK;
+        t.split = in / per;
+        in -= t.split * per;
+        t.k0 = static_cast<int>(static_cast<int64_t>(kb) * t.split / p.splits);
+        t.k1 = static_cast<int>(static_cast<int64_t>(kb) * (t.split + 1) / p.splits);
+      } else {
+        t.k1 = kb_rows;
+      }
+      t.nt = in % p.n_tiles;
+      t.m0 = in / p.n_tiles * RM + rank * BM;
+    }
+    t.n0 = t.nt * p.bn;
+    return t;
+  }
+};
 
 template <bool MN>
 __device__ __forceinline__ uint64_t operand_desc(uint32_t base, int kk) {
@@ -166,22 +201,22 @@ __global__ void __launch_bounds__(kThreads, 1)
 head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmA2,
                  const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmB2,
                  const GemmArgs p) {
-  constexpr bool kLogits = MODE == HEAD_STATS || MODE == HEAD_KEEP;
-  constexpr bool kAMn = MODE == HEAD_DW, kBMn = !kLogits;
-  constexpr int kStages = n_stages(PAIR), kStageBytes = stage_bytes(PAIR);
+  constexpr bool kLogits = MODE != HEAD_GRADS;
   constexpr int RM = PAIR ? 2 * BM : BM;
+  // Pairs: six of 32 KB, known when compiled (a stage count of the launch's cost 3 % of the
+  // large products); single CTAs: as many of a narrow tile's as the ring holds.
+  const int kStages = PAIR ? kRingBytes / kPairStage : p.stages;
+  const int kStageBytes = PAIR ? kPairStage : p.stage_bytes;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  Tail* tail = reinterpret_cast<Tail*>(smem + kStages * kStageBytes);
+  Tail* tail = reinterpret_cast<Tail*>(smem + kRingBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = PAIR ? static_cast<int>(cluster_ctarank()) : 0;
   const bool leader = rank == 0;
-  const int unit0 = PAIR ? blockIdx.x >> 1 : blockIdx.x;
-  const int stride = PAIR ? gridDim.x >> 1 : gridDim.x;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) {
+    for (int s = 0; s < kMaxStages; ++s) {
       mbar_init(&tail->full[s], 1);
       mbar_init(&tail->empty[s], 1);
     }
@@ -205,9 +240,8 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
   const int n_all = p.cnt->n;
   const int n = max(0, min(n_all - p.row0, p.piece));   // rows of this piece
   const bool whole = n_all == p.T;   // every token counts: x is read where it lies
-  const int m_units = MODE == HEAD_DW ? (p.V + RM - 1) / RM : (n + RM - 1) / RM;
-  const int kb_rows = (n + BK - 1) / BK;
-  const int total = m_units * p.n_tiles * (MODE == HEAD_DX ? p.splits : 1);
+  const Schedule<MODE, PAIR> plan(p, n, PAIR ? blockIdx.x >> 1 : blockIdx.x, PAIR ? gridDim.x >> 1 : gridDim.x,
+                                  rank);
   const uint32_t tbase = tail->tmem_base;
   volatile int* abort_flag = &tail->abort_flag;
   const uint32_t full_lead = PAIR ? smem_addr_in_rank(&tail->full[0], 0) : 0u;
@@ -224,11 +258,16 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
       int stage = 0;
       uint32_t phase = 0;
       bool ok = true;
+      // logits: x or its compact copy, and w; gradients: dz for both (as it lies, 64 x 64
+      // boxes), and w or x
       const CUtensorMap* ma = kLogits && !whole ? &tmA2 : &tmA;
-      const CUtensorMap* mb = MODE == HEAD_DW && !whole ? &tmB2 : &tmB;
-      if (lane == 0) { prefetch_tmap(ma); prefetch_tmap(mb); }
-      for (int u = unit0; u < total && ok; u += stride) {
-        const Unit t = unit_of<MODE, PAIR>(u, p, m_units, rank, kb_rows);
+      const CUtensorMap* mx = whole ? &tmA2 : &tmB2;
+      if (lane == 0) { prefetch_tmap(ma); prefetch_tmap(&tmB); }
+      // Single CTAs all read the few rows of x there are: each begins at a k block of its
+      // own, or they would queue for the same lines (12 tokens x 2432 x 32366: 36 -> 34 us).
+      const int turn = static_cast<int>(static_cast<int64_t>(p.d / BK) * blockIdx.x / gridDim.x);
+      for (int i = 0, u; ok && (u = plan.at(i)) >= 0; ++i) {
+        const Unit t = plan.unit(u);
         const int bc = t.n0 + (PAIR ? rank * b_rows : 0);   // this CTA's first column
         for (int kb = t.k0; kb < t.k1; ++kb) {
           if (!mbar_wait(&tail->empty[stage], phase ^ 1u, abort_flag)) { ok = false; break; }
@@ -238,25 +277,23 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
             uint64_t* bar = &tail->full[stage];
             const uint32_t lbar = full_lead + stage * 8;
             if (leader) mbar_arrive_expect_tx(bar, PAIR ? 2 * cta_bytes : cta_bytes);
-            if (kAMn) {
-              for (int a = 0; a < BM / 64; ++a) {
-                if (PAIR) tma_load_2d_pair(sa + a * kMnAtom, ma, t.m0 + 64 * a, kb * BK, lbar);
-                else tma_load_2d(sa + a * kMnAtom, ma, t.m0 + 64 * a, kb * BK, bar);
+            if constexpr (kLogits) {
+              if (PAIR) {
+                tma_load_2d_pair(sa, ma, kb * BK, p.row0 + t.m0, lbar);
+                tma_load_2d_pair(sb, &tmB, kb * BK, bc, lbar);
+              } else {
+                const int at = kb + turn < t.k1 ? kb + turn : kb + turn - t.k1;
+                tma_load_2d(sa, ma, at * BK, p.row0 + t.m0, bar);
+                tma_load_2d(sb, &tmB, at * BK, bc, bar);
               }
             } else {
-              const int row = kLogits ? p.row0 + t.m0 : t.m0;
-              if (PAIR) tma_load_2d_pair(sa, ma, kb * BK, row, lbar);
-              else tma_load_2d(sa, ma, kb * BK, row, bar);
-            }
-            if (kBMn) {
-              const int krow = MODE == HEAD_DW ? p.row0 + kb * BK : kb * BK;
-              for (int a = 0; a < b_rows / 64; ++a) {
-                if (PAIR) tma_load_2d_pair(sb + a * kMnAtom, mb, bc + 64 * a, krow, lbar);
-                else tma_load_2d(sb + a * kMnAtom, mb, bc + 64 * a, krow, bar);
-              }
-            } else {
-              if (PAIR) tma_load_2d_pair(sb, mb, kb * BK, bc, lbar);
-              else tma_load_2d(sb, mb, kb * BK, bc, bar);
+              // (128 rows of 64 columns, or 64 rows of 128: two boxes either way)
+              for (int a = 0; a < 2; ++a)
+                tma_load_2d_pair(sa + a * kMnAtom, ma, t.dw ? t.m0 + 64 * a : kb * BK,
+                                 t.dw ? kb * BK : t.m0 + 64 * a, lbar);
+              for (int a = 0; a < b_rows / 64; ++a)
+                tma_load_2d_pair(sb + a * kMnAtom, t.dw ? mx : &tmB, bc + 64 * a,
+                                 kb * BK + (t.dw ? p.row0 : 0), lbar);
             }
           }
           __syncwarp();
@@ -279,12 +316,14 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
         int stage = 0, it = 0;
         uint32_t phase = 0;
         bool ok = true;
-        const uint32_t idesc = idesc_bf16_f32(RM, p.bn) | (kAMn ? 1u << 15 : 0u) | (kBMn ? 1u << 16 : 0u);
-        for (int u = unit0; u < total && ok; u += stride) {
-          const Unit t = unit_of<MODE, PAIR>(u, p, m_units, rank, kb_rows);
+        for (int i = 0, u; ok && (u = plan.at(i)) >= 0; ++i) {
+          const Unit t = plan.unit(u);
+          // bits 15 and 16: A (dw) and B (both gradients) lie along M and N
+          const uint32_t idesc = idesc_bf16_f32(RM, p.bn) | (t.dw && !kLogits ? 1u << 15 : 0u) |
+                                 (kLogits ? 0u : 1u << 16);
           int kb = t.k0;
           do {   // (a unit without k blocks still hands over its accumulator)
-            const int end = kLogits ? min(t.k1, kb + p.seg) : t.k1;
+            const int end = min(t.k1, p.seg < t.k1 - kb ? kb + p.seg : t.k1);
             const int a = it & 1;
             const uint32_t aph = (it >> 1) & 1;
             ++it;
@@ -300,8 +339,9 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
   #pragma unroll
               for (int kk = 0; kk < BK / 16; ++kk) {
                 const bool add = kb != first || kk != 0;
-                if (PAIR) tc_mma_f16_pair(acc, operand_desc<kAMn>(sa, kk), operand_desc<kBMn>(sb, kk), idesc, add);
-                else tc_mma_f16(acc, operand_desc<kAMn>(sa, kk), operand_desc<kBMn>(sb, kk), idesc, add);
+                const uint64_t da = !kLogits && t.dw ? operand_desc<true>(sa, kk) : operand_desc<false>(sa, kk);
+                if (PAIR) tc_mma_f16_pair(acc, da, operand_desc<!kLogits>(sb, kk), idesc, add);
+                else tc_mma_f16(acc, da, operand_desc<!kLogits>(sb, kk), idesc, add);
               }
               if (PAIR) tc_commit_pair(&tail->empty[stage], 0x3);
               else tc_commit(&tail->empty[stage]);
@@ -327,16 +367,16 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
     uint32_t* buf = reinterpret_cast<uint32_t*>(reinterpret_cast<uint8_t*>(tail) + kTailBytes) +
                     (warp - kEpiWarp0) * 1024;
     float g = 0.f;
-    if (MODE == HEAD_DW) {
+    if (!kLogits) {
       const HeadScale sc = head_scale(n_all, p.cnt->n_ce, p.cnt->n_kd, p.coef, p.coef_kd, p.coef_z, p.tau);
       g = sc.unit * (p.dloss ? *p.dloss : 1.f);
     }
     int it = 0;
     bool ok = true;
     const int hw = p.bn / 2;   // columns of this warp's half
-    for (int u = unit0; u < total && ok; u += stride) {
-      const Unit t = unit_of<MODE, PAIR>(u, p, m_units, rank, kb_rows);
-      const int rows_all = MODE == HEAD_DW ? p.V : n;
+    for (int i = 0, u; ok && (u = plan.at(i)) >= 0; ++i) {
+      const Unit t = plan.unit(u);
+      const int rows_all = !kLogits && t.dw ? p.V : n;
       const int valid = min(32, rows_all - t.m0 - quarter * 32);   // rows of this warp (may be < 1)
       const int c0 = t.n0 + half * hw;                             // its first column
       const int64_t row = t.m0 + quarter * 32 + lane;
@@ -475,71 +515,89 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
           if (TWO) p.ps2[at] = s2;
         }
       } else {
-        // dx: fp32 parts; dw: scaled, added to earlier pieces', in its type
+        // dx: its token's row, or an fp32 part; dw: added to earlier pieces', in its type
+        const int token = !t.dw && p.splits == 1 && lane < valid ? p.idx[p.row0 + row] : 0;
         if (!take()) { ok = false; break; }
         const uint32_t acc = lanes + a * BN;
         if (valid < 1) { release(); continue; }
         const bool none = t.k0 == t.k1;   // no products: the accumulator holds nothing
+        const bool parts = !t.dw && p.splits > 1;
+        float* sum = p.out_bf16 ? p.acc : static_cast<float*>(p.dw);
+        const bool to_sum = t.dw && (!p.out_bf16 || !p.last);
+        const bool adds = t.dw && (!p.first || to_sum);
         const int lim = min(hw, p.d - c0);
-        uint32_t v[32];
-        for (int c = 0; c < lim; c += 32) {
-          tmem_ld32(acc + c, v);
-          tmem_ld_wait();
-          if (none) {
+        if (p.out_bf16 && !parts && !adds) {
+          // the usual end: 64 columns of bf16 at a time
+          for (int c = 0; c < lim; c += 64) {
+            uint32_t v[64];
+            tmem_ld32(acc + c, v);
+            tmem_ld32(acc + c + 32, v + 32);
+            tmem_ld_wait();
 #pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = 0u;
-          }
-          if constexpr (MODE == HEAD_DX) {
-            float* out = p.part + (static_cast<int64_t>(t.split) * p.piece + t.m0 + quarter * 32) * p.d + c0 + c;
+            for (int j = 0; j < 8; ++j) {
+              float f[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-              *reinterpret_cast<uint4*>(own_piece(buf, j)) =
-                  make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-            flush_rows(buf, reinterpret_cast<char*>(out), static_cast<int64_t>(p.d) * 4, valid);
-          } else {
-  #pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(g * __uint_as_float(v[j]));
-            const int64_t at = (static_cast<int64_t>(t.m0) + quarter * 32) * p.d + c0 + c;
-            float* sum = p.out_bf16 ? p.acc : static_cast<float*>(p.out);
-            const bool to_sum = !p.out_bf16 || !p.last;
-            if (!p.first || to_sum) {
-              // the rows through shared memory, eight lanes each, added to what is there
-  #pragma unroll
-              for (int j = 0; j < 8; ++j)
-                *reinterpret_cast<uint4*>(own_piece(buf, j)) =
-                    make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-              __syncwarp();
-  #pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const int r = i * 4 + lane / 8, q = lane & 7;
-                if (r >= valid) continue;
-                float4 f = *reinterpret_cast<const float4*>(buf + r * 32 + 4 * (q ^ (r & 7)));
-                float4* dst = reinterpret_cast<float4*>(sum + at + static_cast<int64_t>(r) * p.d + 4 * q);
-                if (!p.first) {
-                  const float4 o = *dst;
-                  f.x += o.x; f.y += o.y; f.z += o.z; f.w += o.w;
-                }
-                if (to_sum) *dst = f;
-                else
-                  *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + at + static_cast<int64_t>(r) * p.d + 4 * q) =
-                      make_uint2(pack_bf16x2(f.x, f.y), pack_bf16x2(f.z, f.w));
-              }
-              __syncwarp();
+              for (int i8 = 0; i8 < 8; ++i8) f[i8] = none ? 0.f : g * __uint_as_float(v[8 * j + i8]);
+              *reinterpret_cast<uint4*>(own_piece(buf, j)) = pack16(f, __nv_bfloat16());
+            }
+            if (t.dw) {
+              flush_rows(buf, reinterpret_cast<char*>(static_cast<__nv_bfloat16*>(p.dw) +
+                                                      (static_cast<int64_t>(t.m0) + quarter * 32) * p.d + c0 + c),
+                         static_cast<int64_t>(p.d) * 2, valid);
               continue;
             }
-            // a single piece, bf16: 64 columns to a flush
-            const int j0 = (c & 32) ? 4 : 0;
-  #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              float f[8];
-  #pragma unroll
-              for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(v[8 * j + i]);
-              *reinterpret_cast<uint4*>(own_piece(buf, j0 + j)) = pack16(f, __nv_bfloat16());
+            __syncwarp();
+#pragma unroll
+            for (int it8 = 0; it8 < 8; ++it8) {
+              const int r = it8 * 4 + lane / 8, q = lane & 7;
+              const int to = __shfl_sync(0xffffffffu, token, r);
+              if (r < valid)
+                st_v4(static_cast<__nv_bfloat16*>(p.dx) + static_cast<int64_t>(to) * p.d + c0 + c + 8 * q,
+                      *reinterpret_cast<const uint4*>(buf + r * 32 + 4 * (q ^ (r & 7))));
             }
-            if (c & 32)
-              flush_rows(buf, reinterpret_cast<char*>(static_cast<__nv_bfloat16*>(p.out) + at - 32),
-                         static_cast<int64_t>(p.d) * 2, valid);
+            __syncwarp();
           }
+          release();
+          continue;
+        }
+        // fp32: 32 columns at a time through shared memory, eight lanes a row
+        for (int c = 0; c < lim; c += 32) {
+          uint32_t v[32];
+          tmem_ld32(acc + c, v);
+          tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            float f[4];
+#pragma unroll
+            for (int i4 = 0; i4 < 4; ++i4)
+              f[i4] = none ? 0.f : (parts ? 1.f : g) * __uint_as_float(v[4 * j + i4]);
+            *reinterpret_cast<uint4*>(own_piece(buf, j)) = pack16(f, 0.f);
+          }
+          __syncwarp();
+          const int64_t at = (static_cast<int64_t>(t.m0) + quarter * 32) * p.d + c0 + c;   // (dw, parts)
+#pragma unroll
+          for (int it8 = 0; it8 < 8; ++it8) {
+            const int r = it8 * 4 + lane / 8, q = lane & 7;
+            const int to = __shfl_sync(0xffffffffu, token, r);
+            if (r >= valid) continue;
+            float4 f = *reinterpret_cast<const float4*>(buf + r * 32 + 4 * (q ^ (r & 7)));
+            const int64_t mine = at + static_cast<int64_t>(r) * p.d + 4 * q;
+            if (parts) {
+              *reinterpret_cast<float4*>(p.part + static_cast<int64_t>(t.split) * p.piece * p.d + mine) = f;
+            } else if (!t.dw) {
+              *reinterpret_cast<float4*>(static_cast<float*>(p.dx) + static_cast<int64_t>(to) * p.d + c0 + c + 4 * q) = f;
+            } else {
+              if (!p.first) {
+                const float4 o = *reinterpret_cast<const float4*>(sum + mine);
+                f.x += o.x; f.y += o.y; f.z += o.z; f.w += o.w;
+              }
+              if (to_sum) *reinterpret_cast<float4*>(sum + mine) = f;
+              else
+                *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.dw) + mine) =
+                    make_uint2(pack_bf16x2(f.x, f.y), pack_bf16x2(f.z, f.w));
+            }
+          }
+          __syncwarp();
         }
         release();
       }
@@ -566,7 +624,7 @@ int launch_one(const LaunchCtx& ctx, const CUtensorMap& ma, const CUtensorMap& m
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute attr[2];
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem_bytes(PAIR);
+  cfg.dynamicSmemBytes = kSmemBytes;
   cfg.stream = ctx.stream;
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = PAIR ? 2 : 1;
@@ -579,8 +637,8 @@ int launch_one(const LaunchCtx& ctx, const CUtensorMap& ma, const CUtensorMap& m
   static cudaError_t err = cudaSuccess;
   static int n_pairs = 0;
   std::call_once(once, [&] {
-    err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes(PAIR));
-    if (err == cudaSuccess && (MODE == HEAD_STATS || MODE == HEAD_KEEP)) {
+    err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    if (err == cudaSuccess && MODE != HEAD_GRADS) {
       // the split of the registers adds up to a launch with this many: another count
       // (of another compiler) would leave warps waiting for theirs
       cudaFuncAttributes fa;
@@ -602,6 +660,7 @@ GemmArgs base_args(const LaunchCtx& ctx, const HeadPlan& p, const HeadArgs& a, i
   g.cnt = reinterpret_cast<const HeadCounts*>(a.ws + p.o_cnt);
   g.T = p.T; g.row0 = row0; g.piece = p.piece; g.V = p.V; g.d = p.d;
   g.E = p.E; g.ldp = p.piece; g.ld = p.ld;
+  g.idx = reinterpret_cast<const int32_t*>(a.ws + p.o_idx);
   g.ent = reinterpret_cast<const int32_t*>(a.ws + p.o_ent);
   g.zt = reinterpret_cast<float*>(a.ws + p.o_zt);
   g.pm = reinterpret_cast<float*>(a.ws + p.o_m);
@@ -609,11 +668,16 @@ GemmArgs base_args(const LaunchCtx& ctx, const HeadPlan& p, const HeadArgs& a, i
   g.ps2 = reinterpret_cast<float*>(a.ws + p.o_s2);
   g.kept = reinterpret_cast<uint16_t*>(a.ws + p.o_kept);
   g.inv_tau = 1.f / p.tau; g.q_inv = 1.f / p.q_step;
-  g.splits = p.splits;
   g.part = reinterpret_cast<float*>(a.ws + p.o_part);
   g.dloss = a.dloss; g.coef = p.coef; g.coef_kd = p.coef_kd; g.coef_z = p.coef_z; g.tau = p.tau;
   g.dev_err = ctx.dev_err;
   return g;
+}
+// Stages of single CTAs: A's rows and `b_rows` of B (multiples of 8, so that stages start on
+// 1024 bytes).
+void ring(GemmArgs& g, int b_rows) {
+  g.stage_bytes = kABytes + b_rows * BK * 2;
+  g.stages = std::min(kMaxStages, kRingBytes / g.stage_bytes);
 }
 // rows of the compact copy of x
 int64_t copy_rows(const HeadPlan& p) {
@@ -634,9 +698,10 @@ int launch_head_logits_bf16(const LaunchCtx& ctx, const HeadPlan& p, const HeadA
   GemmArgs g = base_args(ctx, p, a, row0);
   g.bn = p.bn;
   g.n_tiles = p.n_tiles;
-  // k blocks of 64 to a sum: 512 products where the tensor cores are the bound, 128 where
-  // the weights' stream is
-  g.seg = pair ? 8 : 2;
+  // 512 products to a sum in TMEM (with 128 the two accumulators' way to registers and back
+  // is what a small batch waits for: 11 tokens x 3008 x 3951 took 25 us)
+  g.seg = 8;
+  ring(g, p.bn);
 #define OCCULT_HEAD_LOGITS(MODE)                                                           \
   (pair ? (p.two ? launch_one<MODE, true, true>(ctx, mx, mc, mw, mw, g)                    \
                  : launch_one<MODE, true, false>(ctx, mx, mc, mw, mw, g))                  \
@@ -646,35 +711,26 @@ int launch_head_logits_bf16(const LaunchCtx& ctx, const HeadPlan& p, const HeadA
 #undef OCCULT_HEAD_LOGITS
 }
 
-int launch_head_dx_bf16(const LaunchCtx& ctx, const HeadPlan& p, const HeadArgs& a, int row0) {
-  const bool pair = paired(p);
-  CUtensorMap mz, mw;
-  int rc = tensor_map_bf16(&mz, a.ws + p.o_kept, p.piece, p.ld, BK, BM);
-  if (!rc) rc = tensor_map_bf16(&mw, a.w, p.V, p.d, 64, BK);
+int launch_head_grads_bf16(const LaunchCtx& ctx, const HeadPlan& p, const HeadArgs& a, int row0,
+                           bool first, bool last) {
+  CUtensorMap mz, mw, mx, mc;
+  int rc = tensor_map_bf16(&mz, a.ws + p.o_kept, p.piece, p.ld, 64, 64);
+  if (!rc) rc = tensor_map_bf16(&mw, a.w, p.V, p.d, 64, 64);
+  if (!rc) rc = tensor_map_bf16(&mx, a.x, p.T, p.d, 64, 64);
+  if (!rc) rc = tensor_map_bf16(&mc, a.ws + p.o_xc, copy_rows(p), p.d, 64, 64);
   if (rc) return rc;
   GemmArgs g = base_args(ctx, p, a, row0);
   g.bn = p.d <= 128 ? 128 : BN;
   g.n_tiles = (p.d + g.bn - 1) / g.bn;
-  return pair ? launch_one<HEAD_DX, true, false>(ctx, mz, mz, mw, mw, g)
-              : launch_one<HEAD_DX, false, false>(ctx, mz, mz, mw, mw, g);
-}
-
-int launch_head_dw_bf16(const LaunchCtx& ctx, const HeadPlan& p, const HeadArgs& a, int row0,
-                        bool first, bool last) {
-  CUtensorMap mz, mx, mc;
-  int rc = tensor_map_bf16(&mz, a.ws + p.o_kept, p.piece, p.ld, 64, BK);
-  if (!rc) rc = tensor_map_bf16(&mx, a.x, p.T, p.d, 64, BK);
-  if (!rc) rc = tensor_map_bf16(&mc, a.ws + p.o_xc, copy_rows(p), p.d, 64, BK);
-  if (rc) return rc;
-  GemmArgs g = base_args(ctx, p, a, row0);
-  g.bn = p.d <= 128 ? 128 : BN;
-  g.n_tiles = (p.d + g.bn - 1) / g.bn;
-  g.out = a.dw;
+  g.splits = head_splits(p, a);
+  g.seg = 1 << 30;
+  g.dx = a.dx;
+  g.dw = a.dw;
   g.acc = reinterpret_cast<float*>(a.ws + p.o_acc);
   g.out_bf16 = p.grad_dtype == OCCULT_BF16;
   g.first = first;
   g.last = last;
-  return launch_one<HEAD_DW, true, false>(ctx, mz, mz, mx, mc, g);
+  return launch_one<HEAD_GRADS, true, false>(ctx, mz, mx, mw, mc, g);
 }
 
 }  // namespace occult

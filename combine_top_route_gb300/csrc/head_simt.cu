@@ -16,14 +16,18 @@ namespace {
 
 constexpr int TK = 32;
 
-// acc[i][j] += sum_k a(ty + 16 i, k) b(tx + 16 j, k) over [k_lo, k_hi): the loaders give an
-// element or 0 outside.  A_K / B_K: the operand's rows run along k (its threads then read
+// A thread's rows (columns): two next to each other, 32 further on two more.
+template <int TS>
+__device__ __forceinline__ int spot(int t, int i) { return 2 * t + (i & 1) + 32 * (i >> 1); }
+
+// acc[i][j] += sum_k a(spot(ty, i), k) b(spot(tx, j), k) over [k_lo, k_hi): the loaders give
+// an element or 0 outside.  A_K / B_K: the operand's rows run along k (its threads then read
 // along k, else along m / n).
 template <int TS, bool A_K, bool B_K, typename LA, typename LB>
 __device__ __forceinline__ void tile_product(float (&acc)[TS / 16][TS / 16], int k_lo, int k_hi,
                                              LA a, LB b) {
   constexpr int V = TS / 16, PER = TS * TK / 256;
-  __shared__ float sa[TK][TS + 1], sb[TK][TS + 1];
+  __shared__ __align__(8) float sa[TK][TS + 2], sb[TK][TS + 2];
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   float ra[PER], rb[PER];
   auto fetch = [&](int k0) {
@@ -46,15 +50,20 @@ __device__ __forceinline__ void tile_product(float (&acc)[TS / 16][TS / 16], int
     }
     __syncthreads();
     if (k0 + TK < k_hi) fetch(k0 + TK);
-#pragma unroll
+    // (unrolled in part: a small call's time is the code's way in as much as its run)
+#pragma unroll 8
     for (int k = 0; k < TK; ++k) {
-      float fa[V], fb[V];
+      float2 fa[V / 2], fb[V / 2];
 #pragma unroll
-      for (int i = 0; i < V; ++i) { fa[i] = sa[k][ty + 16 * i]; fb[i] = sb[k][tx + 16 * i]; }
+      for (int i = 0; i < V / 2; ++i) {
+        fa[i] = *reinterpret_cast<const float2*>(&sa[k][2 * ty + 32 * i]);
+        fb[i] = *reinterpret_cast<const float2*>(&sb[k][2 * tx + 32 * i]);
+      }
 #pragma unroll
       for (int i = 0; i < V; ++i)
 #pragma unroll
-        for (int j = 0; j < V; ++j) acc[i][j] = fmaf(fa[i], fb[j], acc[i][j]);
+        for (int j = 0; j < V; ++j)
+          acc[i][j] = fmaf(i & 1 ? fa[i >> 1].y : fa[i >> 1].x, j & 1 ? fb[j >> 1].y : fb[j >> 1].x, acc[i][j]);
     }
     __syncthreads();
   }
@@ -98,7 +107,7 @@ __global__ void __launch_bounds__(256) head_logits_f32_kernel(const SimtArgs a) 
     for (int i = 0; i < V; ++i)
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        const int r = ty + 16 * i, c = tx + 16 * j;
+        const int r = spot<TS>(ty, i), c = spot<TS>(tx, j);
         s_z[r][c] = c0 + c < a.V ? acc[i][j] : NEG;
         if (a.kept && m0 + r < n && c0 + c < a.V) a.kept[static_cast<size_t>(m0 + r) * a.ld + c0 + c] = acc[i][j];
       }
@@ -134,65 +143,67 @@ __global__ void __launch_bounds__(256) head_logits_f32_kernel(const SimtArgs a) 
   }
 }
 
-// dx: parts [split][row][d] of the sum over the vocabulary (blockIdx.z).
+// dx: parts [split][row][d] of the sum over the vocabulary; tile `blk` of its launch's.
 template <int TS>
-__global__ void __launch_bounds__(256) head_dx_f32_kernel(const SimtArgs a) {
+__device__ __forceinline__ void dx_tile(const SimtArgs& a, int blk) {
   constexpr int V = TS / 16;
-  pdl_wait();
-  pdl_trigger();
   const int n = min(a.cnt->n - a.row0, a.piece);
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  const int c0 = blockIdx.x * TS, sp = blockIdx.z;
+  const int cols = (a.d + TS - 1) / TS;
+  const int sp = blk % a.splits, c0 = blk / a.splits % cols * TS, m0 = blk / a.splits / cols * TS;
+  if (m0 >= n) return;
   const int k_lo = static_cast<int>(static_cast<int64_t>(a.V) * sp / a.splits);
   const int k_hi = static_cast<int>(static_cast<int64_t>(a.V) * (sp + 1) / a.splits);
-  for (int m0 = blockIdx.y * TS; m0 < n; m0 += gridDim.y * TS) {
-    float acc[V][V] = {};
-    tile_product<TS, true, false>(
-        acc, k_lo, k_hi,
-        [&](int m, int k) { return m0 + m < n ? a.kept[static_cast<size_t>(m0 + m) * a.ld + k] : 0.f; },
-        [&](int c, int k) { return c0 + c < a.d ? a.w[static_cast<size_t>(k) * a.d + c0 + c] : 0.f; });
+  float acc[V][V] = {};
+  tile_product<TS, true, false>(
+      acc, k_lo, k_hi,
+      [&](int m, int k) { return m0 + m < n ? a.kept[static_cast<size_t>(m0 + m) * a.ld + k] : 0.f; },
+      [&](int c, int k) { return c0 + c < a.d ? a.w[static_cast<size_t>(k) * a.d + c0 + c] : 0.f; });
 #pragma unroll
-    for (int i = 0; i < V; ++i)
+  for (int i = 0; i < V; ++i)
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const int r = m0 + ty + 16 * i, c = c0 + tx + 16 * j;
-        if (r < n && c < a.d) a.part[(static_cast<size_t>(sp) * a.piece + r) * a.d + c] = acc[i][j];
-      }
-  }
+    for (int j = 0; j < V; ++j) {
+      const int r = m0 + spot<TS>(ty, i), c = c0 + spot<TS>(tx, j);
+      if (r < n && c < a.d) a.part[(static_cast<size_t>(sp) * a.piece + r) * a.d + c] = acc[i][j];
+    }
 }
 
 template <int TS>
-__global__ void __launch_bounds__(256) head_dw_f32_kernel(const SimtArgs a) {
+__device__ __forceinline__ void dw_tile(const SimtArgs& a, int blk) {
   constexpr int V = TS / 16;
-  pdl_wait();
-  pdl_trigger();
   const int n = max(0, min(a.cnt->n - a.row0, a.piece));
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  const int c0 = blockIdx.x * TS;
+  const int cols = (a.d + TS - 1) / TS, c0 = blk % cols * TS, m0 = blk / cols * TS;
   const HeadScale sc = head_scale(a.cnt->n, a.cnt->n_ce, a.cnt->n_kd, a.coef, a.coef_kd, a.coef_z, a.tau);
   const float g = sc.unit * (a.dloss ? *a.dloss : 1.f);
   const float* x = x_rows(a);
-  for (int m0 = blockIdx.y * TS; m0 < a.V; m0 += gridDim.y * TS) {
-    float acc[V][V] = {};
-    tile_product<TS, false, false>(
-        acc, 0, n,
-        [&](int m, int k) { return m0 + m < a.V ? a.kept[static_cast<size_t>(k) * a.ld + m0 + m] : 0.f; },
-        [&](int c, int k) {
-          return c0 + c < a.d ? x[static_cast<size_t>(k) * a.d + c0 + c] : 0.f;
-        });
-    float* sum = a.bf16 ? a.acc : static_cast<float*>(a.out);
+  float acc[V][V] = {};
+  tile_product<TS, false, false>(
+      acc, 0, n,
+      [&](int m, int k) { return m0 + m < a.V ? a.kept[static_cast<size_t>(k) * a.ld + m0 + m] : 0.f; },
+      [&](int c, int k) { return c0 + c < a.d ? x[static_cast<size_t>(k) * a.d + c0 + c] : 0.f; });
+  float* sum = a.bf16 ? a.acc : static_cast<float*>(a.out);
 #pragma unroll
-    for (int i = 0; i < V; ++i)
+  for (int i = 0; i < V; ++i)
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const int v = m0 + ty + 16 * i, c = c0 + tx + 16 * j;
-        if (v >= a.V || c >= a.d) continue;
-        const size_t at = static_cast<size_t>(v) * a.d + c;
-        const float f = g * acc[i][j] + (a.first ? 0.f : sum[at]);
-        if (a.bf16 && a.last) static_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(f);
-        else sum[at] = f;
-      }
-  }
+    for (int j = 0; j < V; ++j) {
+      const int v = m0 + spot<TS>(ty, i), c = c0 + spot<TS>(tx, j);
+      if (v >= a.V || c >= a.d) continue;
+      const size_t at = static_cast<size_t>(v) * a.d + c;
+      const float f = g * acc[i][j] + (a.first ? 0.f : sum[at]);
+      if (a.bf16 && a.last) static_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(f);
+      else sum[at] = f;
+    }
+}
+
+// The first `dx_blocks` blocks take a tile of dx each, the others one of dw.
+template <int TX, int TW>
+__global__ void __launch_bounds__(256) head_grads_f32_kernel(const SimtArgs a, int dx_blocks) {
+  pdl_wait();
+  pdl_trigger();
+  const int blk = blockIdx.x;
+  if (blk < dx_blocks) dx_tile<TX>(a, blk);
+  else dw_tile<TW>(a, blk - dx_blocks);
 }
 
 SimtArgs simt_args(const HeadPlan& p, const HeadArgs& a, int row0) {
@@ -213,7 +224,7 @@ SimtArgs simt_args(const HeadPlan& p, const HeadArgs& a, int row0) {
   g.part = reinterpret_cast<float*>(ws + p.o_part);
   g.acc = reinterpret_cast<float*>(ws + p.o_acc);
   g.row0 = row0; g.piece = p.piece; g.V = p.V; g.d = p.d; g.E = p.E; g.ld = p.ld;
-  g.halves = p.halves; g.splits = p.splits; g.two = p.two;
+  g.halves = p.halves; g.two = p.two;
   g.bf16 = p.grad_dtype == OCCULT_BF16;
   g.inv_tau = 1.f / p.tau; g.tau = p.tau;
   g.coef = p.coef; g.coef_kd = p.coef_kd; g.coef_z = p.coef_z;
@@ -231,24 +242,21 @@ int launch_head_logits_f32(const LaunchCtx& ctx, const HeadPlan& p, const HeadAr
                                 0, ctx.stream, g));
 }
 
-int launch_head_dx_f32(const LaunchCtx& ctx, const HeadPlan& p, const HeadArgs& a, int row0) {
-  const SimtArgs g = simt_args(p, a, row0);
-  const int ts = head_f32_tile(p.T, p.d);
-  const dim3 grid((p.d + ts - 1) / ts, tiles(std::min(p.piece, p.T - row0), ts, 1024), p.splits);
-  return cuda_status(launch_pdl(ts == 32 ? head_dx_f32_kernel<32> : head_dx_f32_kernel<64>, grid, 256, 0,
-                                ctx.stream, g));
-}
-
-int launch_head_dw_f32(const LaunchCtx& ctx, const HeadPlan& p, const HeadArgs& a, int row0,
-                       bool first, bool last) {
+int launch_head_grads_f32(const LaunchCtx& ctx, const HeadPlan& p, const HeadArgs& a, int row0,
+                          bool first, bool last) {
   SimtArgs g = simt_args(p, a, row0);
   g.out = a.dw;
   g.first = first;
   g.last = last;
-  const int ts = head_f32_tile(p.V, p.d);
-  const dim3 grid((p.d + ts - 1) / ts, tiles(p.V, ts, 4096));
-  return cuda_status(launch_pdl(ts == 32 ? head_dw_f32_kernel<32> : head_dw_f32_kernel<64>, grid, 256, 0,
-                                ctx.stream, g));
+  g.splits = head_splits(p, a);
+  const auto count = [](int64_t n, int ts) { return (n + ts - 1) / ts; };
+  const int tx = head_f32_tile(p.T, p.d), tw = head_f32_tile(p.V, p.d);
+  const int64_t dx = a.dx ? count(std::min(p.piece, p.T - row0), tx) * count(p.d, tx) * g.splits : 0;
+  const int64_t dw = a.dw ? count(p.V, tw) * count(p.d, tw) : 0;
+  if (dx + dw >= (1ll << 31)) return OCCULT_ERR_UNSUPPORTED;
+  auto* kern = tx == 32 ? (tw == 32 ? head_grads_f32_kernel<32, 32> : head_grads_f32_kernel<32, 64>)
+                        : (tw == 32 ? head_grads_f32_kernel<64, 32> : head_grads_f32_kernel<64, 64>);
+  return cuda_status(launch_pdl(kern, static_cast<unsigned>(dx + dw), 256, 0, ctx.stream, g, static_cast<int>(dx)));
 }
 
 }  // namespace occult

@@ -261,11 +261,14 @@ __device__ __forceinline__ void draw(uint32_t (&key)[PL], int j, uint32_t& mine)
 
 // Places too near to each other for their words: more of them until one is clearly lower,
 // then in order by logits, or by fp64 ranks where there is a bias.  False: the whole
-// choice has to be made in fp64.
+// choice has to be made in fp64.  A softmax's ranks are made with the total in fp32, which
+// is within 2^-19 of itself and errs for all of them alike: it moves the difference of two
+// ranks by no more than that of the difference of their scores; two that are nearer than
+// this need the total in fp64, and with it every expert.
 template <bool SIG, bool BIAS, int PL>
 __device__ __noinline__ bool order_near(uint32_t (&key)[PL], uint32_t mine, int have, int k, int Ne,
                                         uint32_t gap_max, const float* row, const float* s_bias,
-                                        int& my_id) {
+                                        float top, float total, int& my_id) {
   const int lane = threadIdx.x & 31;
   float z = mine >= kOn ? row[my_id] : 0.f;
   {
@@ -277,7 +280,6 @@ __device__ __noinline__ bool order_near(uint32_t (&key)[PL], uint32_t mine, int 
                                (mine >> 8) - (nxt >> 8) <= gap_max && !(z == nz && b == nb)))
       return true;
   }
-  if (BIAS && !SIG) return false;   // a softmax's total in fp64 takes every expert
   for (;;) {
     const uint32_t last = __shfl_sync(kFull, mine, have - 1), prev = __shfl_sync(kFull, mine, have - 2);
     if (last < kOn || (prev >> 8) - (last >> 8) > gap_max || have == Ne) break;
@@ -287,17 +289,38 @@ __device__ __noinline__ bool order_near(uint32_t (&key)[PL], uint32_t mine, int 
   my_id = 255 - static_cast<int>(mine & 255u);
   const bool on = lane < have && mine >= kOn;
   uint64_t r = 0;   // above 0 for places that are on: they stand before the others
+  double v = 0.;
+  float p = 0.f;    // a softmax's score
   if (on) {
     z = row[my_id];
-    r = BIAS ? order_bits64(1. / (1. + exp(-static_cast<double>(z))) + static_cast<double>(s_bias[my_id]))
-             : static_cast<uint64_t>(order_bits(z)) + 1;
+    if (BIAS) {
+      if (SIG) {
+        v = 1. / (1. + exp(-static_cast<double>(z)));
+      } else {
+        v = exp(static_cast<double>(z) - static_cast<double>(top)) * (1. / static_cast<double>(total));
+        p = static_cast<float>(v);
+      }
+      v += static_cast<double>(s_bias[my_id]);
+      r = order_bits64(v);
+    } else {
+      r = static_cast<uint64_t>(order_bits(z)) + 1;
+    }
   }
   int place = on ? 0 : lane;
+  bool unsure = false;
   for (int j = 0; j < have; ++j) {
     const uint64_t o = shfl64(r, j);
     const int e = __shfl_sync(kFull, my_id, j);
     if (on && (o > r || (o == r && e < my_id))) ++place;
+    if (BIAS && !SIG) {
+      const float gap = fabsf(static_cast<float>(__shfl_sync(kFull, v, j) - v));
+      const float dp = fabsf(__shfl_sync(kFull, p, j) - p);
+      const bool there = __shfl_sync(kFull, static_cast<int>(on), j) != 0;
+      // (scores of one logit are equal, whatever the total)
+      unsure |= on && there && dp > 0.f && gap <= 0x1p-19f * dp + 0x1p-50f;
+    }
   }
+  if (BIAS && !SIG && __any_sync(kFull, unsure)) return false;
   int sorted = my_id;
   for (int j = 0; j < have; ++j) {
     const int at = __shfl_sync(kFull, place, j), e = __shfl_sync(kFull, my_id, j);
@@ -517,7 +540,8 @@ route_scored_kernel(const RouteArgs a) {
       const uint32_t nxt = __shfl_down_sync(kFull, mine, 1);
       if (__any_sync(kFull, lane < a.k && lane < 31 && mine >= kOn && nxt >= kOn &&
                                 (mine >> 8) - (nxt >> 8) <= gap_max))
-        exact = !order_near<SIG, BIAS, PL>(key, mine, rounds, a.k, a.Ne, gap_max, row, s_bias, my_id);
+        exact = !order_near<SIG, BIAS, PL>(key, mine, rounds, a.k, a.Ne, gap_max, row, s_bias, top,
+                                             total, my_id);
     }
     if (exact) my_id = choose_exactly<SIG, PL>(a, row, s_exp);
     if (my_id < 0 || my_id >= a.Ne) my_id = 0;   // (devices that do not share the experts evenly)
