@@ -1063,8 +1063,11 @@ static int check_head(const occult_desc_t* desc, const occult_head_t* opt) {
   OCCULT_REQUIRE(opt->coef >= 0.f && opt->coef < 1e30f && opt->coef_kd >= 0.f &&
                  opt->coef_kd < 1e30f && opt->coef_z >= 0.f && opt->coef_z < 1e30f);
   OCCULT_REQUIRE(opt->topk == 0 || (opt->temperature >= 0.25f && opt->temperature <= 10.f));
-  if (opt->topk > OCCULT_MAX_TEACHER || desc->d > 16384 || opt->vocab > (1 << 28))
+  if (opt->topk > OCCULT_MAX_TEACHER || desc->d > 16384 || opt->vocab > (1 << 28) ||
+      desc->T > (1 << 30))
     return OCCULT_ERR_UNSUPPORTED;
+  // tiles are numbered in 32 bits
+  if ((desc->T / 32 + 1ll) * (opt->vocab / 32 + 1ll) >= (1ll << 31)) return OCCULT_ERR_UNSUPPORTED;
   return static_cast<int64_t>(desc->T) * (opt->topk + 1) < (1ll << 31) ? OCCULT_OK
                                                                        : OCCULT_ERR_UNSUPPORTED;
 }

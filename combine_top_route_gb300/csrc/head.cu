@@ -579,7 +579,11 @@ HeadPlan head_plan(const occult_desc_t& ds, const occult_head_t& opt, bool step)
   int64_t piece = opt.piece > 0 ? opt.piece : (int64_t(1) << 30) / row_bytes;
   piece = std::min<int64_t>(1 << 20, piece);
   piece = std::max<int64_t>(kHeadRowAlign, piece / kHeadRowAlign * kHeadRowAlign);
-  p.piece = step ? static_cast<int>(std::min<int64_t>(piece, Tr)) : Tr;
+  // (without gradients a piece is what keeps the parts of the sums within some 512 MB, in
+  // whole bands of the product's rows)
+  if (!step)
+    piece = std::max<int64_t>(8192, (int64_t(1) << 29) / (12 * ((p.V + (bf ? 127 : 31)) / (bf ? 128 : 32))) / 8192 * 8192);
+  p.piece = static_cast<int>(std::min<int64_t>(piece, Tr));
   p.n_pieces = (Tr + p.piece - 1) / p.piece;
   // (the gradient of the logits is put together in parts of 128 columns)
   const int rows = std::min(p.piece, std::max(1, ds.T));

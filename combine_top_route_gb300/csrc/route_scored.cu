@@ -407,7 +407,8 @@ route_scored_kernel(const RouteArgs a) {
   const int my_group = lane >> a.group_shift;
   const int rounds = min(min(a.k + 1, a.Ne), 32);
 
-  for (int t = blockIdx.x * kWarps + warp; t < a.T; t += gridDim.x * kWarps) {
+  // (unsigned: the last step may pass 2^31)
+  for (uint32_t t = blockIdx.x * kWarps + warp; t < static_cast<uint32_t>(a.T); t += gridDim.x * kWarps) {
     const float* row = a.logits + static_cast<size_t>(t) * a.Ne;
     float z[PL];
     if (PL % 4 == 0 && a.vec) {
@@ -590,7 +591,7 @@ route_scored_grad_kernel(const float* __restrict__ logits, const int32_t* __rest
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   float* sm = s_row[warp];
-  for (int t = blockIdx.x * kWarps + warp; t < T; t += gridDim.x * kWarps) {
+  for (uint32_t t = blockIdx.x * kWarps + warp; t < static_cast<uint32_t>(T); t += gridDim.x * kWarps) {
     const float* row = logits + static_cast<size_t>(t) * Ne;
     float z[PL];
     float top = 0.f, total = 1.f;
@@ -650,7 +651,7 @@ bias_step_kernel(const int32_t* __restrict__ counts, int G, int Ne, float rate,
 }
 
 int blocks_for(const LaunchCtx& ctx, int T, int per_sm) {
-  const int blocks = (T + kWarps - 1) / kWarps;
+  const int blocks = (T - 1) / kWarps + 1;
   return blocks < ctx.num_sms * per_sm ? blocks : ctx.num_sms * per_sm;
 }
 

@@ -956,8 +956,9 @@ int occult_head_workspace_size(const occult_desc_t* desc, const occult_head_t* o
  *   ws      occult_head_workspace_size bytes.
  * Rows of x that neither term counts are not used and may hold anything.  Sums run in a
  * fixed order.  bf16 heads run on the tensor cores (fp32 accumulation).  Pointers are
- * 16-byte aligned; labels, teacher_*, loss, lse, token_loss and dloss 4-byte.  d <= 16384,
- * T * (K + 1) < 2^31.
+ * 16-byte aligned; labels, teacher_*, loss, lse, token_loss and dloss 4-byte.  No output
+ * overlaps an input.  d <= 16384, V <= 2^28, T <= 2^30, T * (K + 1) < 2^31 and
+ * (T / 32 + 1) * (V / 32 + 1) < 2^31.
  */
 int occult_head_loss(const occult_desc_t* desc, const occult_head_t* opt, const void* x,
                      const void* w, const int32_t* labels, const int32_t* teacher_ids,

@@ -158,6 +158,9 @@ def test_head_refuses_what_it_does_not_run(occ):
     assert head(occ, True, opt=occ.occult_head_t(vocab=1 << 29)) == UNSUPPORTED
     assert head(occ, True, ds=desc(occ, d=16448)) == UNSUPPORTED
     assert head(occ, False, ds=desc(occ, d=2050)) == UNSUPPORTED
+    few = dict(n_experts=1, top_k=1, n_vdev=1)
+    assert head(occ, False, ds=desc(occ, T=(1 << 30) + 1, **few)) == UNSUPPORTED
+    assert head(occ, False, ds=desc(occ, T=1 << 24, **few), opt=occ.occult_head_t(vocab=1 << 17)) == UNSUPPORTED
     assert head(occ, True, ds=desc(occ, T=1 << 25, n_experts=8, top_k=2),
                 opt=occ.occult_head_t(vocab=1000, topk=100), t_ids=V, t_logits=V) == UNSUPPORTED
 

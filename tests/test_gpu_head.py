@@ -384,3 +384,93 @@ def test_scoring_few_tokens(occ, T, d, V, K, tau):
     if K:
         ids[:, 0] = -1
     check(occ, c, step=False, tau=tau, coef=0.6, coef_kd=0.4)
+
+
+def test_losses_in_pieces(occ):
+    """More parts of sums than a workspace of half a GiB holds: the loss goes in pieces."""
+    T, d, V = 9000, 64, 750_000
+    g = torch.Generator(device="cuda").manual_seed(5)
+    w = (1.5 / 8 * torch.randn(V, d, generator=g, device="cuda")).bfloat16()
+    x = torch.randn(T, d, generator=g, device="cuda").bfloat16()
+    labels = torch.randint(0, V, (T,), generator=g, device="cuda").int()
+    ds = occ.desc_for(synth.CONFIGS["olmoe_fwd"].with_(T=T, d=d))
+    opt = occ.occult_head_t(vocab=V)
+    need = occ.head_workspace_size(ds, opt, step=False)
+    assert need < 1 << 30
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    loss, lse, token = (torch.full((n,), SENTINEL, device="cuda") for n in (4, T, T))
+    occ.occult_head_loss(ds, opt, x, w, loss, ws, labels=labels, lse=lse, token_loss=token)
+    some = torch.cat([torch.arange(0, T, 211), torch.arange(8160, 8230)]).cuda()
+    z = x[some].double() @ w.double().t()
+    want = torch.logsumexp(z, dim=1)
+    # logits of 64 products: ez = (64 / 16 + 8) 2 u a, a < 64 * 4 * 1.2, and 300 u of the sum
+    tol = 12 * 2 * U * 64 * 4 * 1.2 + 300 * U + 4 * U * 20
+    assert ((lse[some].double() - want).abs() < tol).all()
+    at = z.gather(1, labels[some].long()[:, None])[:, 0]
+    assert ((token[some].double() - (want - at)).abs() < 2 * tol).all()
+    assert abs(float(loss[1]) - float(token.double().mean())) < 1e-5 * float(loss[1])
+    assert abs(float(loss[3]) - float(lse.double().square().mean())) < 1e-5 * float(loss[3])
+
+
+def test_two_streams_at_once(occ):
+    """Two steps over workspaces of their own, on two streams at the same time."""
+    T, d, V = 600, 256, 4000
+    cs = [case(T, d, V, K=5, ignored=0.2, seed=s) for s in (1, 2)]
+    kw = dict(tau=2.0, coef=0.5, coef_kd=0.5)
+    want = [run(occ, *c, **kw) for c in cs]
+    ds = occ.desc_for(synth.CONFIGS["olmoe_fwd"].with_(T=T, d=d))
+    opt = occ.occult_head_t(vocab=V, topk=5, coef=0.5, coef_kd=0.5, temperature=2.0)
+    streams = [torch.cuda.Stream() for _ in cs]
+    args = [dict(x=gpu(c[0], torch.bfloat16), w=gpu(c[1], torch.bfloat16), labels=gpu(c[2]), teacher_ids=gpu(c[3]),
+                 teacher_logits=gpu(c[4]), loss=torch.empty(4, device="cuda"),
+                 ws=torch.empty(occ.head_workspace_size(ds, opt), dtype=torch.uint8, device="cuda"),
+                 dx=torch.empty(T * d, device="cuda"), dw=torch.empty(V * d, device="cuda")) for c in cs]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for s, a in zip(streams, args):
+            occ.occult_head_step(ds, opt, stream=s, **a)
+    torch.cuda.synchronize()
+    for a, w in zip(args, want):
+        assert (a["dx"].view(T, d).double().cpu().numpy() == w["dx"]).all()
+        assert (a["dw"].view(V, d).double().cpu().numpy() == w["dw"]).all()
+
+
+_CAPTURE = """
+import sys, torch
+sys.path.insert(0, {root!r})
+import combine_top_route_gb300 as occ, synth
+T, d, V = {T}, 128, 1000
+ds = occ.desc_for(synth.CONFIGS["olmoe_fwd"].with_(T=T, d=d))
+opt = occ.occult_head_t(vocab=V)
+need = max(occ.head_workspace_size(ds, opt, step=b) for b in (True, False))
+ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+x, w = torch.randn(T, d, device="cuda").bfloat16(), torch.randn(V, d, device="cuda").bfloat16()
+labels = torch.arange(T, device="cuda").int()
+loss, dx, dw = torch.empty(2, 4, device="cuda"), torch.empty(T, d, device="cuda"), torch.empty(V, d, device="cuda")
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    occ.occult_head_step(ds, opt, x, w, loss[0], ws, dx=dx, dw=dw, labels=labels)
+    occ.occult_head_loss(ds, opt, x, w, loss[1], ws, labels=labels)
+g.replay()
+torch.cuda.synchronize()
+a = loss.clone()
+occ.occult_head_step(ds, opt, x, w, loss[0], ws, dx=dx, dw=dw, labels=labels)
+occ.occult_head_loss(ds, opt, x, w, loss[1], ws, labels=labels)
+torch.cuda.synchronize()
+assert torch.equal(a, loss) and torch.isfinite(a).all() and abs(float(a[0, 1] - a[1, 1])) < 1e-4, (a, loss)
+assert occ.device_error() == 0
+print("captured")
+"""
+
+
+@pytest.mark.parametrize("T", [2, 300])
+def test_the_first_call_may_be_captured(occ, T):
+    """A process whose first call of the head is into a graph."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    out = subprocess.run([sys.executable, "-c", _CAPTURE.format(root=root, T=T)], capture_output=True, text=True,
+                         timeout=300)
+    assert out.returncode == 0 and "captured" in out.stdout, out.stderr[-2000:]

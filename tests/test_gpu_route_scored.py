@@ -313,3 +313,23 @@ def test_the_layer_takes_the_routing(occ):
     assert c[1] == T * k and c[2] <= 3
     per = np.bincount(ids.cpu().numpy().ravel(), minlength=Ne)[placement.ravel()]
     assert (np.diff(exp_off.cpu().numpy()) == per).all()
+
+
+@pytest.mark.parametrize("sigmoid", [True, False])
+def test_more_tokens_than_warps(occ, sigmoid):
+    z = logits_of(20011, 32, 1)
+    bias = (np.random.default_rng(3).normal(size=32) * 0.1).astype(np.float32)
+    check(occ, z, 4, 4, bias, sigmoid=sigmoid, n_groups=4, keep=2, best=2)
+    e2v, kw = place(32, 4), dict(sigmoid=sigmoid, scale=1.0, renorm=True)
+    ids = scored.route(z, 4, e2v, **kw)[0].astype(np.int32)
+    dg = np.random.default_rng(5).normal(size=(20011, 4)).astype(np.float32)
+    ds, opt = setup(occ, z, 4, 4, **kw)
+    out = torch.full((20011 * 32,), float(SENTINEL), device="cuda")
+    occ.occult_route_scored_grad(ds, opt, gpu(z), gpu(ids, torch.int32), gpu(dg), out)
+    want = scored.grad(z, ids, dg, **kw)
+    got = out.view(20011, 32).double().cpu().numpy()
+    # (see test_grad: at most twice the largest |dgate| over a sum of four scores)
+    s = np.array([scored.scores(r, sigmoid)[0] for r in z])
+    S = np.take_along_axis(s, ids.astype(np.int64), 1).sum(axis=1)
+    err = (6 * score_err(z) + 60 * U) * (2 * np.abs(dg).max(axis=1) / S)[:, None] * s * 2 + 1e-36
+    assert (np.abs(got - want) <= err).all()
