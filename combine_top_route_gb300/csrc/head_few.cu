@@ -3,9 +3,12 @@
 // at the copy rate), and the fp32 units keep up with it: no tensor core tile would be
 // more than a thirty-second full.
 //
-// A block has a run of vocabulary rows, which come in as bulk copies of some 64 KB through
-// a ring in shared memory (one thread asks for them, from before the launch ahead is done:
-// nothing ahead of that one is still running).  A warp takes two rows of a stage at a
+// A block has a run of vocabulary rows, which come in as bulk copies, a row each, through a
+// ring of 64 KB stages in shared memory (one warp asks for them, from before the launch
+// ahead is done: nothing ahead of that one is still running).  The case above takes 40 us
+// with its rows' launch, as long as any read of 206 MB here (a plain sum of as many bytes
+// 40 us; of 4.3 GB at 6.6 TB/s); four rows a warp straight to registers took 47 us, a
+// stage in one copy 41, a ring for each warp 41.  A warp takes two rows of a stage at a
 // time, a lane 16 bytes of each per step; products are added in fp32 in 32 sums, joined over
 // the lanes, so that a warp knows its rows' logits and keeps a maximum and a sum of powers
 // of two for each token.  The entries' logits are products of their own, a warp each, so
@@ -109,11 +112,12 @@ __global__ void __launch_bounds__(kThreads, 1) head_few_kernel(const FewArgs a) 
     uint32_t phase = 0;
     for (int v = v0; v < v1; v += a.rows) {
       if (!mbar_wait(&tail.empty[stage], phase ^ 1u, abort_flag)) { ok = false; break; }
-      if (lane == 0) {
-        const uint32_t bytes = static_cast<uint32_t>(min(a.rows, v1 - v)) * row_bytes;
-        mbar_arrive_expect_tx(&tail.full[stage], bytes);
-        bulk_load(ring + stage * stage_bytes, a.w + static_cast<size_t>(v) * a.d, bytes, &tail.full[stage]);
-      }
+      const int rows = min(a.rows, v1 - v);
+      if (lane == 0) mbar_arrive_expect_tx(&tail.full[stage], static_cast<uint32_t>(rows) * row_bytes);
+      __syncwarp();
+      for (int r = lane; r < rows; r += 32)
+        bulk_load(ring + stage * stage_bytes + r * row_bytes, a.w + static_cast<size_t>(v + r) * a.d, row_bytes,
+                  &tail.full[stage]);
       __syncwarp();
       if (++stage == a.stages) { stage = 0; phase ^= 1u; }
     }
