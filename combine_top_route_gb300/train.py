@@ -218,7 +218,11 @@ class OccultBlock:
 
 
 class OccultHead:
-    """The end of a model: the last norm, the product with the vocabulary and its losses."""
+    """The end of a model: the last norm, the product with the vocabulary and its losses.
+
+    Every row of the residual stream must be finite, those that no term counts as well: the
+    norm's weight sums over all of them (a row that counts nowhere adds 0 times its norm).
+    """
 
     def __init__(self, desc: occult_desc_t, w_head: torch.Tensor, device="cuda", eps: float = 1e-6,
                  res_dtype=torch.bfloat16, topk: int = 0, coef: float = 1.0, coef_kd: float = 0.0,

@@ -955,7 +955,8 @@ int occult_head_workspace_size(const occult_desc_t* desc, const occult_head_t* o
  *           ignored.
  *   ws      occult_head_workspace_size bytes.
  * Rows of x that neither term counts are not used and may hold anything.  Sums run in a
- * fixed order.  bf16 heads run on the tensor cores (fp32 accumulation).  Pointers are
+ * fixed order.  bf16 heads run on the tensor cores (fp32 accumulation; the loss of up to
+ * four tokens on the fp32 units).  Pointers are
  * 16-byte aligned; labels, teacher_*, loss, lse, token_loss and dloss 4-byte.  No output
  * overlaps an input.  d <= 16384, V <= 2^28, T <= 2^30, T * (K + 1) < 2^31 and
  * (T / 32 + 1) * (V / 32 + 1) < 2^31.
