@@ -215,7 +215,8 @@ __global__ void __launch_bounds__(kSumWarps * 32)
 head_sum_kernel(HeadCounts* cnt, const HeadLossOut o, const float* __restrict__ pm,
                 const float* __restrict__ ps, const float* __restrict__ ps2, int ldp, int halves, int row0,
                 int rows_max, const int32_t* __restrict__ idx, const uint8_t* __restrict__ flag,
-                float* __restrict__ l1, float* __restrict__ l2, float* __restrict__ sums, int block0,
+                float* __restrict__ tops, float* __restrict__ l1, float* __restrict__ l2,
+                float* __restrict__ sums, int block0,
                 int n_blocks) {
   __shared__ float s_m[kSumWarps][33], s_s[kSumWarps][33], s_s2[kSumWarps][33];
   __shared__ float s_ce[32], s_kd[32], s_z[32];
@@ -266,13 +267,11 @@ head_sum_kernel(HeadCounts* cnt, const HeadLossOut o, const float* __restrict__ 
     const float m = lane < kSumWarps ? s_m[lane][own] : NEG;
     const float top = warp_max(m);
     const float safe = top == NEG ? 0.f : top;
-    const float L = safe + log2f(warp_sum(lane < kSumWarps ? s_s[lane][own] * ex2(m - safe) : 0.f));
-    float L2 = L;
-    if (TWO)
-      L2 = safe * inv_tau +
-           log2f(warp_sum(lane < kSumWarps ? s_s2[lane][own] * ex2((m - safe) * inv_tau) : 0.f));
-    if (lane == 0) { l1[r] = L; l2[r] = L2; }
-    row_losses(o, r, flag[r], idx[r], L, L2, inv_tau, mine);
+    const float a = log2f(warp_sum(lane < kSumWarps ? s_s[lane][own] * ex2(m - safe) : 0.f));
+    float b = a;
+    if (TWO) b = log2f(warp_sum(lane < kSumWarps ? s_s2[lane][own] * ex2((m - safe) * inv_tau) : 0.f));
+    if (lane == 0) { tops[r] = safe; l1[r] = a; l2[r] = b; }
+    row_losses(o, r, flag[r], idx[r], safe, a, b, inv_tau, mine);
   }
   if (lane == 0) { s_ce[warp] = mine.ce; s_kd[warp] = mine.kd; s_z[warp] = mine.z; }
   __syncthreads();
@@ -316,7 +315,7 @@ head_sum_kernel(HeadCounts* cnt, const HeadLossOut o, const float* __restrict__ 
 // ---- gradient of the logits -----------------------------------------------------------
 struct DzArgs {
   const HeadCounts* cnt;
-  const float *pm, *l1, *l2;
+  const float *pm, *tops, *l1, *l2;
   const uint8_t* flag;
   int ldp, row0, piece, V, ld;
   float inv_tau, q_step, coef, coef_kd, coef_z, tau;
@@ -362,8 +361,9 @@ head_dz_bf16_kernel(const DzArgs a, uint16_t* __restrict__ kept) {
     if (r < n) {
       m = a.pm[static_cast<size_t>(h) * a.ldp + r];
       m = (m == -__int_as_float(0x7f800000) ? 0.f : m) + 65536.f * a.q_step;
-      L1 = a.l1[a.row0 + r];
-      L2 = a.l2[a.row0 + r];
+      const float top = a.tops[a.row0 + r];
+      L1 = top + a.l1[a.row0 + r];
+      L2 = fmaf(top, a.inv_tau, a.l2[a.row0 + r]);
       row_factors(a, sc, a.flag[a.row0 + r], L1, k1, k2);
     }
 #pragma unroll
@@ -402,10 +402,10 @@ head_dz_bf16_kernel(const DzArgs a, uint16_t* __restrict__ kept) {
 // Gradient at entry e of row r, the first of its token: the softmaxes at the entry's own fp32
 // logit, minus the factors of every entry of that token.
 __device__ __forceinline__ float entry_dz(const DzArgs& a, const HeadScale& sc, const HeadLossOut& o, size_t at,
-                                          int e, int id, float L1, float L2, float k1, float k2) {
-  const float z = o.zt[at];
-  float g = k1 * exp2f(z * kLog2e - L1);
-  if (a.two) g += k2 * exp2f(z * (kLog2e * a.inv_tau) - L2);
+                                          int e, int id, float top, float l1, float l2, float k1, float k2) {
+  const float y = over_top(o.zt[at], top);
+  float g = k1 * exp2f(y - l1);
+  if (a.two) g += k2 * exp2f(y * a.inv_tau - l2);
   for (int f = e; f < o.E && o.ent[at + f - e] == id; ++f) {
     const float q = o.ent_q[at + f - e];
     g -= q < 0.f ? sc.k_ce : sc.k_kd * q;
@@ -428,9 +428,9 @@ head_dz_entries_kernel(const DzArgs a, const HeadLossOut o, __nv_bfloat16* __res
     const int id = o.ent[at];
     if (id == kHeadNoEntry || (e > 0 && o.ent[at - 1] == id)) continue;   // the first one writes
     float k1, k2;
-    row_factors(a, sc, a.flag[rg], a.l1[rg], k1, k2);
+    row_factors(a, sc, a.flag[rg], a.tops[rg] + a.l1[rg], k1, k2);
     dz[static_cast<size_t>(r) * a.ld + id] =
-        __float2bfloat16_rn(entry_dz(a, sc, o, at, e, id, a.l1[rg], a.l2[rg], k1, k2));
+        __float2bfloat16_rn(entry_dz(a, sc, o, at, e, id, a.tops[rg], a.l1[rg], a.l2[rg], k1, k2));
   }
 }
 
@@ -444,9 +444,9 @@ head_dz_f32_kernel(const DzArgs a, const HeadLossOut o, float* __restrict__ kept
   const HeadScale sc = head_scale(a.cnt->n, a.cnt->n_ce, a.cnt->n_kd, a.coef, a.coef_kd, a.coef_z, a.tau);
   for (int r = blockIdx.x; r < n; r += gridDim.x) {
     const size_t rg = static_cast<size_t>(a.row0) + r;
-    const float L1 = a.l1[rg], L2 = a.l2[rg];
+    const float top = a.tops[rg], l1 = a.l1[rg], l2 = a.l2[rg];
     float k1, k2;
-    row_factors(a, sc, a.flag[rg], L1, k1, k2);
+    row_factors(a, sc, a.flag[rg], top + l1, k1, k2);
     float* row = kept + static_cast<size_t>(r) * a.ld;
     for (int c0 = threadIdx.x; c0 < a.V; c0 += 4 * blockDim.x) {
       float z[4];   // (loaded ahead of the first store)
@@ -458,8 +458,9 @@ head_dz_f32_kernel(const DzArgs a, const HeadLossOut o, float* __restrict__ kept
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int c = c0 + j * blockDim.x;
-        float g = k1 * exp2f(z[j] * kLog2e - L1);
-        if (a.two) g += k2 * exp2f(z[j] * (kLog2e * a.inv_tau) - L2);
+        const float y = over_top(z[j], top);
+        float g = k1 * exp2f(y - l1);
+        if (a.two) g += k2 * exp2f(y * a.inv_tau - l2);
         if (c < a.V) row[c] = g;
       }
     }
@@ -468,7 +469,7 @@ head_dz_f32_kernel(const DzArgs a, const HeadLossOut o, float* __restrict__ kept
       const size_t at = rg * o.E + e;
       const int id = o.ent[at];
       if (id == kHeadNoEntry || (e > 0 && o.ent[at - 1] == id)) continue;
-      row[id] = entry_dz(a, sc, o, at, e, id, L1, L2, k1, k2);
+      row[id] = entry_dz(a, sc, o, at, e, id, top, l1, l2, k1, k2);
     }
   }
 }
@@ -605,7 +606,7 @@ HeadPlan head_plan(const occult_desc_t& ds, const occult_head_t& opt, bool step)
   p.o_xc = take(T * p.d * (bf ? 2 : 4));
   p.o_m = take(4 * P * p.halves); p.o_s = take(4 * P * p.halves);
   p.o_s2 = take(p.two ? 4 * P * p.halves : 0);
-  p.o_l1 = take(4 * T); p.o_l2 = take(4 * T);
+  p.o_top = take(4 * T); p.o_l1 = take(4 * T); p.o_l2 = take(4 * T);
   p.o_sum = take(12 * (T / 32 + p.n_pieces));
   p.o_kept = take(step ? P * row_bytes : 0);
   const size_t parts = std::max(p.splits, p.splits_alone);
@@ -626,6 +627,7 @@ int launch_head(const LaunchCtx& ctx, const HeadPlan& p, const HeadArgs& a) {
   auto* pm = reinterpret_cast<float*>(ws + p.o_m);
   auto* ps = reinterpret_cast<float*>(ws + p.o_s);
   auto* ps2 = reinterpret_cast<float*>(ws + p.o_s2);
+  auto* tops = reinterpret_cast<float*>(ws + p.o_top);
   auto* l1 = reinterpret_cast<float*>(ws + p.o_l1);
   auto* l2 = reinterpret_cast<float*>(ws + p.o_l2);
   auto* sums = reinterpret_cast<float*>(ws + p.o_sum);
@@ -655,12 +657,12 @@ int launch_head(const LaunchCtx& ctx, const HeadPlan& p, const HeadArgs& a) {
     auto* sum = warps == 32 ? (p.two ? head_sum_kernel<true, 32> : head_sum_kernel<false, 32>)
                             : (p.two ? head_sum_kernel<true, 16> : head_sum_kernel<false, 16>);
     e = launch_pdl(sum, blocks, warps * 32, 0, ctx.stream, cnt, head_loss_out(p, a), pm, ps, ps2, p.piece,
-                   p.halves, row0, rows, idx, flag, l1, l2, sums, block0, n_blocks);
+                   p.halves, row0, rows, idx, flag, tops, l1, l2, sums, block0, n_blocks);
     if (e != cudaSuccess) return OCCULT_ERR_CUDA;
     block0 += blocks;
     if (!p.step) continue;
     DzArgs z{};
-    z.cnt = cnt; z.pm = pm; z.l1 = l1; z.l2 = l2; z.flag = flag;
+    z.cnt = cnt; z.pm = pm; z.tops = tops; z.l1 = l1; z.l2 = l2; z.flag = flag;
     z.ldp = p.piece; z.row0 = row0; z.piece = p.piece; z.V = p.V; z.ld = p.ld;
     z.inv_tau = 1.f / p.tau; z.q_step = p.q_step; z.tau = p.tau;
     z.coef = p.coef; z.coef_kd = p.coef_kd; z.coef_z = p.coef_z;

@@ -37,7 +37,7 @@ struct HeadPlan {
   float tau, coef, coef_kd, coef_z;
   float q_step;             // octaves of a unit of the kept 16-bit logits
   // workspace
-  size_t o_cnt, o_idx, o_flag, o_ent, o_q, o_zt, o_xc, o_m, o_s, o_s2, o_l1, o_l2, o_sum,
+  size_t o_cnt, o_idx, o_flag, o_ent, o_q, o_zt, o_xc, o_m, o_s, o_s2, o_top, o_l1, o_l2, o_sum,
       o_kept, o_part, o_acc, total;
 };
 
@@ -86,20 +86,25 @@ __device__ __forceinline__ float warp_max(float v) {
   return v;
 }
 
-// A warp finishes compact row r from the log2 of its sums (L at temperature 1, L2 at tau):
-// writes the token's outputs and adds its terms to `sum`.
+// A row's sums are of 2^(z log2(e) - top), `top` its maximum in octaves, and at temperature
+// tau of that exponent over tau; l1 and l2 are their log2.  top and l1 stay apart: a token
+// that is nearly sure of its label has z log2(e) - top - l1 near 0, which top + l1 in one
+// fp32 would leave without its digits (2e-6 octaves at a logit of 20, where 1 - p may be 1e-3).
+__device__ __forceinline__ float over_top(float z, float top) { return fmaf(z, kLog2e, -top); }
+
+// A warp finishes compact row r: writes the token's outputs and adds its terms to `sum`.
 struct RowSums { float ce, kd, z; };
-__device__ __forceinline__ void row_losses(const HeadLossOut& o, size_t r, int flag, int token, float L,
-                                           float L2, float inv_tau, RowSums& sum) {
+__device__ __forceinline__ void row_losses(const HeadLossOut& o, size_t r, int flag, int token, float top,
+                                           float l1, float l2, float inv_tau, RowSums& sum) {
   const int lane = threadIdx.x & 31;
-  const float lse = L * kLn2;
+  const float lse = (top + l1) * kLn2;
   float tok = 0.f, kd = 0.f;
   for (int e = lane; e < o.E; e += 32) {
     const int id = __ldcg(o.ent + r * o.E + e);
     const float q = __ldcg(o.ent_q + r * o.E + e), z = __ldcg(o.zt + r * o.E + e);
     if (id == kHeadNoEntry) continue;
-    if (q < 0.f) tok = lse - z;
-    else if (q != 0.f) kd += q * (logf(q) - (z * inv_tau - L2 * kLn2));
+    if (q < 0.f) tok = (l1 - over_top(z, top)) * kLn2;
+    else if (q != 0.f) kd += q * (logf(q) - (over_top(z, top) * inv_tau - l2) * kLn2);
   }
   tok = warp_sum(tok);
   const float ce = (flag & kRowCe) ? tok : 0.f;

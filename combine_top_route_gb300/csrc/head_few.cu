@@ -163,12 +163,12 @@ __global__ void __launch_bounds__(kThreads, 1) head_few_kernel(const FewArgs a) 
         }, xs, a.d);
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-          const float y0 = acc[0][t] * kLog2e, y1 = both ? acc[1][t] * kLog2e : NEG;
-          const float hi = fmaxf(m[t], fmaxf(y0, y1)), to = hi == NEG ? 0.f : hi;
-          s[t] = s[t] * ex2(m[t] - to) + (ex2(y0 - to) + ex2(y1 - to));
+          const float z1 = both ? acc[1][t] : NEG;
+          const float hi = fmaxf(m[t], fmaxf(acc[0][t], z1) * kLog2e), to = hi == NEG ? 0.f : hi;
+          const float y0 = over_top(acc[0][t], to), y1 = over_top(z1, to);
+          s[t] = s[t] * ex2(m[t] - to) + (ex2(y0) + ex2(y1));
           if (TWO)
-            s2[t] = s2[t] * ex2((m[t] - to) * a.inv_tau) +
-                    (ex2((y0 - to) * a.inv_tau) + ex2((y1 - to) * a.inv_tau));
+            s2[t] = s2[t] * ex2((m[t] - to) * a.inv_tau) + (ex2(y0 * a.inv_tau) + ex2(y1 * a.inv_tau));
           m[t] = hi;
         }
       }
@@ -229,9 +229,9 @@ __global__ void __launch_bounds__(kThreads, 1) head_few_kernel(const FewArgs a) 
       if (TWO) p2 = fmaf(vt[i], ex2((vm[i] - my) * a.inv_tau), p2);
     }
     const float top = warp_max(hi), to = top == NEG ? 0.f : top;
-    const float L = to + log2f(warp_sum(p * ex2(hi - to)));
-    const float L2 = TWO ? to * a.inv_tau + log2f(warp_sum(p2 * ex2((hi - to) * a.inv_tau))) : L;
-    row_losses(a.out, r, a.flag[r], a.idx[r], L, L2, a.inv_tau, sum);
+    const float l1 = log2f(warp_sum(p * ex2(hi - to)));
+    const float l2 = TWO ? log2f(warp_sum(p2 * ex2((hi - to) * a.inv_tau))) : l1;
+    row_losses(a.out, r, a.flag[r], a.idx[r], to, l1, l2, a.inv_tau, sum);
   }
   if (lane == 0) mean_losses(a.out, *a.cnt, sum.ce, sum.kd, sum.z);
 }

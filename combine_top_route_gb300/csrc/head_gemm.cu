@@ -465,7 +465,6 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
         }
         // the sums, and the logits to keep
         const float my = (m == NEG ? 0.f : m) * kLog2e;
-        const float m_t = my * p.inv_tau, ct = kLog2e * p.inv_tau;
         const float qc = -kLog2e * p.q_inv, qm = my * p.q_inv;
         float s = 0.f, s2 = 0.f;
         char* keep = nullptr;
@@ -474,22 +473,19 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
 #pragma unroll
         for (int c = 0; c < 128; c += 32) {
           if (MODE == HEAD_KEEP || c < lim) {
-            float sa = 0.f, sb = 0.f;
+            float sa = 0.f, sb = 0.f, ta = 0.f, tb = 0.f;
 #pragma unroll
             for (int j = 0; j < 32; j += 2) {
-              sa += ex2(fmaf(z[c + j], kLog2e, -my));
-              sb += ex2(fmaf(z[c + j + 1], kLog2e, -my));
+              const float y0 = over_top(z[c + j], my), y1 = over_top(z[c + j + 1], my);
+              sa += ex2(y0);
+              sb += ex2(y1);
+              if (TWO) {
+                ta += ex2(y0 * p.inv_tau);
+                tb += ex2(y1 * p.inv_tau);
+              }
             }
             s += sa + sb;
-            if (TWO) {
-              sa = sb = 0.f;
-#pragma unroll
-              for (int j = 0; j < 32; j += 2) {
-                sa += ex2(fmaf(z[c + j], ct, -m_t));
-                sb += ex2(fmaf(z[c + j + 1], ct, -m_t));
-              }
-              s2 += sa + sb;
-            }
+            if (TWO) s2 += ta + tb;
           }
           if (MODE == HEAD_KEEP) {
             // the low bits of t + 2^23 are t to the nearest: no conversion unit (the

@@ -474,3 +474,54 @@ def test_the_first_call_may_be_captured(occ, T):
     out = subprocess.run([sys.executable, "-c", _CAPTURE.format(root=root, T=T)], capture_output=True, text=True,
                          timeout=300)
     assert out.returncode == 0 and "captured" in out.stdout, out.stderr[-2000:]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T", [2, 300])
+@pytest.mark.parametrize("taught", [False, True])
+def test_tokens_that_are_nearly_sure(occ, dtype, T, taught):
+    """1 - p down to 6e-6 of a label's or a teacher's token keeps its digits.
+
+    Every logit is one exact product: a label's of 20 to 32, a rival's g below it, the
+    others too low to count, so that a row's sum over its largest term is 1 + e^-g.  What
+    is off: the exponential of the largest (2^-22, near 1), the sum's two roundings (2^-24
+    each), the probability's exponential (2^-23): 2^-21 in all; the arguments and the
+    logarithms, 1e-5 of the result; a bf16 layer's rounding, 2^-8 of it.
+    """
+    d, V, tau = 64, 1009, 2.0 if taught else 1.0
+    j = np.arange(d)
+    label, z, g = (37 * j + 5) % V, (160 + 7 * j % 95) / 8, 4.0 + 2 * (j % 5)
+    w = np.full((V, d), -512.0, np.float32)
+    w[label, j] = z
+    w[(label + 500) % V, j] = z - g
+    at = np.arange(T) % d
+    x = np.zeros((T, d), np.float32)
+    x[np.arange(T), at] = 1
+    delta = np.exp(-g / tau)                     # a rival's share of its label's
+    want, miss = np.log1p(delta)[at], delta / (1 + delta)
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    ds = occ.desc_for(synth.CONFIGS["olmoe_fwd"].with_(T=T, d=d, dtype=dtype))
+    opt = occ.occult_head_t(vocab=V, topk=int(taught), coef=1.0 - taught, coef_kd=float(taught), temperature=tau)
+    given = dict(labels=gpu(label[at].astype(np.int32)))
+    if taught:
+        given = dict(teacher_ids=gpu(label[at].astype(np.int32)[:, None]), teacher_logits=torch.zeros(T, 1, device="cuda"))
+    xs, ws_ = gpu(x, dt), gpu(w, dt)
+    dw = torch.empty(V, d, device="cuda")
+    for step in (False, True):
+        ws = torch.empty(occ.head_workspace_size(ds, opt, step=step), dtype=torch.uint8, device="cuda")
+        loss, tok = torch.empty(4, device="cuda"), torch.empty(T, device="cuda")
+        kw = dict(given) if taught else dict(given, token_loss=tok)
+        if step:
+            occ.occult_head_step(ds, opt, xs, ws_, loss, ws, dw=dw, **kw)
+        else:
+            occ.occult_head_loss(ds, opt, xs, ws_, loss, ws, **kw)
+        if not taught:
+            off = np.abs(tok.double().cpu().numpy() - want)
+            assert (off <= 2.0 ** -21 + 1e-5 * want).all(), off.max()
+        mean = float(loss[2]) / tau ** 2 if taught else float(loss[1])
+        assert abs(mean - want.mean()) <= 2.0 ** -21 + 1e-5 * want.mean()
+    # a token's gradient at its label, over the tokens that share it
+    n = np.bincount(at, minlength=d)
+    got = -dw.double().cpu().numpy()[label, j] * T / tau
+    tol = n * (2.0 ** -21 + (1e-5 + (2.0 ** -8 if dtype == "bf16" else 0)) * miss)
+    assert (np.abs(got - n * miss) <= tol).all(), (np.abs(got - n * miss) / np.maximum(tol, 1e-30)).max()
