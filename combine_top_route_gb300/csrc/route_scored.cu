@@ -560,7 +560,9 @@ route_scored_kernel(const RouteArgs a) {
     float g = lane < a.k ? score_of<SIG>(row[my_id], top, total) : 0.f;
     if (a.renorm) {
       const float sum = warp_sum(g);
-      g = sum == 0.f ? 0.f : __fdividef(g, sum);
+      // (the fast division is for sums of normal size)
+      if (sum >= 0x1p-120f) g = __fdividef(g, sum);
+      else g = sum == 0.f ? 0.f : g / sum;
     }
     const uint32_t vm = __reduce_or_sync(kFull, lane < a.k ? 1u << s_dev[my_id] : 0u);
     if (lane < a.k) {
@@ -617,8 +619,9 @@ route_scored_grad_kernel(const float* __restrict__ logits, const int32_t* __rest
     float ds = u;
     if (renorm) {
       const float S = warp_sum(s);
-      const float us = warp_sum(u * s);
-      ds = S == 0.f || id < 0 ? 0.f : (u - us / S) / S;
+      // (by shares of the sum: a token's only expert has 1 of it exactly, and no gradient)
+      const float mean = warp_sum(S == 0.f ? 0.f : u * (s / S));
+      ds = S == 0.f || id < 0 ? 0.f : (u - mean) / S;
     }
     const float all = SIG ? 0.f : warp_sum(ds * s);
 #pragma unroll

@@ -864,7 +864,8 @@ typedef struct occult_score {
  *            lower expert (group)
  *   gate_j = scale * s_j            (desc->renorm: scale * s_j / sum_i s_i, the sum
  *            over the chosen; 0 where that sum is 0)
- * The bias moves the choice, never the gates.
+ * The bias moves the choice, never the gates.  Scores are held in fp32: one below its range
+ * is 0 in the gates and their gradient.
  *   logits  fp32 [T, Ne].  A logit of -inf, or of fp32's lowest value, switches its
  *           expert off: s_e = 0, no part of a group's worth (a group without any
  *           other expert ranks last), and chosen, lowest expert first, only where

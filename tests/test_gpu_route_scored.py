@@ -217,6 +217,27 @@ def test_grad(occ):
                 assert (np.abs(got - want) <= err).all(), (T, Ne, sigmoid, renorm)
 
 
+@pytest.mark.parametrize("sigmoid", [True, False])
+@pytest.mark.parametrize("low", [0.0, -85.0])
+def test_an_only_expert_has_the_whole_gate(occ, sigmoid, low):
+    """One expert a token, renormalised: its gate is the scale (to the fast division's two units,
+    2^-22) and has no gradient, exactly (s / s is 1 in IEEE arithmetic), however small its
+    score."""
+    T, Ne = 257, 62
+    ds = occ.desc_for(synth.CONFIGS["olmoe_fwd"].with_(T=T, n_experts=Ne, top_k=1, n_vdev=2, renorm=1))
+    opt = occ.occult_score_t(occ.SCORE_SIGMOID if sigmoid else occ.SCORE_SOFTMAX, scale=2.5)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    logits = low + torch.randn(T, Ne, generator=g, device="cuda")
+    ids, vmask = (torch.empty(T, dtype=torch.int32, device="cuda") for _ in range(2))
+    gates, dgates = torch.empty(T, device="cuda"), torch.randn(T, generator=g, device="cuda")
+    dlogits = torch.full((T, Ne), 7.0, device="cuda")
+    e2v = (torch.arange(Ne, device="cuda") % 2).int()
+    occ.occult_route_scored(ds, opt, logits, e2v, ids, gates, vmask)
+    occ.occult_route_scored_grad(ds, opt, logits, ids, dgates, dlogits)
+    assert (ids.long() == logits.argmax(1)).all()
+    assert (gates.double() / 2.5 - 1).abs().max() <= 2.0 ** -22 and (dlogits == 0).all()
+
+
 def test_grad_is_the_difference_quotient(occ):
     """The kernel's own gates, moved along random directions, against its gradient."""
     rng = np.random.default_rng(7)
