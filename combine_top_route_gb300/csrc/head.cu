@@ -23,12 +23,13 @@ namespace {
 // ---- entries ----------------------------------------------------------------------
 // A warp makes a row's entries: the teacher's probabilities at temperature tau, and the
 // label (q = -1), in ascending token order, absent ones behind.  Returns whether the
-// teacher says anything.  `ids`: 160 words of the warp's own.
-constexpr int kEntPer = (OCCULT_MAX_TEACHER + 1 + 31) / 32;
+// teacher says anything.  `ids`: 128 words of the warp's own, on 16 bytes.
+// A lane has every 32nd teacher entry; an entry's place is the number of those in front of it.
+constexpr int kEntPer = OCCULT_MAX_TEACHER / 32;
 __device__ __forceinline__ bool make_entries(const int32_t* __restrict__ t_ids, const float* __restrict__ t_logits,
-                                             int t, int f, int label, int V, int K, float inv_tau, int* ids,
+                                             int t, int f, int label, int V, int K, float inv_tau, uint32_t* ids,
                                              int32_t* __restrict__ ent, float* __restrict__ ent_q) {
-  const int lane = threadIdx.x & 31, E = K + 1;
+  const int lane = threadIdx.x & 31;
   const float NEG = -__int_as_float(0x7f800000);
   int id[kEntPer];
   float q[kEntPer];
@@ -63,68 +64,112 @@ __device__ __forceinline__ bool make_entries(const int32_t* __restrict__ t_ids, 
   for (int i = 0; i < kEntPer; ++i) {
     const int j = lane + 32 * i;
     q[i] *= inv;
-    if (j == K) {
-      id[i] = (f & kRowCe) ? label : kHeadNoEntry;
-      q[i] = -1.f;
-    }
-    ids[j] = j < E ? id[i] : kHeadNoEntry;
+    // (places behind the K hold what stands behind every entry)
+    ids[j] = j < K ? static_cast<uint32_t>(id[i]) : 0xffffffffu;
   }
   __syncwarp();
-  int rank[kEntPer];
+  const uint32_t own = (f & kRowCe) ? label : kHeadNoEntry;
+  uint32_t rank[kEntPer], before = 0;   // before: entries in front of the label, the equal ones too
 #pragma unroll
-  for (int i = 0; i < kEntPer; ++i) rank[i] = 0;
-  for (int k = 0; k < E; ++k) {
-    const int other = ids[k];
+  for (int i = 0; i < kEntPer; ++i) {
+    rank[i] = own < static_cast<uint32_t>(id[i]) ? 1 : 0;
+    before += __popc(__ballot_sync(kFull, lane + 32 * i < K && static_cast<uint32_t>(id[i]) <= own));
+  }
 #pragma unroll
-    for (int i = 0; i < kEntPer; ++i)
-      if (32 * i < E) rank[i] += (other < id[i] || (other == id[i] && k < lane + 32 * i)) ? 1 : 0;
+  for (int b = 0; b < kEntPer; ++b) {
+    if (32 * b >= K) break;
+#pragma unroll 4
+    for (int k = 0; k < 32; k += 4) {
+      const uint4 four = *reinterpret_cast<const uint4*>(ids + 32 * b + k);
+      const uint32_t other[4] = {four.x, four.y, four.z, four.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int i = 0; i < kEntPer; ++i)
+          // equal ones in their order: those of a smaller number stand in front
+          if (32 * i < K)
+            rank[i] += other[j] < static_cast<uint32_t>(id[i]) + (b < i || (b == i && k + j < lane) ? 1u : 0u) ? 1 : 0;
+    }
   }
 #pragma unroll
   for (int i = 0; i < kEntPer; ++i)
-    if (lane + 32 * i < E) {
+    if (lane + 32 * i < K) {
       ent[rank[i]] = id[i];
       ent_q[rank[i]] = q[i];
     }
+  if (lane == 0) {
+    ent[before] = static_cast<int32_t>(own);
+    ent_q[before] = -1.f;
+  }
   __syncwarp();
   return sum != 0.f;
 }
 
 // ---- rows -----------------------------------------------------------------------
 // Which tokens a term counts, and their compact rows in token order.  A block has `per`
-// tokens of its own and counts all of them (a few KB from L2, which is cheaper than
-// another launch): those before its own give its first row, all of them the totals.
+// tokens of its own and counts all of them, from labels and teacher ids themselves where
+// those are few KB for every block, else from the tallies of a launch of its own
+// (head_tally_kernel): those before its own give its first row, all of them the totals.
 // Where some token is left out, the rows of x are copied to their compact place on the way
 // (else the products read x itself), with zeros up to the next multiple of 64, so that
 // dw's reduction may run over them; and that token's outputs are zeros.  With a teacher a
 // warp then makes the entries of its tokens' rows.
 constexpr int kRowThreads = 256;
+// What a token is to the loss.
+__device__ __forceinline__ int token_flag(const int32_t* __restrict__ labels, const int32_t* __restrict__ t_ids,
+                                          int t, int V, int K) {
+  int f = 0;
+  if (labels && static_cast<unsigned>(labels[t]) < static_cast<unsigned>(V)) f |= kRowCe;
+  if (K && static_cast<unsigned>(t_ids[static_cast<size_t>(t) * K]) < static_cast<unsigned>(V)) f |= kRowKd;
+  return f;
+}
+// Tallies of 256 tokens each: counted, with a label, with a teacher.
+__global__ void __launch_bounds__(kRowThreads)
+head_tally_kernel(const int32_t* __restrict__ labels, const int32_t* __restrict__ t_ids, int T, int V, int K,
+                  int4* __restrict__ tally) {
+  pdl_wait();
+  pdl_trigger();
+  const int t = blockIdx.x * kRowThreads + threadIdx.x;
+  const int f = t < T ? token_flag(labels, t_ids, t, V, K) : 0;
+  const int n = __syncthreads_count(f != 0), ce = __syncthreads_count(f & kRowCe);
+  const int kd = __syncthreads_count(f & kRowKd);
+  if (threadIdx.x == 0) tally[blockIdx.x] = make_int4(n, ce, kd, 0);
+}
 __global__ void __launch_bounds__(kRowThreads)
 head_rows_kernel(const int32_t* __restrict__ labels, const int32_t* __restrict__ t_ids,
                  const float* __restrict__ t_logits, int T, int V, int K, float inv_tau, int per,
                  HeadCounts* cnt, int32_t* __restrict__ idx, uint8_t* __restrict__ flag,
                  int32_t* __restrict__ ent, float* __restrict__ ent_q, float* __restrict__ lse,
                  float* __restrict__ token_loss, const uint4* __restrict__ x, uint4* __restrict__ xc, int vecs,
-                 char* __restrict__ dx, int dx_bytes) {
-  __shared__ int s_ids[kRowThreads / 32][32 * kEntPer];
+                 char* __restrict__ dx, int dx_bytes, const int4* __restrict__ tally) {
+  __shared__ __align__(16) uint32_t s_ids[kRowThreads / 32][32 * kEntPer];
   __shared__ int s_sum[4][kRowThreads / 32], s_warp[kRowThreads / 32], s_pos[kRowThreads];
   pdl_wait();
   pdl_trigger();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int t0 = min(T, static_cast<int>(blockIdx.x) * per), t1 = min(T, t0 + per);
-  auto flag_of = [&](int t) -> int {
-    int f = 0;
-    if (labels && static_cast<unsigned>(labels[t]) < static_cast<unsigned>(V)) f |= kRowCe;
-    if (K && static_cast<unsigned>(t_ids[static_cast<size_t>(t) * K]) < static_cast<unsigned>(V)) f |= kRowKd;
-    return f;
-  };
+  auto flag_of = [&](int t) { return token_flag(labels, t_ids, t, V, K); };
   int sum[4] = {0, 0, 0, 0};   // rows before this block's, rows, with a label, with a teacher
+  if (tally) {
+    const int whole = t0 / kRowThreads;   // tallies before this block's tokens
+#pragma unroll 4
+    for (int i = tid; i < (T + kRowThreads - 1) / kRowThreads; i += kRowThreads) {
+      const int4 c = tally[i];
+      sum[0] += i < whole ? c.x : 0;
+      sum[1] += c.x;
+      sum[2] += c.y;
+      sum[3] += c.z;
+    }
+    if (whole * kRowThreads + tid < t0) sum[0] += flag_of(whole * kRowThreads + tid) != 0 ? 1 : 0;
+  } else {
 #pragma unroll 8
-  for (int t = tid; t < T; t += kRowThreads) {
-    const int f = flag_of(t);
-    sum[0] += (f != 0 && t < t0) ? 1 : 0;
-    sum[1] += f != 0 ? 1 : 0;
-    sum[2] += (f & kRowCe) ? 1 : 0;
-    sum[3] += (f & kRowKd) ? 1 : 0;
+    for (int t = tid; t < T; t += kRowThreads) {
+      const int f = flag_of(t);
+      sum[0] += (f != 0 && t < t0) ? 1 : 0;
+      sum[1] += f != 0 ? 1 : 0;
+      sum[2] += (f & kRowCe) ? 1 : 0;
+      sum[3] += (f & kRowKd) ? 1 : 0;
+    }
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -518,6 +563,12 @@ head_dx_kernel(const HeadCounts* cnt, const int32_t* __restrict__ idx, const flo
   }
 }
 
+// Bytes of labels and ids, over all blocks, from which a launch of tallies pays (12091 tokens
+// with 64 teacher entries, 330 MB: rows 69 us, now tallies 3, rows 22, a third of which the
+// entries' order by two compares an entry; 5936 with one, 158 MB: 12.4 and 3 + 9.1; 2048
+// with 32, 19 MB: 11 without, and 8.5 with the entries' new order alone).
+constexpr int64_t kTallyBytes = 1 << 25;
+
 size_t up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
 }  // namespace
@@ -601,6 +652,7 @@ HeadPlan head_plan(const occult_desc_t& ds, const occult_head_t& opt, bool step)
   auto take = [&](size_t bytes) { const size_t at = o; o += up(bytes, 256); return at; };
   const size_t T = Tr, P = p.piece;
   p.o_cnt = take(sizeof(HeadCounts));
+  p.o_tally = take(16 * (T / kHeadRowAlign));
   p.o_idx = take(4 * T); p.o_flag = take(T);
   p.o_ent = take(4 * T * p.E); p.o_q = take(4 * T * p.E); p.o_zt = take(4 * T * p.E);
   p.o_xc = take(T * p.d * (bf ? 2 : 4));
@@ -637,11 +689,21 @@ int launch_head(const LaunchCtx& ctx, const HeadPlan& p, const HeadArgs& a) {
   // row of entries
   const int per = static_cast<int>(up((p.T + 1023) / 1024, p.K ? 8 : 32));
   const int grad_size = p.grad_dtype == OCCULT_BF16 ? 2 : 4;
-  cudaError_t e = launch_pdl(head_rows_kernel, (p.T + per - 1) / per, kRowThreads, 0, ctx.stream, a.labels,
+  const int row_blocks = (p.T + per - 1) / per;
+  // counting reads 4 bytes of a token's label and 32 of its teacher's first id, in every block
+  int4* tally = nullptr;
+  cudaError_t e = cudaSuccess;
+  if (static_cast<int64_t>(row_blocks) * p.T * (p.K ? 36 : 4) > kTallyBytes) {
+    tally = reinterpret_cast<int4*>(ws + p.o_tally);
+    e = launch_pdl(head_tally_kernel, (p.T + kRowThreads - 1) / kRowThreads, kRowThreads, 0, ctx.stream, a.labels,
+                   a.t_ids, p.T, p.V, p.K, tally);
+    if (e != cudaSuccess) return OCCULT_ERR_CUDA;
+  }
+  e = launch_pdl(head_rows_kernel, row_blocks, kRowThreads, 0, ctx.stream, a.labels,
                              a.t_ids, a.t_logits, p.T, p.V, p.K, 1.f / p.tau, per, cnt, idx, flag, ent, ent_q,
                              a.lse, a.token_loss, static_cast<const uint4*>(a.x),
                              reinterpret_cast<uint4*>(ws + p.o_xc), p.d / (bf ? 8 : 4),
-                             static_cast<char*>(a.dx), p.d * grad_size);
+                             static_cast<char*>(a.dx), p.d * grad_size, tally);
   if (e != cudaSuccess) return OCCULT_ERR_CUDA;
   int n_blocks = 0;
   for (int i = 0; i < p.n_pieces; ++i)
@@ -670,8 +732,8 @@ int launch_head(const LaunchCtx& ctx, const HeadPlan& p, const HeadArgs& a) {
     if (bf) {
       auto* kept = reinterpret_cast<uint16_t*>(ws + p.o_kept);
       // some eight blocks an SM, however many of the rows count
-      const int gx = (p.ld / 128 + 7) / 8, row_blocks = (rows + kHeadRowAlign - 1) / kHeadRowAlign * (kHeadRowAlign / kDzRows);
-      const dim3 grid(gx, std::min(row_blocks, std::max(1, (ctx.num_sms * 8 + gx - 1) / gx)));
+      const int gx = (p.ld / 128 + 7) / 8, steps = (rows + kHeadRowAlign - 1) / kHeadRowAlign * (kHeadRowAlign / kDzRows);
+      const dim3 grid(gx, std::min(steps, std::max(1, (ctx.num_sms * 8 + gx - 1) / gx)));
       e = launch_pdl(head_dz_bf16_kernel, grid, 256, 0, ctx.stream, z, kept);
       if (e != cudaSuccess) return OCCULT_ERR_CUDA;
       const int eb = static_cast<int>(std::min<int64_t>((static_cast<int64_t>(rows) * p.E + 255) / 256,

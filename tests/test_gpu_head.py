@@ -233,6 +233,21 @@ def test_ignored_rows_and_pieces(occ, ignored, piece):
         check(occ, (x, w, labels, ids, tl), step=False)
 
 
+@pytest.mark.parametrize("T,K,ignored", [(3001, 3, 0.4), (2816, 64, 0.0), (3001, 128, 1.0)])
+@pytest.mark.parametrize("labelled", [True, False])
+def test_many_tokens_with_teachers(occ, T, K, ignored, labelled):
+    """So many that rows are counted by tallies of 256 tokens: ends inside one, tokens left out
+    on both sides of their borders, labels without a teacher and teachers without a label."""
+    x, w, labels, ids, tl = case(T, 64, 300, K=K, ignored=ignored, seed=5)
+    labels[::7] = -1
+    if ignored < 1:
+        labels[250:260], ids[250:260, 0] = -1, -1
+    kw = dict(tau=2.0, coef=0.5 if labelled else 0.0, coef_kd=0.5, coef_z=1e-3)
+    c = (x, w, labels if labelled else None, ids, tl)
+    check(occ, c, piece=1024, **kw)
+    check(occ, c, step=False, **kw)
+
+
 def test_one_gradient_alone(occ):
     c = case(300, 192, 1200, K=8)
     kw = dict(tau=2.0, coef=0.5, coef_kd=0.5)
