@@ -564,8 +564,9 @@ head_dx_kernel(const HeadCounts* cnt, const int32_t* __restrict__ idx, const flo
 }
 
 // Bytes of labels and ids, over all blocks, from which a launch of tallies pays (12091 tokens
-// with 64 teacher entries, 330 MB: 46 us of counting, now 3 in the tallies and a rest; 5936
-// with one, 158 MB: rows 12.4 us, and 3 + 9.1; 2048 with 32, 19 MB: 8.5 us without).
+// with 64 teacher entries, 330 MB: rows 69 us, with tallies 3 + 43, of which 22 since entries
+// are ordered by two compares each; 5936 with one, 158 MB: 12.4 us, and 3 + 9.1; 2048 with
+// 32, 19 MB: 8.5 us without).
 constexpr int64_t kTallyBytes = 1 << 25;
 
 size_t up(size_t v, size_t a) { return (v + a - 1) / a * a; }
