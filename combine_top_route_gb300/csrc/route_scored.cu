@@ -591,7 +591,7 @@ __device__ __forceinline__ void softmax_stats(const float (&z)[PL], int Ne, floa
 
 // ---- gradient -------------------------------------------------------------------
 // The row is put together in shared memory: the k chosen experts' terms on zeros, then
-// (softmax) the common term of every expert, and written as it lies.
+// (softmax, not renormalised) the common term of every expert, and written as it lies.
 template <bool SIG, int PL>
 __global__ void __launch_bounds__(kWarps * 32)
 route_scored_grad_kernel(const float* __restrict__ logits, const int32_t* __restrict__ ids,
@@ -616,25 +616,29 @@ route_scored_grad_kernel(const float* __restrict__ logits, const int32_t* __rest
     if (id < 0 || id >= Ne) id = -1;
     const float u = id >= 0 ? scale * dgates[static_cast<size_t>(t) * k + lane] : 0.f;
     const float s = id >= 0 ? score_of<SIG>(row[id], top, total) : 0.f;
-    float ds = u;
+    // The chosen experts' terms.  Renormalised, a gate depends on the scores' shares of their sum
+    // alone: p_j (u_j - sum p_i u_i), which no sum is too small for (a token's only expert has 1 of
+    // it exactly, and no gradient); the terms add up to 0, so that a softmax has no other ones.
+    float own = SIG ? u * s : u, all = 0.f;
     if (renorm) {
       const float S = warp_sum(s);
-      // (by shares of the sum: a token's only expert has 1 of it exactly, and no gradient)
-      const float mean = warp_sum(S == 0.f ? 0.f : u * (s / S));
-      ds = S == 0.f || id < 0 ? 0.f : (u - mean) / S;
+      const float p = S == 0.f ? 0.f : s / S;
+      own = p * (u - warp_sum(u * p));
+    } else if (!SIG) {
+      all = warp_sum(u * s);
     }
-    const float all = SIG ? 0.f : warp_sum(ds * s);
+    if (SIG) own *= 1.f - s;
 #pragma unroll
     for (int i = 0; i < PL; ++i) sm[lane + 32 * i] = 0.f;
     __syncwarp();
     // (two slots of one expert, which the router does not write, add up)
-    if (id >= 0) atomicAdd(&sm[id], SIG ? ds * s * (1.f - s) : ds);
+    if (id >= 0) atomicAdd(&sm[id], own);
     __syncwarp();
     float* out = dlogits + static_cast<size_t>(t) * Ne;
 #pragma unroll
     for (int i = 0; i < PL; ++i) {
       const int e = lane + 32 * i;
-      if (e < Ne) out[e] = SIG ? sm[e] : score_of<SIG>(z[i], top, total) * (sm[e] - all);
+      if (e < Ne) out[e] = SIG || renorm ? sm[e] : score_of<SIG>(z[i], top, total) * (sm[e] - all);
     }
     __syncwarp();
   }

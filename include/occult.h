@@ -885,11 +885,11 @@ int occult_route_scored(const occult_desc_t* desc, const occult_score_t* opt,
 
 /*
  * occult_route_scored_grad -- gradient of sum_tj dgates_tj * gates_tj with respect to
- * the logits (the choice of experts is piecewise constant).  With u_j = scale dg_j,
- * S = sum_j s_j over the chosen, and ds_j = u_j, or with desc->renorm
- * ds_j = (u_j - sum_i u_i s_i / S) / S (0 where S = 0):
- *   sigmoid  dz_e = sum_{j: id_j = e} ds_j s_e (1 - s_e)
- *   softmax  dz_e = s_e (sum_{j: id_j = e} ds_j - sum_j ds_j s_j)
+ * the logits (the choice of experts is piecewise constant).  With u_j = scale dg_j and,
+ * of the chosen, S = sum_j s_j and the shares p_j = s_j / S (0 where S = 0):
+ *   sigmoid  dz_e = sum_{j: id_j = e} u_j s_e (1 - s_e)
+ *   softmax  dz_e = s_e (sum_{j: id_j = e} u_j - sum_j u_j s_j)
+ *   desc->renorm: dz_e = sum_{j: id_j = e} p_j (u_j - sum_i u_i p_i), by sigmoids times 1 - s_e
  *   ids      int32 [T, k] from occult_route_scored; one outside [0, Ne) takes no part.
  *   dgates   fp32 [T, k] (occult_gate_grad);  dlogits  out fp32 [T, Ne], written.
  * Pointers are 4-byte aligned.

@@ -354,3 +354,55 @@ def test_more_tokens_than_warps(occ, sigmoid):
     S = np.take_along_axis(s, ids.astype(np.int64), 1).sum(axis=1)
     err = (6 * score_err(z) + 60 * U) * (2 * np.abs(dg).max(axis=1) / S)[:, None] * s * 2 + 1e-36
     assert (np.abs(got - want) <= err).all()
+
+
+def grad_of(occ, z, ids, dg, **kw):
+    """The kernel's dlogits for a given choice."""
+    (T, Ne), k = z.shape, ids.shape[1]
+    ds, opt = setup(occ, z, k, 1, **kw)
+    out = torch.full((T * Ne + 8,), float(SENTINEL), device="cuda")
+    occ.occult_route_scored_grad(ds, opt, gpu(z), gpu(ids, torch.int32), gpu(dg), out)
+    torch.cuda.synchronize()
+    assert (out[T * Ne:] == SENTINEL).all()
+    return out[:T * Ne].view(T, Ne).double().cpu().numpy()
+
+
+def chosen(rng, T, Ne, k):
+    return np.stack([rng.permutation(Ne)[:k] for _ in range(T)]).astype(np.int32)
+
+
+@pytest.mark.parametrize("sigmoid", [True, False])
+def test_grad_of_scores_near_the_end_of_the_range(occ, sigmoid):
+    """Chosen scores whose sum is below fp32's normal numbers: shares of it, and no infinity.
+
+    A score is then within a unit of the subnormals, 2^-149, besides its relative error; a
+    sigmoid below 2^-128 is 0 (its exponential is infinite).  With e_j the errors of the
+    scores, a share s_j / S moves by (e_j + share sum e) / S, the mean of the u_i by |u|max
+    times the sum of those.
+    """
+    rng = np.random.default_rng(11)
+    T, Ne, k = 80, 16, 4
+    z = rng.uniform(-88.6, -87.0, size=(T, Ne)).astype(np.float32)
+    ids = chosen(rng, T, Ne, k)
+    if sigmoid:
+        z[::5, ::2] = -100.0          # of scores that are 0 beside these
+        z[1] = -100.0
+        z[2, ids[2, :2]] = -88.3, -88.5
+        ids[2, 2:] = -1
+        known = np.where(z < -88.73, -np.inf, z)
+    else:
+        z[:, 0] = 0.0                 # an expert that the bias keeps out has nearly everything
+        ids = 1 + chosen(rng, T, Ne - 1, k)
+        known = z
+    dg = rng.choice([3.0, -3.0, 0.5], size=(T, k)).astype(np.float32)
+    got = grad_of(occ, z, ids, dg, sigmoid=sigmoid, renorm=True, scale=2.5)
+    assert np.isfinite(got).all()
+    want = scored.grad(known, ids, dg, sigmoid=sigmoid, renorm=True, scale=2.5)
+    s = np.array([scored.scores(r, sigmoid)[0] for r in known])
+    for t in range(T):
+        live = [e for e in ids[t] if e >= 0]
+        S, big = max(s[t, live].sum(), 2.0 ** -149), 2.5 * 2 * np.abs(dg[t]).max()
+        e = score_err(known) * s[t] + 2.0 ** -149
+        err = np.full(Ne, 1e-12)      # (the oracle's own sum of ds s, which is 0, over scores up to 1)
+        err[live] += big * (e[live] + s[t, live] / S * 3 * e[live].sum()) / S + 60 * U * big * s[t, live] / S
+        assert (np.abs(got[t] - want[t]) <= err).all(), (t, np.max(np.abs(got[t] - want[t]) / err))
