@@ -617,15 +617,35 @@ route_scored_grad_kernel(const float* __restrict__ logits, const int32_t* __rest
     const float u = id >= 0 ? scale * dgates[static_cast<size_t>(t) * k + lane] : 0.f;
     const float s = id >= 0 ? score_of<SIG>(row[id], top, total) : 0.f;
     // The chosen experts' terms.  Renormalised, a gate depends on the scores' shares of their sum
-    // alone: p_j (u_j - sum p_i u_i), which no sum is too small for (a token's only expert has 1 of
-    // it exactly, and no gradient); the terms add up to 0, so that a softmax has no other ones.
+    // alone: p_j (u_j - sum p_i u_i), which no sum is too small for; the terms add up to 0, so that a
+    // softmax has no other ones.  Differences are taken from the largest score's u first: where its
+    // share is nearly 1, its own term is as small as the others' together, and u_j less a mean
+    // that is nearly u_j would keep no digit of it (a token's only expert has none, exactly).
     float own = SIG ? u * s : u, all = 0.f;
+    int sure = -1;         // softmax: an expert with more than half of the sum, and its term
+    float sure_term = 0.f;
     if (renorm) {
       const float S = warp_sum(s);
       const float p = S == 0.f ? 0.f : s / S;
-      own = p * (u - warp_sum(u * p));
+      const uint32_t bits = __float_as_uint(s);
+      const int lead = __ffs(__ballot_sync(kFull, bits == __reduce_max_sync(kFull, bits))) - 1;
+      const float base = __shfl_sync(kFull, u, lead);
+      const float v = id >= 0 ? u - base : 0.f;
+      own = p * (v - warp_sum(v * p));
     } else if (!SIG) {
       all = warp_sum(u * s);
+      const uint32_t half = __ballot_sync(kFull, s > 0.5f);
+      if (half) {
+        // the same cancellation: u (1 - s) less the others' u s, 1 - s from the other exponentials
+        sure = __shfl_sync(kFull, id, __ffs(half) - 1);
+        float rest = 0.f;
+#pragma unroll
+        for (int i = 0; i < PL; ++i)
+          if (lane + 32 * i != sure && !(z[i] <= kLowest)) rest += expf(z[i] - top);
+        rest = warp_sum(rest) / total;
+        const float mine = warp_sum(id == sure ? u : 0.f);
+        sure_term = (1.f - rest) * (mine * rest - warp_sum(id == sure ? 0.f : u * s));
+      }
     }
     if (SIG) own *= 1.f - s;
 #pragma unroll
@@ -638,7 +658,8 @@ route_scored_grad_kernel(const float* __restrict__ logits, const int32_t* __rest
 #pragma unroll
     for (int i = 0; i < PL; ++i) {
       const int e = lane + 32 * i;
-      if (e < Ne) out[e] = SIG || renorm ? sm[e] : score_of<SIG>(z[i], top, total) * (sm[e] - all);
+      if (e < Ne)
+        out[e] = SIG || renorm ? sm[e] : e == sure ? sure_term : score_of<SIG>(z[i], top, total) * (sm[e] - all);
     }
     __syncwarp();
   }

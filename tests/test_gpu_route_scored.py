@@ -406,3 +406,68 @@ def test_grad_of_scores_near_the_end_of_the_range(occ, sigmoid):
         err = np.full(Ne, 1e-12)      # (the oracle's own sum of ds s, which is 0, over scores up to 1)
         err[live] += big * (e[live] + s[t, live] / S * 3 * e[live].sum()) / S + 60 * U * big * s[t, live] / S
         assert (np.abs(got[t] - want[t]) <= err).all(), (t, np.max(np.abs(got[t] - want[t]) / err))
+
+
+def grad_bound(z, ids, dg, sigmoid, renorm, scale, rel):
+    """Errors of dlogits relative to what each is the sum of.
+
+    With c = 1 - s of sigmoids and p_j = s_j / S, renormalised: dz_j = p_j c_j (u_j - sum p_i u_i)
+    = p_j c_j sum p_i (u_j - u_i): `rel` of p_j c_j sum p_i |u_j - u_i|, and k + 2 times that, since
+    the differences are taken from the largest share's u (p >= 1 / k) first.  Otherwise, sigmoid:
+    `rel` of itself; softmax: `rel` of s_e (|v_e| (1 - s_e) + sum over the others of |v_i| s_i),
+    v the u of an expert, 0 where it is not chosen.
+    """
+    T, Ne = z.shape
+    err = np.zeros((T, Ne))
+    for t in range(T):
+        s = scored.scores(z[t], sigmoid)[0]
+        live = [(scale * float(u), e) for u, e in zip(dg[t], ids[t]) if e >= 0]
+        c = {e: 1 / (1 + np.exp(float(z[t, e]))) if sigmoid else 1.0 for _, e in live}
+        if renorm:
+            S = sum(s[e] for _, e in live)
+            for u, e in live:
+                err[t, e] = rel * (len(live) + 2) * s[e] / S * c[e] * sum(s[i] / S * abs(u - v) for v, i in live)
+        elif sigmoid:
+            for u, e in live:
+                err[t, e] = rel * abs(u) * s[e] * c[e]
+        else:
+            v = np.zeros(Ne)
+            for u, e in live:
+                v[e] += u
+            rest = np.array([s[np.arange(Ne) != e].sum() for e in range(Ne)])   # 1 - s, without the cancellation
+            rest_v = np.array([(np.abs(v) * s)[np.arange(Ne) != e].sum() for e in range(Ne)])
+            err[t] = rel * s * (np.abs(v) * rest + rest_v)
+    return err
+
+
+@pytest.mark.parametrize("sigmoid", [True, False])
+@pytest.mark.parametrize("renorm", [True, False])
+def test_grad_where_one_expert_has_nearly_all(occ, sigmoid, renorm):
+    """A share, or a softmax's score, within 1e-3 to 1e-11 of 1: its gradient is as small as the
+    others' together, and keeps its digits."""
+    rng = np.random.default_rng(17)
+    T, Ne, k = 96, 60, 5
+    z = rng.normal(size=(T, Ne)).astype(np.float32) - 24
+    ids, dg = chosen(rng, T, Ne, k), rng.normal(size=(T, k)).astype(np.float32)
+    lead = rng.uniform(-14, 2, size=T).astype(np.float32)      # 10 to 26 above the others
+    z[np.arange(T), ids[np.arange(T), np.arange(T) % k]] = lead
+    ids[5] = chosen(rng, 1, Ne, k)      # one that is not chosen may have it
+    kw = dict(sigmoid=sigmoid, renorm=renorm, scale=1.7)
+    got = grad_of(occ, z, ids, dg, **kw)
+    want = np.zeros_like(got)
+    for t in range(T):
+        s, u = scored.scores(z[t], sigmoid)[0], 1.7 * dg[t].astype(np.float64)
+        c = 1 / (1 + np.exp(z[t].astype(np.float64))) if sigmoid else np.ones(Ne)
+        p = s[ids[t]] / s[ids[t]].sum()
+        if renorm:
+            want[t, ids[t]] = p * c[ids[t]] * (p * (u[:, None] - u)).sum(axis=1)
+        elif sigmoid:
+            want[t, ids[t]] = u * s[ids[t]] * c[ids[t]]
+        else:
+            v = np.zeros(Ne)
+            v[ids[t]] = u
+            want[t] = [s[e] * (s * (v[e] - v)).sum() for e in range(Ne)]
+    # (a sum of 60 exponentials besides: 8 u)
+    rel = 6 * score_err(z) + 80 * U
+    off, err = np.abs(got - want), grad_bound(z, ids, dg, rel=rel, **kw) + 1e-37
+    assert (off <= err).all(), np.max(off / err)
