@@ -647,7 +647,8 @@ route_scored_grad_kernel(const float* __restrict__ logits, const int32_t* __rest
         sure_term = (1.f - rest) * (mine * rest - warp_sum(id == sure ? 0.f : u * s));
       }
     }
-    if (SIG) own *= 1.f - s;
+    // 1 - s = e^-z s: the difference keeps no digit of it from logits of 17 on
+    if (SIG && s > 0.f) own *= expf(-row[id]) * s;
 #pragma unroll
     for (int i = 0; i < PL; ++i) sm[lane + 32 * i] = 0.f;
     __syncwarp();

@@ -471,3 +471,27 @@ def test_grad_where_one_expert_has_nearly_all(occ, sigmoid, renorm):
     rel = 6 * score_err(z) + 80 * U
     off, err = np.abs(got - want), grad_bound(z, ids, dg, rel=rel, **kw) + 1e-37
     assert (off <= err).all(), np.max(off / err)
+
+
+@pytest.mark.parametrize("renorm", [True, False])
+def test_grad_of_sure_sigmoids(occ, renorm):
+    """Logits of 8 to 40: 1 - s keeps its digits (the exponential's 4 u, two sums and divisions of
+    u each, s and the products: 24 u; renormalised the shares' errors besides)."""
+    rng = np.random.default_rng(13)
+    T, Ne, k = 120, 32, 4
+    z = rng.uniform(8, 40, size=(T, Ne)).astype(np.float32)
+    z[::3] = rng.uniform(-4, 10, size=z[::3].shape)
+    z[1::3, ::2] -= 40
+    ids, dg = chosen(rng, T, Ne, k), rng.normal(size=(T, k)).astype(np.float32)
+    kw = dict(sigmoid=True, renorm=renorm, scale=1.7)
+    got = grad_of(occ, z, ids, dg, **kw)
+    # (the formula with 1 - s as 1 / (1 + e^z))
+    want = np.zeros_like(got)
+    for t in range(T):
+        s = scored.scores(z[t], True)[0][ids[t]]
+        u = 1.7 * dg[t].astype(np.float64)
+        c = 1 / (1 + np.exp(z[t, ids[t]].astype(np.float64)))
+        p = s / s.sum()
+        want[t, ids[t]] = p * c * (p * (u[:, None] - u)).sum(axis=1) if renorm else u * s * c
+    rel = 6 * score_err(z) + 60 * U if renorm else 24 * U
+    assert (np.abs(got - want) <= grad_bound(z, ids, dg, rel=rel, **kw) + 1e-37).all()
