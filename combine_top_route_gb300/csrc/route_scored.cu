@@ -12,9 +12,12 @@
 // one, the upper bits of the logits.  Places nearer to each other than that (a few tokens
 // in ten thousand, one in a hundred without a bias) are put in order by their logits, or
 // by their ranks in fp64 where there is a bias: one exponential on the lanes that hold the
-// candidates.  Two worths too near at the border of the kept groups (one token in 10^5)
-// send that token through the whole choice in fp64.  fp64 for every token would cost more
-// than the rest together: the chip has two fp64 lanes an SM.
+// candidates.  Two worths within some 4e-6 at the border of the kept groups are made again in
+// fp64, from the candidates of these two groups where they are few, else by the whole choice in
+// fp64: one token in 10^5 of logits of deviation 1, and more of wider ones, most of whose worths
+// are that small (of one best score without a bias none: its logit orders as it does).
+// fp64 for every token would cost more than the rest together: the chip has two fp64 lanes
+// an SM.
 //
 // Instructions bound the choice, not its bytes: 32768 tokens x 256 experts in 8 groups, 4
 // of them and 8 experts kept, sigmoid with a bias, take 34 us (33.5 MB of logits, 5 us at
@@ -52,9 +55,6 @@ __device__ __forceinline__ uint32_t order_bits(float v) {
 __device__ __forceinline__ uint64_t order_bits64(double v) {
   const uint64_t u = static_cast<uint64_t>(__double_as_longlong(v + 0.));
   return (u >> 63) ? ~u : u | (1ull << 63);
-}
-__device__ __forceinline__ double from_bits64(uint64_t u) {
-  return __longlong_as_double(static_cast<long long>((u >> 63) ? u & ~(1ull << 63) : ~u));
 }
 __device__ __forceinline__ uint64_t shfl_xor64(uint64_t v, int o) {
   return static_cast<uint64_t>(__shfl_xor_sync(kFull, static_cast<unsigned long long>(v), o));
@@ -109,21 +109,67 @@ __device__ __forceinline__ float score_of(float z, float top, float total) {
 // An fp64 instruction takes a warp 64 cycles of its scheduler here, a logistic function
 // some fifty of them; comparisons are made on integers of the same order.
 
-// The worth of a group of lanes from the best two (as ordered integers, 0: none).
-__device__ __forceinline__ uint64_t group_worth(uint64_t b1, uint64_t b2, int group_lanes, int best) {
-  for (int o = 1; o < group_lanes; o <<= 1) {
-    const uint64_t c1 = shfl_xor64(b1, o), c2 = shfl_xor64(b2, o);
-    const uint64_t lo = min(b1, c1);
-    b2 = max(max(b2, c2), lo);
-    b1 = max(b1, c1);
+// A score as the sum of `whole` and `rest`: a sigmoid above a half is 1 less its complement, so
+// that the rests of z and -z cancel and sigmoid(x) + sigmoid(-x) is 1 for every x.
+struct Score64 {
+  double whole, rest;
+  __device__ __forceinline__ double value() const { return whole + rest; }
+};
+template <bool SIG>
+__device__ __forceinline__ Score64 score64(float z, float top, double inv) {
+  if (!SIG) return {0., exp(static_cast<double>(z) - static_cast<double>(top)) * inv};
+  const double c = 1. / (1. + exp(fabs(static_cast<double>(z))));
+  return z > 0.f ? Score64{1., -c} : Score64{0., c};
+}
+// Rank of an expert that is on, as an ordered integer: by score and bias, without a bias by its
+// logit, which no score is too near 0 or 1 for.  A NaN ranks below every number.
+template <bool SIG>
+__device__ __forceinline__ uint64_t rank64(float z, int e, const float* bias, float top, double inv) {
+  if (!bias) return order_bits64(static_cast<double>(z));
+  const double v = score64<SIG>(z, top, inv).value() + static_cast<double>(bias[e]);
+  return order_bits64(v == v ? v : static_cast<double>(OCCULT_NEG_INF));
+}
+
+// The worth of a group, as two ordered integers: the sum of its scores and biases in fp64, and
+// what that sum's rounding left out.  All 0: no expert that is on.
+struct Worth {
+  uint64_t hi, lo;
+  __device__ __forceinline__ bool above(const Worth& o) const { return hi > o.hi || (hi == o.hi && lo > o.lo); }
+  __device__ __forceinline__ bool same(const Worth& o) const { return hi == o.hi && lo == o.lo; }
+  __device__ __forceinline__ Worth of(int lane) const { return {shfl64(hi, lane), shfl64(lo, lane)}; }
+};
+
+// Worth of a group of lanes from the best two of each: ranks r1, r2 (0: none) of experts e1, e2,
+// equal ranks by the lower expert.  One best score without a bias orders as its logit.
+template <bool SIG>
+__device__ __forceinline__ Worth group_worth(uint64_t r1, uint64_t r2, int e1, int e2, const RouteArgs& a,
+                                             const float* row, const float* bias, float top, double inv) {
+  for (int o = 1; o < a.group_lanes; o <<= 1) {
+    const uint64_t q1 = shfl_xor64(r1, o), q2 = shfl_xor64(r2, o);
+    const int f1 = __shfl_xor_sync(kFull, e1, o), f2 = __shfl_xor_sync(kFull, e2, o);
+    const bool theirs = q1 > r1 || (q1 == r1 && f1 < e1);
+    // behind the first: the other lane's first, or the second of its own lane
+    const uint64_t s1 = theirs ? r1 : q1, s2 = theirs ? q2 : r2;
+    const int g1 = theirs ? e1 : f1, g2 = theirs ? f2 : e2;
+    const bool second = s2 > s1 || (s2 == s1 && g2 < g1);
+    r2 = second ? s2 : s1;
+    e2 = second ? g2 : g1;
+    if (theirs) { r1 = q1; e1 = f1; }
   }
-  if (b1 == 0) return 0;
-  double w = from_bits64(b1);
-  if (best == 2 && b2 != 0) w += from_bits64(b2);
-  // as multiples of 2^-48: sums that the formula makes equal, as sigmoid(x) +
-  // sigmoid(-x) = 1 for every x, then do not hang on the last bits of exp
-  if (fabs(w) < 256.) w = rint(w * 0x1p48) * 0x1p-48;
-  return order_bits64(w);
+  if (r1 == 0) return {0, 0};
+  if (!bias && a.best == 1) return {r1, 0};
+  Score64 s = score64<SIG>(row[e1], top, inv);
+  if (bias) s.whole += static_cast<double>(bias[e1]);
+  if (a.best == 2 && r2 != 0) {
+    const Score64 n = score64<SIG>(row[e2], top, inv);
+    s.whole += n.whole + (bias ? static_cast<double>(bias[e2]) : 0.);
+    s.rest += n.rest;
+  }
+  const double sum = s.whole + s.rest, back = sum - s.whole;
+  const double left = (s.whole - (sum - back)) + (s.rest - back);   // (exactly what the sum left out)
+  if (!(fabs(sum) < 1e300))   // biases that are no numbers or infinite
+    return {order_bits64(sum == sum ? sum : static_cast<double>(OCCULT_NEG_INF)), order_bits64(0.)};
+  return {order_bits64(sum), order_bits64(left)};
 }
 
 // The whole choice of one token, ranks and worths as doubles.  Returns slot `lane`'s
@@ -144,6 +190,8 @@ __device__ __noinline__ int choose_exactly(const RouteArgs& a, const float* row,
 #pragma unroll
     for (int i = 0; i < PL; ++i) top = fmaxf(top, z[i]);
     top = warp_max(top);
+  }
+  if (!SIG && a.bias) {   // (without a bias the total is a common factor: left out)
     double total = 0.;
     for (int i = 0; i < PL; ++i)
       if (!is_off(z[i])) total += exp(static_cast<double>(z[i]) - static_cast<double>(top));
@@ -151,26 +199,23 @@ __device__ __noinline__ int choose_exactly(const RouteArgs& a, const float* row,
     inv = 1. / total;
   }
   uint64_t b1 = 0, b2 = 0;
+  int e1 = 0x7fffffff, e2 = 0x7fffffff;
 #pragma unroll 1
   for (int i = 0; i < PL; ++i) {
     const int e = s_exp[lane * PL + i];
     r[i] = 0;
     if (is_off(z[i])) continue;
-    double v = SIG ? 1. / (1. + exp(-static_cast<double>(z[i])))
-                   : exp(static_cast<double>(z[i]) - static_cast<double>(top)) * inv;
-    if (a.bias) v += static_cast<double>(a.bias[e]);
-    // a NaN ranks below every number
-    r[i] = order_bits64(v == v ? v : static_cast<double>(OCCULT_NEG_INF));
-    if (r[i] > b1) { b2 = b1; b1 = r[i]; } else if (r[i] > b2) b2 = r[i];
+    r[i] = rank64<SIG>(z[i], e, a.bias, top, inv);
+    if (r[i] > b1) { b2 = b1; e2 = e1; b1 = r[i]; e1 = e; } else if (r[i] > b2) { b2 = r[i]; e2 = e; }
   }
   bool in = true;
   if (a.G > 1) {
-    const uint64_t worth = group_worth(b1, b2, a.group_lanes, a.best);
+    const Worth worth = group_worth<SIG>(b1, b2, e1, e2, a, row, a.bias, top, inv);
     const int mine = lane / a.group_lanes;
     int place = 0;
     for (int g = 0; g < a.G; ++g) {
-      const uint64_t w = shfl64(worth, g * a.group_lanes);
-      place += (w > worth || (w == worth && g < mine)) ? 1 : 0;
+      const Worth w = worth.of(g * a.group_lanes);
+      place += (w.above(worth) || (w.same(worth) && g < mine)) ? 1 : 0;
     }
     in = mine < a.G && place < a.keep;
   }
@@ -178,9 +223,7 @@ __device__ __noinline__ int choose_exactly(const RouteArgs& a, const float* row,
 #pragma unroll 1
   for (int i = 0; i < PL; ++i) {
     const int e = s_exp[lane * PL + i];
-    r[i] = e < 0 || !in ? 0
-         : is_off(z[i]) ? 1
-         : a.bias ? r[i] : static_cast<uint64_t>(order_bits(z[i]));
+    r[i] = e < 0 || !in ? 0 : is_off(z[i]) ? 1 : r[i];
   }
   int mine = 0;
   uint32_t gone = 0;
@@ -208,28 +251,24 @@ __device__ __noinline__ int choose_exactly(const RouteArgs& a, const float* row,
 
 // The border of the kept groups, `last` the last kept and `next` the first left out, whose
 // worths fp32 cannot tell apart: made again in fp64 from the experts of these two that can
-// be among their best (`e1`, `e2`: a lane's two, where `c1`, `c2`).
+// be among their best (`e1`, `e2`: a lane's two, where `c1`, `c2`).  (Not for softmax with a bias,
+// which needs the total.)
 // True: the group left out is the better one.
 template <bool SIG, bool BIAS>
 __device__ __noinline__ bool next_is_better(const RouteArgs& a, const float* row, const float* s_bias,
                                             float top, int e1, int e2, bool c1, bool c2, int last,
                                             int next) {
-  auto rank = [&](int e, bool c) -> uint64_t {
-    if (!__any_sync(kFull, c)) return 0;
-    uint64_t r = 0;
-    if (c) {
-      const double z = static_cast<double>(row[e]);
-      // (without a bias a softmax's total is a common factor: left out)
-      double v = SIG ? 1. / (1. + exp(-z)) : exp(z - static_cast<double>(top));
-      if (BIAS) v += static_cast<double>(s_bias[e]);
-      r = order_bits64(v);
-    }
-    return r;
-  };
-  const uint64_t r1 = rank(e1, c1), r2 = rank(e2, c2);
-  const uint64_t worth = group_worth(max(r1, r2), min(r1, r2), a.group_lanes, a.best);
-  const uint64_t w0 = shfl64(worth, last * a.group_lanes), w1 = shfl64(worth, next * a.group_lanes);
-  return w1 > w0 || (w1 == w0 && next < last);
+  const float* bias = BIAS ? s_bias : nullptr;
+  uint64_t r1 = c1 ? rank64<SIG>(row[e1], e1, bias, top, 1.) : 0, r2 = c2 ? rank64<SIG>(row[e2], e2, bias, top, 1.) : 0;
+  if (r2 > r1 || (r2 == r1 && e2 < e1)) {
+    const uint64_t r = r1;
+    const int e = e1;
+    r1 = r2; e1 = e2;
+    r2 = r; e2 = e;
+  }
+  const Worth worth = group_worth<SIG>(r1, r2, e1, e2, a, row, bias, top, 1.);
+  const Worth w0 = worth.of(last * a.group_lanes), w1 = worth.of(next * a.group_lanes);
+  return w1.above(w0) || (w1.same(w0) && next < last);
 }
 
 template <int PL>
@@ -305,7 +344,7 @@ __device__ __noinline__ bool order_near(uint32_t (&key)[PL], uint32_t mine, int 
     z = row[my_id];
     if (BIAS) {
       if (SIG) {
-        v = 1. / (1. + exp(-static_cast<double>(z)));
+        v = score64<SIG>(z, top, 1.).value();
       } else {
         v = exp(static_cast<double>(z) - static_cast<double>(top)) * (1. / static_cast<double>(total));
         p = static_cast<float>(v);
@@ -473,7 +512,9 @@ route_scored_kernel(const RouteArgs a) {
 
     bool exact = odd;
     if (a.G > 1) {
-      // the group's best two: with a bias from the words, else from the scores
+      // the group's best two: with a bias from the words, else from the scores, the one best by its
+      // logit, which orders as its score does and needs no other look
+      const bool by_logit = !BIAS && a.best == 1;
       float b1 = kLowest, b2 = kLowest;
       if (BIAS) {
         const float back = span / 8388600.f;
@@ -483,7 +524,7 @@ route_scored_kernel(const RouteArgs a) {
       } else {
 #pragma unroll
         for (int i = 0; i < PL; ++i) {
-          const float r = is_off(z[i]) ? kLowest : s[i];
+          const float r = is_off(z[i]) ? kLowest : by_logit ? z[i] : s[i];
           b2 = fmaxf(b2, fminf(b1, r));
           b1 = fmaxf(b1, r);
         }
@@ -505,7 +546,7 @@ route_scored_kernel(const RouteArgs a) {
         g_last = (__ffs(__ballot_sync(kFull, wkey == last)) - 1) >> a.group_shift;
         if (my_group == g_last) { wkey = 0; in = 1; }
       }
-      if (a.keep < a.G) {
+      if (a.keep < a.G && !by_logit) {
         auto unbits = [](uint32_t u) { return __uint_as_float((u & 0x80000000u) ? u & 0x7fffffffu : ~u); };
         const uint32_t next = __reduce_max_sync(kFull, wkey);
         const float w0 = unbits(last), w1 = unbits(next);

@@ -874,9 +874,9 @@ typedef struct occult_score {
  *   bias    fp32 [Ne] nullable; a NaN puts its expert behind every other that is on.
  *   expert_to_vdev  int32 [Ne] device of each expert, each with Ne/Nd of them.
  *   ids, gates, vmask  out, as occult_route: for occult_build_brim.
- * The choice is that of the formula to 64 bits: ranks and worths too near for fp32
- * are compared in fp64, worths as multiples of 2^-48 (on which sigmoid(x) + sigmoid(-x)
- * is 1 for every x).
+ * The choice is that of the formula to 64 bits: ranks and worths too near for fp32 are
+ * compared in fp64, sums of scores with sigmoid(x) + sigmoid(-x) = 1 for every x, and the one
+ * best score of a group without a bias as its logit.
  * Pointers are 4-byte aligned.
  */
 int occult_route_scored(const occult_desc_t* desc, const occult_score_t* opt,

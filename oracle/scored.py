@@ -3,10 +3,12 @@
 Scores are the logistic function or the softmax of the logits; a logit of -inf, of
 fp32's lowest value or NaN switches its expert off.  Experts are chosen by score plus
 bias (by logit where there is no bias) within the groups of largest worth; equal ranks
-go to the lower id (worths are compared as multiples of 2^-48, on which sigmoid(x) +
-sigmoid(-x) is 1 for every x).  Gates are the chosen scores, renormalised on request, scaled.
+and worths go to the lower id.  Gates are the chosen scores, renormalised on request, scaled.
 """
 from __future__ import annotations
+
+import math
+from fractions import Fraction
 
 import numpy as np
 
@@ -19,24 +21,53 @@ def scores(z, sigmoid):
     on = z > LOWEST
     s = np.zeros(len(z))
     if sigmoid:
-        s[on] = 1.0 / (1.0 + np.exp(-z[on]))
+        small = 1.0 / (1.0 + np.exp(np.minimum(np.abs(z[on]), 700.0)))   # of -|z|
+        s[on] = np.where(z[on] > 0, 1.0 - small, np.where(z[on] < -700, 0.0, small))
     elif on.any():
         e = np.exp(z[on] - z[on].max())
         s[on] = e / e.sum()
     return s, on
 
 
+def worth_of(z, s, bias, best, sigmoid):
+    """Worth of a group from its experts that are on: the exact sum of its best scores and biases.
+
+    A sigmoid above a half is 1 less its complement, so that sigmoid(x) + sigmoid(-x) is 1 for
+    every x.  Without a bias scores order as the logits do, which no range of numbers ends; the
+    one best score of a group is then given by its logit.
+    """
+    if len(z) == 0:
+        return -math.inf
+    rank = z if bias is None else [a + b if a + b == a + b else -math.inf for a, b in zip(s, bias)]
+    if best == 1 and bias is None:
+        return max(z)
+    terms = []
+    for i in sorted(range(len(z)), key=lambda i: (-rank[i], i))[:best]:
+        if sigmoid:
+            rest = 1.0 / (1.0 + math.exp(abs(z[i]))) if abs(z[i]) < 700 else 0.0
+            terms += [1.0, -rest] if z[i] > 0 else [rest]
+        else:
+            terms.append(float(s[i]))
+        if bias is not None:
+            terms.append(float(bias[i]))
+    if not all(map(math.isfinite, terms)):
+        w = sum(terms)
+        return w if w == w else -math.inf
+    return sum(map(Fraction, terms))
+
+
 def choose(z, bias, groups, keep, best, k, sigmoid):
     """The k experts of one token; ``groups``: group of every expert."""
     s, on = scores(z, sigmoid)
+    z = np.asarray(z, dtype=np.float64)
     total = s if bias is None else s + np.asarray(bias, dtype=np.float64)
-    rank = np.asarray(z, dtype=np.float64) if bias is None else total
+    total = np.where(np.isnan(total), -np.inf, total)
+    rank = z if bias is None else total
     G = max(groups) + 1
     worth = []
     for g in range(G):
-        mine = sorted((total[e] for e in range(len(z)) if groups[e] == g and on[e]), reverse=True)
-        w = sum(mine[:best]) if mine else -np.inf
-        worth.append(np.rint(w * 2.0 ** 48) * 2.0 ** -48 if abs(w) < 256 else w)
+        mine = [e for e in range(len(z)) if groups[e] == g and on[e]]
+        worth.append(worth_of(z[mine], s[mine], None if bias is None else [bias[e] for e in mine], best, sigmoid))
     kept = sorted(range(G), key=lambda g: (-worth[g], g))[:keep]
     level = [2 if groups[e] not in kept else 0 if on[e] else 1 for e in range(len(z))]
     order = sorted(range(len(z)), key=lambda e: (level[e], -rank[e] if level[e] == 0 else 0.0, e))

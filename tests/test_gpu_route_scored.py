@@ -495,3 +495,51 @@ def test_grad_of_sure_sigmoids(occ, renorm):
         want[t, ids[t]] = p * c * (p * (u[:, None] - u)).sum(axis=1) if renorm else u * s * c
     rel = 6 * score_err(z) + 60 * U if renorm else 24 * U
     assert (np.abs(got - want) <= grad_bound(z, ids, dg, rel=rel, **kw) + 1e-37).all()
+
+
+@pytest.mark.parametrize("Ne,G,keep,k", [(64, 8, 4, 6), (48, 3, 2, 4), (256, 8, 4, 8), (60, 4, 1, 4)])
+@pytest.mark.parametrize("best", [1, 2])
+def test_groups_of_small_worth(occ, Ne, G, keep, k, best):
+    """Groups whose scores all lie far below the largest, or far below 1: still by their worth."""
+    rng = np.random.default_rng(Ne + best)
+    for spread in (10.0, 30.0):
+        z = (rng.normal(size=(150, Ne)) * spread).astype(np.float32)
+        for sigmoid in (False, True):
+            for by_vdev in (False, True):
+                check(occ, z, k, G if by_vdev else 4, None, sigmoid=sigmoid, n_groups=G, keep=keep, best=best,
+                      by_vdev=by_vdev)
+    for low in (-45.0, -80.0):
+        z = (low + rng.normal(size=(150, Ne))).astype(np.float32)
+        check(occ, z, k, 4, None, n_groups=G, keep=keep, best=best)
+        check(occ, z, k, 4, None, sigmoid=False, n_groups=G, keep=keep, best=best)
+    # one group of eight equal logits, and two whose best are a factor e apart, 33 below
+    z = np.full((4, 48), -60.0, np.float32)
+    z[:, :8], z[:, 20], z[:, 40] = 0.0, -34.0, -33.0
+    z[1, [21, 41]] = -34.0, -33.0
+    z[2, [20, 40]], z[3, [20, 40]] = (-33.0, -34.0), (-34.0, -34.0)
+    for sigmoid in (False, True):
+        ids = check(occ, z, 9, 4, None, sigmoid=sigmoid, n_groups=3, keep=2, best=best, renorm=False)
+        assert ids[:, 8].tolist() == [40, 40, 20, 20]
+
+
+@pytest.mark.parametrize("biased", [True, False])
+def test_groups_of_equal_worth(occ, biased):
+    """sigmoid(x) + sigmoid(-x) is 1 for every x: such groups are equal, and the lower one is kept,
+    whatever the bias of the pair adds up to; a hair more and the higher one is."""
+    rng = np.random.default_rng(19)
+    T, G, per = 200, 8, 4
+    x = rng.uniform(0, 12, size=(T, G)).astype(np.float32)
+    z = np.full((T, G, per), -np.inf, np.float32)
+    z[:, :, 1], z[:, :, 3] = x, -x
+    bias = np.zeros((G, per), np.float32)
+    if biased:     # halves and quarters that cancel in every pair, whichever stands first
+        b = rng.integers(-3, 4, size=G).astype(np.float32) / 4
+        bias[:, 1], bias[:, 3] = 3 + b, 3 - b
+    kw = dict(n_groups=G, keep=3, best=2, renorm=False)
+    z, bias = z.reshape(T, -1), bias.reshape(-1) if biased else None
+    ids = check(occ, z, 6, 4, bias, **kw)
+    assert (np.sort(ids, axis=1) == [1, 3, 5, 7, 9, 11]).all()
+    up = z.copy()
+    up[:, 7 * per + 3] += np.maximum(np.abs(up[:, 7 * per + 3]), 1) * np.float32(2.0 ** -20)
+    ids = check(occ, up, 6, 4, bias, **kw)
+    assert (np.sort(ids, axis=1) == [1, 3, 5, 7, 29, 31]).all()

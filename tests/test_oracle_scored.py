@@ -58,3 +58,18 @@ def test_choices():
 def test_bias_step():
     b = scored.bias_step(np.zeros(4), [[3, 1, 0, 4], [1, 1, 0, 6]], 0.1)
     np.testing.assert_allclose(b, [0.0, 0.1, 0.1, -0.1])
+
+
+@pytest.mark.parametrize("best", [1, 2])
+def test_worths_of_any_size(best):
+    """Groups are kept by their worth however small it is, and true ties fall to the lower one."""
+    e2v = np.zeros(6, int)
+    kw = dict(n_groups=3, keep=2, best=best)
+    z = np.array([[0.0, -1, -70, -71, -69.5, -71], [0.0, -1, -69.5, -71, -69.5, -71], [-80.0, -90, -90, -81, -79, -90]])
+    for sigmoid in (True, False):
+        ids = scored.route(z, 4, e2v, sigmoid=sigmoid, **kw)[0]
+        assert np.sort(ids, axis=1).tolist() == [[0, 1, 4, 5], [0, 1, 2, 3], [0, 1, 4, 5]]
+    # x and -x: 1 for every x
+    z = np.array([[3.3, -3.3, 0.0, 0.0, 17.7, -17.7]])
+    assert scored.route(z, 4, e2v, n_groups=3, keep=2, best=2)[0].tolist() == [[0, 2, 3, 1]]
+    assert scored.route(z, 2, e2v, n_groups=3, keep=1, best=1)[0].tolist() == [[4, 5]]
