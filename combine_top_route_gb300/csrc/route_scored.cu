@@ -472,6 +472,7 @@ route_scored_kernel(const RouteArgs a) {
       for (int i = 0; i < PL; ++i) z[i] = ex[i] >= 0 ? row[ex[i]] : kLowest;
     }
     float top = 0.f, total = 1.f, s[PL];
+    bool no_number = false;   // a softmax's row with a NaN logit
     if (!SIG) {
       top = kLowest;
 #pragma unroll
@@ -485,6 +486,16 @@ route_scored_kernel(const RouteArgs a) {
         total += s[i];
       }
       total = warp_sum(total);
+      no_number = !(total == total);
+      if (no_number) {   // the choice goes by the scores of the others; the gates are NaN
+        total = 0.f;
+#pragma unroll
+        for (int i = 0; i < PL; ++i) {
+          if (is_off(z[i])) s[i] = 0.f;
+          total += s[i];
+        }
+        total = warp_sum(total);
+      }
       const float inv = total > 0.f ? 1.f / total : 0.f;
 #pragma unroll
       for (int i = 0; i < PL; ++i) s[i] *= inv;
@@ -598,6 +609,7 @@ route_scored_kernel(const RouteArgs a) {
     if (exact) my_id = choose_exactly<SIG, PL>(a, row, s_exp);
     if (my_id < 0 || my_id >= a.Ne) my_id = 0;   // (devices that do not share the experts evenly)
 
+    if (!SIG && no_number) total = __int_as_float(0x7fc00000);
     float g = lane < a.k ? score_of<SIG>(row[my_id], top, total) : 0.f;
     if (a.renorm) {
       const float sum = warp_sum(g);

@@ -543,3 +543,26 @@ def test_groups_of_equal_worth(occ, biased):
     up[:, 7 * per + 3] += np.maximum(np.abs(up[:, 7 * per + 3]), 1) * np.float32(2.0 ** -20)
     ids = check(occ, up, 6, 4, bias, **kw)
     assert (np.sort(ids, axis=1) == [1, 3, 5, 7, 29, 31]).all()
+
+
+@pytest.mark.parametrize("biased", [True, False])
+@pytest.mark.parametrize("sigmoid", [True, False])
+@pytest.mark.parametrize("G,keep,best", [(1, 1, 1), (4, 2, 1), (4, 2, 2)])
+def test_nan_logits_rank_as_switched_off(occ, biased, sigmoid, G, keep, best):
+    """A NaN logit leaves the choice among its row's other experts as if it were -inf; a
+    softmax's gates of that row are NaN, as the formula's are, a sigmoid's others what they are."""
+    rng = np.random.default_rng(23)
+    z = logits_of(90, 64, 9)
+    nan = rng.random(z.shape) < 0.1
+    nan[::3] = False
+    nan[1, 1:] = True
+    bias = (rng.normal(size=64) * 0.05).astype(np.float32) if biased else None
+    kw = dict(sigmoid=sigmoid, n_groups=G, keep=keep, best=best, renorm=False)
+    want = check(occ, np.where(nan, np.float32(-np.inf), z), 6, 4, bias, **kw)
+    ids, gates, _ = run(occ, np.where(nan, np.float32(np.nan), z), 6, place(64, 4), 4, bias, **kw)
+    assert (ids == want).all()
+    bad = np.take_along_axis(nan, want, 1)      # (chosen where nothing else is left)
+    if sigmoid:
+        assert (np.isnan(gates) == bad).all()
+    else:
+        assert (np.isnan(gates) == nan.any(axis=1)[:, None]).all()
