@@ -360,7 +360,7 @@ head_sum_kernel(HeadCounts* cnt, const HeadLossOut o, const float* __restrict__ 
 // ---- gradient of the logits -----------------------------------------------------------
 struct DzArgs {
   const HeadCounts* cnt;
-  const float *pm, *tops, *l1, *l2;
+  const float *pk, *tops, *l1, *l2;
   const uint8_t* flag;
   int ldp, row0, piece, V, ld;
   float inv_tau, q_step, coef, coef_kd, coef_z, tau;
@@ -377,8 +377,9 @@ __device__ __forceinline__ void row_factors(const DzArgs& a, const HeadScale& sc
   }
 }
 
-// bf16 layers: the kept 16-bit logits (units of q_step octaves below the maximum of
-// their 128 columns) become bf16 gradients where they lie.  A warp takes 16 rows of 128
+// bf16 layers: the kept 16-bit logits (units of q_step octaves below the largest of their
+// 128 columns that is no entry, the last one for all that lies lower: no probability) become
+// bf16 gradients where they lie.  A warp takes 16 rows of 128
 // columns, 16 lanes a row's 256 bytes, all of its loads in flight at once.
 constexpr int kDzRows = 16;
 __global__ void __launch_bounds__(256)
@@ -404,8 +405,7 @@ head_dz_bf16_kernel(const DzArgs a, uint16_t* __restrict__ kept) {
     const int r = r0 + (lane & (kDzRows - 1));
     float m = 0.f, L1 = 0.f, L2 = 0.f, k1 = 0.f, k2 = 0.f;
     if (r < n) {
-      m = a.pm[static_cast<size_t>(h) * a.ldp + r];
-      m = (m == -__int_as_float(0x7f800000) ? 0.f : m) + 65536.f * a.q_step;
+      m = a.pk[static_cast<size_t>(h) * a.ldp + r] + 65536.f * a.q_step;
       const float top = a.tops[a.row0 + r];
       L1 = top + a.l1[a.row0 + r];
       L2 = fmaf(top, a.inv_tau, a.l2[a.row0 + r]);
@@ -429,7 +429,7 @@ head_dz_bf16_kernel(const DzArgs a, uint16_t* __restrict__ kept) {
         // 65536 + q by its bits: the conversion unit is the exponentials' as well
         const float q = __uint_as_float(0x47800000u | (j & 1 ? (wds[j >> 1] >> 9) & 0x7fff80u
                                                              : (wds[j >> 1] & 0xffffu) << 7));
-        const float y = fmaf(q, -a.q_step, mm);
+        const float y = q == 131071.f ? -__int_as_float(0x7f800000) : fmaf(q, -a.q_step, mm);
         g[j] = ka * ex2(y - La);
         if (a.two) g[j] = fmaf(kb, ex2(fmaf(y, a.inv_tau, -Lb)), g[j]);
       }
@@ -658,6 +658,7 @@ HeadPlan head_plan(const occult_desc_t& ds, const occult_head_t& opt, bool step)
   p.o_xc = take(T * p.d * (bf ? 2 : 4));
   p.o_m = take(4 * P * p.halves); p.o_s = take(4 * P * p.halves);
   p.o_s2 = take(p.two ? 4 * P * p.halves : 0);
+  p.o_mk = take(bf && step ? 4 * P * p.halves : 0);
   p.o_top = take(4 * T); p.o_l1 = take(4 * T); p.o_l2 = take(4 * T);
   p.o_sum = take(12 * (T / 32 + p.n_pieces));
   p.o_kept = take(step ? P * row_bytes : 0);
@@ -724,7 +725,7 @@ int launch_head(const LaunchCtx& ctx, const HeadPlan& p, const HeadArgs& a) {
     block0 += blocks;
     if (!p.step) continue;
     DzArgs z{};
-    z.cnt = cnt; z.pm = pm; z.tops = tops; z.l1 = l1; z.l2 = l2; z.flag = flag;
+    z.cnt = cnt; z.pk = reinterpret_cast<const float*>(ws + p.o_mk); z.tops = tops; z.l1 = l1; z.l2 = l2; z.flag = flag;
     z.ldp = p.piece; z.row0 = row0; z.piece = p.piece; z.V = p.V; z.ld = p.ld;
     z.inv_tau = 1.f / p.tau; z.q_step = p.q_step; z.tau = p.tau;
     z.coef = p.coef; z.coef_kd = p.coef_kd; z.coef_z = p.coef_z;

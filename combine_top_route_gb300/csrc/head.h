@@ -37,7 +37,7 @@ struct HeadPlan {
   float tau, coef, coef_kd, coef_z;
   float q_step;             // octaves of a unit of the kept 16-bit logits
   // workspace
-  size_t o_cnt, o_tally, o_idx, o_flag, o_ent, o_q, o_zt, o_xc, o_m, o_s, o_s2, o_top, o_l1, o_l2, o_sum,
+  size_t o_cnt, o_tally, o_idx, o_flag, o_ent, o_q, o_zt, o_xc, o_m, o_s, o_s2, o_mk, o_top, o_l1, o_l2, o_sum,
       o_kept, o_part, o_acc, total;
 };
 

@@ -4,9 +4,14 @@
 //           the maximum and the sum of powers of two of every row's 128 columns, picks
 //           out the logits of the row's entries (its label and teacher tokens, sorted, so
 //           that a tile looks its first one up and walks on), and for a training step
-//           keeps the logits in 16 bits: octaves below the part's maximum, in steps fine
-//           enough (3.7e-4 octaves at temperature 1) that a probability is within 1.3e-4
-//           of itself, a thirtieth of bf16's rounding of the gradient made from it.
+//           keeps the logits in 16 bits: octaves below the largest of the part that is no
+//           entry (an entry's gradient is made from its own fp32 logit), in steps s of
+//           max(24, 20 tau) / 65535, the last of them for all that lies lower.  A probability
+//           is within s ln 2 / 2 of itself (over tau where tempered): 1.3e-4 up to tau = 1.2,
+//           a thirtieth of bf16's rounding of the gradient made from it, 2.1e-4 at 2, 1.1e-3
+//           at 10; below the range, 2^-24 of the part's largest (2^-20 tempered), it is 0.
+//           Entries would take the range away from the others: of a token sure of its label
+//           the other tokens' probabilities are all its gradient is made of.
 //   gradients  dx = dz w over the vocabulary (cut into parts where its tiles would not
 //           go round) and dw = dz^T x over the rows, the tiles of both in one launch: dx's
 //           first, dealt in turn, then dw's, of which pairs that got one dx tile less
@@ -66,7 +71,7 @@ struct GemmArgs {
   const int32_t* ent;
   float* zt;
   int E;
-  float *pm, *ps, *ps2;
+  float *pm, *ps, *ps2, *pk;   // parts' maxima and sums; pk: the kept logits' upper ends
   int ldp, ld;
   uint16_t* kept;
   float inv_tau, q_inv;
@@ -442,30 +447,53 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
           for (int j = 0; j < 128; ++j)
             if (j >= lim) z[j] = NEG;
         }
-        // the maximum, and the entries' logits
-        float m = NEG;
+        // the maximum, the entries' logits, and (kept) the maximum of the others
+        float m = NEG, mk = NEG;
 #pragma unroll
         for (int c = 0; c < 128; c += 32) {
+          float top = NEG;
 #pragma unroll
-          for (int j = 0; j < 32; ++j) m = fmaxf(m, z[c + j]);
+          for (int j = 0; j < 32; ++j) top = fmaxf(top, z[c + j]);
+          m = fmaxf(m, top);
           const int end = c0 + min(c + 32, lim);
           if (c < lim && __any_sync(0xffffffffu, next < end)) {
 #pragma unroll
             for (int j = 0; j < 8; ++j)
               *reinterpret_cast<float4*>(own_piece(buf, j)) =
                   make_float4(z[c + 4 * j], z[c + 4 * j + 1], z[c + 4 * j + 2], z[c + 4 * j + 3]);
-            while (next < end) {
-              const int at = next - c0 - c;
-              zt[e] = __uint_as_float(own_piece(buf, at >> 2)[at & 3]);
+            bool again = false;
+            float v = NEG;
+            for (int id = -1; next < end;) {
+              if (next != id) {   // (the first of its token)
+                id = next;
+                const int at = next - c0 - c;
+                uint32_t* p = own_piece(buf, at >> 2) + (at & 3);
+                v = __uint_as_float(*p);
+                if (MODE == HEAD_KEEP) {
+                  *p = __float_as_uint(NEG);
+                  again |= v == top;
+                }
+              }
+              zt[e] = v;
               ++e;
               next = e < p.E ? ent[e] : kHeadNoEntry;
             }
+            if (MODE == HEAD_KEEP && again) {
+              top = NEG;
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                const float4 f = *reinterpret_cast<const float4*>(own_piece(buf, j));
+                top = fmaxf(top, fmaxf(fmaxf(f.x, f.y), fmaxf(f.z, f.w)));
+              }
+            }
             __syncwarp();
           }
+          if (MODE == HEAD_KEEP) mk = fmaxf(mk, top);
         }
         // the sums, and the logits to keep
         const float my = (m == NEG ? 0.f : m) * kLog2e;
-        const float qc = -kLog2e * p.q_inv, qm = my * p.q_inv;
+        const float mine = (mk == NEG ? 0.f : mk) * kLog2e;
+        const float qc = -kLog2e * p.q_inv, qm = mine * p.q_inv;
         float s = 0.f, s2 = 0.f;
         char* keep = nullptr;
         if (MODE == HEAD_KEEP)
@@ -488,8 +516,8 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
             if (TWO) s2 += ta + tb;
           }
           if (MODE == HEAD_KEEP) {
-            // the low bits of t + 2^23 are t to the nearest: no conversion unit (the
-            // maximum's own t may round below 0)
+            // the low bits of t + 2^23 are t to the nearest: no conversion unit (an
+            // entry's t may be below 0, and the maximum's own round there)
             const int j0 = (c & 32) ? 4 : 0;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -509,6 +537,7 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
           p.pm[at] = m == NEG ? NEG : my;
           p.ps[at] = s;
           if (TWO) p.ps2[at] = s2;
+          if (MODE == HEAD_KEEP) p.pk[at] = mine;
         }
       } else {
         // dx: its token's row, or an fp32 part; dw: added to earlier pieces', in its type
@@ -662,6 +691,7 @@ GemmArgs base_args(const LaunchCtx& ctx, const HeadPlan& p, const HeadArgs& a, i
   g.pm = reinterpret_cast<float*>(a.ws + p.o_m);
   g.ps = reinterpret_cast<float*>(a.ws + p.o_s);
   g.ps2 = reinterpret_cast<float*>(a.ws + p.o_s2);
+  g.pk = reinterpret_cast<float*>(a.ws + p.o_mk);
   g.kept = reinterpret_cast<uint16_t*>(a.ws + p.o_kept);
   g.inv_tau = 1.f / p.tau; g.q_inv = 1.f / p.q_step;
   g.part = reinterpret_cast<float*>(a.ws + p.o_part);

@@ -978,7 +978,11 @@ int occult_head_loss(const occult_desc_t* desc, const occult_head_t* opt, const 
  * The batch goes in pieces of opt->piece tokens; one piece's logits stay in the
  * workspace in 16 bits (fp32 layers: 32), so that the gradients need no second product.
  * bf16 layers round dz to bf16 once (its factor coef/N is applied to the fp32 sums);
- * outputs in OCCULT_F32 then carry that rounding.
+ * outputs in OCCULT_F32 then carry that rounding.  Before it, with s = max(24, 20 tau) /
+ * 65535, a probability of bf16 layers is within s ln 2 / 2 of itself (tempered: s ln 2 /
+ * (2 tau)), and one below 2^-24 (tempered: min(2^-20, 2^(-24 / tau))) of the largest of its
+ * tokens' run of 128 may be 0; labels' and teachers' tokens take no part in either, theirs
+ * are made from fp32 logits.
  */
 int occult_head_step(const occult_desc_t* desc, const occult_head_t* opt, const void* x,
                      const void* w, const int32_t* labels, const int32_t* teacher_ids,

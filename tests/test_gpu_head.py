@@ -540,3 +540,61 @@ def test_tokens_that_are_nearly_sure(occ, dtype, T, taught):
     got = -dw.double().cpu().numpy()[label, j] * T / tau
     tol = n * (2.0 ** -21 + (1e-5 + (2.0 ** -8 if dtype == "bf16" else 0)) * miss)
     assert (np.abs(got - n * miss) <= tol).all(), (np.abs(got - n * miss) / np.maximum(tol, 1e-30)).max()
+
+
+@pytest.mark.parametrize("tau,taught", [(1.0, False), (1.0, True), (2.0, True), (0.25, True), (10.0, True)])
+@pytest.mark.parametrize("V", [300, 1009])
+def test_all_gradients_of_sure_tokens(occ, tau, taught, V):
+    """Labels (or a teacher's tokens) 12 to 40 octaves, times tau, above every other token: the
+    gradients of the others, and so dx, are as small as they are together.
+
+    x picks a column of w each, so that every logit is one exact product and column t of dw is
+    the token's dz.  A bf16 layer keeps a step's logits in steps of s = max(24, 20 tau) / 65535
+    octaves below the largest of their 128 that is no entry: a probability is within
+    s ln 2 / 2 (over tau where tempered) of itself, and one that lies a whole range below, 2^-24
+    of that largest's at most (2^-20 tempered), may be 0; one rounding to bf16; sums and
+    exponentials 2^-20.
+    """
+    d, T = 64, 64
+    rng = np.random.default_rng(int(10 * tau) + V)
+    w = torch.as_tensor(rng.normal(size=(V, d)) * 1.8 * max(1.0, tau ** 0.5)).bfloat16().float().numpy()
+    labels = rng.permutation(V)[:T].astype(np.int32)
+    up = np.log(2) * (12 + 28 * np.arange(T) / T) * max(1.0, tau)
+    w[labels, np.arange(T)] = torch.as_tensor(w.max(axis=0) + up).bfloat16().float().numpy()
+    x = np.eye(T, d, dtype=np.float32)
+    kw = dict(tau=tau, coef=1.0)
+    c = (x, w, labels, None, None)
+    K = 0
+    if taught:
+        K = 3
+        ids = rng.integers(0, V, size=(T, K)).astype(np.int32)
+        ids[:, 0] = labels
+        kw = dict(tau=tau, coef=0.5, coef_kd=0.5)
+        c = (x, w, labels, ids, np.array([[9.0, -90.0, -np.inf]] * T, np.float32))
+    got = run(occ, *c, **kw)
+    want = ohead.losses(*c, **kw)
+    p1, p2 = (np.exp(v - v.max(axis=1, keepdims=True)) for v in (w.T.astype(np.float64), w.T / tau))
+    p1, p2 = p1 / p1.sum(axis=1, keepdims=True), p2 / p2.sum(axis=1, keepdims=True)
+    s = max(24.0, 20 * tau) / 65535 * np.log(2) / 2
+    a, b = (0.5 / T, 0.5 * tau / T) if taught else (1.0 / T, 0.0)
+    entry = np.zeros((T, V), bool)
+    entry[np.arange(T), labels] = True
+    if taught:
+        entry[np.arange(T)[:, None], ids] = True
+    err = np.zeros((T, V))
+    for c0 in range(0, V, 128):
+        part = slice(c0, min(V, c0 + 128))
+        top1, top2 = (np.where(entry, 0, p)[:, part].max(axis=1, keepdims=True) for p in (p1, p2))
+        reach = max(24.0, 20 * tau)
+        err[:, part] = a * (s * p1[:, part] + 2.0 ** -reach * top1) + b * (s / tau * p2[:, part] + 2.0 ** (-reach / tau) * top2)
+    # an entry's own is of the size of what all others are together
+    miss = a * (np.where(entry, 0, p1).sum(axis=1, keepdims=True)) + b * (np.where(entry, 0, p2).sum(axis=1, keepdims=True))
+    size = a * p1 + b * p2
+    err = np.where(entry, 2.0 ** -20 * (miss + a + b), err + 2.0 ** -20 * size)
+    exact = want["dw"].T[:T]                     # dz [T, V]
+    err = err + 2.0 ** -8 * (np.abs(exact) + err)
+    off = np.abs(got["dw"].T[:T] - exact)
+    assert (off <= err * (1 + 2.0 ** -10)).all(), np.max(off / err)
+    bound = err @ np.abs(w) + (V / 16 + 8) * 2 * U * (np.abs(exact) @ np.abs(w))
+    off = np.abs(got["dx"] - want["dx"])
+    assert (off <= bound * (1 + 2.0 ** -7)).all(), np.max(off / bound)
