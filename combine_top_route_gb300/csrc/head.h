@@ -131,7 +131,8 @@ __device__ __forceinline__ void mean_losses(const HeadLossOut& o, const HeadCoun
 
 // Factors of a term's gradient over the mean of its tokens, and the common factor that
 // is kept out of the rounded gradients of the logits: the cross entropy's where it
-// counts, so that its -1 at the label is exact.
+// counts, so that its -1 at the label is exact.  A factor 2^-40 of another's and less does
+// not count: the other's ratio to it need not be a number.
 struct HeadScale {
   float unit;      // common factor
   float k_ce, k_kd, k_z;   // coef / N_ce, coef_kd tau / N_kd, 2 coef_z / N over it
@@ -142,7 +143,8 @@ __host__ __device__ inline HeadScale head_scale(int n, int n_ce, int n_kd, float
   const float a = n_ce > 0 ? coef / static_cast<float>(n_ce) : 0.f;
   const float b = n_kd > 0 ? coef_kd * tau / static_cast<float>(n_kd) : 0.f;
   const float c = n > 0 ? 2.f * coef_z / static_cast<float>(n) : 0.f;
-  s.unit = a > 0.f ? a : b > 0.f ? b : c > 0.f ? c : 1.f;
+  const float least = 0x1p-40f * (a > b ? (a > c ? a : c) : (b > c ? b : c));
+  s.unit = a > 0.f && a >= least ? a : b > 0.f && b >= least ? b : c > 0.f ? c : 1.f;
   s.k_ce = a / s.unit;
   s.k_kd = b / s.unit;
   s.k_z = c / s.unit;

@@ -598,3 +598,20 @@ def test_all_gradients_of_sure_tokens(occ, tau, taught, V):
     bound = err @ np.abs(w) + (V / 16 + 8) * 2 * U * (np.abs(exact) @ np.abs(w))
     off = np.abs(got["dx"] - want["dx"])
     assert (off <= bound * (1 + 2.0 ** -7)).all(), np.max(off / bound)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("coefs", [(1e-42, 0.7, 1e-2), (1e-38, 0.0, 1e-2), (0.0, 1e-40, 1.0), (1e28, 1e-12, 0.0)])
+def test_terms_of_far_apart_weights(occ, dtype, coefs):
+    """A term that weighs next to nothing leaves the others' gradients as they are alone."""
+    coef, coef_kd, coef_z = coefs
+    c = case(200, 128, 700, dtype, K=4, ignored=0.2)
+    kw = dict(dtype=dtype, tau=2.0)
+    big = dict(coef=coef if coef > 1e-20 else 0.0, coef_kd=coef_kd if coef_kd > 1e-5 else 0.0, coef_z=coef_z)
+    got = run(occ, *c, coef=coef, coef_kd=coef_kd, coef_z=coef_z, **kw)
+    alone = run(occ, *c, **big, **kw)
+    for name in ("dx", "dw"):
+        assert np.isfinite(got[name]).all()
+        # (the common factor differs: dz is rounded to bf16 at another place, once each)
+        tol = (2.0 ** -7 if dtype == "bf16" else 2.0 ** -20)
+        assert np.linalg.norm(got[name] - alone[name]) <= tol * np.linalg.norm(alone[name])
