@@ -3,7 +3,6 @@
 #include <stdio.h>
 
 #include <initializer_list>
-#include <mutex>
 
 #include "common.cuh"
 #include "head.h"
@@ -16,16 +15,13 @@ __device__ int g_dev_err;
 
 namespace {
 
-constexpr int kMaxDevices = 64;
-
 struct DeviceInfo {
-  std::once_flag once;
   int num_sms = 0;
   bool clusters = false;
   int* err = nullptr;
   cudaError_t status = cudaSuccess;
 };
-DeviceInfo g_devices[kMaxDevices];
+PerDevice<DeviceInfo> g_devices;
 
 // Stands for the kernels of such clusters in the question whether they can be placed.
 __global__ void cluster_kernel() {}
@@ -58,15 +54,15 @@ bool can_place_clusters() {
 int launch_ctx(occult_stream_t stream, LaunchCtx* ctx) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return OCCULT_ERR_CUDA;
-  DeviceInfo& di = g_devices[dev];
-  std::call_once(di.once, [&] {
-    di.status = cudaDeviceGetAttribute(&di.num_sms, cudaDevAttrMultiProcessorCount, dev);
-    if (di.status == cudaSuccess)
-      di.status = cudaGetSymbolAddress(reinterpret_cast<void**>(&di.err), g_dev_err);
-    if (di.status == cudaSuccess) di.clusters = can_place_clusters();
+  const DeviceInfo& di = g_devices.get(dev, [&](DeviceInfo& d) {
+    d.status = cudaDeviceGetAttribute(&d.num_sms, cudaDevAttrMultiProcessorCount, dev);
+    if (d.status == cudaSuccess)
+      d.status = cudaGetSymbolAddress(reinterpret_cast<void**>(&d.err), g_dev_err);
+    if (d.status == cudaSuccess) d.clusters = can_place_clusters();
   });
   if (di.status != cudaSuccess) return OCCULT_ERR_CUDA;
   ctx->stream = static_cast<cudaStream_t>(stream);
+  ctx->device = dev;
   ctx->dev_err = di.err;
   ctx->num_sms = di.num_sms;
   ctx->clusters = di.clusters;

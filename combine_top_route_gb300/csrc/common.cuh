@@ -8,6 +8,7 @@
 #include <stdint.h>
 
 #include "../../include/occult.h"
+#include "per_device.h"
 
 namespace occult {
 
@@ -16,6 +17,7 @@ namespace occult {
 // ----------------------------------------------------------------------------
 struct LaunchCtx {
   cudaStream_t stream;
+  int device;       // the current one, 0 .. kMaxDevices - 1
   int* dev_err;     // device error word (see occult_device_error)
   int num_sms;
   bool clusters;    // whether clusters of kClusterCtas CTAs, an SM each, can be placed

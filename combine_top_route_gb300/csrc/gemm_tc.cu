@@ -1357,19 +1357,18 @@ int launch_tc(const LaunchCtx& ctx, const CUtensorMap& ma, const CUtensorMap& mb
   cfg.attrs = PAIR ? attr : attr + 1;
   cfg.numAttrs = PAIR ? 2 : 1;
   // persistent grid: one CTA per SM, or as many co-resident CTA pairs as fit
-  static std::once_flag once;
-  static cudaError_t attr_err = cudaSuccess;
-  static int n_pairs = 0;
-  std::call_once(once, [&] {
-    attr_err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    smem_bytes(PAIR, EPI, SWAP));
-    if (PAIR && attr_err == cudaSuccess) {
+  struct Fit { cudaError_t err; int n_pairs; };
+  static PerDevice<Fit> fits;
+  const Fit& fit = fits.get(ctx.device, [&](Fit& f) {
+    f.err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 smem_bytes(PAIR, EPI, SWAP));
+    if (PAIR && f.err == cudaSuccess) {
       cfg.gridDim = dim3(2 * (ctx.num_sms / 2));
-      attr_err = cudaOccupancyMaxActiveClusters(&n_pairs, kern, &cfg);
+      f.err = cudaOccupancyMaxActiveClusters(&f.n_pairs, kern, &cfg);
     }
   });
-  if (attr_err != cudaSuccess || (PAIR && n_pairs < 1)) return OCCULT_ERR_CUDA;
-  cfg.gridDim = dim3(PAIR ? 2 * n_pairs : ctx.num_sms);
+  if (fit.err != cudaSuccess || (PAIR && fit.n_pairs < 1)) return OCCULT_ERR_CUDA;
+  cfg.gridDim = dim3(PAIR ? 2 * fit.n_pairs : ctx.num_sms);
   return cuda_status(cudaLaunchKernelEx(&cfg, kern, ma, mb, mc, md, p));
 }
 

@@ -15,7 +15,6 @@
 // that no row has to be looked up.  The last block to arrive joins the blocks' sums and
 // finishes the losses.
 #include <algorithm>
-#include <mutex>
 
 #include "head.h"
 #include "kernels.h"
@@ -239,12 +238,11 @@ __global__ void __launch_bounds__(kThreads, 1) head_few_kernel(const FewArgs a) 
 template <int NT, bool TWO>
 int launch_few(const LaunchCtx& ctx, const HeadPlan& p, FewArgs g) {
   auto kern = head_few_kernel<NT, TWO>;
-  static std::once_flag once;
-  static cudaError_t err = cudaSuccess;
-  std::call_once(once, [&] {
-    err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
-  });
-  if (err != cudaSuccess) return OCCULT_ERR_CUDA;
+  static PerDevice<cudaError_t> fits;
+  if (fits.get(ctx.device, [&](cudaError_t& e) {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
+      }) != cudaSuccess)
+    return OCCULT_ERR_CUDA;
   // stages of about 64 KB, three of them, beside x (d <= 16384: at most 128 KB)
   const int row_bytes = p.d * 2, room = kRingBytes - NT * row_bytes;
   g.rows = std::max(1, std::min(64 * 1024, room / 3) / row_bytes);

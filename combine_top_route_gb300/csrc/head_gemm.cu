@@ -27,7 +27,6 @@
 // pair the even CTA's), warps 4..11 epilogue, two to a TMEM lane quarter, half of the
 // columns each.  Every wait is bounded.
 #include <algorithm>
-#include <mutex>
 
 #include "head.h"
 #include "kernels.h"
@@ -658,25 +657,24 @@ int launch_one(const LaunchCtx& ctx, const CUtensorMap& ma, const CUtensorMap& m
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = PAIR ? attr : attr + 1;
   cfg.numAttrs = PAIR ? 2 : 1;
-  static std::once_flag once;
-  static cudaError_t err = cudaSuccess;
-  static int n_pairs = 0;
-  std::call_once(once, [&] {
-    err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
-    if (err == cudaSuccess && MODE != HEAD_GRADS) {
+  struct Fit { cudaError_t err; int n_pairs; };
+  static PerDevice<Fit> fits;
+  const Fit& fit = fits.get(ctx.device, [&](Fit& f) {
+    f.err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    if (f.err == cudaSuccess && MODE != HEAD_GRADS) {
       // the split of the registers adds up to a launch with this many: another count
       // (of another compiler) would leave warps waiting for theirs
       cudaFuncAttributes fa;
-      err = cudaFuncGetAttributes(&fa, kern);
-      if (err == cudaSuccess && fa.numRegs != kLaunchRegs) err = cudaErrorLaunchOutOfResources;
+      f.err = cudaFuncGetAttributes(&fa, kern);
+      if (f.err == cudaSuccess && fa.numRegs != kLaunchRegs) f.err = cudaErrorLaunchOutOfResources;
     }
-    if (PAIR && err == cudaSuccess) {
+    if (PAIR && f.err == cudaSuccess) {
       cfg.gridDim = dim3(2 * (ctx.num_sms / 2));
-      err = cudaOccupancyMaxActiveClusters(&n_pairs, kern, &cfg);
+      f.err = cudaOccupancyMaxActiveClusters(&f.n_pairs, kern, &cfg);
     }
   });
-  if (err != cudaSuccess || (PAIR && n_pairs < 1)) return OCCULT_ERR_CUDA;
-  cfg.gridDim = dim3(PAIR ? 2 * n_pairs : ctx.num_sms);
+  if (fit.err != cudaSuccess || (PAIR && fit.n_pairs < 1)) return OCCULT_ERR_CUDA;
+  cfg.gridDim = dim3(PAIR ? 2 * fit.n_pairs : ctx.num_sms);
   return cuda_status(cudaLaunchKernelEx(&cfg, kern, ma, ma2, mb, mb2, g));
 }
 
