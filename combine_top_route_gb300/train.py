@@ -258,13 +258,16 @@ class OccultHead:
 
     def _inputs(self, labels, teacher):
         ids, logits = (None, None) if teacher is None else teacher
+        if labels is None:
+            self.token_loss.zero_()
         return dict(labels=labels, teacher_ids=ids, teacher_logits=logits, lse=self.lse,
                     token_loss=None if labels is None else self.token_loss)
 
     def loss(self, r: torch.Tensor, labels: Optional[torch.Tensor] = None, teacher=None):
         """[4] {total, cross entropy, distillation, z} of the residual stream r, without a
         gradient; ``labels`` int32 [T], ``teacher`` (int32 [T, K] tokens, fp32 [T, K] logits).
-        The tokens' own losses are left in ``token_loss``, their log-sums in ``lse``."""
+        The tokens' own losses are left in ``token_loss`` (0 without labels), their log-sums in
+        ``lse``."""
         self._norm(r)
         occult_head_loss(self.desc, self.opt, self.x, self.w, self.losses, self.ws,
                          **self._inputs(labels, teacher))

@@ -1,0 +1,83 @@
+"""OccultHead in the forms that a model uses it in, and the chain under a softmax router.
+
+Gradients against fp64 autograd of the same formulas.  bf16: the tolerance of the chain's other
+tests (2-norm of the difference over that of the gradient, some twenty roundings to bf16 of
+2^-9 / sqrt(3) each, amplified by the norms: 1.5 %).  fp32: products of up to 300 terms, each
+within 2^-24, twice over, and the norm's: 1e-4 of the 2-norm; bf16 residual streams round
+dr once, 2^-8.
+"""
+import os
+import sys
+
+import numpy as np
+import pytest
+import torch
+
+import synth
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+sys.path.insert(0, os.path.join(ROOT, "examples"))
+
+pytestmark = pytest.mark.gpu
+
+REL = 0.015
+
+
+@pytest.fixture(scope="module")
+def occ():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from combine_top_route_gb300 import build
+    build.build()
+    import combine_top_route_gb300 as occ
+    occ.lib()
+    yield occ
+    assert occ.device_error() == 0
+
+
+def rel(a, b):
+    return float((a.double() - b).norm() / b.norm())
+
+
+def rms(v):
+    return v * (v.square().mean(1, keepdim=True) + 1e-6).rsqrt()
+
+
+def head_total(o, z, labels, teacher):
+    """The head's total in fp64, from the logits."""
+    lse = z.logsumexp(1)
+    on = torch.zeros_like(lse, dtype=torch.bool)
+    total = 0.0
+    if labels is not None:
+        on = labels >= 0
+        total = total + o.coef * (lse - z.gather(1, labels.clamp(min=0).long()[:, None])[:, 0])[on].mean()
+    if teacher is not None:
+        ids, tl = teacher
+        q, logp = (tl.double() / o.temperature).softmax(1), (z / o.temperature).log_softmax(1).gather(1, ids.long())
+        total = total + o.coef_kd * o.temperature ** 2 * (q * (q.log() - logp)).sum(1).mean()
+        on = torch.ones_like(on)
+    return total + o.coef_z * lse[on].square().mean()
+
+
+def fp32_head(occ, T=200, d=64, V=300, res=torch.float32, **kw):
+    desc = occ.desc_for(synth.CONFIGS["olmoe_fwd"].with_(T=T, d=d, dtype="f32"))
+    g = torch.Generator(device="cuda").manual_seed(1)
+    w = torch.randn(V, d, generator=g, device="cuda") / 8
+    head = occ.OccultHead(desc, w, res_dtype=res, **kw)
+    head.w_norm.copy_(1 + 0.2 * torch.randn(d, generator=g, device="cuda"))
+    r = torch.randn(T, d, generator=g, device="cuda").to(res)
+    labels = torch.randint(0, V, (T,), generator=g, device="cuda").int()
+    labels[::6] = -1
+    ids = torch.stack([torch.randperm(V, generator=g, device="cuda")[:4] for _ in range(T)]).int()
+    return head, r, labels, (ids, torch.randn(T, 4, generator=g, device="cuda"))
+
+
+def test_token_losses_are_of_the_last_call(occ):
+    """A call without labels leaves no other call's token losses behind."""
+    head, r, labels, teacher = fp32_head(occ, topk=4, coef=0.5, coef_kd=0.5)
+    for call in (head.step, head.loss):
+        head.loss(r, labels, teacher)
+        assert (head.token_loss[labels >= 0] > 0).all()
+        call(r, None, teacher)
+        assert (head.token_loss == 0).all()
+        assert (head.lse != 0).all()
