@@ -151,7 +151,7 @@ class OccultBlock:
         self.rstd_pre = e(T)
         self.rstd_post = e(T) if post_norm else None
         G = balance_groups(desc, self.bal_opt)
-        self.counts = e(G, Ne, dtype=torch.int32)
+        self.counts = torch.zeros(G, Ne, dtype=torch.int32, device=dev)
         self.grad_w, self.losses = e(G * Ne + 1), e(4)
         self.bal_ws = e(max(1, balance_workspace_size(desc, self.bal_opt)), dtype=torch.uint8)
         self.norm_ws = e(max(1, workspace_size(desc, WS_BLOCK_NORM_BWD)), dtype=torch.uint8)

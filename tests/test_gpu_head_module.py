@@ -81,3 +81,18 @@ def test_token_losses_are_of_the_last_call(occ):
         call(r, None, teacher)
         assert (head.token_loss == 0).all()
         assert (head.lse != 0).all()
+
+
+def test_bias_step_before_any_forward(occ):
+    """No loads yet: the bias stays."""
+    cfg = synth.CONFIGS["olmoe_train"].with_(T=64, d=128, inter=64, n_experts=8, top_k=2, n_vdev=4)
+    held = [torch.full((n,), 7 * i, dtype=torch.int32, device="cuda") for i in range(1, 400) for n in (8, 128)]
+    for t in held:
+        t[0] = 1000
+    torch.cuda.synchronize()
+    del t, held          # what freshly allocated memory then holds
+    block = occ.OccultBlock(occ.desc_for(cfg), synth.expert_weights(cfg, device="cuda"),
+                            torch.arange(8, dtype=torch.int32).view(4, 2), torch.zeros(8, 128),
+                            score=occ.occult_score_t(bias_rate=0.5), bias=torch.zeros(8))
+    block.bias_step()
+    assert (block.moe.bias == 0).all() and (block.counts == 0).all()
