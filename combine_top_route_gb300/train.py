@@ -226,10 +226,11 @@ class OccultHead:
 
     def __init__(self, desc: occult_desc_t, w_head: torch.Tensor, device="cuda", eps: float = 1e-6,
                  res_dtype=torch.bfloat16, topk: int = 0, coef: float = 1.0, coef_kd: float = 0.0,
-                 coef_z: float = 0.0, temperature: float = 1.0, piece: int = 0):
+                 coef_z: float = 0.0, temperature: float = 1.0, piece: int = 0, train: bool = True):
         """``desc``: T, d and dtype are the head's; ``w_head`` [V, d] (in the layer type and on
         the device it is used where it is); ``topk``: teacher entries a token; the other
-        options as in occult_head_t."""
+        options as in occult_head_t; ``train=False``: ``loss`` alone, without the gradients'
+        buffers and the workspace of a step's logits."""
         dev, dt = torch.device(device), desc.torch_dtype
         T, d, V = desc.T, desc.d, w_head.shape[0]
         if tuple(w_head.shape) != (V, d):
@@ -244,13 +245,22 @@ class OccultHead:
         self.w_norm = torch.ones(d, dtype=dt, device=dev)
         self.x, self.rstd = e(T, d, dtype=dt), e(T)
         self.losses, self.lse, self.token_loss = e(4), e(T), e(T)
-        self.dx, self.dr, self.dw, self.dw_norm = e(T, d), e(T, d, dtype=res_dtype), e(V, d), e(d)
-        need = max(head_workspace_size(desc, self.opt, step=b) for b in (True, False))
+        self.train = train
+        self.dx = self.dr = self.dw = self.dw_norm = self.norm_ws = None
+        need = head_workspace_size(desc, self.opt, step=False)
+        if train:
+            self.dx, self.dr, self.dw, self.dw_norm = e(T, d), e(T, d, dtype=res_dtype), e(V, d), e(d)
+            self.norm_ws = e(max(1, workspace_size(desc, WS_BLOCK_NORM_BWD)), dtype=torch.uint8)
+            need = max(need, head_workspace_size(desc, self.opt, step=True))
         self.ws = e(max(1, need), dtype=torch.uint8)
-        self.norm_ws = e(max(1, workspace_size(desc, WS_BLOCK_NORM_BWD)), dtype=torch.uint8)
+
+    def _trains(self):
+        if not self.train:
+            raise RuntimeError("OccultHead was built without train=True")
 
     def parameters(self):
         """[(name, parameter, its fp32 gradient)], as OccultBlock.parameters."""
+        self._trains()
         return [("w_head", self.w, self.dw), ("w_norm", self.w_norm, self.dw_norm)]
 
     def _norm(self, r):
@@ -277,6 +287,7 @@ class OccultHead:
              dloss: Optional[torch.Tensor] = None):
         """(losses [4], gradient of r): as ``loss``, with the total's gradients (times the
         fp32 CUDA tensor ``dloss``); the weights' are left in their buffers."""
+        self._trains()
         self._norm(r)
         occult_head_step(self.desc, self.opt, self.x, self.w, self.losses, self.ws, dx=self.dx,
                          dw=self.dw, dloss=dloss, **self._inputs(labels, teacher))

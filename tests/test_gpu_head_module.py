@@ -96,3 +96,21 @@ def test_bias_step_before_any_forward(occ):
                             score=occ.occult_score_t(bias_rate=0.5), bias=torch.zeros(8))
     block.bias_step()
     assert (block.moe.bias == 0).all() and (block.counts == 0).all()
+
+
+def test_a_head_that_only_scores(occ):
+    """train=False: no gradients and no kept logits; the same losses; a step is refused."""
+    desc = occ.desc_for(synth.CONFIGS["olmoe_fwd"].with_(T=300, d=128))
+    g = torch.Generator(device="cuda").manual_seed(2)
+    w = (torch.randn(4000, 128, generator=g, device="cuda") / 8).bfloat16()
+    r = torch.randn(300, 128, generator=g, device="cuda").bfloat16()
+    labels = torch.randint(0, 4000, (300,), generator=g, device="cuda").int()
+    full, lean = occ.OccultHead(desc, w), occ.OccultHead(desc, w, train=False)
+    a, b = full.loss(r, labels).clone(), lean.loss(r, labels)
+    assert torch.equal(a, b) and torch.equal(full.token_loss, lean.token_loss)
+    assert lean.dw is None and lean.dx is None
+    assert lean.ws.numel() == occ.head_workspace_size(desc, lean.opt, step=False) < full.ws.numel()
+    with pytest.raises(RuntimeError, match="train=True"):
+        lean.step(r, labels)
+    with pytest.raises(RuntimeError, match="train=True"):
+        lean.parameters()
