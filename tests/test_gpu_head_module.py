@@ -59,6 +59,45 @@ def head_total(o, z, labels, teacher):
     return total + o.coef_z * lse[on].square().mean()
 
 
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("biased", [True, False])
+def test_gradients_of_the_chain_under_a_softmax_router(occ, renorm, biased):
+    from train_model import Model, batch
+    cfg = synth.CONFIGS["olmoe_train"].with_(name="model", T=384, d=128, inter=64, n_experts=8, top_k=2, n_vdev=4,
+                                             renorm=renorm)
+    model = Model(cfg, 500, coef=0.8, coef_z=1e-2)
+    block, head, moe = model.block, model.head, model.block.moe
+    moe.score.score, moe.score.scale = occ.SCORE_SOFTMAX, 2.0
+    for name in ("w1", "w2"):
+        moe.w[name].mul_(4)      # activations of order one in a layer this narrow
+    g = torch.Generator(device="cuda").manual_seed(5)
+    moe.bias = 0.05 * torch.randn(8, generator=g, device="cuda") if biased else None
+    pairs, labels, _ = batch(cfg, 500, 1, 0)
+    labels[::5] = -100
+    losses = model.gradients(pairs, labels)
+    p = {n: t.detach().double().requires_grad_() for n, t, _ in model.parameters()}
+    r = model.stream(pairs).double().requires_grad_()
+    x = rms(r) * p["w_pre"]
+    logits = x @ p["w_router"].T
+    ids = moe.ids.long()
+    gates = logits.softmax(1).gather(1, ids)
+    gates = 2.0 * (gates / gates.sum(1, keepdim=True) if renorm else gates)
+    y = torch.zeros_like(x)
+    for e in range(8):
+        rows, slot = (ids == e).nonzero(as_tuple=True)
+        w1, w2 = p["w1"].view(8, 128, 128)[e], p["w2"].view(8, 128, 64)[e]
+        h = torch.nn.functional.silu(x[rows] @ w1[:64].T) * (x[rows] @ w1[64:].T)
+        y = y.index_add(0, rows, gates[rows, slot][:, None] * (h @ w2.T))
+    out = r + p["gate"] * (rms(y) * p["w_post"])
+    total = head_total(head.opt, (rms(out) * p["w_norm"]) @ p["w_head"].T, labels, None)
+    (total + block.bal_opt.coef_z * logits.logsumexp(1).square().mean()).backward()
+    torch.cuda.synchronize()
+    assert abs(float(losses[0]) / float(total.detach()) - 1) < REL
+    assert rel(block.dr, r.grad) < REL
+    for name, _, grad in model.parameters():
+        assert rel(grad.view_as(p[name].grad), p[name].grad) < REL, name
+
+
 def fp32_head(occ, T=200, d=64, V=300, res=torch.float32, **kw):
     desc = occ.desc_for(synth.CONFIGS["olmoe_fwd"].with_(T=T, d=d, dtype="f32"))
     g = torch.Generator(device="cuda").manual_seed(1)
@@ -70,6 +109,29 @@ def fp32_head(occ, T=200, d=64, V=300, res=torch.float32, **kw):
     labels[::6] = -1
     ids = torch.stack([torch.randperm(V, generator=g, device="cuda")[:4] for _ in range(T)]).int()
     return head, r, labels, (ids, torch.randn(T, 4, generator=g, device="cuda"))
+
+
+@pytest.mark.parametrize("res", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("taught", [False, True])
+def test_head_of_an_fp32_layer(occ, res, taught):
+    kw = dict(coef=0.6, coef_z=1e-2)
+    if taught:
+        kw.update(topk=4, coef_kd=0.5, temperature=2.0)
+    head, r, labels, teacher = fp32_head(occ, res=res, **kw)
+    teacher = teacher if taught else None
+    up = torch.full((1,), 0.25, device="cuda")
+    losses, dr = head.step(r, labels, teacher, dloss=up)
+    p = {n: t.detach().double().requires_grad_() for n, t, _ in head.parameters()}
+    x = r.double().requires_grad_()
+    total = head_total(head.opt, (rms(x) * p["w_norm"]) @ p["w_head"].T, labels, teacher)
+    (0.25 * total).backward()
+    torch.cuda.synchronize()
+    assert abs(float(losses[0]) / float(total.detach()) - 1) < 1e-5
+    assert rel(dr, x.grad) < (1e-4 if res == torch.float32 else 2.0 ** -8)
+    for name, _, grad in head.parameters():
+        assert rel(grad, p[name].grad) < 1e-4, name
+    again = head.loss(r, labels, teacher)
+    assert abs(float(again[0]) / float(total.detach()) - 1) < 1e-5
 
 
 def test_token_losses_are_of_the_last_call(occ):
