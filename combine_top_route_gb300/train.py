@@ -124,7 +124,10 @@ class OccultBlock:
         used where they are, so that an optimizer's steps change the caller's tensors;
         the other weights are copied); ``w_router`` fp32 [Ne, d];
         ``gate`` fp32 [d] or None; ``balance``: the weights of the expert, device and z
-        terms; ``group_len``: tokens of a sequence for them (0: the batch); ``score`` and
+        terms, which are made from softmax(logits) whatever the router's scores are: beside a
+        router of sigmoids the expert and device terms pull at probabilities that choose
+        nothing, and a bias evens the loads out instead (weights 0, 0);
+        ``group_len``: tokens of a sequence for them (0: the batch); ``score`` and
         ``bias``: the scored router's, as OccultMoE takes them."""
         if desc.dtype != OCCULT_BF16 or desc.n_shared:
             raise ValueError("OccultBlock trains bf16 layers without shared experts")

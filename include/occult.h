@@ -719,7 +719,7 @@ int occult_balance_workspace_size(const occult_desc_t* desc, const occult_balanc
 /*
  * occult_balance_loss -- per-expert counts and the router's auxiliary losses.
  * The tokens are cut into groups of group_len (the last may be shorter); with
- * p_t = softmax(logits_t), over the N_g unmasked tokens of group g
+ * p_t = softmax(logits_t) (of any router), over the N_g unmasked tokens of group g
  *   c_ge = slots of those tokens that chose expert e,  f_ge = Ne c_ge / (k N_g),
  *   P_ge = mean of p_te;   A = groups with an unmasked token, N = sum_g N_g
  *   expert = 1/A sum_g sum_e f_ge P_ge
