@@ -14,20 +14,23 @@
 // by their ranks in fp64 where there is a bias: one exponential on the lanes that hold the
 // candidates.  Two worths within some 4e-6 at the border of the kept groups are made again in
 // fp64, from the candidates of these two groups where they are few, else by the whole choice in
-// fp64: one token in 10^5 of logits of deviation 1, and more of wider ones, most of whose worths
-// are that small (of one best score without a bias none: its logit orders as it does).
+// fp64: one token in 10^5 of logits of deviation 1.  Of wider ones more worths are that near, or
+// that small: 32768 tokens x 256 experts in 8 groups by their best two go from 42 us (deviation
+// 1) to 247 (8) by sigmoids, from 58 to 306 by a softmax with a bias, from 38 to 88 by one
+// without.  One best score without a bias is its logit and needs none of it (36 us at any).
 // fp64 for every token would cost more than the rest together: the chip has two fp64 lanes
 // an SM.
 //
-// Instructions bound the choice, not its bytes: 32768 tokens x 256 experts in 8 groups, 4
-// of them and 8 experts kept, sigmoid with a bias, take 34 us (33.5 MB of logits, 5 us at
-// the copy rate) with 57 % of the issue slots used and the integer pipe 36 % busy; most of the
-// rest are waits for the step before (sort, then one dependent maximum a place).  145 us
+// A token's chain of steps bounds the choice, not its bytes: 32768 tokens x 256 experts in 8
+// groups, 4 of them and 8 experts kept, sigmoid with a bias, take 34 to 37 us (33.5 MB of logits,
+// 5 us at the copy rate) with 54 to 57 % of the issue slots used and the integer pipe 36 to 42 %
+// busy: the rest are waits for the step before (sort, then one dependent maximum a place).  145 us
 // with the choice in fp64 for every tie within fp32's error, 66 before near places were
 // told apart from their candidates alone; two tokens a warp, half a warp each, and tokens
 // dealt out by a shared counter were no faster.  16383 tokens x 60 experts: 11 us.  Few
 // tokens wait for the launch and one token's chain: 512 x 256 in 5 us.  The gradient moves
-// 8 bytes a logit at the copy rate (11 us for the 67 MB of the first case).
+// 8 bytes a logit near the copy rate (10 to 13 us for the 67 MB of the first case; by a softmax,
+// whose every score is made again, 18 us renormalised, 23 not).
 #include "common.cuh"
 #include "kernels.h"
 
