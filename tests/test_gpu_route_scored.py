@@ -566,3 +566,22 @@ def test_nan_logits_rank_as_switched_off(occ, biased, sigmoid, G, keep, best):
         assert (np.isnan(gates) == bad).all()
     else:
         assert (np.isnan(gates) == nan.any(axis=1)[:, None]).all()
+
+
+@pytest.mark.parametrize("sigmoid", [True, False])
+@pytest.mark.parametrize("renorm", [True, False])
+def test_grad_of_one_expert_in_two_slots(occ, sigmoid, renorm):
+    """Slots of one expert, which the router does not write, add up: where they are its row's
+    leading one as well, and beside a dropped slot."""
+    rng = np.random.default_rng(29)
+    T, Ne, k = 60, 40, 5
+    z = logits_of(T, Ne, 4)
+    ids, dg = chosen(rng, T, Ne, k), rng.normal(size=(T, k)).astype(np.float32)
+    ids[:, 3] = ids[:, 1]
+    ids[::4, 4] = -1
+    z[np.arange(0, T, 2), ids[::2, 1]] += 9
+    kw = dict(sigmoid=sigmoid, renorm=renorm, scale=1.7)
+    got, want = grad_of(occ, z, ids, dg, **kw), scored.grad(z, ids, dg, **kw)
+    # (a sum of 40 exponentials besides; the oracle's own differences, 2^-50 of the size of the terms)
+    err = 2 * grad_bound(z, ids, dg, rel=6 * score_err(z) + 80 * U, **kw) + 2.0 ** -50 * 2 * np.abs(dg).max()
+    assert (np.abs(got - want) <= err).all(), np.max(np.abs(got - want) / err)
