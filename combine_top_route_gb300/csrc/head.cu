@@ -188,6 +188,7 @@ head_rows_kernel(const int32_t* __restrict__ labels, const int32_t* __restrict__
     cnt->n_ce = sum[2];
     cnt->n_kd = sum[3];
     cnt->ticket = 0;
+    cnt->stretch = 1.f;
   }
   const bool copy = n < T;
   int row = sum[0];   // first row of the block's next tokens
@@ -250,22 +251,70 @@ head_rows_kernel(const int32_t* __restrict__ labels, const int32_t* __restrict__
       xc[i] = make_uint4(0, 0, 0, 0);
 }
 
+// ---- the gradient's scalars ---------------------------------------------------------
+struct DzArgs {
+  const HeadCounts* cnt;
+  const float *pk, *tops, *l1, *l2;
+  const uint8_t* flag;
+  int ldp, row0, piece, V, ld;
+  float inv_tau, q_step, coef, coef_kd, coef_z, tau;
+  bool two;
+};
+// A row's factors of the two softmaxes.
+__device__ __forceinline__ void row_factors(const DzArgs& a, const HeadScale& sc, int f, float L,
+                                            float& k1, float& k2) {
+  k1 = ((f & kRowCe) ? sc.k_ce : 0.f) + sc.k_z * (L * kLn2);
+  k2 = (f & kRowKd) ? sc.k_kd : 0.f;
+  if (!a.two) {   // one softmax for both
+    k1 += k2;
+    k2 = 0.f;
+  }
+}
+__device__ __forceinline__ HeadScale scale_of(const DzArgs& a) {
+  return head_scale(a.cnt->n, a.cnt->n_ce, a.cnt->n_kd, a.coef, a.coef_kd, a.coef_z, a.tau, a.cnt->stretch);
+}
+
+// Gradient at entry e of row r, the first of its token: the softmaxes at the entry's own fp32
+// logit, minus the factors of every entry of that token.
+__device__ __forceinline__ float entry_dz(const DzArgs& a, const HeadScale& sc, const HeadLossOut& o, size_t at,
+                                          int e, int id, float top, float l1, float l2, float k1, float k2) {
+  const float y = over_top(o.zt[at], top);
+  float g = k1 * exp2f(y - l1);
+  if (a.two) g += k2 * exp2f(y * a.inv_tau - l2);
+  for (int f = e; f < o.E && o.ent[at + f - e] == id; ++f) {
+    const float q = o.ent_q[at + f - e];
+    g -= q < 0.f ? sc.k_ce : sc.k_kd * q;
+  }
+  return g;
+}
+
 // ---- a row's sums, losses and the means ---------------------------------------------
 // A block takes 32 rows: its warps join every so many parts of all of them (a lane a row,
 // so that reads run along the rows), then finish the rows one by one.  The last block to
 // arrive adds the blocks' sums in their order.  32 warps a block where there are few of
 // them, 16 where two to an SM save a second round of blocks.
-template <bool TWO, int kSumWarps>
-__global__ void __launch_bounds__(kSumWarps * 32)
+//
+// TUNE (steps of bf16 layers): a row's warp also makes its entries' gradients and what each
+// stretch's rounding to bf16 takes from them; the launch's last block picks the piece's.
+template <bool TWO, int kSumWarps, bool TUNE>
+__global__ void __launch_bounds__(kSumWarps * 32, 32 / kSumWarps)
 head_sum_kernel(HeadCounts* cnt, const HeadLossOut o, const float* __restrict__ pm,
                 const float* __restrict__ ps, const float* __restrict__ ps2, int ldp, int halves, int row0,
                 int rows_max, const int32_t* __restrict__ idx, const uint8_t* __restrict__ flag,
                 float* __restrict__ tops, float* __restrict__ l1, float* __restrict__ l2,
                 float* __restrict__ sums, int block0,
-                int n_blocks) {
+                int n_blocks, const DzArgs z, float* __restrict__ tune) {
+  static_assert(kSumWarps >= kStretches, "a warp a stretch");
   __shared__ float s_m[kSumWarps][33], s_s[kSumWarps][33], s_s2[kSumWarps][33];
   __shared__ float s_ce[32], s_kd[32], s_z[32];
-  __shared__ bool s_last;
+  __shared__ float s_off[TUNE ? kSumWarps : 1][kStretches], s_all[kStretches];
+  __shared__ bool s_last, s_pick;
+  auto pick = [&] {   // the stretch of the least loss; 1 where none is less
+    int best = 0;
+    for (int j = 1; j < kStretches; ++j)
+      if (s_all[j] < s_all[best]) best = j;
+    cnt->stretch = exp2f(static_cast<float>(best) / kStretches);
+  };
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -307,6 +356,11 @@ head_sum_kernel(HeadCounts* cnt, const HeadLossOut o, const float* __restrict__ 
   }
   __syncthreads();
   RowSums mine{0.f, 0.f, 0.f};
+  const HeadScale sc = head_scale(cnt->n, cnt->n_ce, cnt->n_kd, z.coef, z.coef_kd, z.coef_z, z.tau, 1.f);
+  // a lane's stretch is number lane % 8; of 32 entries it takes every fourth
+  static_assert(kStretches == 8, "four lanes a stretch");
+  const float by = exp2f(static_cast<float>(lane % kStretches) / kStretches), shrink = 1.f / by;
+  float off = 0.f;
   for (int own = warp; own < 32 && r_first + own < n; own += kSumWarps) {
     const size_t r = static_cast<size_t>(row0) + r_first + own;
     const float m = lane < kSumWarps ? s_m[lane][own] : NEG;
@@ -316,7 +370,34 @@ head_sum_kernel(HeadCounts* cnt, const HeadLossOut o, const float* __restrict__ 
     float b = a;
     if (TWO) b = log2f(warp_sum(lane < kSumWarps ? s_s2[lane][own] * ex2((m - safe) * inv_tau) : 0.f));
     if (lane == 0) { tops[r] = safe; l1[r] = a; l2[r] = b; }
-    row_losses(o, r, flag[r], idx[r], safe, a, b, inv_tau, mine);
+    const int f = flag[r];
+    if (TUNE) {
+      float k1, k2;
+      row_factors(z, sc, f, safe + a, k1, k2);
+      row_losses(o, r, f, idx[r], safe, a, b, inv_tau, mine, [&](int id, float q, float y) {
+        // as entry_dz, of two entries of one token at most: a choice hangs on it, no result
+        const float own = q < 0.f ? sc.k_ce : sc.k_kd * q;
+        const int before = __shfl_up_sync(kFull, id, 1), next = __shfl_down_sync(kFull, id, 1);
+        const float other = __shfl_down_sync(kFull, own, 1);
+        float g = k1 * ex2(y - a) - own;
+        if (TWO) g += k2 * ex2(y * inv_tau - b);
+        if (lane < 31 && next == id) g -= other;
+        if (id == kHeadNoEntry || (lane > 0 && before == id)) g = 0.f;
+#pragma unroll 2
+        for (int k = 0; k < min(32, o.E); k += 4) {
+          const float v = __shfl_sync(kFull, g, k + lane / kStretches) * shrink;
+          const float lost = __bfloat162float(__float2bfloat16_rn(v)) - v;
+          off = fmaf(lost, lost, off);
+        }
+      });
+    } else {
+      row_losses(o, r, f, idx[r], safe, a, b, inv_tau, mine);
+    }
+  }
+  if (TUNE) {
+    off += __shfl_xor_sync(kFull, off, kStretches);
+    off += __shfl_xor_sync(kFull, off, 2 * kStretches);
+    if (lane < kStretches) s_off[warp][lane] = off * by * by;
   }
   if (lane == 0) { s_ce[warp] = mine.ce; s_kd[warp] = mine.kd; s_z[warp] = mine.z; }
   __syncthreads();
@@ -324,59 +405,61 @@ head_sum_kernel(HeadCounts* cnt, const HeadLossOut o, const float* __restrict__ 
   if (warp == 0) {
     const float a = warp_sum(have ? s_ce[lane] : 0.f), b = warp_sum(have ? s_kd[lane] : 0.f),
                 c = warp_sum(have ? s_z[lane] : 0.f);
+    if (TUNE && lane < kStretches) {
+      float v = 0.f;
+      for (int w = 0; w < kSumWarps; ++w) v += s_off[w][lane];
+      if (gridDim.x == 1) s_all[lane] = v;
+      else tune[kStretches * static_cast<size_t>(blockIdx.x) + lane] = v;
+    }
+    if (n_blocks > 1) {
+      if (lane < 3) sums[3 * static_cast<size_t>(block0 + blockIdx.x) + lane] = lane == 0 ? a : lane == 1 ? b : c;
+      __threadfence();
+    }
+    __syncwarp();
     if (lane == 0 && n_blocks == 1) {
       mean_losses(o, *cnt, a, b, c);   // a block alone
-      s_last = false;
+      s_last = s_pick = false;
     } else if (lane == 0) {
-      float* out = sums + 3 * static_cast<size_t>(block0 + blockIdx.x);
-      out[0] = a;
-      out[1] = b;
-      out[2] = c;
-      __threadfence();
-      s_last = atomicAdd(&cnt->ticket, 1u) == static_cast<unsigned>(n_blocks - 1);
+      const int before = static_cast<int>(atomicAdd(&cnt->ticket, 1u));
+      s_last = before == n_blocks - 1;
+      s_pick = gridDim.x > 1 && before == block0 + static_cast<int>(gridDim.x) - 1;
     }
+    if (TUNE && lane == 0 && gridDim.x == 1) pick();
   }
   __syncthreads();
-  if (!s_last) return;
+  if (!s_last && !s_pick) return;
   __threadfence();
-  // every block of the call is done: each thread adds a run of them, then a tree
-  float a = 0.f, b = 0.f, c = 0.f;
-  for (int i = threadIdx.x; i < n_blocks; i += blockDim.x) {
-    a += __ldcg(sums + 3 * static_cast<size_t>(i));
-    b += __ldcg(sums + 3 * static_cast<size_t>(i) + 1);
-    c += __ldcg(sums + 3 * static_cast<size_t>(i) + 2);
-  }
+  // every block of the launch (the call) is done: a warp adds a stretch's losses, and each thread
+  // a run of the blocks' sums, then a tree
+  float v = 0.f, a = 0.f, b = 0.f, c = 0.f;
+  if (TUNE && s_pick && warp < kStretches)
+    for (int i = lane; i < static_cast<int>(gridDim.x); i += 32)
+      v += __ldcg(tune + kStretches * static_cast<size_t>(i) + warp);
+  if (s_last)
+    for (int i = threadIdx.x; i < n_blocks; i += blockDim.x) {
+      a += __ldcg(sums + 3 * static_cast<size_t>(i));
+      b += __ldcg(sums + 3 * static_cast<size_t>(i) + 1);
+      c += __ldcg(sums + 3 * static_cast<size_t>(i) + 2);
+    }
+  v = warp_sum(v);
   a = warp_sum(a); b = warp_sum(b); c = warp_sum(c);
-  if (lane == 0) { s_ce[warp] = a; s_kd[warp] = b; s_z[warp] = c; }
+  if (lane == 0) {
+    s_ce[warp] = a; s_kd[warp] = b; s_z[warp] = c;
+    if (TUNE && warp < kStretches) s_all[warp] = v;
+  }
   __syncthreads();
   if (warp == 0) {
     a = warp_sum(have ? s_ce[lane] : 0.f);
     b = warp_sum(have ? s_kd[lane] : 0.f);
     c = warp_sum(have ? s_z[lane] : 0.f);
-    if (lane == 0) mean_losses(o, *cnt, a, b, c);
+    if (lane == 0) {
+      if (s_last) mean_losses(o, *cnt, a, b, c);
+      if (TUNE && s_pick) pick();
+    }
   }
 }
 
 // ---- gradient of the logits -----------------------------------------------------------
-struct DzArgs {
-  const HeadCounts* cnt;
-  const float *pk, *tops, *l1, *l2;
-  const uint8_t* flag;
-  int ldp, row0, piece, V, ld;
-  float inv_tau, q_step, coef, coef_kd, coef_z, tau;
-  bool two;
-};
-// A row's factors of the two softmaxes.
-__device__ __forceinline__ void row_factors(const DzArgs& a, const HeadScale& sc, int f, float L,
-                                            float& k1, float& k2) {
-  k1 = ((f & kRowCe) ? sc.k_ce : 0.f) + sc.k_z * (L * kLn2);
-  k2 = (f & kRowKd) ? sc.k_kd : 0.f;
-  if (!a.two) {   // one softmax for both
-    k1 += k2;
-    k2 = 0.f;
-  }
-}
-
 // bf16 layers: the kept 16-bit logits (units of q_step octaves below the largest of their
 // 128 columns that is no entry, the last one for all that lies lower: no probability) become
 // bf16 gradients where they lie.  A warp takes 16 rows of 128
@@ -390,7 +473,7 @@ head_dz_bf16_kernel(const DzArgs a, uint16_t* __restrict__ kept) {
   const int n = min(a.cnt->n - a.row0, a.piece);
   const int h = blockIdx.x * 8 + warp;
   if (n <= 0 || h * 128 >= a.ld) return;
-  const HeadScale sc = head_scale(a.cnt->n, a.cnt->n_ce, a.cnt->n_kd, a.coef, a.coef_kd, a.coef_z, a.tau);
+  const HeadScale sc = scale_of(a);
   const int rows = (n + kHeadRowAlign - 1) & ~(kHeadRowAlign - 1);
   const int c0 = h * 128 + (lane & 15) * 8;
   const bool edge = h * 128 + 128 > a.V;
@@ -444,27 +527,13 @@ head_dz_bf16_kernel(const DzArgs a, uint16_t* __restrict__ kept) {
   }
 }
 
-// Gradient at entry e of row r, the first of its token: the softmaxes at the entry's own fp32
-// logit, minus the factors of every entry of that token.
-__device__ __forceinline__ float entry_dz(const DzArgs& a, const HeadScale& sc, const HeadLossOut& o, size_t at,
-                                          int e, int id, float top, float l1, float l2, float k1, float k2) {
-  const float y = over_top(o.zt[at], top);
-  float g = k1 * exp2f(y - l1);
-  if (a.two) g += k2 * exp2f(y * a.inv_tau - l2);
-  for (int f = e; f < o.E && o.ent[at + f - e] == id; ++f) {
-    const float q = o.ent_q[at + f - e];
-    g -= q < 0.f ? sc.k_ce : sc.k_kd * q;
-  }
-  return g;
-}
-
 // bf16 layers: the entries' columns, written over.
 __global__ void __launch_bounds__(256)
 head_dz_entries_kernel(const DzArgs a, const HeadLossOut o, __nv_bfloat16* __restrict__ dz) {
   pdl_wait();
   pdl_trigger();
   const int n = min(a.cnt->n - a.row0, a.piece);
-  const HeadScale sc = head_scale(a.cnt->n, a.cnt->n_ce, a.cnt->n_kd, a.coef, a.coef_kd, a.coef_z, a.tau);
+  const HeadScale sc = scale_of(a);
   const int64_t total = static_cast<int64_t>(n) * o.E;
   for (int64_t i = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; i < total;
        i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
@@ -486,7 +555,7 @@ __global__ void __launch_bounds__(256)
 head_dz_f32_kernel(const DzArgs a, const HeadLossOut o, float* __restrict__ kept) {
   pdl_wait();
   const int n = min(a.cnt->n - a.row0, a.piece);
-  const HeadScale sc = head_scale(a.cnt->n, a.cnt->n_ce, a.cnt->n_kd, a.coef, a.coef_kd, a.coef_z, a.tau);
+  const HeadScale sc = scale_of(a);
   for (int r = blockIdx.x; r < n; r += gridDim.x) {
     const size_t rg = static_cast<size_t>(a.row0) + r;
     const float top = a.tops[rg], l1 = a.l1[rg], l2 = a.l2[rg];
@@ -535,7 +604,7 @@ head_dx_kernel(const HeadCounts* cnt, const int32_t* __restrict__ idx, const flo
   pdl_wait();
   pdl_trigger();
   const int n = min(cnt->n - row0, piece);
-  const HeadScale sc = head_scale(cnt->n, cnt->n_ce, cnt->n_kd, coef, coef_kd, coef_z, tau);
+  const HeadScale sc = head_scale(cnt->n, cnt->n_ce, cnt->n_kd, coef, coef_kd, coef_z, tau, cnt->stretch);
   const float g = sc.unit * (dloss ? *dloss : 1.f);
   for (int r0 = blockIdx.x * kDxTokens; r0 < n; r0 += gridDim.x * kDxTokens) {
     int t[kDxTokens];
@@ -661,6 +730,7 @@ HeadPlan head_plan(const occult_desc_t& ds, const occult_head_t& opt, bool step)
   p.o_mk = take(bf && step ? 4 * P * p.halves : 0);
   p.o_top = take(4 * T); p.o_l1 = take(4 * T); p.o_l2 = take(4 * T);
   p.o_sum = take(12 * (T / 32 + p.n_pieces));
+  p.o_tune = take(bf && step ? 4 * kStretches * (P / 32) : 0);
   p.o_kept = take(step ? P * row_bytes : 0);
   const size_t parts = std::max(p.splits, p.splits_alone);
   p.o_part = take(step && (!bf || parts > 1) ? 4 * parts * P * p.d : 0);
@@ -717,19 +787,22 @@ int launch_head(const LaunchCtx& ctx, const HeadPlan& p, const HeadArgs& a) {
     if (rc) return rc;
     const int blocks = (rows + 31) / 32;
     const int warps = blocks > ctx.num_sms ? 16 : 32;
-    auto* sum = warps == 32 ? (p.two ? head_sum_kernel<true, 32> : head_sum_kernel<false, 32>)
-                            : (p.two ? head_sum_kernel<true, 16> : head_sum_kernel<false, 16>);
-    e = launch_pdl(sum, blocks, warps * 32, 0, ctx.stream, cnt, head_loss_out(p, a), pm, ps, ps2, p.piece,
-                   p.halves, row0, rows, idx, flag, tops, l1, l2, sums, block0, n_blocks);
-    if (e != cudaSuccess) return OCCULT_ERR_CUDA;
-    block0 += blocks;
-    if (!p.step) continue;
     DzArgs z{};
     z.cnt = cnt; z.pk = reinterpret_cast<const float*>(ws + p.o_mk); z.tops = tops; z.l1 = l1; z.l2 = l2; z.flag = flag;
     z.ldp = p.piece; z.row0 = row0; z.piece = p.piece; z.V = p.V; z.ld = p.ld;
     z.inv_tau = 1.f / p.tau; z.q_step = p.q_step; z.tau = p.tau;
     z.coef = p.coef; z.coef_kd = p.coef_kd; z.coef_z = p.coef_z;
     z.two = p.two;
+#define OCCULT_HEAD_SUM(TWO, TUNE) (warps == 32 ? head_sum_kernel<TWO, 32, TUNE> : head_sum_kernel<TWO, 16, TUNE>)
+    auto* sum = bf && p.step ? (p.two ? OCCULT_HEAD_SUM(true, true) : OCCULT_HEAD_SUM(false, true))
+                             : (p.two ? OCCULT_HEAD_SUM(true, false) : OCCULT_HEAD_SUM(false, false));
+#undef OCCULT_HEAD_SUM
+    e = launch_pdl(sum, blocks, warps * 32, 0, ctx.stream, cnt, head_loss_out(p, a), pm, ps, ps2, p.piece,
+                   p.halves, row0, rows, idx, flag, tops, l1, l2, sums, block0, n_blocks, z,
+                   reinterpret_cast<float*>(ws + p.o_tune));
+    if (e != cudaSuccess) return OCCULT_ERR_CUDA;
+    block0 += blocks;
+    if (!p.step) continue;
     if (bf) {
       auto* kept = reinterpret_cast<uint16_t*>(ws + p.o_kept);
       // some eight blocks an SM, however many of the rows count

@@ -372,7 +372,8 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                     (warp - kEpiWarp0) * 1024;
     float g = 0.f;
     if (!kLogits) {
-      const HeadScale sc = head_scale(n_all, p.cnt->n_ce, p.cnt->n_kd, p.coef, p.coef_kd, p.coef_z, p.tau);
+      const HeadScale sc = head_scale(n_all, p.cnt->n_ce, p.cnt->n_kd, p.coef, p.coef_kd, p.coef_z, p.tau,
+                                      p.cnt->stretch);
       g = sc.unit * (p.dloss ? *p.dloss : 1.f);
     }
     int it = 0;

@@ -176,7 +176,7 @@ __device__ __forceinline__ void dw_tile(const SimtArgs& a, int blk) {
   const int n = max(0, min(a.cnt->n - a.row0, a.piece));
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   const int cols = (a.d + TS - 1) / TS, c0 = blk % cols * TS, m0 = blk / cols * TS;
-  const HeadScale sc = head_scale(a.cnt->n, a.cnt->n_ce, a.cnt->n_kd, a.coef, a.coef_kd, a.coef_z, a.tau);
+  const HeadScale sc = head_scale(a.cnt->n, a.cnt->n_ce, a.cnt->n_kd, a.coef, a.coef_kd, a.coef_z, a.tau, 1.f);
   const float g = sc.unit * (a.dloss ? *a.dloss : 1.f);
   const float* x = x_rows(a);
   float acc[V][V] = {};

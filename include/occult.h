@@ -977,7 +977,8 @@ int occult_head_loss(const occult_desc_t* desc, const occult_head_t* opt, const 
  *   dw      out [V, d] in opt->grad_dtype, nullable (dx or dw is needed).  Written.
  * The batch goes in pieces of opt->piece tokens; one piece's logits stay in the
  * workspace in 16 bits (fp32 layers: 32), so that the gradients need no second product.
- * bf16 layers round dz to bf16 once (its factor coef/N is applied to the fp32 sums);
+ * bf16 layers round dz to bf16 once (its factor coef/N is applied to the fp32 sums, times a
+ * power of 2^(1/8) under which a piece's labels' and teachers' tokens lose least);
  * outputs in OCCULT_F32 then carry that rounding.  Before it, with s = max(24, 20 tau) /
  * 65535, a probability of bf16 layers is within s ln 2 / 2 of itself (tempered: s ln 2 /
  * (2 tau)), and one below 2^-24 (tempered: min(2^-20, 2^(-24 / tau))) of the largest of its

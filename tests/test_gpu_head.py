@@ -615,3 +615,44 @@ def test_terms_of_far_apart_weights(occ, dtype, coefs):
         # (the common factor differs: dz is rounded to bf16 at another place, once each)
         tol = (2.0 ** -7 if dtype == "bf16" else 2.0 ** -20)
         assert np.linalg.norm(got[name] - alone[name]) <= tol * np.linalg.norm(alone[name])
+
+
+def bf16(v):
+    return torch.as_tensor(v, dtype=torch.float64).float().bfloat16().double().numpy()
+
+
+@pytest.mark.parametrize("case_", ["few", "pieces", "taught"])
+def test_entries_gradients_lose_half_a_unit_at_most_where_it_is_small(occ, case_):
+    """A piece whose entries' gradients all have one size is rounded where half a unit is least of it.
+
+    Half a unit of bf16 is 2^-8 of a number just above a power of two and 2^-9 of one just below.
+    Some stretch 2^(j / 8) of the eight takes any number to a fraction of 2^(7 / 8) and more, so
+    that the least error is at most 2^-8 / 2^(7 / 8) = 0.00213 of it, and the exponentials' 2^-19.
+    The sizes here are those that lose the most as they are.  x picks a column of w, so that a
+    column of dw is the pieces' dz, over tokens of one dz each.
+    """
+    d, V = 64, 5
+    tau = 2.0 if case_ == "taught" else 1.0
+    # labels' logits above four others at 0: 1 - p of them, by what bf16 takes from it
+    z = bf16(np.linspace(0.5, 6.0, 3000))
+    miss = 4 / (4 + np.exp(z / tau))
+    loss = np.abs(bf16(miss) - miss) / miss
+    worst = z[np.argsort(-loss)[:64]]
+    assert np.sort(loss)[-64:].min() > 0.0025   # (the inputs alone, before any call)
+    w = np.zeros((V, d), np.float32)
+    w[0] = worst
+    calls = [(np.full(n, i), 0) for i in range(64) for n in (1, 3)] if case_ != "pieces" else [
+        (np.repeat([i, i + 1, i + 2], [256, 256, 90]), 256) for i in range(0, 60, 12)]
+    for cols, piece in calls:
+        T = len(cols)
+        x = np.zeros((T, d), np.float32)
+        x[np.arange(T), cols] = 1
+        lab = np.zeros(T, np.int32)
+        kw = dict(piece=piece, tau=tau)
+        if case_ == "taught":
+            got = run(occ, x, w, None, lab[:, None], np.zeros((T, 1), np.float32), coef=0.0, coef_kd=1.0, **kw)
+        else:
+            got = run(occ, x, w, lab, None, None, **kw)
+        for c in np.unique(cols):
+            want = -(cols == c).sum() / T * tau * 4 / (4 + np.exp(float(w[0, c]) / tau))
+            assert abs(got["dw"][0, c] / want - 1) <= 2.0 ** -8 / 2 ** (7 / 8) + 2.0 ** -19 + 2 * U * T
