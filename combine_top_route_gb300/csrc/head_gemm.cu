@@ -723,9 +723,12 @@ int launch_head_logits_bf16(const LaunchCtx& ctx, const HeadPlan& p, const HeadA
   GemmArgs g = base_args(ctx, p, a, row0);
   g.bn = p.bn;
   g.n_tiles = p.n_tiles;
-  // 512 products to a sum in TMEM (with 128 the two accumulators' way to registers and back
-  // is what a small batch waits for: 11 tokens x 3008 x 3951 took 25 us)
-  g.seg = 8;
+  // Products to a sum in TMEM: 512 in pairs (with 256 the epilogue has to keep up with twice as
+  // many: 4096 tokens x 2048 x 50304 took 520 us for 475), 256 in single CTAs, which wait for
+  // the weights anyway, and whose few tokens' losses do not average the truncation out (with
+  // 128 the accumulators' way to registers and back is what they wait for: 11 x 3008 x 3951
+  // took 25 us)
+  g.seg = pair ? 8 : 4;
   ring(g, p.bn);
 #define OCCULT_HEAD_LOGITS(MODE)                                                           \
   (pair ? (p.two ? launch_one<MODE, true, true>(ctx, mx, mc, mw, mw, g)                    \

@@ -656,3 +656,23 @@ def test_entries_gradients_lose_half_a_unit_at_most_where_it_is_small(occ, case_
         for c in np.unique(cols):
             want = -(cols == c).sum() / T * tau * 4 / (4 + np.exp(float(w[0, c]) / tau))
             assert abs(got["dw"][0, c] / want - 1) <= 2.0 ** -8 / 2 ** (7 / 8) + 2.0 ** -19 + 2 * U * T
+
+
+@pytest.mark.parametrize("T,step", [(1, True), (5, False), (128, False), (128, True)])
+@pytest.mark.parametrize("d", [512, 2048])
+def test_logits_of_few_tokens_lose_a_segment_at_most(occ, T, step, d):
+    """Sums that the tensor cores truncate at every step: 256 products to a segment.
+
+    The first of a logit's products is 1, and every further 16 of them add up to a little
+    less than fp32's step above 1: one of the tensor cores' steps each, dropped.  A segment of
+    256 has 16 steps and the later ones have no large term, so that less than 16 * 2^-23 is
+    lost; joining up to eight segments rounds to nearest (2^-24 each), the log-sum of the one
+    logit is its product with log2(e) and back, three roundings of 2^-24 of 1.5.
+    """
+    x = np.ones((T, d), np.float32)
+    w = np.full((1, d), 127 / 128 * 2.0 ** -27, np.float32)
+    w[0, :16] = 0
+    w[0, 0] = 1
+    want = 1 + (d / 16 - 1) * 127 / 128 * 2.0 ** -23
+    got = run(occ, x, w, np.zeros(T, np.int32), None, None, step=step)
+    assert np.abs(got["lse"] - want).max() <= 16 * 2.0 ** -23 + 8 * U + 3 * 1.5 * U
